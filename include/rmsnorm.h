@@ -227,6 +227,132 @@ int rmsnorm_bwd_naive(const void *x, const void *w, const void *dy,
                       int dtype, cudaStream_t stream);
 
 /*
+ * Rotary positions of several axes (time, height, width) for queries and
+ * keys, with the RMSNorm of their heads in front: what a transformer runs
+ * after the query and key projections, in one pass over both.
+ * For each head row x of D = head_dim elements, with weights:
+ *   n = x * rstd * w,  rstd = 1 / sqrt(mean(x^2) + eps)   (w per tensor, [D])
+ * and n = x without. Then rotary_dim / 2 pairs turn by
+ *   theta_p = positions[axis(p), batch, token] * inv_freq[p]
+ *   y_a = n_a cos(theta) - n_b sin(theta),  y_b = n_b cos(theta) + n_a sin(theta)
+ * where pair p is elements (p, p + rotary_dim/2), or (2p, 2p+1) with
+ * `adjacent`; the other head_dim - rotary_dim elements, the last ones, are n.
+ * sections[i] pairs belong to axis i (their sum is rotary_dim / 2): in
+ * blocks, axis 0 first, or with `interleaved` dealt in turn to the axes that
+ * have pairs left (0, 1, 2, 0, 1, 2, ...). inv_freq[p] is per pair, in the
+ * order of the pairs. The angle is the exact product taken modulo one turn,
+ * so far positions keep their digits (frequencies below 2^25; an infinite or
+ * NaN frequency gives NaN). n is not rounded between the norm and the
+ * rotation: each output is rounded once.
+ */
+#define RMSNORM_ROPE_MAX_AXES 4
+#define RMSNORM_ROPE_MAX_HEAD_DIM 256
+
+/* Strides in elements over (batch, token, head); not negative. A head's
+   elements are dense. */
+typedef struct {
+    int64_t batch, token, head;
+} rmsnorm_strides_t;
+
+typedef struct {
+    int64_t batch, length; /* batch * length tokens */
+    int32_t q_heads, k_heads; /* k_heads may be 0: no keys */
+    int32_t head_dim;      /* even, 2..RMSNORM_ROPE_MAX_HEAD_DIM */
+    int32_t rotary_dim;    /* even, 2..head_dim */
+    int32_t axes;          /* 1..RMSNORM_ROPE_MAX_AXES */
+    int32_t sections[RMSNORM_ROPE_MAX_AXES]; /* pairs of each axis; >= 0 */
+    int32_t interleaved, adjacent; /* 0 or 1 */
+    int32_t positions_64;  /* positions are int64 (1) or int32 (0) */
+    int64_t position_stride[3]; /* positions over (axis, batch, token), in
+                              elements, not negative; 0 = shared */
+    rmsnorm_strides_t q, k;         /* the forward's inputs */
+    rmsnorm_strides_t q_out, k_out; /* its outputs, and their gradients in the
+                              backward */
+    rmsnorm_strides_t dq, dk;       /* backward: the inputs' gradients */
+} rmsnorm_rope_t;
+
+/*
+ * Forward. Reads q [batch, length, q_heads, head_dim] and k (k_heads), wq and
+ * wk [head_dim] (both NULL: no norm, eps unused), positions and inv_freq
+ * [rotary_dim / 2]; writes q_out and k_out. dtype names the types of q, k and
+ * of the weights as for the norm. q_out may be the q buffer with q's strides,
+ * and k_out k's (in place); otherwise no output may overlap an input or
+ * itself. One kernel launch, no workspace. batch, length or q_heads + k_heads
+ * of 0: nothing to do. With k_heads 0 the key pointers are not looked at, with
+ * q_heads 0 the query's.
+ * RMSNORM_ERR_INVALID_ARG: a descriptor outside the limits above, a negative
+ * stride, 2^31 or more tokens, a NULL pointer, one weight without the other
+ * (when both tensors have heads), eps negative or NaN.
+ */
+int rmsnorm_qk_rope_fwd(const rmsnorm_rope_t *rope, const void *q,
+                        const void *k, const void *wq, const void *wk,
+                        const void *positions, const float *inv_freq,
+                        void *q_out, void *k_out, float eps, int dtype,
+                        cudaStream_t stream);
+
+/*
+ * Backward. Reads what the forward read and the gradients dq_out and dk_out
+ * of its outputs (strides q_out, k_out); writes dq and dk (strides dq, dk) and,
+ * with weights, dwq and dwk [head_dim] (fp32, overwritten). The row's rstd is
+ * computed again; without weights q and k are not read and may be NULL. dq may
+ * be the dq_out buffer with its strides, dk likewise. dwq and dwk are
+ * deterministic: persistent blocks, partial rows, a column sum in a fixed
+ * order; the partial rows come from the stream-ordered allocator
+ * (RMSNORM_ERR_NOMEM). With no tokens dwq and dwk are set to zero. A gradient
+ * of a tensor without heads is neither read nor written, its dw likewise.
+ */
+int rmsnorm_qk_rope_bwd(const rmsnorm_rope_t *rope, const void *q,
+                        const void *k, const void *wq, const void *wk,
+                        const void *positions, const float *inv_freq,
+                        const void *dq_out, const void *dk_out, void *dq,
+                        void *dk, float *dwq, float *dwk, float eps, int dtype,
+                        cudaStream_t stream);
+
+/* Activation applied after a group norm's affine map. */
+typedef enum {
+    RMSNORM_ACT_NONE = 0,
+    RMSNORM_ACT_SILU = 1, /* z / (1 + exp(-z)) */
+    RMSNORM_ACT_GELU = 2  /* z Phi(z), Phi the normal distribution function */
+} rmsnorm_act_t;
+
+/*
+ * Group norm with an activation on channels-last tensors: x is B samples of
+ * S positions of C channels ([B, S, C], dense), G groups of C / G neighbouring
+ * channels. Over the S * C/G values of a (sample, group):
+ *   mean, var = mean((x - mean)^2),  rstd = 1 / sqrt(var + eps)
+ *   z = (x - mean) * rstd * w_c + b_c,  y = act(z)
+ * Reads x, w and b [C] (both NULL: 1 and 0); writes y and, in fp32, mean and
+ * rstd [B, G]. dtype names the types of x, y and of w and b as for the norm.
+ * The statistics are taken about local means (no digits lost to a mean far
+ * from zero) and are deterministic.
+ * B == 0 or S == 0: nothing to do (mean and rstd of empty slabs are left as
+ * they are). B, S < 0, C <= 0 or C > 2^31-1, G <= 0, C % G != 0, S * (C/G) >=
+ * 2^31, a negative or NaN eps, an unknown activation, a NULL pointer, or one
+ * of w and b without the other: RMSNORM_ERR_INVALID_ARG. A workspace comes
+ * from the stream-ordered allocator where the slab is split over many blocks
+ * (RMSNORM_ERR_NOMEM).
+ */
+int rmsnorm_group_norm_fwd(const void *x, const void *w, const void *b,
+                           void *y, float *mean, float *rstd, int64_t B,
+                           int64_t S, int64_t C, int64_t G, float eps, int act,
+                           int dtype, cudaStream_t stream);
+
+/*
+ * Backward of rmsnorm_group_norm_fwd from its mean and rstd. With
+ * xhat = (x - mean) rstd and dz = dy * act'(xhat w + b):
+ *   dx = rstd * (dz w - mean(dz w) - xhat * mean(dz w xhat))   (over a slab)
+ *   dw_c = sum over samples and positions of dz xhat,  db_c = sum of dz
+ * Writes dx [B, S, C] and, unless w is NULL, dw and db [C] (fp32, overwritten,
+ * deterministic; zero when B or S is 0). dx may be the dy buffer. Arguments
+ * and errors as the forward's.
+ */
+int rmsnorm_group_norm_bwd(const void *x, const void *w, const void *b,
+                           const void *dy, const float *mean,
+                           const float *rstd, void *dx, float *dw, float *db,
+                           int64_t B, int64_t S, int64_t C, int64_t G, int act,
+                           int dtype, cudaStream_t stream);
+
+/*
  * Device-side status. Every wait inside the kernels (on a bulk copy landing
  * in shared memory) is bounded in time; a wait that runs out records
  * RMSNORM_ERR_DEVICE_TIMEOUT in a status word on the device and the kernel

@@ -5,12 +5,19 @@ The computation lives in the CUDA library ``librmsnorm.so`` (C ABI in
 functions mirror the C entry points one for one. ``forward`` and ``backward``
 are conveniences that allocate outputs with PyTorch (device memory only) and
 raise ``RMSNormError`` on a non-OK status; ``add_forward`` and
-``add_backward`` do the same for the residual add. ``autograd`` holds
-differentiable wrappers (``rms_norm``, ``fused_add_rms_norm``, ``RMSNorm``).
+``add_backward`` do the same for the residual add, ``qk_rope_forward`` and
+``qk_rope_backward`` for the QK-norm with rotary positions of several axes,
+``group_norm_forward`` and ``group_norm_backward`` for group norm with an
+activation on channels-last tensors. ``autograd`` holds differentiable wrappers
+(``rms_norm``, ``fused_add_rms_norm``, ``qk_norm_rope``, ``group_norm`` and the
+modules ``RMSNorm``, ``QKNormRope``, ``GroupNorm``).
 """
 from __future__ import annotations
 
 from ._lib import (  # noqa: F401
+    ACT_GELU,
+    ACT_NONE,
+    ACT_SILU,
     BF16,
     BF16_W_F32,
     ERR_CUDA,
@@ -32,9 +39,13 @@ from ._lib import (  # noqa: F401
     PROBE_2R1W,
     PROBE_COPY,
     PROBE_WRITE,
+    ROPE_MAX_AXES,
+    ROPE_MAX_HEAD_DIM,
     VARIANTS,
     Plan,
     RMSNormError,
+    Rope,
+    Strides,
     check,
     checked_variant,
     library_path,
@@ -48,13 +59,23 @@ from ._lib import (  # noqa: F401
     rmsnorm_bwd_ws,
     rmsnorm_fwd,
     rmsnorm_get_last_device_error,
+    rmsnorm_group_norm_bwd,
+    rmsnorm_group_norm_fwd,
     rmsnorm_noalloc_scratch_bytes,
     rmsnorm_plan,
     rmsnorm_probe,
+    rmsnorm_qk_rope_bwd,
+    rmsnorm_qk_rope_fwd,
     rmsnorm_set_wait_limit_ns,
     rmsnorm_status_string,
     rmsnorm_test_drop_copy,
     rmsnorm_version,
+)
+from .image_ops import (  # noqa: F401
+    group_norm_backward,
+    group_norm_forward,
+    qk_rope_backward,
+    qk_rope_forward,
 )
 
 __version__ = "0.2.0"

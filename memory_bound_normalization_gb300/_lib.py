@@ -46,6 +46,13 @@ PROBE_COPY = 0
 PROBE_WRITE = 1
 PROBE_2R1W = 2
 
+ACT_NONE = 0
+ACT_SILU = 1
+ACT_GELU = 2
+
+ROPE_MAX_AXES = 4
+ROPE_MAX_HEAD_DIM = 256
+
 VARIANTS = {0: "none", 1: "rowgroup", 2: "cta_row", 3: "cluster_row", 4: "scalar",
             5: "two_pass", 6: "ring"}
 
@@ -61,6 +68,10 @@ EXPORTS = (
     "rmsnorm_noalloc_scratch_bytes",
     "rmsnorm_bwd_noalloc",
     "rmsnorm_bwd_naive",
+    "rmsnorm_qk_rope_fwd",
+    "rmsnorm_qk_rope_bwd",
+    "rmsnorm_group_norm_fwd",
+    "rmsnorm_group_norm_bwd",
     "rmsnorm_get_last_device_error",
     "rmsnorm_status_string",
     "rmsnorm_set_wait_limit_ns",
@@ -98,6 +109,37 @@ class Plan(ctypes.Structure):
         d = {name: getattr(self, name) for name, _ in self._fields_}
         d["variant_name"] = VARIANTS.get(self.variant, "?")
         return d
+
+
+class Strides(ctypes.Structure):
+    """rmsnorm_strides_t: strides in elements over (batch, token, head)."""
+
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    """rmsnorm_rope_t: the shapes, strides and pairs of a rotary call."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("length", ctypes.c_int64),
+        ("q_heads", ctypes.c_int32),
+        ("k_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * ROPE_MAX_AXES),
+        ("interleaved", ctypes.c_int32),
+        ("adjacent", ctypes.c_int32),
+        ("positions_64", ctypes.c_int32),
+        ("position_stride", ctypes.c_int64 * 3),
+        ("q", Strides),
+        ("k", Strides),
+        ("q_out", Strides),
+        ("k_out", Strides),
+        ("dq", Strides),
+        ("dk", Strides),
+    ]
 
 
 _lock = threading.Lock()
@@ -142,6 +184,10 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.rmsnorm_noalloc_scratch_bytes.argtypes = []
         lib.rmsnorm_noalloc_scratch_bytes.restype = sz
         lib.rmsnorm_bwd_naive.argtypes = [vp, vp, vp, vp, vp, i64, i64, f, i, vp]
+        lib.rmsnorm_qk_rope_fwd.argtypes = [vp] * 9 + [f, i, vp]
+        lib.rmsnorm_qk_rope_bwd.argtypes = [vp] * 13 + [f, i, vp]
+        lib.rmsnorm_group_norm_fwd.argtypes = [vp] * 6 + [i64] * 4 + [f, i, i, vp]
+        lib.rmsnorm_group_norm_bwd.argtypes = [vp] * 9 + [i64] * 4 + [i, i, vp]
         lib.rmsnorm_get_last_device_error.argtypes = [vp]
         lib.rmsnorm_status_string.argtypes = [i]
         lib.rmsnorm_status_string.restype = ctypes.c_char_p
@@ -155,6 +201,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.rmsnorm_version.restype = ctypes.c_char_p
         for name in ("rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_bwd_ws", "rmsnorm_add_fwd",
                      "rmsnorm_add_bwd", "rmsnorm_bwd_noalloc", "rmsnorm_bwd_naive",
+                     "rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_group_norm_fwd",
+                     "rmsnorm_group_norm_bwd",
                      "rmsnorm_get_last_device_error",
                      "rmsnorm_probe", "rmsnorm_plan"):
             getattr(lib, name).restype = ctypes.c_int
@@ -239,6 +287,55 @@ def rmsnorm_bwd_naive(x, w, dy, dx, dw, M: int, N: int, eps: float, dtype: int,
     """The naive three-kernel backward (an ablation); see include/rmsnorm.h."""
     return load_library().rmsnorm_bwd_naive(_ptr(x), _ptr(w), _ptr(dy), _ptr(dx), _ptr(dw), M, N,
                                             eps, dtype, _stream(stream))
+
+
+def _strided_ptr(t) -> int | None:
+    """Device address of a tensor whose strides travel in a descriptor."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError(f"tensor argument on {t.device}: the library takes CUDA tensors")
+    return t.data_ptr()
+
+
+def rmsnorm_qk_rope_fwd(rope, q, k, wq, wk, positions, inv_freq, q_out, k_out, eps: float,
+                        dtype: int, stream=None) -> int:
+    """`rope` is a Rope, packed bytes of one, or None; tensors it gives strides
+    for may be strided."""
+    return load_library().rmsnorm_qk_rope_fwd(
+        _rope_ptr(rope), _strided_ptr(q), _strided_ptr(k), _ptr(wq), _ptr(wk),
+        _strided_ptr(positions), _ptr(inv_freq), _strided_ptr(q_out), _strided_ptr(k_out), eps,
+        dtype, _stream(stream))
+
+
+def rmsnorm_qk_rope_bwd(rope, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk,
+                        eps: float, dtype: int, stream=None) -> int:
+    return load_library().rmsnorm_qk_rope_bwd(
+        _rope_ptr(rope), _strided_ptr(q), _strided_ptr(k), _ptr(wq), _ptr(wk),
+        _strided_ptr(positions), _ptr(inv_freq), _strided_ptr(dq_out), _strided_ptr(dk_out),
+        _strided_ptr(dq), _strided_ptr(dk), _ptr(dwq), _ptr(dwk), eps, dtype, _stream(stream))
+
+
+def _rope_ptr(rope):
+    if isinstance(rope, Rope):
+        return ctypes.addressof(rope)
+    if isinstance(rope, bytes) and len(rope) != ctypes.sizeof(Rope):
+        raise ValueError("a packed rope descriptor of the wrong size")
+    return rope  # bytes pass as their address
+
+
+def rmsnorm_group_norm_fwd(x, w, b, y, mean, rstd, B: int, S: int, C: int, G: int, eps: float,
+                           act: int, dtype: int, stream=None) -> int:
+    return load_library().rmsnorm_group_norm_fwd(_ptr(x), _ptr(w), _ptr(b), _ptr(y), _ptr(mean),
+                                                 _ptr(rstd), B, S, C, G, eps, act, dtype,
+                                                 _stream(stream))
+
+
+def rmsnorm_group_norm_bwd(x, w, b, dy, mean, rstd, dx, dw, db, B: int, S: int, C: int, G: int,
+                           act: int, dtype: int, stream=None) -> int:
+    return load_library().rmsnorm_group_norm_bwd(_ptr(x), _ptr(w), _ptr(b), _ptr(dy), _ptr(mean),
+                                                 _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), B, S, C,
+                                                 G, act, dtype, _stream(stream))
 
 
 def rmsnorm_get_last_device_error(stream=None) -> int:

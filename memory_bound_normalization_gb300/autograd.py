@@ -7,13 +7,19 @@ CUDA library. ``RMSNorm`` is the module form. The weight gradient comes back
 in fp32, as the library computes it; autograd casts it to the weight's dtype
 (an fp32 master weight needs no cast). Inputs must be contiguous CUDA
 tensors; rows are the last dimension.
+
+``group_norm`` / ``GroupNorm`` (channels last, with an activation) and
+``qk_norm_rope`` / ``QKNormRope`` (QK-norm and rotary positions of several
+axes) do the same over their operators.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from . import dtype_code
+from . import image_ops
 
 
 def _rows(t: torch.Tensor):
@@ -102,3 +108,122 @@ class RMSNorm(torch.nn.Module):
                                        (torch.bfloat16, torch.float16)):
             raise TypeError(f"weight {w.dtype} cannot serve activations {x.dtype}")
         return rms_norm(x, w, self.eps)
+
+
+class _GroupNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, num_groups, eps, activation):
+        y, mean, rstd = image_ops.group_norm_forward(x, num_groups, weight, bias, eps, activation)
+        ctx.save_for_backward(x, weight, bias, mean, rstd)
+        ctx.num_groups, ctx.activation = num_groups, activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, bias, mean, rstd = ctx.saved_tensors
+        dx, dw, db = image_ops.group_norm_backward(x, ctx.num_groups, weight, bias,
+                                                   dy.contiguous(), mean, rstd, ctx.activation)
+        return dx, dw, db, None, None, None
+
+
+def group_norm(x: torch.Tensor, num_groups: int, weight: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, eps: float = 1e-5,
+               activation: str = "none") -> torch.Tensor:
+    """act(group norm of x over its positions and each group's channels), x
+    [B, ..., C] with the channels last, differentiable in x, weight and bias."""
+    return _GroupNormFn.apply(x.contiguous(), None if weight is None else weight.contiguous(),
+                              None if bias is None else bias.contiguous(), int(num_groups),
+                              float(eps), activation)
+
+
+class GroupNorm(torch.nn.Module):
+    """Group norm with an activation over [B, ..., C]; fp32 weight and bias by
+    default, which serve 16-bit activations as they are."""
+
+    def __init__(self, num_groups: int, num_channels: int, eps: float = 1e-5,
+                 activation: str = "none", affine: bool = True, device=None,
+                 weight_dtype: torch.dtype = torch.float32):
+        super().__init__()
+        if num_channels % num_groups:
+            raise ValueError(f"{num_channels} channels do not divide into {num_groups} groups")
+        self.num_groups, self.eps, self.activation = num_groups, eps, activation
+        if affine:
+            self.weight = torch.nn.Parameter(torch.ones(num_channels, device=device,
+                                                        dtype=weight_dtype))
+            self.bias = torch.nn.Parameter(torch.zeros(num_channels, device=device,
+                                                       dtype=weight_dtype))
+        else:
+            self.register_parameter("weight", None)
+            self.register_parameter("bias", None)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return group_norm(x, self.num_groups, self.weight, self.bias, self.eps, self.activation)
+
+
+def _dense_heads(t):
+    return t if t is None or t.stride(-1) == 1 else t.contiguous()
+
+
+class _QKRopeFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, positions, inv_freq, sections, interleaved, adjacent, eps):
+        qo, ko = image_ops.qk_rope_forward(q, k, wq, wk, positions, inv_freq, sections,
+                                           interleaved, adjacent, eps)
+        ctx.save_for_backward(q, k, wq, wk, positions, inv_freq)
+        ctx.style = (interleaved, adjacent, eps)
+        ctx.sections = sections
+        return qo, ko
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, wq, wk, positions, inv_freq = ctx.saved_tensors
+        dq, dk, dwq, dwk = image_ops.qk_rope_backward(
+            q, k, wq, wk, positions, inv_freq, ctx.sections, _dense_heads(dq_out),
+            None if k is None else _dense_heads(dk_out), *ctx.style)
+        return dq, dk, dwq, dwk, None, None, None, None, None, None
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, wq: torch.Tensor | None,
+                 wk: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+                 sections, interleaved: bool = False, adjacent: bool = False, eps: float = 1e-6):
+    """(q, k) after the RMSNorm of their heads (without weights: no norm) and
+    the rotation by positions of several axes, differentiable in q, k, wq and
+    wk; see image_ops.qk_rope_forward for the layouts."""
+    return _QKRopeFn.apply(_dense_heads(q), _dense_heads(k),
+                           None if wq is None else wq.contiguous(),
+                           None if wk is None else wk.contiguous(), positions,
+                           inv_freq.contiguous(), tuple(int(n) for n in sections),
+                           bool(interleaved), bool(adjacent), float(eps))
+
+
+class QKNormRope(torch.nn.Module):
+    """QK-norm and rotary positions of several axes for heads of `head_dim`.
+    `sections`: pairs of each axis; frequencies theta^(-p / pairs) over all
+    pairs. norm=False leaves the rotation alone."""
+
+    def __init__(self, head_dim: int, sections, theta: float = 10000.0, eps: float = 1e-6,
+                 interleaved: bool = False, adjacent: bool = False, norm: bool = True,
+                 device=None, weight_dtype: torch.dtype = torch.float32):
+        super().__init__()
+        self.sections = tuple(int(n) for n in sections)
+        self.interleaved, self.adjacent, self.eps = interleaved, adjacent, eps
+        pairs = sum(self.sections)
+        if not 0 < 2 * pairs <= head_dim:
+            raise ValueError(f"{pairs} pairs do not fit in heads of {head_dim}")
+        freq = torch.arange(pairs, device=device, dtype=torch.float64).div_(-pairs)
+        self.inv_freq = torch.pow(theta, freq).float()
+        for name in ("q_weight", "k_weight"):
+            w = torch.ones(head_dim, device=device, dtype=weight_dtype) if norm else None
+            self.register_parameter(name, None if w is None else torch.nn.Parameter(w))
+
+    def _apply(self, fn, *args, **kwargs):
+        # the frequencies follow the module's device but stay fp32
+        super()._apply(fn, *args, **kwargs)
+        self.inv_freq = self.inv_freq.to(fn(self.inv_freq).device)
+        return self
+
+    def forward(self, q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor):
+        return qk_norm_rope(q, k, self.q_weight, self.k_weight, positions, self.inv_freq,
+                            self.sections, self.interleaved, self.adjacent, self.eps)

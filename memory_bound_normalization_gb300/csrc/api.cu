@@ -6,8 +6,10 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <utility>
 
 #include "kernels.h"
+#include "ops.h"
 
 namespace rmsn {
 
@@ -157,6 +159,177 @@ int bwd_alloc_run(const void* x, const void* w, const void* dy, const float* rst
     return st;
 }
 
+// ------------------------------------------------ rotary positions
+// Checks of the descriptor; on success fills everything of `a` that does not
+// depend on the tensors.
+int rope_descriptor(const rmsnorm_rope_t* r, int dtype, RopeArgs* a) {
+    if (r == nullptr || !dtype_known(dtype)) return RMSNORM_ERR_INVALID_ARG;
+    if (r->batch < 0 || r->length < 0 || r->q_heads < 0 || r->k_heads < 0)
+        return RMSNORM_ERR_INVALID_ARG;
+    if (r->length > INT32_MAX || (r->length > 0 && r->batch > INT32_MAX / r->length))
+        return RMSNORM_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(r->q_heads) + r->k_heads > 65536) return RMSNORM_ERR_INVALID_ARG;
+    if (r->head_dim < 2 || r->head_dim > RMSNORM_ROPE_MAX_HEAD_DIM || r->head_dim % 2 ||
+        r->rotary_dim < 2 || r->rotary_dim > r->head_dim || r->rotary_dim % 2)
+        return RMSNORM_ERR_INVALID_ARG;
+    if (r->axes < 1 || r->axes > RMSNORM_ROPE_MAX_AXES) return RMSNORM_ERR_INVALID_ARG;
+    int left[RMSNORM_ROPE_MAX_AXES];
+    int64_t sum = 0;
+    for (int i = 0; i < r->axes; ++i) {
+        if (r->sections[i] < 0) return RMSNORM_ERR_INVALID_ARG;
+        left[i] = r->sections[i];
+        sum += r->sections[i];
+    }
+    if (sum != r->rotary_dim / 2) return RMSNORM_ERR_INVALID_ARG;
+    for (int64_t v : r->position_stride)
+        if (v < 0) return RMSNORM_ERR_INVALID_ARG;
+    int next = 0;
+    for (int p = 0; p < r->rotary_dim / 2; ++p) {
+        while (left[next] == 0) next = (next + 1) % r->axes;
+        a->axis[p] = static_cast<unsigned char>(next);
+        if (--left[next] == 0 || r->interleaved) next = (next + 1) % r->axes;
+    }
+    a->tokens = r->batch * r->length;
+    a->length = static_cast<int>(r->length);
+    a->head_dim = r->head_dim;
+    a->rot = r->rotary_dim;
+    a->pos64 = r->positions_64 != 0;
+    a->w_f32 = weight_size(dtype) == 4;
+    for (int i = 0; i < 3; ++i) a->ps[i] = r->position_stride[i];
+    a->t[0].heads = r->q_heads;
+    a->t[1].heads = r->k_heads;
+    return RMSNORM_OK;
+}
+
+// A tensor of a rotary call: non-null, aligned to its elements, strides not
+// negative.
+int rope_tensor(const void* p, const rmsnorm_strides_t& s, int size, int64_t (&out)[3]) {
+    if (p == nullptr || s.batch < 0 || s.token < 0 || s.head < 0) return RMSNORM_ERR_INVALID_ARG;
+    if (!aligned(p, size)) return RMSNORM_ERR_MISALIGNED;
+    out[0] = s.batch;
+    out[1] = s.token;
+    out[2] = s.head;
+    return RMSNORM_OK;
+}
+
+// Both directions of the rotary call, the descriptor checked and tokens > 0.
+// Without weights the backward is the forward of the gradient with the angle
+// turned back.
+int rope_run(const rmsnorm_rope_t* r, RopeArgs& a, const void* q, const void* k, const void* wq,
+             const void* wk, const void* positions, const float* inv_freq, const void* dq_out,
+             const void* dk_out, void* oq, void* ok, float* dwq, float* dwk, float eps, int dtype,
+             bool bwd, cudaStream_t stream) {
+    const int sz = dtype_size(dtype), wsz = weight_size(dtype);
+    const bool has[2] = {a.t[0].heads > 0, a.t[1].heads > 0};
+    const void* w[2] = {wq, wk};
+    float* dw[2] = {dwq, dwk};
+    if (has[0] && has[1] && (wq == nullptr) != (wk == nullptr)) return RMSNORM_ERR_INVALID_ARG;
+    const bool norm = (has[0] ? wq : wk) != nullptr;
+    if (positions == nullptr || inv_freq == nullptr) return RMSNORM_ERR_INVALID_ARG;
+    const void* x[2] = {q, k};
+    const void* dy[2] = {dq_out, dk_out};
+    void* o[2] = {oq, ok};
+    const rmsnorm_strides_t* xs[2] = {&r->q, &r->k};
+    const rmsnorm_strides_t* ys[2] = {&r->q_out, &r->k_out};
+    const rmsnorm_strides_t* ds[2] = {&r->dq, &r->dk};
+    for (int i = 0; i < 2; ++i) {
+        if (!has[i]) continue;
+        RopeTensor& t = a.t[i];
+        int st;
+        if (!bwd || norm) {
+            st = rope_tensor(x[i], *xs[i], sz, t.xs);
+            if (st != RMSNORM_OK) return st;
+            t.x = x[i];
+        }
+        if (bwd) {
+            st = rope_tensor(dy[i], *ys[i], sz, norm ? t.dys : t.xs);
+            if (st != RMSNORM_OK) return st;
+            (norm ? t.dy : t.x) = dy[i];
+        }
+        st = rope_tensor(o[i], bwd ? *ds[i] : *ys[i], sz, t.os);
+        if (st != RMSNORM_OK) return st;
+        t.out = o[i];
+        if (norm) {
+            if (bwd && dw[i] == nullptr) return RMSNORM_ERR_INVALID_ARG;
+            if (!aligned(w[i], wsz)) return RMSNORM_ERR_MISALIGNED;
+            t.w = w[i];
+            t.dw = dw[i];
+        }
+    }
+    if (!aligned(positions, a.pos64 ? 8 : 4) || !aligned(inv_freq, 4)) return RMSNORM_ERR_MISALIGNED;
+    // a call without queries has its keys first
+    if (!has[0]) std::swap(a.t[0], a.t[1]);
+    a.pos = positions;
+    a.inv_freq = inv_freq;
+    a.eps = eps;
+    a.sign = bwd ? -1.f : 1.f;
+    const DeviceInfo* dev = nullptr;
+    int st = current_device(&dev);
+    if (st != RMSNORM_OK) return st;
+    a.status = dev->status_word;
+    const bool adjacent = r->adjacent != 0;
+    if (!bwd || !norm) return cuda_status(rope_fwd_launch(*dev, dtype, adjacent, a, stream));
+    int rows[2];
+    st = cuda_status(rope_bwd_rows(*dev, dtype, adjacent, a, rows));
+    if (st != RMSNORM_OK) return st;
+    void* ws = nullptr;
+    const size_t need = static_cast<size_t>(rows[0] + rows[1]) * a.head_dim * 4;
+    if (cuda_status(cudaMallocAsync(&ws, need, stream)) != RMSNORM_OK) return RMSNORM_ERR_NOMEM;
+    a.partial = static_cast<float*>(ws);
+    st = cuda_status(rope_bwd_launch(*dev, dtype, adjacent, a, rows, stream));
+    const int freed = cuda_status(cudaFreeAsync(ws, stream));
+    return st != RMSNORM_OK ? st : freed;
+}
+
+// ------------------------------------------------------- group norm
+int group_norm_run(bool bwd, GroupNormArgs& a, int64_t C, int64_t G, int dtype,
+                   cudaStream_t stream) {
+    if (!dtype_known(dtype) || a.B < 0 || a.S < 0 || C <= 0 || C > INT32_MAX || G <= 0 || C % G)
+        return RMSNORM_ERR_INVALID_ARG;
+    if (a.act < RMSNORM_ACT_NONE || a.act > RMSNORM_ACT_GELU) return RMSNORM_ERR_INVALID_ARG;
+    if (a.S > INT32_MAX / (C / G)) return RMSNORM_ERR_INVALID_ARG;
+    a.C = static_cast<int>(C);
+    a.G = static_cast<int>(G);
+    const int sz = dtype_size(dtype), wsz = weight_size(dtype);
+    if (!aligned(a.mean, 4) || !aligned(a.rstd, 4) || !aligned(a.dw, 4) || !aligned(a.db, 4))
+        return RMSNORM_ERR_MISALIGNED;
+    if (a.B == 0 || a.S == 0) {
+        for (float* p : {a.dw, a.db})
+            if (p != nullptr) {
+                const int st = cuda_status(cudaMemsetAsync(p, 0, static_cast<size_t>(C) * 4, stream));
+                if (st != RMSNORM_OK) return st;
+            }
+        return RMSNORM_OK;
+    }
+    if (a.x == nullptr || a.out == nullptr || a.mean == nullptr || a.rstd == nullptr ||
+        (bwd && a.dy == nullptr) || (a.w == nullptr) != (a.b == nullptr) ||
+        (bwd && a.w != nullptr && (a.dw == nullptr || a.db == nullptr)))
+        return RMSNORM_ERR_INVALID_ARG;
+    if (!aligned(a.x, sz) || !aligned(a.out, sz) || !aligned(a.dy, sz) || !aligned(a.w, wsz) ||
+        !aligned(a.b, wsz))
+        return RMSNORM_ERR_MISALIGNED;
+    if (a.B > INT64_MAX / 16 / a.S / C) return RMSNORM_ERR_INVALID_ARG;
+    if (bwd && a.w == nullptr) a.dw = a.db = nullptr;
+    a.w_f32 = wsz == 4;
+    const bool vec = aligned(a.x, 16) && aligned(a.out, 16) && aligned(a.dy, 16) && (C * sz) % 16 == 0;
+    const DeviceInfo* dev = nullptr;
+    int st = current_device(&dev);
+    if (st != RMSNORM_OK) return st;
+    a.status = dev->status_word;
+    a.wait_limit_ns = g_wait_limit_ns.load();
+    const size_t need = group_norm_workspace(*dev, dtype, vec, bwd, a);
+    void* ws = nullptr;
+    if (need > 0 && cuda_status(cudaMallocAsync(&ws, need, stream)) != RMSNORM_OK)
+        return RMSNORM_ERR_NOMEM;
+    const cudaError_t err = group_norm_launch(*dev, dtype, vec, bwd, a, ws, stream);
+    st = err == cudaErrorInvalidValue ? (cudaGetLastError(), RMSNORM_ERR_UNSUPPORTED) : cuda_status(err);
+    if (ws != nullptr) {
+        const int freed = cuda_status(cudaFreeAsync(ws, stream));
+        if (st == RMSNORM_OK) st = freed;
+    }
+    return st;
+}
+
 }  // namespace
 
 int pdl_mode() {
@@ -284,6 +457,78 @@ int rmsnorm_bwd_naive(const void* x, const void* w, const void* dy, void* dx, fl
     const int freed = cuda_status(cudaFreeAsync(ws, stream));
     if (st == RMSNORM_OK) st = freed;
     return st;
+}
+
+int rmsnorm_qk_rope_fwd(const rmsnorm_rope_t* rope, const void* q, const void* k, const void* wq,
+                        const void* wk, const void* positions, const float* inv_freq, void* q_out,
+                        void* k_out, float eps, int dtype, cudaStream_t stream) {
+    RopeArgs a{};
+    int st = rope_descriptor(rope, dtype, &a);
+    if (st != RMSNORM_OK) return st;
+    if (!(eps >= 0.f)) return RMSNORM_ERR_INVALID_ARG;
+    if (a.tokens == 0 || a.t[0].heads + a.t[1].heads == 0) return RMSNORM_OK;
+    return rope_run(rope, a, q, k, wq, wk, positions, inv_freq, nullptr, nullptr, q_out, k_out,
+                    nullptr, nullptr, eps, dtype, false, stream);
+}
+
+int rmsnorm_qk_rope_bwd(const rmsnorm_rope_t* rope, const void* q, const void* k, const void* wq,
+                        const void* wk, const void* positions, const float* inv_freq,
+                        const void* dq_out, const void* dk_out, void* dq, void* dk, float* dwq,
+                        float* dwk, float eps, int dtype, cudaStream_t stream) {
+    RopeArgs a{};
+    int st = rope_descriptor(rope, dtype, &a);
+    if (st != RMSNORM_OK) return st;
+    if (!(eps >= 0.f)) return RMSNORM_ERR_INVALID_ARG;
+    if (!aligned(dwq, 4) || !aligned(dwk, 4)) return RMSNORM_ERR_MISALIGNED;
+    if (a.tokens == 0 || a.t[0].heads + a.t[1].heads == 0) {
+        float* dws[2] = {a.t[0].heads ? dwq : nullptr, a.t[1].heads ? dwk : nullptr};
+        for (float* p : dws)
+            if (p != nullptr) {
+                st = cuda_status(cudaMemsetAsync(p, 0, static_cast<size_t>(a.head_dim) * 4, stream));
+                if (st != RMSNORM_OK) return st;
+            }
+        return RMSNORM_OK;
+    }
+    return rope_run(rope, a, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk,
+                    eps, dtype, true, stream);
+}
+
+int rmsnorm_group_norm_fwd(const void* x, const void* w, const void* b, void* y, float* mean,
+                           float* rstd, int64_t B, int64_t S, int64_t C, int64_t G, float eps,
+                           int act, int dtype, cudaStream_t stream) {
+    if (!(eps >= 0.f)) return RMSNORM_ERR_INVALID_ARG;
+    GroupNormArgs a{};
+    a.x = x;
+    a.w = w;
+    a.b = b;
+    a.out = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.B = B;
+    a.S = S;
+    a.eps = eps;
+    a.act = act;
+    return group_norm_run(false, a, C, G, dtype, stream);
+}
+
+int rmsnorm_group_norm_bwd(const void* x, const void* w, const void* b, const void* dy,
+                           const float* mean, const float* rstd, void* dx, float* dw, float* db,
+                           int64_t B, int64_t S, int64_t C, int64_t G, int act, int dtype,
+                           cudaStream_t stream) {
+    GroupNormArgs a{};
+    a.x = x;
+    a.w = w;
+    a.b = b;
+    a.dy = dy;
+    a.out = dx;
+    a.mean = const_cast<float*>(mean);  // only read in this direction
+    a.rstd = const_cast<float*>(rstd);
+    a.dw = dw;
+    a.db = db;
+    a.B = B;
+    a.S = S;
+    a.act = act;
+    return group_norm_run(true, a, C, G, dtype, stream);
 }
 
 int rmsnorm_get_last_device_error(cudaStream_t stream) {

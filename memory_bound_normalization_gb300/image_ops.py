@@ -1,0 +1,257 @@
+"""Group norm with an activation, and the query/key norm with rotary positions
+of several axes: tensor-level calls of the C ABI (rmsnorm_group_norm_*,
+rmsnorm_qk_rope_* in include/rmsnorm.h).
+
+The functions check their arguments, allocate outputs with PyTorch and raise
+``RMSNormError`` on a non-OK status, like ``forward`` and ``backward``. They
+run on the tensors' own device and, unless ``stream`` is given, on its current
+stream. ``autograd`` holds the differentiable forms.
+"""
+from __future__ import annotations
+
+import struct
+
+from . import _lib
+from ._lib import ERR_INVALID_ARG, RMSNormError, check
+
+ACTIVATIONS = {"none": _lib.ACT_NONE, "silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU}
+
+# rmsnorm_rope_t: 2 int64, 12 int32, 3 + 18 int64 (no padding)
+_ROPE = struct.Struct("=2q12i21q")
+
+
+def _refuse(what: str):
+    raise RMSNormError(ERR_INVALID_ARG, what)
+
+
+def _codes(dtype, w_dtype):
+    from . import dtype_code
+
+    return dtype_code(dtype, w_dtype)
+
+
+class _On:
+    """The device of the call made current for it, where it is not already."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        import torch
+
+        self.guard = None
+        if device.type == "cuda" and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            _refuse(f"{name} is on {t.device}, the input on {device}")
+
+
+# ------------------------------------------------------------- group norm
+def _group_norm_shape(x, num_groups, weight, bias, activation):
+    if x.dim() < 2:
+        _refuse(f"group norm of a tensor of {x.dim()} dimensions: expected [B, ..., C]")
+    if activation not in ACTIVATIONS:
+        _refuse(f"activation {activation!r}: one of {', '.join(ACTIVATIONS)}")
+    B, C = x.shape[0], x.shape[-1]
+    if num_groups < 1 or C % num_groups or C == 0:
+        _refuse(f"{C} channels in {num_groups} groups")
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    if (weight is None) != (bias is None):
+        _refuse("group norm takes a weight and a bias, or neither")
+    if weight is not None:
+        if weight.shape != (C,) or bias.shape != (C,):
+            _refuse(f"weight {tuple(weight.shape)} and bias {tuple(bias.shape)} of {C} channels")
+        if weight.dtype != bias.dtype:
+            _refuse(f"weight {weight.dtype} and bias {bias.dtype} differ")
+    return B, S, C
+
+
+def group_norm_forward(x, num_groups: int, weight=None, bias=None, eps: float = 1e-5,
+                       activation: str = "none", stream=None):
+    """y, mean, rstd of act(group_norm(x) * weight + bias), x [B, ..., C]
+    contiguous with the channels last; mean and rstd fp32 [B, num_groups].
+    activation: "none", "silu" or "gelu" (exact). An NCHW tensor in
+    channels_last memory format passes as x.permute(0, 2, 3, 1)."""
+    import torch
+
+    B, S, C = _group_norm_shape(x, num_groups, weight, bias, activation)
+    dev = x.device
+    _same_device(dev, weight=weight, bias=bias)
+    code = _codes(x.dtype, None if weight is None else weight.dtype)
+    with _On(dev):
+        y = torch.empty_like(x)
+        mean = torch.empty((B, num_groups), dtype=torch.float32, device=dev)
+        rstd = torch.empty((B, num_groups), dtype=torch.float32, device=dev)
+        check(_lib.rmsnorm_group_norm_fwd(x, weight, bias, y, mean, rstd, B, S, C, num_groups, eps,
+                                          ACTIVATIONS[activation], code, stream),
+              "rmsnorm_group_norm_fwd")
+    return y, mean, rstd
+
+
+def group_norm_backward(x, num_groups: int, weight, bias, dy, mean, rstd,
+                        activation: str = "none", stream=None):
+    """dx, dweight, dbias (fp32; None without a weight) from the forward's mean
+    and rstd."""
+    import torch
+
+    B, S, C = _group_norm_shape(x, num_groups, weight, bias, activation)
+    dev = x.device
+    _same_device(dev, weight=weight, bias=bias, dy=dy, mean=mean, rstd=rstd)
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        _refuse(f"dy {tuple(dy.shape)} {dy.dtype} of x {tuple(x.shape)} {x.dtype}")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.shape != (B, num_groups) or t.dtype != torch.float32:
+            _refuse(f"{name} {tuple(t.shape)} {t.dtype}: expected fp32 {(B, num_groups)}")
+    code = _codes(x.dtype, None if weight is None else weight.dtype)
+    with _On(dev):
+        dx = torch.empty_like(x)
+        dw = db = None
+        if weight is not None:
+            dw = torch.empty(C, dtype=torch.float32, device=dev)
+            db = torch.empty(C, dtype=torch.float32, device=dev)
+        check(_lib.rmsnorm_group_norm_bwd(x, weight, bias, dy, mean, rstd, dx, dw, db, B, S, C,
+                                          num_groups, ACTIVATIONS[activation], code, stream),
+              "rmsnorm_group_norm_bwd")
+    return dx, dw, db
+
+
+# ------------------------------------------------- rotary positions, QK-norm
+def _strides(t):
+    """(batch, token, head) strides of [T, H, D] or [B, T, H, D]."""
+    s = t.stride()
+    if s[-1] != 1:
+        raise ValueError("the last dimension of a head is not dense (call .contiguous() first)")
+    return (s[-4] if len(s) == 4 else 0, s[-3], s[-2])
+
+
+_NONE = (0, 0, 0)
+
+
+def _rope_shape(q, k, wq, wk, positions, inv_freq, sections):
+    import torch
+
+    if q.dim() not in (3, 4):
+        _refuse(f"queries of {q.dim()} dimensions: expected [T, H, D] or [B, T, H, D]")
+    dev = q.device
+    _same_device(dev, k=k, wq=wq, wk=wk, positions=positions, inv_freq=inv_freq)
+    D = q.shape[-1]
+    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or
+                          k.shape[-1] != D or k.dtype != q.dtype):
+        _refuse(f"keys {tuple(k.shape)} {k.dtype} of queries {tuple(q.shape)} {q.dtype}")
+    if k is None:
+        if wk is not None:
+            _refuse("a key weight without keys")
+    elif (wq is None) != (wk is None):
+        _refuse("weights for queries and keys, or for neither")
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None and (w.shape != (D,) or w.dtype != wq.dtype):
+            _refuse(f"{name} {tuple(w.shape)} {w.dtype} of heads of {D}")
+    lead = tuple(q.shape[:-2])
+    B, T = lead if len(lead) == 2 else (1, lead[0])
+    axes = len(sections)
+    if not 1 <= axes <= _lib.ROPE_MAX_AXES:
+        _refuse(f"{axes} position axes: 1 to {_lib.ROPE_MAX_AXES}")
+    if positions.dtype not in (torch.int32, torch.int64):
+        _refuse(f"positions of {positions.dtype}: int32 or int64")
+    shape = tuple(positions.shape)
+    if shape not in ((axes,) + lead, (axes, T)):
+        _refuse(f"positions {shape} of {axes} axes and tokens {lead}")
+    ps = positions.stride()
+    ps = (ps[0], ps[1], ps[2]) if len(shape) == 3 else (ps[0], 0, ps[1])
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.numel() != sum(sections):
+        _refuse(f"inv_freq {tuple(inv_freq.shape)} {inv_freq.dtype}: expected fp32, a value for "
+                f"each of {sum(sections)} pairs")
+    code = _codes(q.dtype, None if wq is None else wq.dtype)
+    head = (B, T, q.shape[-2], 0 if k is None else k.shape[-2], D, 2 * inv_freq.numel(), axes,
+            *sections, *((0,) * (_lib.ROPE_MAX_AXES - axes)))
+    return head, positions.dtype == torch.int64, ps, code, dev
+
+
+def _pack(head, interleaved, adjacent, pos64, ps, *strides):
+    try:
+        return _ROPE.pack(*head, bool(interleaved), bool(adjacent), pos64, *ps,
+                          *(v for s in strides for v in s))
+    except struct.error as e:
+        _refuse(f"rotary descriptor: {e}")
+
+
+def _like(name, t, of):
+    if t.shape != of.shape or t.dtype != of.dtype or t.device != of.device:
+        _refuse(f"{name} {tuple(t.shape)} {t.dtype} on {t.device}: expected {tuple(of.shape)} "
+                f"{of.dtype} on {of.device}")
+
+
+def qk_rope_forward(q, k, wq, wk, positions, inv_freq, sections, interleaved: bool = False,
+                    adjacent: bool = False, eps: float = 1e-6, out=None, stream=None):
+    """q_out, k_out: RMSNorm of each head (weights wq, wk [D]; None: no norm),
+    then 2 * len(inv_freq) elements of it turned by positions * inv_freq.
+
+    q [T, Hq, D] or [B, T, Hq, D], k likewise with Hk heads (or None), strided
+    views allowed as long as a head is dense; positions int32 or int64
+    [axes, T] or [axes, B, T]; sections: pairs of each axis, in blocks, or
+    dealt in turn with `interleaved`; `adjacent` pairs elements (2p, 2p+1)
+    instead of (p, p + rotary/2). `out` gives the output tensors, (q, k) itself
+    for an update in place."""
+    import torch
+
+    head, pos64, ps, code, dev = _rope_shape(q, k, wq, wk, positions, inv_freq, sections)
+    with _On(dev):
+        if out is None:
+            qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev)
+        else:
+            qo, ko = out
+            _like("out of the queries", qo, q)
+            if (ko is None) != (k is None):
+                _refuse("an output for the keys where there are keys")
+            if k is not None:
+                _like("out of the keys", ko, k)
+        desc = _pack(head, interleaved, adjacent, pos64, ps, _strides(q),
+                     _NONE if k is None else _strides(k), _strides(qo),
+                     _NONE if k is None else _strides(ko), _NONE, _NONE)
+        check(_lib.rmsnorm_qk_rope_fwd(desc, q, k, wq, wk, positions, inv_freq, qo, ko, eps, code,
+                                       stream), "rmsnorm_qk_rope_fwd")
+    return qo, ko
+
+
+def qk_rope_backward(q, k, wq, wk, positions, inv_freq, sections, dq_out, dk_out,
+                     interleaved: bool = False, adjacent: bool = False, eps: float = 1e-6,
+                     stream=None):
+    """dq, dk, dwq, dwk (fp32; None without weights) from the forward's inputs
+    and the gradients of its outputs."""
+    import torch
+
+    head, pos64, ps, code, dev = _rope_shape(q, k, wq, wk, positions, inv_freq, sections)
+    _like("dq_out", dq_out, q)
+    if (dk_out is None) != (k is None):
+        _refuse("a gradient for the keys where there are keys")
+    if k is not None:
+        _like("dk_out", dk_out, k)
+    with _On(dev):
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        dk = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev)
+        dwq = dwk = None
+        if wq is not None:
+            dwq = torch.empty(wq.shape, dtype=torch.float32, device=dev)
+            if k is not None:
+                dwk = torch.empty(wq.shape, dtype=torch.float32, device=dev)
+        desc = _pack(head, interleaved, adjacent, pos64, ps, _strides(q),
+                     _NONE if k is None else _strides(k), _strides(dq_out),
+                     _NONE if k is None else _strides(dk_out), _strides(dq),
+                     _NONE if k is None else _strides(dk))
+        check(_lib.rmsnorm_qk_rope_bwd(desc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq,
+                                       dk, dwq, dwk, eps, code, stream), "rmsnorm_qk_rope_bwd")
+    return dq, dk, dwq, dwk
