@@ -308,6 +308,25 @@ int rmsnorm_qk_rope_bwd(const rmsnorm_rope_t *rope, const void *q,
                         void *dk, float *dwq, float *dwk, float eps, int dtype,
                         cudaStream_t stream);
 
+/*
+ * rmsnorm_qk_rope_bwd with a caller-provided workspace: device memory of at
+ * least rmsnorm_qk_rope_bwd_workspace_size(head_dim, device) bytes, 16-byte
+ * aligned, not shared with another call in flight; smaller or NULL
+ * (with weights and tokens) returns RMSNORM_ERR_INVALID_ARG, misaligned
+ * RMSNORM_ERR_MISALIGNED. Allocates nothing.
+ */
+int rmsnorm_qk_rope_bwd_ws(const rmsnorm_rope_t *rope, const void *q,
+                           const void *k, const void *wq, const void *wk,
+                           const void *positions, const float *inv_freq,
+                           const void *dq_out, const void *dk_out, void *dq,
+                           void *dk, float *dwq, float *dwk, float eps,
+                           int dtype, void *workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+/* Bytes of workspace rmsnorm_qk_rope_bwd_ws needs for heads of head_dim on
+   `device` (a CUDA ordinal), whatever the tokens and heads; 0 if invalid. */
+size_t rmsnorm_qk_rope_bwd_workspace_size(int head_dim, int device);
+
 /* Activation applied after a group norm's affine map. */
 typedef enum {
     RMSNORM_ACT_NONE = 0,
@@ -351,6 +370,35 @@ int rmsnorm_group_norm_bwd(const void *x, const void *w, const void *b,
                            const float *rstd, void *dx, float *dw, float *db,
                            int64_t B, int64_t S, int64_t C, int64_t G, int act,
                            int dtype, cudaStream_t stream);
+
+/*
+ * rmsnorm_group_norm_fwd and _bwd with a caller-provided workspace: device
+ * memory of at least rmsnorm_group_norm_workspace_size(B, S, C, G, dtype,
+ * backward, current device) bytes, 16-byte aligned, not shared with another
+ * call in flight. A smaller or NULL one where some is needed returns
+ * RMSNORM_ERR_INVALID_ARG, a misaligned one RMSNORM_ERR_MISALIGNED. They
+ * allocate nothing.
+ */
+int rmsnorm_group_norm_fwd_ws(const void *x, const void *w, const void *b,
+                              void *y, float *mean, float *rstd, int64_t B,
+                              int64_t S, int64_t C, int64_t G, float eps,
+                              int act, int dtype, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+int rmsnorm_group_norm_bwd_ws(const void *x, const void *w, const void *b,
+                              const void *dy, const float *mean,
+                              const float *rstd, void *dx, float *dw,
+                              float *db, int64_t B, int64_t S, int64_t C,
+                              int64_t G, int act, int dtype, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Bytes of workspace the calls above need for this shape on `device` (a CUDA
+ * ordinal), whatever the alignment of the tensors; `backward` is 0 or 1. 0
+ * when none is needed or the arguments are invalid.
+ */
+size_t rmsnorm_group_norm_workspace_size(int64_t B, int64_t S, int64_t C,
+                                         int64_t G, int dtype, int backward,
+                                         int device);
 
 /*
  * Device-side status. Every wait inside the kernels (on a bulk copy landing

@@ -60,11 +60,16 @@ from ._lib import (  # noqa: F401
     rmsnorm_fwd,
     rmsnorm_get_last_device_error,
     rmsnorm_group_norm_bwd,
+    rmsnorm_group_norm_bwd_ws,
     rmsnorm_group_norm_fwd,
+    rmsnorm_group_norm_fwd_ws,
+    rmsnorm_group_norm_workspace_size,
     rmsnorm_noalloc_scratch_bytes,
     rmsnorm_plan,
     rmsnorm_probe,
     rmsnorm_qk_rope_bwd,
+    rmsnorm_qk_rope_bwd_workspace_size,
+    rmsnorm_qk_rope_bwd_ws,
     rmsnorm_qk_rope_fwd,
     rmsnorm_set_wait_limit_ns,
     rmsnorm_status_string,

@@ -70,8 +70,13 @@ EXPORTS = (
     "rmsnorm_bwd_naive",
     "rmsnorm_qk_rope_fwd",
     "rmsnorm_qk_rope_bwd",
+    "rmsnorm_qk_rope_bwd_ws",
+    "rmsnorm_qk_rope_bwd_workspace_size",
     "rmsnorm_group_norm_fwd",
     "rmsnorm_group_norm_bwd",
+    "rmsnorm_group_norm_fwd_ws",
+    "rmsnorm_group_norm_bwd_ws",
+    "rmsnorm_group_norm_workspace_size",
     "rmsnorm_get_last_device_error",
     "rmsnorm_status_string",
     "rmsnorm_set_wait_limit_ns",
@@ -186,6 +191,13 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.rmsnorm_bwd_naive.argtypes = [vp, vp, vp, vp, vp, i64, i64, f, i, vp]
         lib.rmsnorm_qk_rope_fwd.argtypes = [vp] * 9 + [f, i, vp]
         lib.rmsnorm_qk_rope_bwd.argtypes = [vp] * 13 + [f, i, vp]
+        lib.rmsnorm_qk_rope_bwd_ws.argtypes = [vp] * 13 + [f, i, vp, sz, vp]
+        lib.rmsnorm_qk_rope_bwd_workspace_size.argtypes = [i, i]
+        lib.rmsnorm_qk_rope_bwd_workspace_size.restype = sz
+        lib.rmsnorm_group_norm_fwd_ws.argtypes = [vp] * 6 + [i64] * 4 + [f, i, i, vp, sz, vp]
+        lib.rmsnorm_group_norm_bwd_ws.argtypes = [vp] * 9 + [i64] * 4 + [i, i, vp, sz, vp]
+        lib.rmsnorm_group_norm_workspace_size.argtypes = [i64] * 4 + [i, i, i]
+        lib.rmsnorm_group_norm_workspace_size.restype = sz
         lib.rmsnorm_group_norm_fwd.argtypes = [vp] * 6 + [i64] * 4 + [f, i, i, vp]
         lib.rmsnorm_group_norm_bwd.argtypes = [vp] * 9 + [i64] * 4 + [i, i, vp]
         lib.rmsnorm_get_last_device_error.argtypes = [vp]
@@ -202,7 +214,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         for name in ("rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_bwd_ws", "rmsnorm_add_fwd",
                      "rmsnorm_add_bwd", "rmsnorm_bwd_noalloc", "rmsnorm_bwd_naive",
                      "rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_group_norm_fwd",
-                     "rmsnorm_group_norm_bwd",
+                     "rmsnorm_group_norm_bwd", "rmsnorm_qk_rope_bwd_ws",
+                     "rmsnorm_group_norm_fwd_ws", "rmsnorm_group_norm_bwd_ws",
                      "rmsnorm_get_last_device_error",
                      "rmsnorm_probe", "rmsnorm_plan"):
             getattr(lib, name).restype = ctypes.c_int
@@ -230,7 +243,8 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a Stream object for it takes 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -316,6 +330,20 @@ def rmsnorm_qk_rope_bwd(rope, q, k, wq, wk, positions, inv_freq, dq_out, dk_out,
         _strided_ptr(dq), _strided_ptr(dk), _ptr(dwq), _ptr(dwk), eps, dtype, _stream(stream))
 
 
+def rmsnorm_qk_rope_bwd_ws(rope, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq,
+                           dwk, eps: float, dtype: int, workspace, workspace_bytes: int,
+                           stream=None) -> int:
+    return load_library().rmsnorm_qk_rope_bwd_ws(
+        _rope_ptr(rope), _strided_ptr(q), _strided_ptr(k), _ptr(wq), _ptr(wk),
+        _strided_ptr(positions), _ptr(inv_freq), _strided_ptr(dq_out), _strided_ptr(dk_out),
+        _strided_ptr(dq), _strided_ptr(dk), _ptr(dwq), _ptr(dwk), eps, dtype, _ptr(workspace),
+        workspace_bytes, _stream(stream))
+
+
+def rmsnorm_qk_rope_bwd_workspace_size(head_dim: int, device: int) -> int:
+    return load_library().rmsnorm_qk_rope_bwd_workspace_size(head_dim, device)
+
+
 def _rope_ptr(rope):
     if isinstance(rope, Rope):
         return ctypes.addressof(rope)
@@ -336,6 +364,27 @@ def rmsnorm_group_norm_bwd(x, w, b, dy, mean, rstd, dx, dw, db, B: int, S: int, 
     return load_library().rmsnorm_group_norm_bwd(_ptr(x), _ptr(w), _ptr(b), _ptr(dy), _ptr(mean),
                                                  _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db), B, S, C,
                                                  G, act, dtype, _stream(stream))
+
+
+def rmsnorm_group_norm_fwd_ws(x, w, b, y, mean, rstd, B: int, S: int, C: int, G: int, eps: float,
+                              act: int, dtype: int, workspace, workspace_bytes: int,
+                              stream=None) -> int:
+    return load_library().rmsnorm_group_norm_fwd_ws(
+        _ptr(x), _ptr(w), _ptr(b), _ptr(y), _ptr(mean), _ptr(rstd), B, S, C, G, eps, act, dtype,
+        _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def rmsnorm_group_norm_bwd_ws(x, w, b, dy, mean, rstd, dx, dw, db, B: int, S: int, C: int, G: int,
+                              act: int, dtype: int, workspace, workspace_bytes: int,
+                              stream=None) -> int:
+    return load_library().rmsnorm_group_norm_bwd_ws(
+        _ptr(x), _ptr(w), _ptr(b), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db),
+        B, S, C, G, act, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def rmsnorm_group_norm_workspace_size(B: int, S: int, C: int, G: int, dtype: int, backward: int,
+                                      device: int) -> int:
+    return load_library().rmsnorm_group_norm_workspace_size(B, S, C, G, dtype, backward, device)
 
 
 def rmsnorm_get_last_device_error(stream=None) -> int:

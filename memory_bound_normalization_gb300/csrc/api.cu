@@ -1,6 +1,7 @@
 // C ABI of librmsnorm.so (declared in include/rmsnorm.h): argument checks,
 // per-device properties, the device status word, workspace handling and
 // dispatch to the kernel translation units.
+#include <algorithm>
 #include <atomic>
 #include <cstdlib>
 #include <cmath>
@@ -159,6 +160,27 @@ int bwd_alloc_run(const void* x, const void* w, const void* dy, const float* rst
     return st;
 }
 
+// Workspace of a call: the caller's, or one from the stream-ordered allocator.
+struct Workspace {
+    void* p = nullptr;
+    size_t bytes = 0;
+    bool given = false;
+
+    int take(size_t need, cudaStream_t s) {
+        if (given) {
+            if (need > 0 && (p == nullptr || bytes < need)) return RMSNORM_ERR_INVALID_ARG;
+            return aligned(p, 16) ? RMSNORM_OK : RMSNORM_ERR_MISALIGNED;
+        }
+        if (need == 0) return RMSNORM_OK;
+        return cuda_status(cudaMallocAsync(&p, need, s)) == RMSNORM_OK ? RMSNORM_OK : RMSNORM_ERR_NOMEM;
+    }
+    int give(int status, cudaStream_t s) {
+        if (given || p == nullptr) return status;
+        const int freed = cuda_status(cudaFreeAsync(p, s));
+        return status != RMSNORM_OK ? status : freed;
+    }
+};
+
 // ------------------------------------------------ rotary positions
 // Checks of the descriptor; on success fills everything of `a` that does not
 // depend on the tensors.
@@ -218,7 +240,7 @@ int rope_tensor(const void* p, const rmsnorm_strides_t& s, int size, int64_t (&o
 int rope_run(const rmsnorm_rope_t* r, RopeArgs& a, const void* q, const void* k, const void* wq,
              const void* wk, const void* positions, const float* inv_freq, const void* dq_out,
              const void* dk_out, void* oq, void* ok, float* dwq, float* dwk, float eps, int dtype,
-             bool bwd, cudaStream_t stream) {
+             bool bwd, const Workspace& given, cudaStream_t stream) {
     const int sz = dtype_size(dtype), wsz = weight_size(dtype);
     const bool has[2] = {a.t[0].heads > 0, a.t[1].heads > 0};
     const void* w[2] = {wq, wk};
@@ -272,31 +294,59 @@ int rope_run(const rmsnorm_rope_t* r, RopeArgs& a, const void* q, const void* k,
     int rows[2];
     st = cuda_status(rope_bwd_rows(*dev, dtype, adjacent, a, rows));
     if (st != RMSNORM_OK) return st;
-    void* ws = nullptr;
-    const size_t need = static_cast<size_t>(rows[0] + rows[1]) * a.head_dim * 4;
-    if (cuda_status(cudaMallocAsync(&ws, need, stream)) != RMSNORM_OK) return RMSNORM_ERR_NOMEM;
-    a.partial = static_cast<float*>(ws);
+    Workspace ws = given;
+    st = ws.take(static_cast<size_t>(rows[0] + rows[1]) * a.head_dim * 4, stream);
+    if (st != RMSNORM_OK) return st;
+    a.partial = static_cast<float*>(ws.p);
     st = cuda_status(rope_bwd_launch(*dev, dtype, adjacent, a, rows, stream));
-    const int freed = cuda_status(cudaFreeAsync(ws, stream));
-    return st != RMSNORM_OK ? st : freed;
+    return ws.give(st, stream);
+}
+
+int rope_bwd_any(const rmsnorm_rope_t* rope, const void* q, const void* k, const void* wq,
+                 const void* wk, const void* positions, const float* inv_freq, const void* dq_out,
+                 const void* dk_out, void* dq, void* dk, float* dwq, float* dwk, float eps,
+                 int dtype, const Workspace& ws, cudaStream_t stream) {
+    RopeArgs a{};
+    int st = rope_descriptor(rope, dtype, &a);
+    if (st != RMSNORM_OK) return st;
+    if (!(eps >= 0.f)) return RMSNORM_ERR_INVALID_ARG;
+    if (!aligned(dwq, 4) || !aligned(dwk, 4)) return RMSNORM_ERR_MISALIGNED;
+    if (a.tokens == 0 || a.t[0].heads + a.t[1].heads == 0) {
+        float* dws[2] = {a.t[0].heads ? dwq : nullptr, a.t[1].heads ? dwk : nullptr};
+        for (float* p : dws)
+            if (p != nullptr) {
+                st = cuda_status(cudaMemsetAsync(p, 0, static_cast<size_t>(a.head_dim) * 4, stream));
+                if (st != RMSNORM_OK) return st;
+            }
+        return RMSNORM_OK;
+    }
+    return rope_run(rope, a, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk,
+                    eps, dtype, true, ws, stream);
 }
 
 // ------------------------------------------------------- group norm
-int group_norm_run(bool bwd, GroupNormArgs& a, int64_t C, int64_t G, int dtype,
-                   cudaStream_t stream) {
-    if (!dtype_known(dtype) || a.B < 0 || a.S < 0 || C <= 0 || C > INT32_MAX || G <= 0 || C % G)
+int group_norm_shape(GroupNormArgs* a, int64_t C, int64_t G, int dtype) {
+    if (!dtype_known(dtype) || a->B < 0 || a->S < 0 || C <= 0 || C > INT32_MAX || G <= 0 || C % G)
         return RMSNORM_ERR_INVALID_ARG;
+    if (a->S > INT32_MAX / (C / G)) return RMSNORM_ERR_INVALID_ARG;
+    if (a->S > 0 && a->B > INT64_MAX / 16 / a->S / C) return RMSNORM_ERR_INVALID_ARG;
+    a->C = static_cast<int>(C);
+    a->G = static_cast<int>(G);
+    return RMSNORM_OK;
+}
+
+int group_norm_run(bool bwd, GroupNormArgs& a, int64_t C, int64_t G, int dtype,
+                   const Workspace& given, cudaStream_t stream) {
+    int st = group_norm_shape(&a, C, G, dtype);
+    if (st != RMSNORM_OK) return st;
     if (a.act < RMSNORM_ACT_NONE || a.act > RMSNORM_ACT_GELU) return RMSNORM_ERR_INVALID_ARG;
-    if (a.S > INT32_MAX / (C / G)) return RMSNORM_ERR_INVALID_ARG;
-    a.C = static_cast<int>(C);
-    a.G = static_cast<int>(G);
     const int sz = dtype_size(dtype), wsz = weight_size(dtype);
     if (!aligned(a.mean, 4) || !aligned(a.rstd, 4) || !aligned(a.dw, 4) || !aligned(a.db, 4))
         return RMSNORM_ERR_MISALIGNED;
     if (a.B == 0 || a.S == 0) {
         for (float* p : {a.dw, a.db})
             if (p != nullptr) {
-                const int st = cuda_status(cudaMemsetAsync(p, 0, static_cast<size_t>(C) * 4, stream));
+                st = cuda_status(cudaMemsetAsync(p, 0, static_cast<size_t>(C) * 4, stream));
                 if (st != RMSNORM_OK) return st;
             }
         return RMSNORM_OK;
@@ -308,26 +358,45 @@ int group_norm_run(bool bwd, GroupNormArgs& a, int64_t C, int64_t G, int dtype,
     if (!aligned(a.x, sz) || !aligned(a.out, sz) || !aligned(a.dy, sz) || !aligned(a.w, wsz) ||
         !aligned(a.b, wsz))
         return RMSNORM_ERR_MISALIGNED;
-    if (a.B > INT64_MAX / 16 / a.S / C) return RMSNORM_ERR_INVALID_ARG;
     if (bwd && a.w == nullptr) a.dw = a.db = nullptr;
     a.w_f32 = wsz == 4;
     const bool vec = aligned(a.x, 16) && aligned(a.out, 16) && aligned(a.dy, 16) && (C * sz) % 16 == 0;
     const DeviceInfo* dev = nullptr;
-    int st = current_device(&dev);
+    st = current_device(&dev);
     if (st != RMSNORM_OK) return st;
     a.status = dev->status_word;
-    a.wait_limit_ns = g_wait_limit_ns.load();
-    const size_t need = group_norm_workspace(*dev, dtype, vec, bwd, a);
-    void* ws = nullptr;
-    if (need > 0 && cuda_status(cudaMallocAsync(&ws, need, stream)) != RMSNORM_OK)
-        return RMSNORM_ERR_NOMEM;
-    const cudaError_t err = group_norm_launch(*dev, dtype, vec, bwd, a, ws, stream);
-    st = err == cudaErrorInvalidValue ? (cudaGetLastError(), RMSNORM_ERR_UNSUPPORTED) : cuda_status(err);
-    if (ws != nullptr) {
-        const int freed = cuda_status(cudaFreeAsync(ws, stream));
-        if (st == RMSNORM_OK) st = freed;
-    }
-    return st;
+    Workspace ws = given;
+    st = ws.take(group_norm_workspace(*dev, dtype, vec, bwd, a), stream);
+    if (st != RMSNORM_OK) return st;
+    st = cuda_status(group_norm_launch(*dev, dtype, vec, bwd, a, ws.p, stream));
+    return ws.give(st, stream);
+}
+
+GroupNormArgs group_norm_fwd_args(const void* x, const void* w, const void* b, void* y, float* mean,
+                                  float* rstd, int64_t B, int64_t S, float eps, int act) {
+    GroupNormArgs a{};
+    a.x = x;
+    a.w = w;
+    a.b = b;
+    a.out = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.B = B;
+    a.S = S;
+    a.eps = eps;
+    a.act = act;
+    return a;
+}
+GroupNormArgs group_norm_bwd_args(const void* x, const void* w, const void* b, const void* dy,
+                                  const float* mean, const float* rstd, void* dx, float* dw,
+                                  float* db, int64_t B, int64_t S, int act) {
+    // mean and rstd are only read in this direction
+    GroupNormArgs a = group_norm_fwd_args(x, w, b, dx, const_cast<float*>(mean),
+                                          const_cast<float*>(rstd), B, S, 0.f, act);
+    a.dy = dy;
+    a.dw = dw;
+    a.db = db;
+    return a;
 }
 
 }  // namespace
@@ -468,67 +537,78 @@ int rmsnorm_qk_rope_fwd(const rmsnorm_rope_t* rope, const void* q, const void* k
     if (!(eps >= 0.f)) return RMSNORM_ERR_INVALID_ARG;
     if (a.tokens == 0 || a.t[0].heads + a.t[1].heads == 0) return RMSNORM_OK;
     return rope_run(rope, a, q, k, wq, wk, positions, inv_freq, nullptr, nullptr, q_out, k_out,
-                    nullptr, nullptr, eps, dtype, false, stream);
+                    nullptr, nullptr, eps, dtype, false, Workspace{}, stream);
 }
 
 int rmsnorm_qk_rope_bwd(const rmsnorm_rope_t* rope, const void* q, const void* k, const void* wq,
                         const void* wk, const void* positions, const float* inv_freq,
                         const void* dq_out, const void* dk_out, void* dq, void* dk, float* dwq,
                         float* dwk, float eps, int dtype, cudaStream_t stream) {
-    RopeArgs a{};
-    int st = rope_descriptor(rope, dtype, &a);
-    if (st != RMSNORM_OK) return st;
-    if (!(eps >= 0.f)) return RMSNORM_ERR_INVALID_ARG;
-    if (!aligned(dwq, 4) || !aligned(dwk, 4)) return RMSNORM_ERR_MISALIGNED;
-    if (a.tokens == 0 || a.t[0].heads + a.t[1].heads == 0) {
-        float* dws[2] = {a.t[0].heads ? dwq : nullptr, a.t[1].heads ? dwk : nullptr};
-        for (float* p : dws)
-            if (p != nullptr) {
-                st = cuda_status(cudaMemsetAsync(p, 0, static_cast<size_t>(a.head_dim) * 4, stream));
-                if (st != RMSNORM_OK) return st;
-            }
-        return RMSNORM_OK;
-    }
-    return rope_run(rope, a, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk,
-                    eps, dtype, true, stream);
+    return rope_bwd_any(rope, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk,
+                        eps, dtype, Workspace{}, stream);
+}
+
+int rmsnorm_qk_rope_bwd_ws(const rmsnorm_rope_t* rope, const void* q, const void* k, const void* wq,
+                           const void* wk, const void* positions, const float* inv_freq,
+                           const void* dq_out, const void* dk_out, void* dq, void* dk, float* dwq,
+                           float* dwk, float eps, int dtype, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+    return rope_bwd_any(rope, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk,
+                        eps, dtype, Workspace{workspace, workspace_bytes, true}, stream);
+}
+
+size_t rmsnorm_qk_rope_bwd_workspace_size(int head_dim, int device) {
+    if (head_dim < 2 || head_dim > RMSNORM_ROPE_MAX_HEAD_DIM || head_dim % 2) return 0;
+    const DeviceInfo* dev = device_info(device);
+    return dev == nullptr ? 0 : static_cast<size_t>(rope_bwd_max_rows(*dev)) * head_dim * 4;
 }
 
 int rmsnorm_group_norm_fwd(const void* x, const void* w, const void* b, void* y, float* mean,
                            float* rstd, int64_t B, int64_t S, int64_t C, int64_t G, float eps,
                            int act, int dtype, cudaStream_t stream) {
     if (!(eps >= 0.f)) return RMSNORM_ERR_INVALID_ARG;
-    GroupNormArgs a{};
-    a.x = x;
-    a.w = w;
-    a.b = b;
-    a.out = y;
-    a.mean = mean;
-    a.rstd = rstd;
-    a.B = B;
-    a.S = S;
-    a.eps = eps;
-    a.act = act;
-    return group_norm_run(false, a, C, G, dtype, stream);
+    GroupNormArgs a = group_norm_fwd_args(x, w, b, y, mean, rstd, B, S, eps, act);
+    return group_norm_run(false, a, C, G, dtype, Workspace{}, stream);
+}
+
+int rmsnorm_group_norm_fwd_ws(const void* x, const void* w, const void* b, void* y, float* mean,
+                              float* rstd, int64_t B, int64_t S, int64_t C, int64_t G, float eps,
+                              int act, int dtype, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream) {
+    if (!(eps >= 0.f)) return RMSNORM_ERR_INVALID_ARG;
+    GroupNormArgs a = group_norm_fwd_args(x, w, b, y, mean, rstd, B, S, eps, act);
+    return group_norm_run(false, a, C, G, dtype, Workspace{workspace, workspace_bytes, true}, stream);
 }
 
 int rmsnorm_group_norm_bwd(const void* x, const void* w, const void* b, const void* dy,
                            const float* mean, const float* rstd, void* dx, float* dw, float* db,
                            int64_t B, int64_t S, int64_t C, int64_t G, int act, int dtype,
                            cudaStream_t stream) {
-    GroupNormArgs a{};
-    a.x = x;
-    a.w = w;
-    a.b = b;
-    a.dy = dy;
-    a.out = dx;
-    a.mean = const_cast<float*>(mean);  // only read in this direction
-    a.rstd = const_cast<float*>(rstd);
-    a.dw = dw;
-    a.db = db;
-    a.B = B;
-    a.S = S;
-    a.act = act;
-    return group_norm_run(true, a, C, G, dtype, stream);
+    GroupNormArgs a = group_norm_bwd_args(x, w, b, dy, mean, rstd, dx, dw, db, B, S, act);
+    return group_norm_run(true, a, C, G, dtype, Workspace{}, stream);
+}
+
+int rmsnorm_group_norm_bwd_ws(const void* x, const void* w, const void* b, const void* dy,
+                              const float* mean, const float* rstd, void* dx, float* dw, float* db,
+                              int64_t B, int64_t S, int64_t C, int64_t G, int act, int dtype,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    GroupNormArgs a = group_norm_bwd_args(x, w, b, dy, mean, rstd, dx, dw, db, B, S, act);
+    return group_norm_run(true, a, C, G, dtype, Workspace{workspace, workspace_bytes, true}, stream);
+}
+
+size_t rmsnorm_group_norm_workspace_size(int64_t B, int64_t S, int64_t C, int64_t G, int dtype,
+                                         int backward, int device) {
+    GroupNormArgs a = group_norm_fwd_args(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, B, S,
+                                          0.f, RMSNORM_ACT_NONE);
+    if (group_norm_shape(&a, C, G, dtype) != RMSNORM_OK || B == 0 || S == 0) return 0;
+    const DeviceInfo* dev = device_info(device);
+    if (dev == nullptr) return 0;
+    float one = 0.f;
+    a.dw = a.db = &one;  // the largest need: with weight gradients
+    size_t need = group_norm_workspace(*dev, dtype, false, backward != 0, a);
+    if ((C * dtype_size(dtype)) % 16 == 0)
+        need = std::max(need, group_norm_workspace(*dev, dtype, true, backward != 0, a));
+    return need;
 }
 
 int rmsnorm_get_last_device_error(cudaStream_t stream) {

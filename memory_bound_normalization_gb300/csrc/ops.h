@@ -47,6 +47,8 @@ struct RopeArgs {
 // Rows of partial sums a backward with the norm writes for each tensor.
 cudaError_t rope_bwd_rows(const DeviceInfo& dev, int dtype, bool adjacent, const RopeArgs& a,
                           int rows[2]);
+// The most rows any call of the device writes, both tensors together.
+int rope_bwd_max_rows(const DeviceInfo& dev);
 cudaError_t rope_fwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, RopeArgs a,
                             cudaStream_t s);
 cudaError_t rope_bwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, RopeArgs a,
@@ -68,7 +70,6 @@ struct GroupNormArgs {
     int act;
     int w_f32;
     int* status;
-    uint64_t wait_limit_ns;
 };
 
 // Workspace bytes of a call (0: none), and the call itself. `vec`: every

@@ -587,6 +587,8 @@ cudaError_t rope_fwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, Rop
                       static_cast<int>(tiles * a.splits), kRopeThreads, smem, 1, s, a);
 }
 
+int rope_bwd_max_rows(const DeviceInfo& dev) { return 3 * dev.sm_count + 2; }
+
 cudaError_t rope_bwd_rows(const DeviceInfo& dev, int dtype, bool adjacent, const RopeArgs& in,
                           int rows[2]) {
     RopeArgs a = in;
@@ -594,7 +596,7 @@ cudaError_t rope_bwd_rows(const DeviceInfo& dev, int dtype, bool adjacent, const
     a.tile = bwd_tile(a);
     const int64_t tiles = cdiv(a.tokens, a.tile);
     // three blocks an SM, shared out by the heads of the two tensors
-    const int64_t total = 3 * static_cast<int64_t>(dev.sm_count);
+    const int64_t total = rope_bwd_max_rows(dev) - 2;
     const int64_t heads = a.t[0].heads + a.t[1].heads;
     rows[0] = static_cast<int>(std::max<int64_t>(1, std::min(tiles, total * a.t[0].heads / heads)));
     rows[1] = a.t[1].heads == 0

@@ -9,6 +9,7 @@ stream. ``autograd`` holds the differentiable forms.
 """
 from __future__ import annotations
 
+import functools
 import struct
 
 from . import _lib
@@ -30,31 +31,37 @@ def _codes(dtype, w_dtype):
     return dtype_code(dtype, w_dtype)
 
 
-class _On:
-    """The device of the call made current for it, where it is not already."""
+def _here(device: int) -> bool:
+    """Whether `device` (a tensor's get_device()) is the current one; a call on
+    another runs again with it made current."""
+    import torch
 
-    __slots__ = ("guard",)
-
-    def __init__(self, device):
-        import torch
-
-        self.guard = None
-        if device.type == "cuda" and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+    if device < 0:
+        raise ValueError("tensor argument on the host: the library takes CUDA tensors")
+    return device == torch.cuda.current_device()
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            _refuse(f"{name} is on {t.device}, the input on {device}")
+def _foreign(stream) -> bool:
+    """Whether `stream` is another than the current one, which the caching
+    allocator's memory is ordered on. Such a call leaves its workspace to the
+    library, which takes it in that stream's order."""
+    return stream is not None and _lib._stream(stream) != _lib._stream(None)
+
+
+@functools.lru_cache(maxsize=256)
+def _group_norm_workspace(B, S, C, G, code, backward, device):
+    return _lib.rmsnorm_group_norm_workspace_size(B, S, C, G, code, backward, device)
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_workspace(head_dim, device):
+    return _lib.rmsnorm_qk_rope_bwd_workspace_size(head_dim, device)
+
+
+def _one_device(device: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            _refuse(f"tensors on devices {t.get_device()} and {device}")
 
 
 # ------------------------------------------------------------- group norm
@@ -88,16 +95,23 @@ def group_norm_forward(x, num_groups: int, weight=None, bias=None, eps: float = 
     import torch
 
     B, S, C = _group_norm_shape(x, num_groups, weight, bias, activation)
-    dev = x.device
-    _same_device(dev, weight=weight, bias=bias)
     code = _codes(x.dtype, None if weight is None else weight.dtype)
-    with _On(dev):
-        y = torch.empty_like(x)
-        mean = torch.empty((B, num_groups), dtype=torch.float32, device=dev)
-        rstd = torch.empty((B, num_groups), dtype=torch.float32, device=dev)
-        check(_lib.rmsnorm_group_norm_fwd(x, weight, bias, y, mean, rstd, B, S, C, num_groups, eps,
-                                          ACTIVATIONS[activation], code, stream),
-              "rmsnorm_group_norm_fwd")
+    dev = x.get_device()
+    _one_device(dev, weight, bias)
+    if not _here(dev):
+        with torch.cuda.device(dev):
+            return group_norm_forward(x, num_groups, weight, bias, eps, activation, stream)
+    where = x.device
+    y = torch.empty_like(x)
+    mean = torch.empty((B, num_groups), dtype=torch.float32, device=where)
+    rstd = torch.empty((B, num_groups), dtype=torch.float32, device=where)
+    args = (x, weight, bias, y, mean, rstd, B, S, C, num_groups, eps, ACTIVATIONS[activation], code)
+    if _foreign(stream):
+        check(_lib.rmsnorm_group_norm_fwd(*args, stream), "rmsnorm_group_norm_fwd")
+    else:
+        need = _group_norm_workspace(B, S, C, num_groups, code, 0, dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=where) if need else None
+        check(_lib.rmsnorm_group_norm_fwd_ws(*args, ws, need, stream), "rmsnorm_group_norm_fwd_ws")
     return y, mean, rstd
 
 
@@ -108,23 +122,32 @@ def group_norm_backward(x, num_groups: int, weight, bias, dy, mean, rstd,
     import torch
 
     B, S, C = _group_norm_shape(x, num_groups, weight, bias, activation)
-    dev = x.device
-    _same_device(dev, weight=weight, bias=bias, dy=dy, mean=mean, rstd=rstd)
     if dy.shape != x.shape or dy.dtype != x.dtype:
         _refuse(f"dy {tuple(dy.shape)} {dy.dtype} of x {tuple(x.shape)} {x.dtype}")
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t.shape != (B, num_groups) or t.dtype != torch.float32:
             _refuse(f"{name} {tuple(t.shape)} {t.dtype}: expected fp32 {(B, num_groups)}")
     code = _codes(x.dtype, None if weight is None else weight.dtype)
-    with _On(dev):
-        dx = torch.empty_like(x)
-        dw = db = None
-        if weight is not None:
-            dw = torch.empty(C, dtype=torch.float32, device=dev)
-            db = torch.empty(C, dtype=torch.float32, device=dev)
-        check(_lib.rmsnorm_group_norm_bwd(x, weight, bias, dy, mean, rstd, dx, dw, db, B, S, C,
-                                          num_groups, ACTIVATIONS[activation], code, stream),
-              "rmsnorm_group_norm_bwd")
+    dev = x.get_device()
+    _one_device(dev, weight, bias, dy, mean, rstd)
+    if not _here(dev):
+        with torch.cuda.device(dev):
+            return group_norm_backward(x, num_groups, weight, bias, dy, mean, rstd, activation,
+                                       stream)
+    where = x.device
+    dx = torch.empty_like(x)
+    dw = db = None
+    if weight is not None:
+        dw = torch.empty(C, dtype=torch.float32, device=where)
+        db = torch.empty(C, dtype=torch.float32, device=where)
+    args = (x, weight, bias, dy, mean, rstd, dx, dw, db, B, S, C, num_groups,
+            ACTIVATIONS[activation], code)
+    if _foreign(stream):
+        check(_lib.rmsnorm_group_norm_bwd(*args, stream), "rmsnorm_group_norm_bwd")
+    else:
+        need = _group_norm_workspace(B, S, C, num_groups, code, 1, dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=where) if need else None
+        check(_lib.rmsnorm_group_norm_bwd_ws(*args, ws, need, stream), "rmsnorm_group_norm_bwd_ws")
     return dx, dw, db
 
 
@@ -145,8 +168,6 @@ def _rope_shape(q, k, wq, wk, positions, inv_freq, sections):
 
     if q.dim() not in (3, 4):
         _refuse(f"queries of {q.dim()} dimensions: expected [T, H, D] or [B, T, H, D]")
-    dev = q.device
-    _same_device(dev, k=k, wq=wq, wk=wk, positions=positions, inv_freq=inv_freq)
     D = q.shape[-1]
     if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or
                           k.shape[-1] != D or k.dtype != q.dtype):
@@ -177,6 +198,8 @@ def _rope_shape(q, k, wq, wk, positions, inv_freq, sections):
     code = _codes(q.dtype, None if wq is None else wq.dtype)
     head = (B, T, q.shape[-2], 0 if k is None else k.shape[-2], D, 2 * inv_freq.numel(), axes,
             *sections, *((0,) * (_lib.ROPE_MAX_AXES - axes)))
+    dev = q.get_device()
+    _one_device(dev, k, wq, wk, positions, inv_freq)
     return head, positions.dtype == torch.int64, ps, code, dev
 
 
@@ -208,22 +231,26 @@ def qk_rope_forward(q, k, wq, wk, positions, inv_freq, sections, interleaved: bo
     import torch
 
     head, pos64, ps, code, dev = _rope_shape(q, k, wq, wk, positions, inv_freq, sections)
-    with _On(dev):
-        if out is None:
-            qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev)
-        else:
-            qo, ko = out
-            _like("out of the queries", qo, q)
-            if (ko is None) != (k is None):
-                _refuse("an output for the keys where there are keys")
-            if k is not None:
-                _like("out of the keys", ko, k)
-        desc = _pack(head, interleaved, adjacent, pos64, ps, _strides(q),
-                     _NONE if k is None else _strides(k), _strides(qo),
-                     _NONE if k is None else _strides(ko), _NONE, _NONE)
-        check(_lib.rmsnorm_qk_rope_fwd(desc, q, k, wq, wk, positions, inv_freq, qo, ko, eps, code,
-                                       stream), "rmsnorm_qk_rope_fwd")
+    keys = k is not None
+    if out is not None:
+        qo, ko = out
+        _like("out of the queries", qo, q)
+        if (ko is not None) != keys:
+            _refuse("an output for the keys where there are keys")
+        if keys:
+            _like("out of the keys", ko, k)
+    sq, sk = _strides(q), _strides(k) if keys else _NONE
+    if not _here(dev):
+        with torch.cuda.device(dev):
+            return qk_rope_forward(q, k, wq, wk, positions, inv_freq, sections, interleaved,
+                                   adjacent, eps, out, stream)
+    if out is None:
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ko = torch.empty(k.shape, dtype=q.dtype, device=q.device) if keys else None
+    desc = _pack(head, interleaved, adjacent, pos64, ps, sq, sk, _strides(qo),
+                 _strides(ko) if keys else _NONE, _NONE, _NONE)
+    check(_lib.rmsnorm_qk_rope_fwd(desc, q, k, wq, wk, positions, inv_freq, qo, ko, eps, code,
+                                   stream), "rmsnorm_qk_rope_fwd")
     return qo, ko
 
 
@@ -240,18 +267,28 @@ def qk_rope_backward(q, k, wq, wk, positions, inv_freq, sections, dq_out, dk_out
         _refuse("a gradient for the keys where there are keys")
     if k is not None:
         _like("dk_out", dk_out, k)
-    with _On(dev):
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        dk = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev)
-        dwq = dwk = None
-        if wq is not None:
-            dwq = torch.empty(wq.shape, dtype=torch.float32, device=dev)
-            if k is not None:
-                dwk = torch.empty(wq.shape, dtype=torch.float32, device=dev)
-        desc = _pack(head, interleaved, adjacent, pos64, ps, _strides(q),
-                     _NONE if k is None else _strides(k), _strides(dq_out),
-                     _NONE if k is None else _strides(dk_out), _strides(dq),
-                     _NONE if k is None else _strides(dk))
-        check(_lib.rmsnorm_qk_rope_bwd(desc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq,
-                                       dk, dwq, dwk, eps, code, stream), "rmsnorm_qk_rope_bwd")
+    keys = k is not None
+    strides = (_strides(q), _strides(k) if keys else _NONE, _strides(dq_out),
+               _strides(dk_out) if keys else _NONE)
+    if not _here(dev):
+        with torch.cuda.device(dev):
+            return qk_rope_backward(q, k, wq, wk, positions, inv_freq, sections, dq_out, dk_out,
+                                    interleaved, adjacent, eps, stream)
+    where = q.device
+    dq = torch.empty(q.shape, dtype=q.dtype, device=where)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=where) if keys else None
+    dwq = dwk = None
+    if wq is not None:
+        dwq = torch.empty(wq.shape, dtype=torch.float32, device=where)
+        if keys:
+            dwk = torch.empty(wq.shape, dtype=torch.float32, device=where)
+    desc = _pack(head, interleaved, adjacent, pos64, ps, *strides, _strides(dq),
+                 _strides(dk) if keys else _NONE)
+    args = (desc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk, eps, code)
+    if wq is None or _foreign(stream):
+        check(_lib.rmsnorm_qk_rope_bwd(*args, stream), "rmsnorm_qk_rope_bwd")
+    else:
+        need = _rope_workspace(q.shape[-1], dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=where)
+        check(_lib.rmsnorm_qk_rope_bwd_ws(*args, ws, need, stream), "rmsnorm_qk_rope_bwd_ws")
     return dq, dk, dwq, dwk
