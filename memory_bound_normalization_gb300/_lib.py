@@ -164,6 +164,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load librmsnorm.so (optionally building it first). Raises OSError if
     it cannot be loaded; there is no other implementation to fall back on."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

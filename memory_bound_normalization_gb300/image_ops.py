@@ -6,10 +6,14 @@ The functions check their arguments, allocate outputs with PyTorch and raise
 ``RMSNormError`` on a non-OK status, like ``forward`` and ``backward``. They
 run on the tensors' own device and, unless ``stream`` is given, on its current
 stream. ``autograd`` holds the differentiable forms.
+
+A call's checks, its type code, workspace size and packed descriptor depend on
+the layouts of its arguments alone, so they are kept per layout (shapes,
+strides, types, device and options; never an address or a value): a decode
+step's call spends its time in the launch and the two allocations.
 """
 from __future__ import annotations
 
-import functools
 import struct
 
 from . import _lib
@@ -41,21 +45,34 @@ def _here(device: int) -> bool:
     return device == torch.cuda.current_device()
 
 
-def _foreign(stream) -> bool:
-    """Whether `stream` is another than the current one, which the caching
-    allocator's memory is ordered on. Such a call leaves its workspace to the
-    library, which takes it in that stream's order."""
-    return stream is not None and _lib._stream(stream) != _lib._stream(None)
+_KEPT: dict = {}
 
 
-@functools.lru_cache(maxsize=256)
-def _group_norm_workspace(B, S, C, G, code, backward, device):
-    return _lib.rmsnorm_group_norm_workspace_size(B, S, C, G, code, backward, device)
+def _keep(key, made):
+    if len(_KEPT) >= 1024:
+        _KEPT.clear()
+    _KEPT[key] = made
+    return made
 
 
-@functools.lru_cache(maxsize=64)
-def _rope_workspace(head_dim, device):
-    return _lib.rmsnorm_qk_rope_bwd_workspace_size(head_dim, device)
+def _layout(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_stream(stream):
+    """(the handle to run on, whether it is another stream than the current
+    one). The caching allocator's memory is ordered on the current stream, so a
+    call on another leaves its workspace to the library, which takes it in that
+    stream's order."""
+    here = _lib._stream(None)
+    if stream is None:
+        return here, False
+    there = _lib._stream(stream)
+    return there, there != here
 
 
 def _one_device(device: int, *tensors):
@@ -86,6 +103,18 @@ def _group_norm_shape(x, num_groups, weight, bias, activation):
     return B, S, C
 
 
+def _group_norm_forward_layout(x, num_groups, weight, bias, activation):
+    B, S, C = _group_norm_shape(x, num_groups, weight, bias, activation)
+    code = _codes(x.dtype, None if weight is None else weight.dtype)
+    dev = x.get_device()
+    _one_device(dev, weight, bias)
+    _here(dev)
+    for t in (x, weight, bias):
+        _lib._ptr(t)  # dense device memory
+    need = _lib.rmsnorm_group_norm_workspace_size(B, S, C, num_groups, code, 0, dev)
+    return (B, S, C, num_groups), code, ACTIVATIONS[activation], need, dev, (B, num_groups)
+
+
 def group_norm_forward(x, num_groups: int, weight=None, bias=None, eps: float = 1e-5,
                        activation: str = "none", stream=None):
     """y, mean, rstd of act(group_norm(x) * weight + bias), x [B, ..., C]
@@ -94,31 +123,29 @@ def group_norm_forward(x, num_groups: int, weight=None, bias=None, eps: float = 
     channels_last memory format passes as x.permute(0, 2, 3, 1)."""
     import torch
 
-    B, S, C = _group_norm_shape(x, num_groups, weight, bias, activation)
-    code = _codes(x.dtype, None if weight is None else weight.dtype)
-    dev = x.get_device()
-    _one_device(dev, weight, bias)
+    key = ("gn", _layout(x), num_groups, _layout(weight), _layout(bias), activation)
+    size, code, act, need, dev, per_group = _KEPT.get(key) or _keep(
+        key, _group_norm_forward_layout(x, num_groups, weight, bias, activation))
     if not _here(dev):
         with torch.cuda.device(dev):
             return group_norm_forward(x, num_groups, weight, bias, eps, activation, stream)
-    where = x.device
+    lib, where = _lib.load_library(), x.device
+    handle, foreign = _on_stream(stream)
     y = torch.empty_like(x)
-    mean = torch.empty((B, num_groups), dtype=torch.float32, device=where)
-    rstd = torch.empty((B, num_groups), dtype=torch.float32, device=where)
-    args = (x, weight, bias, y, mean, rstd, B, S, C, num_groups, eps, ACTIVATIONS[activation], code)
-    if _foreign(stream):
-        check(_lib.rmsnorm_group_norm_fwd(*args, stream), "rmsnorm_group_norm_fwd")
+    mean = torch.empty(per_group, dtype=torch.float32, device=where)
+    rstd = torch.empty(per_group, dtype=torch.float32, device=where)
+    args = (x.data_ptr(), _at(weight), _at(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+            *size, eps, act, code)
+    if foreign:
+        check(lib.rmsnorm_group_norm_fwd(*args, handle), "rmsnorm_group_norm_fwd")
     else:
-        need = _group_norm_workspace(B, S, C, num_groups, code, 0, dev)
         ws = torch.empty(need, dtype=torch.uint8, device=where) if need else None
-        check(_lib.rmsnorm_group_norm_fwd_ws(*args, ws, need, stream), "rmsnorm_group_norm_fwd_ws")
+        check(lib.rmsnorm_group_norm_fwd_ws(*args, _at(ws), need, handle),
+              "rmsnorm_group_norm_fwd_ws")
     return y, mean, rstd
 
 
-def group_norm_backward(x, num_groups: int, weight, bias, dy, mean, rstd,
-                        activation: str = "none", stream=None):
-    """dx, dweight, dbias (fp32; None without a weight) from the forward's mean
-    and rstd."""
+def _group_norm_backward_layout(x, num_groups, weight, bias, dy, mean, rstd, activation):
     import torch
 
     B, S, C = _group_norm_shape(x, num_groups, weight, bias, activation)
@@ -130,24 +157,42 @@ def group_norm_backward(x, num_groups: int, weight, bias, dy, mean, rstd,
     code = _codes(x.dtype, None if weight is None else weight.dtype)
     dev = x.get_device()
     _one_device(dev, weight, bias, dy, mean, rstd)
+    _here(dev)
+    for t in (x, weight, bias, dy, mean, rstd):
+        _lib._ptr(t)  # dense device memory
+    need = _lib.rmsnorm_group_norm_workspace_size(B, S, C, num_groups, code, 1, dev)
+    return (B, S, C, num_groups), code, ACTIVATIONS[activation], need, dev, (C,)
+
+
+def group_norm_backward(x, num_groups: int, weight, bias, dy, mean, rstd,
+                        activation: str = "none", stream=None):
+    """dx, dweight, dbias (fp32; None without a weight) from the forward's mean
+    and rstd."""
+    import torch
+
+    key = ("gnb", _layout(x), num_groups, _layout(weight), _layout(bias), _layout(dy),
+           _layout(mean), _layout(rstd), activation)
+    size, code, act, need, dev, per_channel = _KEPT.get(key) or _keep(
+        key, _group_norm_backward_layout(x, num_groups, weight, bias, dy, mean, rstd, activation))
     if not _here(dev):
         with torch.cuda.device(dev):
             return group_norm_backward(x, num_groups, weight, bias, dy, mean, rstd, activation,
                                        stream)
-    where = x.device
+    lib, where = _lib.load_library(), x.device
+    handle, foreign = _on_stream(stream)
     dx = torch.empty_like(x)
     dw = db = None
     if weight is not None:
-        dw = torch.empty(C, dtype=torch.float32, device=where)
-        db = torch.empty(C, dtype=torch.float32, device=where)
-    args = (x, weight, bias, dy, mean, rstd, dx, dw, db, B, S, C, num_groups,
-            ACTIVATIONS[activation], code)
-    if _foreign(stream):
-        check(_lib.rmsnorm_group_norm_bwd(*args, stream), "rmsnorm_group_norm_bwd")
+        dw = torch.empty(per_channel, dtype=torch.float32, device=where)
+        db = torch.empty(per_channel, dtype=torch.float32, device=where)
+    args = (x.data_ptr(), _at(weight), _at(bias), dy.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+            dx.data_ptr(), _at(dw), _at(db), *size, act, code)
+    if foreign:
+        check(lib.rmsnorm_group_norm_bwd(*args, handle), "rmsnorm_group_norm_bwd")
     else:
-        need = _group_norm_workspace(B, S, C, num_groups, code, 1, dev)
         ws = torch.empty(need, dtype=torch.uint8, device=where) if need else None
-        check(_lib.rmsnorm_group_norm_bwd_ws(*args, ws, need, stream), "rmsnorm_group_norm_bwd_ws")
+        check(lib.rmsnorm_group_norm_bwd_ws(*args, _at(ws), need, handle),
+              "rmsnorm_group_norm_bwd_ws")
     return dx, dw, db
 
 
@@ -217,6 +262,32 @@ def _like(name, t, of):
                 f"{of.dtype} on {of.device}")
 
 
+def _dense(t):
+    """Strides that torch.empty(t.shape) has."""
+    *lead, H, D = t.shape
+    return (lead[0] and lead[1] * H * D if len(lead) == 2 else 0, H * D, D)
+
+
+def _rope_forward_layout(q, k, wq, wk, positions, inv_freq, sections, interleaved, adjacent, qo, ko):
+    head, pos64, ps, code, dev = _rope_shape(q, k, wq, wk, positions, inv_freq, sections)
+    keys = k is not None
+    if qo is not None or ko is not None:
+        if qo is None:
+            _refuse("an output for the queries")
+        _like("out of the queries", qo, q)
+        if (ko is not None) != keys:
+            _refuse("an output for the keys where there are keys")
+        if keys:
+            _like("out of the keys", ko, k)
+    desc = _pack(head, interleaved, adjacent, pos64, ps, _strides(q),
+                 _strides(k) if keys else _NONE, _dense(q) if qo is None else _strides(qo),
+                 (_dense(k) if ko is None else _strides(ko)) if keys else _NONE, _NONE, _NONE)
+    _here(dev)
+    for t in (wq, wk, inv_freq):
+        _lib._ptr(t)  # dense device memory
+    return desc, code, dev
+
+
 def qk_rope_forward(q, k, wq, wk, positions, inv_freq, sections, interleaved: bool = False,
                     adjacent: bool = False, eps: float = 1e-6, out=None, stream=None):
     """q_out, k_out: RMSNorm of each head (weights wq, wk [D]; None: no norm),
@@ -230,28 +301,43 @@ def qk_rope_forward(q, k, wq, wk, positions, inv_freq, sections, interleaved: bo
     for an update in place."""
     import torch
 
-    head, pos64, ps, code, dev = _rope_shape(q, k, wq, wk, positions, inv_freq, sections)
-    keys = k is not None
-    if out is not None:
-        qo, ko = out
-        _like("out of the queries", qo, q)
-        if (ko is not None) != keys:
-            _refuse("an output for the keys where there are keys")
-        if keys:
-            _like("out of the keys", ko, k)
-    sq, sk = _strides(q), _strides(k) if keys else _NONE
+    qo, ko = (None, None) if out is None else out
+    sections = tuple(sections)
+    key = ("qk", _layout(q), _layout(k), _layout(wq), _layout(wk), _layout(positions),
+           _layout(inv_freq), sections, interleaved, adjacent, _layout(qo), _layout(ko))
+    desc, code, dev = _KEPT.get(key) or _keep(key, _rope_forward_layout(
+        q, k, wq, wk, positions, inv_freq, sections, interleaved, adjacent, qo, ko))
     if not _here(dev):
         with torch.cuda.device(dev):
             return qk_rope_forward(q, k, wq, wk, positions, inv_freq, sections, interleaved,
                                    adjacent, eps, out, stream)
-    if out is None:
+    if qo is None:
         qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        ko = torch.empty(k.shape, dtype=q.dtype, device=q.device) if keys else None
-    desc = _pack(head, interleaved, adjacent, pos64, ps, sq, sk, _strides(qo),
-                 _strides(ko) if keys else _NONE, _NONE, _NONE)
-    check(_lib.rmsnorm_qk_rope_fwd(desc, q, k, wq, wk, positions, inv_freq, qo, ko, eps, code,
-                                   stream), "rmsnorm_qk_rope_fwd")
+        if k is not None:
+            ko = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    check(_lib.load_library().rmsnorm_qk_rope_fwd(
+        desc, q.data_ptr(), _at(k), _at(wq), _at(wk), positions.data_ptr(), inv_freq.data_ptr(),
+        qo.data_ptr(), _at(ko), eps, code, _lib._stream(stream)), "rmsnorm_qk_rope_fwd")
     return qo, ko
+
+
+def _rope_backward_layout(q, k, wq, wk, positions, inv_freq, sections, interleaved, adjacent,
+                          dq_out, dk_out):
+    head, pos64, ps, code, dev = _rope_shape(q, k, wq, wk, positions, inv_freq, sections)
+    keys = k is not None
+    _like("dq_out", dq_out, q)
+    if (dk_out is not None) != keys:
+        _refuse("a gradient for the keys where there are keys")
+    if keys:
+        _like("dk_out", dk_out, k)
+    desc = _pack(head, interleaved, adjacent, pos64, ps, _strides(q),
+                 _strides(k) if keys else _NONE, _strides(dq_out),
+                 _strides(dk_out) if keys else _NONE, _dense(q), _dense(k) if keys else _NONE)
+    _here(dev)
+    for t in (wq, wk, inv_freq):
+        _lib._ptr(t)  # dense device memory
+    need = 0 if wq is None else _lib.rmsnorm_qk_rope_bwd_workspace_size(q.shape[-1], dev)
+    return desc, code, dev, need
 
 
 def qk_rope_backward(q, k, wq, wk, positions, inv_freq, sections, dq_out, dk_out,
@@ -261,34 +347,31 @@ def qk_rope_backward(q, k, wq, wk, positions, inv_freq, sections, dq_out, dk_out
     and the gradients of its outputs."""
     import torch
 
-    head, pos64, ps, code, dev = _rope_shape(q, k, wq, wk, positions, inv_freq, sections)
-    _like("dq_out", dq_out, q)
-    if (dk_out is None) != (k is None):
-        _refuse("a gradient for the keys where there are keys")
-    if k is not None:
-        _like("dk_out", dk_out, k)
-    keys = k is not None
-    strides = (_strides(q), _strides(k) if keys else _NONE, _strides(dq_out),
-               _strides(dk_out) if keys else _NONE)
+    sections = tuple(sections)
+    key = ("qkb", _layout(q), _layout(k), _layout(wq), _layout(wk), _layout(positions),
+           _layout(inv_freq), sections, interleaved, adjacent, _layout(dq_out), _layout(dk_out))
+    desc, code, dev, need = _KEPT.get(key) or _keep(key, _rope_backward_layout(
+        q, k, wq, wk, positions, inv_freq, sections, interleaved, adjacent, dq_out, dk_out))
     if not _here(dev):
         with torch.cuda.device(dev):
             return qk_rope_backward(q, k, wq, wk, positions, inv_freq, sections, dq_out, dk_out,
                                     interleaved, adjacent, eps, stream)
-    where = q.device
+    lib, where = _lib.load_library(), q.device
+    handle, foreign = _on_stream(stream)
     dq = torch.empty(q.shape, dtype=q.dtype, device=where)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=where) if keys else None
+    dk = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=where)
     dwq = dwk = None
     if wq is not None:
         dwq = torch.empty(wq.shape, dtype=torch.float32, device=where)
-        if keys:
+        if k is not None:
             dwk = torch.empty(wq.shape, dtype=torch.float32, device=where)
-    desc = _pack(head, interleaved, adjacent, pos64, ps, *strides, _strides(dq),
-                 _strides(dk) if keys else _NONE)
-    args = (desc, q, k, wq, wk, positions, inv_freq, dq_out, dk_out, dq, dk, dwq, dwk, eps, code)
-    if wq is None or _foreign(stream):
-        check(_lib.rmsnorm_qk_rope_bwd(*args, stream), "rmsnorm_qk_rope_bwd")
+    args = (desc, q.data_ptr(), _at(k), _at(wq), _at(wk), positions.data_ptr(),
+            inv_freq.data_ptr(), dq_out.data_ptr(), _at(dk_out), dq.data_ptr(), _at(dk), _at(dwq),
+            _at(dwk), eps, code)
+    if foreign or not need:
+        check(lib.rmsnorm_qk_rope_bwd(*args, handle), "rmsnorm_qk_rope_bwd")
     else:
-        need = _rope_workspace(q.shape[-1], dev)
         ws = torch.empty(need, dtype=torch.uint8, device=where)
-        check(_lib.rmsnorm_qk_rope_bwd_ws(*args, ws, need, stream), "rmsnorm_qk_rope_bwd_ws")
+        check(lib.rmsnorm_qk_rope_bwd_ws(*args, ws.data_ptr(), need, handle),
+              "rmsnorm_qk_rope_bwd_ws")
     return dq, dk, dwq, dwk
