@@ -605,9 +605,14 @@ size_t rmsnorm_group_norm_workspace_size(int64_t B, int64_t S, int64_t C, int64_
     if (dev == nullptr) return 0;
     float one = 0.f;
     a.dw = a.db = &one;  // the largest need: with weight gradients
+    // whatever the tensors' alignment and the activation, whose kernels may
+    // differ in how many blocks run at once
     size_t need = group_norm_workspace(*dev, dtype, false, backward != 0, a);
-    if ((C * dtype_size(dtype)) % 16 == 0)
-        need = std::max(need, group_norm_workspace(*dev, dtype, true, backward != 0, a));
+    for (int act = RMSNORM_ACT_NONE; act <= RMSNORM_ACT_GELU; ++act) {
+        a.act = act;
+        if ((C * dtype_size(dtype)) % 16 == 0)
+            need = std::max(need, group_norm_workspace(*dev, dtype, true, backward != 0, a));
+    }
     return need;
 }
 

@@ -1,5 +1,6 @@
-// The kernel families of the group norm (host code only): the general path
-// (group_norm_scalar.cu).
+// The kernel families of the group norm: what the host side (group_norm.cu)
+// and the kernels (group_norm_kernels.cuh, one translation unit for each
+// activation type) share, and the general path (group_norm_scalar.cu).
 #pragma once
 
 #include "ops.h"
@@ -8,5 +9,47 @@ namespace rmsn {
 
 size_t gn_scalar_workspace(bool bwd, const GroupNormArgs& a);
 cudaError_t gn_scalar_launch(int dtype, bool bwd, const GroupNormArgs& a, void* ws, cudaStream_t s);
+
+constexpr int kMaxThreads = 512;
+constexpr int kMaxSmem = 227 * 1024;
+
+struct SlabArgs {
+    GroupNormArgs a;
+    int nvec;      // 16-byte vectors of a slab's row
+    int lanes;     // positions a block takes at once
+    int splits;    // slabs of a sample (runs of channels)
+    int cw, gw;    // channels and groups of a slab
+    int D;         // channels of a group
+    int cluster;   // blocks that join their sums
+    int chunks;    // clusters of a slab
+    int part_rows, part_more;  // positions of a block, and how many blocks take one more
+    int join;      // warps (forward) that share a group's sums in a block
+    int64_t sample0;
+    float2* stats; // stream: [slab][chunk][gw], (mean, M2) or (sum w P, sum w Q)
+    float* rows;   // backward: partial rows [sample * chunks + chunk][2 C] (Q, then P)
+};
+
+// Shared memory besides the resident slab: the threads' sums [2][lanes][cw],
+// two values a group, twice (the block's and the slab's), and the warps' parts
+// of a group's sums.
+__host__ __device__ __forceinline__ int sums_floats(int lanes, int cw) { return 2 * lanes * cw; }
+constexpr int kJoinFloats = 2 * kMaxThreads / 32;
+inline int fixed_smem(int lanes, int cw, int gw) {
+    return (sums_floats(lanes, cw) + 4 * gw + kJoinFloats) * 4;
+}
+
+// Positions a thread's copies run ahead, and positions of a group of copies.
+constexpr int kDepth = 6, kGroup = 2;
+inline int ring_smem(int lanes, int nvec, bool bwd) {
+    return kDepth * lanes * nvec * 16 * (bwd ? 2 : 1);
+}
+
+using SlabFn = void (*)(const SlabArgs);
+// Both passes of a slab that stays in shared memory; a slab's sums; its second
+// pass.
+enum class SlabKind { kResident, kSums, kApply };
+SlabFn gn_kernel_f32(bool bwd, int act, SlabKind k);
+SlabFn gn_kernel_bf16(bool bwd, int act, SlabKind k);
+SlabFn gn_kernel_f16(bool bwd, int act, SlabKind k);
 
 }  // namespace rmsn

@@ -1,0 +1,777 @@
+// Group norm with an activation, channels last, by 16-byte vectors.
+//
+// A slab is one sample's positions by a run of whole groups of channels. A
+// block takes a contiguous range of its positions; each thread owns one
+// 16-byte vector of channels and strides over positions, so its channels'
+// constants and sums stay in registers, whatever the group width (a vector may
+// span groups: sums are kept per channel and joined per group afterwards).
+//
+// Forward statistics. A thread sums d = x - p and d^2 about its own first
+// value p of each channel, which turns into (count, mean, M2); these are joined
+// over the block, the cluster and the slab by
+//   mean = sum n_i m_i / n,   M2 = sum M2_i + n_i (m_i - mean)^2
+// so neither a mean far from zero nor one wild first value costs digits (a wild
+// p spoils only the few hundred values of one thread, and then only relative to
+// its own square, which is part of M2).
+// Backward sums. Per channel P = sum dz, Q = sum dz xhat: they give the slab's
+// means (sum_c w P, sum_c w Q) and, added over samples, db and dw.
+//
+// Bound by DRAM: x once in and y once out (x, dy, dx). Between the sums and the
+// second pass the slab has to be kept near. Two families:
+//   resident  the slab fits the shared memory of a cluster of at most 16
+//             blocks: one kernel, each thread keeps what it read in its own
+//             shared-memory slots, the blocks' sums meet in distributed shared
+//             memory. One read of x.
+//   stream    larger slabs: a kernel for the sums (clusters join their blocks'
+//             sums, so few partial results are written) and one that applies
+//             them, in the opposite order so that it starts with what L2 still
+//             holds; samples go in batches that L2 holds.
+#pragma once
+
+#include "group_norm.cuh"
+#include "group_norm.h"
+
+namespace rmsn {
+namespace {
+
+// First position of a block's range: S split as evenly as it goes.
+__device__ __forceinline__ int64_t part_begin(const SlabArgs& g, int part) {
+    return static_cast<int64_t>(part) * g.part_rows + min(part, g.part_more);
+}
+// Positions of the n blocks from `part` on.
+__device__ __forceinline__ float part_count(const SlabArgs& g, int part, int n) {
+    return static_cast<float>(part_begin(g, part + n) - part_begin(g, part));
+}
+
+// Where a block works.
+struct Place {
+    int64_t sample, r0;  // its first position
+    int split, chunk, rank, slab, rows;
+};
+__device__ __forceinline__ Place place_of(const SlabArgs& g) {
+    Place p;
+    const int cl = static_cast<int>(blockIdx.x) / g.cluster;
+    p.rank = static_cast<int>(blockIdx.x) - cl * g.cluster;
+    p.slab = cl / g.chunks;
+    p.chunk = cl - p.slab * g.chunks;
+    const int s = p.slab / g.splits;
+    p.split = p.slab - s * g.splits;
+    p.sample = g.sample0 + s;
+    const int part = p.chunk * g.cluster + p.rank;
+    p.r0 = part_begin(g, part);
+    p.rows = g.part_rows + (part < g.part_more ? 1 : 0);
+    return p;
+}
+
+// i / d for 0 <= i < 2^20 and d >= 1, by the reciprocal in fp32: (i + 1/2) / d
+// is at least 1/(2d) from an integer, more than its rounding.
+__device__ __forceinline__ int quotient(int i, float inv_d) {
+    return static_cast<int>((static_cast<float>(i) + 0.5f) * inv_d);
+}
+
+__device__ __forceinline__ float2 ld_cluster_f32x2(const float2* local, uint32_t rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(cluster_map(local, rank))
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(const float* local, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                 : "=f"(v)
+                 : "r"(cluster_map(local, rank))
+                 : "memory");
+    return v;
+}
+
+// A thread's channels: scale and offset of the affine map.
+template <typename T>
+__device__ __forceinline__ void load_channels(const SlabArgs& g, const void* p, int64_t c, float one,
+                                              float2 (&f)[Pack<T>::PAIRS]) {
+    constexpr int PAIRS = Pack<T>::PAIRS;
+    if (p == nullptr) {
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) f[e] = f2_splat(one);
+    } else if (g.a.w_f32) {
+        // weights need only their own alignment
+        const float* w = static_cast<const float*>(p) + c;
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) f[e] = make_float2(w[2 * e], w[2 * e + 1]);
+    } else {
+        const T* w = static_cast<const T*>(p) + c;
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) f[e] = make_float2(to_f32(w[2 * e]), to_f32(w[2 * e + 1]));
+    }
+}
+
+// Constants of a thread's channels from per-group values in shared or global
+// memory: v[group of the channel].
+template <typename T, typename F>
+__device__ __forceinline__ void per_channel(const SlabArgs& g, int c, float inv_d, F value,
+                                            float2 (&f)[Pack<T>::PAIRS]) {
+#pragma unroll
+    for (int e = 0; e < Pack<T>::PAIRS; ++e)
+        f[e] = make_float2(value(quotient(c + 2 * e, inv_d)), value(quotient(c + 2 * e + 1, inv_d)));
+}
+
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+    return __fadd2_rn(a, make_float2(-b.x, -b.y));
+}
+
+// Copies 16 bytes into this thread's own shared-memory slot; visible to it once
+// the group that holds the copy is waited for. No other thread reads the slot,
+// so no barrier is needed.
+__device__ __forceinline__ bool slot_in(uint32_t slot) {
+    const uint32_t b = smem_u32(rmsn_dynamic_smem);
+    return slot >= b && slot - b + 16u <= dynamic_smem_bytes();
+}
+__device__ __forceinline__ void copy_own(uint32_t slot, const void* src, int* status) {
+    if (!RMSN_OK(slot_in(slot), status)) return;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 ld_slot(uint32_t slot) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(slot)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+__device__ __forceinline__ float rcp_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float2 exp2_pair(float2 v) {
+    return make_float2(exp2_fast(v.x), exp2_fast(v.y));
+}
+__device__ __forceinline__ float2 rcp_pair(float2 v) {
+    return make_float2(rcp_fast(v.x), rcp_fast(v.y));
+}
+
+// The normal distribution function of z and e^(-z^2/2), for 16-bit outputs:
+// Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26 (|error|
+// of erf below 1.5e-7): with x = |z| / sqrt 2, t = 1 / (1 + p x),
+//   erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2).
+__device__ __forceinline__ void normal_pair(float2 z, float2& phi, float2& bell) {
+    const float2 x = make_float2(fabsf(z.x), fabsf(z.y));
+    const float2 t = rcp_pair(__ffma2_rn(x, f2_splat(0.3275911f * 0.70710678f), f2_splat(1.f)));
+    // e^(-z^2/2) = 2^(-z^2 log2(e) / 2)
+    bell = exp2_pair(__fmul2_rn(__fmul2_rn(z, z), f2_splat(-0.72134752f)));
+    float2 q = __ffma2_rn(t, f2_splat(0.5f * 1.061405429f), f2_splat(-0.5f * 1.453152027f));
+    q = __ffma2_rn(q, t, f2_splat(0.5f * 1.421413741f));
+    q = __ffma2_rn(q, t, f2_splat(-0.5f * 0.284496736f));
+    q = __ffma2_rn(q, t, f2_splat(0.5f * 0.254829592f));
+    q = __fmul2_rn(__fmul2_rn(q, t), bell);
+    phi = make_float2(z.x < 0.f ? q.x : 1.f - q.x, z.y < 0.f ? q.y : 1.f - q.y);
+}
+
+// 16-bit outputs take the fast exponential and reciprocal (off by some 2^-21,
+// far inside half a step of 2^-12); fp32 outputs the accurate functions. The
+// 16-bit passes would otherwise be bound by instructions, not by DRAM: the
+// accurate forms cost the backward's first pass 18 instructions an element,
+// where DRAM leaves room for 22.
+template <typename T, int ACT>
+__device__ __forceinline__ float2 act_pair(float2 z) {
+    if constexpr (ACT == RMSNORM_ACT_NONE) return z;
+    if constexpr (sizeof(T) == 4) {
+        return make_float2(act_value(z.x, ACT), act_value(z.y, ACT));
+    } else if constexpr (ACT == RMSNORM_ACT_SILU) {
+        const float2 e = exp2_pair(__fmul2_rn(z, f2_splat(-1.44269504f)));
+        return __fmul2_rn(z, rcp_pair(__fadd2_rn(e, f2_splat(1.f))));
+    } else {
+        float2 phi, bell;
+        normal_pair(z, phi, bell);
+        return __fmul2_rn(z, phi);
+    }
+}
+template <typename T, int ACT>
+__device__ __forceinline__ float2 slope_pair(float2 z) {
+    if constexpr (sizeof(T) == 4) {
+        return make_float2(act_slope(z.x, ACT), act_slope(z.y, ACT));
+    } else if constexpr (ACT == RMSNORM_ACT_SILU) {
+        // s (1 + z (1 - s)) = s + (z s) (1 - s)
+        const float2 e = exp2_pair(__fmul2_rn(z, f2_splat(-1.44269504f)));
+        const float2 s = rcp_pair(__fadd2_rn(e, f2_splat(1.f)));
+        const float2 r = __ffma2_rn(s, f2_splat(-1.f), f2_splat(1.f));
+        return __fmul2_rn(s, __ffma2_rn(z, r, f2_splat(1.f)));
+    } else {
+        float2 phi, bell;
+        normal_pair(z, phi, bell);
+        return __ffma2_rn(__fmul2_rn(z, f2_splat(0.39894228f)), bell, phi);
+    }
+}
+
+// The constants and sums of a thread's channels, and the two passes' steps.
+// Products with the mean are folded into constants: their rounding is of the
+// size of the mean's own.
+template <typename T, bool BWD, int ACT>
+struct Columns;
+
+template <typename T, int ACT>
+struct Columns<T, false, ACT> {
+    static constexpr int PAIRS = Pack<T>::PAIRS;
+    float2 pivot[PAIRS], s1[PAIRS], s2[PAIRS];
+    float2 scale[PAIRS], shift[PAIRS];  // rstd w and b - mean rstd w
+
+    __device__ __forceinline__ void start(const uint4& first) {
+        Pack<T>::unpack2(first, pivot);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) s1[e] = s2[e] = make_float2(0.f, 0.f);
+    }
+    __device__ __forceinline__ void add(const uint4& v) {
+        float2 f[PAIRS];
+        Pack<T>::unpack2(v, f);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            const float2 d = sub2(f[e], pivot[e]);
+            s1[e] = __fadd2_rn(s1[e], d);
+            s2[e] = __ffma2_rn(d, d, s2[e]);
+        }
+    }
+    // The second pass's constants from the slab's (mean, rstd) of each group.
+    __device__ __forceinline__ void finish(const SlabArgs& g, const float2* slab, int64_t c0, int c,
+                                           float inv_d) {
+        float2 w[PAIRS], m[PAIRS];
+        load_channels<T>(g, g.a.w, c0 + c, 1.f, w);
+        load_channels<T>(g, g.a.b, c0 + c, 0.f, shift);
+        per_channel<T>(g, c, inv_d, [&](int k) { return slab[k].x; }, m);
+        per_channel<T>(g, c, inv_d, [&](int k) { return slab[k].y; }, scale);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            scale[e] = __fmul2_rn(scale[e], w[e]);
+            shift[e] = __ffma2_rn(make_float2(-m[e].x, -m[e].y), scale[e], shift[e]);
+        }
+    }
+    // act(x scale + shift), rounded once
+    __device__ __forceinline__ uint4 apply(const uint4& v) const {
+        float2 f[PAIRS];
+        Pack<T>::unpack2(v, f);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) f[e] = act_pair<T, ACT>(__ffma2_rn(f[e], scale[e], shift[e]));
+        return Pack<T>::pack2(f);
+    }
+};
+
+template <typename T, int ACT>
+struct Columns<T, true, ACT> {
+    static constexpr int PAIRS = Pack<T>::PAIRS;
+    // First pass: x - mean, z = (x - mean) k1 + b with k1 = rstd w, and the sums
+    // of dz and dz (x - mean). Second: z = x k1 + k2, dx = dz k1 + (x k3 + k4)
+    // with k2 = b - mean k1, k3 = -rstd^2 B, k4 = -rstd A - mean k3.
+    float2 mean[PAIRS], k1[PAIRS], b[PAIRS];
+    float2 p[PAIRS], q[PAIRS];
+    float2 k2[PAIRS], k3[PAIRS], k4[PAIRS];
+
+    __device__ __forceinline__ void start(const SlabArgs& g, const float* mean_of,
+                                          const float* rstd_of, int64_t c0, int c, float inv_d) {
+        float2 w[PAIRS];
+        per_channel<T>(g, c, inv_d, [&](int k) { return rstd_of[k]; }, k1);
+        per_channel<T>(g, c, inv_d, [&](int k) { return -mean_of[k]; }, mean);
+        load_channels<T>(g, g.a.w, c0 + c, 1.f, w);
+        load_channels<T>(g, g.a.b, c0 + c, 0.f, b);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            k1[e] = __fmul2_rn(k1[e], w[e]);
+            p[e] = q[e] = make_float2(0.f, 0.f);
+        }
+    }
+    __device__ __forceinline__ void add(const uint4& x, const uint4& dy) {
+        float2 c[PAIRS], d[PAIRS];
+        Pack<T>::unpack2(x, c);
+        Pack<T>::unpack2(dy, d);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            c[e] = __fadd2_rn(c[e], mean[e]);
+            if constexpr (ACT != RMSNORM_ACT_NONE)
+                d[e] = __fmul2_rn(d[e], slope_pair<T, ACT>(__ffma2_rn(c[e], k1[e], b[e])));
+            p[e] = __fadd2_rn(p[e], d[e]);
+            q[e] = __ffma2_rn(d[e], c[e], q[e]);
+        }
+    }
+    // sum dz xhat, once the sum of dz (x - mean) is complete
+    __device__ __forceinline__ void scale_q(const SlabArgs& g, const float* rstd_of, int c, float inv_d) {
+        float2 r[PAIRS];
+        per_channel<T>(g, c, inv_d, [&](int k) { return rstd_of[k]; }, r);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) q[e] = __fmul2_rn(q[e], r[e]);
+    }
+    // The second pass's constants; slab holds the means A and B of each group.
+    __device__ __forceinline__ void finish(const SlabArgs& g, const float* rstd_of,
+                                           const float2* slab, int c, float inv_d) {
+        float2 r[PAIRS], A[PAIRS], B[PAIRS];
+        per_channel<T>(g, c, inv_d, [&](int k) { return rstd_of[k]; }, r);
+        per_channel<T>(g, c, inv_d, [&](int k) { return -slab[k].x; }, A);
+        per_channel<T>(g, c, inv_d, [&](int k) { return -slab[k].y; }, B);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            k2[e] = __ffma2_rn(mean[e], k1[e], b[e]);
+            k3[e] = __fmul2_rn(__fmul2_rn(B[e], r[e]), r[e]);
+            k4[e] = __ffma2_rn(mean[e], k3[e], __fmul2_rn(A[e], r[e]));
+        }
+    }
+    // dx = rstd (dz w - A - xhat B), rounded once
+    __device__ __forceinline__ uint4 apply(const uint4& xv, const uint4& dy) const {
+        float2 x[PAIRS], d[PAIRS];
+        Pack<T>::unpack2(xv, x);
+        Pack<T>::unpack2(dy, d);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            if constexpr (ACT != RMSNORM_ACT_NONE)
+                d[e] = __fmul2_rn(d[e], slope_pair<T, ACT>(__ffma2_rn(x[e], k1[e], k2[e])));
+            d[e] = __ffma2_rn(d[e], k1[e], __ffma2_rn(x[e], k3[e], k4[e]));
+        }
+        return Pack<T>::pack2(d);
+    }
+};
+
+// Joins the block's sums: (mean, M2) per group into `mine`. Where there are
+// fewer groups than warps, g.join warps share a group's entries and add their
+// parts in order.
+template <typename T, int ACT>
+__device__ __forceinline__ void join_block(const SlabArgs& g, const Columns<T, false, ACT>& col,
+                                           float* sums, float* parts, float2* mine, int rows, int n,
+                                           int lane, int vec, float inv_d) {
+    constexpr int PAIRS = Pack<T>::PAIRS, VEC = Pack<T>::VEC;
+    float* means = sums;
+    float* m2s = sums + g.lanes * g.cw;
+    if (lane < g.lanes) {
+        const float inv_n = n > 0 ? 1.f / static_cast<float>(n) : 0.f;
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            const int at = lane * g.cw + vec * VEC + 2 * e;
+            // the mean's distance from the pivot, and the squares about the mean
+            const float2 d = __fmul2_rn(col.s1[e], f2_splat(inv_n));
+            *reinterpret_cast<float2*>(means + at) = __fadd2_rn(col.pivot[e], d);
+            *reinterpret_cast<float2*>(m2s + at) = sub2(col.s2[e], __fmul2_rn(col.s1[e], d));
+        }
+    }
+    __syncthreads();
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
+    const int entries = g.lanes * g.D;
+    const int each = rows / g.lanes, more = rows - each * g.lanes;  // a lane's positions
+    const float inv_count = 1.f / (static_cast<float>(rows) * static_cast<float>(g.D));
+    const int share = g.join, teams = warps / share, part = warp % share;
+    const int first = part * 32 + l, step = share * 32;
+    for (int k0 = 0; k0 < g.gw; k0 += teams) {
+        const int k = k0 + warp / share;
+        const bool live = warp < teams * share && k < g.gw;
+        float s = 0.f;
+        if (live)
+            for (int i = first; i < entries; i += step) {
+                const int r = quotient(i, inv_d);
+                s = fmaf(static_cast<float>(each + (r < more)),
+                         means[r * g.cw + k * g.D + (i - r * g.D)], s);
+            }
+        s = group_allreduce<32>(s);
+        if (share > 1) {
+            if (l == 0) parts[warp] = s;
+            __syncthreads();
+            s = 0.f;
+            for (int j = 0; j < share; ++j) s += parts[warp - part + j];
+        }
+        const float mean = rows > 0 ? s * inv_count : 0.f;
+        float m2 = 0.f;
+        if (live)
+            for (int i = first; i < entries; i += step) {
+                const int r = quotient(i, inv_d);
+                const int at = r * g.cw + k * g.D + (i - r * g.D);
+                const float c = static_cast<float>(each + (r < more)), d = means[at] - mean;
+                m2 += fmaf(c * d, d, c > 0.f ? m2s[at] : 0.f);
+            }
+        m2 = group_allreduce<32>(m2);
+        if (share > 1) {
+            if (l == 0) parts[kMaxThreads / 32 + warp] = m2;
+            __syncthreads();
+            m2 = 0.f;
+            for (int j = 0; j < share; ++j) m2 += parts[kMaxThreads / 32 + warp - part + j];
+        }
+        if (live && part == 0 && l == 0) mine[k] = make_float2(mean, m2);
+    }
+}
+
+// Joins the block's sums: per channel over its lanes (in place, into the first
+// lane's row of `sums`: P, and Q behind it), then (sum w P, sum w Q) per group
+// into `mine`. Where there are fewer channels than threads, several threads
+// share a channel's lanes.
+template <typename T, int ACT>
+__device__ __forceinline__ void join_block(const SlabArgs& g, const Columns<T, true, ACT>& col,
+                                           float* sums, float2* mine, int lane, int vec,
+                                           int64_t c0) {
+    constexpr int PAIRS = Pack<T>::PAIRS, VEC = Pack<T>::VEC;
+    float* ps = sums;
+    float* qs = sums + g.lanes * g.cw;
+    if (lane < g.lanes) {
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            const int at = lane * g.cw + vec * VEC + 2 * e;
+            *reinterpret_cast<float2*>(ps + at) = col.p[e];
+            *reinterpret_cast<float2*>(qs + at) = col.q[e];
+        }
+    }
+    __syncthreads();
+    // part j of a channel adds the rows j, j + share, ... into row j, then part
+    // 0 the parts' rows
+    const int share = min(g.lanes, g.join);
+    for (int i = threadIdx.x; i < 2 * g.cw * share; i += blockDim.x) {
+        const int j = i / (2 * g.cw), c = i - j * 2 * g.cw;
+        float* at = (c < g.cw ? ps + c : qs + (c - g.cw)) + j * g.cw;
+        float s = 0.f;
+#pragma unroll 8
+        for (int r = j; r < g.lanes; r += share) s += at[(r - j) * g.cw];
+        at[0] = s;
+    }
+    __syncthreads();
+    if (share > 1) {
+        for (int c = threadIdx.x; c < 2 * g.cw; c += blockDim.x) {
+            float* at = c < g.cw ? ps + c : qs + (c - g.cw);
+            float s = 0.f;
+            for (int j = 0; j < share; ++j) s += at[j * g.cw];
+            at[0] = s;
+        }
+        __syncthreads();
+    }
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
+    for (int k = warp; k < g.gw; k += warps) {
+        float sp = 0.f, sq = 0.f;
+        for (int i = l; i < g.D; i += 32) {
+            const int c = k * g.D + i;
+            float w = 1.f;
+            if (g.a.w != nullptr)
+                w = g.a.w_f32 ? static_cast<const float*>(g.a.w)[c0 + c]
+                              : to_f32(static_cast<const T*>(g.a.w)[c0 + c]);
+            sp = fmaf(w, ps[c], sp);
+            sq = fmaf(w, qs[c], sq);
+        }
+        sp = group_allreduce<32>(sp);
+        sq = group_allreduce<32>(sq);
+        if (l == 0) mine[k] = make_float2(sp, sq);
+    }
+}
+
+// The statistics of (mean, M2) results with their counts, in rank order.
+struct Joined {
+    float mean, m2;
+};
+template <typename Get, typename Count>
+__device__ __forceinline__ Joined join_means(int n, float total, Get get, Count count) {
+    float s = 0.f;
+    for (int k = 0; k < n; ++k) s = fmaf(count(k), get(k).x, s);
+    const float mean = s / total;
+    float m2 = 0.f;
+    for (int k = 0; k < n; ++k) {
+        const float2 v = get(k);
+        const float d = v.x - mean;
+        m2 += fmaf(count(k) * d, d, v.y);
+    }
+    return {mean, m2};
+}
+
+// A thread's way through its positions: copies run kDepth positions ahead, in
+// groups of kGroup, into the thread's own slots. RING slots are reused (a group
+// is refilled as soon as it is read); without it every position has a slot and
+// stays there for the second pass.
+template <typename T, bool BWD, bool RING>
+struct Feed {
+    const T* x;      // the next position to copy
+    const T* dy;
+    int64_t step;    // elements from a position to the thread's next
+    uint32_t slots;  // this thread's first slot (a shared-memory address)
+    uint32_t pitch;  // bytes from a tensor's slot to the next one's
+    int n;
+    static constexpr uint32_t TENSORS = BWD ? 2 : 1;
+
+    __device__ __forceinline__ void issue(uint32_t slot, int left, int* status) {
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            if (u < left) {
+                copy_own(slot + u * TENSORS * pitch, x, status);
+                if constexpr (BWD) copy_own(slot + (u * TENSORS + 1) * pitch, dy, status);
+            }
+            x += step;
+            if constexpr (BWD) dy += step;
+        }
+        copies_commit();
+    }
+    // visit(i, x vector, dy vector) for every position in order
+    template <typename Visit>
+    __device__ __forceinline__ void run(int* status, Visit visit) {
+        const uint32_t group = kGroup * TENSORS * pitch;
+        uint32_t ahead = slots;
+#pragma unroll
+        for (int i = 0; i < kDepth; i += kGroup) {
+            issue(ahead, n - i, status);
+            ahead += group;
+        }
+        uint32_t at = slots;
+        [[maybe_unused]] const uint32_t end = ahead;
+#pragma unroll 1
+        for (int i = 0; i < n; i += kGroup) {
+            copies_wait<kDepth / kGroup - 1>();
+            uint4 xv[kGroup], dv[kGroup];
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) {
+                if (i + u < n) {
+                    xv[u] = ld_slot(at + u * TENSORS * pitch);
+                    if constexpr (BWD) dv[u] = ld_slot(at + (u * TENSORS + 1) * pitch);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u)
+                if (i + u < n) visit(i + u, xv[u], dv[u]);
+            issue(RING ? at : ahead, n - i - kDepth, status);
+            at += group;
+            if constexpr (RING) at = at == end ? slots : at;
+            else ahead += group;
+        }
+        copies_wait<0>();
+    }
+};
+
+// The sums of a slab (stream), or both passes over it (resident).
+template <typename T, bool BWD, int ACT, bool RESIDENT>
+__global__ void __maxnreg__(RESIDENT ? 128 : BWD ? 80 : 64) gn_slab_kernel(const __grid_constant__ SlabArgs g) {
+    constexpr int VEC = Pack<T>::VEC;
+    const Place at = place_of(g);
+    const int lane = static_cast<int>(threadIdx.x) / g.nvec;
+    const int vec = static_cast<int>(threadIdx.x) - lane * g.nvec;
+    const bool active = lane < g.lanes;
+    const float inv_d = 1.f / static_cast<float>(g.D);
+    float* sums = reinterpret_cast<float*>(rmsn_dynamic_smem);
+    float2* mine = reinterpret_cast<float2*>(sums + sums_floats(g.lanes, g.cw));
+    float2* slab = mine + g.gw;
+    float* parts = reinterpret_cast<float*>(slab + g.gw);
+    uint4* keep = reinterpret_cast<uint4*>(parts + kJoinFloats);
+    const int slots = g.lanes * g.nvec;  // a pass of the block over `lanes` positions
+    const int rows = at.rows;
+    const int64_t c0 = static_cast<int64_t>(at.split) * g.cw;
+    const int c = vec * VEC;
+    const int64_t base = (at.sample * g.a.S + at.r0 + lane) * g.a.C + c0 + c;
+    const int n = active && rows > lane ? (rows - lane - 1) / g.lanes + 1 : 0;
+    Feed<T, BWD, !RESIDENT> feed;
+    feed.x = static_cast<const T*>(g.a.x) + base;
+    feed.dy = BWD ? static_cast<const T*>(g.a.dy) + base : nullptr;
+    feed.step = static_cast<int64_t>(g.lanes) * g.a.C;
+    feed.slots = smem_u32(keep + threadIdx.x);
+    feed.pitch = static_cast<uint32_t>(slots) * 16u;
+    feed.n = n;
+    [[maybe_unused]] const uint32_t group_slots = feed.pitch * Feed<T, BWD, !RESIDENT>::TENSORS;
+    [[maybe_unused]] const float* rstd_of =
+        BWD ? g.a.rstd + at.sample * g.a.G + at.split * g.gw : nullptr;
+    Columns<T, BWD, ACT> col;
+    wait_for_prerequisite_grid();  // no global access before this
+
+    if constexpr (BWD) {
+        if (active)
+            col.start(g, g.a.mean + at.sample * g.a.G + at.split * g.gw, rstd_of, c0, c, inv_d);
+        feed.run(g.a.status, [&](int, const uint4& x, const uint4& dy) { col.add(x, dy); });
+        if (active) col.scale_q(g, rstd_of, c, inv_d);
+    } else {
+        col.start(make_uint4(0, 0, 0, 0));
+        feed.run(g.a.status, [&](int i, const uint4& x, const uint4&) {
+            if (i == 0) col.start(x);
+            col.add(x);
+        });
+    }
+    if constexpr (BWD) join_block<T>(g, col, sums, mine, lane, vec, c0);
+    else join_block<T>(g, col, sums, parts, mine, rows, n, lane, vec, inv_d);
+
+    // the cluster's blocks meet
+    __syncwarp();
+    if (g.cluster > 1) cluster_sync_all();
+    else __syncthreads();
+    const int part0 = at.chunk * g.cluster;
+    for (int k = threadIdx.x; k < g.gw; k += blockDim.x) {
+        if (!RESIDENT && at.rank != 0) break;
+        float2 v = make_float2(0.f, 0.f);
+        if constexpr (BWD) {
+            for (int r = 0; r < g.cluster; ++r) {
+                const float2 t = g.cluster > 1 ? ld_cluster_f32x2(mine + k, r) : mine[k];
+                v = __fadd2_rn(v, t);
+            }
+        } else {
+            const float d = static_cast<float>(g.D);
+            const Joined j = join_means(
+                g.cluster, part_count(g, part0, g.cluster) * d,
+                [&](int r) { return g.cluster > 1 ? ld_cluster_f32x2(mine + k, r) : mine[k]; },
+                [&](int r) { return part_count(g, part0 + r, 1) * d; });
+            v = make_float2(j.mean, j.m2);
+        }
+        if constexpr (RESIDENT) {
+            const float inv = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
+            if constexpr (BWD) {
+                slab[k] = make_float2(v.x * inv, v.y * inv);
+            } else {
+                v.y = rsqrtf(v.y * inv + g.a.eps);
+                slab[k] = v;
+                if (at.rank == 0) {
+                    const int64_t o = at.sample * g.a.G + at.split * g.gw + k;
+                    g.a.mean[o] = v.x;
+                    g.a.rstd[o] = v.y;
+                }
+            }
+        } else {
+            g.stats[(static_cast<int64_t>(at.slab) * g.chunks + at.chunk) * g.gw + k] = v;
+        }
+    }
+    if constexpr (BWD) {
+        // each block adds its share of the cluster's channel sums
+        if (g.a.dw != nullptr) {
+            const int lo = static_cast<int>(static_cast<int64_t>(2 * g.cw) * at.rank / g.cluster);
+            const int hi = static_cast<int>(static_cast<int64_t>(2 * g.cw) * (at.rank + 1) / g.cluster);
+            for (int i = lo + threadIdx.x; i < hi; i += blockDim.x) {
+                const bool q = i >= g.cw;
+                const int c = q ? i - g.cw : i;
+                const float* src = sums + (q ? g.lanes * g.cw : 0) + c;
+                float s = 0.f;
+                for (int r = 0; r < g.cluster; ++r) s += g.cluster > 1 ? ld_cluster_f32(src, r) : *src;
+                float* d;
+                if (g.rows == nullptr) d = (q ? g.a.dw : g.a.db) + c0 + c;
+                else
+                    d = g.rows + (at.sample * g.chunks + at.chunk) * 2 * g.a.C + (q ? 0 : g.a.C) + c0 + c;
+                *d = s;
+            }
+        }
+    }
+    __syncwarp();
+    if (g.cluster > 1) cluster_arrive_relaxed();  // this block is done reading its peers
+    allow_dependent_launch();
+
+    if constexpr (RESIDENT) {
+        __syncthreads();
+        if (n > 0) {
+            if constexpr (BWD) col.finish(g, rstd_of, slab, c, inv_d);
+            else col.finish(g, slab, c0, c, inv_d);
+            T* out = static_cast<T*>(g.a.out) + base;
+            [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(sizeof(T));
+            uint32_t slot = feed.slots;
+#pragma unroll 2
+            for (int i = 0; i < n; ++i) {
+                uint4 v;
+                if constexpr (BWD) v = col.apply(ld_slot(slot), ld_slot(slot + feed.pitch));
+                else v = col.apply(ld_slot(slot));
+                slot += group_slots;
+                if (RMSN_OK(span_in(out, 16, g.a.out, bytes), g.a.status)) st_global_16(out, v);
+                out += feed.step;
+            }
+        }
+    }
+    __syncwarp();
+    if (g.cluster > 1) cluster_wait();  // no block leaves while a peer reads it
+}
+
+// Stream: the second pass, over the same ranges of positions from their ends.
+template <typename T, bool BWD, int ACT>
+__global__ void __maxnreg__(BWD ? 80 : 64) gn_apply_kernel(const __grid_constant__ SlabArgs g) {
+    constexpr int VEC = Pack<T>::VEC;
+    const Place at = place_of(g);
+    const int lane = static_cast<int>(threadIdx.x) / g.nvec;
+    const int vec = static_cast<int>(threadIdx.x) - lane * g.nvec;
+    const bool active = lane < g.lanes;
+    const float inv_d = 1.f / static_cast<float>(g.D);
+    float2* slab = reinterpret_cast<float2*>(rmsn_dynamic_smem);
+    uint4* keep = reinterpret_cast<uint4*>(slab + (g.gw + 1) / 2 * 2);
+    const int rows = at.rows;
+    const int64_t c0 = static_cast<int64_t>(at.split) * g.cw;
+    const int64_t step = static_cast<int64_t>(g.lanes) * g.a.C;
+    const int n = active && rows > lane ? (rows - lane - 1) / g.lanes + 1 : 0;
+    wait_for_prerequisite_grid();  // the partial results are complete
+    {
+        const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
+        const float inv = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
+        const float2* stats = g.stats + static_cast<int64_t>(at.slab) * g.chunks * g.gw;
+        for (int k = warp; k < g.gw; k += warps) {
+            float2 v = make_float2(0.f, 0.f);
+            if constexpr (BWD) {
+                for (int i = l; i < g.chunks; i += 32)
+                    v = __fadd2_rn(v, stats[static_cast<int64_t>(i) * g.gw + k]);
+                v.x = group_allreduce<32>(v.x) * inv;
+                v.y = group_allreduce<32>(v.y) * inv;
+            } else {
+                auto count = [&](int i) {
+                    return part_count(g, i * g.cluster, g.cluster) * static_cast<float>(g.D);
+                };
+                float s = 0.f;
+                for (int i = l; i < g.chunks; i += 32)
+                    s = fmaf(count(i), stats[static_cast<int64_t>(i) * g.gw + k].x, s);
+                const float mean = group_allreduce<32>(s) * inv;
+                float m2 = 0.f;
+                for (int i = l; i < g.chunks; i += 32) {
+                    const float2 t = stats[static_cast<int64_t>(i) * g.gw + k];
+                    const float d = t.x - mean;
+                    m2 += fmaf(count(i) * d, d, t.y);
+                }
+                v = make_float2(mean, rsqrtf(group_allreduce<32>(m2) * inv + g.a.eps));
+                if (at.chunk == 0 && at.rank == 0 && l == 0) {
+                    const int64_t o = at.sample * g.a.G + at.split * g.gw + k;
+                    g.a.mean[o] = v.x;
+                    g.a.rstd[o] = v.y;
+                }
+            }
+            if (l == 0) slab[k] = v;
+        }
+    }
+    __syncthreads();
+    allow_dependent_launch();
+    if (n == 0) return;
+    const int c = vec * VEC;
+    const int64_t last = (at.sample * g.a.S + at.r0 + lane) * g.a.C + c0 + c +
+                         static_cast<int64_t>(n - 1) * step;
+    Columns<T, BWD, ACT> col;
+    if constexpr (BWD) {
+        const float* rstd_of = g.a.rstd + at.sample * g.a.G + at.split * g.gw;
+        col.start(g, g.a.mean + at.sample * g.a.G + at.split * g.gw, rstd_of, c0, c, inv_d);
+        col.finish(g, rstd_of, slab, c, inv_d);
+    } else {
+        col.finish(g, slab, c0, c, inv_d);
+    }
+    // dx may be the dy buffer: the copies of a position are waited for before
+    // this thread, and no other, writes it
+    Feed<T, BWD, true> feed;
+    feed.x = static_cast<const T*>(g.a.x) + last;
+    feed.dy = BWD ? static_cast<const T*>(g.a.dy) + last : nullptr;
+    feed.step = -step;
+    feed.slots = smem_u32(keep + threadIdx.x);
+    feed.pitch = static_cast<uint32_t>(g.lanes * g.nvec) * 16u;
+    feed.n = n;
+    T* out = static_cast<T*>(g.a.out) + last;
+    [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(sizeof(T));
+    feed.run(g.a.status, [&](int, const uint4& x, const uint4& dy) {
+        uint4 v;
+        if constexpr (BWD) v = col.apply(x, dy);
+        else v = col.apply(x);
+        if (RMSN_OK(span_in(out, 16, g.a.out, bytes), g.a.status)) st_global_16(out, v);
+        out -= step;
+    });
+}
+
+template <typename T, bool BWD, int ACT>
+SlabFn slab_kernel(SlabKind k) {
+    if (k == SlabKind::kResident) return &gn_slab_kernel<T, BWD, ACT, true>;
+    if (k == SlabKind::kSums) return &gn_slab_kernel<T, BWD, ACT, false>;
+    return &gn_apply_kernel<T, BWD, ACT>;
+}
+template <typename T>
+SlabFn slab_kernel_of(bool bwd, int act, SlabKind k) {
+    if (act == RMSNORM_ACT_SILU)
+        return bwd ? slab_kernel<T, true, RMSNORM_ACT_SILU>(k) : slab_kernel<T, false, RMSNORM_ACT_SILU>(k);
+    if (act == RMSNORM_ACT_GELU)
+        return bwd ? slab_kernel<T, true, RMSNORM_ACT_GELU>(k) : slab_kernel<T, false, RMSNORM_ACT_GELU>(k);
+    return bwd ? slab_kernel<T, true, RMSNORM_ACT_NONE>(k) : slab_kernel<T, false, RMSNORM_ACT_NONE>(k);
+}
+
+}  // namespace
+}  // namespace rmsn
