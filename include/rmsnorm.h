@@ -248,8 +248,8 @@ int rmsnorm_bwd_naive(const void *x, const void *w, const void *dy,
 #define RMSNORM_ROPE_MAX_AXES 4
 #define RMSNORM_ROPE_MAX_HEAD_DIM 256
 
-/* Strides in elements over (batch, token, head); not negative. A head's
-   elements are dense. */
+/* Strides in elements over (batch, token, head); not negative, the heads'
+   below 2^32 bytes. A head's elements are dense. */
 typedef struct {
     int64_t batch, token, head;
 } rmsnorm_strides_t;

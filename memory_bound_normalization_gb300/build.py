@@ -33,7 +33,8 @@ CHECKED_LIB_PATH = os.path.join(CHECKED_BUILD_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "bwd_f32.cu", "bwd_bf16.cu", "bwd_f16.cu",
            "bwd_res_f32.cu", "bwd_res_bf16.cu", "bwd_res_f16.cu", "naive.cu", "probe.cu",
-           "noalloc.cu", "rope.cu", "pair_sum.cu", "group_norm.cu",
+           "noalloc.cu", "rope.cu", "rope_f32.cu", "rope_bf16.cu", "rope_f16.cu",
+           "pair_sum.cu", "group_norm.cu",
            "group_norm_f32.cu", "group_norm_bf16.cu", "group_norm_f16.cu", "group_norm_scalar.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -215,6 +215,7 @@ int rope_descriptor(const rmsnorm_rope_t* r, int dtype, RopeArgs* a) {
     a->length = static_cast<int>(r->length);
     a->head_dim = r->head_dim;
     a->rot = r->rotary_dim;
+    a->axes = r->axes;
     a->pos64 = r->positions_64 != 0;
     a->w_f32 = weight_size(dtype) == 4;
     for (int i = 0; i < 3; ++i) a->ps[i] = r->position_stride[i];
@@ -224,9 +225,10 @@ int rope_descriptor(const rmsnorm_rope_t* r, int dtype, RopeArgs* a) {
 }
 
 // A tensor of a rotary call: non-null, aligned to its elements, strides not
-// negative.
+// negative and the heads' below 2^32 bytes.
 int rope_tensor(const void* p, const rmsnorm_strides_t& s, int size, int64_t (&out)[3]) {
-    if (p == nullptr || s.batch < 0 || s.token < 0 || s.head < 0) return RMSNORM_ERR_INVALID_ARG;
+    if (p == nullptr || s.batch < 0 || s.token < 0 || s.head < 0 || s.head > UINT32_MAX / size)
+        return RMSNORM_ERR_INVALID_ARG;
     if (!aligned(p, size)) return RMSNORM_ERR_MISALIGNED;
     out[0] = s.batch;
     out[1] = s.token;

@@ -32,7 +32,7 @@ struct RopeArgs {
     const float* inv_freq;
     int64_t tokens;   // batch * length
     int length;
-    int head_dim, rot;
+    int head_dim, rot, axes;
     float eps;
     int pos64, w_f32;
     float sign;       // -1 turns back (the backward)

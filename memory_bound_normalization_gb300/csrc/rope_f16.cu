@@ -1,0 +1,10 @@
+// Rotary kernels of f16 tensors.
+#include "rope_kernels.cuh"
+
+namespace rmsn {
+
+RopeFn rope_kernel_f16(int e, int units, bool bwd, bool adjacent, bool norm) {
+    return kernel_for_type<__half>(e, units, bwd, adjacent, norm);
+}
+
+}  // namespace rmsn

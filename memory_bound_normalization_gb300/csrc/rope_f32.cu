@@ -1,0 +1,10 @@
+// Rotary kernels of f32 tensors.
+#include "rope_kernels.cuh"
+
+namespace rmsn {
+
+RopeFn rope_kernel_f32(int e, int units, bool bwd, bool adjacent, bool norm) {
+    return kernel_for_type<float>(e, units, bwd, adjacent, norm);
+}
+
+}  // namespace rmsn

@@ -1,0 +1,775 @@
+// Rotary positions of several axes for queries and keys, with the RMSNorm of
+// their heads (the QK-norm) fused in front, forward and backward.
+//
+// A head of D elements holds rot/2 rotated pairs (a, b) and D - rot elements
+// that pass. With theta = position[axis(p)] * inv_freq[p]:
+//   forward   n = x * rstd * w (n = x without weights)
+//             y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin
+//   backward  g = dy turned back by theta,  h = g * w,  xhat = x * rstd
+//             dx = rstd * (h - xhat * mean(h * xhat)),  dw = sum g * xhat
+// The backward recomputes rstd: the row is in registers for the second sum
+// anyway, and one saved value per 128-element row would cost 1.6% of traffic.
+//
+// Everything is bound by DRAM: a row is read once into registers and written
+// once. A group of `lanes` lanes shares a row and each lane owns whole pairs
+// (both halves), so the rotation needs no exchange between lanes and the row
+// sum is one butterfly. The elements that pass are pairs of a zero angle.
+//
+// Angles: one turn is 2^64, so the product of an integer position and the
+// frequency in turns wraps exactly where the circle does, however far the
+// position; an fp32 product at position 2^20 would be off by 0.06 radians.
+#pragma once
+
+#include "common.cuh"
+#include "rope.h"
+
+namespace rmsn {
+namespace {
+
+// E elements of T as floats, by one load or store of E * sizeof(T) bytes.
+template <int BYTES> struct Word;
+template <> struct Word<16> { using type = uint4; };
+template <> struct Word<8> { using type = uint2; };
+template <> struct Word<4> { using type = uint32_t; };
+template <> struct Word<2> { using type = uint16_t; };
+
+template <typename T, int E>
+struct Elems {
+    static constexpr int P = (E + 1) / 2;  // float2 values; one element leaves .y zero
+    using W = typename Word<E * static_cast<int>(sizeof(T))>::type;
+    union U {
+        W w;
+        T e[E];
+        __device__ U() {}
+    };
+    // coherent: the output may be the input's buffer
+    __device__ __forceinline__ static W load(const T* p) {
+        W v;
+        if constexpr (sizeof(W) == 16)
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+        else if constexpr (sizeof(W) == 8)
+            asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+        else
+            v = *reinterpret_cast<const W*>(p);
+        return v;
+    }
+    __device__ __forceinline__ static void unpack(const W& w, float2 (&f)[P]) {
+        if constexpr (sizeof(W) == 16) {
+            Pack<T>::unpack2(w, f);
+        } else {
+            U u;
+            u.w = w;
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                f[i] = make_float2(to_f32(u.e[2 * i]), 2 * i + 1 < E ? to_f32(u.e[(2 * i + 1) % E]) : 0.f);
+        }
+    }
+    // each element rounded once, to nearest even
+    __device__ __forceinline__ static W pack(const float2 (&f)[P]) {
+        if constexpr (sizeof(W) == 16) {
+            return Pack<T>::pack2(f);
+        } else {
+            U u;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float v = i % 2 ? f[i / 2].y : f[i / 2].x;
+                if constexpr (std::is_same<T, float>::value) u.e[i] = v;
+                else u.e[i] = Pack<T>::from_float(v);
+            }
+            return u.w;
+        }
+    }
+};
+
+// inv_freq / 2 pi in units of 2^-64 turns: the 24-bit mantissa times 2^66/2pi,
+// shifted by the exponent. Off by at most one unit for |inv_freq| < 2^25.
+__device__ __forceinline__ uint64_t turns_per_position(float f) {
+    const uint32_t bits = __float_as_uint(f);
+    const int e = max(1, static_cast<int>((bits >> 23) & 255));
+    const uint32_t m = (bits & 0x7fffffu) | ((bits & 0x7f800000u) ? 0x800000u : 0u);
+    constexpr uint64_t kTwo66OverTwoPi = 0xA2F9836E4E441529ull;
+    const uint64_t lo = kTwo66OverTwoPi * m, hi = __umul64hi(kTwo66OverTwoPi, m);
+    const int shift = 152 - e;  // of hi:lo to the right
+    uint64_t v;
+    if (shift >= 64) v = shift < 128 ? hi >> (shift - 64) : 0;
+    else if (shift > 0) v = (lo >> shift) | (hi << (64 - shift));
+    else v = shift > -64 ? lo << -shift : 0;
+    return (bits >> 31) ? 0ull - v : v;
+}
+
+// cos and sin of pos * turns, with 2^64 turns a circle. 16-bit outputs take the
+// fast functions (off by 2^-20, half a step of fp16 is 2^-12).
+template <typename T>
+__device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t turns) {
+    const int64_t at = static_cast<int64_t>(static_cast<uint64_t>(pos) * turns);
+    float s, c;
+    if constexpr (sizeof(T) == 2) {
+        // the top 32 bits of the angle, in radians
+        __sincosf(static_cast<float>(static_cast<int32_t>(at >> 32)) * 1.46291807926715968e-9f, &s, &c);
+    } else {
+        sincospif(__ll2float_rn(at) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
+    }
+    return make_float2(c, s);
+}
+
+// The tables (cos and sin of a token's pairs; the weights of a pair's members)
+// hold D floats: two pairs a 16-byte word, firsts before seconds, so that they
+// load as the float2 values they multiply; lanes of a group read consecutive
+// words and do not conflict.
+// UNITS, where it is not 0, is the number of units of a head, a power of two and
+// the lanes of a group: table offsets, lane masks and the row sum's steps are
+// then constants. (Left to run time, they and the kernel parameters reloaded
+// for them made up half of the forward's instructions.)
+template <int E>
+__device__ __forceinline__ int table_at(int units, int p) {
+    if constexpr (E == 1) return 2 * p;
+    const int u = p / E, e = p % E;
+    return ((e / 2) * units + u) * 4 + e % 2;
+}
+template <int E>
+constexpr int kSecond = E == 1 ? 1 : 2;  // floats from a pair's first value to its second
+
+// The two E-element pieces of unit u: its first elements and its second.
+template <int E, bool ADJ>
+__device__ __forceinline__ void unit_offsets(const RopeArgs& a, int u, int& lo, int& hi) {
+    const int p = u * E;
+    if constexpr (ADJ) {
+        lo = 2 * p;
+        hi = 2 * p + E;
+    } else {
+        const int half = a.rot / 2;
+        if (p < half) {
+            lo = p;
+            hi = p + half;
+        } else {
+            lo = a.rot + (p - half);
+            hi = lo + (a.head_dim - a.rot) / 2;
+        }
+    }
+}
+// Element index of the members of pair p.
+template <bool ADJ>
+__device__ __forceinline__ void pair_members(const RopeArgs& a, int p, int& i, int& j) {
+    const int half = a.rot / 2;
+    if (ADJ) {
+        i = 2 * p;
+        j = i + 1;
+    } else if (p < half) {
+        i = p;
+        j = p + half;
+    } else {
+        i = a.rot + (p - half);
+        j = i + (a.head_dim - a.rot) / 2;
+    }
+}
+// (first members, second members) of the unit's pairs from its two pieces, and
+// back.
+template <int E, bool ADJ>
+__device__ __forceinline__ void split_pairs(const float2 (&lo)[(E + 1) / 2], const float2 (&hi)[(E + 1) / 2],
+                                            float2 (&f)[(E + 1) / 2], float2 (&s)[(E + 1) / 2]) {
+    constexpr int P = (E + 1) / 2;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        if constexpr (ADJ && E > 1) {
+            const float2 v = 2 * i < P ? lo[(2 * i) % P] : hi[(2 * i) % P];
+            const float2 w = 2 * i + 1 < P ? lo[(2 * i + 1) % P] : hi[(2 * i + 1) % P];
+            f[i] = make_float2(v.x, w.x);
+            s[i] = make_float2(v.y, w.y);
+        } else {
+            f[i] = lo[i];
+            s[i] = hi[i];
+        }
+    }
+}
+template <int E, bool ADJ>
+__device__ __forceinline__ void join_pairs(const float2 (&f)[(E + 1) / 2], const float2 (&s)[(E + 1) / 2],
+                                           float2 (&lo)[(E + 1) / 2], float2 (&hi)[(E + 1) / 2]) {
+    constexpr int P = (E + 1) / 2;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        if constexpr (ADJ && E > 1) {
+            const float2 v = make_float2(f[i].x, s[i].x), w = make_float2(f[i].y, s[i].y);
+            if (2 * i < P) lo[(2 * i) % P] = v;
+            else hi[(2 * i) % P] = v;
+            if (2 * i + 1 < P) lo[(2 * i + 1) % P] = w;
+            else hi[(2 * i + 1) % P] = w;
+        } else {
+            lo[i] = f[i];
+            hi[i] = s[i];
+        }
+    }
+}
+
+template <int UNITS>
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+    if constexpr (UNITS > 0) return group_allreduce<UNITS>(v);
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2)
+        if (off < lanes) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+__device__ __forceinline__ int64_t position_at(const RopeArgs& a, int64_t at) {
+    return a.pos64 ? static_cast<const int64_t*>(a.pos)[at]
+                   : static_cast<int64_t>(static_cast<const int32_t*>(a.pos)[at]);
+}
+
+// Element offset of a token in a tensor with these (batch, token) strides.
+__device__ __forceinline__ int64_t token_offset(const RopeArgs& a, int64_t batch, int64_t token,
+                                                int64_t tok) {
+    const unsigned b = static_cast<unsigned>(tok) / static_cast<unsigned>(a.length);
+    return b * batch + (tok - static_cast<int64_t>(b) * a.length) * token;
+}
+
+// What a block knows of a tile of tokens: the tokens' addresses in up to four
+// tensors and their positions. Three of them in turn: while the block's
+// slowest warp still reads this tile's and the next one's, the one after is
+// written.
+constexpr int kTensors = 4;
+struct TileInfo {
+    int64_t addr[kTensors][kRopeMaxTile];
+    int64_t pos[RMSNORM_ROPE_MAX_AXES][kRopeMaxTile];
+};
+static_assert((kTensors + RMSNORM_ROPE_MAX_AXES) * kRopeMaxTile <= kRopeThreads,
+              "a thread for each value");
+
+// A block's range of tokens, split evenly, in tiles of at most a.tile tokens.
+struct TileRange {
+    int64_t first;
+    int tokens, tile, tiles;
+    __device__ __forceinline__ TileRange(const RopeArgs& a, int part, int parts) {
+        first = a.tokens * part / parts;
+        tokens = static_cast<int>(a.tokens * (part + 1) / parts - first);
+        tiles = (tokens + a.tile - 1) / a.tile;
+        tile = tiles > 0 ? (tokens + tiles - 1) / tiles : 1;
+    }
+    __device__ __forceinline__ int count(int i) const { return min(tile, tokens - i * tile); }
+};
+// A tensor's base address and its strides over (batch, token), in bytes.
+struct TokenBase {
+    int64_t base, batch, token;
+};
+__device__ __forceinline__ TokenBase token_base(const void* p, const int64_t (&s)[3], int size) {
+    return {reinterpret_cast<int64_t>(p), s[0] * size, s[1] * size};
+}
+// This thread's value of a tile's info, to be stored once it is needed: a
+// position's load is then long back. `mine`: the tensor whose tokens it does.
+__device__ __forceinline__ int64_t fetch_info(const RopeArgs& a, const TileRange& range, int tile,
+                                              const TokenBase& mine) {
+    const int i = threadIdx.x / kRopeMaxTile, t = threadIdx.x % kRopeMaxTile;
+    if (i >= kTensors + a.axes || tile >= range.tiles || t >= range.count(tile)) return 0;
+    const int64_t tok = range.first + tile * range.tile + t;
+    if (i < kTensors) return mine.base + token_offset(a, mine.batch, mine.token, tok);
+    return position_at(a, (i - kTensors) * a.ps[0] + token_offset(a, a.ps[1], a.ps[2], tok));
+}
+__device__ __forceinline__ void store_info(const RopeArgs& a, TileInfo& info, int64_t v) {
+    const int i = threadIdx.x / kRopeMaxTile, t = threadIdx.x % kRopeMaxTile;
+    if (i < kTensors) info.addr[i][t] = v;
+    else if (i < kTensors + a.axes) info.pos[i - kTensors][t] = v;
+}
+
+// A thread's pair: which one, and what turns it. Threads beyond a whole number
+// of tokens' pairs have none.
+struct PairOf {
+    uint64_t turns;
+    int pair, token, stride, axis;  // its first token of a tile, and the step
+    bool has, turned, bad;
+};
+__device__ __forceinline__ PairOf pair_of(const RopeArgs& a) {
+    PairOf p;
+    const int pairs = a.head_dim / 2;
+    p.stride = kRopeThreads / pairs;  // at least 2
+    p.token = threadIdx.x / pairs;
+    p.pair = threadIdx.x - p.token * pairs;
+    p.has = p.token < p.stride;
+    p.turned = p.has && p.pair < a.rot / 2;
+    p.axis = p.turned ? a.axis[p.pair] : 0;
+    const float f = p.turned ? a.inv_freq[p.pair] : 0.f;
+    p.turns = turns_per_position(f);
+    p.bad = !isfinite(f);
+    return p;
+}
+// cos/sin of every pair of a tile's tokens into `tab` (D floats a token).
+template <typename T, int E>
+__device__ __forceinline__ void fill_angles(const RopeArgs& a, const PairOf& p, float* tab,
+                                            const TileInfo& info, int tokens) {
+    if (!p.has) return;
+    float* d = tab + table_at<E>(a.units, p.pair);
+#pragma unroll 2
+    for (int t = p.token; t < tokens; t += p.stride) {
+        float2 cs = make_float2(1.f, 0.f);
+        if (p.turned) cs = cos_sin<T>(info.pos[p.axis][t], p.turns);
+        if (p.bad) cs.x = cs.y = __int_as_float(0x7fc00000);  // NaN
+        d[t * a.head_dim] = cs.x;
+        d[t * a.head_dim + kSecond<E>] = a.sign * cs.y;
+    }
+}
+
+// Weights of one tensor as fp32, in the order of the angle tables.
+template <typename T, int E, bool ADJ>
+__device__ __forceinline__ void fill_weights(const RopeArgs& a, const void* w, float* tab) {
+    for (int p = threadIdx.x; p < a.head_dim / 2; p += kRopeThreads) {
+        int i, j;
+        pair_members<ADJ>(a, p, i, j);
+        float* d = tab + table_at<E>(a.units, p);
+        d[0] = a.w_f32 ? static_cast<const float*>(w)[i] : to_f32(static_cast<const T*>(w)[i]);
+        d[kSecond<E>] = a.w_f32 ? static_cast<const float*>(w)[j] : to_f32(static_cast<const T*>(w)[j]);
+    }
+}
+
+template <int E, int UNITS>
+__device__ __forceinline__ void read_table(const float* tab, int some_units, int u,
+                                           float2 (&f)[(E + 1) / 2], float2 (&s)[(E + 1) / 2]) {
+    const int units = UNITS > 0 ? UNITS : some_units;
+    if constexpr (E == 1) {
+        const float2 v = *reinterpret_cast<const float2*>(tab + 2 * u);
+        f[0] = make_float2(v.x, 0.f);
+        s[0] = make_float2(v.y, 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(tab + (i * units + u) * 4);
+            f[i] = make_float2(v.x, v.y);
+            s[i] = make_float2(v.z, v.w);
+        }
+    }
+}
+
+// x * c - y * s and y * c + x * s. (The negation rides on scalar multiply-adds:
+// the packed form has none, and two sign flips a pair cost more.)
+__device__ __forceinline__ void turn(float2 x, float2 y, float2 c, float2 s, float2& ox, float2& oy) {
+    const float2 xc = __fmul2_rn(x, c), xs = __fmul2_rn(x, s);
+    ox = make_float2(fmaf(-y.x, s.x, xc.x), fmaf(-y.y, s.y, xc.y));
+    oy = __ffma2_rn(y, c, xs);
+}
+
+// One past the last element of a tensor that the call may touch (strides
+// are not negative), for the checked build.
+[[maybe_unused]] __device__ __forceinline__ int64_t extent_bytes(const RopeArgs& a, const RopeTensor& t,
+                                                const int64_t (&s)[3], int size) {
+    const int64_t batch = a.tokens / a.length;
+    return ((batch - 1) * s[0] + (a.length - 1) * s[1] + (t.heads - 1) * s[2] + a.head_dim) * size;
+}
+
+// Units a lane owns at most: head_dim / 2 pairs over 32 lanes.
+template <int E> constexpr int kUnitsPerLane = E >= 4 ? 1 : kRopeMaxPairs / 32 / E;
+
+// Byte offsets of a lane's pieces in a head: the first one's, and the second's
+// distance from it, constant where the geometry is.
+template <typename T, int E, bool ADJ, int UNITS>
+struct Pieces {
+    static constexpr int NU = UNITS > 0 ? 1 : kUnitsPerLane<E>;
+    int lo[NU], gap[UNITS > 0 ? 1 : NU];
+    __device__ __forceinline__ void start(const RopeArgs& a, int lane, int lanes) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            int l, h;
+            unit_offsets<E, ADJ>(a, lane + i * lanes, l, h);
+            lo[i] = l * static_cast<int>(sizeof(T));
+            gap[i] = (h - l) * static_cast<int>(sizeof(T));
+        }
+    }
+    __device__ __forceinline__ int hop(int i) const {
+        if constexpr (UNITS > 0) return (ADJ ? E : E * UNITS) * static_cast<int>(sizeof(T));
+        return gap[i];
+    }
+};
+// Address of a head's row: strides of heads are below 2^32 bytes.
+__device__ __forceinline__ uint64_t row_address(int64_t token, int head, uint32_t step) {
+    return static_cast<uint64_t>(token) + static_cast<uint64_t>(static_cast<uint32_t>(head)) * step;
+}
+
+// A group's way through the rows (token, head) of a tile, groups apart.
+struct RowCursor {
+    int t, head;
+    __device__ __forceinline__ void start(int group, int heads) {
+        t = group / heads;
+        head = group - t * heads;
+    }
+    __device__ __forceinline__ void advance(int dt, int dh, int heads) {
+        t += dt;
+        head += dh;
+        if (head >= heads) {
+            head -= heads;
+            ++t;
+        }
+    }
+};
+
+// Both kernels are persistent: a block strides over tiles of tokens. The
+// angles of the next tile are filled into the other of two tables before this
+// tile's rows are worked on, so one barrier a tile is enough; each group of
+// lanes takes rows (token, head), the next row's loads issued before the
+// current one is worked on, across tiles too.
+
+// ------------------------------------------------------------------ forward
+// With few tokens the blocks of a tile share out its heads.
+template <typename T, int E, bool ADJ, bool NORM, int UNITS>
+__global__ void __launch_bounds__(kRopeThreads, E >= 4 ? 4 : 3) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int NU = UNITS > 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
+    const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
+    using X = Elems<T, E>;
+    using W = typename X::W;
+    __shared__ TileInfo info[3];
+    float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem);  // [2][D] when NORM
+    float* tabs = wtab + (NORM ? 2 * D : 0);            // [2][tile][D]
+    const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
+    const int groups = kRopeThreads / lanes;
+
+    const int part = static_cast<int>(blockIdx.x) / a.splits;
+    const int split = static_cast<int>(blockIdx.x) - part * a.splits;
+    const TileRange range(a, part, static_cast<int>(gridDim.x) / a.splits);
+    if (range.tiles == 0) return;
+    const TokenBase mine = [&] {
+        const int i = threadIdx.x / kRopeMaxTile;
+        const RopeTensor& x = a.t[i >= 2 ? 1 : 0];
+        return i % 2 ? token_base(x.out, x.os, sizeof(T)) : token_base(x.x, x.xs, sizeof(T));
+    }();
+    // heads [h0, h0 + heads) of each token of either tensor
+    const int qh0 = a.t[0].heads * split / a.splits, kh0 = a.t[1].heads * split / a.splits;
+    const int qheads = a.t[0].heads * (split + 1) / a.splits - qh0;
+    const int kheads = a.t[1].heads * (split + 1) / a.splits - kh0;
+    Pieces<T, E, ADJ, UNITS> at;
+    at.start(a, lane, lanes);
+    const float inv_d = 1.f / static_cast<float>(D);
+    wait_for_prerequisite_grid();  // no global access before this
+
+    int64_t fetched = fetch_info(a, range, 0, mine);
+    const PairOf pair = pair_of(a);
+    if constexpr (NORM) {
+        fill_weights<T, E, ADJ>(a, a.t[0].w, wtab);
+        if (a.t[1].heads > 0) fill_weights<T, E, ADJ>(a, a.t[1].w, wtab + D);
+    }
+    store_info(a, info[0], fetched);
+    fetched = fetch_info(a, range, 1, mine);
+    __syncthreads();
+    RowCursor row{0, 0};
+    W lo[NU], hi[NU];
+    auto load = [&](int tokens, const int64_t* addr, int h0, uint32_t head_step) {
+        if (row.t >= tokens) return;
+        const uint64_t src = row_address(addr[row.t], h0 + row.head, head_step);
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+            if (UNITS > 0 || lane + i * lanes < a.units) {
+                const uint64_t p = src + at.lo[i];
+                lo[i] = X::load(reinterpret_cast<const T*>(p));
+                hi[i] = X::load(reinterpret_cast<const T*>(p + at.hop(i)));
+            }
+    };
+    // starts on the rows of tensor w of a tile
+    auto begin = [&](int w, int tokens, const TileInfo& from) {
+        const int h0 = w ? kh0 : qh0, n = w ? kheads : qheads;
+        row.start(group, max(n, 1));
+        load(n > 0 ? tokens : 0, from.addr[2 * w], h0,
+             static_cast<uint32_t>(a.t[w].xs[2] * sizeof(T)));
+    };
+    begin(0, range.count(0), info[0]);
+    fill_angles<T, E>(a, pair, tabs, info[0], range.count(0));
+    int buf = 0, slot = 0;
+    const int tensors = a.t[1].heads > 0 ? 2 : 1;
+#pragma unroll 1
+    for (int tile = 0; tile < range.tiles; ++tile, buf ^= 1) {
+        const int tokens = range.count(tile);
+        const bool more = tile + 1 < range.tiles;
+        const int after = slot == 2 ? 0 : slot + 1;
+        const float* tab = tabs + buf * a.tile * D;
+        if (more) {
+            store_info(a, info[after], fetched);
+            fetched = fetch_info(a, range, tile + 2, mine);
+        }
+        __syncthreads();  // this tile's table is filled; the other one's readers are done
+        if (more)
+            fill_angles<T, E>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[after], range.count(tile + 1));
+#pragma unroll 1
+        for (int w = 0; w < tensors; ++w) {
+            const int h0 = w ? kh0 : qh0, heads = w ? kheads : qheads;
+            const int dt = heads > 0 ? groups / heads : 0, dh = groups - dt * heads;
+            const uint32_t in_step = static_cast<uint32_t>(a.t[w].xs[2] * sizeof(T));
+            const uint32_t out_step = static_cast<uint32_t>(a.t[w].os[2] * sizeof(T));
+            const int64_t* in_addr = info[slot].addr[2 * w];
+            const int64_t* out_addr = info[slot].addr[2 * w + 1];
+            const int passes = (tokens * heads + groups - 1) / groups;
+#pragma unroll 1
+            for (int pass = 0; pass < max(passes, 1); ++pass) {
+                const RowCursor cur = row;
+                const bool live = cur.t < tokens && pass < passes;
+                float2 f[NU][P], s[NU][P];
+#pragma unroll
+                for (int i = 0; i < NU; ++i) {
+                    float2 l[P], h[P];
+                    X::unpack(lo[i], l);
+                    X::unpack(hi[i], h);
+                    split_pairs<E, ADJ>(l, h, f[i], s[i]);
+                }
+                if (pass + 1 < passes) {
+                    row.advance(dt, dh, heads);
+                    load(tokens, in_addr, h0, in_step);
+                } else if (w + 1 < tensors) {
+                    begin(w + 1, tokens, info[slot]);
+                } else if (more) {
+                    begin(0, range.count(tile + 1), info[after]);
+                }
+                if constexpr (NORM) {
+                    float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < NU; ++i)
+                        if (live && (UNITS > 0 || lane + i * lanes < a.units)) {
+#pragma unroll
+                            for (int e = 0; e < P; ++e)
+                                ss = __ffma2_rn(f[i][e], f[i][e], __ffma2_rn(s[i][e], s[i][e], ss));
+                        }
+                    const float2 rs = f2_splat(rsqrtf(lanes_sum<UNITS>(ss.x + ss.y, lanes) * inv_d + a.eps));
+#pragma unroll
+                    for (int i = 0; i < NU; ++i)
+                        if (live && (UNITS > 0 || lane + i * lanes < a.units)) {
+                            float2 wf[P], ws[P];
+                            read_table<E, UNITS>(wtab + w * D, a.units, lane + i * lanes, wf, ws);
+#pragma unroll
+                            for (int e = 0; e < P; ++e) {
+                                f[i][e] = __fmul2_rn(__fmul2_rn(f[i][e], rs), wf[e]);
+                                s[i][e] = __fmul2_rn(__fmul2_rn(s[i][e], rs), ws[e]);
+                            }
+                        }
+                }
+                if (!live) continue;
+                const uint64_t dst = row_address(out_addr[cur.t], h0 + cur.head, out_step);
+#pragma unroll
+                for (int i = 0; i < NU; ++i) {
+                    if (UNITS == 0 && lane + i * lanes >= a.units) continue;
+                    float2 c[P], n[P], yf[P], ys[P], yl[P], yh[P];
+                    read_table<E, UNITS>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
+#pragma unroll
+                    for (int e = 0; e < P; ++e) turn(f[i][e], s[i][e], c[e], n[e], yf[e], ys[e]);
+                    join_pairs<E, ADJ>(yf, ys, yl, yh);
+                    W* dl = reinterpret_cast<W*>(dst + at.lo[i]);
+                    W* dhi = reinterpret_cast<W*>(dst + at.lo[i] + at.hop(i));
+                    if (RMSN_OK(span_in(dl, sizeof(W), a.t[w].out, extent_bytes(a, a.t[w], a.t[w].os, sizeof(T))) &&
+                                    span_in(dhi, sizeof(W), a.t[w].out, extent_bytes(a, a.t[w], a.t[w].os, sizeof(T))),
+                                a.status)) {
+                        *dl = X::pack(yl);
+                        *dhi = X::pack(yh);
+                    }
+                }
+            }
+        }
+        slot = after;
+    }
+    allow_dependent_launch();
+}
+
+// ----------------------------------------------------------------- backward
+// The first blocks0 blocks take the queries and the others the keys, with
+// their lanes' shares of dw in registers; at the end the groups' shares are
+// added in a fixed order into the block's partial row. No floating-point
+// atomics.
+template <typename T, int E, bool ADJ, int UNITS>
+__global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
+    rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int NU = UNITS > 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
+    const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
+    using X = Elems<T, E>;
+    using W = typename X::W;
+    __shared__ TileInfo info[3];
+    float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem);
+    float* tabs = wtab + D;  // [2][tile][D]
+    const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
+    const int groups = kRopeThreads / lanes;
+
+    const int which = static_cast<int>(blockIdx.x) >= a.blocks0 ? 1 : 0;
+    const RopeTensor& x = a.t[which];
+    const TileRange range(a, static_cast<int>(blockIdx.x) - which * a.blocks0,
+                          which ? static_cast<int>(gridDim.x) - a.blocks0 : a.blocks0);
+    const int heads = x.heads;
+    const TokenBase mine = [&] {
+        const int i = threadIdx.x / kRopeMaxTile;
+        if (i == 0) return token_base(x.x, x.xs, sizeof(T));
+        return i == 1 ? token_base(x.dy, x.dys, sizeof(T)) : token_base(x.out, x.os, sizeof(T));
+    }();
+    const float inv_d = 1.f / static_cast<float>(D);
+    const int dt = groups / heads, dh = groups - dt * heads;
+    const uint32_t x_step = static_cast<uint32_t>(x.xs[2] * sizeof(T));
+    const uint32_t dy_step = static_cast<uint32_t>(x.dys[2] * sizeof(T));
+    const uint32_t out_step = static_cast<uint32_t>(x.os[2] * sizeof(T));
+    Pieces<T, E, ADJ, UNITS> at;
+    at.start(a, lane, lanes);
+    float2 dwf[NU][P], dws[NU][P];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) dwf[i][e] = dws[i][e] = make_float2(0.f, 0.f);
+    }
+    wait_for_prerequisite_grid();  // no global access before this
+
+    int64_t fetched = fetch_info(a, range, 0, mine);
+    const PairOf pair = pair_of(a);
+    fill_weights<T, E, ADJ>(a, x.w, wtab);
+    store_info(a, info[0], fetched);
+    fetched = fetch_info(a, range, 1, mine);
+    __syncthreads();
+    W lo[NU], hi[NU], glo[NU], ghi[NU];
+    auto load = [&](const RowCursor& r, int tokens, const TileInfo& from) {
+        if (r.t >= tokens) return;
+        const uint64_t src = row_address(from.addr[0][r.t], r.head, x_step);
+        const uint64_t dys = row_address(from.addr[1][r.t], r.head, dy_step);
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+            if (UNITS > 0 || lane + i * lanes < a.units) {
+                const uint64_t p = src + at.lo[i], q = dys + at.lo[i];
+                lo[i] = X::load(reinterpret_cast<const T*>(p));
+                hi[i] = X::load(reinterpret_cast<const T*>(p + at.hop(i)));
+                glo[i] = X::load(reinterpret_cast<const T*>(q));
+                ghi[i] = X::load(reinterpret_cast<const T*>(q + at.hop(i)));
+            }
+    };
+    // fill_weights is complete: this lane's weights, in registers
+    float2 wf[NU][P], ws[NU][P];
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+        if (UNITS > 0 || lane + i * lanes < a.units)
+            read_table<E, UNITS>(wtab, a.units, lane + i * lanes, wf[i], ws[i]);
+    RowCursor row;
+    row.start(group, heads);
+    if (range.tiles > 0) {
+        load(row, range.count(0), info[0]);
+        fill_angles<T, E>(a, pair, tabs, info[0], range.count(0));
+    }
+    int buf = 0, slot = 0;
+#pragma unroll 1
+    for (int tile = 0; tile < range.tiles; ++tile, buf ^= 1) {
+        const int tokens = range.count(tile);
+        const bool more = tile + 1 < range.tiles;
+        const int after = slot == 2 ? 0 : slot + 1;
+        const float* tab = tabs + buf * a.tile * D;
+        if (more) {
+            store_info(a, info[after], fetched);
+            fetched = fetch_info(a, range, tile + 2, mine);
+        }
+        __syncthreads();  // this tile's table is filled; the other one's readers are done
+        if (more)
+            fill_angles<T, E>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[after], range.count(tile + 1));
+        const int passes = (tokens * heads + groups - 1) / groups;
+        for (int pass = 0; pass < passes; ++pass) {
+            const RowCursor cur = row;
+            const bool live = cur.t < tokens;
+            W xl[NU], xh[NU];
+            float2 gf[NU][P], gs[NU][P];
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                float2 l[P], h[P];
+                xl[i] = lo[i];
+                xh[i] = hi[i];
+                X::unpack(glo[i], l);
+                X::unpack(ghi[i], h);
+                split_pairs<E, ADJ>(l, h, gf[i], gs[i]);
+            }
+            if (pass + 1 < passes) {
+                row.advance(dt, dh, heads);
+                load(row, tokens, info[slot]);
+            } else if (more) {
+                row.start(group, heads);
+                load(row, range.count(tile + 1), info[after]);
+            }
+            float2 ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                if (!live || (UNITS == 0 && lane + i * lanes >= a.units)) continue;
+                float2 l[P], h[P], f[P], s[P], c[P], n[P];
+                X::unpack(xl[i], l);
+                X::unpack(xh[i], h);
+                split_pairs<E, ADJ>(l, h, f, s);
+                read_table<E, UNITS>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
+#pragma unroll
+                for (int e = 0; e < P; ++e) turn(gf[i][e], gs[i][e], c[e], n[e], gf[i][e], gs[i][e]);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    ss = __ffma2_rn(f[e], f[e], __ffma2_rn(s[e], s[e], ss));
+                    hx = __ffma2_rn(__fmul2_rn(gf[i][e], wf[i][e]), f[e],
+                                    __ffma2_rn(__fmul2_rn(gs[i][e], ws[i][e]), s[e], hx));
+                }
+            }
+            const float sum = lanes_sum<UNITS>(ss.x + ss.y, lanes), dot = lanes_sum<UNITS>(hx.x + hx.y, lanes);
+            const float rs = rsqrtf(sum * inv_d + a.eps);
+            const float2 rs2 = f2_splat(rs);
+            // rs (h - xhat mean(h xhat)) = (g rs) w + x coef
+            const float2 coef = f2_splat(-rs * rs * rs * (dot * inv_d));
+            if (!live) continue;
+            const uint64_t dst = row_address(info[slot].addr[2][cur.t], cur.head, out_step);
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                if (UNITS == 0 && lane + i * lanes >= a.units) continue;
+                float2 l[P], h[P], f[P], s[P];
+                X::unpack(xl[i], l);
+                X::unpack(xh[i], h);
+                split_pairs<E, ADJ>(l, h, f, s);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const float2 gfr = __fmul2_rn(gf[i][e], rs2), gsr = __fmul2_rn(gs[i][e], rs2);
+                    dwf[i][e] = __ffma2_rn(gfr, f[e], dwf[i][e]);
+                    dws[i][e] = __ffma2_rn(gsr, s[e], dws[i][e]);
+                    f[e] = __ffma2_rn(gfr, wf[i][e], __fmul2_rn(f[e], coef));
+                    s[e] = __ffma2_rn(gsr, ws[i][e], __fmul2_rn(s[e], coef));
+                }
+                join_pairs<E, ADJ>(f, s, l, h);
+                W* dl = reinterpret_cast<W*>(dst + at.lo[i]);
+                W* dhi = reinterpret_cast<W*>(dst + at.lo[i] + at.hop(i));
+                if (RMSN_OK(span_in(dl, sizeof(W), x.out, extent_bytes(a, x, x.os, sizeof(T))) &&
+                                span_in(dhi, sizeof(W), x.out, extent_bytes(a, x, x.os, sizeof(T))),
+                            a.status)) {
+                    *dl = X::pack(l);
+                    *dhi = X::pack(h);
+                }
+            }
+        }
+        slot = after;
+    }
+    // the groups' shares, in the tables' space, added in ascending group order
+    allow_dependent_launch();
+    float* part = tabs;  // [groups][D]
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+        const int u = lane + i * lanes;
+        if (UNITS == 0 && u >= a.units) continue;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            int p, q;
+            pair_members<ADJ>(a, u * E + e, p, q);
+            part[group * D + p] = e % 2 ? dwf[i][e / 2].y : dwf[i][e / 2].x;
+            part[group * D + q] = e % 2 ? dws[i][e / 2].y : dws[i][e / 2].x;
+        }
+    }
+    __syncthreads();
+    float* sums = a.partial + static_cast<int64_t>(blockIdx.x) * D;
+    for (int d = threadIdx.x; d < D; d += kRopeThreads) {
+        float s = 0.f;
+        for (int g = 0; g < groups; ++g) s += part[g * D + d];
+        if (RMSN_OK(span_in(sums + d, 4, a.partial,
+                            static_cast<int64_t>(gridDim.x) * D * 4), a.status))
+            sums[d] = s;
+    }
+}
+
+template <typename T, int E, int UNITS>
+RopeFn kernel_of(bool bwd, bool adjacent, bool norm) {
+    if (bwd) return adjacent ? &rope_bwd_kernel<T, E, true, UNITS> : &rope_bwd_kernel<T, E, false, UNITS>;
+    if (adjacent)
+        return norm ? &rope_fwd_kernel<T, E, true, true, UNITS> : &rope_fwd_kernel<T, E, true, false, UNITS>;
+    return norm ? &rope_fwd_kernel<T, E, false, true, UNITS> : &rope_fwd_kernel<T, E, false, false, UNITS>;
+}
+template <typename T>
+RopeFn kernel_for_type(int e, int units, bool bwd, bool adjacent, bool norm) {
+    // 16-byte pieces of heads of 64, 128 and 256: constant geometry
+    constexpr int E = 16 / sizeof(T), U = 32 / E;
+    if (e == E) {
+        if (units == U) return kernel_of<T, E, U>(bwd, adjacent, norm);
+        if (units == 2 * U) return kernel_of<T, E, 2 * U>(bwd, adjacent, norm);
+        if (units == 4 * U) return kernel_of<T, E, 4 * U>(bwd, adjacent, norm);
+        return kernel_of<T, E, 0>(bwd, adjacent, norm);
+    }
+    if constexpr (E != 4)
+        if (e == 4) return kernel_of<T, 4, 0>(bwd, adjacent, norm);
+    return kernel_of<T, 1, 0>(bwd, adjacent, norm);
+}
+}  // namespace
+}  // namespace rmsn
