@@ -60,12 +60,16 @@ int bwd_smem(const RopeArgs& a) {
     return a.head_dim * 4 * (1 + std::max(2 * a.tile, kRopeThreads / a.lanes));
 }
 
+// Tokens of a tile at most: two angle tables fit in 40 KB, so that no kernel
+// needs more shared memory than every launch may have.
+int max_tile(const RopeArgs& a) { return std::min(kRopeMaxTile, 40 * 1024 / (8 * a.head_dim)); }
+
 int bwd_tile(const RopeArgs& a) {
     const int groups = kRopeThreads / a.lanes;
     int heads = 1;
     for (const RopeTensor& t : a.t)
         if (t.heads > 0) heads = std::max(heads, t.heads);
-    return std::max(1, std::min(kRopeMaxTile, 8 * groups / heads));
+    return std::max(1, std::min(max_tile(a), 8 * groups / heads));
 }
 
 }  // namespace
@@ -80,7 +84,7 @@ cudaError_t rope_fwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, Rop
     // some eight passes of the block's groups over a tile's rows, but no fewer
     // tiles than SMs; few tokens share their heads out
     a.tile = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>({kRopeMaxTile, cdiv(8 * groups, heads), a.tokens / (2 * dev.sm_count)})));
+        1, std::min<int64_t>({max_tile(a), cdiv(8 * groups, heads), a.tokens / (2 * dev.sm_count)})));
     a.splits = 1;
     if (a.tile == 1)
         a.splits = static_cast<int>(std::max<int64_t>(
@@ -88,8 +92,8 @@ cudaError_t rope_fwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, Rop
     const int64_t per_sm = e >= 4 ? 4 : 3;  // what the kernels' launch bounds leave room for
     const int blocks = static_cast<int>(std::min<int64_t>(cdiv(a.tokens, a.tile), per_sm * dev.sm_count));
     const int smem = a.head_dim * 4 * (2 * a.tile + (norm ? 2 : 0));
-    return launch_pdl(kernel_for(dtype, e, fixed_units(a, adjacent), false, adjacent, norm), blocks * a.splits, kRopeThreads,
-                      smem, 1, s, a);
+    return launch_pdl(kernel_for(dtype, e, fixed_units(a, adjacent), false, adjacent, norm),
+                      blocks * a.splits, kRopeThreads, smem, 1, s, a);
 }
 
 int rope_bwd_max_rows(const DeviceInfo& dev) { return kRopeBwdBlocks * dev.sm_count + 2; }
@@ -116,8 +120,8 @@ cudaError_t rope_bwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, Rop
     shape_of(&a, e);
     a.tile = bwd_tile(a);
     a.blocks0 = rows[0];
-    cudaError_t err = launch_pdl(kernel_for(dtype, e, fixed_units(a, adjacent), true, adjacent, true), rows[0] + rows[1],
-                                 kRopeThreads, bwd_smem(a), 1, s, a);
+    cudaError_t err = launch_pdl(kernel_for(dtype, e, fixed_units(a, adjacent), true, adjacent, true),
+                                 rows[0] + rows[1], kRopeThreads, bwd_smem(a), 1, s, a);
     if (err != cudaSuccess) return err;
     PairSum p{};
     for (int i = 0; i < 2; ++i) {
