@@ -367,6 +367,7 @@ int group_norm_run(bool bwd, GroupNormArgs& a, int64_t C, int64_t G, int dtype,
     st = current_device(&dev);
     if (st != RMSNORM_OK) return st;
     a.status = dev->status_word;
+    a.wait_limit_ns = g_wait_limit_ns.load();
     Workspace ws = given;
     st = ws.take(group_norm_workspace(*dev, dtype, vec, bwd, a), stream);
     if (st != RMSNORM_OK) return st;
@@ -402,6 +403,8 @@ GroupNormArgs group_norm_bwd_args(const void* x, const void* w, const void* b, c
 }
 
 }  // namespace
+
+int64_t take_drop_unit() { return g_drop_unit.exchange(-1); }
 
 int pdl_mode() {
     static const int mode = [] {

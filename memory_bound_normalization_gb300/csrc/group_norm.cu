@@ -66,19 +66,16 @@ int resident_clusters(const DeviceInfo& dev, SlabFn fn, int threads, int smem, i
 
 struct Plan {
     bool ok = false, resident = false;
-    int splits = 1, cluster = 1, chunks = 1, lanes = 1, threads = 32, smem = 0, nvec = 0;
-    int64_t samples = 1;  // stream: samples of a batch
+    int splits = 1, cluster = 1, lanes = 1, threads = 32, smem = 0, nvec = 0;
+    int parts = 1, together = 1, rounds = 1;  // stream
+    bool drop = false;
 };
 
-void geometry(Plan* p, int nvec, int threads) {
+void geometry(Plan* p, int nvec) {
     p->nvec = nvec;
-    p->lanes = std::max(1, threads / nvec);
+    p->lanes = std::max(1, kMaxThreads / nvec);
     p->threads = round_up(p->lanes * nvec, 32);
 }
-
-// Bytes of x (and dy) that a batch of the stream family may hold: what L2
-// keeps besides the output written meanwhile.
-constexpr int64_t kBatchBytes = 64ll << 20;
 
 Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& a) {
     Plan best;
@@ -95,7 +92,7 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
         if (wide / 16 > kMaxThreads) continue;
         Plan p;
         p.splits = splits;
-        geometry(&p, static_cast<int>(wide / 16), kMaxThreads);
+        geometry(&p, static_cast<int>(wide / 16));
         const int fixed = round_up(fixed_smem(p.lanes, a.C / splits, a.G / splits), 16);
         for (int cluster = 1; cluster <= 16; cluster *= 2) {
             const int64_t rows = cdiv(a.S, cluster);
@@ -118,36 +115,43 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
             best_cost = cost;
         }
     }
-    // stream: all SMs on two launches
+    // stream: rounds of slabs that half of L2 holds (the other half holds what
+    // is written meanwhile), rows split no finer than 128 bytes, the width of an
+    // L2 line: narrower pieces read at half the DRAM rate
+    const int64_t budget = std::max<int64_t>(1 << 20, static_cast<int64_t>(dev.l2_bytes) * 9 / 16);
+    const int64_t slab_rows = a.S * tensors;
     Plan p;
-    while (p.splits <= a.G && row_bytes / p.splits / 16 > kMaxThreads) p.splits *= 2;
-    if (p.splits > a.G || a.G % p.splits || row_bytes % (16ll * p.splits)) return best;
-    geometry(&p, static_cast<int>(row_bytes / p.splits / 16), 256);
-    p.smem = fixed_smem(p.lanes, a.C / p.splits, a.G / p.splits) + ring_smem(p.lanes, p.nvec, bwd);
+    auto wide = [&] { return row_bytes / p.splits; };
+    auto splittable = [&] {
+        return a.G % (2 * p.splits) == 0 && row_bytes % (2 * p.splits) == 0 && wide() / 2 % 16 == 0;
+    };
+    while ((wide() > 16 * kStreamThreads || (wide() >= 256 && wide() * slab_rows > budget)) && splittable())
+        p.splits *= 2;
+    if (wide() > 16 * kStreamThreads) return best;
+    const int64_t slabs = a.B * p.splits;
+    if (slabs > INT32_MAX / 1024) return best;
+    p.nvec = static_cast<int>(wide() / 16);
+    p.lanes = kStreamThreads / p.nvec;
+    p.threads = kStreamThreads;
+    const int scratch = stream_scratch(p.lanes, a.C / p.splits);
+    p.smem = stream_ring(bwd) + scratch + a.G / p.splits * 8;
     if (p.smem > kMaxSmem) return best;
-    const double total = static_cast<double>(a.B) * a.S * row_bytes * tensors;
-    const double cost = 6.0 + total * (bwd ? 2.0 : 2.5) / (44e3 * dev.sm_count);
+    const double total = static_cast<double>(a.B) * slab_rows * row_bytes;
+    const SlabFn fn = kernel_for(dtype, bwd, a.act, SlabKind::kStream);
+    const int64_t most = resident_clusters(dev, fn, p.threads, p.smem, 1);
+    if (most < 1) return best;
+    p.together = static_cast<int>(std::min<int64_t>(
+        {slabs, most, std::max<int64_t>(1, budget / (wide() * slab_rows))}));
+    p.rounds = static_cast<int>(cdiv(slabs, p.together));
+    p.together = static_cast<int>(cdiv(slabs, p.rounds));
+    // at least two groups of positions a thread, where the slab has them
+    p.parts = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>(most / p.together, a.S / (2 * kGroup * p.lanes))));
+    if ((a.S / p.parts + 1) * row_bytes > UINT32_MAX || a.B * p.parts > INT32_MAX) return best;
+    const double cost = 12.0 + 3.0 * p.rounds + total * (bwd ? 1.5 : 2.0) / (44e3 * dev.sm_count);
     if (best.ok && best_cost <= cost) return best;
-    if (resident_clusters(dev, kernel_for(dtype, bwd, a.act, SlabKind::kApply), p.threads, p.smem, 1) < 1)
-        return best;  // also raises the kernel's shared-memory limit
-    // the largest cluster that leaves no more than a few SMs without a block
-    int clusters = 0;
-    const SlabFn sums = kernel_for(dtype, bwd, a.act, SlabKind::kSums);
-    const int most = resident_clusters(dev, sums, p.threads, p.smem, 1);
-    for (p.cluster = 8; p.cluster > 1; p.cluster /= 2) {
-        clusters = resident_clusters(dev, sums, p.threads, p.smem, p.cluster);
-        if (clusters * p.cluster >= most * 0.95) break;
-    }
-    if (p.cluster == 1) clusters = most;
-    if (clusters < 1) return best;
-    p.samples = std::max<int64_t>(
-        1, std::min<int64_t>(a.B, kBatchBytes / (a.S * row_bytes * tensors)));
-    const int64_t slabs = p.samples * p.splits;
-    p.chunks = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(clusters / slabs, a.S / (p.cluster * p.lanes))));
-    if (slabs * p.chunks * p.cluster > INT32_MAX || a.B * p.chunks > INT32_MAX) return best;
     p.ok = true;
-    p.resident = false;
+    p.drop = total * (bwd ? 1.5 : 2.0) > dev.l2_bytes / 2;
     return p;
 }
 
@@ -191,25 +195,34 @@ SlabArgs args_of(const Plan& p, bool bwd, const GroupNormArgs& a) {
     g.gw = a.G / p.splits;
     g.D = a.C / a.G;
     g.cluster = p.cluster;
-    g.chunks = p.chunks;
-    const int parts = p.chunks * p.cluster;
+    g.parts = p.parts;
+    g.together = p.together;
+    g.rounds = p.rounds;
+    g.drop = p.drop;
+    g.scratch = stream_scratch(p.lanes, g.cw);
+    const int parts = p.resident ? p.cluster : p.parts;
     g.part_rows = static_cast<int>(a.S / parts);
     g.part_more = static_cast<int>(a.S % parts);
-    // a power of two of warps a group (forward), or of threads a channel
-    const int room = bwd ? p.threads / (2 * g.cw) : p.threads / 32 / g.gw;
+    // a power of two of warps a group (resident forward), or of threads a channel
+    const int room = bwd || !p.resident ? p.threads / (2 * g.cw) : p.threads / 32 / g.gw;
     g.join = 1;
     while (g.join < 16 && 2 * g.join <= room) g.join *= 2;
+    g.drop_unit = -1;
     return g;
 }
 
+// Workspace of the stream family: arrivals, then results, then partial rows.
+size_t rounded(size_t n) { return (n + 255) / 256 * 256; }
+size_t arrived_bytes(const Plan& p, const GroupNormArgs& a) {
+    return p.resident ? 0 : rounded(static_cast<size_t>(a.B) * p.splits * 4);
+}
 size_t stats_bytes(const Plan& p, const GroupNormArgs& a) {
-    return p.resident ? 0
-                      : (static_cast<size_t>(p.samples) * p.chunks * a.G * 8 + 255) / 256 * 256;
+    return p.resident ? 0 : rounded(static_cast<size_t>(a.B) * a.G * p.parts * 8);
 }
 // Rows of dw partial sums, 0 where the kernel writes dw and db itself.
 int64_t partial_rows(const Plan& p, bool bwd, const GroupNormArgs& a) {
-    const int64_t rows = a.B * p.chunks;
-    return bwd && a.dw != nullptr && rows > 1 ? rows : 0;
+    const int64_t rows = a.B * (p.resident ? 1 : p.parts);
+    return bwd && a.dw != nullptr && (rows > 1 || !p.resident) ? rows : 0;
 }
 
 }  // namespace
@@ -218,7 +231,8 @@ size_t group_norm_workspace(const DeviceInfo& dev, int dtype, bool vec, bool bwd
                             const GroupNormArgs& a) {
     const Plan p = plan_of(dev, dtype, vec, bwd, a);
     if (!p.ok) return gn_scalar_workspace(bwd, a);
-    return stats_bytes(p, a) + static_cast<size_t>(partial_rows(p, bwd, a)) * 2 * a.C * 4;
+    return arrived_bytes(p, a) + stats_bytes(p, a) +
+           static_cast<size_t>(partial_rows(p, bwd, a)) * 2 * a.C * 4;
 }
 
 cudaError_t group_norm_launch(const DeviceInfo& dev, int dtype, bool vec, bool bwd,
@@ -227,23 +241,31 @@ cudaError_t group_norm_launch(const DeviceInfo& dev, int dtype, bool vec, bool b
     if (!p.ok) return gn_scalar_launch(dtype, bwd, a, workspace, s);
     SlabArgs g = args_of(p, bwd, a);
     const int64_t rows = partial_rows(p, bwd, a);
-    g.stats = static_cast<float2*>(workspace);
-    if (rows > 0) g.rows = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(p, a));
-    cudaError_t err = cudaSuccess;
+    char* ws = static_cast<char*>(workspace);
+    const size_t arrived = arrived_bytes(p, a);
+    g.arrived = reinterpret_cast<unsigned*>(ws);
+    g.stats = reinterpret_cast<float2*>(ws + arrived);
+    if (rows > 0) g.rows = reinterpret_cast<float*>(ws + arrived + stats_bytes(p, a));
+    cudaError_t err;
     if (p.resident) {
         err = launch_pdl(kernel_for(dtype, bwd, a.act, SlabKind::kResident),
                          static_cast<int>(a.B * p.splits * p.cluster), p.threads, p.smem, p.cluster, s, g);
     } else {
-        for (int64_t b = 0; b < a.B && err == cudaSuccess; b += p.samples) {
-            g.sample0 = b;
-            const int64_t n = std::min<int64_t>(p.samples, a.B - b);
-            const int grid = static_cast<int>(n * p.splits * p.chunks * p.cluster);
-            err = launch_pdl(kernel_for(dtype, bwd, a.act, SlabKind::kSums), grid, p.threads, p.smem, p.cluster, s, g);
-            if (err == cudaSuccess)
-                err = launch_pdl(kernel_for(dtype, bwd, a.act, SlabKind::kApply), grid, p.threads,
-                                 static_cast<size_t>((g.gw + 1) / 2 * 16 + ring_smem(p.lanes, p.nvec, bwd)),
-                                 1, s, g);
-        }
+        g.drop_unit = take_drop_unit();
+        err = cudaMemsetAsync(ws, 0, arrived, s);
+        if (err != cudaSuccess) return err;
+        // the blocks wait for one another: all of them run at once, or none
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(p.together * p.parts));
+        cfg.blockDim = dim3(kStreamThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(p.smem);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeCooperative;
+        attr[0].val.cooperative = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        err = cudaLaunchKernelEx(&cfg, kernel_for(dtype, bwd, a.act, SlabKind::kStream), g);
     }
     if (err != cudaSuccess || rows == 0) return err;
     PairSum sum{};

@@ -20,13 +20,20 @@ struct SlabArgs {
     int splits;    // slabs of a sample (runs of channels)
     int cw, gw;    // channels and groups of a slab
     int D;         // channels of a group
-    int cluster;   // blocks that join their sums
-    int chunks;    // clusters of a slab
+    int cluster;   // resident: blocks of a slab, which join their sums
     int part_rows, part_more;  // positions of a block, and how many blocks take one more
-    int join;      // warps (forward) that share a group's sums in a block
-    int64_t sample0;
-    float2* stats; // stream: [slab][chunk][gw], (mean, M2) or (sum w P, sum w Q)
-    float* rows;   // backward: partial rows [sample * chunks + chunk][2 C] (Q, then P)
+    int join;      // warps that share a group's sums in a block, or threads a channel's
+    // stream
+    int parts;     // blocks of a slab
+    int together;  // slabs of a round
+    int rounds;
+    int scratch;   // bytes of the sums and channel constants
+    int drop;      // L2 is told what is used for the last time
+    unsigned* arrived;  // [slab]: blocks that have published their results
+    float2* stats;      // [slab][group][part]: (mean, M2), or (sum w P, sum w Q)
+    int64_t drop_unit;  // failure injection: the slab block 0 does not count itself in
+    // backward: partial rows [2 C] (Q, then P): a sample's, or a sample's part's
+    float* rows;
 };
 
 // Shared memory besides the resident slab: the threads' sums [2][lanes][cw],
@@ -40,14 +47,14 @@ inline int fixed_smem(int lanes, int cw, int gw) {
 
 // Positions a thread's copies run ahead, and positions of a group of copies.
 constexpr int kDepth = 6, kGroup = 2;
-inline int ring_smem(int lanes, int nvec, bool bwd) {
-    return kDepth * lanes * nvec * 16 * (bwd ? 2 : 1);
-}
+constexpr int kStreamThreads = 256;
+// The stream kernel's shared memory: the ring of copies; the sums of its
+// threads and the constants of its channels, in one place.
+inline int stream_ring(bool bwd) { return kDepth * kStreamThreads * 16 * (bwd ? 2 : 1); }
+inline int stream_scratch(int lanes, int cw) { return (2 * lanes > 4 ? 2 * lanes : 4) * cw * 4; }
 
 using SlabFn = void (*)(const SlabArgs);
-// Both passes of a slab that stays in shared memory; a slab's sums; its second
-// pass.
-enum class SlabKind { kResident, kSums, kApply };
+enum class SlabKind { kResident, kStream };
 SlabFn gn_kernel_f32(bool bwd, int act, SlabKind k);
 SlabFn gn_kernel_bf16(bool bwd, int act, SlabKind k);
 SlabFn gn_kernel_f16(bool bwd, int act, SlabKind k);

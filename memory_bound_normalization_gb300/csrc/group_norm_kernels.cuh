@@ -22,10 +22,9 @@
 //             blocks: one kernel, each thread keeps what it read in its own
 //             shared-memory slots, the blocks' sums meet in distributed shared
 //             memory. One read of x.
-//   stream    larger slabs: a kernel for the sums (clusters join their blocks'
-//             sums, so few partial results are written) and one that applies
-//             them, in the opposite order so that it starts with what L2 still
-//             holds; samples go in batches that L2 holds.
+//   stream    larger slabs: persistent blocks of one cooperative launch sum a
+//             slab and apply it in the opposite order, so that the second pass
+//             starts with what L2 still holds.
 #pragma once
 
 #include "group_norm.cuh"
@@ -46,20 +45,16 @@ __device__ __forceinline__ float part_count(const SlabArgs& g, int part, int n) 
 // Where a block works.
 struct Place {
     int64_t sample, r0;  // its first position
-    int split, chunk, rank, slab, rows;
+    int split, rank, rows;
 };
 __device__ __forceinline__ Place place_of(const SlabArgs& g) {
     Place p;
-    const int cl = static_cast<int>(blockIdx.x) / g.cluster;
-    p.rank = static_cast<int>(blockIdx.x) - cl * g.cluster;
-    p.slab = cl / g.chunks;
-    p.chunk = cl - p.slab * g.chunks;
-    const int s = p.slab / g.splits;
-    p.split = p.slab - s * g.splits;
-    p.sample = g.sample0 + s;
-    const int part = p.chunk * g.cluster + p.rank;
-    p.r0 = part_begin(g, part);
-    p.rows = g.part_rows + (part < g.part_more ? 1 : 0);
+    const int slab = static_cast<int>(blockIdx.x) / g.cluster;
+    p.rank = static_cast<int>(blockIdx.x) - slab * g.cluster;
+    p.sample = slab / g.splits;
+    p.split = slab - static_cast<int>(p.sample) * g.splits;
+    p.r0 = part_begin(g, p.rank);
+    p.rows = g.part_rows + (p.rank < g.part_more ? 1 : 0);
     return p;
 }
 
@@ -104,6 +99,28 @@ __device__ __forceinline__ void load_channels(const SlabArgs& g, const void* p, 
 #pragma unroll
         for (int e = 0; e < PAIRS; ++e) f[e] = make_float2(to_f32(w[2 * e]), to_f32(w[2 * e + 1]));
     }
+}
+
+template <typename T>
+__device__ __forceinline__ float channel(const SlabArgs& g, const void* p, int c, float none) {
+    if (p == nullptr) return none;
+    return g.a.w_f32 ? static_cast<const float*>(p)[c] : to_f32(static_cast<const T*>(p)[c]);
+}
+// A thread's channels of a row of floats in shared memory (16-byte aligned).
+template <typename T>
+__device__ __forceinline__ void read_channels(const float* row, float2 (&f)[Pack<T>::PAIRS]) {
+#pragma unroll
+    for (int e = 0; e < Pack<T>::PAIRS; e += 2) {
+        const float4 v = *reinterpret_cast<const float4*>(row + 2 * e);
+        f[e] = make_float2(v.x, v.y);
+        f[e + 1] = make_float2(v.z, v.w);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void write_channels(float* row, const float2 (&f)[Pack<T>::PAIRS]) {
+#pragma unroll
+    for (int e = 0; e < Pack<T>::PAIRS; e += 2)
+        *reinterpret_cast<float4*>(row + 2 * e) = make_float4(f[e].x, f[e].y, f[e + 1].x, f[e + 1].y);
 }
 
 // Constants of a thread's channels from per-group values in shared or global
@@ -480,11 +497,10 @@ __device__ __forceinline__ Joined join_means(int n, float total, Get get, Count 
     return {mean, m2};
 }
 
-// A thread's way through its positions: copies run kDepth positions ahead, in
-// groups of kGroup, into the thread's own slots. RING slots are reused (a group
-// is refilled as soon as it is read); without it every position has a slot and
-// stays there for the second pass.
-template <typename T, bool BWD, bool RING>
+// Resident: a thread's way through its positions. Copies run kDepth positions
+// ahead, in groups of kGroup, into the thread's own slots, a slot for every
+// position, which stays there for the second pass.
+template <typename T, bool BWD>
 struct Feed {
     const T* x;      // the next position to copy
     const T* dy;
@@ -517,7 +533,6 @@ struct Feed {
             ahead += group;
         }
         uint32_t at = slots;
-        [[maybe_unused]] const uint32_t end = ahead;
 #pragma unroll 1
         for (int i = 0; i < n; i += kGroup) {
             copies_wait<kDepth / kGroup - 1>();
@@ -532,18 +547,18 @@ struct Feed {
 #pragma unroll
             for (int u = 0; u < kGroup; ++u)
                 if (i + u < n) visit(i + u, xv[u], dv[u]);
-            issue(RING ? at : ahead, n - i - kDepth, status);
+            issue(ahead, n - i - kDepth, status);
             at += group;
-            if constexpr (RING) at = at == end ? slots : at;
-            else ahead += group;
+            ahead += group;
         }
         copies_wait<0>();
     }
 };
 
-// The sums of a slab (stream), or both passes over it (resident).
-template <typename T, bool BWD, int ACT, bool RESIDENT>
-__global__ void __maxnreg__(RESIDENT ? 128 : BWD ? 80 : 64) gn_slab_kernel(const __grid_constant__ SlabArgs g) {
+// ----------------------------------------------------------------- resident
+// Both passes over a slab that its cluster keeps.
+template <typename T, bool BWD, int ACT>
+__global__ void __launch_bounds__(kMaxThreads) gn_resident_kernel(const __grid_constant__ SlabArgs g) {
     constexpr int VEC = Pack<T>::VEC;
     const Place at = place_of(g);
     const int lane = static_cast<int>(threadIdx.x) / g.nvec;
@@ -561,14 +576,14 @@ __global__ void __maxnreg__(RESIDENT ? 128 : BWD ? 80 : 64) gn_slab_kernel(const
     const int c = vec * VEC;
     const int64_t base = (at.sample * g.a.S + at.r0 + lane) * g.a.C + c0 + c;
     const int n = active && rows > lane ? (rows - lane - 1) / g.lanes + 1 : 0;
-    Feed<T, BWD, !RESIDENT> feed;
+    Feed<T, BWD> feed;
     feed.x = static_cast<const T*>(g.a.x) + base;
     feed.dy = BWD ? static_cast<const T*>(g.a.dy) + base : nullptr;
     feed.step = static_cast<int64_t>(g.lanes) * g.a.C;
     feed.slots = smem_u32(keep + threadIdx.x);
     feed.pitch = static_cast<uint32_t>(slots) * 16u;
     feed.n = n;
-    [[maybe_unused]] const uint32_t group_slots = feed.pitch * Feed<T, BWD, !RESIDENT>::TENSORS;
+    [[maybe_unused]] const uint32_t group_slots = feed.pitch * Feed<T, BWD>::TENSORS;
     [[maybe_unused]] const float* rstd_of =
         BWD ? g.a.rstd + at.sample * g.a.G + at.split * g.gw : nullptr;
     Columns<T, BWD, ACT> col;
@@ -593,9 +608,7 @@ __global__ void __maxnreg__(RESIDENT ? 128 : BWD ? 80 : 64) gn_slab_kernel(const
     __syncwarp();
     if (g.cluster > 1) cluster_sync_all();
     else __syncthreads();
-    const int part0 = at.chunk * g.cluster;
     for (int k = threadIdx.x; k < g.gw; k += blockDim.x) {
-        if (!RESIDENT && at.rank != 0) break;
         float2 v = make_float2(0.f, 0.f);
         if constexpr (BWD) {
             for (int r = 0; r < g.cluster; ++r) {
@@ -605,26 +618,22 @@ __global__ void __maxnreg__(RESIDENT ? 128 : BWD ? 80 : 64) gn_slab_kernel(const
         } else {
             const float d = static_cast<float>(g.D);
             const Joined j = join_means(
-                g.cluster, part_count(g, part0, g.cluster) * d,
+                g.cluster, part_count(g, 0, g.cluster) * d,
                 [&](int r) { return g.cluster > 1 ? ld_cluster_f32x2(mine + k, r) : mine[k]; },
-                [&](int r) { return part_count(g, part0 + r, 1) * d; });
+                [&](int r) { return part_count(g, r, 1) * d; });
             v = make_float2(j.mean, j.m2);
         }
-        if constexpr (RESIDENT) {
-            const float inv = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
-            if constexpr (BWD) {
-                slab[k] = make_float2(v.x * inv, v.y * inv);
-            } else {
-                v.y = rsqrtf(v.y * inv + g.a.eps);
-                slab[k] = v;
-                if (at.rank == 0) {
-                    const int64_t o = at.sample * g.a.G + at.split * g.gw + k;
-                    g.a.mean[o] = v.x;
-                    g.a.rstd[o] = v.y;
-                }
-            }
+        const float inv = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
+        if constexpr (BWD) {
+            slab[k] = make_float2(v.x * inv, v.y * inv);
         } else {
-            g.stats[(static_cast<int64_t>(at.slab) * g.chunks + at.chunk) * g.gw + k] = v;
+            v.y = rsqrtf(v.y * inv + g.a.eps);
+            slab[k] = v;
+            if (at.rank == 0) {
+                const int64_t o = at.sample * g.a.G + at.split * g.gw + k;
+                g.a.mean[o] = v.x;
+                g.a.rstd[o] = v.y;
+            }
         }
     }
     if constexpr (BWD) {
@@ -641,7 +650,7 @@ __global__ void __maxnreg__(RESIDENT ? 128 : BWD ? 80 : 64) gn_slab_kernel(const
                 float* d;
                 if (g.rows == nullptr) d = (q ? g.a.dw : g.a.db) + c0 + c;
                 else
-                    d = g.rows + (at.sample * g.chunks + at.chunk) * 2 * g.a.C + (q ? 0 : g.a.C) + c0 + c;
+                    d = g.rows + (at.sample) * 2 * g.a.C + (q ? 0 : g.a.C) + c0 + c;
                 *d = s;
             }
         }
@@ -650,119 +659,446 @@ __global__ void __maxnreg__(RESIDENT ? 128 : BWD ? 80 : 64) gn_slab_kernel(const
     if (g.cluster > 1) cluster_arrive_relaxed();  // this block is done reading its peers
     allow_dependent_launch();
 
-    if constexpr (RESIDENT) {
-        __syncthreads();
-        if (n > 0) {
-            if constexpr (BWD) col.finish(g, rstd_of, slab, c, inv_d);
-            else col.finish(g, slab, c0, c, inv_d);
-            T* out = static_cast<T*>(g.a.out) + base;
-            [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(sizeof(T));
-            uint32_t slot = feed.slots;
+    __syncthreads();
+    if (n > 0) {
+        if constexpr (BWD) col.finish(g, rstd_of, slab, c, inv_d);
+        else col.finish(g, slab, c0, c, inv_d);
+        T* out = static_cast<T*>(g.a.out) + base;
+        [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(sizeof(T));
+        uint32_t slot = feed.slots;
 #pragma unroll 2
-            for (int i = 0; i < n; ++i) {
-                uint4 v;
-                if constexpr (BWD) v = col.apply(ld_slot(slot), ld_slot(slot + feed.pitch));
-                else v = col.apply(ld_slot(slot));
-                slot += group_slots;
-                if (RMSN_OK(span_in(out, 16, g.a.out, bytes), g.a.status)) st_global_16(out, v);
-                out += feed.step;
-            }
+        for (int i = 0; i < n; ++i) {
+            uint4 v;
+            if constexpr (BWD) v = col.apply(ld_slot(slot), ld_slot(slot + feed.pitch));
+            else v = col.apply(ld_slot(slot));
+            slot += group_slots;
+            if (RMSN_OK(span_in(out, 16, g.a.out, bytes), g.a.status)) st_global_16(out, v);
+            out += feed.step;
         }
     }
     __syncwarp();
     if (g.cluster > 1) cluster_wait();  // no block leaves while a peer reads it
 }
 
-// Stream: the second pass, over the same ranges of positions from their ends.
+// ------------------------------------------------------------------- stream
+// One cooperative launch for slabs that no cluster holds: persistent blocks
+// take the slabs in rounds of as many as L2 keeps (g.together, g.parts blocks a
+// slab). In a round a block sums its positions, publishes its groups' results
+// and counts itself in; while the others arrive, its copies of the second pass,
+// which goes from its last position back to the first, are under way. Copies
+// run kDepth positions ahead across passes and rounds, so that DRAM stays busy
+// while sums are joined. The wait for the others is bounded in time.
+template <typename T, bool BWD>
+struct Copies {
+    static constexpr int TENSORS = BWD ? 2 : 1;
+    static constexpr uint32_t PITCH = kStreamThreads * 16, GROUP = kGroup * TENSORS * PITCH;
+    static constexpr int GROUPS = kDepth / kGroup;
+    // a pass: where its copies come from and how many positions it has
+    struct Pass {
+        const char* x;
+        const char* dy;
+        uint32_t off, step;  // bytes of this thread's next position, and to the one after
+        int n;
+        bool last_use;       // read for the last time: L2 need not keep it
+    };
+    uint32_t first, slot;  // shared-memory addresses of this thread's ring and its next group
+    uint64_t drop;         // L2 policies
+    int* status;
+
+    __device__ __forceinline__ void copy(uint32_t to, const char* from, bool last_use) const {
+        if (!RMSN_OK(slot_in(to), status)) return;
+        if (last_use)
+            asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(drop) : "memory");
+        else
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    }
+    // copies a group of a pass of which `left` positions remain
+    __device__ __forceinline__ void issue(Pass& p, int left) const {
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            if (u < left) {
+                copy(slot + u * TENSORS * PITCH, p.x + p.off, p.last_use);
+                if constexpr (BWD) copy(slot + (u * TENSORS + 1) * PITCH, p.dy + p.off, p.last_use);
+            }
+            p.off += p.step;
+        }
+        copies_commit();
+    }
+    __device__ __forceinline__ void advance() { slot = slot + GROUP == first + GROUPS * GROUP ? first : slot + GROUP; }
+    // A pass whose first GROUPS groups are under way: visits its positions in
+    // order, and starts the next pass's copies as its own run out. `p` is the
+    // pass's next position to copy.
+    template <typename Visit>
+    __device__ __forceinline__ void run(Pass& p, Pass& next, Visit visit) {
+        const int full = p.n / kGroup - GROUPS;  // groups whose successor GROUPS on is whole
+        int i = 0;
+#pragma unroll 1
+        for (; i < full; ++i) {
+            copies_wait<GROUPS - 1>();
+            uint4 xv[kGroup], dv[kGroup];
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) {
+                xv[u] = ld_slot(slot + u * TENSORS * PITCH);
+                if constexpr (BWD) dv[u] = ld_slot(slot + (u * TENSORS + 1) * PITCH);
+            }
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) visit(xv[u], dv[u]);
+            issue(p, kGroup);
+            advance();
+        }
+        const int groups = max((p.n + kGroup - 1) / kGroup, GROUPS);
+        int ahead = 0;  // positions of the next pass under way
+#pragma unroll 1
+        for (; i < groups; ++i) {
+            copies_wait<GROUPS - 1>();
+            uint4 xv[kGroup], dv[kGroup];
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u)
+                if (i * kGroup + u < p.n) {
+                    xv[u] = ld_slot(slot + u * TENSORS * PITCH);
+                    if constexpr (BWD) dv[u] = ld_slot(slot + (u * TENSORS + 1) * PITCH);
+                }
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u)
+                if (i * kGroup + u < p.n) visit(xv[u], dv[u]);
+            if (i + GROUPS < groups) {
+                issue(p, p.n - (i + GROUPS) * kGroup);
+            } else {
+                issue(next, next.n - ahead);
+                ahead += kGroup;
+            }
+            advance();
+        }
+    }
+};
+
+// Sums of a block's channels over its lanes, C sums of each of two kinds in
+// rows of `sums` ([2][lanes][cw]), into the first lane's rows; g.join threads
+// share a channel's lanes, and part 0 adds the parts.
+__device__ __forceinline__ void sum_lanes(const SlabArgs& g, float* sums) {
+    const int share = min(g.lanes, g.join), columns = 2 * g.cw;
+    for (int i = threadIdx.x; i < columns * share; i += blockDim.x) {
+        const int j = i / columns, c = i - j * columns;
+        float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw) + j * g.cw;
+        float s = 0.f;
+#pragma unroll 8
+        for (int r = j; r < g.lanes; r += share) s += at[(r - j) * g.cw];
+        at[0] = s;
+    }
+    __syncthreads();
+    if (share > 1) {
+        for (int c = threadIdx.x; c < columns; c += blockDim.x) {
+            float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw);
+            float s = 0.f;
+            for (int j = 0; j < share; ++j) s += at[j * g.cw];
+            at[0] = s;
+        }
+        __syncthreads();
+    }
+}
+
 template <typename T, bool BWD, int ACT>
-__global__ void __maxnreg__(BWD ? 80 : 64) gn_apply_kernel(const __grid_constant__ SlabArgs g) {
-    constexpr int VEC = Pack<T>::VEC;
-    const Place at = place_of(g);
+__global__ void __maxnreg__(BWD ? 80 : 64) gn_stream_kernel(const __grid_constant__ SlabArgs g) {
+    constexpr int VEC = Pack<T>::VEC, PAIRS = Pack<T>::PAIRS, SIZE = sizeof(T);
+    using Ring = Copies<T, BWD>;
     const int lane = static_cast<int>(threadIdx.x) / g.nvec;
     const int vec = static_cast<int>(threadIdx.x) - lane * g.nvec;
     const bool active = lane < g.lanes;
     const float inv_d = 1.f / static_cast<float>(g.D);
-    float2* slab = reinterpret_cast<float2*>(rmsn_dynamic_smem);
-    uint4* keep = reinterpret_cast<uint4*>(slab + (g.gw + 1) / 2 * 2);
-    const int rows = at.rows;
-    const int64_t c0 = static_cast<int64_t>(at.split) * g.cw;
-    const int64_t step = static_cast<int64_t>(g.lanes) * g.a.C;
+    const float inv_count = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
+    const int team = static_cast<int>(blockIdx.x) / g.parts;
+    const int part = static_cast<int>(blockIdx.x) - team * g.parts;
+    const int64_t r0 = part_begin(g, part);
+    const int rows = g.part_rows + (part < g.part_more ? 1 : 0);
     const int n = active && rows > lane ? (rows - lane - 1) / g.lanes + 1 : 0;
-    wait_for_prerequisite_grid();  // the partial results are complete
-    {
-        const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
-        const float inv = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
-        const float2* stats = g.stats + static_cast<int64_t>(at.slab) * g.chunks * g.gw;
-        for (int k = warp; k < g.gw; k += warps) {
-            float2 v = make_float2(0.f, 0.f);
-            if constexpr (BWD) {
-                for (int i = l; i < g.chunks; i += 32)
-                    v = __fadd2_rn(v, stats[static_cast<int64_t>(i) * g.gw + k]);
-                v.x = group_allreduce<32>(v.x) * inv;
-                v.y = group_allreduce<32>(v.y) * inv;
-            } else {
-                auto count = [&](int i) {
-                    return part_count(g, i * g.cluster, g.cluster) * static_cast<float>(g.D);
-                };
-                float s = 0.f;
-                for (int i = l; i < g.chunks; i += 32)
-                    s = fmaf(count(i), stats[static_cast<int64_t>(i) * g.gw + k].x, s);
-                const float mean = group_allreduce<32>(s) * inv;
-                float m2 = 0.f;
-                for (int i = l; i < g.chunks; i += 32) {
-                    const float2 t = stats[static_cast<int64_t>(i) * g.gw + k];
-                    const float d = t.x - mean;
-                    m2 += fmaf(count(i) * d, d, t.y);
+    const int c = vec * VEC;
+    // shared memory: the ring; then, in one place, the threads' sums and the
+    // channels' constants, which are never needed at once; the groups' results
+    unsigned char* scratch = rmsn_dynamic_smem + Ring::GROUPS * Ring::GROUP;
+    float* sums = reinterpret_cast<float*>(scratch);
+    float* table = sums;  // up to 4 constants a channel, [4][cw]
+    float2* slab = reinterpret_cast<float2*>(scratch + g.scratch);
+
+    Ring ring;
+    ring.first = ring.slot = smem_u32(rmsn_dynamic_smem) + threadIdx.x * 16;
+    ring.drop = l2_policy_evict_first();
+    ring.status = g.a.status;
+    const uint32_t pitch = static_cast<uint32_t>(g.a.C) * SIZE;  // bytes of a position
+    auto place = [&](int round, int64_t& sample, int& split) {
+        const int64_t i = static_cast<int64_t>(round) * g.together + team;
+        sample = i / g.splits;
+        split = static_cast<int>(i - sample * g.splits);
+        return sample < g.a.B;
+    };
+    auto pass_of = [&](int round, bool second) {
+        typename Ring::Pass p{};
+        int64_t sample;
+        int split;
+        if (round >= g.rounds || !place(round, sample, split)) return p;
+        const int64_t at = ((sample * g.a.S + r0) * g.a.C + static_cast<int64_t>(split) * g.cw) * SIZE;
+        p.x = static_cast<const char*>(g.a.x) + at;
+        if constexpr (BWD) p.dy = static_cast<const char*>(g.a.dy) + at;
+        p.n = n;
+        p.step = pitch * g.lanes;
+        p.off = pitch * lane + c * SIZE;
+        if (second) {
+            p.off += p.step * static_cast<uint32_t>(n > 0 ? n - 1 : 0);
+            p.step = 0u - p.step;
+        }
+        p.last_use = second && g.drop;
+        return p;
+    };
+    bool failed = false;  // thread 0's: a wait ran out
+    typename Ring::Pass pass = pass_of(0, false);
+#pragma unroll
+    for (int i = 0; i < Ring::GROUPS; ++i) {
+        ring.issue(pass, pass.n - i * kGroup);
+        ring.advance();
+    }
+
+    for (int round = 0; round < g.rounds; ++round) {
+        int64_t sample;
+        int split;
+        const bool live = place(round, sample, split);
+        const int c0 = split * g.cw;
+        const int64_t slab_i = static_cast<int64_t>(round) * g.together + team;
+        Columns<T, BWD, ACT> col;
+        typename Ring::Pass again = pass_of(round, true);
+        const int mine_n = live ? n : 0;
+        pass.n = mine_n;
+        const int64_t group0 = sample * g.a.G + split * g.gw;
+        if constexpr (BWD) {
+            // -mean, rstd w and b of each channel
+            if (live)
+                for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
+                    const int k = quotient(i, inv_d);
+                    const float r = g.a.rstd[group0 + k];
+                    table[i] = -g.a.mean[group0 + k];
+                    table[g.cw + i] = r * channel<T>(g, g.a.w, c0 + i, 1.f);
+                    table[2 * g.cw + i] = channel<T>(g, g.a.b, c0 + i, 0.f);
                 }
-                v = make_float2(mean, rsqrtf(group_allreduce<32>(m2) * inv + g.a.eps));
-                if (at.chunk == 0 && at.rank == 0 && l == 0) {
-                    const int64_t o = at.sample * g.a.G + at.split * g.gw + k;
-                    g.a.mean[o] = v.x;
-                    g.a.rstd[o] = v.y;
+            __syncthreads();
+            if (active) {
+                read_channels<T>(table + c, col.mean);
+                read_channels<T>(table + g.cw + c, col.k1);
+                read_channels<T>(table + 2 * g.cw + c, col.b);
+            }
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) col.p[e] = col.q[e] = make_float2(0.f, 0.f);
+            ring.run(pass, again, [&](const uint4& x, const uint4& dy) { col.add(x, dy); });
+            __syncthreads();  // every thread has its constants
+            if (active) {
+                write_channels<T>(sums + lane * g.cw + c, col.p);
+                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, col.q);
+            }
+            __syncthreads();
+            sum_lanes(g, sums);
+            // sum dz (x - mean) becomes sum dz xhat; groups' sums weighted by w
+            const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
+            float* ps = sums;
+            float* qs = sums + g.lanes * g.cw;
+            for (int k = warp; k < g.gw; k += warps) {
+                const float r = live ? g.a.rstd[group0 + k] : 0.f;
+                float sp = 0.f, sq = 0.f;
+                for (int i = l; i < g.D; i += 32) {
+                    const int ch = k * g.D + i;
+                    const float w = live ? channel<T>(g, g.a.w, c0 + ch, 1.f) : 0.f;
+                    const float q = qs[ch] * r;
+                    qs[ch] = q;
+                    sp = fmaf(w, ps[ch], sp);
+                    sq = fmaf(w, q, sq);
+                }
+                sp = group_allreduce<32>(sp);
+                sq = group_allreduce<32>(sq);
+                if (l == 0 && live)
+                    g.stats[(slab_i * g.gw + k) * g.parts + part] = make_float2(sp, sq);
+            }
+            __syncthreads();
+            if (g.rows != nullptr && live) {
+                float* row = g.rows + (sample * g.parts + part) * 2 * g.a.C + c0;
+                for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
+                    row[i] = qs[i];
+                    row[g.a.C + i] = ps[i];
                 }
             }
-            if (l == 0) slab[k] = v;
+        } else {
+            col.start(make_uint4(0, 0, 0, 0));
+            bool first = true;
+            ring.run(pass, again, [&](const uint4& x, const uint4&) {
+                if (first) {
+                    col.start(x);
+                    first = false;
+                }
+                col.add(x);
+            });
+            // channel means over the lanes, then squares about them, then groups
+            const float inv_n = mine_n > 0 ? 1.f / static_cast<float>(mine_n) : 0.f;
+            const float inv_rows = 1.f / static_cast<float>(max(rows, 1));
+            float2 own[PAIRS];  // sum of the thread's values
+            __syncthreads();  // the sums' place: every thread has its constants
+            if (active) {
+                float2 none[PAIRS];
+#pragma unroll
+                for (int e = 0; e < PAIRS; ++e) {
+                    own[e] = __ffma2_rn(col.pivot[e], f2_splat(static_cast<float>(mine_n)), col.s1[e]);
+                    none[e] = make_float2(0.f, 0.f);
+                }
+                write_channels<T>(sums + lane * g.cw + c, own);
+                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, none);
+            }
+            __syncthreads();
+            sum_lanes(g, sums);
+            float2 mean[PAIRS], m2[PAIRS];
+            if (active) {
+                read_channels<T>(sums + c, mean);
+#pragma unroll
+                for (int e = 0; e < PAIRS; ++e) {
+                    mean[e] = __fmul2_rn(mean[e], f2_splat(inv_rows));
+                    // squares of the thread's values about the channel's mean
+                    const float2 d = __fmul2_rn(col.s1[e], f2_splat(inv_n));
+                    const float2 off = sub2(__fadd2_rn(col.pivot[e], d), mean[e]);
+                    m2[e] = sub2(col.s2[e], __fmul2_rn(col.s1[e], d));
+                    m2[e] = __ffma2_rn(__fmul2_rn(off, off), f2_splat(static_cast<float>(mine_n)), m2[e]);
+                    if (mine_n == 0) m2[e] = make_float2(0.f, 0.f);
+                }
+            }
+            __syncthreads();
+            if (active) {
+                // the other half carries the means through, in the first lane's row
+                write_channels<T>(sums + lane * g.cw + c, m2);
+#pragma unroll
+                for (int e = 0; e < PAIRS; ++e) mean[e] = lane == 0 ? mean[e] : make_float2(0.f, 0.f);
+                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, mean);
+            }
+            __syncthreads();
+            sum_lanes(g, sums);
+            const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
+            const float* means = sums + g.lanes * g.cw;
+            const float frows = static_cast<float>(rows);
+            for (int k = warp; k < g.gw; k += warps) {
+                float s = 0.f;
+                for (int i = l; i < g.D; i += 32) s += means[k * g.D + i];
+                const float m = group_allreduce<32>(s) * inv_d;
+                float v = 0.f;
+                for (int i = l; i < g.D; i += 32) {
+                    const float d = means[k * g.D + i] - m;
+                    v += fmaf(frows * d, d, sums[k * g.D + i]);
+                }
+                v = group_allreduce<32>(v);
+                if (l == 0 && live) g.stats[(slab_i * g.gw + k) * g.parts + part] = make_float2(m, v);
+            }
         }
+        // count this block in, then wait for the slab's others
+        __syncthreads();
+        if (live && threadIdx.x == 0) {
+            unsigned* arrived = g.arrived + slab_i;
+            if (blockIdx.x != 0 || slab_i != g.drop_unit)  // failure injection: not counted in
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(arrived) : "memory");
+            if (!failed) {
+                const uint64_t t0 = global_timer_ns();
+                unsigned seen;
+                while (true) {
+                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(arrived) : "memory");
+                    if (seen >= static_cast<unsigned>(g.parts)) break;
+                    if (global_timer_ns() - t0 > g.a.wait_limit_ns) {
+                        failed = true;  // later waits are not made
+                        report_status(g.a.status, kStatusTimeout);
+                        break;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        // the slab's means: (mean, rstd), or the means of dz w and dz w xhat
+        if (live) {
+            const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
+            const float fd = static_cast<float>(g.D);
+            for (int k = warp; k < g.gw; k += warps) {
+                const float2* from = g.stats + (slab_i * g.gw + k) * g.parts;
+                float2 v = make_float2(0.f, 0.f);
+                if constexpr (BWD) {
+                    for (int i = l; i < g.parts; i += 32) v = __fadd2_rn(v, __ldcg(from + i));
+                    v.x = group_allreduce<32>(v.x) * inv_count;
+                    v.y = group_allreduce<32>(v.y) * inv_count;
+                } else {
+                    float s = 0.f;
+                    for (int i = l; i < g.parts; i += 32)
+                        s = fmaf(part_count(g, i, 1) * fd, __ldcg(from + i).x, s);
+                    const float m = group_allreduce<32>(s) * inv_count;
+                    float m2 = 0.f;
+                    for (int i = l; i < g.parts; i += 32) {
+                        const float2 t = __ldcg(from + i);
+                        const float d = t.x - m;
+                        m2 += fmaf(part_count(g, i, 1) * fd * d, d, t.y);
+                    }
+                    v = make_float2(m, rsqrtf(group_allreduce<32>(m2) * inv_count + g.a.eps));
+                    if (part == 0 && l == 0) {
+                        g.a.mean[group0 + k] = v.x;
+                        g.a.rstd[group0 + k] = v.y;
+                    }
+                }
+                if (l == 0) slab[k] = v;
+            }
+        }
+        __syncthreads();
+        if (live)
+            for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
+                const int k = quotient(i, inv_d);
+                const float2 v = slab[k];
+                const float w = channel<T>(g, g.a.w, c0 + i, 1.f), b = channel<T>(g, g.a.b, c0 + i, 0.f);
+                if constexpr (BWD) {
+                    const float m = g.a.mean[group0 + k], r = g.a.rstd[group0 + k];
+                    const float k3 = -v.y * r * r;
+                    table[i] = r * w;
+                    table[g.cw + i] = fmaf(-m, r * w, b);
+                    table[2 * g.cw + i] = k3;
+                    table[3 * g.cw + i] = fmaf(-m, k3, -v.x * r);
+                } else {
+                    table[i] = v.y * w;
+                    table[g.cw + i] = fmaf(-v.x, v.y * w, b);
+                }
+            }
+        __syncthreads();
+        if (active) {
+            if constexpr (BWD) {
+                read_channels<T>(table + c, col.k1);
+                read_channels<T>(table + g.cw + c, col.k2);
+                read_channels<T>(table + 2 * g.cw + c, col.k3);
+                read_channels<T>(table + 3 * g.cw + c, col.k4);
+            } else {
+                read_channels<T>(table + c, col.scale);
+                read_channels<T>(table + g.cw + c, col.shift);
+            }
+        }
+        // The second pass. dx may be the dy buffer: a position's copies are
+        // waited for before this thread, and no other, writes it.
+        typename Ring::Pass following = pass_of(round + 1, false);
+        char* out = static_cast<char*>(g.a.out) +
+                    ((sample * g.a.S + r0) * g.a.C + c0) * static_cast<int64_t>(SIZE) + pitch * lane + c * SIZE;
+        const int64_t back = static_cast<int64_t>(pitch) * g.lanes;
+        out += back * (mine_n - 1);
+        [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(SIZE);
+        again.n = mine_n;
+        ring.run(again, following, [&](const uint4& x, const uint4& dy) {
+            uint4 v;
+            if constexpr (BWD) v = col.apply(x, dy);
+            else v = col.apply(x);
+            if (RMSN_OK(span_in(out, 16, g.a.out, bytes), g.a.status)) {
+                if (g.drop) st_global_16_hint(out, v, ring.drop);
+                else st_global_16(out, v);
+            }
+            out -= back;
+        });
+        pass = following;
+        __syncthreads();  // the table's and the slab's readers are done
     }
-    __syncthreads();
-    allow_dependent_launch();
-    if (n == 0) return;
-    const int c = vec * VEC;
-    const int64_t last = (at.sample * g.a.S + at.r0 + lane) * g.a.C + c0 + c +
-                         static_cast<int64_t>(n - 1) * step;
-    Columns<T, BWD, ACT> col;
-    if constexpr (BWD) {
-        const float* rstd_of = g.a.rstd + at.sample * g.a.G + at.split * g.gw;
-        col.start(g, g.a.mean + at.sample * g.a.G + at.split * g.gw, rstd_of, c0, c, inv_d);
-        col.finish(g, rstd_of, slab, c, inv_d);
-    } else {
-        col.finish(g, slab, c0, c, inv_d);
-    }
-    // dx may be the dy buffer: the copies of a position are waited for before
-    // this thread, and no other, writes it
-    Feed<T, BWD, true> feed;
-    feed.x = static_cast<const T*>(g.a.x) + last;
-    feed.dy = BWD ? static_cast<const T*>(g.a.dy) + last : nullptr;
-    feed.step = -step;
-    feed.slots = smem_u32(keep + threadIdx.x);
-    feed.pitch = static_cast<uint32_t>(g.lanes * g.nvec) * 16u;
-    feed.n = n;
-    T* out = static_cast<T*>(g.a.out) + last;
-    [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(sizeof(T));
-    feed.run(g.a.status, [&](int, const uint4& x, const uint4& dy) {
-        uint4 v;
-        if constexpr (BWD) v = col.apply(x, dy);
-        else v = col.apply(x);
-        if (RMSN_OK(span_in(out, 16, g.a.out, bytes), g.a.status)) st_global_16(out, v);
-        out -= step;
-    });
+    copies_wait<0>();
 }
 
 template <typename T, bool BWD, int ACT>
 SlabFn slab_kernel(SlabKind k) {
-    if (k == SlabKind::kResident) return &gn_slab_kernel<T, BWD, ACT, true>;
-    if (k == SlabKind::kSums) return &gn_slab_kernel<T, BWD, ACT, false>;
-    return &gn_apply_kernel<T, BWD, ACT>;
+    if (k == SlabKind::kResident) return &gn_resident_kernel<T, BWD, ACT>;
+    return &gn_stream_kernel<T, BWD, ACT>;
 }
 template <typename T>
 SlabFn slab_kernel_of(bool bwd, int act, SlabKind k) {

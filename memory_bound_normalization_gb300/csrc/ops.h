@@ -70,7 +70,11 @@ struct GroupNormArgs {
     int act;
     int w_f32;
     int* status;
+    uint64_t wait_limit_ns;
 };
+
+// The failure-injection hook's unit (-1: none), which is thereby used up.
+int64_t take_drop_unit();
 
 // Workspace bytes of a call (0: none), and the call itself. `vec`: every
 // pointer is 16-byte aligned and a row of channels is a whole number of
