@@ -133,8 +133,7 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     p.nvec = static_cast<int>(wide() / 16);
     p.lanes = kStreamThreads / p.nvec;
     p.threads = kStreamThreads;
-    const int scratch = stream_scratch(p.lanes, a.C / p.splits);
-    p.smem = stream_ring(bwd) + scratch + a.G / p.splits * 8;
+    p.smem = stream_smem(bwd, p.lanes, a.C / p.splits, a.G / p.splits);
     if (p.smem > kMaxSmem) return best;
     const double total = static_cast<double>(a.B) * slab_rows * row_bytes;
     const SlabFn fn = kernel_for(dtype, bwd, a.act, SlabKind::kStream);
@@ -146,7 +145,7 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     p.together = static_cast<int>(cdiv(slabs, p.rounds));
     // at least two groups of positions a thread, where the slab has them
     p.parts = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(most / p.together, a.S / (2 * kGroup * p.lanes))));
+        1, std::min<int64_t>({most / p.together, kStreamMaxParts, a.S / (2 * kGroup * p.lanes)})));
     if ((a.S / p.parts + 1) * row_bytes > UINT32_MAX || a.B * p.parts > INT32_MAX) return best;
     const double cost = 12.0 + 3.0 * p.rounds + total * (bwd ? 1.5 : 2.0) / (44e3 * dev.sm_count);
     if (best.ok && best_cost <= cost) return best;
@@ -199,7 +198,6 @@ SlabArgs args_of(const Plan& p, bool bwd, const GroupNormArgs& a) {
     g.together = p.together;
     g.rounds = p.rounds;
     g.drop = p.drop;
-    g.scratch = stream_scratch(p.lanes, g.cw);
     const int parts = p.resident ? p.cluster : p.parts;
     g.part_rows = static_cast<int>(a.S / parts);
     g.part_more = static_cast<int>(a.S % parts);

@@ -27,7 +27,6 @@ struct SlabArgs {
     int parts;     // blocks of a slab
     int together;  // slabs of a round
     int rounds;
-    int scratch;   // bytes of the sums and channel constants
     int drop;      // L2 is told what is used for the last time
     unsigned* arrived;  // [slab]: blocks that have published their results
     float2* stats;      // [slab][group][part]: (mean, M2), or (sum w P, sum w Q)
@@ -47,11 +46,14 @@ inline int fixed_smem(int lanes, int cw, int gw) {
 
 // Positions a thread's copies run ahead, and positions of a group of copies.
 constexpr int kDepth = 6, kGroup = 2;
-constexpr int kStreamThreads = 256;
+constexpr int kStreamThreads = 512;  // one block an SM
+constexpr int kStreamMaxParts = 256;
 // The stream kernel's shared memory: the ring of copies; the sums of its
-// threads and the constants of its channels, in one place.
+// threads; its channels' constants and groups' results.
 inline int stream_ring(bool bwd) { return kDepth * kStreamThreads * 16 * (bwd ? 2 : 1); }
-inline int stream_scratch(int lanes, int cw) { return (2 * lanes > 4 ? 2 * lanes : 4) * cw * 4; }
+inline int stream_smem(bool bwd, int lanes, int cw, int gw) {
+    return stream_ring(bwd) + (2 * lanes + 4) * cw * 4 + gw * 8;
+}
 
 using SlabFn = void (*)(const SlabArgs);
 enum class SlabKind { kResident, kStream };

@@ -772,11 +772,13 @@ struct Copies {
     }
 };
 
-// Sums of a block's channels over its lanes, C sums of each of two kinds in
-// rows of `sums` ([2][lanes][cw]), into the first lane's rows; g.join threads
-// share a channel's lanes, and part 0 adds the parts.
+// Sums of a block's channels over its lanes: two values a channel in `sums`
+// ([2][lanes][cw]), added into the first lane's rows. g.join threads share a
+// channel's lanes (part j adds rows j, j + share, ... into row j), then part 0
+// adds the parts.
 __device__ __forceinline__ void sum_lanes(const SlabArgs& g, float* sums) {
     const int share = min(g.lanes, g.join), columns = 2 * g.cw;
+    __syncthreads();
     for (int i = threadIdx.x; i < columns * share; i += blockDim.x) {
         const int j = i / columns, c = i - j * columns;
         float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw) + j * g.cw;
@@ -790,6 +792,7 @@ __device__ __forceinline__ void sum_lanes(const SlabArgs& g, float* sums) {
         for (int c = threadIdx.x; c < columns; c += blockDim.x) {
             float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw);
             float s = 0.f;
+#pragma unroll 4
             for (int j = 0; j < share; ++j) s += at[j * g.cw];
             at[0] = s;
         }
@@ -798,126 +801,118 @@ __device__ __forceinline__ void sum_lanes(const SlabArgs& g, float* sums) {
 }
 
 template <typename T, bool BWD, int ACT>
-__global__ void __maxnreg__(BWD ? 80 : 64) gn_stream_kernel(const __grid_constant__ SlabArgs g) {
+__global__ void __launch_bounds__(kStreamThreads) gn_stream_kernel(const __grid_constant__ SlabArgs g) {
     constexpr int VEC = Pack<T>::VEC, PAIRS = Pack<T>::PAIRS, SIZE = sizeof(T);
     using Ring = Copies<T, BWD>;
+    using Pass = typename Ring::Pass;
     const int lane = static_cast<int>(threadIdx.x) / g.nvec;
     const int vec = static_cast<int>(threadIdx.x) - lane * g.nvec;
     const bool active = lane < g.lanes;
-    const float inv_d = 1.f / static_cast<float>(g.D);
-    const float inv_count = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
+    const float inv_d = 1.f / static_cast<float>(g.D), fd = static_cast<float>(g.D);
+    const float inv_count = 1.f / (static_cast<float>(g.a.S) * fd);
     const int team = static_cast<int>(blockIdx.x) / g.parts;
     const int part = static_cast<int>(blockIdx.x) - team * g.parts;
     const int64_t r0 = part_begin(g, part);
     const int rows = g.part_rows + (part < g.part_more ? 1 : 0);
-    const int n = active && rows > lane ? (rows - lane - 1) / g.lanes + 1 : 0;
+    const int n_all = active && rows > lane ? (rows - lane - 1) / g.lanes + 1 : 0;
     const int c = vec * VEC;
-    // shared memory: the ring; then, in one place, the threads' sums and the
-    // channels' constants, which are never needed at once; the groups' results
-    unsigned char* scratch = rmsn_dynamic_smem + Ring::GROUPS * Ring::GROUP;
-    float* sums = reinterpret_cast<float*>(scratch);
-    float* table = sums;  // up to 4 constants a channel, [4][cw]
-    float2* slab = reinterpret_cast<float2*>(scratch + g.scratch);
+    // shared memory: the ring, the threads' sums [2][lanes][cw], the channels'
+    // constants [4][cw], the groups' results
+    float* sums = reinterpret_cast<float*>(rmsn_dynamic_smem + Ring::GROUPS * Ring::GROUP);
+    float* chan = sums + 2 * g.lanes * g.cw;
+    float2* slab = reinterpret_cast<float2*>(chan + 4 * g.cw);
 
     Ring ring;
     ring.first = ring.slot = smem_u32(rmsn_dynamic_smem) + threadIdx.x * 16;
     ring.drop = l2_policy_evict_first();
     ring.status = g.a.status;
     const uint32_t pitch = static_cast<uint32_t>(g.a.C) * SIZE;  // bytes of a position
-    auto place = [&](int round, int64_t& sample, int& split) {
-        const int64_t i = static_cast<int64_t>(round) * g.together + team;
-        sample = i / g.splits;
-        split = static_cast<int>(i - sample * g.splits);
-        return sample < g.a.B;
-    };
+    const uint32_t own = pitch * lane + c * SIZE;
     auto pass_of = [&](int round, bool second) {
-        typename Ring::Pass p{};
-        int64_t sample;
-        int split;
-        if (round >= g.rounds || !place(round, sample, split)) return p;
-        const int64_t at = ((sample * g.a.S + r0) * g.a.C + static_cast<int64_t>(split) * g.cw) * SIZE;
+        Pass p{};
+        const int64_t i = static_cast<int64_t>(round) * g.together + team;
+        const int64_t sample = i / g.splits;
+        if (round >= g.rounds || sample >= g.a.B) return p;
+        const int64_t at =
+            ((sample * g.a.S + r0) * g.a.C + (i - sample * g.splits) * g.cw) * static_cast<int64_t>(SIZE);
         p.x = static_cast<const char*>(g.a.x) + at;
         if constexpr (BWD) p.dy = static_cast<const char*>(g.a.dy) + at;
-        p.n = n;
+        p.n = n_all;
         p.step = pitch * g.lanes;
-        p.off = pitch * lane + c * SIZE;
+        p.off = own;
         if (second) {
-            p.off += p.step * static_cast<uint32_t>(n > 0 ? n - 1 : 0);
+            p.off += p.step * static_cast<uint32_t>(n_all > 0 ? n_all - 1 : 0);
             p.step = 0u - p.step;
         }
         p.last_use = second && g.drop;
         return p;
     };
     bool failed = false;  // thread 0's: a wait ran out
-    typename Ring::Pass pass = pass_of(0, false);
+    Pass pass = pass_of(0, false);
 #pragma unroll
     for (int i = 0; i < Ring::GROUPS; ++i) {
         ring.issue(pass, pass.n - i * kGroup);
         ring.advance();
     }
 
+#pragma unroll 1
     for (int round = 0; round < g.rounds; ++round) {
-        int64_t sample;
-        int split;
-        const bool live = place(round, sample, split);
-        const int c0 = split * g.cw;
         const int64_t slab_i = static_cast<int64_t>(round) * g.together + team;
-        Columns<T, BWD, ACT> col;
-        typename Ring::Pass again = pass_of(round, true);
-        const int mine_n = live ? n : 0;
-        pass.n = mine_n;
+        const int64_t sample = slab_i / g.splits;
+        const int split = static_cast<int>(slab_i - sample * g.splits);
+        const bool live = sample < g.a.B;
+        const int n = live ? n_all : 0, c0 = split * g.cw;
         const int64_t group0 = sample * g.a.G + split * g.gw;
-        if constexpr (BWD) {
-            // -mean, rstd w and b of each channel
-            if (live)
-                for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
+        if (live)
+            for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
+                const float w = channel<T>(g, g.a.w, c0 + i, 1.f), b = channel<T>(g, g.a.b, c0 + i, 0.f);
+                if constexpr (BWD) {
                     const int k = quotient(i, inv_d);
                     const float r = g.a.rstd[group0 + k];
-                    table[i] = -g.a.mean[group0 + k];
-                    table[g.cw + i] = r * channel<T>(g, g.a.w, c0 + i, 1.f);
-                    table[2 * g.cw + i] = channel<T>(g, g.a.b, c0 + i, 0.f);
+                    chan[i] = -g.a.mean[group0 + k];
+                    chan[g.cw + i] = r * w;
+                    chan[3 * g.cw + i] = r;
+                } else {
+                    chan[g.cw + i] = w;
                 }
+                chan[2 * g.cw + i] = b;
+            }
+        Pass again = pass_of(round, true);
+        Columns<T, BWD, ACT> col;
+        if constexpr (BWD) {
             __syncthreads();
             if (active) {
-                read_channels<T>(table + c, col.mean);
-                read_channels<T>(table + g.cw + c, col.k1);
-                read_channels<T>(table + 2 * g.cw + c, col.b);
+                read_channels<T>(chan + c, col.mean);
+                read_channels<T>(chan + g.cw + c, col.k1);
+                read_channels<T>(chan + 2 * g.cw + c, col.b);
             }
 #pragma unroll
             for (int e = 0; e < PAIRS; ++e) col.p[e] = col.q[e] = make_float2(0.f, 0.f);
             ring.run(pass, again, [&](const uint4& x, const uint4& dy) { col.add(x, dy); });
-            __syncthreads();  // every thread has its constants
             if (active) {
                 write_channels<T>(sums + lane * g.cw + c, col.p);
                 write_channels<T>(sums + (g.lanes + lane) * g.cw + c, col.q);
             }
-            __syncthreads();
             sum_lanes(g, sums);
-            // sum dz (x - mean) becomes sum dz xhat; groups' sums weighted by w
-            const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
-            float* ps = sums;
-            float* qs = sums + g.lanes * g.cw;
+            // with k1 = rstd w: sum k1 P = rstd sum w dz, sum k1 Q = sum w dz xhat
+            const float* ps = sums;
+            const float* qs = sums + g.lanes * g.cw;
             for (int k = warp; k < g.gw; k += warps) {
-                const float r = live ? g.a.rstd[group0 + k] : 0.f;
                 float sp = 0.f, sq = 0.f;
                 for (int i = l; i < g.D; i += 32) {
-                    const int ch = k * g.D + i;
-                    const float w = live ? channel<T>(g, g.a.w, c0 + ch, 1.f) : 0.f;
-                    const float q = qs[ch] * r;
-                    qs[ch] = q;
-                    sp = fmaf(w, ps[ch], sp);
-                    sq = fmaf(w, q, sq);
+                    const float k1 = chan[g.cw + k * g.D + i];
+                    sp = fmaf(k1, ps[k * g.D + i], sp);
+                    sq = fmaf(k1, qs[k * g.D + i], sq);
                 }
                 sp = group_allreduce<32>(sp);
                 sq = group_allreduce<32>(sq);
-                if (l == 0 && live)
-                    g.stats[(slab_i * g.gw + k) * g.parts + part] = make_float2(sp, sq);
+                if (l == 0 && live) g.stats[(slab_i * g.gw + k) * g.parts + part] = make_float2(sp, sq);
             }
-            __syncthreads();
             if (g.rows != nullptr && live) {
                 float* row = g.rows + (sample * g.parts + part) * 2 * g.a.C + c0;
                 for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
-                    row[i] = qs[i];
+                    row[i] = qs[i] * chan[3 * g.cw + i];
                     row[g.a.C + i] = ps[i];
                 }
             }
@@ -932,60 +927,53 @@ __global__ void __maxnreg__(BWD ? 80 : 64) gn_stream_kernel(const __grid_constan
                 col.add(x);
             });
             // channel means over the lanes, then squares about them, then groups
-            const float inv_n = mine_n > 0 ? 1.f / static_cast<float>(mine_n) : 0.f;
-            const float inv_rows = 1.f / static_cast<float>(max(rows, 1));
-            float2 own[PAIRS];  // sum of the thread's values
-            __syncthreads();  // the sums' place: every thread has its constants
+            const float fn = static_cast<float>(n), inv_n = n > 0 ? 1.f / fn : 0.f;
+            const float frows = static_cast<float>(rows), inv_rows = 1.f / fmaxf(frows, 1.f);
+            float2 u[PAIRS], v[PAIRS];
             if (active) {
-                float2 none[PAIRS];
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
-                    own[e] = __ffma2_rn(col.pivot[e], f2_splat(static_cast<float>(mine_n)), col.s1[e]);
-                    none[e] = make_float2(0.f, 0.f);
+                    u[e] = __ffma2_rn(col.pivot[e], f2_splat(fn), col.s1[e]);
+                    v[e] = make_float2(0.f, 0.f);
                 }
-                write_channels<T>(sums + lane * g.cw + c, own);
-                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, none);
+                write_channels<T>(sums + lane * g.cw + c, u);
+                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, v);
             }
-            __syncthreads();
             sum_lanes(g, sums);
-            float2 mean[PAIRS], m2[PAIRS];
             if (active) {
-                read_channels<T>(sums + c, mean);
+                read_channels<T>(sums + c, u);
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
-                    mean[e] = __fmul2_rn(mean[e], f2_splat(inv_rows));
+                    u[e] = __fmul2_rn(u[e], f2_splat(inv_rows));
                     // squares of the thread's values about the channel's mean
                     const float2 d = __fmul2_rn(col.s1[e], f2_splat(inv_n));
-                    const float2 off = sub2(__fadd2_rn(col.pivot[e], d), mean[e]);
-                    m2[e] = sub2(col.s2[e], __fmul2_rn(col.s1[e], d));
-                    m2[e] = __ffma2_rn(__fmul2_rn(off, off), f2_splat(static_cast<float>(mine_n)), m2[e]);
-                    if (mine_n == 0) m2[e] = make_float2(0.f, 0.f);
+                    const float2 off = sub2(__fadd2_rn(col.pivot[e], d), u[e]);
+                    v[e] = sub2(col.s2[e], __fmul2_rn(col.s1[e], d));
+                    v[e] = __ffma2_rn(__fmul2_rn(off, off), f2_splat(fn), v[e]);
+                    if (n == 0) v[e] = make_float2(0.f, 0.f);
                 }
             }
             __syncthreads();
             if (active) {
                 // the other half carries the means through, in the first lane's row
-                write_channels<T>(sums + lane * g.cw + c, m2);
+                write_channels<T>(sums + lane * g.cw + c, v);
 #pragma unroll
-                for (int e = 0; e < PAIRS; ++e) mean[e] = lane == 0 ? mean[e] : make_float2(0.f, 0.f);
-                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, mean);
+                for (int e = 0; e < PAIRS; ++e) u[e] = lane == 0 ? u[e] : make_float2(0.f, 0.f);
+                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, u);
             }
-            __syncthreads();
             sum_lanes(g, sums);
-            const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
             const float* means = sums + g.lanes * g.cw;
-            const float frows = static_cast<float>(rows);
             for (int k = warp; k < g.gw; k += warps) {
                 float s = 0.f;
                 for (int i = l; i < g.D; i += 32) s += means[k * g.D + i];
                 const float m = group_allreduce<32>(s) * inv_d;
-                float v = 0.f;
+                float m2 = 0.f;
                 for (int i = l; i < g.D; i += 32) {
                     const float d = means[k * g.D + i] - m;
-                    v += fmaf(frows * d, d, sums[k * g.D + i]);
+                    m2 += fmaf(frows * d, d, sums[k * g.D + i]);
                 }
-                v = group_allreduce<32>(v);
-                if (l == 0 && live) g.stats[(slab_i * g.gw + k) * g.parts + part] = make_float2(m, v);
+                m2 = group_allreduce<32>(m2);
+                if (l == 0 && live) g.stats[(slab_i * g.gw + k) * g.parts + part] = make_float2(m, m2);
             }
         }
         // count this block in, then wait for the slab's others
@@ -996,8 +984,8 @@ __global__ void __maxnreg__(BWD ? 80 : 64) gn_stream_kernel(const __grid_constan
                 asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(arrived) : "memory");
             if (!failed) {
                 const uint64_t t0 = global_timer_ns();
-                unsigned seen;
                 while (true) {
+                    unsigned seen;
                     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(arrived) : "memory");
                     if (seen >= static_cast<unsigned>(g.parts)) break;
                     if (global_timer_ns() - t0 > g.a.wait_limit_ns) {
@@ -1009,88 +997,90 @@ __global__ void __maxnreg__(BWD ? 80 : 64) gn_stream_kernel(const __grid_constan
             }
         }
         __syncthreads();
-        // the slab's means: (mean, rstd), or the means of dz w and dz w xhat
-        if (live) {
-            const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
-            const float fd = static_cast<float>(g.D);
-            for (int k = warp; k < g.gw; k += warps) {
-                const float2* from = g.stats + (slab_i * g.gw + k) * g.parts;
-                float2 v = make_float2(0.f, 0.f);
-                if constexpr (BWD) {
-                    for (int i = l; i < g.parts; i += 32) v = __fadd2_rn(v, __ldcg(from + i));
-                    v.x = group_allreduce<32>(v.x) * inv_count;
-                    v.y = group_allreduce<32>(v.y) * inv_count;
-                } else {
-                    float s = 0.f;
-                    for (int i = l; i < g.parts; i += 32)
-                        s = fmaf(part_count(g, i, 1) * fd, __ldcg(from + i).x, s);
-                    const float m = group_allreduce<32>(s) * inv_count;
-                    float m2 = 0.f;
-                    for (int i = l; i < g.parts; i += 32) {
-                        const float2 t = __ldcg(from + i);
-                        const float d = t.x - m;
-                        m2 += fmaf(part_count(g, i, 1) * fd * d, d, t.y);
-                    }
-                    v = make_float2(m, rsqrtf(group_allreduce<32>(m2) * inv_count + g.a.eps));
-                    if (part == 0 && l == 0) {
-                        g.a.mean[group0 + k] = v.x;
-                        g.a.rstd[group0 + k] = v.y;
-                    }
+        // the slab's means of each group: (mean, rstd), or rstd times the mean of
+        // dz w and the mean of dz w xhat. All of a lane's results are read at once.
+        for (int k = live ? warp : g.gw; k < g.gw; k += warps) {
+            const float2* from = g.stats + (slab_i * g.gw + k) * g.parts;
+            float2 t[kStreamMaxParts / 32];
+#pragma unroll
+            for (int i = 0; i < kStreamMaxParts / 32; ++i)
+                t[i] = l + 32 * i < g.parts ? __ldcg(from + l + 32 * i) : make_float2(0.f, 0.f);
+            float2 v = make_float2(0.f, 0.f);
+            if constexpr (BWD) {
+#pragma unroll
+                for (int i = 0; i < kStreamMaxParts / 32; ++i) v = __fadd2_rn(v, t[i]);
+                v.x = group_allreduce<32>(v.x) * inv_count;
+                v.y = group_allreduce<32>(v.y) * inv_count;
+            } else {
+                float count[kStreamMaxParts / 32];
+#pragma unroll
+                for (int i = 0; i < kStreamMaxParts / 32; ++i) {
+                    const int j = l + 32 * i;
+                    count[i] = j < g.parts ? static_cast<float>(g.part_rows + (j < g.part_more ? 1 : 0)) * fd : 0.f;
+                    v.x = fmaf(count[i], t[i].x, v.x);
                 }
-                if (l == 0) slab[k] = v;
+                v.x = group_allreduce<32>(v.x) * inv_count;
+#pragma unroll
+                for (int i = 0; i < kStreamMaxParts / 32; ++i) {
+                    const float d = t[i].x - v.x;
+                    v.y += fmaf(count[i] * d, d, t[i].y);
+                }
+                v.y = rsqrtf(group_allreduce<32>(v.y) * inv_count + g.a.eps);
+                if (part == 0 && l == 0) {
+                    g.a.mean[group0 + k] = v.x;
+                    g.a.rstd[group0 + k] = v.y;
+                }
             }
+            if (l == 0) slab[k] = v;
         }
         __syncthreads();
         if (live)
             for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
-                const int k = quotient(i, inv_d);
-                const float2 v = slab[k];
-                const float w = channel<T>(g, g.a.w, c0 + i, 1.f), b = channel<T>(g, g.a.b, c0 + i, 0.f);
+                const float2 v = slab[quotient(i, inv_d)];
                 if constexpr (BWD) {
-                    const float m = g.a.mean[group0 + k], r = g.a.rstd[group0 + k];
+                    const float m = chan[i], r = chan[3 * g.cw + i];
                     const float k3 = -v.y * r * r;
-                    table[i] = r * w;
-                    table[g.cw + i] = fmaf(-m, r * w, b);
-                    table[2 * g.cw + i] = k3;
-                    table[3 * g.cw + i] = fmaf(-m, k3, -v.x * r);
+                    chan[2 * g.cw + i] = fmaf(m, chan[g.cw + i], chan[2 * g.cw + i]);
+                    chan[i] = k3;
+                    chan[3 * g.cw + i] = fmaf(m, k3, -v.x);
                 } else {
-                    table[i] = v.y * w;
-                    table[g.cw + i] = fmaf(-v.x, v.y * w, b);
+                    const float scale = v.y * chan[g.cw + i];
+                    chan[g.cw + i] = scale;
+                    chan[2 * g.cw + i] = fmaf(-v.x, scale, chan[2 * g.cw + i]);
                 }
             }
         __syncthreads();
         if (active) {
             if constexpr (BWD) {
-                read_channels<T>(table + c, col.k1);
-                read_channels<T>(table + g.cw + c, col.k2);
-                read_channels<T>(table + 2 * g.cw + c, col.k3);
-                read_channels<T>(table + 3 * g.cw + c, col.k4);
+                read_channels<T>(chan + c, col.k3);
+                read_channels<T>(chan + g.cw + c, col.k1);
+                read_channels<T>(chan + 2 * g.cw + c, col.k2);
+                read_channels<T>(chan + 3 * g.cw + c, col.k4);
             } else {
-                read_channels<T>(table + c, col.scale);
-                read_channels<T>(table + g.cw + c, col.shift);
+                read_channels<T>(chan + g.cw + c, col.scale);
+                read_channels<T>(chan + 2 * g.cw + c, col.shift);
             }
         }
         // The second pass. dx may be the dy buffer: a position's copies are
         // waited for before this thread, and no other, writes it.
-        typename Ring::Pass following = pass_of(round + 1, false);
-        char* out = static_cast<char*>(g.a.out) +
-                    ((sample * g.a.S + r0) * g.a.C + c0) * static_cast<int64_t>(SIZE) + pitch * lane + c * SIZE;
+        Pass following = pass_of(round + 1, false);
         const int64_t back = static_cast<int64_t>(pitch) * g.lanes;
-        out += back * (mine_n - 1);
+        char* out = static_cast<char*>(g.a.out) +
+                    ((sample * g.a.S + r0) * g.a.C + c0) * static_cast<int64_t>(SIZE) + own + back * (n - 1);
         [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(SIZE);
-        again.n = mine_n;
+        const bool drop = g.drop;
         ring.run(again, following, [&](const uint4& x, const uint4& dy) {
             uint4 v;
             if constexpr (BWD) v = col.apply(x, dy);
             else v = col.apply(x);
             if (RMSN_OK(span_in(out, 16, g.a.out, bytes), g.a.status)) {
-                if (g.drop) st_global_16_hint(out, v, ring.drop);
+                if (drop) st_global_16_hint(out, v, ring.drop);
                 else st_global_16(out, v);
             }
             out -= back;
         });
         pass = following;
-        __syncthreads();  // the table's and the slab's readers are done
+        __syncthreads();  // the constants' readers are done
     }
     copies_wait<0>();
 }
