@@ -139,8 +139,10 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     const SlabFn fn = kernel_for(dtype, bwd, a.act, SlabKind::kStream);
     const int64_t most = resident_clusters(dev, fn, p.threads, p.smem, 1);
     if (most < 1) return best;
+    // two at least, as long as what both keep is near L2's size
+    const int64_t fit = budget / (wide() * slab_rows);
     p.together = static_cast<int>(std::min<int64_t>(
-        {slabs, most, std::max<int64_t>(1, budget / (wide() * slab_rows))}));
+        {slabs, most, fit >= 2 ? fit : wide() * slab_rows <= budget ? 2 : 1}));
     p.rounds = static_cast<int>(cdiv(slabs, p.together));
     p.together = static_cast<int>(cdiv(slabs, p.rounds));
     // at least two groups of positions a thread, where the slab has them

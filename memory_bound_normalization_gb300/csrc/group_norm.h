@@ -46,8 +46,8 @@ inline int fixed_smem(int lanes, int cw, int gw) {
 
 // Positions a thread's copies run ahead, and positions of a group of copies.
 constexpr int kDepth = 6, kGroup = 2;
-constexpr int kStreamThreads = 512;  // one block an SM
-constexpr int kStreamMaxParts = 256;
+constexpr int kStreamThreads = 256;  // two blocks an SM
+constexpr int kStreamMaxParts = 320;
 // The stream kernel's shared memory: the ring of copies; the sums of its
 // threads; its channels' constants and groups' results.
 inline int stream_ring(bool bwd) { return kDepth * kStreamThreads * 16 * (bwd ? 2 : 1); }

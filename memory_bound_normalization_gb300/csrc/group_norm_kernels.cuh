@@ -800,8 +800,23 @@ __device__ __forceinline__ void sum_lanes(const SlabArgs& g, float* sums) {
     }
 }
 
+// Waits until every block of a slab has published its results, for a limited
+// time; a wait that runs out is reported.
+__device__ __forceinline__ bool all_arrived(const SlabArgs& g, int64_t slab) {
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        unsigned seen;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(g.arrived + slab) : "memory");
+        if (seen >= static_cast<unsigned>(g.parts)) return true;
+        if (global_timer_ns() - t0 > g.a.wait_limit_ns) {
+            report_status(g.a.status, kStatusTimeout);
+            return false;
+        }
+    }
+}
+
 template <typename T, bool BWD, int ACT>
-__global__ void __launch_bounds__(kStreamThreads) gn_stream_kernel(const __grid_constant__ SlabArgs g) {
+__global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __grid_constant__ SlabArgs g) {
     constexpr int VEC = Pack<T>::VEC, PAIRS = Pack<T>::PAIRS, SIZE = sizeof(T);
     using Ring = Copies<T, BWD>;
     using Pass = typename Ring::Pass;
@@ -856,6 +871,12 @@ __global__ void __launch_bounds__(kStreamThreads) gn_stream_kernel(const __grid_
         ring.advance();
     }
 
+    // Two teams: the second starts when the first has its sums, so that one
+    // reads while the other, and its wait, leave DRAM to it.
+    if (g.together == 2 && team == 1 && g.rounds > 1) {
+        if (threadIdx.x == 0) failed = !all_arrived(g, 0);
+        __syncthreads();
+    }
 #pragma unroll 1
     for (int round = 0; round < g.rounds; ++round) {
         const int64_t slab_i = static_cast<int64_t>(round) * g.together + team;
@@ -979,22 +1000,9 @@ __global__ void __launch_bounds__(kStreamThreads) gn_stream_kernel(const __grid_
         // count this block in, then wait for the slab's others
         __syncthreads();
         if (live && threadIdx.x == 0) {
-            unsigned* arrived = g.arrived + slab_i;
             if (blockIdx.x != 0 || slab_i != g.drop_unit)  // failure injection: not counted in
-                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(arrived) : "memory");
-            if (!failed) {
-                const uint64_t t0 = global_timer_ns();
-                while (true) {
-                    unsigned seen;
-                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(arrived) : "memory");
-                    if (seen >= static_cast<unsigned>(g.parts)) break;
-                    if (global_timer_ns() - t0 > g.a.wait_limit_ns) {
-                        failed = true;  // later waits are not made
-                        report_status(g.a.status, kStatusTimeout);
-                        break;
-                    }
-                }
-            }
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.arrived + slab_i) : "memory");
+            if (!failed) failed = !all_arrived(g, slab_i);  // later waits are not made
         }
         __syncthreads();
         // the slab's means of each group: (mean, rstd), or rstd times the mean of
