@@ -147,7 +147,7 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     p.together = static_cast<int>(cdiv(slabs, p.rounds));
     // at least two groups of positions a thread, where the slab has them
     p.parts = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>({most / p.together, kStreamMaxParts, a.S / (2 * kGroup * p.lanes)})));
+        1, std::min<int64_t>({most / p.together, kStreamMaxParts, a.S / (4 * p.lanes)})));
     if ((a.S / p.parts + 1) * row_bytes > UINT32_MAX || a.B * p.parts > INT32_MAX) return best;
     const double cost = 12.0 + 3.0 * p.rounds + total * (bwd ? 1.5 : 2.0) / (44e3 * dev.sm_count);
     if (best.ok && best_cost <= cost) return best;

@@ -48,9 +48,10 @@ inline int fixed_smem(int lanes, int cw, int gw) {
 constexpr int kDepth = 6, kGroup = 2;
 constexpr int kStreamThreads = 256;  // two blocks an SM
 constexpr int kStreamMaxParts = 320;
+constexpr int stream_depth(bool bwd) { return bwd ? 8 : 12; }
 // The stream kernel's shared memory: the ring of copies; the sums of its
 // threads; its channels' constants and groups' results.
-inline int stream_ring(bool bwd) { return kDepth * kStreamThreads * 16 * (bwd ? 2 : 1); }
+inline int stream_ring(bool bwd) { return stream_depth(bwd) * kStreamThreads * 16 * (bwd ? 2 : 1); }
 inline int stream_smem(bool bwd, int lanes, int cw, int gw) {
     return stream_ring(bwd) + (2 * lanes + 4) * cw * 4 + gw * 8;
 }

@@ -686,13 +686,13 @@ __global__ void __launch_bounds__(kMaxThreads) gn_resident_kernel(const __grid_c
 // slab). In a round a block sums its positions, publishes its groups' results
 // and counts itself in; while the others arrive, its copies of the second pass,
 // which goes from its last position back to the first, are under way. Copies
-// run kDepth positions ahead across passes and rounds, so that DRAM stays busy
+// run some positions ahead across passes and rounds, so that DRAM stays busy
 // while sums are joined. The wait for the others is bounded in time.
 template <typename T, bool BWD>
 struct Copies {
     static constexpr int TENSORS = BWD ? 2 : 1;
-    static constexpr uint32_t PITCH = kStreamThreads * 16, GROUP = kGroup * TENSORS * PITCH;
-    static constexpr int GROUPS = kDepth / kGroup;
+    static constexpr uint32_t PITCH = kStreamThreads * 16, GROUP = TENSORS * PITCH;
+    static constexpr int DEPTH = BWD ? stream_depth(true) : stream_depth(false);
     // a pass: where its copies come from and how many positions it has
     struct Pass {
         const char* x;
@@ -712,63 +712,48 @@ struct Copies {
         else
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
     }
-    // copies a group of a pass of which `left` positions remain
-    __device__ __forceinline__ void issue(Pass& p, int left) const {
-#pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-            if (u < left) {
-                copy(slot + u * TENSORS * PITCH, p.x + p.off, p.last_use);
-                if constexpr (BWD) copy(slot + (u * TENSORS + 1) * PITCH, p.dy + p.off, p.last_use);
-            }
+    // copies a pass's next position, if it has one
+    __device__ __forceinline__ void issue(Pass& p, bool has) const {
+        if (has) {
+            copy(slot, p.x + p.off, p.last_use);
+            if constexpr (BWD) copy(slot + PITCH, p.dy + p.off, p.last_use);
             p.off += p.step;
         }
         copies_commit();
     }
-    __device__ __forceinline__ void advance() { slot = slot + GROUP == first + GROUPS * GROUP ? first : slot + GROUP; }
-    // A pass whose first GROUPS groups are under way: visits its positions in
+    __device__ __forceinline__ void advance() { slot = slot + GROUP == first + DEPTH * GROUP ? first : slot + GROUP; }
+    // A pass whose first DEPTH copies are under way: visits its positions in
     // order, and starts the next pass's copies as its own run out. `p` is the
-    // pass's next position to copy.
-    template <typename Visit>
-    __device__ __forceinline__ void run(Pass& p, Pass& next, Visit visit) {
-        const int full = p.n / kGroup - GROUPS;  // groups whose successor GROUPS on is whole
+    // pass's next position to copy, and the next pass's in the end.
+    template <typename Next, typename Visit>
+    __device__ __forceinline__ void run(Pass& p, Next next_pass, Visit visit) {
         int i = 0;
 #pragma unroll 1
-        for (; i < full; ++i) {
-            copies_wait<GROUPS - 1>();
-            uint4 xv[kGroup], dv[kGroup];
-#pragma unroll
-            for (int u = 0; u < kGroup; ++u) {
-                xv[u] = ld_slot(slot + u * TENSORS * PITCH);
-                if constexpr (BWD) dv[u] = ld_slot(slot + (u * TENSORS + 1) * PITCH);
-            }
-#pragma unroll
-            for (int u = 0; u < kGroup; ++u) visit(xv[u], dv[u]);
-            issue(p, kGroup);
+        for (; i < p.n - DEPTH; ++i) {
+            copies_wait<DEPTH - 1>();
+            const uint4 x = ld_slot(slot);
+            uint4 dy = x;
+            if constexpr (BWD) dy = ld_slot(slot + PITCH);
+            visit(x, dy);
+            issue(p, true);
             advance();
         }
-        const int groups = max((p.n + kGroup - 1) / kGroup, GROUPS);
+        Pass next = next_pass();
+        const int end = max(p.n, DEPTH);
         int ahead = 0;  // positions of the next pass under way
 #pragma unroll 1
-        for (; i < groups; ++i) {
-            copies_wait<GROUPS - 1>();
-            uint4 xv[kGroup], dv[kGroup];
-#pragma unroll
-            for (int u = 0; u < kGroup; ++u)
-                if (i * kGroup + u < p.n) {
-                    xv[u] = ld_slot(slot + u * TENSORS * PITCH);
-                    if constexpr (BWD) dv[u] = ld_slot(slot + (u * TENSORS + 1) * PITCH);
-                }
-#pragma unroll
-            for (int u = 0; u < kGroup; ++u)
-                if (i * kGroup + u < p.n) visit(xv[u], dv[u]);
-            if (i + GROUPS < groups) {
-                issue(p, p.n - (i + GROUPS) * kGroup);
-            } else {
-                issue(next, next.n - ahead);
-                ahead += kGroup;
+        for (; i < end; ++i) {
+            copies_wait<DEPTH - 1>();
+            if (i < p.n) {
+                const uint4 x = ld_slot(slot);
+                uint4 dy = x;
+                if constexpr (BWD) dy = ld_slot(slot + PITCH);
+                visit(x, dy);
             }
+            issue(next, ahead++ < next.n);
             advance();
         }
+        p = next;
     }
 };
 
@@ -834,7 +819,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
     const int c = vec * VEC;
     // shared memory: the ring, the threads' sums [2][lanes][cw], the channels'
     // constants [4][cw], the groups' results
-    float* sums = reinterpret_cast<float*>(rmsn_dynamic_smem + Ring::GROUPS * Ring::GROUP);
+    float* sums = reinterpret_cast<float*>(rmsn_dynamic_smem + Ring::DEPTH * Ring::GROUP);
     float* chan = sums + 2 * g.lanes * g.cw;
     float2* slab = reinterpret_cast<float2*>(chan + 4 * g.cw);
 
@@ -866,8 +851,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
     bool failed = false;  // thread 0's: a wait ran out
     Pass pass = pass_of(0, false);
 #pragma unroll
-    for (int i = 0; i < Ring::GROUPS; ++i) {
-        ring.issue(pass, pass.n - i * kGroup);
+    for (int i = 0; i < Ring::DEPTH; ++i) {
+        ring.issue(pass, i < pass.n);
         ring.advance();
     }
 
@@ -899,7 +884,6 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
                 }
                 chan[2 * g.cw + i] = b;
             }
-        Pass again = pass_of(round, true);
         Columns<T, BWD, ACT> col;
         if constexpr (BWD) {
             __syncthreads();
@@ -910,7 +894,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
             }
 #pragma unroll
             for (int e = 0; e < PAIRS; ++e) col.p[e] = col.q[e] = make_float2(0.f, 0.f);
-            ring.run(pass, again, [&](const uint4& x, const uint4& dy) { col.add(x, dy); });
+            ring.run(pass, [&] { return pass_of(round, true); }, [&](const uint4& x, const uint4& dy) { col.add(x, dy); });
             if (active) {
                 write_channels<T>(sums + lane * g.cw + c, col.p);
                 write_channels<T>(sums + (g.lanes + lane) * g.cw + c, col.q);
@@ -940,7 +924,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
         } else {
             col.start(make_uint4(0, 0, 0, 0));
             bool first = true;
-            ring.run(pass, again, [&](const uint4& x, const uint4&) {
+            ring.run(pass, [&] { return pass_of(round, true); }, [&](const uint4& x, const uint4&) {
                 if (first) {
                     col.start(x);
                     first = false;
@@ -1071,13 +1055,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
         }
         // The second pass. dx may be the dy buffer: a position's copies are
         // waited for before this thread, and no other, writes it.
-        Pass following = pass_of(round + 1, false);
         const int64_t back = static_cast<int64_t>(pitch) * g.lanes;
         char* out = static_cast<char*>(g.a.out) +
                     ((sample * g.a.S + r0) * g.a.C + c0) * static_cast<int64_t>(SIZE) + own + back * (n - 1);
         [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(SIZE);
         const bool drop = g.drop;
-        ring.run(again, following, [&](const uint4& x, const uint4& dy) {
+        ring.run(pass, [&] { return pass_of(round + 1, false); }, [&](const uint4& x, const uint4& dy) {
             uint4 v;
             if constexpr (BWD) v = col.apply(x, dy);
             else v = col.apply(x);
@@ -1087,7 +1070,6 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
             }
             out -= back;
         });
-        pass = following;
         __syncthreads();  // the constants' readers are done
     }
     copies_wait<0>();
