@@ -186,7 +186,7 @@ Plan plan_of(const DeviceInfo& dev, int dtype, bool vec, bool bwd, const GroupNo
     return p;
 }
 
-SlabArgs args_of(const Plan& p, bool bwd, const GroupNormArgs& a) {
+SlabArgs args_of(const Plan& p, const GroupNormArgs& a) {
     SlabArgs g{};
     g.a = a;
     g.nvec = p.nvec;
@@ -203,8 +203,7 @@ SlabArgs args_of(const Plan& p, bool bwd, const GroupNormArgs& a) {
     const int parts = p.resident ? p.cluster : p.parts;
     g.part_rows = static_cast<int>(a.S / parts);
     g.part_more = static_cast<int>(a.S % parts);
-    // a power of two of warps a group (resident forward), or of threads a channel
-    const int room = bwd || !p.resident ? p.threads / (2 * g.cw) : p.threads / 32 / g.gw;
+    const int room = p.threads / (2 * g.cw);
     g.join = 1;
     while (g.join < 16 && 2 * g.join <= room) g.join *= 2;
     g.drop_unit = -1;
@@ -239,7 +238,7 @@ cudaError_t group_norm_launch(const DeviceInfo& dev, int dtype, bool vec, bool b
                               const GroupNormArgs& a, void* workspace, cudaStream_t s) {
     const Plan p = plan_of(dev, dtype, vec, bwd, a);
     if (!p.ok) return gn_scalar_launch(dtype, bwd, a, workspace, s);
-    SlabArgs g = args_of(p, bwd, a);
+    SlabArgs g = args_of(p, a);
     const int64_t rows = partial_rows(p, bwd, a);
     char* ws = static_cast<char*>(workspace);
     const size_t arrived = arrived_bytes(p, a);

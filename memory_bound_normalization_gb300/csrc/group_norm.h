@@ -22,7 +22,7 @@ struct SlabArgs {
     int D;         // channels of a group
     int cluster;   // resident: blocks of a slab, which join their sums
     int part_rows, part_more;  // positions of a block, and how many blocks take one more
-    int join;      // warps that share a group's sums in a block, or threads a channel's
+    int join;      // threads that share a channel's sums in a block
     // stream
     int parts;     // blocks of a slab
     int together;  // slabs of a round
@@ -35,17 +35,12 @@ struct SlabArgs {
     float* rows;
 };
 
-// Shared memory besides the resident slab: the threads' sums [2][lanes][cw],
-// two values a group, twice (the block's and the slab's), and the warps' parts
-// of a group's sums.
-__host__ __device__ __forceinline__ int sums_floats(int lanes, int cw) { return 2 * lanes * cw; }
-constexpr int kJoinFloats = 2 * kMaxThreads / 32;
-inline int fixed_smem(int lanes, int cw, int gw) {
-    return (sums_floats(lanes, cw) + 4 * gw + kJoinFloats) * 4;
-}
+// Shared memory besides the slots: the threads' sums, the channels' constants,
+// and two values a group, twice (the block's and the slab's).
+inline int fixed_smem(int lanes, int cw, int gw) { return (2 * lanes * cw + 4 * cw + 4 * gw) * 4; }
 
 // Positions a thread's copies run ahead, and positions of a group of copies.
-constexpr int kDepth = 6, kGroup = 2;
+constexpr int kDepth = 16, kGroup = 2;
 constexpr int kStreamThreads = 256;  // two blocks an SM
 constexpr int kStreamMaxParts = 320;
 constexpr int stream_depth(bool bwd) { return bwd ? 8 : 12; }

@@ -81,26 +81,7 @@ __device__ __forceinline__ float ld_cluster_f32(const float* local, uint32_t ran
     return v;
 }
 
-// A thread's channels: scale and offset of the affine map.
-template <typename T>
-__device__ __forceinline__ void load_channels(const SlabArgs& g, const void* p, int64_t c, float one,
-                                              float2 (&f)[Pack<T>::PAIRS]) {
-    constexpr int PAIRS = Pack<T>::PAIRS;
-    if (p == nullptr) {
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) f[e] = f2_splat(one);
-    } else if (g.a.w_f32) {
-        // weights need only their own alignment
-        const float* w = static_cast<const float*>(p) + c;
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) f[e] = make_float2(w[2 * e], w[2 * e + 1]);
-    } else {
-        const T* w = static_cast<const T*>(p) + c;
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) f[e] = make_float2(to_f32(w[2 * e]), to_f32(w[2 * e + 1]));
-    }
-}
-
+// A channel's weight or bias.
 template <typename T>
 __device__ __forceinline__ float channel(const SlabArgs& g, const void* p, int c, float none) {
     if (p == nullptr) return none;
@@ -121,16 +102,6 @@ __device__ __forceinline__ void write_channels(float* row, const float2 (&f)[Pac
 #pragma unroll
     for (int e = 0; e < Pack<T>::PAIRS; e += 2)
         *reinterpret_cast<float4*>(row + 2 * e) = make_float4(f[e].x, f[e].y, f[e + 1].x, f[e + 1].y);
-}
-
-// Constants of a thread's channels from per-group values in shared or global
-// memory: v[group of the channel].
-template <typename T, typename F>
-__device__ __forceinline__ void per_channel(const SlabArgs& g, int c, float inv_d, F value,
-                                            float2 (&f)[Pack<T>::PAIRS]) {
-#pragma unroll
-    for (int e = 0; e < Pack<T>::PAIRS; ++e)
-        f[e] = make_float2(value(quotient(c + 2 * e, inv_d)), value(quotient(c + 2 * e + 1, inv_d)));
 }
 
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
@@ -259,20 +230,6 @@ struct Columns<T, false, ACT> {
             s2[e] = __ffma2_rn(d, d, s2[e]);
         }
     }
-    // The second pass's constants from the slab's (mean, rstd) of each group.
-    __device__ __forceinline__ void finish(const SlabArgs& g, const float2* slab, int64_t c0, int c,
-                                           float inv_d) {
-        float2 w[PAIRS], m[PAIRS];
-        load_channels<T>(g, g.a.w, c0 + c, 1.f, w);
-        load_channels<T>(g, g.a.b, c0 + c, 0.f, shift);
-        per_channel<T>(g, c, inv_d, [&](int k) { return slab[k].x; }, m);
-        per_channel<T>(g, c, inv_d, [&](int k) { return slab[k].y; }, scale);
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) {
-            scale[e] = __fmul2_rn(scale[e], w[e]);
-            shift[e] = __ffma2_rn(make_float2(-m[e].x, -m[e].y), scale[e], shift[e]);
-        }
-    }
     // act(x scale + shift), rounded once
     __device__ __forceinline__ uint4 apply(const uint4& v) const {
         float2 f[PAIRS];
@@ -293,19 +250,6 @@ struct Columns<T, true, ACT> {
     float2 p[PAIRS], q[PAIRS];
     float2 k2[PAIRS], k3[PAIRS], k4[PAIRS];
 
-    __device__ __forceinline__ void start(const SlabArgs& g, const float* mean_of,
-                                          const float* rstd_of, int64_t c0, int c, float inv_d) {
-        float2 w[PAIRS];
-        per_channel<T>(g, c, inv_d, [&](int k) { return rstd_of[k]; }, k1);
-        per_channel<T>(g, c, inv_d, [&](int k) { return -mean_of[k]; }, mean);
-        load_channels<T>(g, g.a.w, c0 + c, 1.f, w);
-        load_channels<T>(g, g.a.b, c0 + c, 0.f, b);
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) {
-            k1[e] = __fmul2_rn(k1[e], w[e]);
-            p[e] = q[e] = make_float2(0.f, 0.f);
-        }
-    }
     __device__ __forceinline__ void add(const uint4& x, const uint4& dy) {
         float2 c[PAIRS], d[PAIRS];
         Pack<T>::unpack2(x, c);
@@ -317,27 +261,6 @@ struct Columns<T, true, ACT> {
                 d[e] = __fmul2_rn(d[e], slope_pair<T, ACT>(__ffma2_rn(c[e], k1[e], b[e])));
             p[e] = __fadd2_rn(p[e], d[e]);
             q[e] = __ffma2_rn(d[e], c[e], q[e]);
-        }
-    }
-    // sum dz xhat, once the sum of dz (x - mean) is complete
-    __device__ __forceinline__ void scale_q(const SlabArgs& g, const float* rstd_of, int c, float inv_d) {
-        float2 r[PAIRS];
-        per_channel<T>(g, c, inv_d, [&](int k) { return rstd_of[k]; }, r);
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) q[e] = __fmul2_rn(q[e], r[e]);
-    }
-    // The second pass's constants; slab holds the means A and B of each group.
-    __device__ __forceinline__ void finish(const SlabArgs& g, const float* rstd_of,
-                                           const float2* slab, int c, float inv_d) {
-        float2 r[PAIRS], A[PAIRS], B[PAIRS];
-        per_channel<T>(g, c, inv_d, [&](int k) { return rstd_of[k]; }, r);
-        per_channel<T>(g, c, inv_d, [&](int k) { return -slab[k].x; }, A);
-        per_channel<T>(g, c, inv_d, [&](int k) { return -slab[k].y; }, B);
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) {
-            k2[e] = __ffma2_rn(mean[e], k1[e], b[e]);
-            k3[e] = __fmul2_rn(__fmul2_rn(B[e], r[e]), r[e]);
-            k4[e] = __ffma2_rn(mean[e], k3[e], __fmul2_rn(A[e], r[e]));
         }
     }
     // dx = rstd (dz w - A - xhat B), rounded once
@@ -355,97 +278,16 @@ struct Columns<T, true, ACT> {
     }
 };
 
-// Joins the block's sums: (mean, M2) per group into `mine`. Where there are
-// fewer groups than warps, g.join warps share a group's entries and add their
-// parts in order.
-template <typename T, int ACT>
-__device__ __forceinline__ void join_block(const SlabArgs& g, const Columns<T, false, ACT>& col,
-                                           float* sums, float* parts, float2* mine, int rows, int n,
-                                           int lane, int vec, float inv_d) {
-    constexpr int PAIRS = Pack<T>::PAIRS, VEC = Pack<T>::VEC;
-    float* means = sums;
-    float* m2s = sums + g.lanes * g.cw;
-    if (lane < g.lanes) {
-        const float inv_n = n > 0 ? 1.f / static_cast<float>(n) : 0.f;
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) {
-            const int at = lane * g.cw + vec * VEC + 2 * e;
-            // the mean's distance from the pivot, and the squares about the mean
-            const float2 d = __fmul2_rn(col.s1[e], f2_splat(inv_n));
-            *reinterpret_cast<float2*>(means + at) = __fadd2_rn(col.pivot[e], d);
-            *reinterpret_cast<float2*>(m2s + at) = sub2(col.s2[e], __fmul2_rn(col.s1[e], d));
-        }
-    }
+// Sums of a block's channels over its lanes: two values a channel in `sums`
+// ([2][lanes][cw]), added into the first lane's rows. g.join threads share a
+// channel's lanes (part j adds rows j, j + share, ... into row j), then part 0
+// adds the parts.
+__device__ __forceinline__ void sum_lanes(const SlabArgs& g, float* sums) {
+    const int share = min(g.lanes, g.join), columns = 2 * g.cw;
     __syncthreads();
-    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
-    const int entries = g.lanes * g.D;
-    const int each = rows / g.lanes, more = rows - each * g.lanes;  // a lane's positions
-    const float inv_count = 1.f / (static_cast<float>(rows) * static_cast<float>(g.D));
-    const int share = g.join, teams = warps / share, part = warp % share;
-    const int first = part * 32 + l, step = share * 32;
-    for (int k0 = 0; k0 < g.gw; k0 += teams) {
-        const int k = k0 + warp / share;
-        const bool live = warp < teams * share && k < g.gw;
-        float s = 0.f;
-        if (live)
-            for (int i = first; i < entries; i += step) {
-                const int r = quotient(i, inv_d);
-                s = fmaf(static_cast<float>(each + (r < more)),
-                         means[r * g.cw + k * g.D + (i - r * g.D)], s);
-            }
-        s = group_allreduce<32>(s);
-        if (share > 1) {
-            if (l == 0) parts[warp] = s;
-            __syncthreads();
-            s = 0.f;
-            for (int j = 0; j < share; ++j) s += parts[warp - part + j];
-        }
-        const float mean = rows > 0 ? s * inv_count : 0.f;
-        float m2 = 0.f;
-        if (live)
-            for (int i = first; i < entries; i += step) {
-                const int r = quotient(i, inv_d);
-                const int at = r * g.cw + k * g.D + (i - r * g.D);
-                const float c = static_cast<float>(each + (r < more)), d = means[at] - mean;
-                m2 += fmaf(c * d, d, c > 0.f ? m2s[at] : 0.f);
-            }
-        m2 = group_allreduce<32>(m2);
-        if (share > 1) {
-            if (l == 0) parts[kMaxThreads / 32 + warp] = m2;
-            __syncthreads();
-            m2 = 0.f;
-            for (int j = 0; j < share; ++j) m2 += parts[kMaxThreads / 32 + warp - part + j];
-        }
-        if (live && part == 0 && l == 0) mine[k] = make_float2(mean, m2);
-    }
-}
-
-// Joins the block's sums: per channel over its lanes (in place, into the first
-// lane's row of `sums`: P, and Q behind it), then (sum w P, sum w Q) per group
-// into `mine`. Where there are fewer channels than threads, several threads
-// share a channel's lanes.
-template <typename T, int ACT>
-__device__ __forceinline__ void join_block(const SlabArgs& g, const Columns<T, true, ACT>& col,
-                                           float* sums, float2* mine, int lane, int vec,
-                                           int64_t c0) {
-    constexpr int PAIRS = Pack<T>::PAIRS, VEC = Pack<T>::VEC;
-    float* ps = sums;
-    float* qs = sums + g.lanes * g.cw;
-    if (lane < g.lanes) {
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) {
-            const int at = lane * g.cw + vec * VEC + 2 * e;
-            *reinterpret_cast<float2*>(ps + at) = col.p[e];
-            *reinterpret_cast<float2*>(qs + at) = col.q[e];
-        }
-    }
-    __syncthreads();
-    // part j of a channel adds the rows j, j + share, ... into row j, then part
-    // 0 the parts' rows
-    const int share = min(g.lanes, g.join);
-    for (int i = threadIdx.x; i < 2 * g.cw * share; i += blockDim.x) {
-        const int j = i / (2 * g.cw), c = i - j * 2 * g.cw;
-        float* at = (c < g.cw ? ps + c : qs + (c - g.cw)) + j * g.cw;
+    for (int i = threadIdx.x; i < columns * share; i += blockDim.x) {
+        const int j = i / columns, c = i - j * columns;
+        float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw) + j * g.cw;
         float s = 0.f;
 #pragma unroll 8
         for (int r = j; r < g.lanes; r += share) s += at[(r - j) * g.cw];
@@ -453,48 +295,214 @@ __device__ __forceinline__ void join_block(const SlabArgs& g, const Columns<T, t
     }
     __syncthreads();
     if (share > 1) {
-        for (int c = threadIdx.x; c < 2 * g.cw; c += blockDim.x) {
-            float* at = c < g.cw ? ps + c : qs + (c - g.cw);
+        for (int c = threadIdx.x; c < columns; c += blockDim.x) {
+            float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw);
             float s = 0.f;
+#pragma unroll 4
             for (int j = 0; j < share; ++j) s += at[j * g.cw];
             at[0] = s;
         }
         __syncthreads();
     }
-    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
-    for (int k = warp; k < g.gw; k += warps) {
-        float sp = 0.f, sq = 0.f;
-        for (int i = l; i < g.D; i += 32) {
-            const int c = k * g.D + i;
-            float w = 1.f;
-            if (g.a.w != nullptr)
-                w = g.a.w_f32 ? static_cast<const float*>(g.a.w)[c0 + c]
-                              : to_f32(static_cast<const T*>(g.a.w)[c0 + c]);
-            sp = fmaf(w, ps[c], sp);
-            sq = fmaf(w, qs[c], sq);
+}
+
+// A thread's place in its block, the same in both families.
+struct Seat {
+    int lane, vec, c;   // its lane of positions, its vector, its first channel
+    bool active;
+    int warps, warp, l;
+    float inv_d;
+    __device__ __forceinline__ Seat(const SlabArgs& g, int vec_elems) {
+        lane = static_cast<int>(threadIdx.x) / g.nvec;
+        vec = static_cast<int>(threadIdx.x) - lane * g.nvec;
+        c = vec * vec_elems;
+        active = lane < g.lanes;
+        warps = blockDim.x / 32;
+        warp = threadIdx.x / 32;
+        l = threadIdx.x % 32;
+        inv_d = 1.f / static_cast<float>(g.D);
+    }
+    __device__ __forceinline__ int positions(const SlabArgs& g, int rows) const {
+        return active && rows > lane ? (rows - lane - 1) / g.lanes + 1 : 0;
+    }
+};
+
+// A slab's channels in shared memory ([4][cw]): -mean, rstd w, b and rstd, or w
+// in the second row and b in the third. Thread i keeps channel i.
+template <typename T, bool BWD>
+__device__ __forceinline__ void load_channels(const SlabArgs& g, const Seat& s, float* chan, int c0,
+                                              int64_t group0) {
+    for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
+        const float w = channel<T>(g, g.a.w, c0 + i, 1.f), b = channel<T>(g, g.a.b, c0 + i, 0.f);
+        if constexpr (BWD) {
+            const int k = quotient(i, s.inv_d);
+            const float r = g.a.rstd[group0 + k], m = g.a.mean[group0 + k];
+            chan[i] = -m;
+            chan[g.cw + i] = r * w;
+            chan[3 * g.cw + i] = r;
+        } else {
+            chan[g.cw + i] = w;
         }
-        sp = group_allreduce<32>(sp);
-        sq = group_allreduce<32>(sq);
-        if (l == 0) mine[k] = make_float2(sp, sq);
+        chan[2 * g.cw + i] = b;
     }
 }
 
-// The statistics of (mean, M2) results with their counts, in rank order.
-struct Joined {
-    float mean, m2;
-};
-template <typename Get, typename Count>
-__device__ __forceinline__ Joined join_means(int n, float total, Get get, Count count) {
-    float s = 0.f;
-    for (int k = 0; k < n; ++k) s = fmaf(count(k), get(k).x, s);
-    const float mean = s / total;
-    float m2 = 0.f;
-    for (int k = 0; k < n; ++k) {
-        const float2 v = get(k);
-        const float d = v.x - mean;
-        m2 += fmaf(count(k) * d, d, v.y);
+// The first pass's constants of a thread's channels (backward), and its sums.
+template <typename T, int ACT>
+__device__ __forceinline__ void start(Columns<T, false, ACT>& col, const SlabArgs&, const Seat&, const float*) {
+    col.start(make_uint4(0, 0, 0, 0));
+}
+template <typename T, int ACT>
+__device__ __forceinline__ void start(Columns<T, true, ACT>& col, const SlabArgs& g, const Seat& s,
+                                      const float* chan) {
+    if (s.active) {
+        read_channels<T>(chan + s.c, col.mean);
+        read_channels<T>(chan + g.cw + s.c, col.k1);
+        read_channels<T>(chan + 2 * g.cw + s.c, col.b);
     }
-    return {mean, m2};
+#pragma unroll
+    for (int e = 0; e < Pack<T>::PAIRS; ++e) col.p[e] = col.q[e] = make_float2(0.f, 0.f);
+}
+
+// Joins the block's first pass: emit(k, (mean, M2)) for each group of channels.
+// Channel means over the lanes first, then squares about them, then groups.
+template <typename T, int ACT, typename Emit>
+__device__ __forceinline__ void join(const Columns<T, false, ACT>& col, const SlabArgs& g, const Seat& s,
+                                     float* sums, const float*, int rows, int n, Emit emit) {
+    constexpr int PAIRS = Pack<T>::PAIRS;
+    const float fn = static_cast<float>(n), inv_n = n > 0 ? 1.f / fn : 0.f;
+    const float frows = static_cast<float>(rows), inv_rows = 1.f / fmaxf(frows, 1.f);
+    float2 u[PAIRS], v[PAIRS];
+    if (s.active) {
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            u[e] = __ffma2_rn(col.pivot[e], f2_splat(fn), col.s1[e]);
+            v[e] = make_float2(0.f, 0.f);
+        }
+        write_channels<T>(sums + s.lane * g.cw + s.c, u);
+        write_channels<T>(sums + (g.lanes + s.lane) * g.cw + s.c, v);
+    }
+    sum_lanes(g, sums);
+    if (s.active) {
+        read_channels<T>(sums + s.c, u);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            u[e] = __fmul2_rn(u[e], f2_splat(inv_rows));
+            // squares of the thread's values about the channel's mean
+            const float2 d = __fmul2_rn(col.s1[e], f2_splat(inv_n));
+            const float2 off = sub2(__fadd2_rn(col.pivot[e], d), u[e]);
+            v[e] = sub2(col.s2[e], __fmul2_rn(col.s1[e], d));
+            v[e] = __ffma2_rn(__fmul2_rn(off, off), f2_splat(fn), v[e]);
+            if (n == 0) v[e] = make_float2(0.f, 0.f);
+        }
+    }
+    __syncthreads();
+    if (s.active) {
+        // the other half carries the means through, in the first lane's row
+        write_channels<T>(sums + s.lane * g.cw + s.c, v);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) u[e] = s.lane == 0 ? u[e] : make_float2(0.f, 0.f);
+        write_channels<T>(sums + (g.lanes + s.lane) * g.cw + s.c, u);
+    }
+    sum_lanes(g, sums);
+    const float* means = sums + g.lanes * g.cw;
+    for (int k = s.warp; k < g.gw; k += s.warps) {
+        float t = 0.f;
+        for (int i = s.l; i < g.D; i += 32) t += means[k * g.D + i];
+        const float m = group_allreduce<32>(t) * s.inv_d;
+        float m2 = 0.f;
+        for (int i = s.l; i < g.D; i += 32) {
+            const float d = means[k * g.D + i] - m;
+            m2 += fmaf(frows * d, d, sums[k * g.D + i]);
+        }
+        m2 = group_allreduce<32>(m2);
+        if (s.l == 0) emit(k, make_float2(m, m2));
+    }
+}
+// The backward's: emit(k, (rstd sum w dz, sum w dz xhat)), which sums of P and
+// of Q = sum dz (x - mean) weighted by k1 = rstd w are. The channels' sums stay
+// in the first lane's rows of `sums`: P, and Q behind all lanes of P.
+template <typename T, int ACT, typename Emit>
+__device__ __forceinline__ void join(const Columns<T, true, ACT>& col, const SlabArgs& g, const Seat& s,
+                                     float* sums, const float* chan, int, int, Emit emit) {
+    if (s.active) {
+        write_channels<T>(sums + s.lane * g.cw + s.c, col.p);
+        write_channels<T>(sums + (g.lanes + s.lane) * g.cw + s.c, col.q);
+    }
+    sum_lanes(g, sums);
+    const float* ps = sums;
+    const float* qs = sums + g.lanes * g.cw;
+    for (int k = s.warp; k < g.gw; k += s.warps) {
+        float sp = 0.f, sq = 0.f;
+        for (int i = s.l; i < g.D; i += 32) {
+            const float k1 = chan[g.cw + k * g.D + i];
+            sp = fmaf(k1, ps[k * g.D + i], sp);
+            sq = fmaf(k1, qs[k * g.D + i], sq);
+        }
+        sp = group_allreduce<32>(sp);
+        sq = group_allreduce<32>(sq);
+        if (s.l == 0) emit(k, make_float2(sp, sq));
+    }
+}
+
+// The slab's result of a group from NP results a lane with their counts of
+// values (0: none there), by a fixed tree: (mean, rstd), or the backward's two
+// sums as means.
+template <bool BWD, int NP>
+__device__ __forceinline__ float2 combine(const float2 (&t)[NP], const float (&count)[NP], float inv_count,
+                                          float eps) {
+    float2 v = make_float2(0.f, 0.f);
+    if constexpr (BWD) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v = __fadd2_rn(v, t[i]);
+        v.x = group_allreduce<32>(v.x) * inv_count;
+        v.y = group_allreduce<32>(v.y) * inv_count;
+    } else {
+        // mean = sum n m / n, M2 = sum M2 + n (m - mean)^2
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v.x = fmaf(count[i], t[i].x, v.x);
+        v.x = group_allreduce<32>(v.x) * inv_count;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const float d = t[i].x - v.x;
+            v.y += fmaf(count[i] * d, d, t[i].y);
+        }
+        v.y = rsqrtf(group_allreduce<32>(v.y) * inv_count + eps);
+    }
+    return v;
+}
+
+// The second pass's constants from the slab's results, in the channels' place,
+// and a thread's own. Every thread has written `slab` and is done with `chan`.
+template <typename T, bool BWD, int ACT>
+__device__ __forceinline__ void finish(Columns<T, BWD, ACT>& col, const SlabArgs& g, const Seat& s,
+                                       float* chan, const float2* slab) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
+        const float2 v = slab[quotient(i, s.inv_d)];
+        if constexpr (BWD) {
+            const float m = chan[i], r = chan[3 * g.cw + i];
+            const float k3 = -v.y * r * r;
+            chan[2 * g.cw + i] = fmaf(m, chan[g.cw + i], chan[2 * g.cw + i]);
+            chan[i] = k3;
+            chan[3 * g.cw + i] = fmaf(m, k3, -v.x);
+        } else {
+            const float scale = v.y * chan[g.cw + i];
+            chan[g.cw + i] = scale;
+            chan[2 * g.cw + i] = fmaf(-v.x, scale, chan[2 * g.cw + i]);
+        }
+    }
+    __syncthreads();
+    if (!s.active) return;
+    if constexpr (BWD) {
+        read_channels<T>(chan + s.c, col.k3);
+        read_channels<T>(chan + g.cw + s.c, col.k1);
+        read_channels<T>(chan + 2 * g.cw + s.c, col.k2);
+        read_channels<T>(chan + 3 * g.cw + s.c, col.k4);
+    } else {
+        read_channels<T>(chan + g.cw + s.c, col.scale);
+        read_channels<T>(chan + 2 * g.cw + s.c, col.shift);
+    }
 }
 
 // Resident: a thread's way through its positions. Copies run kDepth positions
@@ -522,17 +530,16 @@ struct Feed {
         }
         copies_commit();
     }
+    // the first kDepth positions' copies
+    __device__ __forceinline__ void prepare(int* status) {
+#pragma unroll
+        for (int i = 0; i < kDepth; i += kGroup) issue(slots + i * TENSORS * pitch, n - i, status);
+    }
     // visit(i, x vector, dy vector) for every position in order
     template <typename Visit>
     __device__ __forceinline__ void run(int* status, Visit visit) {
         const uint32_t group = kGroup * TENSORS * pitch;
-        uint32_t ahead = slots;
-#pragma unroll
-        for (int i = 0; i < kDepth; i += kGroup) {
-            issue(ahead, n - i, status);
-            ahead += group;
-        }
-        uint32_t at = slots;
+        uint32_t at = slots, ahead = slots + kDepth * TENSORS * pitch;
 #pragma unroll 1
         for (int i = 0; i < n; i += kGroup) {
             copies_wait<kDepth / kGroup - 1>();
@@ -559,99 +566,82 @@ struct Feed {
 // Both passes over a slab that its cluster keeps.
 template <typename T, bool BWD, int ACT>
 __global__ void __launch_bounds__(kMaxThreads) gn_resident_kernel(const __grid_constant__ SlabArgs g) {
-    constexpr int VEC = Pack<T>::VEC;
     const Place at = place_of(g);
-    const int lane = static_cast<int>(threadIdx.x) / g.nvec;
-    const int vec = static_cast<int>(threadIdx.x) - lane * g.nvec;
-    const bool active = lane < g.lanes;
-    const float inv_d = 1.f / static_cast<float>(g.D);
+    const Seat s(g, Pack<T>::VEC);
+    // shared memory: the threads' sums [2][lanes][cw], the channels' constants
+    // [4][cw], the block's and the slab's results of each group, the slots
     float* sums = reinterpret_cast<float*>(rmsn_dynamic_smem);
-    float2* mine = reinterpret_cast<float2*>(sums + sums_floats(g.lanes, g.cw));
+    float* chan = sums + 2 * g.lanes * g.cw;
+    float2* mine = reinterpret_cast<float2*>(chan + 4 * g.cw);
     float2* slab = mine + g.gw;
-    float* parts = reinterpret_cast<float*>(slab + g.gw);
-    uint4* keep = reinterpret_cast<uint4*>(parts + kJoinFloats);
-    const int slots = g.lanes * g.nvec;  // a pass of the block over `lanes` positions
-    const int rows = at.rows;
-    const int64_t c0 = static_cast<int64_t>(at.split) * g.cw;
-    const int c = vec * VEC;
-    const int64_t base = (at.sample * g.a.S + at.r0 + lane) * g.a.C + c0 + c;
-    const int n = active && rows > lane ? (rows - lane - 1) / g.lanes + 1 : 0;
+    uint4* keep = reinterpret_cast<uint4*>(slab + g.gw);
+    const int c0 = at.split * g.cw, n = s.positions(g, at.rows);
+    const int64_t base = (at.sample * g.a.S + at.r0 + s.lane) * g.a.C + c0 + s.c;
+    const int64_t group0 = at.sample * g.a.G + at.split * g.gw;
     Feed<T, BWD> feed;
     feed.x = static_cast<const T*>(g.a.x) + base;
     feed.dy = BWD ? static_cast<const T*>(g.a.dy) + base : nullptr;
     feed.step = static_cast<int64_t>(g.lanes) * g.a.C;
     feed.slots = smem_u32(keep + threadIdx.x);
-    feed.pitch = static_cast<uint32_t>(slots) * 16u;
+    feed.pitch = static_cast<uint32_t>(g.lanes * g.nvec) * 16u;
     feed.n = n;
-    [[maybe_unused]] const uint32_t group_slots = feed.pitch * Feed<T, BWD>::TENSORS;
-    [[maybe_unused]] const float* rstd_of =
-        BWD ? g.a.rstd + at.sample * g.a.G + at.split * g.gw : nullptr;
     Columns<T, BWD, ACT> col;
     wait_for_prerequisite_grid();  // no global access before this
 
-    if constexpr (BWD) {
-        if (active)
-            col.start(g, g.a.mean + at.sample * g.a.G + at.split * g.gw, rstd_of, c0, c, inv_d);
-        feed.run(g.a.status, [&](int, const uint4& x, const uint4& dy) { col.add(x, dy); });
-        if (active) col.scale_q(g, rstd_of, c, inv_d);
-    } else {
-        col.start(make_uint4(0, 0, 0, 0));
-        feed.run(g.a.status, [&](int i, const uint4& x, const uint4&) {
+    feed.prepare(g.a.status);
+    load_channels<T, BWD>(g, s, chan, c0, group0);
+    __syncthreads();
+    start(col, g, s, chan);
+    feed.run(g.a.status, [&](int i, const uint4& x, const uint4& dy) {
+        if constexpr (BWD) {
+            col.add(x, dy);
+        } else {
             if (i == 0) col.start(x);
             col.add(x);
-        });
-    }
-    if constexpr (BWD) join_block<T>(g, col, sums, mine, lane, vec, c0);
-    else join_block<T>(g, col, sums, parts, mine, rows, n, lane, vec, inv_d);
+        }
+    });
+    join(col, g, s, sums, chan, at.rows, n, [&](int k, float2 v) { mine[k] = v; });
 
-    // the cluster's blocks meet
+    // the cluster's blocks meet; lane r of a warp reads block r's result
     __syncwarp();
     if (g.cluster > 1) cluster_sync_all();
     else __syncthreads();
-    for (int k = threadIdx.x; k < g.gw; k += blockDim.x) {
-        float2 v = make_float2(0.f, 0.f);
-        if constexpr (BWD) {
-            for (int r = 0; r < g.cluster; ++r) {
-                const float2 t = g.cluster > 1 ? ld_cluster_f32x2(mine + k, r) : mine[k];
-                v = __fadd2_rn(v, t);
-            }
-        } else {
-            const float d = static_cast<float>(g.D);
-            const Joined j = join_means(
-                g.cluster, part_count(g, 0, g.cluster) * d,
-                [&](int r) { return g.cluster > 1 ? ld_cluster_f32x2(mine + k, r) : mine[k]; },
-                [&](int r) { return part_count(g, r, 1) * d; });
-            v = make_float2(j.mean, j.m2);
+    const float inv_count = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
+    const float count[1] = {s.l < g.cluster ? static_cast<float>(g.part_rows + (s.l < g.part_more ? 1 : 0)) *
+                                                  static_cast<float>(g.D)
+                                            : 0.f};
+    for (int k = s.warp; k < g.gw; k += s.warps) {
+        float2 t[1] = {make_float2(0.f, 0.f)};
+        if (g.cluster > 1) {
+            if (s.l < g.cluster) t[0] = ld_cluster_f32x2(mine + k, s.l);
+        } else if (s.l == 0) {
+            t[0] = mine[k];
         }
-        const float inv = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
-        if constexpr (BWD) {
-            slab[k] = make_float2(v.x * inv, v.y * inv);
-        } else {
-            v.y = rsqrtf(v.y * inv + g.a.eps);
+        __syncwarp();
+        const float2 v = combine<BWD>(t, count, inv_count, g.a.eps);
+        if (s.l == 0) {
             slab[k] = v;
-            if (at.rank == 0) {
-                const int64_t o = at.sample * g.a.G + at.split * g.gw + k;
-                g.a.mean[o] = v.x;
-                g.a.rstd[o] = v.y;
+            if (!BWD && at.rank == 0) {
+                g.a.mean[group0 + k] = v.x;
+                g.a.rstd[group0 + k] = v.y;
             }
         }
     }
     if constexpr (BWD) {
         // each block adds its share of the cluster's channel sums
         if (g.a.dw != nullptr) {
-            const int lo = static_cast<int>(static_cast<int64_t>(2 * g.cw) * at.rank / g.cluster);
-            const int hi = static_cast<int>(static_cast<int64_t>(2 * g.cw) * (at.rank + 1) / g.cluster);
+            const int lo = 2 * g.cw * at.rank / g.cluster, hi = 2 * g.cw * (at.rank + 1) / g.cluster;
             for (int i = lo + threadIdx.x; i < hi; i += blockDim.x) {
                 const bool q = i >= g.cw;
                 const int c = q ? i - g.cw : i;
                 const float* src = sums + (q ? g.lanes * g.cw : 0) + c;
-                float s = 0.f;
-                for (int r = 0; r < g.cluster; ++r) s += g.cluster > 1 ? ld_cluster_f32(src, r) : *src;
-                float* d;
-                if (g.rows == nullptr) d = (q ? g.a.dw : g.a.db) + c0 + c;
-                else
-                    d = g.rows + (at.sample) * 2 * g.a.C + (q ? 0 : g.a.C) + c0 + c;
-                *d = s;
+                float t = 0.f;
+#pragma unroll 4
+                for (int r = 0; r < g.cluster; ++r) t += g.cluster > 1 ? ld_cluster_f32(src, r) : *src;
+                if (q) t *= chan[3 * g.cw + c];
+                float* d = g.rows == nullptr ? (q ? g.a.dw : g.a.db)
+                                             : g.rows + at.sample * 2 * g.a.C + (q ? 0 : g.a.C);
+                d[c0 + c] = t;
             }
         }
     }
@@ -659,22 +649,18 @@ __global__ void __launch_bounds__(kMaxThreads) gn_resident_kernel(const __grid_c
     if (g.cluster > 1) cluster_arrive_relaxed();  // this block is done reading its peers
     allow_dependent_launch();
 
-    __syncthreads();
-    if (n > 0) {
-        if constexpr (BWD) col.finish(g, rstd_of, slab, c, inv_d);
-        else col.finish(g, slab, c0, c, inv_d);
-        T* out = static_cast<T*>(g.a.out) + base;
-        [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(sizeof(T));
-        uint32_t slot = feed.slots;
+    finish(col, g, s, chan, slab);
+    T* out = static_cast<T*>(g.a.out) + base;
+    [[maybe_unused]] const int64_t bytes = g.a.B * g.a.S * g.a.C * static_cast<int64_t>(sizeof(T));
+    uint32_t slot = feed.slots;
 #pragma unroll 2
-        for (int i = 0; i < n; ++i) {
-            uint4 v;
-            if constexpr (BWD) v = col.apply(ld_slot(slot), ld_slot(slot + feed.pitch));
-            else v = col.apply(ld_slot(slot));
-            slot += group_slots;
-            if (RMSN_OK(span_in(out, 16, g.a.out, bytes), g.a.status)) st_global_16(out, v);
-            out += feed.step;
-        }
+    for (int i = 0; i < n; ++i) {
+        uint4 v;
+        if constexpr (BWD) v = col.apply(ld_slot(slot), ld_slot(slot + feed.pitch));
+        else v = col.apply(ld_slot(slot));
+        slot += feed.pitch * Feed<T, BWD>::TENSORS;
+        if (RMSN_OK(span_in(out, 16, g.a.out, bytes), g.a.status)) st_global_16(out, v);
+        out += feed.step;
     }
     __syncwarp();
     if (g.cluster > 1) cluster_wait();  // no block leaves while a peer reads it
@@ -757,34 +743,6 @@ struct Copies {
     }
 };
 
-// Sums of a block's channels over its lanes: two values a channel in `sums`
-// ([2][lanes][cw]), added into the first lane's rows. g.join threads share a
-// channel's lanes (part j adds rows j, j + share, ... into row j), then part 0
-// adds the parts.
-__device__ __forceinline__ void sum_lanes(const SlabArgs& g, float* sums) {
-    const int share = min(g.lanes, g.join), columns = 2 * g.cw;
-    __syncthreads();
-    for (int i = threadIdx.x; i < columns * share; i += blockDim.x) {
-        const int j = i / columns, c = i - j * columns;
-        float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw) + j * g.cw;
-        float s = 0.f;
-#pragma unroll 8
-        for (int r = j; r < g.lanes; r += share) s += at[(r - j) * g.cw];
-        at[0] = s;
-    }
-    __syncthreads();
-    if (share > 1) {
-        for (int c = threadIdx.x; c < columns; c += blockDim.x) {
-            float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw);
-            float s = 0.f;
-#pragma unroll 4
-            for (int j = 0; j < share; ++j) s += at[j * g.cw];
-            at[0] = s;
-        }
-        __syncthreads();
-    }
-}
-
 // Waits until every block of a slab has published its results, for a limited
 // time; a wait that runs out is reported.
 __device__ __forceinline__ bool all_arrived(const SlabArgs& g, int64_t slab) {
@@ -802,21 +760,16 @@ __device__ __forceinline__ bool all_arrived(const SlabArgs& g, int64_t slab) {
 
 template <typename T, bool BWD, int ACT>
 __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __grid_constant__ SlabArgs g) {
-    constexpr int VEC = Pack<T>::VEC, PAIRS = Pack<T>::PAIRS, SIZE = sizeof(T);
+    constexpr int SIZE = sizeof(T);
     using Ring = Copies<T, BWD>;
     using Pass = typename Ring::Pass;
-    const int lane = static_cast<int>(threadIdx.x) / g.nvec;
-    const int vec = static_cast<int>(threadIdx.x) - lane * g.nvec;
-    const bool active = lane < g.lanes;
-    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, l = threadIdx.x % 32;
-    const float inv_d = 1.f / static_cast<float>(g.D), fd = static_cast<float>(g.D);
-    const float inv_count = 1.f / (static_cast<float>(g.a.S) * fd);
+    const Seat s(g, Pack<T>::VEC);
+    const float fd = static_cast<float>(g.D), inv_count = 1.f / (static_cast<float>(g.a.S) * fd);
     const int team = static_cast<int>(blockIdx.x) / g.parts;
     const int part = static_cast<int>(blockIdx.x) - team * g.parts;
     const int64_t r0 = part_begin(g, part);
     const int rows = g.part_rows + (part < g.part_more ? 1 : 0);
-    const int n_all = active && rows > lane ? (rows - lane - 1) / g.lanes + 1 : 0;
-    const int c = vec * VEC;
+    const int n_all = s.positions(g, rows);
     // shared memory: the ring, the threads' sums [2][lanes][cw], the channels'
     // constants [4][cw], the groups' results
     float* sums = reinterpret_cast<float*>(rmsn_dynamic_smem + Ring::DEPTH * Ring::GROUP);
@@ -828,7 +781,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
     ring.drop = l2_policy_evict_first();
     ring.status = g.a.status;
     const uint32_t pitch = static_cast<uint32_t>(g.a.C) * SIZE;  // bytes of a position
-    const uint32_t own = pitch * lane + c * SIZE;
+    const uint32_t own = pitch * s.lane + s.c * SIZE;
     auto pass_of = [&](int round, bool second) {
         Pass p{};
         const int64_t i = static_cast<int64_t>(round) * g.together + team;
@@ -870,115 +823,32 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
         const bool live = sample < g.a.B;
         const int n = live ? n_all : 0, c0 = split * g.cw;
         const int64_t group0 = sample * g.a.G + split * g.gw;
-        if (live)
-            for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
-                const float w = channel<T>(g, g.a.w, c0 + i, 1.f), b = channel<T>(g, g.a.b, c0 + i, 0.f);
-                if constexpr (BWD) {
-                    const int k = quotient(i, inv_d);
-                    const float r = g.a.rstd[group0 + k];
-                    chan[i] = -g.a.mean[group0 + k];
-                    chan[g.cw + i] = r * w;
-                    chan[3 * g.cw + i] = r;
-                } else {
-                    chan[g.cw + i] = w;
-                }
-                chan[2 * g.cw + i] = b;
-            }
+        if (live) load_channels<T, BWD>(g, s, chan, c0, group0);
+        __syncthreads();
         Columns<T, BWD, ACT> col;
-        if constexpr (BWD) {
-            __syncthreads();
-            if (active) {
-                read_channels<T>(chan + c, col.mean);
-                read_channels<T>(chan + g.cw + c, col.k1);
-                read_channels<T>(chan + 2 * g.cw + c, col.b);
-            }
-#pragma unroll
-            for (int e = 0; e < PAIRS; ++e) col.p[e] = col.q[e] = make_float2(0.f, 0.f);
-            ring.run(pass, [&] { return pass_of(round, true); }, [&](const uint4& x, const uint4& dy) { col.add(x, dy); });
-            if (active) {
-                write_channels<T>(sums + lane * g.cw + c, col.p);
-                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, col.q);
-            }
-            sum_lanes(g, sums);
-            // with k1 = rstd w: sum k1 P = rstd sum w dz, sum k1 Q = sum w dz xhat
-            const float* ps = sums;
-            const float* qs = sums + g.lanes * g.cw;
-            for (int k = warp; k < g.gw; k += warps) {
-                float sp = 0.f, sq = 0.f;
-                for (int i = l; i < g.D; i += 32) {
-                    const float k1 = chan[g.cw + k * g.D + i];
-                    sp = fmaf(k1, ps[k * g.D + i], sp);
-                    sq = fmaf(k1, qs[k * g.D + i], sq);
-                }
-                sp = group_allreduce<32>(sp);
-                sq = group_allreduce<32>(sq);
-                if (l == 0 && live) g.stats[(slab_i * g.gw + k) * g.parts + part] = make_float2(sp, sq);
-            }
-            if (g.rows != nullptr && live) {
-                float* row = g.rows + (sample * g.parts + part) * 2 * g.a.C + c0;
-                for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
-                    row[i] = qs[i] * chan[3 * g.cw + i];
-                    row[g.a.C + i] = ps[i];
-                }
-            }
-        } else {
-            col.start(make_uint4(0, 0, 0, 0));
-            bool first = true;
-            ring.run(pass, [&] { return pass_of(round, true); }, [&](const uint4& x, const uint4&) {
+        start(col, g, s, chan);
+        [[maybe_unused]] bool first = true;
+        ring.run(pass, [&] { return pass_of(round, true); }, [&](const uint4& x, const uint4& dy) {
+            if constexpr (BWD) {
+                col.add(x, dy);
+            } else {
                 if (first) {
                     col.start(x);
                     first = false;
                 }
                 col.add(x);
-            });
-            // channel means over the lanes, then squares about them, then groups
-            const float fn = static_cast<float>(n), inv_n = n > 0 ? 1.f / fn : 0.f;
-            const float frows = static_cast<float>(rows), inv_rows = 1.f / fmaxf(frows, 1.f);
-            float2 u[PAIRS], v[PAIRS];
-            if (active) {
-#pragma unroll
-                for (int e = 0; e < PAIRS; ++e) {
-                    u[e] = __ffma2_rn(col.pivot[e], f2_splat(fn), col.s1[e]);
-                    v[e] = make_float2(0.f, 0.f);
-                }
-                write_channels<T>(sums + lane * g.cw + c, u);
-                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, v);
             }
-            sum_lanes(g, sums);
-            if (active) {
-                read_channels<T>(sums + c, u);
-#pragma unroll
-                for (int e = 0; e < PAIRS; ++e) {
-                    u[e] = __fmul2_rn(u[e], f2_splat(inv_rows));
-                    // squares of the thread's values about the channel's mean
-                    const float2 d = __fmul2_rn(col.s1[e], f2_splat(inv_n));
-                    const float2 off = sub2(__fadd2_rn(col.pivot[e], d), u[e]);
-                    v[e] = sub2(col.s2[e], __fmul2_rn(col.s1[e], d));
-                    v[e] = __ffma2_rn(__fmul2_rn(off, off), f2_splat(fn), v[e]);
-                    if (n == 0) v[e] = make_float2(0.f, 0.f);
+        });
+        join(col, g, s, sums, chan, rows, n, [&](int k, float2 v) {
+            if (live) g.stats[(slab_i * g.gw + k) * g.parts + part] = v;
+        });
+        if constexpr (BWD) {
+            if (g.rows != nullptr && live) {
+                float* row = g.rows + (sample * g.parts + part) * 2 * g.a.C + c0;
+                for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
+                    row[i] = sums[g.lanes * g.cw + i] * chan[3 * g.cw + i];
+                    row[g.a.C + i] = sums[i];
                 }
-            }
-            __syncthreads();
-            if (active) {
-                // the other half carries the means through, in the first lane's row
-                write_channels<T>(sums + lane * g.cw + c, v);
-#pragma unroll
-                for (int e = 0; e < PAIRS; ++e) u[e] = lane == 0 ? u[e] : make_float2(0.f, 0.f);
-                write_channels<T>(sums + (g.lanes + lane) * g.cw + c, u);
-            }
-            sum_lanes(g, sums);
-            const float* means = sums + g.lanes * g.cw;
-            for (int k = warp; k < g.gw; k += warps) {
-                float s = 0.f;
-                for (int i = l; i < g.D; i += 32) s += means[k * g.D + i];
-                const float m = group_allreduce<32>(s) * inv_d;
-                float m2 = 0.f;
-                for (int i = l; i < g.D; i += 32) {
-                    const float d = means[k * g.D + i] - m;
-                    m2 += fmaf(frows * d, d, sums[k * g.D + i]);
-                }
-                m2 = group_allreduce<32>(m2);
-                if (l == 0 && live) g.stats[(slab_i * g.gw + k) * g.parts + part] = make_float2(m, m2);
             }
         }
         // count this block in, then wait for the slab's others
@@ -989,70 +859,28 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
             if (!failed) failed = !all_arrived(g, slab_i);  // later waits are not made
         }
         __syncthreads();
-        // the slab's means of each group: (mean, rstd), or rstd times the mean of
-        // dz w and the mean of dz w xhat. All of a lane's results are read at once.
-        for (int k = live ? warp : g.gw; k < g.gw; k += warps) {
+        // the slab's results; all that a lane adds are read at once
+        for (int k = live ? s.warp : g.gw; k < g.gw; k += s.warps) {
+            constexpr int NP = kStreamMaxParts / 32;
             const float2* from = g.stats + (slab_i * g.gw + k) * g.parts;
-            float2 t[kStreamMaxParts / 32];
+            float2 t[NP];
+            float count[NP];
 #pragma unroll
-            for (int i = 0; i < kStreamMaxParts / 32; ++i)
-                t[i] = l + 32 * i < g.parts ? __ldcg(from + l + 32 * i) : make_float2(0.f, 0.f);
-            float2 v = make_float2(0.f, 0.f);
-            if constexpr (BWD) {
-#pragma unroll
-                for (int i = 0; i < kStreamMaxParts / 32; ++i) v = __fadd2_rn(v, t[i]);
-                v.x = group_allreduce<32>(v.x) * inv_count;
-                v.y = group_allreduce<32>(v.y) * inv_count;
-            } else {
-                float count[kStreamMaxParts / 32];
-#pragma unroll
-                for (int i = 0; i < kStreamMaxParts / 32; ++i) {
-                    const int j = l + 32 * i;
-                    count[i] = j < g.parts ? static_cast<float>(g.part_rows + (j < g.part_more ? 1 : 0)) * fd : 0.f;
-                    v.x = fmaf(count[i], t[i].x, v.x);
-                }
-                v.x = group_allreduce<32>(v.x) * inv_count;
-#pragma unroll
-                for (int i = 0; i < kStreamMaxParts / 32; ++i) {
-                    const float d = t[i].x - v.x;
-                    v.y += fmaf(count[i] * d, d, t[i].y);
-                }
-                v.y = rsqrtf(group_allreduce<32>(v.y) * inv_count + g.a.eps);
-                if (part == 0 && l == 0) {
+            for (int i = 0; i < NP; ++i) {
+                const int j = s.l + 32 * i;
+                t[i] = j < g.parts ? __ldcg(from + j) : make_float2(0.f, 0.f);
+                count[i] = j < g.parts ? static_cast<float>(g.part_rows + (j < g.part_more ? 1 : 0)) * fd : 0.f;
+            }
+            const float2 v = combine<BWD>(t, count, inv_count, g.a.eps);
+            if (s.l == 0) {
+                slab[k] = v;
+                if (!BWD && part == 0) {
                     g.a.mean[group0 + k] = v.x;
                     g.a.rstd[group0 + k] = v.y;
                 }
             }
-            if (l == 0) slab[k] = v;
         }
-        __syncthreads();
-        if (live)
-            for (int i = threadIdx.x; i < g.cw; i += blockDim.x) {
-                const float2 v = slab[quotient(i, inv_d)];
-                if constexpr (BWD) {
-                    const float m = chan[i], r = chan[3 * g.cw + i];
-                    const float k3 = -v.y * r * r;
-                    chan[2 * g.cw + i] = fmaf(m, chan[g.cw + i], chan[2 * g.cw + i]);
-                    chan[i] = k3;
-                    chan[3 * g.cw + i] = fmaf(m, k3, -v.x);
-                } else {
-                    const float scale = v.y * chan[g.cw + i];
-                    chan[g.cw + i] = scale;
-                    chan[2 * g.cw + i] = fmaf(-v.x, scale, chan[2 * g.cw + i]);
-                }
-            }
-        __syncthreads();
-        if (active) {
-            if constexpr (BWD) {
-                read_channels<T>(chan + c, col.k3);
-                read_channels<T>(chan + g.cw + c, col.k1);
-                read_channels<T>(chan + 2 * g.cw + c, col.k2);
-                read_channels<T>(chan + 3 * g.cw + c, col.k4);
-            } else {
-                read_channels<T>(chan + g.cw + c, col.scale);
-                read_channels<T>(chan + 2 * g.cw + c, col.shift);
-            }
-        }
+        finish(col, g, s, chan, slab);
         // The second pass. dx may be the dy buffer: a position's copies are
         // waited for before this thread, and no other, writes it.
         const int64_t back = static_cast<int64_t>(pitch) * g.lanes;
