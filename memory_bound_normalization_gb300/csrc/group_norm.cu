@@ -82,9 +82,9 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     const int size = dtype_size(dtype), tensors = bwd ? 2 : 1;
     const int64_t row_bytes = static_cast<int64_t>(a.C) * size;
     double best_cost = 0;
-    // resident: microseconds a wave of blocks needs, by the slice a block keeps
-    // (44 KB/us is an SM's share of the DRAM rate, in and out), the blocks'
-    // meeting, and a fixed start; rows are split no finer than 128 bytes
+    // resident: microseconds that the waves of blocks need, by the slice a block
+    // keeps (44 KB/us is an SM's share of the DRAM rate, in and out), the blocks'
+    // meeting, and a fixed part; rows are split no finer than 128 bytes
     for (int splits = 1; splits <= a.G; splits *= 2) {
         if (a.G % splits) break;
         const int64_t wide = row_bytes / splits;
@@ -99,15 +99,19 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
             const int64_t slice = cdiv(rows, p.lanes) * p.lanes * wide * tensors;
             if (fixed + slice > kMaxSmem) continue;
             if (cluster > 1 && rows < p.lanes) break;
-            const int64_t blocks = a.B * splits * cluster;
-            if (blocks > INT32_MAX) break;
-            const double waves = static_cast<double>(cdiv(blocks, dev.sm_count));
-            const double cost = waves * (1.5 + (cluster > 8 ? 1.5 : cluster > 1 ? 1.0 : 0.0) +
-                                         slice * (bwd ? 1.5 : 2.0) / 44e3);
-            if (best.ok && cost >= best_cost) continue;
+            if (a.B * splits * cluster > INT32_MAX) break;
+            // how many run at once: clusters of 8 or 16 large blocks leave some
+            // SMs of a GPC unused, so that 16 clusters of 8 are two waves
             const int smem = static_cast<int>(fixed + slice);
-            if (resident_clusters(dev, kernel_for(dtype, bwd, a.act, SlabKind::kResident), p.threads, kMaxSmem, cluster) < 1)
-                continue;
+            const int at_once = resident_clusters(dev, kernel_for(dtype, bwd, a.act, SlabKind::kResident),
+                                                  p.threads, std::min(kMaxSmem, round_up(smem, 16 * 1024)),
+                                                  cluster);
+            if (at_once < 1) continue;
+            const double waves = static_cast<double>(cdiv(a.B * splits, at_once));
+            const double per_sm = std::max(1.0, static_cast<double>(at_once) * cluster / dev.sm_count);
+            const double cost = waves * (4.0 + (cluster > 8 ? 1.0 : cluster > 1 ? 0.5 : 0.0) +
+                                         per_sm * slice * (bwd ? 1.5 : 2.0) / 44e3);
+            if (best.ok && cost >= best_cost) continue;
             p.ok = p.resident = true;
             p.cluster = cluster;
             p.smem = smem;
