@@ -55,22 +55,18 @@ def _keep(key, made):
     return made
 
 
+_NOTHING = (None,)
+
+
 def _layout(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+    return _NOTHING if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _on_stream(stream):
-    """(the handle to run on, whether it is another stream than the current
-    one). The caching allocator's memory is ordered on the current stream, so a
-    call on another leaves its workspace to the library, which takes it in that
-    stream's order."""
-    here = _lib._stream(None)
-    if stream is None:
-        return here, False
+def _foreign(stream, here: int):
+    """(the handle to run on, whether it is another stream than the current one,
+    whose handle is `here`). The caching allocator's memory is ordered on the
+    current stream, so a call on another leaves its workspace to the library,
+    which takes it in that stream's order."""
     there = _lib._stream(stream)
     return there, there != here
 
@@ -123,25 +119,32 @@ def group_norm_forward(x, num_groups: int, weight=None, bias=None, eps: float = 
     channels_last memory format passes as x.permute(0, 2, 3, 1)."""
     import torch
 
-    key = ("gn", _layout(x), num_groups, _layout(weight), _layout(bias), activation)
-    size, code, act, need, dev, per_group = _KEPT.get(key) or _keep(
-        key, _group_norm_forward_layout(x, num_groups, weight, bias, activation))
-    if not _here(dev):
+    key = ("gn", num_groups, activation, *_layout(x), *_layout(weight), *_layout(bias))
+    kept = _KEPT.get(key)
+    if kept is None:
+        kept = _keep(key, _group_norm_forward_layout(x, num_groups, weight, bias, activation))
+    size, code, act, need, dev, per_group = kept
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return group_norm_forward(x, num_groups, weight, bias, eps, activation, stream)
+    handle, foreign = torch._C._cuda_getCurrentRawStream(dev), False
+    if stream is not None:
+        handle, foreign = _foreign(stream, handle)
     lib, where = _lib.load_library(), x.device
-    handle, foreign = _on_stream(stream)
     y = torch.empty_like(x)
     mean = torch.empty(per_group, dtype=torch.float32, device=where)
-    rstd = torch.empty(per_group, dtype=torch.float32, device=where)
-    args = (x.data_ptr(), _at(weight), _at(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            *size, eps, act, code)
+    rstd = torch.empty_like(mean)
+    w, b = (None, None) if weight is None else (weight.data_ptr(), bias.data_ptr())
     if foreign:
-        check(lib.rmsnorm_group_norm_fwd(*args, handle), "rmsnorm_group_norm_fwd")
+        st = lib.rmsnorm_group_norm_fwd(x.data_ptr(), w, b, y.data_ptr(), mean.data_ptr(),
+                                        rstd.data_ptr(), *size, eps, act, code, handle)
     else:
         ws = torch.empty(need, dtype=torch.uint8, device=where) if need else None
-        check(lib.rmsnorm_group_norm_fwd_ws(*args, _at(ws), need, handle),
-              "rmsnorm_group_norm_fwd_ws")
+        st = lib.rmsnorm_group_norm_fwd_ws(
+            x.data_ptr(), w, b, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), *size, eps, act,
+            code, ws.data_ptr() if need else None, need, handle)
+    if st:
+        check(st, "rmsnorm_group_norm_fwd")
     return y, mean, rstd
 
 
@@ -170,29 +173,38 @@ def group_norm_backward(x, num_groups: int, weight, bias, dy, mean, rstd,
     and rstd."""
     import torch
 
-    key = ("gnb", _layout(x), num_groups, _layout(weight), _layout(bias), _layout(dy),
-           _layout(mean), _layout(rstd), activation)
-    size, code, act, need, dev, per_channel = _KEPT.get(key) or _keep(
-        key, _group_norm_backward_layout(x, num_groups, weight, bias, dy, mean, rstd, activation))
-    if not _here(dev):
+    key = ("gnb", num_groups, activation, *_layout(x), *_layout(weight), *_layout(bias),
+           *_layout(dy), *_layout(mean), *_layout(rstd))
+    kept = _KEPT.get(key)
+    if kept is None:
+        kept = _keep(key, _group_norm_backward_layout(x, num_groups, weight, bias, dy, mean, rstd,
+                                                      activation))
+    size, code, act, need, dev, per_channel = kept
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return group_norm_backward(x, num_groups, weight, bias, dy, mean, rstd, activation,
                                        stream)
+    handle, foreign = torch._C._cuda_getCurrentRawStream(dev), False
+    if stream is not None:
+        handle, foreign = _foreign(stream, handle)
     lib, where = _lib.load_library(), x.device
-    handle, foreign = _on_stream(stream)
     dx = torch.empty_like(x)
-    dw = db = None
+    dw = db = w = b = pw = pb = None
     if weight is not None:
         dw = torch.empty(per_channel, dtype=torch.float32, device=where)
-        db = torch.empty(per_channel, dtype=torch.float32, device=where)
-    args = (x.data_ptr(), _at(weight), _at(bias), dy.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            dx.data_ptr(), _at(dw), _at(db), *size, act, code)
+        db = torch.empty_like(dw)
+        w, b, pw, pb = weight.data_ptr(), bias.data_ptr(), dw.data_ptr(), db.data_ptr()
     if foreign:
-        check(lib.rmsnorm_group_norm_bwd(*args, handle), "rmsnorm_group_norm_bwd")
+        st = lib.rmsnorm_group_norm_bwd(x.data_ptr(), w, b, dy.data_ptr(), mean.data_ptr(),
+                                        rstd.data_ptr(), dx.data_ptr(), pw, pb, *size, act, code,
+                                        handle)
     else:
         ws = torch.empty(need, dtype=torch.uint8, device=where) if need else None
-        check(lib.rmsnorm_group_norm_bwd_ws(*args, _at(ws), need, handle),
-              "rmsnorm_group_norm_bwd_ws")
+        st = lib.rmsnorm_group_norm_bwd_ws(
+            x.data_ptr(), w, b, dy.data_ptr(), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), pw,
+            pb, *size, act, code, ws.data_ptr() if need else None, need, handle)
+    if st:
+        check(st, "rmsnorm_group_norm_bwd")
     return dx, dw, db
 
 
@@ -303,21 +315,32 @@ def qk_rope_forward(q, k, wq, wk, positions, inv_freq, sections, interleaved: bo
 
     qo, ko = (None, None) if out is None else out
     sections = tuple(sections)
-    key = ("qk", _layout(q), _layout(k), _layout(wq), _layout(wk), _layout(positions),
-           _layout(inv_freq), sections, interleaved, adjacent, _layout(qo), _layout(ko))
-    desc, code, dev = _KEPT.get(key) or _keep(key, _rope_forward_layout(
-        q, k, wq, wk, positions, inv_freq, sections, interleaved, adjacent, qo, ko))
-    if not _here(dev):
+    key = ("qk", sections, interleaved, adjacent, *_layout(q), *_layout(k), *_layout(wq),
+           *_layout(wk), *_layout(positions), *_layout(inv_freq), *_layout(qo), *_layout(ko))
+    kept = _KEPT.get(key)
+    if kept is None:
+        kept = _keep(key, _rope_forward_layout(q, k, wq, wk, positions, inv_freq, sections,
+                                               interleaved, adjacent, qo, ko))
+    desc, code, dev = kept
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return qk_rope_forward(q, k, wq, wk, positions, inv_freq, sections, interleaved,
                                    adjacent, eps, out, stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _lib._stream(stream)
+    pk = pko = None
     if qo is None:
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        where = q.device
+        qo = torch.empty(q.shape, dtype=q.dtype, device=where)
         if k is not None:
-            ko = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    check(_lib.load_library().rmsnorm_qk_rope_fwd(
-        desc, q.data_ptr(), _at(k), _at(wq), _at(wk), positions.data_ptr(), inv_freq.data_ptr(),
-        qo.data_ptr(), _at(ko), eps, code, _lib._stream(stream)), "rmsnorm_qk_rope_fwd")
+            ko = torch.empty(k.shape, dtype=q.dtype, device=where)
+    if k is not None:
+        pk, pko = k.data_ptr(), ko.data_ptr()
+    st = _lib.load_library().rmsnorm_qk_rope_fwd(
+        desc, q.data_ptr(), pk, None if wq is None else wq.data_ptr(),
+        None if wk is None else wk.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+        qo.data_ptr(), pko, eps, code, handle)
+    if st:
+        check(st, "rmsnorm_qk_rope_fwd")
     return qo, ko
 
 
@@ -348,30 +371,43 @@ def qk_rope_backward(q, k, wq, wk, positions, inv_freq, sections, dq_out, dk_out
     import torch
 
     sections = tuple(sections)
-    key = ("qkb", _layout(q), _layout(k), _layout(wq), _layout(wk), _layout(positions),
-           _layout(inv_freq), sections, interleaved, adjacent, _layout(dq_out), _layout(dk_out))
-    desc, code, dev, need = _KEPT.get(key) or _keep(key, _rope_backward_layout(
-        q, k, wq, wk, positions, inv_freq, sections, interleaved, adjacent, dq_out, dk_out))
-    if not _here(dev):
+    key = ("qkb", sections, interleaved, adjacent, *_layout(q), *_layout(k), *_layout(wq),
+           *_layout(wk), *_layout(positions), *_layout(inv_freq), *_layout(dq_out),
+           *_layout(dk_out))
+    kept = _KEPT.get(key)
+    if kept is None:
+        kept = _keep(key, _rope_backward_layout(q, k, wq, wk, positions, inv_freq, sections,
+                                                interleaved, adjacent, dq_out, dk_out))
+    desc, code, dev, need = kept
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return qk_rope_backward(q, k, wq, wk, positions, inv_freq, sections, dq_out, dk_out,
                                     interleaved, adjacent, eps, stream)
-    lib, where = _lib.load_library(), q.device
-    handle, foreign = _on_stream(stream)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=where)
-    dk = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=where)
-    dwq = dwk = None
-    if wq is not None:
+    handle, foreign = torch._C._cuda_getCurrentRawStream(dev), False
+    if stream is not None:
+        handle, foreign = _foreign(stream, handle)
+    lib, where, dtype = _lib.load_library(), q.device, q.dtype
+    dq = torch.empty(q.shape, dtype=dtype, device=where)
+    dk = dwq = dwk = pk = pdko = pdk = pwq = pwk = pdwq = pdwk = None
+    if k is not None:
+        dk = torch.empty(k.shape, dtype=dtype, device=where)
+        pk, pdko, pdk = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
+    if need:
         dwq = torch.empty(wq.shape, dtype=torch.float32, device=where)
+        pwq, pdwq = wq.data_ptr(), dwq.data_ptr()
         if k is not None:
-            dwk = torch.empty(wq.shape, dtype=torch.float32, device=where)
-    args = (desc, q.data_ptr(), _at(k), _at(wq), _at(wk), positions.data_ptr(),
-            inv_freq.data_ptr(), dq_out.data_ptr(), _at(dk_out), dq.data_ptr(), _at(dk), _at(dwq),
-            _at(dwk), eps, code)
+            dwk = torch.empty_like(dwq)
+            pwk, pdwk = wk.data_ptr(), dwk.data_ptr()
     if foreign or not need:
-        check(lib.rmsnorm_qk_rope_bwd(*args, handle), "rmsnorm_qk_rope_bwd")
+        st = lib.rmsnorm_qk_rope_bwd(
+            desc, q.data_ptr(), pk, pwq, pwk, positions.data_ptr(), inv_freq.data_ptr(),
+            dq_out.data_ptr(), pdko, dq.data_ptr(), pdk, pdwq, pdwk, eps, code, handle)
     else:
         ws = torch.empty(need, dtype=torch.uint8, device=where)
-        check(lib.rmsnorm_qk_rope_bwd_ws(*args, ws.data_ptr(), need, handle),
-              "rmsnorm_qk_rope_bwd_ws")
+        st = lib.rmsnorm_qk_rope_bwd_ws(
+            desc, q.data_ptr(), pk, pwq, pwk, positions.data_ptr(), inv_freq.data_ptr(),
+            dq_out.data_ptr(), pdko, dq.data_ptr(), pdk, pdwq, pdwk, eps, code, ws.data_ptr(),
+            need, handle)
+    if st:
+        check(st, "rmsnorm_qk_rope_bwd")
     return dq, dk, dwq, dwk
