@@ -171,7 +171,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
             return _lib
         checked = checked_variant()
         path = _build.lib_path(checked)
-        if build_if_missing and (not os.path.exists(path) or _build.is_stale(checked)):
+        if build_if_missing and (not os.path.exists(path) or _build.is_stale(checked) or
+                                 _build.binding_is_stale()):
             _build.build(checked=checked)
         if not os.path.exists(path):
             raise OSError(
@@ -316,8 +317,7 @@ def _strided_ptr(t) -> int | None:
 
 def rmsnorm_qk_rope_fwd(rope, q, k, wq, wk, positions, inv_freq, q_out, k_out, eps: float,
                         dtype: int, stream=None) -> int:
-    """`rope` is a Rope, packed bytes of one, or None; tensors it gives strides
-    for may be strided."""
+    """`rope` is a Rope or None; tensors it gives strides for may be strided."""
     return load_library().rmsnorm_qk_rope_fwd(
         _rope_ptr(rope), _strided_ptr(q), _strided_ptr(k), _ptr(wq), _ptr(wk),
         _strided_ptr(positions), _ptr(inv_freq), _strided_ptr(q_out), _strided_ptr(k_out), eps,
@@ -346,12 +346,8 @@ def rmsnorm_qk_rope_bwd_workspace_size(head_dim: int, device: int) -> int:
     return load_library().rmsnorm_qk_rope_bwd_workspace_size(head_dim, device)
 
 
-def _rope_ptr(rope):
-    if isinstance(rope, Rope):
-        return ctypes.addressof(rope)
-    if isinstance(rope, bytes) and len(rope) != ctypes.sizeof(Rope):
-        raise ValueError("a packed rope descriptor of the wrong size")
-    return rope  # bytes pass as their address
+def _rope_ptr(rope: Rope | None):
+    return None if rope is None else ctypes.addressof(rope)
 
 
 def rmsnorm_group_norm_fwd(x, w, b, y, mean, rstd, B: int, S: int, C: int, G: int, eps: float,

@@ -11,15 +11,21 @@ ring access of the kernels against the extent it belongs to and reports a
 failed check as RMSNORM_ERR_OUT_OF_BOUNDS instead of making the access. It is
 a debug build for the tests; the binding loads it only when
 RMSNORM_LIBRARY_VARIANT=checked is set.
+
+The Python binding of the tensor-level image operators (csrc/binding.cpp, host
+code only, compiled by g++ against PyTorch's headers) goes to
+``_build/_binding.so`` and serves both variants; without PyTorch it is left out.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -30,6 +36,8 @@ CHECKED_BUILD_DIR = os.path.join(PKG_DIR, "_build_checked")
 LIB_NAME = "librmsnorm.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 CHECKED_LIB_PATH = os.path.join(CHECKED_BUILD_DIR, LIB_NAME)
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(BUILD_DIR, "_binding.so")
 
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "bwd_f32.cu", "bwd_bf16.cu", "bwd_f16.cu",
            "bwd_res_f32.cu", "bwd_res_bf16.cu", "bwd_res_f16.cu", "naive.cu", "probe.cu",
@@ -99,6 +107,36 @@ def is_stale(checked: bool = False) -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None else list(spec.submodule_search_locations)[0]
+
+
+def binding_is_stale() -> bool:
+    if _torch_dir() is None:
+        return False
+    if not os.path.exists(BINDING_PATH):
+        return True
+    t = os.path.getmtime(BINDING_PATH)
+    return any(os.path.getmtime(f) > t for f in
+               (BINDING_SOURCE, os.path.join(INCLUDE, "rmsnorm.h"), os.path.abspath(__file__)))
+
+
+def _build_binding() -> None:
+    torch = _torch_dir()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    includes = [INCLUDE, os.path.join(torch, "include"),
+                os.path.join(torch, "include", "torch", "csrc", "api", "include"), cuda,
+                sysconfig.get_paths()["include"]]
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+          *(f"-I{d}" for d in includes), BINDING_SOURCE, "-o", tmp,
+          "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+          "-ltorch", "-ltorch_python"], os.path.join(BUILD_DIR, "binding.log"))
+    os.replace(tmp, BINDING_PATH)
+
+
 def _run(cmd: list[str], log: str | None) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     out = (res.stdout or "") + (res.stderr or "")
@@ -143,14 +181,17 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
     library's path."""
     variants = [False, True] if both else [checked]
     todo = [v for v in variants if force or is_stale(v)]
-    if not todo:
+    binding = _torch_dir() is not None and (force or binding_is_stale())
+    if not todo and not binding:
         return lib_path(checked and not both)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
     plans = {v: _variant_jobs(v, extra) for v in todo}
     cmds = [c for v in todo for c in plans[v][0]]
-    workers = jobs or min(len(cmds), max(1, os.cpu_count() or 1))
+    workers = jobs or min(len(cmds) + 1, max(1, os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
-        for fut in [ex.submit(_run, c, log) for c, log in cmds]:
+        futures = [ex.submit(_build_binding)] if binding else []
+        futures += [ex.submit(_run, c, log) for c, log in cmds]
+        for fut in futures:
             fut.result()
     for v in todo:
         _link(plans[v][1], v)

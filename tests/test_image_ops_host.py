@@ -5,6 +5,9 @@ from __future__ import annotations
 
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -12,7 +15,6 @@ import torch
 import image_ref as ref
 import memory_bound_normalization_gb300 as pkg
 from memory_bound_normalization_gb300 import build as libbuild
-from memory_bound_normalization_gb300 import image_ops
 
 A = 1 << 20  # aligned non-null addresses; never dereferenced by these calls
 
@@ -138,20 +140,43 @@ def test_rope_nothing_to_do():
         assert rope_bwd(desc(**empty), dwq=None, dwk=None) == pkg.OK
 
 
-def test_packed_descriptor_is_the_struct():
-    assert image_ops._ROPE.size == ctypes.sizeof(pkg.Rope)
-    head = (2, 3, 4, 2, 64, 64, 3, 8, 12, 12, 0)
-    six = [(768 + i, 256 + i, 64 + i) for i in range(6)]
-    got = pkg.Rope.from_buffer_copy(image_ops._pack(head, True, False, True, (6, 3, 1), *six))
-    assert (got.batch, got.length, got.q_heads, got.k_heads) == (2, 3, 4, 2)
-    assert (got.head_dim, got.rotary_dim, got.axes, list(got.sections)) == (64, 64, 3, [8, 12, 12, 0])
-    assert (got.interleaved, got.adjacent, got.positions_64) == (1, 0, 1)
-    assert list(got.position_stride) == [6, 3, 1]
-    for name, (b, t, h) in zip(("q", "k", "q_out", "k_out", "dq", "dk"), six):
-        s = getattr(got, name)
-        assert (s.batch, s.token, s.head) == (b, t, h)
-    with pytest.raises(ValueError):
-        pkg.rmsnorm_qk_rope_fwd(b"short", A, A, A, A, A, A, A, A, 1e-6, pkg.BF16, 0)
+def test_descriptor_matches_the_header(tmp_path):
+    """The ctypes structure has the layout the header's compiler gives it."""
+    src = tmp_path / "layout.c"
+    names = [n for n, _ in pkg.Rope._fields_]
+    lines = "".join(f'printf("{n} %zu\\n", offsetof(rmsnorm_rope_t, {n}));' for n in names)
+    src.write_text('#include <stdio.h>\n#include "rmsnorm.h"\nint main(void) {' + lines +
+                   'printf("size %zu\\n", sizeof(rmsnorm_rope_t)); return 0; }')
+    cuda = os.path.join(os.path.dirname(os.path.dirname(libbuild._nvcc())), "include")
+    subprocess.run(["gcc", "-I", libbuild.INCLUDE, "-I", cuda, str(src), "-o",
+                    str(tmp_path / "layout")], check=True)
+    out = subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True)
+    got = dict(line.split() for line in out.stdout.splitlines())
+    assert int(got.pop("size")) == ctypes.sizeof(pkg.Rope)
+    assert {n: int(v) for n, v in got.items()} == {n: getattr(pkg.Rope, n).offset for n in names}
+
+
+def test_missing_binding_raises():
+    """Without the compiled binding the tensor-level calls raise; nothing else
+    computes in its place."""
+    code = ("import torch, memory_bound_normalization_gb300 as p\n"
+            "from memory_bound_normalization_gb300 import build\n"
+            "build.BINDING_PATH = '/nonexistent/_binding.so'\n"
+            "x = torch.zeros(2, 4, 8)\n"
+            "try:\n    p.group_norm_forward(x, 2)\nexcept OSError:\n    print('raised')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root,
+                         timeout=120)
+    assert "raised" in res.stdout, res.stderr[-2000:]
+
+
+def test_calls_take_tensors():
+    with pytest.raises(ValueError, match="expected a tensor"):
+        pkg.group_norm_forward([1.0], 1)
+    with pytest.raises(ValueError, match="expected a tensor"):
+        pkg.qk_rope_forward(None, None, None, None, None, None, (1,))
+    with pytest.raises(TypeError):
+        pkg.group_norm_forward(torch.zeros(2, 8), "two")
 
 
 def test_group_norm_calls_refuse():
