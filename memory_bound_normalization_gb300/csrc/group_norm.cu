@@ -207,9 +207,8 @@ SlabArgs args_of(const Plan& p, const GroupNormArgs& a) {
     const int parts = p.resident ? p.cluster : p.parts;
     g.part_rows = static_cast<int>(a.S / parts);
     g.part_more = static_cast<int>(a.S % parts);
-    const int room = p.threads / (2 * g.cw);
-    g.join = 1;
-    while (g.join < 16 && 2 * g.join <= room) g.join *= 2;
+    // threads that share four channels' lanes: as many as there are, up to 16
+    g.join = std::max(1, std::min({16, g.lanes, p.threads / (g.cw / 2)}));
     g.drop_unit = -1;
     return g;
 }

@@ -22,7 +22,7 @@ struct SlabArgs {
     int D;         // channels of a group
     int cluster;   // resident: blocks of a slab, which join their sums
     int part_rows, part_more;  // positions of a block, and how many blocks take one more
-    int join;      // threads that share a channel's sums in a block
+    int join;      // threads that share four channels' sums in a block
     // stream
     int parts;     // blocks of a slab
     int together;  // slabs of a round

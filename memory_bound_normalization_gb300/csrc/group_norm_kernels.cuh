@@ -6,13 +6,13 @@
 // constants and sums stay in registers, whatever the group width (a vector may
 // span groups: sums are kept per channel and joined per group afterwards).
 //
-// Forward statistics. A thread sums d = x - p and d^2 about its own first
-// value p of each channel, which turns into (count, mean, M2); these are joined
-// over the block, the cluster and the slab by
+// Forward statistics. A block sums d = x - p and d^2 for each channel about p,
+// the median of the channel's values at three of the block's positions, which
+// gives (count, mean, M2); these are joined over channels, blocks and the slab by
 //   mean = sum n_i m_i / n,   M2 = sum M2_i + n_i (m_i - mean)^2
-// so neither a mean far from zero nor one wild first value costs digits (a wild
-// p spoils only the few hundred values of one thread, and then only relative to
-// its own square, which is part of M2).
+// so a mean far from zero costs no digits, as long as p lies among the values:
+// the sum of squares is rounded at 2^-24 of n_i (p - m_i)^2. The median of three
+// positions a quarter of the block apart leaves out a border of zeros.
 // Backward sums. Per channel P = sum dz, Q = sum dz xhat: they give the slab's
 // means (sum_c w P, sum_c w Q) and, added over samples, db and dw.
 //
@@ -36,10 +36,6 @@ namespace {
 // First position of a block's range: S split as evenly as it goes.
 __device__ __forceinline__ int64_t part_begin(const SlabArgs& g, int part) {
     return static_cast<int64_t>(part) * g.part_rows + min(part, g.part_more);
-}
-// Positions of the n blocks from `part` on.
-__device__ __forceinline__ float part_count(const SlabArgs& g, int part, int n) {
-    return static_cast<float>(part_begin(g, part + n) - part_begin(g, part));
 }
 
 // Where a block works.
@@ -215,10 +211,17 @@ struct Columns<T, false, ACT> {
     float2 pivot[PAIRS], s1[PAIRS], s2[PAIRS];
     float2 scale[PAIRS], shift[PAIRS];  // rstd w and b - mean rstd w
 
-    __device__ __forceinline__ void start(const uint4& first) {
-        Pack<T>::unpack2(first, pivot);
+    __device__ __forceinline__ void start(const uint4 (&three)[3]) {
+        float2 b[PAIRS], c[PAIRS];
+        Pack<T>::unpack2(three[0], pivot);
+        Pack<T>::unpack2(three[1], b);
+        Pack<T>::unpack2(three[2], c);
+        auto median = [](float p, float q, float r) { return fmaxf(fminf(p, q), fminf(fmaxf(p, q), r)); };
 #pragma unroll
-        for (int e = 0; e < PAIRS; ++e) s1[e] = s2[e] = make_float2(0.f, 0.f);
+        for (int e = 0; e < PAIRS; ++e) {
+            pivot[e] = make_float2(median(pivot[e].x, b[e].x, c[e].x), median(pivot[e].y, b[e].y, c[e].y));
+            s1[e] = s2[e] = make_float2(0.f, 0.f);
+        }
     }
     __device__ __forceinline__ void add(const uint4& v) {
         float2 f[PAIRS];
@@ -279,28 +282,35 @@ struct Columns<T, true, ACT> {
 };
 
 // Sums of a block's channels over its lanes: two values a channel in `sums`
-// ([2][lanes][cw]), added into the first lane's rows. g.join threads share a
-// channel's lanes (part j adds rows j, j + share, ... into row j), then part 0
-// adds the parts.
+// ([2][lanes][cw]), added into the first lane's rows. A thread adds four
+// neighbouring values of every g.join-th lane from lane j on into lane j's row,
+// then the first threads add the g.join rows.
 __device__ __forceinline__ void sum_lanes(const SlabArgs& g, float* sums) {
-    const int share = min(g.lanes, g.join), columns = 2 * g.cw;
+    const int quads = g.cw / 2, half = g.cw / 4;  // of both values, and of one
+    auto at = [&](int q, int lane) {
+        return reinterpret_cast<float4*>(sums + ((q < half ? 0 : g.lanes) + lane) * g.cw + (q < half ? q : q - half) * 4);
+    };
+    auto add = [](float4& s, const float4& v) {
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    };
     __syncthreads();
-    for (int i = threadIdx.x; i < columns * share; i += blockDim.x) {
-        const int j = i / columns, c = i - j * columns;
-        float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw) + j * g.cw;
-        float s = 0.f;
-#pragma unroll 8
-        for (int r = j; r < g.lanes; r += share) s += at[(r - j) * g.cw];
-        at[0] = s;
+    for (int i = threadIdx.x; i < quads * g.join; i += blockDim.x) {
+        const int j = i / quads, q = i - j * quads;
+        float4 s = *at(q, j);
+#pragma unroll 4
+        for (int r = j + g.join; r < g.lanes; r += g.join) add(s, *at(q, r));
+        *at(q, j) = s;
     }
     __syncthreads();
-    if (share > 1) {
-        for (int c = threadIdx.x; c < columns; c += blockDim.x) {
-            float* at = sums + (c < g.cw ? c : g.lanes * g.cw + c - g.cw);
-            float s = 0.f;
+    if (g.join > 1) {
+        for (int q = threadIdx.x; q < quads; q += blockDim.x) {
+            float4 s = *at(q, 0);
 #pragma unroll 4
-            for (int j = 0; j < share; ++j) s += at[j * g.cw];
-            at[0] = s;
+            for (int j = 1; j < g.join; ++j) add(s, *at(q, j));
+            *at(q, 0) = s;
         }
         __syncthreads();
     }
@@ -347,14 +357,24 @@ __device__ __forceinline__ void load_channels(const SlabArgs& g, const Seat& s, 
     }
 }
 
-// The first pass's constants of a thread's channels (backward), and its sums.
+// A thread's channels at three of the block's positions, a quarter of it apart;
+// `p` points to them at its first position, `pitch` bytes before the next.
+__device__ __forceinline__ void load_three(uint4 (&three)[3], const void* p, int rows, int64_t pitch) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        three[i] = ld_global_16_stream(static_cast<const char*>(p) + (static_cast<int64_t>(rows) * (i + 1) / 4) * pitch);
+}
+
+// The first pass's constants of a thread's channels, and its sums. `three`:
+// positions of the block to take the pivots from (forward).
 template <typename T, int ACT>
-__device__ __forceinline__ void start(Columns<T, false, ACT>& col, const SlabArgs&, const Seat&, const float*) {
-    col.start(make_uint4(0, 0, 0, 0));
+__device__ __forceinline__ void start(Columns<T, false, ACT>& col, const SlabArgs&, const Seat&, const float*,
+                                      const uint4 (&three)[3]) {
+    col.start(three);
 }
 template <typename T, int ACT>
 __device__ __forceinline__ void start(Columns<T, true, ACT>& col, const SlabArgs& g, const Seat& s,
-                                      const float* chan) {
+                                      const float* chan, const uint4 (&)[3]) {
     if (s.active) {
         read_channels<T>(chan + s.c, col.mean);
         read_channels<T>(chan + g.cw + s.c, col.k1);
@@ -364,56 +384,28 @@ __device__ __forceinline__ void start(Columns<T, true, ACT>& col, const SlabArgs
     for (int e = 0; e < Pack<T>::PAIRS; ++e) col.p[e] = col.q[e] = make_float2(0.f, 0.f);
 }
 
-// Joins the block's first pass: emit(k, (mean, M2)) for each group of channels.
-// Channel means over the lanes first, then squares about them, then groups.
+// Joins the block's first pass: emit(k, (mean, M2)) for each group of channels,
+// from each channel's sums about its pivot.
 template <typename T, int ACT, typename Emit>
 __device__ __forceinline__ void join(const Columns<T, false, ACT>& col, const SlabArgs& g, const Seat& s,
-                                     float* sums, const float*, int rows, int n, Emit emit) {
-    constexpr int PAIRS = Pack<T>::PAIRS;
-    const float fn = static_cast<float>(n), inv_n = n > 0 ? 1.f / fn : 0.f;
+                                     float* sums, float* chan, int rows, Emit emit) {
+    if (s.active) {
+        write_channels<T>(sums + s.lane * g.cw + s.c, col.s1);
+        write_channels<T>(sums + (g.lanes + s.lane) * g.cw + s.c, col.s2);
+        if (s.lane == 0) write_channels<T>(chan + s.c, col.pivot);
+    }
+    sum_lanes(g, sums);
+    const float* squares = sums + g.lanes * g.cw;
     const float frows = static_cast<float>(rows), inv_rows = 1.f / fmaxf(frows, 1.f);
-    float2 u[PAIRS], v[PAIRS];
-    if (s.active) {
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) {
-            u[e] = __ffma2_rn(col.pivot[e], f2_splat(fn), col.s1[e]);
-            v[e] = make_float2(0.f, 0.f);
-        }
-        write_channels<T>(sums + s.lane * g.cw + s.c, u);
-        write_channels<T>(sums + (g.lanes + s.lane) * g.cw + s.c, v);
-    }
-    sum_lanes(g, sums);
-    if (s.active) {
-        read_channels<T>(sums + s.c, u);
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) {
-            u[e] = __fmul2_rn(u[e], f2_splat(inv_rows));
-            // squares of the thread's values about the channel's mean
-            const float2 d = __fmul2_rn(col.s1[e], f2_splat(inv_n));
-            const float2 off = sub2(__fadd2_rn(col.pivot[e], d), u[e]);
-            v[e] = sub2(col.s2[e], __fmul2_rn(col.s1[e], d));
-            v[e] = __ffma2_rn(__fmul2_rn(off, off), f2_splat(fn), v[e]);
-            if (n == 0) v[e] = make_float2(0.f, 0.f);
-        }
-    }
-    __syncthreads();
-    if (s.active) {
-        // the other half carries the means through, in the first lane's row
-        write_channels<T>(sums + s.lane * g.cw + s.c, v);
-#pragma unroll
-        for (int e = 0; e < PAIRS; ++e) u[e] = s.lane == 0 ? u[e] : make_float2(0.f, 0.f);
-        write_channels<T>(sums + (g.lanes + s.lane) * g.cw + s.c, u);
-    }
-    sum_lanes(g, sums);
-    const float* means = sums + g.lanes * g.cw;
     for (int k = s.warp; k < g.gw; k += s.warps) {
         float t = 0.f;
-        for (int i = s.l; i < g.D; i += 32) t += means[k * g.D + i];
+        for (int i = k * g.D + s.l; i < (k + 1) * g.D; i += 32) t += fmaf(sums[i], inv_rows, chan[i]);
         const float m = group_allreduce<32>(t) * s.inv_d;
         float m2 = 0.f;
-        for (int i = s.l; i < g.D; i += 32) {
-            const float d = means[k * g.D + i] - m;
-            m2 += fmaf(frows * d, d, sums[k * g.D + i]);
+        for (int i = k * g.D + s.l; i < (k + 1) * g.D; i += 32) {
+            // squares about the channel's mean, and its mean's distance from the group's
+            const float off = sums[i] * inv_rows, d = chan[i] + off - m;
+            m2 += fmaf(frows * d, d, fmaf(-sums[i], off, squares[i]));
         }
         m2 = group_allreduce<32>(m2);
         if (s.l == 0) emit(k, make_float2(m, m2));
@@ -424,7 +416,7 @@ __device__ __forceinline__ void join(const Columns<T, false, ACT>& col, const Sl
 // in the first lane's rows of `sums`: P, and Q behind all lanes of P.
 template <typename T, int ACT, typename Emit>
 __device__ __forceinline__ void join(const Columns<T, true, ACT>& col, const SlabArgs& g, const Seat& s,
-                                     float* sums, const float* chan, int, int, Emit emit) {
+                                     float* sums, float* chan, int, Emit emit) {
     if (s.active) {
         write_channels<T>(sums + s.lane * g.cw + s.c, col.p);
         write_channels<T>(sums + (g.lanes + s.lane) * g.cw + s.c, col.q);
@@ -589,18 +581,18 @@ __global__ void __launch_bounds__(kMaxThreads) gn_resident_kernel(const __grid_c
     wait_for_prerequisite_grid();  // no global access before this
 
     feed.prepare(g.a.status);
+    uint4 three[3] = {};
+    if (!BWD && s.active && at.rows > 0)
+        load_three(three, static_cast<const T*>(g.a.x) + base - static_cast<int64_t>(s.lane) * g.a.C, at.rows,
+                   g.a.C * static_cast<int64_t>(sizeof(T)));
     load_channels<T, BWD>(g, s, chan, c0, group0);
     __syncthreads();
-    start(col, g, s, chan);
-    feed.run(g.a.status, [&](int i, const uint4& x, const uint4& dy) {
-        if constexpr (BWD) {
-            col.add(x, dy);
-        } else {
-            if (i == 0) col.start(x);
-            col.add(x);
-        }
+    start(col, g, s, chan, three);
+    feed.run(g.a.status, [&](int, const uint4& x, const uint4& dy) {
+        if constexpr (BWD) col.add(x, dy);
+        else col.add(x);
     });
-    join(col, g, s, sums, chan, at.rows, n, [&](int k, float2 v) { mine[k] = v; });
+    join(col, g, s, sums, chan, at.rows, [&](int k, float2 v) { mine[k] = v; });
 
     // the cluster's blocks meet; lane r of a warp reads block r's result
     __syncwarp();
@@ -823,23 +815,20 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
         const bool live = sample < g.a.B;
         const int n = live ? n_all : 0, c0 = split * g.cw;
         const int64_t group0 = sample * g.a.G + split * g.gw;
+        uint4 three[3] = {};
+        if (!BWD && live && s.active && rows > 0)
+            load_three(three, static_cast<const char*>(g.a.x) + s.c * SIZE +
+                                  ((sample * g.a.S + r0) * g.a.C + c0) * static_cast<int64_t>(SIZE),
+                       rows, pitch);
         if (live) load_channels<T, BWD>(g, s, chan, c0, group0);
         __syncthreads();
         Columns<T, BWD, ACT> col;
-        start(col, g, s, chan);
-        [[maybe_unused]] bool first = true;
+        start(col, g, s, chan, three);
         ring.run(pass, [&] { return pass_of(round, true); }, [&](const uint4& x, const uint4& dy) {
-            if constexpr (BWD) {
-                col.add(x, dy);
-            } else {
-                if (first) {
-                    col.start(x);
-                    first = false;
-                }
-                col.add(x);
-            }
+            if constexpr (BWD) col.add(x, dy);
+            else col.add(x);
         });
-        join(col, g, s, sums, chan, rows, n, [&](int k, float2 v) {
+        join(col, g, s, sums, chan, rows, [&](int k, float2 v) {
             if (live) g.stats[(slab_i * g.gw + k) * g.parts + part] = v;
         });
         if constexpr (BWD) {

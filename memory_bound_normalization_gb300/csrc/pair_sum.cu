@@ -1,60 +1,96 @@
-// Column sums of dw partial rows for two outputs at once (the weight
-// gradients of queries and keys; dw and db of a group norm), in a fixed
-// order: thread row q of a block adds rows q, q + R, q + 2R, ... in ascending
-// order, then a pairwise tree adds the R sums of a column. The same bits on
-// every run for given sizes. A few hundred rows of a few hundred columns: the
-// time is one trip to L2 and the launch, so columns are spread over as many
-// blocks as keep 16-byte row pieces.
+// Column sums of dw partial rows for two outputs at once (the weight gradients
+// of queries and keys; dw and db of a group norm), in a fixed order: a block of
+// eight warps takes W neighbouring columns, thread t adds rows t, t + 256, ...
+// in ascending order, a butterfly adds a warp's lanes and thread 0 the warps.
+// The same bits on every run for given sizes. A few hundred rows of a few
+// hundred columns: the time is the launch and one trip to L2, so every row has
+// a thread of its own where there are no more than 256, and one barrier is all.
 #include "common.cuh"
 #include "ops.h"
 
 namespace rmsn {
 namespace {
 
-template <int C>
-__global__ void __launch_bounds__(1024) pair_sum_kernel(const __grid_constant__ PairSum a) {
-    constexpr int R = 1024 / C;
-    __shared__ float part[R][C + 1];
-    const int cx = threadIdx.x % C, q = threadIdx.x / C;
-    const int which = blockIdx.y;
-    const int col = blockIdx.x * C + cx;
+constexpr int kSumThreads = 256;
+
+template <int W>
+struct Columns;
+template <>
+struct Columns<4> {
+    using V = float4;
+    __device__ static void add(float (&s)[4], const float4& v) {
+        s[0] += v.x;
+        s[1] += v.y;
+        s[2] += v.z;
+        s[3] += v.w;
+    }
+};
+template <>
+struct Columns<2> {
+    using V = float2;
+    __device__ static void add(float (&s)[2], const float2& v) {
+        s[0] += v.x;
+        s[1] += v.y;
+    }
+};
+template <>
+struct Columns<1> {
+    using V = float;
+    __device__ static void add(float (&s)[1], const float& v) { s[0] += v; }
+};
+
+template <int W>
+__global__ void __launch_bounds__(kSumThreads) pair_sum_kernel(const __grid_constant__ PairSum a) {
+    using V = typename Columns<W>::V;
+    __shared__ float part[kSumThreads / 32][W];
+    const int which = blockIdx.y, col = blockIdx.x * W, rows = a.rows[which];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     wait_for_prerequisite_grid();  // partial rows complete and visible
     allow_dependent_launch();
-    const float* src = a.part[which];
     float* out = a.out[which];
-    float s = 0.f;
-    if (col < a.n && out != nullptr) {
+    if (out == nullptr) return;
+    const float* src = a.part[which] + col;
+    float s[W] = {};
 #pragma unroll 4
-        for (int p = q; p < a.rows[which]; p += R) s += src[static_cast<int64_t>(p) * a.stride + col];
-    }
-    part[q][cx] = s;
-    __syncthreads();
+    for (int p = threadIdx.x; p < rows; p += kSumThreads)
+        Columns<W>::add(s, *reinterpret_cast<const V*>(src + static_cast<int64_t>(p) * a.stride));
 #pragma unroll
-    for (int h = R / 2; h > 0; h >>= 1) {
-        if (q < h) part[q][cx] += part[q + h][cx];
-        __syncthreads();
+    for (int i = 0; i < W; ++i) s[i] = group_allreduce<32>(s[i]);
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) part[warp][i] = s[i];
     }
-    if (q == 0 && col < a.n && out != nullptr &&
-        RMSN_OK(span_in(out + col, 4, out, static_cast<int64_t>(a.n) * 4), a.status))
-        out[col] = part[0][cx];
+    __syncthreads();
+    if (threadIdx.x < W && RMSN_OK(span_in(out + col + threadIdx.x, 4, out, static_cast<int64_t>(a.n) * 4), a.status)) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSumThreads / 32; ++w) t += part[w][threadIdx.x];
+        out[col + threadIdx.x] = t;
+    }
 }
 
 }  // namespace
 
 cudaError_t pair_sum_launch(const PairSum& a, cudaStream_t s) {
-    const int c = a.n >= 1024 ? 32 : a.n >= 256 ? 8 : 4;
+    auto fits = [&](int w) {
+        if (a.n % w || a.stride % w) return false;
+        for (const float* p : a.part)
+            if (reinterpret_cast<uintptr_t>(p) % (4 * w)) return false;
+        return true;
+    };
+    const int w = fits(4) ? 4 : fits(2) ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(a.n, c)), 2);
-    cfg.blockDim = dim3(1024);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.n / w), 2);
+    cfg.blockDim = dim3(kSumThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = pdl_allowed();
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (c == 32) return cudaLaunchKernelEx(&cfg, pair_sum_kernel<32>, a);
-    if (c == 8) return cudaLaunchKernelEx(&cfg, pair_sum_kernel<8>, a);
-    return cudaLaunchKernelEx(&cfg, pair_sum_kernel<4>, a);
+    if (w == 4) return cudaLaunchKernelEx(&cfg, pair_sum_kernel<4>, a);
+    if (w == 2) return cudaLaunchKernelEx(&cfg, pair_sum_kernel<2>, a);
+    return cudaLaunchKernelEx(&cfg, pair_sum_kernel<1>, a);
 }
 
 }  // namespace rmsn
