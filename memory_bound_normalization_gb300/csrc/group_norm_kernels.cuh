@@ -104,31 +104,6 @@ __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
     return __fadd2_rn(a, make_float2(-b.x, -b.y));
 }
 
-// Copies 16 bytes into this thread's own shared-memory slot; visible to it once
-// the group that holds the copy is waited for. No other thread reads the slot,
-// so no barrier is needed.
-__device__ __forceinline__ bool slot_in(uint32_t slot) {
-    const uint32_t b = smem_u32(rmsn_dynamic_smem);
-    return slot >= b && slot - b + 16u <= dynamic_smem_bytes();
-}
-__device__ __forceinline__ void copy_own(uint32_t slot, const void* src, int* status) {
-    if (!RMSN_OK(slot_in(slot), status)) return;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot), "l"(src) : "memory");
-}
-__device__ __forceinline__ uint4 ld_slot(uint32_t slot) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(slot)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
-}
-
 __device__ __forceinline__ float rcp_fast(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -684,7 +659,7 @@ struct Copies {
     int* status;
 
     __device__ __forceinline__ void copy(uint32_t to, const char* from, bool last_use) const {
-        if (!RMSN_OK(slot_in(to), status)) return;
+        if (!RMSN_OK(slot_in<16>(to), status)) return;
         if (last_use)
             asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(drop) : "memory");
         else

@@ -1,6 +1,7 @@
 // Rotary positions after the QK-norm, host side: the widest pieces the tensors
 // allow, the geometry and the launches.
 #include <algorithm>
+#include <mutex>
 
 #include "rope.h"
 
@@ -21,8 +22,6 @@ int piece_of(const RopeArgs& a, int dtype, bool adjacent) {
         if (e > 16 / size || e < 4) continue;
         bool ok = adjacent ? a.head_dim % (2 * e) == 0
                            : a.rot / 2 % e == 0 && (a.head_dim - a.rot) / 2 % e == 0;
-        // an adjacent unit must not mix rotated and passing pairs' tables: it
-        // does not, the tables hold every pair; only the pieces have to align
         for (const RopeTensor& t : a.t) {
             if (t.heads == 0) continue;
             ok = ok && fits(t.x, t.xs, e * size, size) && fits(t.dy, t.dys, e * size, size) &&
@@ -42,26 +41,38 @@ RopeFn kernel_for(int dtype, int e, int units, bool bwd, bool adjacent, bool nor
     }
 }
 
-// Units of a head for the kernels of constant geometry: every element turns, or
-// the pairs are neighbours anyway. 0: the others.
-int fixed_units(const RopeArgs& a, bool adjacent) {
-    return adjacent || a.rot == a.head_dim ? a.units : 0;
-}
-
 void shape_of(RopeArgs* a, int e) {
     a->units = a->head_dim / 2 / e;
     a->lanes = 4;
     while (a->lanes < 32 && a->lanes < a->units) a->lanes *= 2;
 }
 
-// Shared memory of the backward: weights, then the larger of the two angle
-// tables and the groups' shares of dw.
-int bwd_smem(const RopeArgs& a) {
-    return a.head_dim * 4 * (1 + std::max(2 * a.tile, kRopeThreads / a.lanes));
+// Shared memory of the backward: rows on the way, weights, then the larger of
+// the two angle tables and the groups' shares of dw.
+int bwd_smem(const RopeArgs& a, int e, int dtype) {
+    return (e >= 4 ? kRopeRingWords * e * dtype_size(dtype) : 0) +
+           a.head_dim * 4 * (1 + std::max(2 * a.tile, kRopeThreads / a.lanes));
 }
 
-// Tokens of a tile at most: two angle tables fit in 40 KB, so that no kernel
-// needs more shared memory than every launch may have.
+// Lets a kernel have the shared memory that its blocks an SM leave it, once a
+// device.
+cudaError_t allow_smem(const DeviceInfo& dev, RopeFn fn) {
+    static std::mutex mu;
+    static struct {
+        int device;
+        RopeFn fn;
+    } done[256];
+    static int n = 0;
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < n; ++i)
+        if (done[i].device == dev.device && done[i].fn == fn) return cudaSuccess;
+    const cudaError_t err = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRopeBwdSmem);
+    if (err == cudaSuccess && n < 256) done[n++] = {dev.device, fn};
+    return err;
+}
+
+// Tokens of a tile at most: two angle tables fit in 40 KB.
 int max_tile(const RopeArgs& a) { return std::min(kRopeMaxTile, 40 * 1024 / (8 * a.head_dim)); }
 
 int bwd_tile(const RopeArgs& a) {
@@ -92,7 +103,7 @@ cudaError_t rope_fwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, Rop
     const int64_t per_sm = e >= 4 ? 4 : 3;  // what the kernels' launch bounds leave room for
     const int blocks = static_cast<int>(std::min<int64_t>(cdiv(a.tokens, a.tile), per_sm * dev.sm_count));
     const int smem = a.head_dim * 4 * (2 * a.tile + (norm ? 2 : 0));
-    return launch_pdl(kernel_for(dtype, e, fixed_units(a, adjacent), false, adjacent, norm),
+    return launch_pdl(kernel_for(dtype, e, a.units, false, adjacent, norm),
                       blocks * a.splits, kRopeThreads, smem, 1, s, a);
 }
 
@@ -115,13 +126,14 @@ cudaError_t rope_bwd_rows(const DeviceInfo& dev, int dtype, bool adjacent, const
 
 cudaError_t rope_bwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, RopeArgs a,
                             const int rows[2], cudaStream_t s) {
-    (void)dev;
     const int e = piece_of(a, dtype, adjacent);
     shape_of(&a, e);
     a.tile = bwd_tile(a);
     a.blocks0 = rows[0];
-    cudaError_t err = launch_pdl(kernel_for(dtype, e, fixed_units(a, adjacent), true, adjacent, true),
-                                 rows[0] + rows[1], kRopeThreads, bwd_smem(a), 1, s, a);
+    const RopeFn fn = kernel_for(dtype, e, a.units, true, adjacent, true);
+    cudaError_t err = allow_smem(dev, fn);
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(fn, rows[0] + rows[1], kRopeThreads, bwd_smem(a, e, dtype), 1, s, a);
     if (err != cudaSuccess) return err;
     PairSum p{};
     for (int i = 0; i < 2; ++i) {

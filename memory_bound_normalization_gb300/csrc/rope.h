@@ -9,6 +9,11 @@ namespace rmsn {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxTile = 32;  // tokens of a tile
 constexpr int kRopeBwdBlocks = 2;  // blocks an SM holds in the backward
+constexpr int kRopeBwdAhead = 3;   // rows a thread's copies run ahead in the backward
+
+// Pieces of a backward block's rows on the way: two of x and two of dy a thread.
+constexpr int kRopeRingWords = kRopeBwdAhead * 4 * kRopeThreads;
+constexpr int kRopeBwdSmem = 100 * 1024;  // of a backward block at most
 
 using RopeFn = void (*)(const RopeArgs);
 // The kernel for pieces of e elements and `units` units a head.

@@ -121,22 +121,40 @@ __device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t turns) {
 // the lanes of a group: table offsets, lane masks and the row sum's steps are
 // then constants. (Left to run time, they and the kernel parameters reloaded
 // for them made up half of the forward's instructions.)
-template <int E>
+//
+// A unit is the E pairs that a lane takes at once, from two pieces of E elements:
+// the pairs' first elements and their second ones; where pairs are neighbours,
+// each piece holds E/2 whole pairs, one piece from either half of the head. (Two
+// neighbouring pieces a lane instead take half a sector with each access: 65
+// against 42 us for the backward of 3760 tokens of 80 bf16 heads of 128.)
+template <int E, bool ADJ>
 __device__ __forceinline__ int table_at(int units, int p) {
     if constexpr (E == 1) return 2 * p;
-    const int u = p / E, e = p % E;
+    int u = p / E, e = p % E;
+    if constexpr (ADJ && E > 1) {
+        const int half = units * (E / 2), upper = p >= half;
+        const int at = p - (upper ? half : 0);
+        u = at / (E / 2);
+        e = at % (E / 2) + (upper ? E / 2 : 0);
+    }
     return ((e / 2) * units + u) * 4 + e % 2;
+}
+// Pair e of unit u.
+template <int E, bool ADJ>
+__device__ __forceinline__ int pair_at(int units, int u, int e) {
+    if constexpr (ADJ && E > 1) return (u + (e < E / 2 ? 0 : units)) * (E / 2) + e % (E / 2);
+    return u * E + e;
 }
 template <int E>
 constexpr int kSecond = E == 1 ? 1 : 2;  // floats from a pair's first value to its second
 
-// The two E-element pieces of unit u: its first elements and its second.
+// The two E-element pieces of unit u.
 template <int E, bool ADJ>
 __device__ __forceinline__ void unit_offsets(const RopeArgs& a, int u, int& lo, int& hi) {
     const int p = u * E;
     if constexpr (ADJ) {
-        lo = 2 * p;
-        hi = 2 * p + E;
+        lo = E == 1 ? 2 * p : p;
+        hi = E == 1 ? lo + 1 : p + a.head_dim / 2;
     } else {
         const int half = a.rot / 2;
         if (p < half) {
@@ -203,11 +221,14 @@ __device__ __forceinline__ void join_pairs(const float2 (&f)[(E + 1) / 2], const
 
 template <int UNITS>
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
-    if constexpr (UNITS > 0) return group_allreduce<UNITS>(v);
+    if constexpr (UNITS > 0) {
+        return group_allreduce<UNITS>(v);
+    } else {
 #pragma unroll
-    for (int off = 16; off >= 1; off /= 2)
-        if (off < lanes) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
+        for (int off = 16; off >= 1; off /= 2)
+            if (off < lanes) v += __shfl_xor_sync(0xffffffffu, v, off);
+        return v;
+    }
 }
 
 __device__ __forceinline__ int64_t position_at(const RopeArgs& a, int64_t at) {
@@ -291,11 +312,11 @@ __device__ __forceinline__ PairOf pair_of(const RopeArgs& a) {
     return p;
 }
 // cos/sin of every pair of a tile's tokens into `tab` (D floats a token).
-template <typename T, int E>
+template <typename T, int E, bool ADJ>
 __device__ __forceinline__ void fill_angles(const RopeArgs& a, const PairOf& p, float* tab,
                                             const TileInfo& info, int tokens) {
     if (!p.has) return;
-    float* d = tab + table_at<E>(a.units, p.pair);
+    float* d = tab + table_at<E, ADJ>(a.units, p.pair);
 #pragma unroll 2
     for (int t = p.token; t < tokens; t += p.stride) {
         float2 cs = make_float2(1.f, 0.f);
@@ -312,7 +333,7 @@ __device__ __forceinline__ void fill_weights(const RopeArgs& a, const void* w, f
     for (int p = threadIdx.x; p < a.head_dim / 2; p += kRopeThreads) {
         int i, j;
         pair_members<ADJ>(a, p, i, j);
-        float* d = tab + table_at<E>(a.units, p);
+        float* d = tab + table_at<E, ADJ>(a.units, p);
         d[0] = a.w_f32 ? static_cast<const float*>(w)[i] : to_f32(static_cast<const T*>(w)[i]);
         d[kSecond<E>] = a.w_f32 ? static_cast<const float*>(w)[j] : to_f32(static_cast<const T*>(w)[j]);
     }
@@ -336,6 +357,12 @@ __device__ __forceinline__ void read_table(const float* tab, int some_units, int
     }
 }
 
+template <typename W>
+__device__ __forceinline__ W slot_word(uint32_t slot) {
+    if constexpr (sizeof(W) == 16) return ld_slot(slot);
+    else return ld_slot_8(slot);
+}
+
 // x * c - y * s and y * c + x * s. (The negation rides on scalar multiply-adds:
 // the packed form has none, and two sign flips a pair cost more.)
 __device__ __forceinline__ void turn(float2 x, float2 y, float2 c, float2 s, float2& ox, float2& oy) {
@@ -356,11 +383,11 @@ __device__ __forceinline__ void turn(float2 x, float2 y, float2 c, float2 s, flo
 template <int E> constexpr int kUnitsPerLane = E >= 4 ? 1 : kRopeMaxPairs / 32 / E;
 
 // Byte offsets of a lane's pieces in a head: the first one's, and the second's
-// distance from it, constant where the geometry is.
+// distance from it.
 template <typename T, int E, bool ADJ, int UNITS>
 struct Pieces {
     static constexpr int NU = UNITS > 0 ? 1 : kUnitsPerLane<E>;
-    int lo[NU], gap[UNITS > 0 ? 1 : NU];
+    int lo[NU], gap[NU];
     __device__ __forceinline__ void start(const RopeArgs& a, int lane, int lanes) {
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
@@ -371,7 +398,7 @@ struct Pieces {
         }
     }
     __device__ __forceinline__ int hop(int i) const {
-        if constexpr (UNITS > 0) return (ADJ ? E : E * UNITS) * static_cast<int>(sizeof(T));
+        if constexpr (ADJ && UNITS > 0) return E * UNITS * static_cast<int>(sizeof(T));
         return gap[i];
     }
 };
@@ -465,7 +492,7 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? 4 : 3) rope_fwd_kernel(
              static_cast<uint32_t>(a.t[w].xs[2] * sizeof(T)));
     };
     begin(0, range.count(0), info[0]);
-    fill_angles<T, E>(a, pair, tabs, info[0], range.count(0));
+    fill_angles<T, E, ADJ>(a, pair, tabs, info[0], range.count(0));
     int buf = 0, slot = 0;
     const int tensors = a.t[1].heads > 0 ? 2 : 1;
 #pragma unroll 1
@@ -480,7 +507,7 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? 4 : 3) rope_fwd_kernel(
         }
         __syncthreads();  // this tile's table is filled; the other one's readers are done
         if (more)
-            fill_angles<T, E>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[after], range.count(tile + 1));
+            fill_angles<T, E, ADJ>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[after], range.count(tile + 1));
 #pragma unroll 1
         for (int w = 0; w < tensors; ++w) {
             const int h0 = w ? kh0 : qh0, heads = w ? kheads : qheads;
@@ -563,6 +590,11 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? 4 : 3) rope_fwd_kernel(
 // their lanes' shares of dw in registers; at the end the groups' shares are
 // added in a fixed order into the block's partial row. No floating-point
 // atomics.
+//
+// 128 registers a thread leave 16 warps an SM, whose next rows alone (32 KB on
+// the way) do not fill DRAM's latency: pieces of 16 or 8 bytes are copied
+// kRopeBwdAhead rows ahead into the thread's own slots of shared memory. A row
+// ahead may lie as many tiles ahead, whose addresses are kept for it.
 template <typename T, int E, bool ADJ, int UNITS>
 __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
     rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
@@ -570,8 +602,14 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
     const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
     using X = Elems<T, E>;
     using W = typename X::W;
-    __shared__ TileInfo info[3];
-    float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem);
+    constexpr bool RING = E >= 4;
+    constexpr int AHEAD = RING ? kRopeBwdAhead : 1, SLOTS = AHEAD + 2;
+    constexpr int RING_BYTES = RING ? kRopeRingWords * static_cast<int>(sizeof(W)) : 0;
+    // While the block's slowest warp still reads the infos of a tile and of the
+    // AHEAD tiles after it, one more is written.
+    __shared__ TileInfo info[SLOTS];
+    uint4* ring = reinterpret_cast<uint4*>(rmsn_dynamic_smem);
+    float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem + RING_BYTES);
     float* tabs = wtab + D;  // [2][tile][D]
     const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
     const int groups = kRopeThreads / lanes;
@@ -601,57 +639,102 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
     }
     wait_for_prerequisite_grid();  // no global access before this
 
-    int64_t fetched = fetch_info(a, range, 0, mine);
+    int64_t fetched[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetched[i] = fetch_info(a, range, i, mine);
     const PairOf pair = pair_of(a);
     fill_weights<T, E, ADJ>(a, x.w, wtab);
-    store_info(a, info[0], fetched);
-    fetched = fetch_info(a, range, 1, mine);
-    __syncthreads();
-    W lo[NU], hi[NU], glo[NU], ghi[NU];
-    auto load = [&](const RowCursor& r, int tokens, const TileInfo& from) {
-        if (r.t >= tokens) return;
-        const uint64_t src = row_address(from.addr[0][r.t], r.head, x_step);
-        const uint64_t dys = row_address(from.addr[1][r.t], r.head, dy_step);
 #pragma unroll
-        for (int i = 0; i < NU; ++i)
-            if (UNITS > 0 || lane + i * lanes < a.units) {
-                const uint64_t p = src + at.lo[i], q = dys + at.lo[i];
-                lo[i] = X::load(reinterpret_cast<const T*>(p));
-                hi[i] = X::load(reinterpret_cast<const T*>(p + at.hop(i)));
-                glo[i] = X::load(reinterpret_cast<const T*>(q));
-                ghi[i] = X::load(reinterpret_cast<const T*>(q + at.hop(i)));
+    for (int i = 0; i < AHEAD; ++i) store_info(a, info[i], fetched[i]);
+    int64_t next_info = fetch_info(a, range, AHEAD, mine);
+    __syncthreads();
+    // The row to fetch next: of which tile, and how many passes that still has.
+    auto passes_of = [&](int tile) { return (range.count(tile) * heads + groups - 1) / groups; };
+    auto info_after = [](int slot) { return slot == SLOTS - 1 ? 0 : slot + 1; };
+    RowCursor row;
+    row.start(group, heads);
+    int row_tile = 0, row_slot = 0, row_tokens = range.tiles > 0 ? range.count(0) : 0;
+    int row_passes = range.tiles > 0 ? passes_of(0) : 0;
+    W lo[NU], hi[NU], glo[NU], ghi[NU];
+    const uint32_t ring_first = smem_u32(ring) + threadIdx.x * static_cast<uint32_t>(sizeof(W));
+    constexpr uint32_t kPiece = kRopeThreads * sizeof(W), kRow = 4 * kPiece;
+    uint32_t ring_at = ring_first;  // this pass's slots, and those of the row AHEAD of it
+    auto fetch = [&](uint32_t to) {
+        if (row_passes > 0) {
+            if (row.t < row_tokens) {
+                const uint64_t src = row_address(info[row_slot].addr[0][row.t], row.head, x_step);
+                const uint64_t dys = row_address(info[row_slot].addr[1][row.t], row.head, dy_step);
+#pragma unroll
+                for (int i = 0; i < NU; ++i)
+                    if (UNITS > 0 || lane + i * lanes < a.units) {
+                        const T* p = reinterpret_cast<const T*>(src + at.lo[i]);
+                        const T* q = reinterpret_cast<const T*>(dys + at.lo[i]);
+                        const T* p2 = reinterpret_cast<const T*>(src + at.lo[i] + at.hop(i));
+                        const T* q2 = reinterpret_cast<const T*>(dys + at.lo[i] + at.hop(i));
+                        if constexpr (RING) {
+                            copy_own<sizeof(W)>(to, p, a.status);
+                            copy_own<sizeof(W)>(to + kPiece, p2, a.status);
+                            copy_own<sizeof(W)>(to + 2 * kPiece, q, a.status);
+                            copy_own<sizeof(W)>(to + 3 * kPiece, q2, a.status);
+                        } else {
+                            lo[i] = X::load(p);
+                            hi[i] = X::load(p2);
+                            glo[i] = X::load(q);
+                            ghi[i] = X::load(q2);
+                        }
+                    }
             }
+            row.advance(dt, dh, heads);
+            if (--row_passes == 0 && ++row_tile < range.tiles) {
+                row.start(group, heads);
+                row_slot = info_after(row_slot);
+                row_tokens = range.count(row_tile);
+                row_passes = passes_of(row_tile);
+            }
+        }
+        if constexpr (RING) copies_commit();
     };
+    // the pass's row, once it is there
+    auto take = [&](uint32_t from) {
+        if constexpr (RING) {
+            copies_wait<AHEAD - 1>();
+            lo[0] = slot_word<W>(from);
+            hi[0] = slot_word<W>(from + kPiece);
+            glo[0] = slot_word<W>(from + 2 * kPiece);
+            ghi[0] = slot_word<W>(from + 3 * kPiece);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(ring_first + i * kRow);
     // fill_weights is complete: this lane's weights, in registers
     float2 wf[NU][P], ws[NU][P];
 #pragma unroll
     for (int i = 0; i < NU; ++i)
         if (UNITS > 0 || lane + i * lanes < a.units)
             read_table<E, UNITS>(wtab, a.units, lane + i * lanes, wf[i], ws[i]);
-    RowCursor row;
-    row.start(group, heads);
-    if (range.tiles > 0) {
-        load(row, range.count(0), info[0]);
-        fill_angles<T, E>(a, pair, tabs, info[0], range.count(0));
-    }
-    int buf = 0, slot = 0;
+    if (range.tiles > 0) fill_angles<T, E, ADJ>(a, pair, tabs, info[0], range.count(0));
+    int buf = 0, slot = 0, fill = AHEAD;
 #pragma unroll 1
     for (int tile = 0; tile < range.tiles; ++tile, buf ^= 1) {
         const int tokens = range.count(tile);
         const bool more = tile + 1 < range.tiles;
-        const int after = slot == 2 ? 0 : slot + 1;
+        const int after = info_after(slot);
         const float* tab = tabs + buf * a.tile * D;
-        if (more) {
-            store_info(a, info[after], fetched);
-            fetched = fetch_info(a, range, tile + 2, mine);
+        if (tile + AHEAD < range.tiles) {
+            store_info(a, info[fill], next_info);
+            next_info = fetch_info(a, range, tile + AHEAD + 1, mine);
+            fill = info_after(fill);
         }
         __syncthreads();  // this tile's table is filled; the other one's readers are done
         if (more)
-            fill_angles<T, E>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[after], range.count(tile + 1));
-        const int passes = (tokens * heads + groups - 1) / groups;
-        for (int pass = 0; pass < passes; ++pass) {
-            const RowCursor cur = row;
+            fill_angles<T, E, ADJ>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[after], range.count(tile + 1));
+        const int passes = passes_of(tile);
+        RowCursor cur;
+        cur.start(group, heads);
+#pragma unroll 1
+        for (int pass = 0; pass < passes; ++pass, cur.advance(dt, dh, heads)) {
             const bool live = cur.t < tokens;
+            take(ring_at);
             W xl[NU], xh[NU];
             float2 gf[NU][P], gs[NU][P];
 #pragma unroll
@@ -663,13 +746,8 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
                 X::unpack(ghi[i], h);
                 split_pairs<E, ADJ>(l, h, gf[i], gs[i]);
             }
-            if (pass + 1 < passes) {
-                row.advance(dt, dh, heads);
-                load(row, tokens, info[slot]);
-            } else if (more) {
-                row.start(group, heads);
-                load(row, range.count(tile + 1), info[after]);
-            }
+            fetch(ring_at);
+            if constexpr (RING) ring_at = ring_at == ring_first + (AHEAD - 1) * kRow ? ring_first : ring_at + kRow;
             float2 ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
@@ -724,6 +802,7 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
         slot = after;
     }
     // the groups' shares, in the tables' space, added in ascending group order
+    if constexpr (RING) copies_wait<0>();
     allow_dependent_launch();
     float* part = tabs;  // [groups][D]
     __syncthreads();
@@ -734,7 +813,7 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             int p, q;
-            pair_members<ADJ>(a, u * E + e, p, q);
+            pair_members<ADJ>(a, pair_at<E, ADJ>(a.units, u, e), p, q);
             part[group * D + p] = e % 2 ? dwf[i][e / 2].y : dwf[i][e / 2].x;
             part[group * D + q] = e % 2 ? dws[i][e / 2].y : dws[i][e / 2].x;
         }
