@@ -50,7 +50,7 @@ void shape_of(RopeArgs* a, int e) {
 // Shared memory of the backward: rows on the way, weights, then the larger of
 // the two angle tables and the groups' shares of dw.
 int bwd_smem(const RopeArgs& a, int e, int dtype) {
-    return (e >= 4 ? kRopeRingWords * e * dtype_size(dtype) : 0) +
+    return (e >= 4 ? kRopeBwdWords * e * dtype_size(dtype) : 0) +
            a.head_dim * 4 * (1 + std::max(2 * a.tile, kRopeThreads / a.lanes));
 }
 
@@ -67,7 +67,7 @@ cudaError_t allow_smem(const DeviceInfo& dev, RopeFn fn) {
     for (int i = 0; i < n; ++i)
         if (done[i].device == dev.device && done[i].fn == fn) return cudaSuccess;
     const cudaError_t err = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRopeBwdSmem);
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRopeMaxSmem);
     if (err == cudaSuccess && n < 256) done[n++] = {dev.device, fn};
     return err;
 }
@@ -100,14 +100,17 @@ cudaError_t rope_fwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, Rop
     if (a.tile == 1)
         a.splits = static_cast<int>(std::max<int64_t>(
             1, std::min<int64_t>(cdiv(heads, groups), 2 * dev.sm_count / a.tokens)));
-    const int64_t per_sm = e >= 4 ? 4 : 3;  // what the kernels' launch bounds leave room for
-    const int blocks = static_cast<int>(std::min<int64_t>(cdiv(a.tokens, a.tile), per_sm * dev.sm_count));
-    const int smem = a.head_dim * 4 * (2 * a.tile + (norm ? 2 : 0));
-    return launch_pdl(kernel_for(dtype, e, a.units, false, adjacent, norm),
-                      blocks * a.splits, kRopeThreads, smem, 1, s, a);
+    const int blocks = static_cast<int>(
+        std::min<int64_t>(cdiv(a.tokens, a.tile), static_cast<int64_t>(kRopeBlocks) * dev.sm_count));
+    const int smem = (e >= 4 ? kRopeFwdWords * e * dtype_size(dtype) : 0) +
+                     a.head_dim * 4 * (2 * a.tile + (norm ? 2 : 0));
+    const RopeFn fn = kernel_for(dtype, e, a.units, false, adjacent, norm);
+    const cudaError_t err = allow_smem(dev, fn);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(fn, blocks * a.splits, kRopeThreads, smem, 1, s, a);
 }
 
-int rope_bwd_max_rows(const DeviceInfo& dev) { return kRopeBwdBlocks * dev.sm_count + 2; }
+int rope_bwd_max_rows(const DeviceInfo& dev) { return kRopeBlocks * dev.sm_count + 2; }
 
 cudaError_t rope_bwd_rows(const DeviceInfo& dev, int dtype, bool adjacent, const RopeArgs& in,
                           int rows[2]) {

@@ -8,12 +8,13 @@ namespace rmsn {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxTile = 32;  // tokens of a tile
-constexpr int kRopeBwdBlocks = 2;  // blocks an SM holds in the backward
-constexpr int kRopeBwdAhead = 3;   // rows a thread's copies run ahead in the backward
-
-// Pieces of a backward block's rows on the way: two of x and two of dy a thread.
-constexpr int kRopeRingWords = kRopeBwdAhead * 4 * kRopeThreads;
-constexpr int kRopeBwdSmem = 100 * 1024;  // of a backward block at most
+constexpr int kRopeBlocks = 2;    // blocks an SM holds
+constexpr int kRopeFwdAhead = 3;  // rows a thread's copies run ahead
+constexpr int kRopeBwdAhead = 2;
+// Pieces of a block's rows on the way: two a tensor and thread.
+constexpr int kRopeFwdWords = kRopeFwdAhead * 2 * kRopeThreads;
+constexpr int kRopeBwdWords = kRopeBwdAhead * 4 * kRopeThreads;
+constexpr int kRopeMaxSmem = 80 * 1024;  // dynamic shared memory of a block at most
 
 using RopeFn = void (*)(const RopeArgs);
 // The kernel for pieces of e elements and `units` units a head.

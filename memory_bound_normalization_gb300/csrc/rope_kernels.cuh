@@ -244,9 +244,9 @@ __device__ __forceinline__ int64_t token_offset(const RopeArgs& a, int64_t batch
 }
 
 // What a block knows of a tile of tokens: the tokens' addresses in up to four
-// tensors and their positions. Three of them in turn: while the block's
-// slowest warp still reads this tile's and the next one's, the one after is
-// written.
+// tensors and their positions. Two more of them than rows ahead: while the
+// block's slowest warp still reads those of a tile and of the tiles of its rows
+// ahead, the one after is written.
 constexpr int kTensors = 4;
 struct TileInfo {
     int64_t addr[kTensors][kRopeMaxTile];
@@ -427,20 +427,31 @@ struct RowCursor {
 // Both kernels are persistent: a block strides over tiles of tokens. The
 // angles of the next tile are filled into the other of two tables before this
 // tile's rows are worked on, so one barrier a tile is enough; each group of
-// lanes takes rows (token, head), the next row's loads issued before the
-// current one is worked on, across tiles too.
+// lanes takes rows (token, head). Pieces of 16 or 8 bytes are copied some rows
+// ahead, across tiles, into the thread's own slots of shared memory: the next
+// rows alone, in registers, do not fill DRAM's latency, and more of them would
+// cost warps. With two blocks an SM, 48 KB on the way an SM (three rows of the
+// forward) and 64 KB (two of the backward) did best, and more is worse again:
+// 16384 tokens of 40 bf16 heads of 128 forward (336 MB) take 58 us with one row
+// (four blocks an SM), 56 with three and 60 with four; the backward of 32768
+// (1 GB) takes 194 us with one, 157 with two, 167 with three, 179 with four.
+// A row ahead may lie as many tiles ahead, whose addresses are kept for it.
 
 // ------------------------------------------------------------------ forward
-// With few tokens the blocks of a tile share out its heads.
+// A token's rows are the heads of q, then those of k. With few tokens the blocks
+// of a tile share out its heads.
 template <typename T, int E, bool ADJ, bool NORM, int UNITS>
-__global__ void __launch_bounds__(kRopeThreads, E >= 4 ? 4 : 3) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int NU = UNITS > 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
     const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
     using X = Elems<T, E>;
     using W = typename X::W;
-    __shared__ TileInfo info[3];
-    float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem);  // [2][D] when NORM
-    float* tabs = wtab + (NORM ? 2 * D : 0);            // [2][tile][D]
+    constexpr bool RING = E >= 4;
+    constexpr int AHEAD = RING ? kRopeFwdAhead : 1, SLOTS = AHEAD + 2;
+    constexpr int RING_BYTES = RING ? kRopeFwdWords * static_cast<int>(sizeof(W)) : 0;
+    __shared__ TileInfo info[SLOTS];
+    float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem + RING_BYTES);  // [2][D] when NORM
+    float* tabs = wtab + (NORM ? 2 * D : 0);                                 // [2][tile][D]
     const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
     const int groups = kRopeThreads / lanes;
 
@@ -456,132 +467,150 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? 4 : 3) rope_fwd_kernel(
     // heads [h0, h0 + heads) of each token of either tensor
     const int qh0 = a.t[0].heads * split / a.splits, kh0 = a.t[1].heads * split / a.splits;
     const int qheads = a.t[0].heads * (split + 1) / a.splits - qh0;
-    const int kheads = a.t[1].heads * (split + 1) / a.splits - kh0;
+    const int heads = qheads + a.t[1].heads * (split + 1) / a.splits - kh0;
+    const int dt = groups / heads, dh = groups - dt * heads;
     Pieces<T, E, ADJ, UNITS> at;
     at.start(a, lane, lanes);
     const float inv_d = 1.f / static_cast<float>(D);
     wait_for_prerequisite_grid();  // no global access before this
 
-    int64_t fetched = fetch_info(a, range, 0, mine);
+    int64_t fetched[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetched[i] = fetch_info(a, range, i, mine);
     const PairOf pair = pair_of(a);
     if constexpr (NORM) {
         fill_weights<T, E, ADJ>(a, a.t[0].w, wtab);
         if (a.t[1].heads > 0) fill_weights<T, E, ADJ>(a, a.t[1].w, wtab + D);
     }
-    store_info(a, info[0], fetched);
-    fetched = fetch_info(a, range, 1, mine);
-    __syncthreads();
-    RowCursor row{0, 0};
-    W lo[NU], hi[NU];
-    auto load = [&](int tokens, const int64_t* addr, int h0, uint32_t head_step) {
-        if (row.t >= tokens) return;
-        const uint64_t src = row_address(addr[row.t], h0 + row.head, head_step);
 #pragma unroll
-        for (int i = 0; i < NU; ++i)
-            if (UNITS > 0 || lane + i * lanes < a.units) {
-                const uint64_t p = src + at.lo[i];
-                lo[i] = X::load(reinterpret_cast<const T*>(p));
-                hi[i] = X::load(reinterpret_cast<const T*>(p + at.hop(i)));
+    for (int i = 0; i < AHEAD; ++i) store_info(a, info[i], fetched[i]);
+    int64_t next_info = fetch_info(a, range, AHEAD, mine);
+    __syncthreads();
+    auto passes_of = [&](int tile) { return (range.count(tile) * heads + groups - 1) / groups; };
+    auto info_after = [](int slot) { return slot == SLOTS - 1 ? 0 : slot + 1; };
+    // The row to fetch next: of which tile, and how many passes that still has.
+    RowCursor row;
+    row.start(group, heads);
+    int row_tile = 0, row_slot = 0, row_passes = passes_of(0);
+    W lo[NU], hi[NU];
+    const uint32_t ring_first = smem_u32(rmsn_dynamic_smem) + threadIdx.x * static_cast<uint32_t>(sizeof(W));
+    constexpr uint32_t kPiece = kRopeThreads * sizeof(W), kRow = 2 * kPiece;
+    uint32_t ring_at = ring_first;  // this pass's slots, and those of the row AHEAD of it
+    auto fetch = [&](uint32_t to) {
+        if (row_passes > 0) {
+            if (row.t < range.count(row_tile)) {
+                const bool second = row.head >= qheads;
+                const uint64_t src =
+                    row_address(info[row_slot].addr[second ? 2 : 0][row.t], row.head + (second ? kh0 - qheads : qh0),
+                                static_cast<uint32_t>((second ? a.t[1].xs[2] : a.t[0].xs[2]) * sizeof(T)));
+#pragma unroll
+                for (int i = 0; i < NU; ++i)
+                    if (UNITS > 0 || lane + i * lanes < a.units) {
+                        const uint64_t p = src + at.lo[i], p2 = p + at.hop(i);
+                        if constexpr (RING) {
+                            copy_own<sizeof(W)>(to, reinterpret_cast<const void*>(p), a.status);
+                            copy_own<sizeof(W)>(to + kPiece, reinterpret_cast<const void*>(p2), a.status);
+                        } else {
+                            lo[i] = X::load(reinterpret_cast<const T*>(p));
+                            hi[i] = X::load(reinterpret_cast<const T*>(p2));
+                        }
+                    }
             }
+            row.advance(dt, dh, heads);
+            if (--row_passes == 0 && ++row_tile < range.tiles) {
+                row.start(group, heads);
+                row_slot = info_after(row_slot);
+                row_passes = passes_of(row_tile);
+            }
+        }
+        if constexpr (RING) copies_commit();
     };
-    // starts on the rows of tensor w of a tile
-    auto begin = [&](int w, int tokens, const TileInfo& from) {
-        const int h0 = w ? kh0 : qh0, n = w ? kheads : qheads;
-        row.start(group, max(n, 1));
-        load(n > 0 ? tokens : 0, from.addr[2 * w], h0,
-             static_cast<uint32_t>(a.t[w].xs[2] * sizeof(T)));
-    };
-    begin(0, range.count(0), info[0]);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(ring_first + i * kRow);
     fill_angles<T, E, ADJ>(a, pair, tabs, info[0], range.count(0));
-    int buf = 0, slot = 0;
-    const int tensors = a.t[1].heads > 0 ? 2 : 1;
+    int buf = 0, slot = 0, fill = AHEAD;
 #pragma unroll 1
     for (int tile = 0; tile < range.tiles; ++tile, buf ^= 1) {
         const int tokens = range.count(tile);
-        const bool more = tile + 1 < range.tiles;
-        const int after = slot == 2 ? 0 : slot + 1;
         const float* tab = tabs + buf * a.tile * D;
-        if (more) {
-            store_info(a, info[after], fetched);
-            fetched = fetch_info(a, range, tile + 2, mine);
+        if (tile + AHEAD < range.tiles) {
+            store_info(a, info[fill], next_info);
+            next_info = fetch_info(a, range, tile + AHEAD + 1, mine);
+            fill = info_after(fill);
         }
         __syncthreads();  // this tile's table is filled; the other one's readers are done
-        if (more)
-            fill_angles<T, E, ADJ>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[after], range.count(tile + 1));
+        if (tile + 1 < range.tiles)
+            fill_angles<T, E, ADJ>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[info_after(slot)],
+                                   range.count(tile + 1));
+        const int passes = passes_of(tile);
+        RowCursor cur;
+        cur.start(group, heads);
 #pragma unroll 1
-        for (int w = 0; w < tensors; ++w) {
-            const int h0 = w ? kh0 : qh0, heads = w ? kheads : qheads;
-            const int dt = heads > 0 ? groups / heads : 0, dh = groups - dt * heads;
-            const uint32_t in_step = static_cast<uint32_t>(a.t[w].xs[2] * sizeof(T));
-            const uint32_t out_step = static_cast<uint32_t>(a.t[w].os[2] * sizeof(T));
-            const int64_t* in_addr = info[slot].addr[2 * w];
-            const int64_t* out_addr = info[slot].addr[2 * w + 1];
-            const int passes = (tokens * heads + groups - 1) / groups;
-#pragma unroll 1
-            for (int pass = 0; pass < max(passes, 1); ++pass) {
-                const RowCursor cur = row;
-                const bool live = cur.t < tokens && pass < passes;
-                float2 f[NU][P], s[NU][P];
+        for (int pass = 0; pass < passes; ++pass, cur.advance(dt, dh, heads)) {
+            const bool live = cur.t < tokens, second = cur.head >= qheads;
+            if constexpr (RING) {
+                copies_wait<AHEAD - 1>();
+                lo[0] = slot_word<W>(ring_at);
+                hi[0] = slot_word<W>(ring_at + kPiece);
+            }
+            float2 f[NU][P], s[NU][P];
 #pragma unroll
-                for (int i = 0; i < NU; ++i) {
-                    float2 l[P], h[P];
-                    X::unpack(lo[i], l);
-                    X::unpack(hi[i], h);
-                    split_pairs<E, ADJ>(l, h, f[i], s[i]);
-                }
-                if (pass + 1 < passes) {
-                    row.advance(dt, dh, heads);
-                    load(tokens, in_addr, h0, in_step);
-                } else if (w + 1 < tensors) {
-                    begin(w + 1, tokens, info[slot]);
-                } else if (more) {
-                    begin(0, range.count(tile + 1), info[after]);
-                }
-                if constexpr (NORM) {
-                    float2 ss = make_float2(0.f, 0.f);
+            for (int i = 0; i < NU; ++i) {
+                float2 l[P], h[P];
+                X::unpack(lo[i], l);
+                X::unpack(hi[i], h);
+                split_pairs<E, ADJ>(l, h, f[i], s[i]);
+            }
+            fetch(ring_at);
+            if constexpr (RING) ring_at = ring_at == ring_first + (AHEAD - 1) * kRow ? ring_first : ring_at + kRow;
+            if constexpr (NORM) {
+                float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int i = 0; i < NU; ++i)
-                        if (live && (UNITS > 0 || lane + i * lanes < a.units)) {
+                for (int i = 0; i < NU; ++i)
+                    if (live && (UNITS > 0 || lane + i * lanes < a.units)) {
 #pragma unroll
-                            for (int e = 0; e < P; ++e)
-                                ss = __ffma2_rn(f[i][e], f[i][e], __ffma2_rn(s[i][e], s[i][e], ss));
-                        }
-                    const float2 rs = f2_splat(rsqrtf(lanes_sum<UNITS>(ss.x + ss.y, lanes) * inv_d + a.eps));
-#pragma unroll
-                    for (int i = 0; i < NU; ++i)
-                        if (live && (UNITS > 0 || lane + i * lanes < a.units)) {
-                            float2 wf[P], ws[P];
-                            read_table<E, UNITS>(wtab + w * D, a.units, lane + i * lanes, wf, ws);
-#pragma unroll
-                            for (int e = 0; e < P; ++e) {
-                                f[i][e] = __fmul2_rn(__fmul2_rn(f[i][e], rs), wf[e]);
-                                s[i][e] = __fmul2_rn(__fmul2_rn(s[i][e], rs), ws[e]);
-                            }
-                        }
-                }
-                if (!live) continue;
-                const uint64_t dst = row_address(out_addr[cur.t], h0 + cur.head, out_step);
-#pragma unroll
-                for (int i = 0; i < NU; ++i) {
-                    if (UNITS == 0 && lane + i * lanes >= a.units) continue;
-                    float2 c[P], n[P], yf[P], ys[P], yl[P], yh[P];
-                    read_table<E, UNITS>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
-#pragma unroll
-                    for (int e = 0; e < P; ++e) turn(f[i][e], s[i][e], c[e], n[e], yf[e], ys[e]);
-                    join_pairs<E, ADJ>(yf, ys, yl, yh);
-                    W* dl = reinterpret_cast<W*>(dst + at.lo[i]);
-                    W* dhi = reinterpret_cast<W*>(dst + at.lo[i] + at.hop(i));
-                    if (RMSN_OK(span_in(dl, sizeof(W), a.t[w].out, extent_bytes(a, a.t[w], a.t[w].os, sizeof(T))) &&
-                                    span_in(dhi, sizeof(W), a.t[w].out, extent_bytes(a, a.t[w], a.t[w].os, sizeof(T))),
-                                a.status)) {
-                        *dl = X::pack(yl);
-                        *dhi = X::pack(yh);
+                        for (int e = 0; e < P; ++e)
+                            ss = __ffma2_rn(f[i][e], f[i][e], __ffma2_rn(s[i][e], s[i][e], ss));
                     }
+                const float2 rs = f2_splat(rsqrtf(lanes_sum<UNITS>(ss.x + ss.y, lanes) * inv_d + a.eps));
+#pragma unroll
+                for (int i = 0; i < NU; ++i)
+                    if (live && (UNITS > 0 || lane + i * lanes < a.units)) {
+                        float2 wf[P], ws[P];
+                        read_table<E, UNITS>(wtab + (second ? D : 0), a.units, lane + i * lanes, wf, ws);
+#pragma unroll
+                        for (int e = 0; e < P; ++e) {
+                            f[i][e] = __fmul2_rn(__fmul2_rn(f[i][e], rs), wf[e]);
+                            s[i][e] = __fmul2_rn(__fmul2_rn(s[i][e], rs), ws[e]);
+                        }
+                    }
+            }
+            if (!live) continue;
+            const uint64_t dst =
+                row_address(info[slot].addr[second ? 3 : 1][cur.t], cur.head + (second ? kh0 - qheads : qh0),
+                            static_cast<uint32_t>((second ? a.t[1].os[2] : a.t[0].os[2]) * sizeof(T)));
+#pragma unroll
+            for (int i = 0; i < NU; ++i) {
+                if (UNITS == 0 && lane + i * lanes >= a.units) continue;
+                float2 c[P], n[P], yf[P], ys[P], yl[P], yh[P];
+                read_table<E, UNITS>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
+#pragma unroll
+                for (int e = 0; e < P; ++e) turn(f[i][e], s[i][e], c[e], n[e], yf[e], ys[e]);
+                join_pairs<E, ADJ>(yf, ys, yl, yh);
+                W* dl = reinterpret_cast<W*>(dst + at.lo[i]);
+                W* dhi = reinterpret_cast<W*>(dst + at.lo[i] + at.hop(i));
+                [[maybe_unused]] const RopeTensor& x = a.t[second ? 1 : 0];
+                if (RMSN_OK(span_in(dl, sizeof(W), x.out, extent_bytes(a, x, x.os, sizeof(T))) &&
+                                span_in(dhi, sizeof(W), x.out, extent_bytes(a, x, x.os, sizeof(T))),
+                            a.status)) {
+                    *dl = X::pack(yl);
+                    *dhi = X::pack(yh);
                 }
             }
         }
-        slot = after;
+        slot = info_after(slot);
     }
+    if constexpr (RING) copies_wait<0>();
     allow_dependent_launch();
 }
 
@@ -590,13 +619,8 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? 4 : 3) rope_fwd_kernel(
 // their lanes' shares of dw in registers; at the end the groups' shares are
 // added in a fixed order into the block's partial row. No floating-point
 // atomics.
-//
-// 128 registers a thread leave 16 warps an SM, whose next rows alone (32 KB on
-// the way) do not fill DRAM's latency: pieces of 16 or 8 bytes are copied
-// kRopeBwdAhead rows ahead into the thread's own slots of shared memory. A row
-// ahead may lie as many tiles ahead, whose addresses are kept for it.
 template <typename T, int E, bool ADJ, int UNITS>
-__global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int NU = UNITS > 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
     const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
@@ -604,11 +628,8 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
     using W = typename X::W;
     constexpr bool RING = E >= 4;
     constexpr int AHEAD = RING ? kRopeBwdAhead : 1, SLOTS = AHEAD + 2;
-    constexpr int RING_BYTES = RING ? kRopeRingWords * static_cast<int>(sizeof(W)) : 0;
-    // While the block's slowest warp still reads the infos of a tile and of the
-    // AHEAD tiles after it, one more is written.
+    constexpr int RING_BYTES = RING ? kRopeBwdWords * static_cast<int>(sizeof(W)) : 0;
     __shared__ TileInfo info[SLOTS];
-    uint4* ring = reinterpret_cast<uint4*>(rmsn_dynamic_smem);
     float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem + RING_BYTES);
     float* tabs = wtab + D;  // [2][tile][D]
     const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
@@ -656,7 +677,7 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
     int row_tile = 0, row_slot = 0, row_tokens = range.tiles > 0 ? range.count(0) : 0;
     int row_passes = range.tiles > 0 ? passes_of(0) : 0;
     W lo[NU], hi[NU], glo[NU], ghi[NU];
-    const uint32_t ring_first = smem_u32(ring) + threadIdx.x * static_cast<uint32_t>(sizeof(W));
+    const uint32_t ring_first = smem_u32(rmsn_dynamic_smem) + threadIdx.x * static_cast<uint32_t>(sizeof(W));
     constexpr uint32_t kPiece = kRopeThreads * sizeof(W), kRow = 4 * kPiece;
     uint32_t ring_at = ring_first;  // this pass's slots, and those of the row AHEAD of it
     auto fetch = [&](uint32_t to) {
@@ -718,7 +739,6 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
     for (int tile = 0; tile < range.tiles; ++tile, buf ^= 1) {
         const int tokens = range.count(tile);
         const bool more = tile + 1 < range.tiles;
-        const int after = info_after(slot);
         const float* tab = tabs + buf * a.tile * D;
         if (tile + AHEAD < range.tiles) {
             store_info(a, info[fill], next_info);
@@ -727,7 +747,7 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
         }
         __syncthreads();  // this tile's table is filled; the other one's readers are done
         if (more)
-            fill_angles<T, E, ADJ>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[after], range.count(tile + 1));
+            fill_angles<T, E, ADJ>(a, pair, tabs + (buf ^ 1) * a.tile * D, info[info_after(slot)], range.count(tile + 1));
         const int passes = passes_of(tile);
         RowCursor cur;
         cur.start(group, heads);
@@ -799,7 +819,7 @@ __global__ void __launch_bounds__(kRopeThreads, E >= 4 ? kRopeBwdBlocks : 2)
                 }
             }
         }
-        slot = after;
+        slot = info_after(slot);
     }
     // the groups' shares, in the tables' space, added in ascending group order
     if constexpr (RING) copies_wait<0>();
