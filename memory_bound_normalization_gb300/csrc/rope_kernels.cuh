@@ -117,10 +117,11 @@ __device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t turns) {
 // hold D floats: two pairs a 16-byte word, firsts before seconds, so that they
 // load as the float2 values they multiply; lanes of a group read consecutive
 // words and do not conflict.
-// UNITS, where it is not 0, is the number of units of a head, a power of two and
-// the lanes of a group: table offsets, lane masks and the row sum's steps are
-// then constants. (Left to run time, they and the kernel parameters reloaded
-// for them made up half of the forward's instructions.)
+// UNITS, where it is positive, is the number of units of a head, a power of two
+// and the lanes of a group: table offsets, lane masks and the row sum's steps
+// are then constants. (Left to run time, they and the kernel parameters reloaded
+// for them made up half of the forward's instructions.) Negative, it is minus the
+// lanes of a group, some of which may have no unit.
 //
 // A unit is the E pairs that a lane takes at once, from two pieces of E elements:
 // the pairs' first elements and their second ones; where pairs are neighbours,
@@ -221,8 +222,8 @@ __device__ __forceinline__ void join_pairs(const float2 (&f)[(E + 1) / 2], const
 
 template <int UNITS>
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
-    if constexpr (UNITS > 0) {
-        return group_allreduce<UNITS>(v);
+    if constexpr (UNITS != 0) {
+        return group_allreduce<(UNITS > 0 ? UNITS : -UNITS)>(v);
     } else {
 #pragma unroll
         for (int off = 16; off >= 1; off /= 2)
@@ -386,7 +387,7 @@ template <int E> constexpr int kUnitsPerLane = E >= 4 ? 1 : kRopeMaxPairs / 32 /
 // distance from it.
 template <typename T, int E, bool ADJ, int UNITS>
 struct Pieces {
-    static constexpr int NU = UNITS > 0 ? 1 : kUnitsPerLane<E>;
+    static constexpr int NU = UNITS != 0 ? 1 : kUnitsPerLane<E>;
     int lo[NU], gap[NU];
     __device__ __forceinline__ void start(const RopeArgs& a, int lane, int lanes) {
 #pragma unroll
@@ -442,8 +443,8 @@ struct RowCursor {
 // of a tile share out its heads.
 template <typename T, int E, bool ADJ, bool NORM, int UNITS>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
-    constexpr int NU = UNITS > 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
-    const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
+    constexpr int NU = UNITS != 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
+    const int lanes = UNITS != 0 ? abs(UNITS) : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
     using X = Elems<T, E>;
     using W = typename X::W;
     constexpr bool RING = E >= 4;
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
                             static_cast<uint32_t>((second ? a.t[1].os[2] : a.t[0].os[2]) * sizeof(T)));
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                if (UNITS == 0 && lane + i * lanes >= a.units) continue;
+                if (UNITS <= 0 && lane + i * lanes >= a.units) continue;
                 float2 c[P], n[P], yf[P], ys[P], yl[P], yh[P];
                 read_table<E, UNITS>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
 #pragma unroll
@@ -622,8 +623,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
 template <typename T, int E, bool ADJ, int UNITS>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
-    constexpr int NU = UNITS > 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
-    const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
+    constexpr int NU = UNITS != 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
+    const int lanes = UNITS != 0 ? abs(UNITS) : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
     using X = Elems<T, E>;
     using W = typename X::W;
     constexpr bool RING = E >= 4;
@@ -771,7 +772,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
             float2 ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                if (!live || (UNITS == 0 && lane + i * lanes >= a.units)) continue;
+                if (!live || (UNITS <= 0 && lane + i * lanes >= a.units)) continue;
                 float2 l[P], h[P], f[P], s[P], c[P], n[P];
                 X::unpack(xl[i], l);
                 X::unpack(xh[i], h);
@@ -795,7 +796,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
             const uint64_t dst = row_address(info[slot].addr[2][cur.t], cur.head, out_step);
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                if (UNITS == 0 && lane + i * lanes >= a.units) continue;
+                if (UNITS <= 0 && lane + i * lanes >= a.units) continue;
                 float2 l[P], h[P], f[P], s[P];
                 X::unpack(xl[i], l);
                 X::unpack(xh[i], h);
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
         const int u = lane + i * lanes;
-        if (UNITS == 0 && u >= a.units) continue;
+        if (UNITS <= 0 && u >= a.units) continue;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             int p, q;
@@ -858,12 +859,14 @@ RopeFn kernel_of(bool bwd, bool adjacent, bool norm) {
 }
 template <typename T>
 RopeFn kernel_for_type(int e, int units, bool bwd, bool adjacent, bool norm) {
-    // 16-byte pieces of heads of 64, 128 and 256: constant geometry
+    // 16-byte pieces of heads of 64, 128 and 256: constant geometry; of heads
+    // between 64 and 128: a constant number of lanes
     constexpr int E = 16 / sizeof(T), U = 32 / E;
     if (e == E) {
         if (units == U) return kernel_of<T, E, U>(bwd, adjacent, norm);
         if (units == 2 * U) return kernel_of<T, E, 2 * U>(bwd, adjacent, norm);
         if (units == 4 * U) return kernel_of<T, E, 4 * U>(bwd, adjacent, norm);
+        if (units > U && units < 2 * U) return kernel_of<T, E, -2 * U>(bwd, adjacent, norm);
         return kernel_of<T, E, 0>(bwd, adjacent, norm);
     }
     if constexpr (E != 4)
