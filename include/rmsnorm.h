@@ -281,7 +281,8 @@ typedef struct {
  * of 0: nothing to do. With k_heads 0 the key pointers are not looked at, with
  * q_heads 0 the query's.
  * RMSNORM_ERR_INVALID_ARG: a descriptor outside the limits above, a negative
- * stride, 2^31 or more tokens, a NULL pointer, one weight without the other
+ * stride, an output with stride 0 over more than one element or at its input's
+ * address with other strides, 2^31 or more tokens, a NULL pointer, one weight without the other
  * (when both tensors have heads), eps negative or NaN.
  */
 int rmsnorm_qk_rope_fwd(const rmsnorm_rope_t *rope, const void *q,
@@ -342,12 +343,14 @@ typedef enum {
  *   z = (x - mean) * rstd * w_c + b_c,  y = act(z)
  * Reads x, w and b [C] (both NULL: 1 and 0); writes y and, in fp32, mean and
  * rstd [B, G]. dtype names the types of x, y and of w and b as for the norm.
- * The statistics are taken about local means (no digits lost to a mean far
- * from zero) and are deterministic.
+ * The statistics are taken about local values (no digits lost to a mean far
+ * from zero) and are deterministic. y must not overlap x.
  * B == 0 or S == 0: nothing to do (mean and rstd of empty slabs are left as
  * they are). B, S < 0, C <= 0 or C > 2^31-1, G <= 0, C % G != 0, S * (C/G) >=
- * 2^31, a negative or NaN eps, an unknown activation, a NULL pointer, or one
- * of w and b without the other: RMSNORM_ERR_INVALID_ARG. A workspace comes
+ * 2^31, more (sample, group) pairs than a grid has blocks (2^31-1 over up to
+ * 64 blocks a pair), a negative or NaN eps, an unknown activation, a NULL
+ * pointer, or one of w and b without the other: RMSNORM_ERR_INVALID_ARG. A
+ * workspace comes
  * from the stream-ordered allocator where the slab is split over many blocks
  * (RMSNORM_ERR_NOMEM).
  */
@@ -375,9 +378,9 @@ int rmsnorm_group_norm_bwd(const void *x, const void *w, const void *b,
  * rmsnorm_group_norm_fwd and _bwd with a caller-provided workspace: device
  * memory of at least rmsnorm_group_norm_workspace_size(B, S, C, G, dtype,
  * backward, current device) bytes, 16-byte aligned, not shared with another
- * call in flight. A smaller or NULL one where some is needed returns
- * RMSNORM_ERR_INVALID_ARG, a misaligned one RMSNORM_ERR_MISALIGNED. They
- * allocate nothing.
+ * call in flight. One smaller than the call at hand needs (which may be less
+ * than that size, or nothing) returns RMSNORM_ERR_INVALID_ARG, a misaligned one
+ * RMSNORM_ERR_MISALIGNED. They allocate nothing.
  */
 int rmsnorm_group_norm_fwd_ws(const void *x, const void *w, const void *b,
                               void *y, float *mean, float *rstd, int64_t B,
@@ -402,7 +405,8 @@ size_t rmsnorm_group_norm_workspace_size(int64_t B, int64_t S, int64_t C,
 
 /*
  * Device-side status. Every wait inside the kernels (on a bulk copy landing
- * in shared memory) is bounded in time; a wait that runs out records
+ * in shared memory, or on the other blocks of a group norm's slab) is bounded
+ * in time; a wait that runs out records
  * RMSNORM_ERR_DEVICE_TIMEOUT in a status word on the device and the kernel
  * returns early instead of hanging. In the checked debug build (compiled
  * with RMSNORM_CHECKS) a kernel access outside its tensor, workspace or
@@ -427,7 +431,9 @@ void rmsnorm_set_wait_limit_ns(uint64_t ns);
  * that stages rows through bulk copies (a backward, or a forward that takes
  * the persistent ring kernel) will not issue the copy of unit `unit` (a
  * row, or a tile of rows for short rows), so the wait for it runs out and
- * the status word reads RMSNORM_ERR_DEVICE_TIMEOUT. Outputs of that call are
+ * the status word reads RMSNORM_ERR_DEVICE_TIMEOUT. A group norm whose slabs
+ * are split over blocks that wait for one another takes it as well: a block
+ * does not report its share of slab `unit`. Outputs of that call are
  * unspecified. One-shot; -1 cancels.
  */
 void rmsnorm_test_drop_copy(int64_t unit);

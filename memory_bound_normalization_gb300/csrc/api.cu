@@ -236,6 +236,16 @@ int rope_tensor(const void* p, const rmsnorm_strides_t& s, int size, int64_t (&o
     return RMSNORM_OK;
 }
 
+// Whether a dimension of more than one element has stride 0.
+bool overlaps_itself(const rmsnorm_rope_t* r, const rmsnorm_strides_t& s, int heads) {
+    return (r->batch > 1 && s.batch == 0) || (r->length > 1 && s.token == 0) || (heads > 1 && s.head == 0);
+}
+// Whether two tensors at one address lie differently.
+bool differ(const rmsnorm_rope_t* r, const rmsnorm_strides_t& s, const rmsnorm_strides_t& t, int heads) {
+    return (r->batch > 1 && s.batch != t.batch) || (r->length > 1 && s.token != t.token) ||
+           (heads > 1 && s.head != t.head);
+}
+
 // Both directions of the rotary call, the descriptor checked and tokens > 0.
 // Without weights the backward is the forward of the gradient with the angle
 // turned back.
@@ -270,8 +280,12 @@ int rope_run(const rmsnorm_rope_t* r, RopeArgs& a, const void* q, const void* k,
             if (st != RMSNORM_OK) return st;
             (norm ? t.dy : t.x) = dy[i];
         }
-        st = rope_tensor(o[i], bwd ? *ds[i] : *ys[i], sz, t.os);
+        const rmsnorm_strides_t& os = bwd ? *ds[i] : *ys[i];
+        st = rope_tensor(o[i], os, sz, t.os);
         if (st != RMSNORM_OK) return st;
+        if (overlaps_itself(r, os, t.heads) || (o[i] == t.x && differ(r, os, bwd && !norm ? *ys[i] : *xs[i], t.heads)) ||
+            (o[i] == t.dy && differ(r, os, *ys[i], t.heads)))
+            return RMSNORM_ERR_INVALID_ARG;
         t.out = o[i];
         if (norm) {
             if (bwd && dw[i] == nullptr) return RMSNORM_ERR_INVALID_ARG;
@@ -368,6 +382,7 @@ int group_norm_run(bool bwd, GroupNormArgs& a, int64_t C, int64_t G, int dtype,
     if (st != RMSNORM_OK) return st;
     a.status = dev->status_word;
     a.wait_limit_ns = g_wait_limit_ns.load();
+    if (!group_norm_fits(*dev, dtype, vec, bwd, a)) return RMSNORM_ERR_INVALID_ARG;
     Workspace ws = given;
     st = ws.take(group_norm_workspace(*dev, dtype, vec, bwd, a), stream);
     if (st != RMSNORM_OK) return st;

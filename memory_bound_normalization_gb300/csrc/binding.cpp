@@ -427,6 +427,10 @@ PyObject* qk_rope_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
         if (!qo) {
             qo = make(q.sizes(), q.scalar_type(), q);
             if (k) ko = make(k->sizes(), q.scalar_type(), q);
+        } else {
+            // autograd is told that what it may have saved has changed
+            for (const Optional* o : {&qo, &ko})
+                if (*o && !(*o)->is_inference()) (*o)->unsafeGetTensorImpl()->bump_version();
         }
         r.d.q_out = strides(*qo);
         if (k) r.d.k_out = strides(*ko);

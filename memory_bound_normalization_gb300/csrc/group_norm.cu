@@ -229,6 +229,10 @@ int64_t partial_rows(const Plan& p, bool bwd, const GroupNormArgs& a) {
 
 }  // namespace
 
+bool group_norm_fits(const DeviceInfo& dev, int dtype, bool vec, bool bwd, const GroupNormArgs& a) {
+    return gn_scalar_fits(a) || plan_of(dev, dtype, vec, bwd, a).ok;
+}
+
 size_t group_norm_workspace(const DeviceInfo& dev, int dtype, bool vec, bool bwd,
                             const GroupNormArgs& a) {
     const Plan p = plan_of(dev, dtype, vec, bwd, a);

@@ -7,6 +7,8 @@
 
 namespace rmsn {
 
+// Whether a grid has a block for every chunk.
+bool gn_scalar_fits(const GroupNormArgs& a);
 size_t gn_scalar_workspace(bool bwd, const GroupNormArgs& a);
 cudaError_t gn_scalar_launch(int dtype, bool bwd, const GroupNormArgs& a, void* ws, cudaStream_t s);
 

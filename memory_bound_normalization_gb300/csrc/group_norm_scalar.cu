@@ -211,8 +211,6 @@ template <typename T>
 cudaError_t launch_typed(bool bwd, const GroupNormArgs& a, void* ws, cudaStream_t s) {
     const int chunks = scalar_chunks(a);
     const int64_t slabs = a.B * a.G * chunks, rows = a.B * chunks, ctiles = cdiv(a.C, 32);
-    if (slabs > INT32_MAX || rows * ctiles > INT32_MAX || rows > INT32_MAX)
-        return cudaErrorInvalidValue;
     if (!bwd) {
         float2* parts = static_cast<float2*>(ws);
         cudaError_t err = launch_pdl(&gn_scalar_stats_kernel<T>, static_cast<int>(slabs), kThreads,
@@ -241,6 +239,11 @@ cudaError_t launch_typed(bool bwd, const GroupNormArgs& a, void* ws, cudaStream_
 }
 
 }  // namespace
+
+bool gn_scalar_fits(const GroupNormArgs& a) {
+    const int64_t wide = std::max<int64_t>(a.G, cdiv(a.C, 32));  // blocks of a chunk
+    return a.B <= INT32_MAX / (wide * scalar_chunks(a));
+}
 
 size_t gn_scalar_workspace(bool bwd, const GroupNormArgs& a) {
     const size_t rows = static_cast<size_t>(a.B) * scalar_chunks(a);

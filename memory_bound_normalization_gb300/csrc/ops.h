@@ -79,6 +79,8 @@ int64_t take_drop_unit();
 // Workspace bytes of a call (0: none), and the call itself. `vec`: every
 // pointer is 16-byte aligned and a row of channels is a whole number of
 // 16-byte vectors.
+// Whether the call's blocks fit a grid.
+bool group_norm_fits(const DeviceInfo& dev, int dtype, bool vec, bool bwd, const GroupNormArgs& a);
 size_t group_norm_workspace(const DeviceInfo& dev, int dtype, bool vec, bool bwd,
                             const GroupNormArgs& a);
 cudaError_t group_norm_launch(const DeviceInfo& dev, int dtype, bool vec, bool bwd,
