@@ -3,10 +3,20 @@
 #include <algorithm>
 #include <mutex>
 
+#include "common.cuh"
 #include "group_norm.h"
 
 namespace rmsn {
 namespace {
+
+// Sets the streamed kernel's arrival counters to zero. A kernel of its own, not
+// a memset: it lets the streamed kernel start at once, which reads x meanwhile
+// and waits for the zeros only before it counts.
+__global__ void zero_kernel(unsigned* p, int n) {
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) p[i] = 0;
+}
 
 // ---------------------------------------------------------------- host side
 SlabFn kernel_for(int dtype, bool bwd, int act, SlabKind k) {
@@ -258,7 +268,9 @@ cudaError_t group_norm_launch(const DeviceInfo& dev, int dtype, bool vec, bool b
                          static_cast<int>(a.B * p.splits * p.cluster), p.threads, p.smem, p.cluster, s, g);
     } else {
         g.drop_unit = take_drop_unit();
-        err = cudaMemsetAsync(ws, 0, arrived, s);
+        const int words = static_cast<int>(a.B * p.splits);
+        err = launch_pdl(&zero_kernel, static_cast<int>(std::min<int64_t>(64, cdiv(words, 256))), 256, 0, 1, s,
+                         g.arrived, words);
         if (err != cudaSuccess) return err;
         // the blocks wait for one another: all of them run at once, or none
         cudaLaunchConfig_t cfg = {};
@@ -266,11 +278,13 @@ cudaError_t group_norm_launch(const DeviceInfo& dev, int dtype, bool vec, bool b
         cfg.blockDim = dim3(kStreamThreads);
         cfg.dynamicSmemBytes = static_cast<size_t>(p.smem);
         cfg.stream = s;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeCooperative;
         attr[0].val.cooperative = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = pdl_allowed();
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         err = cudaLaunchKernelEx(&cfg, kernel_for(dtype, bwd, a.act, SlabKind::kStream), g);
     }
     if (err != cudaSuccess || rows == 0) return err;

@@ -768,6 +768,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
         p.last_use = second && g.drop;
         return p;
     };
+    // The kernel before this one lets it start when all earlier work is done, and
+    // sets the arrival counters: nothing else has to wait for it.
     bool failed = false;  // thread 0's: a wait ran out
     Pass pass = pass_of(0, false);
 #pragma unroll
@@ -779,7 +781,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
     // Two teams: the second starts when the first has its sums, so that one
     // reads while the other, and its wait, leave DRAM to it.
     if (g.together == 2 && team == 1 && g.rounds > 1) {
-        if (threadIdx.x == 0) failed = !all_arrived(g, 0);
+        if (threadIdx.x == 0) {
+            wait_for_prerequisite_grid();
+            failed = !all_arrived(g, 0);
+        }
         __syncthreads();
     }
 #pragma unroll 1
@@ -818,6 +823,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
         // count this block in, then wait for the slab's others
         __syncthreads();
         if (live && threadIdx.x == 0) {
+            wait_for_prerequisite_grid();
             if (blockIdx.x != 0 || slab_i != g.drop_unit)  // failure injection: not counted in
                 asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.arrived + slab_i) : "memory");
             if (!failed) failed = !all_arrived(g, slab_i);  // later waits are not made
@@ -845,6 +851,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
             }
         }
         finish(col, g, s, chan, slab);
+        if (round == g.rounds - 1) allow_dependent_launch();
         // The second pass. dx may be the dy buffer: a position's copies are
         // waited for before this thread, and no other, writes it.
         const int64_t back = static_cast<int64_t>(pitch) * g.lanes;
