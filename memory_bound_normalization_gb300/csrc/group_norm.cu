@@ -94,7 +94,8 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     double best_cost = 0;
     // resident: microseconds that the waves of blocks need, by the slice a block
     // keeps (44 KB/us is an SM's share of the DRAM rate, in and out), the blocks'
-    // meeting, and a fixed part; rows are split no finer than 128 bytes
+    // meeting, and a fixed part (3 us of the backward's are its column sum); rows
+    // are split no finer than 128 bytes
     for (int splits = 1; splits <= a.G; splits *= 2) {
         if (a.G % splits) break;
         const int64_t wide = row_bytes / splits;
@@ -119,7 +120,7 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
             if (at_once < 1) continue;
             const double waves = static_cast<double>(cdiv(a.B * splits, at_once));
             const double per_sm = std::max(1.0, static_cast<double>(at_once) * cluster / dev.sm_count);
-            const double cost = waves * (4.0 + (cluster > 8 ? 1.0 : cluster > 1 ? 0.5 : 0.0) +
+            const double cost = waves * (4.0 + (bwd ? 3.0 / waves : 0.0) + (cluster > 8 ? 1.0 : cluster > 1 ? 0.5 : 0.0) +
                                          per_sm * slice * (bwd ? 1.5 : 2.0) / 44e3);
             if (best.ok && cost >= best_cost) continue;
             p.ok = p.resident = true;
@@ -163,7 +164,11 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     p.parts = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>({most / p.together, kStreamMaxParts, a.S / (4 * p.lanes)})));
     if ((a.S / p.parts + 1) * row_bytes > UINT32_MAX || a.B * p.parts > INT32_MAX) return best;
-    const double cost = 12.0 + 3.0 * p.rounds + total * (bwd ? 1.5 : 2.0) / (44e3 * dev.sm_count);
+    // Where both families fit, the cheaper by this estimate ran faster: 13 samples
+    // of 3439 positions of 264 f16 channels take 23.5 us resident (two waves of
+    // clusters) and 17.6 streamed, 3 of 13452 of 128 take 9.7 and 12.5, backwards
+    // 7 of 6021 of 96 bf16 take 13.8 and 15.7.
+    const double cost = (bwd ? 7.0 : 6.5) + 3.0 * p.rounds + total * (bwd ? 1.5 : 2.0) / (44e3 * dev.sm_count);
     if (best.ok && best_cost <= cost) return best;
     p.ok = true;
     p.drop = total * (bwd ? 1.5 : 2.0) > dev.l2_bytes / 2;
