@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -130,7 +131,7 @@ struct Run {
     c10::cuda::CUDAGuard guard;
     cudaStream_t stream;
     bool foreign;
-    at::Tensor ws;
+    void* ws = nullptr;
     Run(const at::Tensor& x, PyObject* s) : guard(x.device()) {
         stream = c10::cuda::getCurrentCUDAStream(x.get_device()).stream();
         foreign = false;
@@ -140,10 +141,14 @@ struct Run {
             stream = there;
         }
     }
-    void* workspace(size_t need, const at::Tensor& like) {
-        if (need == 0) return nullptr;
-        ws = make({static_cast<int64_t>(need)}, at::kByte, like);
-        return ws.mutable_data_ptr();
+    ~Run() {
+        if (ws != nullptr) c10::cuda::CUDACachingAllocator::raw_delete(ws);
+    }
+    Run(const Run&) = delete;
+    Run& operator=(const Run&) = delete;
+    void* workspace(size_t need) {
+        if (need > 0) ws = c10::cuda::CUDACachingAllocator::raw_alloc(need);
+        return ws;
     }
 };
 
@@ -255,7 +260,7 @@ PyObject* group_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
         const at::Tensor y = make(x.sizes(), x.scalar_type(), x);
         const at::Tensor mean = make({g.B, g.G}, at::kFloat, x), rstd = make({g.B, g.G}, at::kFloat, x);
         const size_t need = run.foreign ? 0 : group_norm_need(g, 0, x.get_device());
-        void* ws = run.workspace(need, x);
+        void* ws = run.workspace(need);
         const void *px = x.const_data_ptr(), *pw = data(w), *pb = data(b);
         void* py = y.mutable_data_ptr();
         float *pm = mean.mutable_data_ptr<float>(), *pr = rstd.mutable_data_ptr<float>();
@@ -302,7 +307,7 @@ PyObject* group_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
             db = make({g.C}, at::kFloat, x);
         }
         const size_t need = run.foreign ? 0 : group_norm_need(g, 1, x.get_device());
-        void* ws = run.workspace(need, x);
+        void* ws = run.workspace(need);
         const void *px = x.const_data_ptr(), *pw = data(w), *pb = data(b), *pdy = dy.const_data_ptr();
         const float *pm = mean.const_data_ptr<float>(), *pr = rstd.const_data_ptr<float>();
         void* pdx = dx.mutable_data_ptr();
@@ -479,7 +484,7 @@ PyObject* qk_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
             if (k) dwk = make(wk->sizes(), at::kFloat, q);
             if (!run.foreign) need = g_entry.rope_need(r.d.head_dim, q.get_device());
         }
-        void* ws = run.workspace(need, q);
+        void* ws = run.workspace(need);
         const void *pq = q.const_data_ptr(), *pk = data(k), *pwq = data(wq), *pwk = data(wk),
                    *pp = pos.const_data_ptr(), *pdqo = dqo.const_data_ptr(), *pdko = data(dko);
         const float* pf = freq.const_data_ptr<float>();
