@@ -29,6 +29,7 @@
 
 #include "group_norm.cuh"
 #include "group_norm.h"
+#include "own_copy.cuh"
 
 namespace rmsn {
 namespace {

@@ -21,6 +21,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "own_copy.cuh"
 #include "rope.h"
 
 namespace rmsn {
