@@ -3,8 +3,9 @@
 // eight warps takes W neighbouring columns, thread t adds rows t, t + 256, ...
 // in ascending order, a butterfly adds a warp's lanes and thread 0 the warps.
 // The same bits on every run for given sizes. A few hundred rows of a few
-// hundred columns: the time is the launch and one trip to L2, so every row has
-// a thread of its own where there are no more than 256, and one barrier is all.
+// hundred columns: the time is the launch and one trip to L2 (some 3 us of 304
+// rows of 128), so every row has a thread of its own where there are no more than
+// 256, and one barrier is all.
 #include "common.cuh"
 #include "ops.h"
 
