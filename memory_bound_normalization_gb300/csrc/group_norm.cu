@@ -168,7 +168,8 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     // of 3439 positions of 264 f16 channels take 23.5 us resident (two waves of
     // clusters) and 17.6 streamed, 3 of 13452 of 128 take 9.7 and 12.5, backwards
     // 7 of 6021 of 96 bf16 take 13.8 and 15.7.
-    const double cost = (bwd ? 7.0 : 6.5) + 3.0 * p.rounds + total * (bwd ? 1.5 : 2.0) / (44e3 * dev.sm_count);
+    // The fixed part counts a launch more on the host: a near tie goes to resident.
+    const double cost = (bwd ? 8.5 : 7.5) + 3.0 * p.rounds + total * (bwd ? 1.5 : 2.0) / (44e3 * dev.sm_count);
     if (best.ok && best_cost <= cost) return best;
     p.ok = true;
     p.drop = total * (bwd ? 1.5 : 2.0) > dev.l2_bytes / 2;
