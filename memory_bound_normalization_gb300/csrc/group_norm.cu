@@ -119,7 +119,8 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
                                                   cluster);
             if (at_once < 1) continue;
             const double waves = static_cast<double>(cdiv(a.B * splits, at_once));
-            const double per_sm = std::max(1.0, static_cast<double>(at_once) * cluster / dev.sm_count);
+            const double per_sm = std::max(
+                1.0, static_cast<double>(std::min<int64_t>(at_once, a.B * splits)) * cluster / dev.sm_count);
             const double cost = waves * (4.0 + (bwd ? 3.0 / waves : 0.0) + (cluster > 8 ? 1.0 : cluster > 1 ? 0.5 : 0.0) +
                                          per_sm * slice * (bwd ? 1.5 : 2.0) / 44e3);
             if (best.ok && cost >= best_cost) continue;
@@ -225,6 +226,8 @@ SlabArgs args_of(const Plan& p, const GroupNormArgs& a) {
     g.part_more = static_cast<int>(a.S % parts);
     // threads that share four channels' lanes: as many as there are, up to 16
     g.join = std::max(1, std::min({16, g.lanes, p.threads / (g.cw / 2)}));
+    g.seg_log = 2;
+    while (g.seg_log < 5 && (1 << g.seg_log) < g.D) ++g.seg_log;
     g.drop_unit = -1;
     return g;
 }

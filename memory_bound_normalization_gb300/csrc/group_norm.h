@@ -25,6 +25,7 @@ struct SlabArgs {
     int cluster;   // resident: blocks of a slab, which join their sums
     int part_rows, part_more;  // positions of a block, and how many blocks take one more
     int join;      // threads that share four channels' sums in a block
+    int seg_log;   // log2 of the lanes that join a group's channels: as many as D, 4 to 32
     // stream
     int parts;     // blocks of a slab
     int together;  // slabs of a round

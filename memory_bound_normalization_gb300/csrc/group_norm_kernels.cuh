@@ -394,8 +394,16 @@ __device__ __forceinline__ void start(Columns<T, true, ACT>& col, const SlabArgs
     for (int e = 0; e < Pack<T>::PAIRS; ++e) col.p[e] = col.q[e] = make_float2(0.f, 0.f);
 }
 
+// Sum over the `width` neighbouring lanes (a power of two) that v belongs to.
+__device__ __forceinline__ float lanes_sum(float v, int width) {
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2)
+        if (off < width) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
 // Joins the block's first pass: emit(k, (mean, M2)) for each group of channels,
-// from each channel's sums about its pivot.
+// from each channel's sums about its pivot. 2^g.seg_log lanes take a group.
 template <typename T, int ACT, typename Emit>
 __device__ __forceinline__ void join(const Columns<T, false, ACT>& col, const SlabArgs& g, const Seat& s,
                                      float* sums, float* chan, int rows, Emit emit) {
@@ -407,18 +415,20 @@ __device__ __forceinline__ void join(const Columns<T, false, ACT>& col, const Sl
     sum_lanes(g, sums);
     const float* squares = sums + g.lanes * g.cw;
     const float frows = static_cast<float>(rows), inv_rows = 1.f / fmaxf(frows, 1.f);
-    for (int k = s.warp; k < g.gw; k += s.warps) {
+    const int seg = 1 << g.seg_log, at_once = 32 >> g.seg_log, sl = s.l & (seg - 1);
+    for (int k0 = s.warp * at_once; k0 < g.gw; k0 += s.warps * at_once) {
+        const int k = k0 + (s.l >> g.seg_log), end = k < g.gw ? (k + 1) * g.D : 0;
         float t = 0.f;
-        for (int i = k * g.D + s.l; i < (k + 1) * g.D; i += 32) t += fmaf(sums[i], inv_rows, chan[i]);
-        const float m = group_allreduce<32>(t) * s.inv_d;
+        for (int i = k * g.D + sl; i < end; i += seg) t += fmaf(sums[i], inv_rows, chan[i]);
+        const float m = lanes_sum(t, seg) * s.inv_d;
         float m2 = 0.f;
-        for (int i = k * g.D + s.l; i < (k + 1) * g.D; i += 32) {
+        for (int i = k * g.D + sl; i < end; i += seg) {
             // squares about the channel's mean, and its mean's distance from the group's
             const float off = sums[i] * inv_rows, d = chan[i] + off - m;
             m2 += fmaf(frows * d, d, fmaf(-sums[i], off, squares[i]));
         }
-        m2 = group_allreduce<32>(m2);
-        if (s.l == 0) emit(k, make_float2(m, m2));
+        m2 = lanes_sum(m2, seg);
+        if (sl == 0 && k < g.gw) emit(k, make_float2(m, m2));
     }
 }
 // The backward's: emit(k, (rstd sum w dz, sum w dz xhat)), which sums of P and
@@ -434,42 +444,44 @@ __device__ __forceinline__ void join(const Columns<T, true, ACT>& col, const Sla
     sum_lanes(g, sums);
     const float* ps = sums;
     const float* qs = sums + g.lanes * g.cw;
-    for (int k = s.warp; k < g.gw; k += s.warps) {
+    const int seg = 1 << g.seg_log, at_once = 32 >> g.seg_log, sl = s.l & (seg - 1);
+    for (int k0 = s.warp * at_once; k0 < g.gw; k0 += s.warps * at_once) {
+        const int k = k0 + (s.l >> g.seg_log), end = k < g.gw ? (k + 1) * g.D : 0;
         float sp = 0.f, sq = 0.f;
-        for (int i = s.l; i < g.D; i += 32) {
-            const float k1 = chan[g.cw + k * g.D + i];
-            sp = fmaf(k1, ps[k * g.D + i], sp);
-            sq = fmaf(k1, qs[k * g.D + i], sq);
+        for (int i = k * g.D + sl; i < end; i += seg) {
+            const float k1 = chan[g.cw + i];
+            sp = fmaf(k1, ps[i], sp);
+            sq = fmaf(k1, qs[i], sq);
         }
-        sp = group_allreduce<32>(sp);
-        sq = group_allreduce<32>(sq);
-        if (s.l == 0) emit(k, make_float2(sp, sq));
+        sp = lanes_sum(sp, seg);
+        sq = lanes_sum(sq, seg);
+        if (sl == 0 && k < g.gw) emit(k, make_float2(sp, sq));
     }
 }
 
-// The slab's result of a group from NP results a lane with their counts of
-// values (0: none there), by a fixed tree: (mean, rstd), or the backward's two
-// sums as means.
+// The slab's result of a group from NP results a lane of `width` lanes with
+// their counts of values (0: none there), by a fixed tree: (mean, rstd), or the
+// backward's two sums as means.
 template <bool BWD, int NP>
 __device__ __forceinline__ float2 combine(const float2 (&t)[NP], const float (&count)[NP], float inv_count,
-                                          float eps) {
+                                          float eps, int width) {
     float2 v = make_float2(0.f, 0.f);
     if constexpr (BWD) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) v = __fadd2_rn(v, t[i]);
-        v.x = group_allreduce<32>(v.x) * inv_count;
-        v.y = group_allreduce<32>(v.y) * inv_count;
+        v.x = lanes_sum(v.x, width) * inv_count;
+        v.y = lanes_sum(v.y, width) * inv_count;
     } else {
         // mean = sum n m / n, M2 = sum M2 + n (m - mean)^2
 #pragma unroll
         for (int i = 0; i < NP; ++i) v.x = fmaf(count[i], t[i].x, v.x);
-        v.x = group_allreduce<32>(v.x) * inv_count;
+        v.x = lanes_sum(v.x, width) * inv_count;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const float d = t[i].x - v.x;
             v.y += fmaf(count[i] * d, d, t[i].y);
         }
-        v.y = rsqrtf(group_allreduce<32>(v.y) * inv_count + eps);
+        v.y = rsqrtf(lanes_sum(v.y, width) * inv_count + eps);
     }
     return v;
 }
@@ -604,24 +616,21 @@ __global__ void __launch_bounds__(kMaxThreads) gn_resident_kernel(const __grid_c
     });
     join(col, g, s, sums, chan, at.rows, [&](int k, float2 v) { mine[k] = v; });
 
-    // the cluster's blocks meet; lane r of a warp reads block r's result
+    // the cluster's blocks meet and read one another's results
     __syncwarp();
     if (g.cluster > 1) cluster_sync_all();
     else __syncthreads();
     const float inv_count = 1.f / (static_cast<float>(g.a.S) * static_cast<float>(g.D));
-    const float count[1] = {s.l < g.cluster ? static_cast<float>(g.part_rows + (s.l < g.part_more ? 1 : 0)) *
-                                                  static_cast<float>(g.D)
-                                            : 0.f};
-    for (int k = s.warp; k < g.gw; k += s.warps) {
+    // as many lanes a group as there are blocks
+    const int log = __ffs(g.cluster) - 1, peer = s.l & (g.cluster - 1), at_once = 32 >> log;
+    const float count[1] = {static_cast<float>(g.part_rows + (peer < g.part_more ? 1 : 0)) * static_cast<float>(g.D)};
+    for (int k0 = s.warp * at_once; k0 < g.gw; k0 += s.warps * at_once) {
+        const int k = k0 + (s.l >> log);
         float2 t[1] = {make_float2(0.f, 0.f)};
-        if (g.cluster > 1) {
-            if (s.l < g.cluster) t[0] = ld_cluster_f32x2(mine + k, s.l);
-        } else if (s.l == 0) {
-            t[0] = mine[k];
-        }
+        if (k < g.gw) t[0] = g.cluster > 1 ? ld_cluster_f32x2(mine + k, peer) : mine[k];
         __syncwarp();
-        const float2 v = combine<BWD>(t, count, inv_count, g.a.eps);
-        if (s.l == 0) {
+        const float2 v = combine<BWD>(t, count, inv_count, g.a.eps, g.cluster);
+        if (peer == 0 && k < g.gw) {
             slab[k] = v;
             if (!BWD && at.rank == 0) {
                 g.a.mean[group0 + k] = v.x;
@@ -864,24 +873,32 @@ __global__ void __launch_bounds__(kStreamThreads, 2) gn_stream_kernel(const __gr
             if (!failed) failed = !all_arrived(g, slab_i);  // later waits are not made
         }
         __syncthreads();
-        // the slab's results; all that a lane adds are read at once
-        for (int k = live ? s.warp : g.gw; k < g.gw; k += s.warps) {
+        // the slab's results, two groups a warp; all that a lane adds are read at once
+        for (int k0 = live ? s.warp : g.gw; k0 < g.gw; k0 += 2 * s.warps) {
             constexpr int NP = kStreamMaxParts / 32;
-            const float2* from = g.stats + (slab_i * g.gw + k) * g.parts;
-            float2 t[NP];
+            float2 t[2][NP];
             float count[NP];
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const int j = s.l + 32 * i;
-                t[i] = j < g.parts ? __ldcg(from + j) : make_float2(0.f, 0.f);
                 count[i] = j < g.parts ? static_cast<float>(g.part_rows + (j < g.part_more ? 1 : 0)) * fd : 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int k = k0 + u * s.warps;
+                    t[u][i] = j < g.parts && k < g.gw ? __ldcg(g.stats + (slab_i * g.gw + k) * g.parts + j)
+                                                      : make_float2(0.f, 0.f);
+                }
             }
-            const float2 v = combine<BWD>(t, count, inv_count, g.a.eps);
-            if (s.l == 0) {
-                slab[k] = v;
-                if (!BWD && part == 0) {
-                    g.a.mean[group0 + k] = v.x;
-                    g.a.rstd[group0 + k] = v.y;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = k0 + u * s.warps;
+                const float2 v = combine<BWD>(t[u], count, inv_count, g.a.eps, 32);
+                if (s.l == 0 && k < g.gw) {
+                    slab[k] = v;
+                    if (!BWD && part == 0) {
+                        g.a.mean[group0 + k] = v.x;
+                        g.a.rstd[group0 + k] = v.y;
+                    }
                 }
             }
         }
