@@ -81,10 +81,31 @@ struct Plan {
     bool drop = false;
 };
 
-void geometry(Plan* p, int nvec) {
+void geometry(Plan* p, int nvec, int threads) {
     p->nvec = nvec;
-    p->lanes = std::max(1, kMaxThreads / nvec);
+    p->lanes = std::max(1, threads / nvec);
     p->threads = round_up(p->lanes * nvec, 32);
+}
+
+// Microseconds that a resident plan takes, near enough to choose by: a wave's
+// fixed part, the meeting of a cluster (whose blocks read one another's sums),
+// the joins (by channels and threads of a block), and the slice each SM keeps
+// (44 KB/us is an SM's share of the DRAM rate, in and out), with few warps at
+// less than that rate in the forward. The backward's column sum comes once.
+// Measured (GPU time, forward unless said): 4 samples of 4096 positions of 320
+// f16 channels in clusters of 16 blocks of 256 threads 10.4 us, of 8 of 256 11.6,
+// of 8 of 512 with twice the slice 11.6; 2 of 64 of 1280 bf16 in single blocks of
+// 256 threads 4.0, of 512 4.8, in clusters of 8 5.6; backward 4 of 1069 of 192 in
+// clusters of 8 of 256 8.3, of 16 9.7, of 8 of 512 9.0.
+double resident_cost(const DeviceInfo& dev, bool bwd, int64_t clusters, int at_once, int cluster, int threads,
+                     int64_t slice, int channels) {
+    const double waves = static_cast<double>(cdiv(clusters, at_once));
+    const int64_t per_sm = cdiv(std::min<int64_t>(clusters, at_once) * cluster, dev.sm_count);
+    const double meet = cluster > 8 ? (bwd ? 2.3 : 1.0) : cluster > 4 ? (bwd ? 1.0 : 0.5) : cluster > 1 ? 0.2 : 0.0;
+    const int64_t busy = per_sm * threads;
+    const double slow = bwd || busy >= 512 ? 1.0 : busy >= 256 ? 1.25 : 1.7;
+    return (bwd ? 1.0 : 0.0) + waves * (2.4 + meet + 0.003 * channels + 1.9 * threads / 512 +
+                                        per_sm * slice * (bwd ? 1.5 : 2.0) / 44e3 * slow);
 }
 
 Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& a) {
@@ -92,43 +113,39 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     const int size = dtype_size(dtype), tensors = bwd ? 2 : 1;
     const int64_t row_bytes = static_cast<int64_t>(a.C) * size;
     double best_cost = 0;
-    // resident: microseconds that the waves of blocks need, by the slice a block
-    // keeps (44 KB/us is an SM's share of the DRAM rate, in and out), the blocks'
-    // meeting, and a fixed part (3 us of the backward's are its column sum); rows
-    // are split no finer than 128 bytes
+    // resident: rows are split no finer than 128 bytes; the backward's two tensors
+    // want 256 threads
     for (int splits = 1; splits <= a.G; splits *= 2) {
         if (a.G % splits) break;
         const int64_t wide = row_bytes / splits;
         if (row_bytes % splits || wide % 16 || (splits > 1 && wide < 128)) break;
-        if (wide / 16 > kMaxThreads) continue;
-        Plan p;
-        p.splits = splits;
-        geometry(&p, static_cast<int>(wide / 16));
-        const int fixed = round_up(fixed_smem(p.lanes, a.C / splits, a.G / splits), 16);
-        for (int cluster = 1; cluster <= 16; cluster *= 2) {
-            const int64_t rows = cdiv(a.S, cluster);
-            const int64_t slice = cdiv(rows, p.lanes) * p.lanes * wide * tensors;
-            if (fixed + slice > kMaxSmem) continue;
-            if (cluster > 1 && rows < p.lanes) break;
-            if (a.B * splits * cluster > INT32_MAX) break;
-            // how many run at once: clusters of 8 or 16 large blocks leave some
-            // SMs of a GPC unused, so that 16 clusters of 8 are two waves
-            const int smem = static_cast<int>(fixed + slice);
-            const int at_once = resident_clusters(dev, kernel_for(dtype, bwd, a.act, SlabKind::kResident),
-                                                  p.threads, std::min(kMaxSmem, round_up(smem, 16 * 1024)),
-                                                  cluster);
-            if (at_once < 1) continue;
-            const double waves = static_cast<double>(cdiv(a.B * splits, at_once));
-            const double per_sm = std::max(
-                1.0, static_cast<double>(std::min<int64_t>(at_once, a.B * splits)) * cluster / dev.sm_count);
-            const double cost = waves * (4.0 + (bwd ? 3.0 / waves : 0.0) + (cluster > 8 ? 1.0 : cluster > 1 ? 0.5 : 0.0) +
-                                         per_sm * slice * (bwd ? 1.5 : 2.0) / 44e3);
-            if (best.ok && cost >= best_cost) continue;
-            p.ok = p.resident = true;
-            p.cluster = cluster;
-            p.smem = smem;
-            best = p;
-            best_cost = cost;
+        for (int threads = kMaxThreads; threads >= (bwd ? 256 : 128); threads /= 2) {
+            if (wide / 16 > threads) continue;
+            Plan p;
+            p.splits = splits;
+            geometry(&p, static_cast<int>(wide / 16), threads);
+            const int fixed = round_up(fixed_smem(p.lanes, a.C / splits, a.G / splits), 16);
+            for (int cluster = 1; cluster <= 16; cluster *= 2) {
+                const int64_t rows = cdiv(a.S, cluster);
+                const int64_t slice = cdiv(rows, p.lanes) * p.lanes * wide * tensors;
+                if (fixed + slice > kMaxSmem) continue;
+                if (cluster > 1 && rows < p.lanes) break;
+                if (a.B * splits * cluster > INT32_MAX) break;
+                // how many run at once: clusters of 8 or 16 large blocks leave some
+                // SMs of a GPC unused, so that 16 clusters of 8 are two waves
+                const int smem = static_cast<int>(fixed + slice);
+                const int at_once = resident_clusters(dev, kernel_for(dtype, bwd, a.act, SlabKind::kResident),
+                                                      p.threads, std::min(kMaxSmem, round_up(smem, 16 * 1024)),
+                                                      cluster);
+                if (at_once < 1) continue;
+                const double cost = resident_cost(dev, bwd, a.B * splits, at_once, cluster, threads, slice, a.C / splits);
+                if (best.ok && cost >= best_cost) continue;
+                p.ok = p.resident = true;
+                p.cluster = cluster;
+                p.smem = smem;
+                best = p;
+                best_cost = cost;
+            }
         }
     }
     // stream: rounds of slabs that half of L2 holds (the other half holds what
