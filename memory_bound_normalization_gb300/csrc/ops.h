@@ -39,6 +39,7 @@ struct RopeArgs {
     int* status;
     // launch geometry (rope_launch fills it in)
     int units, lanes, tile, splits;
+    int per_warp, inv_lanes;  // groups of a warp; 2^16 / lanes, rounded up
     float* partial;   // backward: dw partial rows of t[0], then of t[1]
     int blocks0;      // backward: blocks that take t[0]
     unsigned char axis[kRopeMaxPairs];  // axis of each rotated pair

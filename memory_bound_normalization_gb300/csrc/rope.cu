@@ -41,17 +41,23 @@ RopeFn kernel_for(int dtype, int e, int units, bool bwd, bool adjacent, bool nor
     }
 }
 
+// Lanes of a group: the power of two at or above the units of a head, or as many
+// as the units where a warp then holds more groups.
 void shape_of(RopeArgs* a, int e) {
     a->units = a->head_dim / 2 / e;
     a->lanes = 4;
     while (a->lanes < 32 && a->lanes < a->units) a->lanes *= 2;
+    if (e > 1 && 32 / a->units > 32 / a->lanes) a->lanes = a->units;
+    a->per_warp = 32 / a->lanes;
+    a->inv_lanes = 65536 / a->lanes + 1;
 }
+int groups_of(const RopeArgs& a) { return kRopeThreads / 32 * a.per_warp; }
 
 // Shared memory of the backward: rows on the way, weights, then the larger of
 // the two angle tables and the groups' shares of dw.
 int bwd_smem(const RopeArgs& a, int e, int dtype) {
     return (e >= 4 ? kRopeBwdWords * e * dtype_size(dtype) : 0) +
-           a.head_dim * 4 * (1 + std::max(2 * a.tile, kRopeThreads / a.lanes));
+           a.head_dim * 4 * (1 + std::max(2 * a.tile, groups_of(a)));
 }
 
 // Lets a kernel have the shared memory that its blocks an SM leave it, once a
@@ -79,7 +85,7 @@ int max_tile(const RopeArgs& a) { return std::min(kRopeMaxTile, 40 * 1024 / (8 *
 // than SMs: 25 tokens of 48 bf16 heads of 96 take 5.0 us, where tiles of eight
 // passes on a few blocks take 8.3.
 int bwd_tile(const DeviceInfo& dev, const RopeArgs& a) {
-    const int groups = kRopeThreads / a.lanes;
+    const int groups = groups_of(a);
     int heads = 1;
     for (const RopeTensor& t : a.t)
         if (t.heads > 0) heads = std::max(heads, t.heads);
@@ -95,7 +101,7 @@ cudaError_t rope_fwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, Rop
     shape_of(&a, e);
     const bool norm = a.t[0].w != nullptr;
     const int heads = a.t[0].heads + a.t[1].heads;
-    const int groups = kRopeThreads / a.lanes;
+    const int groups = groups_of(a);
     // some eight passes of the block's groups over a tile's rows, but no fewer
     // tiles than SMs; few tokens share their heads out
     a.tile = static_cast<int>(std::max<int64_t>(

@@ -123,8 +123,11 @@ __device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t turns) {
 // UNITS, where it is positive, is the number of units of a head, a power of two
 // and the lanes of a group: table offsets, lane masks and the row sum's steps
 // are then constants. (Left to run time, they and the kernel parameters reloaded
-// for them made up half of the forward's instructions.) Negative, it is minus the
-// lanes of a group, some of which may have no unit.
+// for them made up half of the forward's instructions.) -1: up to 32 units, a lane
+// each; the lanes of a group are the next power of two, or as many as the units
+// where a warp then holds more groups (5 units: 6 groups instead of 4; 24489 tokens
+// of 24 bf16 heads of 80 forward 50.8 -> 40.4 us). 0: a lane may own several units
+// (single elements).
 //
 // A unit is the E pairs that a lane takes at once, from two pieces of E elements:
 // the pairs' first elements and their second ones; where pairs are neighbours,
@@ -223,16 +226,52 @@ __device__ __forceinline__ void join_pairs(const float2 (&f)[(E + 1) / 2], const
     }
 }
 
+// Sum over a group's lanes, of which the caller is number `lane`.
 template <int UNITS>
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-    if constexpr (UNITS != 0) {
-        return group_allreduce<(UNITS > 0 ? UNITS : -UNITS)>(v);
-    } else {
+__device__ __forceinline__ float lanes_sum(float v, int lanes, int lane) {
+    if constexpr (UNITS > 0) {
+        return group_allreduce<UNITS>(v);
+    } else if (UNITS == 0 || (lanes & (lanes - 1)) == 0) {
 #pragma unroll
         for (int off = 16; off >= 1; off /= 2)
             if (off < lanes) v += __shfl_xor_sync(0xffffffffu, v, off);
         return v;
+    } else {
+        // lane i < off takes what lane i + off has, which is complete for all of
+        // its residue modulo 2 off
+#pragma unroll
+        for (int off = 16; off >= 1; off /= 2)
+            if (off < lanes) {
+                const float u = __shfl_down_sync(0xffffffffu, v, off);
+                if (lane + off < lanes) v += u;
+            }
+        return __shfl_sync(0xffffffffu, v, static_cast<int>(threadIdx.x % 32) - lane);
     }
+}
+
+// A thread's place: its group of lanes and its number in it. `on` is false for
+// lanes that no group or no unit has.
+struct Lane {
+    int lane, group, groups;
+    bool on;
+};
+template <int UNITS>
+__device__ __forceinline__ Lane lane_of(const RopeArgs& a) {
+    Lane p;
+    if constexpr (UNITS > 0) {
+        p.lane = threadIdx.x % UNITS;
+        p.group = threadIdx.x / UNITS;
+        p.groups = kRopeThreads / UNITS;
+        p.on = true;
+    } else {
+        // l / lanes by the reciprocal in 16 bits, exact for l below 32
+        const int l = threadIdx.x % 32, in_warp = l * a.inv_lanes >> 16;
+        p.lane = l - in_warp * a.lanes;
+        p.group = static_cast<int>(threadIdx.x / 32) * a.per_warp + in_warp;
+        p.groups = kRopeThreads / 32 * a.per_warp;
+        p.on = in_warp < a.per_warp && (UNITS == 0 || p.lane < a.units);
+    }
+    return p;
 }
 
 __device__ __forceinline__ int64_t position_at(const RopeArgs& a, int64_t at) {
@@ -447,7 +486,7 @@ struct RowCursor {
 template <typename T, int E, bool ADJ, bool NORM, int UNITS>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int NU = UNITS != 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
-    const int lanes = UNITS != 0 ? abs(UNITS) : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
+    const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
     using X = Elems<T, E>;
     using W = typename X::W;
     constexpr bool RING = E >= 4;
@@ -456,8 +495,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
     __shared__ TileInfo info[SLOTS];
     float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem + RING_BYTES);  // [2][D] when NORM
     float* tabs = wtab + (NORM ? 2 * D : 0);                                 // [2][tile][D]
-    const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
-    const int groups = kRopeThreads / lanes;
+    const Lane me = lane_of<UNITS>(a);
+    const int lane = me.lane, group = me.group, groups = me.groups;
 
     const int part = static_cast<int>(blockIdx.x) / a.splits;
     const int split = static_cast<int>(blockIdx.x) - part * a.splits;
@@ -502,14 +541,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
     uint32_t ring_at = ring_first;  // this pass's slots, and those of the row AHEAD of it
     auto fetch = [&](uint32_t to) {
         if (row_passes > 0) {
-            if (row.t < range.count(row_tile)) {
+            if (me.on && row.t < range.count(row_tile)) {
                 const bool second = row.head >= qheads;
                 const uint64_t src =
                     row_address(info[row_slot].addr[second ? 2 : 0][row.t], row.head + (second ? kh0 - qheads : qh0),
                                 static_cast<uint32_t>((second ? a.t[1].xs[2] : a.t[0].xs[2]) * sizeof(T)));
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
-                    if (UNITS > 0 || lane + i * lanes < a.units) {
+                    if (UNITS != 0 || lane + i * lanes < a.units) {
                         const uint64_t p = src + at.lo[i], p2 = p + at.hop(i);
                         if constexpr (RING) {
                             copy_own<sizeof(W)>(to, reinterpret_cast<const void*>(p), a.status);
@@ -551,7 +590,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
         cur.start(group, heads);
 #pragma unroll 1
         for (int pass = 0; pass < passes; ++pass, cur.advance(dt, dh, heads)) {
-            const bool live = cur.t < tokens, second = cur.head >= qheads;
+            const bool live = me.on && cur.t < tokens, second = cur.head >= qheads;
             if constexpr (RING) {
                 copies_wait<AHEAD - 1>();
                 lo[0] = slot_word<W>(ring_at);
@@ -571,15 +610,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
                 float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
-                    if (live && (UNITS > 0 || lane + i * lanes < a.units)) {
+                    if (live && (UNITS != 0 || lane + i * lanes < a.units)) {
 #pragma unroll
                         for (int e = 0; e < P; ++e)
                             ss = __ffma2_rn(f[i][e], f[i][e], __ffma2_rn(s[i][e], s[i][e], ss));
                     }
-                const float2 rs = f2_splat(rsqrtf(lanes_sum<UNITS>(ss.x + ss.y, lanes) * inv_d + a.eps));
+                const float2 rs = f2_splat(rsqrtf(lanes_sum<UNITS>(ss.x + ss.y, lanes, lane) * inv_d + a.eps));
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
-                    if (live && (UNITS > 0 || lane + i * lanes < a.units)) {
+                    if (live && (UNITS != 0 || lane + i * lanes < a.units)) {
                         float2 wf[P], ws[P];
                         read_table<E, UNITS>(wtab + (second ? D : 0), a.units, lane + i * lanes, wf, ws);
 #pragma unroll
@@ -595,7 +634,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
                             static_cast<uint32_t>((second ? a.t[1].os[2] : a.t[0].os[2]) * sizeof(T)));
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                if (UNITS <= 0 && lane + i * lanes >= a.units) continue;
+                if (UNITS == 0 && lane + i * lanes >= a.units) continue;
                 float2 c[P], n[P], yf[P], ys[P], yl[P], yh[P];
                 read_table<E, UNITS>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
 #pragma unroll
@@ -627,7 +666,7 @@ template <typename T, int E, bool ADJ, int UNITS>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int NU = UNITS != 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
-    const int lanes = UNITS != 0 ? abs(UNITS) : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
+    const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
     using X = Elems<T, E>;
     using W = typename X::W;
     constexpr bool RING = E >= 4;
@@ -636,8 +675,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     __shared__ TileInfo info[SLOTS];
     float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem + RING_BYTES);
     float* tabs = wtab + D;  // [2][tile][D]
-    const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
-    const int groups = kRopeThreads / lanes;
+    const Lane me = lane_of<UNITS>(a);
+    const int lane = me.lane, group = me.group, groups = me.groups;
 
     const int which = static_cast<int>(blockIdx.x) >= a.blocks0 ? 1 : 0;
     const RopeTensor& x = a.t[which];
@@ -686,12 +725,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     uint32_t ring_at = ring_first;  // this pass's slots, and those of the row AHEAD of it
     auto fetch = [&](uint32_t to) {
         if (row_passes > 0) {
-            if (row.t < row_tokens) {
+            if (me.on && row.t < row_tokens) {
                 const uint64_t src = row_address(info[row_slot].addr[0][row.t], row.head, x_step);
                 const uint64_t dys = row_address(info[row_slot].addr[1][row.t], row.head, dy_step);
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
-                    if (UNITS > 0 || lane + i * lanes < a.units) {
+                    if (UNITS != 0 || lane + i * lanes < a.units) {
                         const T* p = reinterpret_cast<const T*>(src + at.lo[i]);
                         const T* q = reinterpret_cast<const T*>(dys + at.lo[i]);
                         const T* p2 = reinterpret_cast<const T*>(src + at.lo[i] + at.hop(i));
@@ -735,7 +774,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     float2 wf[NU][P], ws[NU][P];
 #pragma unroll
     for (int i = 0; i < NU; ++i)
-        if (UNITS > 0 || lane + i * lanes < a.units)
+        if (UNITS != 0 || lane + i * lanes < a.units)
             read_table<E, UNITS>(wtab, a.units, lane + i * lanes, wf[i], ws[i]);
     if (range.tiles > 0) fill_angles<T, E, ADJ>(a, pair, tabs, info[0], range.count(0));
     int buf = 0, slot = 0, fill = AHEAD;
@@ -757,7 +796,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
         cur.start(group, heads);
 #pragma unroll 1
         for (int pass = 0; pass < passes; ++pass, cur.advance(dt, dh, heads)) {
-            const bool live = cur.t < tokens;
+            const bool live = me.on && cur.t < tokens;
             take(ring_at);
             W xl[NU], xh[NU];
             float2 gf[NU][P], gs[NU][P];
@@ -775,7 +814,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
             float2 ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                if (!live || (UNITS <= 0 && lane + i * lanes >= a.units)) continue;
+                if (!live || (UNITS == 0 && lane + i * lanes >= a.units)) continue;
                 float2 l[P], h[P], f[P], s[P], c[P], n[P];
                 X::unpack(xl[i], l);
                 X::unpack(xh[i], h);
@@ -790,7 +829,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
                                     __ffma2_rn(__fmul2_rn(gs[i][e], ws[i][e]), s[e], hx));
                 }
             }
-            const float sum = lanes_sum<UNITS>(ss.x + ss.y, lanes), dot = lanes_sum<UNITS>(hx.x + hx.y, lanes);
+            const float sum = lanes_sum<UNITS>(ss.x + ss.y, lanes, lane), dot = lanes_sum<UNITS>(hx.x + hx.y, lanes, lane);
             const float rs = rsqrtf(sum * inv_d + a.eps);
             const float2 rs2 = f2_splat(rs);
             // rs (h - xhat mean(h xhat)) = (g rs) w + x coef
@@ -799,7 +838,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
             const uint64_t dst = row_address(info[slot].addr[2][cur.t], cur.head, out_step);
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                if (UNITS <= 0 && lane + i * lanes >= a.units) continue;
+                if (UNITS == 0 && lane + i * lanes >= a.units) continue;
                 float2 l[P], h[P], f[P], s[P];
                 X::unpack(xl[i], l);
                 X::unpack(xh[i], h);
@@ -833,7 +872,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
         const int u = lane + i * lanes;
-        if (UNITS <= 0 && u >= a.units) continue;
+        if (!me.on || (UNITS == 0 && u >= a.units)) continue;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             int p, q;
@@ -862,18 +901,16 @@ RopeFn kernel_of(bool bwd, bool adjacent, bool norm) {
 }
 template <typename T>
 RopeFn kernel_for_type(int e, int units, bool bwd, bool adjacent, bool norm) {
-    // 16-byte pieces of heads of 64, 128 and 256: constant geometry; of heads
-    // between 64 and 128: a constant number of lanes
+    // 16-byte pieces of heads of 64, 128 and 256: constant geometry
     constexpr int E = 16 / sizeof(T), U = 32 / E;
     if (e == E) {
         if (units == U) return kernel_of<T, E, U>(bwd, adjacent, norm);
         if (units == 2 * U) return kernel_of<T, E, 2 * U>(bwd, adjacent, norm);
         if (units == 4 * U) return kernel_of<T, E, 4 * U>(bwd, adjacent, norm);
-        if (units > U && units < 2 * U) return kernel_of<T, E, -2 * U>(bwd, adjacent, norm);
-        return kernel_of<T, E, 0>(bwd, adjacent, norm);
+        return kernel_of<T, E, -1>(bwd, adjacent, norm);
     }
     if constexpr (E != 4)
-        if (e == 4) return kernel_of<T, 4, 0>(bwd, adjacent, norm);
+        if (e == 4) return kernel_of<T, 4, -1>(bwd, adjacent, norm);
     return kernel_of<T, 1, 0>(bwd, adjacent, norm);
 }
 }  // namespace
