@@ -32,12 +32,12 @@ int piece_of(const RopeArgs& a, int dtype, bool adjacent) {
     return 1;
 }
 
-RopeFn kernel_for(int dtype, int e, int units, bool bwd, bool adjacent, bool norm) {
+RopeFn kernel_for(int dtype, int e, const RopeArgs& a, bool bwd, bool adjacent, bool norm) {
     switch (dtype) {
-        case RMSNORM_F32: return rope_kernel_f32(e, units, bwd, adjacent, norm);
+        case RMSNORM_F32: return rope_kernel_f32(e, a.units, a.lanes, bwd, adjacent, norm);
         case RMSNORM_BF16:
-        case RMSNORM_BF16_W_F32: return rope_kernel_bf16(e, units, bwd, adjacent, norm);
-        default: return rope_kernel_f16(e, units, bwd, adjacent, norm);
+        case RMSNORM_BF16_W_F32: return rope_kernel_bf16(e, a.units, a.lanes, bwd, adjacent, norm);
+        default: return rope_kernel_f16(e, a.units, a.lanes, bwd, adjacent, norm);
     }
 }
 
@@ -114,7 +114,7 @@ cudaError_t rope_fwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, Rop
         std::min<int64_t>(cdiv(a.tokens, a.tile), static_cast<int64_t>(kRopeBlocks) * dev.sm_count));
     const int smem = (e >= 4 ? kRopeFwdWords * e * dtype_size(dtype) : 0) +
                      a.head_dim * 4 * (2 * a.tile + (norm ? 2 : 0));
-    const RopeFn fn = kernel_for(dtype, e, a.units, false, adjacent, norm);
+    const RopeFn fn = kernel_for(dtype, e, a, false, adjacent, norm);
     const cudaError_t err = allow_smem(dev, fn);
     if (err != cudaSuccess) return err;
     return launch_pdl(fn, blocks * a.splits, kRopeThreads, smem, 1, s, a);
@@ -143,7 +143,7 @@ cudaError_t rope_bwd_launch(const DeviceInfo& dev, int dtype, bool adjacent, Rop
     shape_of(&a, e);
     a.tile = bwd_tile(dev, a);
     a.blocks0 = rows[0];
-    const RopeFn fn = kernel_for(dtype, e, a.units, true, adjacent, true);
+    const RopeFn fn = kernel_for(dtype, e, a, true, adjacent, true);
     cudaError_t err = allow_smem(dev, fn);
     if (err != cudaSuccess) return err;
     err = launch_pdl(fn, rows[0] + rows[1], kRopeThreads, bwd_smem(a, e, dtype), 1, s, a);

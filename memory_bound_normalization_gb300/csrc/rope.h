@@ -17,9 +17,10 @@ constexpr int kRopeBwdWords = kRopeBwdAhead * 4 * kRopeThreads;
 constexpr int kRopeMaxSmem = 80 * 1024;  // dynamic shared memory of a block at most
 
 using RopeFn = void (*)(const RopeArgs);
-// The kernel for pieces of e elements and `units` units a head.
-RopeFn rope_kernel_f32(int e, int units, bool bwd, bool adjacent, bool norm);
-RopeFn rope_kernel_bf16(int e, int units, bool bwd, bool adjacent, bool norm);
-RopeFn rope_kernel_f16(int e, int units, bool bwd, bool adjacent, bool norm);
+// The kernel for pieces of e elements, `units` units a head and `lanes` lanes a
+// group.
+RopeFn rope_kernel_f32(int e, int units, int lanes, bool bwd, bool adjacent, bool norm);
+RopeFn rope_kernel_bf16(int e, int units, int lanes, bool bwd, bool adjacent, bool norm);
+RopeFn rope_kernel_f16(int e, int units, int lanes, bool bwd, bool adjacent, bool norm);
 
 }  // namespace rmsn

@@ -3,8 +3,8 @@
 
 namespace rmsn {
 
-RopeFn rope_kernel_f16(int e, int units, bool bwd, bool adjacent, bool norm) {
-    return kernel_for_type<__half>(e, units, bwd, adjacent, norm);
+RopeFn rope_kernel_f16(int e, int units, int lanes, bool bwd, bool adjacent, bool norm) {
+    return kernel_for_type<__half>(e, units, lanes, bwd, adjacent, norm);
 }
 
 }  // namespace rmsn

@@ -120,14 +120,15 @@ __device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t turns) {
 // hold D floats: two pairs a 16-byte word, firsts before seconds, so that they
 // load as the float2 values they multiply; lanes of a group read consecutive
 // words and do not conflict.
-// UNITS, where it is positive, is the number of units of a head, a power of two
-// and the lanes of a group: table offsets, lane masks and the row sum's steps
-// are then constants. (Left to run time, they and the kernel parameters reloaded
-// for them made up half of the forward's instructions.) -1: up to 32 units, a lane
-// each; the lanes of a group are the next power of two, or as many as the units
-// where a warp then holds more groups (5 units: 6 groups instead of 4; 24489 tokens
-// of 24 bf16 heads of 80 forward 50.8 -> 40.4 us). 0: a lane may own several units
-// (single elements).
+// LANES, where it is positive, is the number of lanes of a group, one for each
+// unit of a head; where it is below -1, minus that number, of which some may have
+// no unit: lane masks, the row sum's steps and (positive) table offsets are then
+// constants. (Left to run time, they and the kernel parameters reloaded for them
+// made up half of the forward's instructions.) -1: any number up to 32. 0: a lane
+// may own several units (single elements).
+// The lanes of a group are the power of two at or above the units, or as many as
+// the units where a warp then holds more groups: 5 units leave 6 groups instead of
+// 4 (24489 tokens of 24 bf16 heads of 80 forward: 50.8 -> 40.0 us).
 //
 // A unit is the E pairs that a lane takes at once, from two pieces of E elements:
 // the pairs' first elements and their second ones; where pairs are neighbours,
@@ -152,6 +153,8 @@ __device__ __forceinline__ int pair_at(int units, int u, int e) {
     if constexpr (ADJ && E > 1) return (u + (e < E / 2 ? 0 : units)) * (E / 2) + e % (E / 2);
     return u * E + e;
 }
+template <int LANES>
+constexpr bool kPowerOfTwo = LANES != 0 && (LANES & (LANES - 1)) == 0;
 template <int E>
 constexpr int kSecond = E == 1 ? 1 : 2;  // floats from a pair's first value to its second
 
@@ -227,11 +230,13 @@ __device__ __forceinline__ void join_pairs(const float2 (&f)[(E + 1) / 2], const
 }
 
 // Sum over a group's lanes, of which the caller is number `lane`.
-template <int UNITS>
-__device__ __forceinline__ float lanes_sum(float v, int lanes, int lane) {
-    if constexpr (UNITS > 0) {
-        return group_allreduce<UNITS>(v);
-    } else if (UNITS == 0 || (lanes & (lanes - 1)) == 0) {
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v, int some_lanes, int lane) {
+    constexpr int N = LANES > 0 ? LANES : LANES < -1 ? -LANES : 0;
+    const int lanes = N > 0 ? N : some_lanes;
+    if constexpr (kPowerOfTwo<N>) {
+        return group_allreduce<N>(v);
+    } else if (LANES == 0 || (N == 0 && (lanes & (lanes - 1)) == 0)) {
 #pragma unroll
         for (int off = 16; off >= 1; off /= 2)
             if (off < lanes) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -255,22 +260,25 @@ struct Lane {
     int lane, group, groups;
     bool on;
 };
-template <int UNITS>
+template <int LANES>
 __device__ __forceinline__ Lane lane_of(const RopeArgs& a) {
+    constexpr int N = LANES > 0 ? LANES : LANES < -1 ? -LANES : 0;
     Lane p;
-    if constexpr (UNITS > 0) {
-        p.lane = threadIdx.x % UNITS;
-        p.group = threadIdx.x / UNITS;
-        p.groups = kRopeThreads / UNITS;
-        p.on = true;
+    const int l = threadIdx.x % 32;
+    int in_warp, per_warp, lanes;
+    if constexpr (N > 0) {
+        in_warp = l / N;
+        per_warp = 32 / N;
+        lanes = N;
     } else {
-        // l / lanes by the reciprocal in 16 bits, exact for l below 32
-        const int l = threadIdx.x % 32, in_warp = l * a.inv_lanes >> 16;
-        p.lane = l - in_warp * a.lanes;
-        p.group = static_cast<int>(threadIdx.x / 32) * a.per_warp + in_warp;
-        p.groups = kRopeThreads / 32 * a.per_warp;
-        p.on = in_warp < a.per_warp && (UNITS == 0 || p.lane < a.units);
+        in_warp = l * a.inv_lanes >> 16;  // exact for l below 32
+        per_warp = a.per_warp;
+        lanes = a.lanes;
     }
+    p.lane = l - in_warp * lanes;
+    p.group = static_cast<int>(threadIdx.x / 32) * per_warp + in_warp;
+    p.groups = kRopeThreads / 32 * per_warp;
+    p.on = (kPowerOfTwo<N> || in_warp < per_warp) && (LANES >= 0 || p.lane < a.units);
     return p;
 }
 
@@ -382,10 +390,10 @@ __device__ __forceinline__ void fill_weights(const RopeArgs& a, const void* w, f
     }
 }
 
-template <int E, int UNITS>
+template <int E, int LANES>
 __device__ __forceinline__ void read_table(const float* tab, int some_units, int u,
                                            float2 (&f)[(E + 1) / 2], float2 (&s)[(E + 1) / 2]) {
-    const int units = UNITS > 0 ? UNITS : some_units;
+    const int units = LANES > 0 ? LANES : some_units;
     if constexpr (E == 1) {
         const float2 v = *reinterpret_cast<const float2*>(tab + 2 * u);
         f[0] = make_float2(v.x, 0.f);
@@ -427,9 +435,9 @@ template <int E> constexpr int kUnitsPerLane = E >= 4 ? 1 : kRopeMaxPairs / 32 /
 
 // Byte offsets of a lane's pieces in a head: the first one's, and the second's
 // distance from it.
-template <typename T, int E, bool ADJ, int UNITS>
+template <typename T, int E, bool ADJ, int LANES>
 struct Pieces {
-    static constexpr int NU = UNITS != 0 ? 1 : kUnitsPerLane<E>;
+    static constexpr int NU = LANES != 0 ? 1 : kUnitsPerLane<E>;
     int lo[NU], gap[NU];
     __device__ __forceinline__ void start(const RopeArgs& a, int lane, int lanes) {
 #pragma unroll
@@ -441,7 +449,7 @@ struct Pieces {
         }
     }
     __device__ __forceinline__ int hop(int i) const {
-        if constexpr (ADJ && UNITS > 0) return E * UNITS * static_cast<int>(sizeof(T));
+        if constexpr (ADJ && LANES > 0) return E * LANES * static_cast<int>(sizeof(T));
         return gap[i];
     }
 };
@@ -483,10 +491,10 @@ struct RowCursor {
 // ------------------------------------------------------------------ forward
 // A token's rows are the heads of q, then those of k. With few tokens the blocks
 // of a tile share out its heads.
-template <typename T, int E, bool ADJ, bool NORM, int UNITS>
+template <typename T, int E, bool ADJ, bool NORM, int LANES>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
-    constexpr int NU = UNITS != 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
-    const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
+    constexpr int NU = LANES != 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
+    const int lanes = LANES > 0 ? LANES : LANES < -1 ? -LANES : a.lanes, D = LANES > 0 ? 2 * E * LANES : a.head_dim;
     using X = Elems<T, E>;
     using W = typename X::W;
     constexpr bool RING = E >= 4;
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
     __shared__ TileInfo info[SLOTS];
     float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem + RING_BYTES);  // [2][D] when NORM
     float* tabs = wtab + (NORM ? 2 * D : 0);                                 // [2][tile][D]
-    const Lane me = lane_of<UNITS>(a);
+    const Lane me = lane_of<LANES>(a);
     const int lane = me.lane, group = me.group, groups = me.groups;
 
     const int part = static_cast<int>(blockIdx.x) / a.splits;
@@ -512,7 +520,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
     const int qheads = a.t[0].heads * (split + 1) / a.splits - qh0;
     const int heads = qheads + a.t[1].heads * (split + 1) / a.splits - kh0;
     const int dt = groups / heads, dh = groups - dt * heads;
-    Pieces<T, E, ADJ, UNITS> at;
+    Pieces<T, E, ADJ, LANES> at;
     at.start(a, lane, lanes);
     const float inv_d = 1.f / static_cast<float>(D);
     wait_for_prerequisite_grid();  // no global access before this
@@ -548,7 +556,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
                                 static_cast<uint32_t>((second ? a.t[1].xs[2] : a.t[0].xs[2]) * sizeof(T)));
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
-                    if (UNITS != 0 || lane + i * lanes < a.units) {
+                    if (LANES != 0 || lane + i * lanes < a.units) {
                         const uint64_t p = src + at.lo[i], p2 = p + at.hop(i);
                         if constexpr (RING) {
                             copy_own<sizeof(W)>(to, reinterpret_cast<const void*>(p), a.status);
@@ -610,17 +618,17 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
                 float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
-                    if (live && (UNITS != 0 || lane + i * lanes < a.units)) {
+                    if (live && (LANES != 0 || lane + i * lanes < a.units)) {
 #pragma unroll
                         for (int e = 0; e < P; ++e)
                             ss = __ffma2_rn(f[i][e], f[i][e], __ffma2_rn(s[i][e], s[i][e], ss));
                     }
-                const float2 rs = f2_splat(rsqrtf(lanes_sum<UNITS>(ss.x + ss.y, lanes, lane) * inv_d + a.eps));
+                const float2 rs = f2_splat(rsqrtf(lanes_sum<LANES>(ss.x + ss.y, lanes, lane) * inv_d + a.eps));
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
-                    if (live && (UNITS != 0 || lane + i * lanes < a.units)) {
+                    if (live && (LANES != 0 || lane + i * lanes < a.units)) {
                         float2 wf[P], ws[P];
-                        read_table<E, UNITS>(wtab + (second ? D : 0), a.units, lane + i * lanes, wf, ws);
+                        read_table<E, LANES>(wtab + (second ? D : 0), a.units, lane + i * lanes, wf, ws);
 #pragma unroll
                         for (int e = 0; e < P; ++e) {
                             f[i][e] = __fmul2_rn(__fmul2_rn(f[i][e], rs), wf[e]);
@@ -634,9 +642,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
                             static_cast<uint32_t>((second ? a.t[1].os[2] : a.t[0].os[2]) * sizeof(T)));
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                if (UNITS == 0 && lane + i * lanes >= a.units) continue;
+                if (LANES == 0 && lane + i * lanes >= a.units) continue;
                 float2 c[P], n[P], yf[P], ys[P], yl[P], yh[P];
-                read_table<E, UNITS>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
+                read_table<E, LANES>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
 #pragma unroll
                 for (int e = 0; e < P; ++e) turn(f[i][e], s[i][e], c[e], n[e], yf[e], ys[e]);
                 join_pairs<E, ADJ>(yf, ys, yl, yh);
@@ -662,11 +670,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
 // their lanes' shares of dw in registers; at the end the groups' shares are
 // added in a fixed order into the block's partial row. No floating-point
 // atomics.
-template <typename T, int E, bool ADJ, int UNITS>
+template <typename T, int E, bool ADJ, int LANES>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
-    constexpr int NU = UNITS != 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
-    const int lanes = UNITS > 0 ? UNITS : a.lanes, D = UNITS > 0 ? 2 * E * UNITS : a.head_dim;
+    constexpr int NU = LANES != 0 ? 1 : kUnitsPerLane<E>, P = (E + 1) / 2;
+    const int lanes = LANES > 0 ? LANES : LANES < -1 ? -LANES : a.lanes, D = LANES > 0 ? 2 * E * LANES : a.head_dim;
     using X = Elems<T, E>;
     using W = typename X::W;
     constexpr bool RING = E >= 4;
@@ -675,7 +683,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     __shared__ TileInfo info[SLOTS];
     float* wtab = reinterpret_cast<float*>(rmsn_dynamic_smem + RING_BYTES);
     float* tabs = wtab + D;  // [2][tile][D]
-    const Lane me = lane_of<UNITS>(a);
+    const Lane me = lane_of<LANES>(a);
     const int lane = me.lane, group = me.group, groups = me.groups;
 
     const int which = static_cast<int>(blockIdx.x) >= a.blocks0 ? 1 : 0;
@@ -693,7 +701,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     const uint32_t x_step = static_cast<uint32_t>(x.xs[2] * sizeof(T));
     const uint32_t dy_step = static_cast<uint32_t>(x.dys[2] * sizeof(T));
     const uint32_t out_step = static_cast<uint32_t>(x.os[2] * sizeof(T));
-    Pieces<T, E, ADJ, UNITS> at;
+    Pieces<T, E, ADJ, LANES> at;
     at.start(a, lane, lanes);
     float2 dwf[NU][P], dws[NU][P];
 #pragma unroll
@@ -730,7 +738,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
                 const uint64_t dys = row_address(info[row_slot].addr[1][row.t], row.head, dy_step);
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
-                    if (UNITS != 0 || lane + i * lanes < a.units) {
+                    if (LANES != 0 || lane + i * lanes < a.units) {
                         const T* p = reinterpret_cast<const T*>(src + at.lo[i]);
                         const T* q = reinterpret_cast<const T*>(dys + at.lo[i]);
                         const T* p2 = reinterpret_cast<const T*>(src + at.lo[i] + at.hop(i));
@@ -774,8 +782,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     float2 wf[NU][P], ws[NU][P];
 #pragma unroll
     for (int i = 0; i < NU; ++i)
-        if (UNITS != 0 || lane + i * lanes < a.units)
-            read_table<E, UNITS>(wtab, a.units, lane + i * lanes, wf[i], ws[i]);
+        if (LANES != 0 || lane + i * lanes < a.units)
+            read_table<E, LANES>(wtab, a.units, lane + i * lanes, wf[i], ws[i]);
     if (range.tiles > 0) fill_angles<T, E, ADJ>(a, pair, tabs, info[0], range.count(0));
     int buf = 0, slot = 0, fill = AHEAD;
 #pragma unroll 1
@@ -814,12 +822,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
             float2 ss = make_float2(0.f, 0.f), hx = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                if (!live || (UNITS == 0 && lane + i * lanes >= a.units)) continue;
+                if (!live || (LANES == 0 && lane + i * lanes >= a.units)) continue;
                 float2 l[P], h[P], f[P], s[P], c[P], n[P];
                 X::unpack(xl[i], l);
                 X::unpack(xh[i], h);
                 split_pairs<E, ADJ>(l, h, f, s);
-                read_table<E, UNITS>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
+                read_table<E, LANES>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
 #pragma unroll
                 for (int e = 0; e < P; ++e) turn(gf[i][e], gs[i][e], c[e], n[e], gf[i][e], gs[i][e]);
 #pragma unroll
@@ -829,7 +837,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
                                     __ffma2_rn(__fmul2_rn(gs[i][e], ws[i][e]), s[e], hx));
                 }
             }
-            const float sum = lanes_sum<UNITS>(ss.x + ss.y, lanes, lane), dot = lanes_sum<UNITS>(hx.x + hx.y, lanes, lane);
+            const float sum = lanes_sum<LANES>(ss.x + ss.y, lanes, lane), dot = lanes_sum<LANES>(hx.x + hx.y, lanes, lane);
             const float rs = rsqrtf(sum * inv_d + a.eps);
             const float2 rs2 = f2_splat(rs);
             // rs (h - xhat mean(h xhat)) = (g rs) w + x coef
@@ -838,7 +846,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
             const uint64_t dst = row_address(info[slot].addr[2][cur.t], cur.head, out_step);
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
-                if (UNITS == 0 && lane + i * lanes >= a.units) continue;
+                if (LANES == 0 && lane + i * lanes >= a.units) continue;
                 float2 l[P], h[P], f[P], s[P];
                 X::unpack(xl[i], l);
                 X::unpack(xh[i], h);
@@ -872,7 +880,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
         const int u = lane + i * lanes;
-        if (!me.on || (UNITS == 0 && u >= a.units)) continue;
+        if (!me.on || (LANES == 0 && u >= a.units)) continue;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             int p, q;
@@ -892,21 +900,26 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     }
 }
 
-template <typename T, int E, int UNITS>
+template <typename T, int E, int LANES>
 RopeFn kernel_of(bool bwd, bool adjacent, bool norm) {
-    if (bwd) return adjacent ? &rope_bwd_kernel<T, E, true, UNITS> : &rope_bwd_kernel<T, E, false, UNITS>;
+    if (bwd) return adjacent ? &rope_bwd_kernel<T, E, true, LANES> : &rope_bwd_kernel<T, E, false, LANES>;
     if (adjacent)
-        return norm ? &rope_fwd_kernel<T, E, true, true, UNITS> : &rope_fwd_kernel<T, E, true, false, UNITS>;
-    return norm ? &rope_fwd_kernel<T, E, false, true, UNITS> : &rope_fwd_kernel<T, E, false, false, UNITS>;
+        return norm ? &rope_fwd_kernel<T, E, true, true, LANES> : &rope_fwd_kernel<T, E, true, false, LANES>;
+    return norm ? &rope_fwd_kernel<T, E, false, true, LANES> : &rope_fwd_kernel<T, E, false, false, LANES>;
 }
 template <typename T>
-RopeFn kernel_for_type(int e, int units, bool bwd, bool adjacent, bool norm) {
-    // 16-byte pieces of heads of 64, 128 and 256: constant geometry
+RopeFn kernel_for_type(int e, int units, int lanes, bool bwd, bool adjacent, bool norm) {
+    // constant geometry for 16-byte pieces of heads of 64, 80, 96, 128 and 256, a
+    // constant number of lanes for those in between
     constexpr int E = 16 / sizeof(T), U = 32 / E;
     if (e == E) {
         if (units == U) return kernel_of<T, E, U>(bwd, adjacent, norm);
         if (units == 2 * U) return kernel_of<T, E, 2 * U>(bwd, adjacent, norm);
         if (units == 4 * U) return kernel_of<T, E, 4 * U>(bwd, adjacent, norm);
+        if (lanes == 40 / E) return kernel_of<T, E, 40 / E>(bwd, adjacent, norm);
+        if constexpr (E == 8)
+            if (lanes == 6) return kernel_of<T, E, 6>(bwd, adjacent, norm);
+        if (lanes == 2 * U) return kernel_of<T, E, -2 * U>(bwd, adjacent, norm);
         return kernel_of<T, E, -1>(bwd, adjacent, norm);
     }
     if constexpr (E != 4)
