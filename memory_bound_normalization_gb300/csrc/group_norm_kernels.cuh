@@ -23,16 +23,16 @@
 //             shared-memory slots, the blocks' sums meet in distributed shared
 //             memory. One read of x. Bound by its steps' latency (launch, first
 //             bytes, two joins): 4 samples of 4096 positions of 320 f16 channels
-//             take 12.4 us forward (21 MB, a floor of 3.1), 8 of 1024 of 640 bf16
-//             backward 14.0 (31 MB, 4.7), 2 of 64 of 1280 forward 5.0.
+//             take 10.4 us forward (21 MB, a floor of 3.1), 8 of 1024 of 640 bf16
+//             backward 13.9 (31 MB, 4.7), 2 of 64 of 1280 forward 3.8.
 //   stream    larger slabs: persistent blocks of one cooperative launch sum a
 //             slab and apply it in the opposite order, so that the second pass
 //             starts with what L2 still holds. Bound by the two passes, whose
 //             second is served by L2 for some six tenths of its bytes (DRAM read
 //             1.4 times x for slabs of 67 MB), and by the meeting between them
 //             (some 5 us a round): 1048576 positions of 128 bf16 channels forward
-//             (537 MB) take 129 us (4.2 TB/s of x and y), 2 samples of 262144 of
-//             256 backward (805 MB) 206 (3.9 TB/s).
+//             (537 MB) take 125 us (4.3 TB/s of x and y), 2 samples of 262144 of
+//             256 backward (805 MB) 204 (3.9 TB/s).
 #pragma once
 
 #include "group_norm.cuh"
