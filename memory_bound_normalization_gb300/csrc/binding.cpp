@@ -233,7 +233,7 @@ size_t group_norm_need(const GroupNorm& g, int backward, int device) {
         size_t need;
         bool set;
     };
-    static std::array<Kept, 64> kept{};  // under the interpreter's lock
+    static std::array<Kept, 1024> kept{};  // under the interpreter's lock
     const uint64_t h = (g.B * 1000003ull + g.S) * 1000003ull + g.C * 31ull + g.G * 7ull + g.code + backward * 5ull;
     Kept& k = kept[(h ^ (h >> 17)) % kept.size()];
     if (!(k.set && k.g.B == g.B && k.g.S == g.S && k.g.C == g.C && k.g.G == g.G && k.g.code == g.code &&

@@ -1,6 +1,7 @@
 // Group norm, host side: the choice of a kernel family, its geometry and the
 // launches.
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 
 #include "common.cuh"
@@ -28,25 +29,27 @@ SlabFn kernel_for(int dtype, bool bwd, int act, SlabKind k) {
     }
 }
 
-// Clusters of a kernel that the device runs at once (0: it refuses the size);
-// the answer is kept, so that a shape's grid is the same on every call.
+// Places of a table of 1024 entries, by a multiplicative hash of the keys.
+unsigned place(std::initializer_list<int64_t> keys) {
+    uint64_t h = 0;
+    for (int64_t k : keys) h = (h ^ static_cast<uint64_t>(k)) * 0x9E3779B97F4A7C15ull, h ^= h >> 29;
+    return static_cast<unsigned>(h % 1024);
+}
+
+// Clusters of a kernel that the device runs at once (0: it refuses the size).
 struct OccEntry {
     int device;
-    SlabFn fn;
+    SlabFn fn;  // nullptr: empty
     int threads, smem, cluster, clusters;
 };
 std::mutex g_occ_mu;
-OccEntry g_occ[512];
-int g_occ_n = 0;
+OccEntry g_occ[1024];
 
 int resident_clusters(const DeviceInfo& dev, SlabFn fn, int threads, int smem, int cluster) {
     std::lock_guard<std::mutex> lk(g_occ_mu);
-    for (int i = 0; i < g_occ_n; ++i) {
-        const OccEntry& e = g_occ[i];
-        if (e.device == dev.device && e.fn == fn && e.threads == threads && e.smem == smem &&
-            e.cluster == cluster)
-            return e.clusters;
-    }
+    OccEntry& e = g_occ[place({dev.device, reinterpret_cast<int64_t>(fn), threads, smem, cluster})];
+    if (e.device == dev.device && e.fn == fn && e.threads == threads && e.smem == smem && e.cluster == cluster)
+        return e.clusters;
     const void* f = reinterpret_cast<const void*>(fn);
     int n = 0;
     cudaError_t err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
@@ -70,7 +73,7 @@ int resident_clusters(const DeviceInfo& dev, SlabFn fn, int threads, int smem, i
         cudaGetLastError();
         n = 0;
     }
-    if (g_occ_n < 512) g_occ[g_occ_n++] = {dev.device, fn, threads, smem, cluster, n};
+    e = {dev.device, fn, threads, smem, cluster, n};
     return n;
 }
 
@@ -194,33 +197,29 @@ Plan make_plan(const DeviceInfo& dev, int dtype, bool bwd, const GroupNormArgs& 
     return p;
 }
 
-// The last plans by shape: making one asks the occupancy tables some twenty
-// times, a few microseconds of a call that may run for as many on the GPU.
+// Plans by shape: making one asks the occupancy tables some dozens of times,
+// longer than a call may run on the GPU. A plan depends on its key alone, so it
+// may be dropped and made again.
 struct PlanEntry {
     int device, dtype, bwd, act, C, G;
-    int64_t B, S;
+    int64_t B, S;  // B 0: empty
     Plan plan;
 };
 std::mutex g_plan_mu;
-PlanEntry g_plans[64];
-int g_plan_n = 0, g_plan_next = 0;
+PlanEntry g_plans[1024];
 
 Plan plan_of(const DeviceInfo& dev, int dtype, bool vec, bool bwd, const GroupNormArgs& a) {
     if (!vec) return Plan{};
+    PlanEntry& e = g_plans[place({a.S, a.B, a.C, a.G, dtype, a.act, bwd ? 1 : 0, dev.device})];
     {
         std::lock_guard<std::mutex> lk(g_plan_mu);
-        for (int i = 0; i < g_plan_n; ++i) {
-            const PlanEntry& e = g_plans[i];
-            if (e.S == a.S && e.B == a.B && e.C == a.C && e.G == a.G && e.dtype == dtype &&
-                e.act == a.act && e.bwd == (bwd ? 1 : 0) && e.device == dev.device)
-                return e.plan;
-        }
+        if (e.S == a.S && e.B == a.B && e.C == a.C && e.G == a.G && e.dtype == dtype && e.act == a.act &&
+            e.bwd == (bwd ? 1 : 0) && e.device == dev.device)
+            return e.plan;
     }
     const Plan p = make_plan(dev, dtype, bwd, a);
     std::lock_guard<std::mutex> lk(g_plan_mu);
-    g_plans[g_plan_next] = {dev.device, dtype, bwd ? 1 : 0, a.act, a.C, a.G, a.B, a.S, p};
-    g_plan_next = (g_plan_next + 1) % 64;
-    g_plan_n = std::min(64, g_plan_n + 1);
+    e = {dev.device, dtype, bwd ? 1 : 0, a.act, a.C, a.G, a.B, a.S, p};
     return p;
 }
 
