@@ -205,6 +205,28 @@ def test_rope_rows_and_tiles(case, dtype, w_dtype, adjacent):
     rp.verify(a, dq, dk, adjacent=adjacent)
 
 
+# every number of units a head can have with 16- and 8-byte pieces, and some of
+# single elements: groups of as many lanes, of the next power of two, idle lanes
+@pytest.mark.parametrize("adjacent", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("dtype,w_dtype", [(F16, F16), (F32, F32)], ids=["f16", "f32"])
+@pytest.mark.parametrize("D", [4, 8, 12, 16, 24, 30, 32, 40, 48, 56, 72, 80, 88, 104, 112, 120, 132, 144, 160, 176,
+                               192, 208, 224, 240, 248])
+def test_rope_every_width(D, dtype, w_dtype, adjacent):
+    a, dq, dk = rp.make((37,), 3, 2, D, (D // 2 - D // 4, D // 4), dtype, w_dtype, seed=D)
+    rp.verify(a, dq, dk, adjacent=adjacent)
+
+
+# group widths around the lanes that join them, channels that split over blocks
+# or not, fewer positions than lanes
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("S", [1, 7, 260])
+@pytest.mark.parametrize("C,G", [(8, 8), (16, 4), (24, 8), (72, 8), (136, 8), (200, 4), (264, 8), (320, 64), (512, 4),
+                                 (1056, 32), (2048, 2)])
+def test_group_norm_widths(C, G, S, dtype):
+    x, w, b, dy = gn.make(3, S, C, dtype, F32, seed=C)
+    gn.both(x, w, b, dy, G, "silu")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("shape", [(1, 20000, 96, 8), (1, 900, 640, 32)], ids=lambda s: "x".join(map(str, s)))
 def test_mean_far_from_zero_behind_borders(shape, dtype):
