@@ -25,13 +25,10 @@
 namespace {
 
 struct Entry {
-    decltype(&rmsnorm_group_norm_fwd) gn_fwd;
     decltype(&rmsnorm_group_norm_fwd_ws) gn_fwd_ws;
-    decltype(&rmsnorm_group_norm_bwd) gn_bwd;
     decltype(&rmsnorm_group_norm_bwd_ws) gn_bwd_ws;
     decltype(&rmsnorm_group_norm_workspace_size) gn_need;
     decltype(&rmsnorm_qk_rope_fwd) rope_fwd;
-    decltype(&rmsnorm_qk_rope_bwd) rope_bwd;
     decltype(&rmsnorm_qk_rope_bwd_ws) rope_bwd_ws;
     decltype(&rmsnorm_qk_rope_bwd_workspace_size) rope_need;
 } g_entry;
@@ -124,22 +121,23 @@ at::Tensor make(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& li
     return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
 }
 
-// The call's stream and its workspace. The caching allocator's memory is
-// ordered on the current stream, so a call on another one leaves its workspace
-// to the library, which takes it in that stream's order.
+// The call's device, stream and workspace. A stream that is given is the current
+// one meanwhile: the caching allocator then gives memory ordered on it, for the
+// outputs as for the workspace.
 struct Run {
     c10::cuda::CUDAGuard guard;
+    std::optional<c10::cuda::CUDAStreamGuard> on;
     cudaStream_t stream;
-    bool foreign;
     void* ws = nullptr;
     Run(const at::Tensor& x, PyObject* s) : guard(x.device()) {
-        stream = c10::cuda::getCurrentCUDAStream(x.get_device()).stream();
-        foreign = false;
-        if (s != Py_None) {
-            const cudaStream_t there = reinterpret_cast<cudaStream_t>(integer(s));
-            foreign = there != stream;
-            stream = there;
-        }
+        const auto device = x.get_device();
+        stream = c10::cuda::getCurrentCUDAStream(device).stream();
+        if (s == Py_None) return;
+        const cudaStream_t there = reinterpret_cast<cudaStream_t>(integer(s));
+        if (there == stream) return;
+        on.emplace(there == nullptr ? c10::cuda::getDefaultCUDAStream(device)
+                                    : c10::cuda::getStreamFromExternal(there, device));
+        stream = there;
     }
     ~Run() {
         if (ws != nullptr) c10::cuda::CUDACachingAllocator::raw_delete(ws);
@@ -259,16 +257,14 @@ PyObject* group_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
         Run run(x, a[6]);
         const at::Tensor y = make(x.sizes(), x.scalar_type(), x);
         const at::Tensor mean = make({g.B, g.G}, at::kFloat, x), rstd = make({g.B, g.G}, at::kFloat, x);
-        const size_t need = run.foreign ? 0 : group_norm_need(g, 0, x.get_device());
+        const size_t need = group_norm_need(g, 0, x.get_device());
         void* ws = run.workspace(need);
         const void *px = x.const_data_ptr(), *pw = data(w), *pb = data(b);
         void* py = y.mutable_data_ptr();
         float *pm = mean.mutable_data_ptr<float>(), *pr = rstd.mutable_data_ptr<float>();
         check("rmsnorm_group_norm_fwd", [&] {
-            return run.foreign ? g_entry.gn_fwd(px, pw, pb, py, pm, pr, g.B, g.S, g.C, g.G, eps, g.act, g.code,
-                                                run.stream)
-                               : g_entry.gn_fwd_ws(px, pw, pb, py, pm, pr, g.B, g.S, g.C, g.G, eps, g.act,
-                                                   g.code, ws, need, run.stream);
+            return g_entry.gn_fwd_ws(px, pw, pb, py, pm, pr, g.B, g.S, g.C, g.G, eps, g.act, g.code, ws, need,
+                                     run.stream);
         });
         return tuple(y, mean, rstd);
     });
@@ -306,7 +302,7 @@ PyObject* group_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
             dw = make({g.C}, at::kFloat, x);
             db = make({g.C}, at::kFloat, x);
         }
-        const size_t need = run.foreign ? 0 : group_norm_need(g, 1, x.get_device());
+        const size_t need = group_norm_need(g, 1, x.get_device());
         void* ws = run.workspace(need);
         const void *px = x.const_data_ptr(), *pw = data(w), *pb = data(b), *pdy = dy.const_data_ptr();
         const float *pm = mean.const_data_ptr<float>(), *pr = rstd.const_data_ptr<float>();
@@ -314,10 +310,8 @@ PyObject* group_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
         float* pdw = dw ? dw->mutable_data_ptr<float>() : nullptr;
         float* pdb = db ? db->mutable_data_ptr<float>() : nullptr;
         check("rmsnorm_group_norm_bwd", [&] {
-            return run.foreign ? g_entry.gn_bwd(px, pw, pb, pdy, pm, pr, pdx, pdw, pdb, g.B, g.S, g.C, g.G,
-                                                g.act, g.code, run.stream)
-                               : g_entry.gn_bwd_ws(px, pw, pb, pdy, pm, pr, pdx, pdw, pdb, g.B, g.S, g.C, g.G,
-                                                   g.act, g.code, ws, need, run.stream);
+            return g_entry.gn_bwd_ws(px, pw, pb, pdy, pm, pr, pdx, pdw, pdb, g.B, g.S, g.C, g.G, g.act, g.code, ws,
+                                     need, run.stream);
         });
         return tuple(dx, dw, db);
     });
@@ -482,7 +476,7 @@ PyObject* qk_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
         if (wq) {
             dwq = make(wq->sizes(), at::kFloat, q);
             if (k) dwk = make(wk->sizes(), at::kFloat, q);
-            if (!run.foreign) need = g_entry.rope_need(r.d.head_dim, q.get_device());
+            need = g_entry.rope_need(r.d.head_dim, q.get_device());
         }
         void* ws = run.workspace(need);
         const void *pq = q.const_data_ptr(), *pk = data(k), *pwq = data(wq), *pwk = data(wk),
@@ -492,10 +486,8 @@ PyObject* qk_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
         float* pdwq = dwq ? dwq->mutable_data_ptr<float>() : nullptr;
         float* pdwk = dwk ? dwk->mutable_data_ptr<float>() : nullptr;
         check("rmsnorm_qk_rope_bwd", [&] {
-            return ws == nullptr ? g_entry.rope_bwd(&r.d, pq, pk, pwq, pwk, pp, pf, pdqo, pdko, pdq, pdk, pdwq,
-                                                    pdwk, eps, r.code, run.stream)
-                                 : g_entry.rope_bwd_ws(&r.d, pq, pk, pwq, pwk, pp, pf, pdqo, pdko, pdq, pdk,
-                                                       pdwq, pdwk, eps, r.code, ws, need, run.stream);
+            return g_entry.rope_bwd_ws(&r.d, pq, pk, pwq, pwk, pp, pf, pdqo, pdko, pdq, pdk, pdwq, pdwk, eps, r.code,
+                                       ws, need, run.stream);
         });
         return tuple(dq, dk, dwq, dwk);
     });
@@ -504,18 +496,15 @@ PyObject* qk_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
 // setup(error type, addresses in the order of Entry)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        if (n != 10) bad_value("setup: an error type and nine addresses");
-        void* p[9];
-        for (int i = 0; i < 9; ++i) p[i] = reinterpret_cast<void*>(integer(a[i + 1]));
-        g_entry = {reinterpret_cast<decltype(g_entry.gn_fwd)>(p[0]),
-                   reinterpret_cast<decltype(g_entry.gn_fwd_ws)>(p[1]),
-                   reinterpret_cast<decltype(g_entry.gn_bwd)>(p[2]),
-                   reinterpret_cast<decltype(g_entry.gn_bwd_ws)>(p[3]),
-                   reinterpret_cast<decltype(g_entry.gn_need)>(p[4]),
-                   reinterpret_cast<decltype(g_entry.rope_fwd)>(p[5]),
-                   reinterpret_cast<decltype(g_entry.rope_bwd)>(p[6]),
-                   reinterpret_cast<decltype(g_entry.rope_bwd_ws)>(p[7]),
-                   reinterpret_cast<decltype(g_entry.rope_need)>(p[8])};
+        if (n != 7) bad_value("setup: an error type and six addresses");
+        void* p[6];
+        for (int i = 0; i < 6; ++i) p[i] = reinterpret_cast<void*>(integer(a[i + 1]));
+        g_entry = {reinterpret_cast<decltype(g_entry.gn_fwd_ws)>(p[0]),
+                   reinterpret_cast<decltype(g_entry.gn_bwd_ws)>(p[1]),
+                   reinterpret_cast<decltype(g_entry.gn_need)>(p[2]),
+                   reinterpret_cast<decltype(g_entry.rope_fwd)>(p[3]),
+                   reinterpret_cast<decltype(g_entry.rope_bwd_ws)>(p[4]),
+                   reinterpret_cast<decltype(g_entry.rope_need)>(p[5])};
         Py_INCREF(a[0]);
         Py_XSETREF(g_error, a[0]);
         Py_RETURN_NONE;

@@ -4,9 +4,9 @@ rmsnorm_qk_rope_* in include/rmsnorm.h).
 
 The functions check their arguments, allocate outputs with PyTorch and raise
 ``RMSNormError`` on a non-OK status, like ``forward`` and ``backward``. They
-run on the tensors' own device and, unless ``stream`` is given, on its current
-stream; workspaces come from PyTorch's allocator too. ``autograd`` holds the
-differentiable forms.
+run on the tensors' own device and on its current stream, or on ``stream`` as if
+that were the current one (outputs belong to it); workspaces come from PyTorch's
+allocator too. ``autograd`` holds the differentiable forms.
 
 Their checks, allocations and calls are compiled (csrc/binding.cpp): in Python
 they took longer than the kernels of a decode step.
@@ -21,9 +21,8 @@ from . import _lib
 from . import build as _build
 
 # the entry points binding.cpp calls, in the order of its table
-_ENTRIES = ("rmsnorm_group_norm_fwd", "rmsnorm_group_norm_fwd_ws", "rmsnorm_group_norm_bwd",
-            "rmsnorm_group_norm_bwd_ws", "rmsnorm_group_norm_workspace_size",
-            "rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_qk_rope_bwd_ws",
+_ENTRIES = ("rmsnorm_group_norm_fwd_ws", "rmsnorm_group_norm_bwd_ws",
+            "rmsnorm_group_norm_workspace_size", "rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd_ws",
             "rmsnorm_qk_rope_bwd_workspace_size")
 _bound = None
 

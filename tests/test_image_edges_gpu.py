@@ -189,6 +189,32 @@ def test_rope_backward_on_another_stream():
             assert torch.equal(u, v)
 
 
+@pytest.mark.parametrize("call", ["group_norm", "rope"])
+def test_memory_of_another_stream(call):
+    """A call on a given stream takes no memory that the current stream still has
+    work queued on."""
+    n = 1 << 20
+    x = torch.randn(1, n // 64, 64, device=DEV)
+    q = x.view(n // 128, 2, 64)
+    pos = torch.zeros(1, n // 128, dtype=torch.int32, device=DEV)
+    freq = torch.ones(32, device=DEV)
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        t = torch.full((n,), 7.0, device=DEV)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)
+        seen = t.clone()
+        del t
+        if call == "group_norm":
+            got = pkg.group_norm_forward(x, 8, stream=s)
+        else:
+            got = pkg.qk_rope_forward(q, None, None, None, pos, freq, (32,), stream=s)
+        s.synchronize()
+        torch.cuda.synchronize()
+        assert (seen == 7).all()
+        del got
+
+
 # ------------------------------------------------------------- shapes
 # (lead, Hq, Hk, D, sections): tiles of one pass and of a part of one, rows that
 # end inside a pass, many heads a token, more tokens than blocks
