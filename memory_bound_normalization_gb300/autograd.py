@@ -11,6 +11,10 @@ tensors; rows are the last dimension.
 ``group_norm`` / ``GroupNorm`` (channels last, with an activation) and
 ``qk_norm_rope`` / ``QKNormRope`` (QK-norm and rotary positions of several
 axes) do the same over their operators.
+
+Backward passes can be captured into CUDA graphs as PyTorch's own can: not while
+an eager graph of the same leaves is alive, whose streams the capture cannot wait
+for (PyTorch raises then).
 """
 from __future__ import annotations
 
