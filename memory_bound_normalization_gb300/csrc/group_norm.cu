@@ -320,7 +320,7 @@ cudaError_t group_norm_launch(const DeviceInfo& dev, int dtype, bool vec, bool b
     sum.out[1] = a.db;
     sum.rows[0] = sum.rows[1] = static_cast<int>(rows);
     sum.n = a.C;
-    sum.stride = 2 * a.C;
+    sum.stride = 2 * static_cast<int64_t>(a.C);
     sum.status = a.status;
     return pair_sum_launch(sum, s);
 }

@@ -7,6 +7,8 @@
 
 namespace rmsn {
 
+// Blocks of 32 channels (any count up to 2^31 - 1).
+__host__ __device__ inline int channel_tiles(int C) { return (C - 1) / 32 + 1; }
 // Whether a grid has a block for every chunk.
 bool gn_scalar_fits(const GroupNormArgs& a);
 size_t gn_scalar_workspace(bool bwd, const GroupNormArgs& a);

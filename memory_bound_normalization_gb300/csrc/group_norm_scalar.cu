@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) gn_scalar_sums_kernel(const __grid_c
                                                                   float* parts, int chunks) {
     __shared__ float sp[8][33], sq[8][33];
     const int cx = threadIdx.x % 32, ry = threadIdx.x / 32;
-    const int ctiles = (a.C + 31) / 32;
+    const int ctiles = channel_tiles(a.C);
     const int64_t row = blockIdx.x / ctiles;  // sample * chunks + chunk
     const int ch = static_cast<int>(blockIdx.x % ctiles) * 32 + cx;
     const int64_t b = row / chunks, k = row % chunks;
@@ -210,7 +210,7 @@ int scalar_chunks(const GroupNormArgs& a) {
 template <typename T>
 cudaError_t launch_typed(bool bwd, const GroupNormArgs& a, void* ws, cudaStream_t s) {
     const int chunks = scalar_chunks(a);
-    const int64_t slabs = a.B * a.G * chunks, rows = a.B * chunks, ctiles = cdiv(a.C, 32);
+    const int64_t slabs = a.B * a.G * chunks, rows = a.B * chunks, ctiles = channel_tiles(a.C);
     if (!bwd) {
         float2* parts = static_cast<float2*>(ws);
         cudaError_t err = launch_pdl(&gn_scalar_stats_kernel<T>, static_cast<int>(slabs), kThreads,
@@ -233,7 +233,7 @@ cudaError_t launch_typed(bool bwd, const GroupNormArgs& a, void* ws, cudaStream_
     p.out[1] = a.db;
     p.rows[0] = p.rows[1] = static_cast<int>(rows);
     p.n = a.C;
-    p.stride = 2 * a.C;
+    p.stride = 2 * static_cast<int64_t>(a.C);
     p.status = a.status;
     return pair_sum_launch(p, s);
 }
@@ -241,7 +241,7 @@ cudaError_t launch_typed(bool bwd, const GroupNormArgs& a, void* ws, cudaStream_
 }  // namespace
 
 bool gn_scalar_fits(const GroupNormArgs& a) {
-    const int64_t wide = std::max<int64_t>(a.G, cdiv(a.C, 32));  // blocks of a chunk
+    const int64_t wide = std::max<int64_t>(a.G, channel_tiles(a.C));  // blocks of a chunk
     return a.B <= INT32_MAX / (wide * scalar_chunks(a));
 }
 

@@ -93,7 +93,8 @@ struct PairSum {
     const float* part[2];
     float* out[2];
     int rows[2];
-    int n, stride;
+    int n;
+    int64_t stride;  // twice the channels of a group norm: past 31 bits from 2^30 on
     int* status;
 };
 cudaError_t pair_sum_launch(const PairSum& a, cudaStream_t s);

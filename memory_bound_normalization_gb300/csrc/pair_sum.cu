@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kSumThreads) pair_sum_kernel(const __grid_cons
     float s[W] = {};
 #pragma unroll 4
     for (int p = threadIdx.x; p < rows; p += kSumThreads)
-        Columns<W>::add(s, *reinterpret_cast<const V*>(src + static_cast<int64_t>(p) * a.stride));
+        Columns<W>::add(s, *reinterpret_cast<const V*>(src + p * a.stride));
 #pragma unroll
     for (int i = 0; i < W; ++i) s[i] = group_allreduce<32>(s[i]);
     if (lane == 0) {

@@ -1,0 +1,73 @@
+"""The host side of the image operators over a CUDA runtime that launches
+nothing (fake_cudart.cpp, preloaded in a process of its own): what is launched,
+on which device, with which strides."""
+from __future__ import annotations
+
+import os
+import shutil
+import subprocess
+import sys
+import textwrap
+
+import pytest
+
+from memory_bound_normalization_gb300 import build as libbuild
+
+TESTS = os.path.dirname(os.path.abspath(__file__))
+
+PROLOGUE = """
+import ctypes, os, sys
+import memory_bound_normalization_gb300 as pkg
+from memory_bound_normalization_gb300 import _lib
+fake = ctypes.CDLL(os.environ["LD_PRELOAD"])
+fake.fake_launch.restype = ctypes.POINTER(ctypes.c_int * 7)
+fake.fake_sum_stride.restype = fake.fake_sum_rows.restype = ctypes.c_longlong
+lib = pkg.load_library()
+A = 1 << 44  # addresses that no launch reads
+
+
+def launches():
+    names = ("device", "grid", "rows", "threads", "smem", "cluster", "allowed")
+    return [dict(zip(names, fake.fake_launch(i).contents)) for i in range(fake.fake_launches())]
+"""
+
+
+@pytest.fixture(scope="module")
+def run(tmp_path_factory):
+    libbuild.build()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc")),
+                        "include")
+    so = str(tmp_path_factory.mktemp("fake") / "fake_cudart.so")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-I", cuda, "-I", libbuild.CSRC, "-I",
+                    libbuild.INCLUDE, os.path.join(TESTS, "fake_cudart.cpp"), "-o", so], check=True)
+
+    def call(body):
+        env = dict(os.environ, LD_PRELOAD=so, PYTHONPATH=os.path.dirname(TESTS))
+        out = subprocess.run([sys.executable, "-c", PROLOGUE + textwrap.dedent(body)], env=env,
+                             capture_output=True, text=True, timeout=120)
+        assert out.returncode == 0, out.stdout + out.stderr
+        return out.stdout
+
+    return call
+
+
+@pytest.mark.parametrize("C,G", [(1 << 20, 8), (1 << 30, 8), ((1 << 30) + 8, 4), ((1 << 31) - 1, 1)])
+def test_partial_rows_of_many_channels(run, C, G):
+    """A partial row is 2 C floats, which pass 31 bits with C at 2^30. (x lies off
+    16 bytes: element by element.)"""
+    run(f"""
+    C, G = {C}, {G}
+    st = lib.rmsnorm_group_norm_bwd_ws(A + 2, A, A, A, A, A, A, A, A, 2, 1, C, G, _lib.ACT_NONE, _lib.BF16, A,
+                                       1 << 40, None)
+    assert st == _lib.OK, st
+    assert [l["rows"] for l in launches()] == [1, 1, 2], launches()
+    assert launches()[0]["grid"] == 2 * ((C + 31) // 32)
+    assert fake.fake_sum_rows() == 2
+    assert fake.fake_sum_stride() == 2 * C, fake.fake_sum_stride()
+    """)
+
+
+@pytest.mark.parametrize("C", [1, 31, 32, 33, (1 << 31) - 33, (1 << 31) - 32, (1 << 31) - 1])
+def test_channel_tiles(run, C):
+    """Tiles of 32 channels, as the kernels count them."""
+    run(f"assert fake.fake_channel_tiles({C}) == {-(-C // 32)}, fake.fake_channel_tiles({C})")
