@@ -19,7 +19,7 @@
 namespace rmsn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kItemThreads;
 
 // Sum over the block, the same bits in every thread.
 __device__ __forceinline__ float block_sum(float v, float* scratch) {
@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kThreads) gn_scalar_bwd_kernel(const __grid_co
     T* dx = static_cast<T*>(a.out);
     wait_for_prerequisite_grid();  // the channel sums are complete
     float p = 0.f, q = 0.f;
-    for (int i = threadIdx.x; i < chunks * D; i += kThreads) {
-        const int ch = c.g * D + i % D;
+    for (unsigned i = threadIdx.x; i < static_cast<unsigned>(chunks * D); i = next_item(i)) {
+        const int ch = c.g * D + static_cast<int>(i % D);
         const float w = a.w != nullptr ? weight_at(a.w, ch, a.w_f32, x) : 1.f;
         const float* r = parts + (c.b * chunks + i / D) * 2 * a.C + ch;
         p = fmaf(w, r[0], p);

@@ -12,8 +12,6 @@
 namespace rmsn {
 namespace {
 
-constexpr int kSumThreads = 256;
-
 template <int W>
 struct Columns;
 template <>
@@ -41,10 +39,11 @@ struct Columns<1> {
 };
 
 template <int W>
-__global__ void __launch_bounds__(kSumThreads) pair_sum_kernel(const __grid_constant__ PairSum a) {
+__global__ void __launch_bounds__(kItemThreads) pair_sum_kernel(const __grid_constant__ PairSum a) {
     using V = typename Columns<W>::V;
-    __shared__ float part[kSumThreads / 32][W];
-    const int which = blockIdx.y, col = blockIdx.x * W, rows = a.rows[which];
+    __shared__ float part[kItemThreads / 32][W];
+    const int which = blockIdx.y, col = blockIdx.x * W;
+    const unsigned rows = a.rows[which];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     wait_for_prerequisite_grid();  // partial rows complete and visible
     allow_dependent_launch();
@@ -53,7 +52,7 @@ __global__ void __launch_bounds__(kSumThreads) pair_sum_kernel(const __grid_cons
     const float* src = a.part[which] + col;
     float s[W] = {};
 #pragma unroll 4
-    for (int p = threadIdx.x; p < rows; p += kSumThreads)
+    for (unsigned p = threadIdx.x; p < rows; p = next_item(p))
         Columns<W>::add(s, *reinterpret_cast<const V*>(src + p * a.stride));
 #pragma unroll
     for (int i = 0; i < W; ++i) s[i] = group_allreduce<32>(s[i]);
@@ -65,7 +64,7 @@ __global__ void __launch_bounds__(kSumThreads) pair_sum_kernel(const __grid_cons
     if (threadIdx.x < W && RMSN_OK(span_in(out + col + threadIdx.x, 4, out, static_cast<int64_t>(a.n) * 4), a.status)) {
         float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < kSumThreads / 32; ++w) t += part[w][threadIdx.x];
+        for (int w = 0; w < kItemThreads / 32; ++w) t += part[w][threadIdx.x];
         out[col + threadIdx.x] = t;
     }
 }
@@ -82,7 +81,7 @@ cudaError_t pair_sum_launch(const PairSum& a, cudaStream_t s) {
     const int w = fits(4) ? 4 : fits(2) ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.n / w), 2);
-    cfg.blockDim = dim3(kSumThreads);
+    cfg.blockDim = dim3(kItemThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

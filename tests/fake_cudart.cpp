@@ -88,5 +88,13 @@ int fake_asked(int device) {
 }
 long long fake_sum_stride() { return g_sum.stride; }
 int fake_channel_tiles(int C) { return rmsn::channel_tiles(C); }
+// Items that a thread takes from p on.
+int fake_items_from(int p, int items) {
+    int n = 0;
+    for (auto i = rmsn::next_item(p - rmsn::kItemThreads); i < static_cast<decltype(i)>(items) && n < 1000;
+         i = rmsn::next_item(i))
+        ++n;
+    return n;
+}
 long long fake_sum_rows() { return g_sum.rows[0]; }
 }

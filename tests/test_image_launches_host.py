@@ -71,3 +71,10 @@ def test_partial_rows_of_many_channels(run, C, G):
 def test_channel_tiles(run, C):
     """Tiles of 32 channels, as the kernels count them."""
     run(f"assert fake.fake_channel_tiles({C}) == {-(-C // 32)}, fake.fake_channel_tiles({C})")
+
+
+@pytest.mark.parametrize("items", [1000, (1 << 31) - 300, (1 << 31) - 1])
+@pytest.mark.parametrize("back", [1, 255, 256, 257, 600])
+def test_items_end(run, items, back):
+    """A thread ends behind the last item, also of 2^31 - 1 (partial rows, channels)."""
+    run(f"assert fake.fake_items_from({items - back}, {items}) == {-(-back // 256)}")
