@@ -36,7 +36,28 @@ unsigned place(std::initializer_list<int64_t> keys) {
     return static_cast<unsigned>(h % 1024);
 }
 
-// Clusters of a kernel that the device runs at once (0: it refuses the size).
+// Makes a device the current one for as long as it lives: a workspace's size may
+// be asked for any device.
+class OnDevice {
+public:
+    explicit OnDevice(int device) {
+        ok = cudaGetDevice(&prev) == cudaSuccess && (prev == device || cudaSetDevice(device) == cudaSuccess);
+        changed = ok && prev != device;
+    }
+    ~OnDevice() {
+        if (changed) cudaSetDevice(prev);
+    }
+    OnDevice(const OnDevice&) = delete;
+    OnDevice& operator=(const OnDevice&) = delete;
+    bool ok = false;
+
+private:
+    int prev = -1;
+    bool changed = false;
+};
+
+// Clusters of a kernel that the device runs at once (0: it refuses the size). The
+// kernel is allowed the size there, so that a plan, once kept, launches.
 struct OccEntry {
     int device;
     SlabFn fn;  // nullptr: empty
@@ -50,6 +71,11 @@ int resident_clusters(const DeviceInfo& dev, SlabFn fn, int threads, int smem, i
     OccEntry& e = g_occ[place({dev.device, reinterpret_cast<int64_t>(fn), threads, smem, cluster})];
     if (e.device == dev.device && e.fn == fn && e.threads == threads && e.smem == smem && e.cluster == cluster)
         return e.clusters;
+    const OnDevice there(dev.device);
+    if (!there.ok) {
+        cudaGetLastError();
+        return 0;
+    }
     const void* f = reinterpret_cast<const void*>(fn);
     int n = 0;
     cudaError_t err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);

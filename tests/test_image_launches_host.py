@@ -78,3 +78,43 @@ def test_channel_tiles(run, C):
 def test_items_end(run, items, back):
     """A thread ends behind the last item, also of 2^31 - 1 (partial rows, channels)."""
     run(f"assert fake.fake_items_from({items - back}, {items}) == {-(-back // 256)}")
+
+
+# shapes of clusters of 16, of one streamed slab, of several rounds
+SHAPES = "[(4, 4096, 320, 32), (1, 60000, 64, 8), (6, 60000, 640, 8)]"
+
+
+@pytest.mark.parametrize("bwd", [0, 1])
+def test_workspace_of_another_device(run, bwd):
+    """Asked for a device that is not current, the size is found out there, the
+    current device stays, and a later call there is launched as it may be."""
+    run(f"""
+    for B, S, C, G in {SHAPES}:
+        need = lib.rmsnorm_group_norm_workspace_size(B, S, C, G, _lib.BF16, {bwd}, 1)
+        assert fake.fake_asked(0) == 0 and fake.fake_asked(1) > 0
+        d = ctypes.c_int(-1)
+        assert fake.cudaGetDevice(ctypes.byref(d)) == 0 and d.value == 0
+    fake.cudaSetDevice(1)
+    for B, S, C, G in {SHAPES}:
+        if {bwd}:
+            st = lib.rmsnorm_group_norm_bwd_ws(A, A, A, A, A, A, A, A, A, B, S, C, G, 0, _lib.BF16, A, 1 << 40, None)
+        else:
+            st = lib.rmsnorm_group_norm_fwd_ws(A, A, A, A, A, A, B, S, C, G, 1e-5, 0, _lib.BF16, A, 1 << 40, None)
+        assert st == _lib.OK, (B, S, C, G, launches())
+    assert all(l["device"] == 1 and l["allowed"] for l in launches()), launches()
+    assert max(l["smem"] for l in launches()) > 48 * 1024
+    assert {bwd} or max(l["cluster"] for l in launches()) == 16  # the backward plans fewer here
+    """)
+
+
+def test_calls_on_two_devices(run):
+    """A shape used on one device and then on the other."""
+    run(f"""
+    for device in (0, 1, 0, 1):
+        fake.cudaSetDevice(device)
+        for B, S, C, G in {SHAPES}:
+            assert lib.rmsnorm_group_norm_bwd(A, A, A, A, A, A, A, A, A, B, S, C, G, 1, _lib.BF16, None) == _lib.OK
+            assert lib.rmsnorm_group_norm_fwd(A, A, A, A, A, A, B, S, C, G, 1e-5, 1, _lib.BF16, None) == _lib.OK
+        assert all(l["allowed"] for l in launches()), launches()
+        assert launches()[-1]["device"] == device
+    """)
