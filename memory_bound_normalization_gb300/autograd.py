@@ -229,5 +229,7 @@ class QKNormRope(torch.nn.Module):
         return self
 
     def forward(self, q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor):
-        return qk_norm_rope(q, k, self.q_weight, self.k_weight, positions, self.inv_freq,
-                            self.sections, self.interleaved, self.adjacent, self.eps)
+        # queries alone: the key weight has nothing to scale
+        return qk_norm_rope(q, k, self.q_weight, None if k is None else self.k_weight, positions,
+                            self.inv_freq, self.sections, self.interleaved, self.adjacent,
+                            self.eps)
