@@ -216,16 +216,24 @@ class QKNormRope(torch.nn.Module):
         pairs = sum(self.sections)
         if not 0 < 2 * pairs <= head_dim:
             raise ValueError(f"{pairs} pairs do not fit in heads of {head_dim}")
-        freq = torch.arange(pairs, device=device, dtype=torch.float64).div_(-pairs)
-        self.inv_freq = torch.pow(theta, freq).float()
+        self.theta = float(theta)
+        self.inv_freq = self._frequencies(device)
         for name in ("q_weight", "k_weight"):
             w = torch.ones(head_dim, device=device, dtype=weight_dtype) if norm else None
             self.register_parameter(name, None if w is None else torch.nn.Parameter(w))
 
+    def _frequencies(self, device):
+        pairs = sum(self.sections)
+        freq = torch.arange(pairs, device=device, dtype=torch.float64).div_(-pairs)
+        return torch.pow(self.theta, freq).float()
+
     def _apply(self, fn, *args, **kwargs):
-        # the frequencies follow the module's device but stay fp32
+        # the frequencies follow the module's device but stay fp32; from the meta
+        # device they have no values to take along
         super()._apply(fn, *args, **kwargs)
-        self.inv_freq = self.inv_freq.to(fn(self.inv_freq).device)
+        device = fn(self.inv_freq).device
+        self.inv_freq = (self._frequencies(device) if self.inv_freq.is_meta
+                         else self.inv_freq.to(device))
         return self
 
     def forward(self, q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor):

@@ -22,3 +22,25 @@ def test_queries_alone_reach_the_device_check(norm):
     pos = torch.zeros(2, 3, dtype=torch.int64)
     with pytest.raises(ValueError, match="CUDA tensors"):
         layer(torch.zeros(3, 4, 16), None, pos)
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_materialised_from_the_meta_device(norm):
+    """A module built without memory gets its frequencies with its memory: they
+    are no parameter that a checkpoint would bring."""
+    want = QKNormRope(16, (5, 2), theta=500.0, norm=norm)
+    layer = QKNormRope(16, (5, 2), theta=500.0, norm=norm, device="meta")
+    assert layer.inv_freq.is_meta
+    outer = torch.nn.Sequential(layer).to_empty(device="cpu")
+    assert outer[0].inv_freq.dtype == torch.float32
+    assert torch.equal(outer[0].inv_freq, want.inv_freq)
+    assert torch.equal(want.to_empty(device="cpu").inv_freq, layer.inv_freq)
+    assert layer.to("meta").inv_freq.is_meta
+
+
+def test_frequencies_follow_the_module():
+    layer = QKNormRope(16, (5, 2))
+    before = layer.inv_freq.clone()
+    layer = layer.to(torch.bfloat16).double().cpu()
+    assert layer.inv_freq.dtype == torch.float32 and torch.equal(layer.inv_freq, before)
+    assert layer.q_weight.dtype == torch.float64
