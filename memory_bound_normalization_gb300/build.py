@@ -14,12 +14,15 @@ RMSNORM_LIBRARY_VARIANT=checked is set.
 
 The Python binding of the tensor-level image operators (csrc/binding.cpp, host
 code only, compiled by g++ against PyTorch's headers) goes to
-``_build/_binding.so`` and serves both variants; without PyTorch it is left out.
+``_build/_binding.so`` and serves both variants; without a PyTorch that has CUDA it
+is left out. It is compiled again when PyTorch or Python is another version than the
+one it was made for.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import hashlib
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -108,14 +111,33 @@ def is_stale(checked: bool = False) -> bool:
 
 
 def _torch_dir() -> str | None:
+    """Where PyTorch lies, None without one that has CUDA."""
     spec = importlib.util.find_spec("torch")
-    return None if spec is None else list(spec.submodule_search_locations)[0]
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    path = list(spec.submodule_search_locations)[0]
+    return path if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
+
+
+def _binding_made_for() -> str:
+    """The versions whose interfaces the binding is compiled against."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "of unknown version"
+    return f"torch {torch} in {_torch_dir()}, {sys.implementation.cache_tag}"
 
 
 def binding_is_stale() -> bool:
     if _torch_dir() is None:
         return False
     if not os.path.exists(BINDING_PATH):
+        return True
+    try:
+        with open(BINDING_PATH + ".info") as fh:
+            if fh.read() != _binding_made_for():
+                return True
+    except OSError:
         return True
     t = os.path.getmtime(BINDING_PATH)
     return any(os.path.getmtime(f) > t for f in
@@ -135,6 +157,8 @@ def _build_binding() -> None:
           "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
           "-ltorch", "-ltorch_python"], os.path.join(BUILD_DIR, "binding.log"))
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_PATH + ".info", "w") as fh:
+        fh.write(_binding_made_for())
 
 
 def _run(cmd: list[str], log: str | None) -> None:
@@ -189,12 +213,14 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
     cmds = [c for v in todo for c in plans[v][0]]
     workers = jobs or min(len(cmds) + 1, max(1, os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
-        futures = [ex.submit(_build_binding)] if binding else []
-        futures += [ex.submit(_run, c, log) for c, log in cmds]
+        of_binding = ex.submit(_build_binding) if binding else None
+        futures = [ex.submit(_run, c, log) for c, log in cmds]
         for fut in futures:
             fut.result()
     for v in todo:
         _link(plans[v][1], v)
+    if of_binding is not None:
+        of_binding.result()  # the library does not depend on it
     return lib_path(checked and not both)
 
 

@@ -36,8 +36,8 @@ def _binding():
 
         lib = _lib.load_library()
         if not os.path.exists(_build.BINDING_PATH):
-            raise OSError(f"{_build.BINDING_PATH} is missing: build the CUDA library first "
-                          "(python -c 'import __graft_entry__ as g; g.build()')")
+            raise OSError(f"{_build.BINDING_PATH} is missing: build the CUDA library first, beside a "
+                          "PyTorch with CUDA (python -c 'import __graft_entry__ as g; g.build()')")
         spec = importlib.util.spec_from_file_location("_binding", _build.BINDING_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
