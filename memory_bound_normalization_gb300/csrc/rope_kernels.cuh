@@ -15,7 +15,9 @@
 // 1 GB, in 156 us: 6.5 TB/s; one token of 8 sequences in 3.4 us, the launch and
 // three trips to memory). A group of `lanes` lanes shares a row and each lane owns whole pairs
 // (both halves), so the rotation needs no exchange between lanes and the row
-// sum is one butterfly. The elements that pass are pairs of a zero angle.
+// sum is one butterfly. The elements that pass are pairs too, whose values are
+// taken past the rotation (a turn by zero would give the partner of an infinity
+// inf * 0).
 //
 // Angles: one turn is 2^64, so the product of an integer position and the
 // frequency in turns wraps exactly where the circle does, however far the
@@ -422,6 +424,26 @@ __device__ __forceinline__ void turn(float2 x, float2 y, float2 c, float2 s, flo
     oy = __ffma2_rn(y, c, xs);
 }
 
+// Puts the pairs of a unit that pass back where the rotation changed them. `passes`
+// has a bit for each of the unit's pairs; a unit of halves passes as a whole.
+template <int E, bool ADJ>
+__device__ __forceinline__ void keep_passing(unsigned passes, const float2 (&f)[(E + 1) / 2],
+                                             const float2 (&s)[(E + 1) / 2], float2 (&yf)[(E + 1) / 2],
+                                             float2 (&ys)[(E + 1) / 2]) {
+    if (passes == 0) return;
+#pragma unroll
+    for (int i = 0; i < (E + 1) / 2; ++i) {
+        if (!ADJ || (passes >> 2 * i & 1)) {
+            yf[i].x = f[i].x;
+            ys[i].x = s[i].x;
+        }
+        if (!ADJ || (passes >> (2 * i + 1) & 1)) {
+            yf[i].y = f[i].y;
+            ys[i].y = s[i].y;
+        }
+    }
+}
+
 // One past the last element of a tensor that the call may touch (strides
 // are not negative), for the checked build.
 [[maybe_unused]] __device__ __forceinline__ int64_t extent_bytes(const RopeArgs& a, const RopeTensor& t,
@@ -434,11 +456,12 @@ __device__ __forceinline__ void turn(float2 x, float2 y, float2 c, float2 s, flo
 template <int E> constexpr int kUnitsPerLane = E >= 4 ? 1 : kRopeMaxPairs / 32 / E;
 
 // Byte offsets of a lane's pieces in a head: the first one's, and the second's
-// distance from it.
+// distance from it; and which of the unit's pairs pass.
 template <typename T, int E, bool ADJ, int LANES>
 struct Pieces {
     static constexpr int NU = LANES != 0 ? 1 : kUnitsPerLane<E>;
     int lo[NU], gap[NU];
+    unsigned passes[NU];
     __device__ __forceinline__ void start(const RopeArgs& a, int lane, int lanes) {
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
@@ -446,6 +469,10 @@ struct Pieces {
             unit_offsets<E, ADJ>(a, lane + i * lanes, l, h);
             lo[i] = l * static_cast<int>(sizeof(T));
             gap[i] = (h - l) * static_cast<int>(sizeof(T));
+            passes[i] = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                passes[i] |= pair_at<E, ADJ>(a.units, lane + i * lanes, e) >= a.rot / 2 ? 1u << e : 0u;
         }
     }
     __device__ __forceinline__ int hop(int i) const {
@@ -647,6 +674,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
                 read_table<E, LANES>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
 #pragma unroll
                 for (int e = 0; e < P; ++e) turn(f[i][e], s[i][e], c[e], n[e], yf[e], ys[e]);
+                keep_passing<E, ADJ>(at.passes[i], f[i], s[i], yf, ys);
                 join_pairs<E, ADJ>(yf, ys, yl, yh);
                 W* dl = reinterpret_cast<W*>(dst + at.lo[i]);
                 W* dhi = reinterpret_cast<W*>(dst + at.lo[i] + at.hop(i));
@@ -823,15 +851,18 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
                 if (!live || (LANES == 0 && lane + i * lanes >= a.units)) continue;
-                float2 l[P], h[P], f[P], s[P], c[P], n[P];
+                float2 l[P], h[P], f[P], s[P], c[P], n[P], df[P], ds[P];
                 X::unpack(xl[i], l);
                 X::unpack(xh[i], h);
                 split_pairs<E, ADJ>(l, h, f, s);
                 read_table<E, LANES>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
 #pragma unroll
-                for (int e = 0; e < P; ++e) turn(gf[i][e], gs[i][e], c[e], n[e], gf[i][e], gs[i][e]);
+                for (int e = 0; e < P; ++e) turn(gf[i][e], gs[i][e], c[e], n[e], df[e], ds[e]);
+                keep_passing<E, ADJ>(at.passes[i], gf[i], gs[i], df, ds);
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
+                    gf[i][e] = df[e];
+                    gs[i][e] = ds[e];
                     ss = __ffma2_rn(f[e], f[e], __ffma2_rn(s[e], s[e], ss));
                     hx = __ffma2_rn(__fmul2_rn(gf[i][e], wf[i][e]), f[e],
                                     __ffma2_rn(__fmul2_rn(gs[i][e], ws[i][e]), s[e], hx));
