@@ -424,22 +424,23 @@ __device__ __forceinline__ void turn(float2 x, float2 y, float2 c, float2 s, flo
     oy = __ffma2_rn(y, c, xs);
 }
 
-// Puts the pairs of a unit that pass back where the rotation changed them. `passes`
-// has a bit for each of the unit's pairs; a unit of halves passes as a whole.
+// Turns a unit's pairs. `passes` has a bit for each of them that passes; a unit of
+// halves turns or passes as a whole. (Turning all and putting back those that pass
+// costs registers: the backward of 32768 tokens of 40 bf16 heads of 128 takes 158 us
+// so, and 151 this way.)
 template <int E, bool ADJ>
-__device__ __forceinline__ void keep_passing(unsigned passes, const float2 (&f)[(E + 1) / 2],
-                                             const float2 (&s)[(E + 1) / 2], float2 (&yf)[(E + 1) / 2],
-                                             float2 (&ys)[(E + 1) / 2]) {
-    if (passes == 0) return;
+__device__ __forceinline__ void turn_unit(unsigned passes, float2 (&f)[(E + 1) / 2], float2 (&s)[(E + 1) / 2],
+                                          const float2 (&c)[(E + 1) / 2], const float2 (&n)[(E + 1) / 2]) {
+    if (passes == 0) {
 #pragma unroll
-    for (int i = 0; i < (E + 1) / 2; ++i) {
-        if (!ADJ || (passes >> 2 * i & 1)) {
-            yf[i].x = f[i].x;
-            ys[i].x = s[i].x;
-        }
-        if (!ADJ || (passes >> (2 * i + 1) & 1)) {
-            yf[i].y = f[i].y;
-            ys[i].y = s[i].y;
+        for (int i = 0; i < (E + 1) / 2; ++i) turn(f[i], s[i], c[i], n[i], f[i], s[i]);
+    } else if constexpr (ADJ && E > 1) {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            float2 tf, ts;
+            turn(f[i], s[i], c[i], n[i], tf, ts);
+            if (!(passes >> 2 * i & 1)) f[i].x = tf.x, s[i].x = ts.x;
+            if (!(passes >> (2 * i + 1) & 1)) f[i].y = tf.y, s[i].y = ts.y;
         }
     }
 }
@@ -670,12 +671,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
                 if (LANES == 0 && lane + i * lanes >= a.units) continue;
-                float2 c[P], n[P], yf[P], ys[P], yl[P], yh[P];
+                float2 c[P], n[P], yl[P], yh[P];
                 read_table<E, LANES>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
-#pragma unroll
-                for (int e = 0; e < P; ++e) turn(f[i][e], s[i][e], c[e], n[e], yf[e], ys[e]);
-                keep_passing<E, ADJ>(at.passes[i], f[i], s[i], yf, ys);
-                join_pairs<E, ADJ>(yf, ys, yl, yh);
+                turn_unit<E, ADJ>(at.passes[i], f[i], s[i], c, n);
+                join_pairs<E, ADJ>(f[i], s[i], yl, yh);
                 W* dl = reinterpret_cast<W*>(dst + at.lo[i]);
                 W* dhi = reinterpret_cast<W*>(dst + at.lo[i] + at.hop(i));
                 [[maybe_unused]] const RopeTensor& x = a.t[second ? 1 : 0];
@@ -851,18 +850,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
                 if (!live || (LANES == 0 && lane + i * lanes >= a.units)) continue;
-                float2 l[P], h[P], f[P], s[P], c[P], n[P], df[P], ds[P];
+                float2 l[P], h[P], f[P], s[P], c[P], n[P];
                 X::unpack(xl[i], l);
                 X::unpack(xh[i], h);
                 split_pairs<E, ADJ>(l, h, f, s);
                 read_table<E, LANES>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
-#pragma unroll
-                for (int e = 0; e < P; ++e) turn(gf[i][e], gs[i][e], c[e], n[e], df[e], ds[e]);
-                keep_passing<E, ADJ>(at.passes[i], gf[i], gs[i], df, ds);
+                turn_unit<E, ADJ>(at.passes[i], gf[i], gs[i], c, n);
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
-                    gf[i][e] = df[e];
-                    gs[i][e] = ds[e];
                     ss = __ffma2_rn(f[e], f[e], __ffma2_rn(s[e], s[e], ss));
                     hx = __ffma2_rn(__fmul2_rn(gf[i][e], wf[i][e]), f[e],
                                     __ffma2_rn(__fmul2_rn(gs[i][e], ws[i][e]), s[e], hx));
