@@ -1,0 +1,91 @@
+"""Values of the group norm that random inputs do not reach: the activations over
+their whole range.
+
+Bounds. With weights of zero z is the bias, exactly, so that y = act(b) and, for one
+position and dy = 1, db = act'(b) in fp32."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import image_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+pkg = pytest.importorskip("memory_bound_normalization_gb300")
+
+DEV = "cuda:0"
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    torch.cuda.set_device(0)
+    pkg.load_library(build_if_missing=True)
+    yield
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    yield
+    assert pkg.rmsnorm_get_last_device_error() == pkg.OK
+
+
+# ------------------------------------------------------------- activations
+# 4096 arguments by 16-byte vectors, and 4097 element by element; every exponent
+# from 2^-20 to the largest argument, both signs
+def arguments(n, largest):
+    g = torch.Generator().manual_seed(n)
+    a = torch.cat([torch.linspace(-largest, largest, n // 2),
+                   torch.exp2(torch.empty(n - n // 2).uniform_(-20, torch.tensor(largest).log2().item(), generator=g))])
+    a[n // 2::2] *= -1
+    return a.to(DEV)
+
+
+def value_and_slope(z, dtype, name, positions):
+    """y and act' of every argument, through the public calls."""
+    C = z.numel()
+    groups = 64 if C % 64 == 0 else 1
+    x = torch.randn(1, positions, C, device=DEV).to(dtype)
+    w = torch.zeros(C, device=DEV)
+    y, mean, rstd = pkg.group_norm_forward(x, groups, w, z, 1e-5, name)
+    dy = torch.zeros_like(x)
+    dy[:, -1] = 1  # one position's slope, so that db holds nothing else
+    _, dw, db = pkg.group_norm_backward(x, groups, w, z, dy, mean, rstd, name)
+    assert (y == y[:, :1]).all()
+    return y[0, 0], db
+
+
+def exact(z, name):
+    Z = z.double().cpu()
+    if name == "silu":
+        s, o = torch.sigmoid(Z), torch.sigmoid(-Z)
+        return Z, Z * s, s * (1 + Z * o), s, o
+    tail = torch.special.erfcx(Z.abs() / 2 ** 0.5) * torch.exp(-Z * Z / 2) / 2
+    phi = torch.where(Z < 0, tail, 1 - tail)
+    density = torch.exp(-Z * Z / 2) / (2 * torch.pi) ** 0.5
+    return Z, Z * phi, phi + Z * density, phi, density
+
+
+TINY = 2.0 ** -118  # results below may be flushed, or lose bits of a subnormal fp32 factor
+
+
+# 16 bits: an approximation is a sixteenth of half an f16 step (2^-16) where f16 has
+# normal values and 2^-13, a sixteenth of half a bf16 step, behind; then one rounding
+@pytest.mark.parametrize("C,positions", [(4096, 1), (4097, 2), (512, 30000)], ids=["vectors", "elements", "streamed"])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_activation_in_16_bits(name, dtype, C, positions):
+    z = arguments(C, 80.0 if name == "silu" else 12.5)
+    y, db = value_and_slope(z, dtype, name, positions)
+    Z, value, slope, s, o = exact(z, name)
+    near = torch.where(Z.abs() <= 4.5, 2.0 ** -16, 2.0 ** -13)
+    err = (y.double().cpu() - value).abs()
+    bound = near * value.abs() + ref.rounding(dtype, value) * 1.001 + TINY
+    assert (err <= bound).all(), f"value {float((err / bound).max()):.2f} of the bound at {float(Z[(err / bound).argmax()])}"
+    terms = s + (Z * s * o).abs() if name == "silu" else s + (Z * o).abs()
+    err = (db.double().cpu() - slope).abs()
+    bound = near * terms + TINY
+    assert (err <= bound).all(), f"slope {float((err / bound).max()):.2f} of the bound at {float(Z[(err / bound).argmax()])}"
