@@ -123,6 +123,12 @@ __device__ __forceinline__ float exp2_fast(float v) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+// v, or the bound (positive) with v's sign where |v| is larger.
+__device__ __forceinline__ float held_to(float v, float bound) {
+    float r;
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(bound));
+    return r;
+}
 __device__ __forceinline__ float2 exp2_pair(float2 v) {
     return make_float2(exp2_fast(v.x), exp2_fast(v.y));
 }
@@ -145,7 +151,10 @@ __device__ __forceinline__ float2 rcp_pair(float2 v) {
 // accuracy; here with y = |z|, half of (1 + sqrt 2 y) e^(y^2/2) erfc(y / sqrt 2) in
 // t = (y - 3) / (y + 3), of degree 9 by least squares at Chebyshev points up to
 // y = 20, behind which the bell is 0: off by 3.1e-7 of its value in fp32
-// arithmetic. One reciprocal serves both quotients.
+// arithmetic. One reciprocal serves both quotients. (The bell's argument is rounded
+// twice, which leaves some z^2 2^-24 of the tail; to put that back, as silu does,
+// makes a backward 12% slower, 166 -> 186 us of 6 samples of 7456 positions of 1024
+// channels, and a form by 1 + erf is off by far more there.)
 template <typename T>
 __device__ __forceinline__ void normal_pair(float2 z, float2& phi, float2& bell) {
     float2 x = make_float2(fabsf(z.x), fabsf(z.y));
@@ -179,21 +188,35 @@ __device__ __forceinline__ void normal_pair(float2 z, float2& phi, float2& bell)
     phi = make_float2(z.x < 0.f ? q.x : 1.f - q.x, z.y < 0.f ? q.y : 1.f - q.y);
 }
 
-// Both take the hardware's exponential and reciprocal: the accurate functions
-// cost the backward's first pass 18 instructions an element in 16 bits, where
-// DRAM leaves room for 22. e^-z is off by 2^-22 and |z| 2^-24 of its value, the
-// reciprocal by 2^-23 of its own, so silu and its slope by no more than some
-// 2^-22 |z| and 2^-22 (1 + |z|): half a step of a 16-bit output is 2^-12, and an
-// fp32 output is at most a few steps of |z| off. (fp32, 6 samples of 7456
-// positions of 1024 channels backward: silu 171 us with the accurate functions and
-// 135 with these, gelu 306 and 168, no activation 134.)
+// 1 + e^-z, to infinity, by the hardware's power 2^t, which is off by 2^-22 of its
+// value and by what rounding t = -z log2(e) leaves out, some |z| 2^-24 of it. In 32
+// bits the latter is put back: e^-z = 2^t e^-r, r = z + t ln 2, which is small where
+// z is held to what the power's range takes. Silu by it and the hardware's reciprocal
+// is within 6 2^-24 of its value for z > -20 (0.7 on average; 3.5 and 0.6 by expf and
+// a division), 8 behind, at the cost of the power alone but for resident slabs (8
+// samples of 1024 positions of 640 fp32 channels backward 23.6 -> 25.0 us). By expf
+// and a division 6 samples of 7456 positions of 1024 fp32 channels backward take 171
+// us, by these 134, as without an activation. 16-bit outputs, whose half step is
+// 2^-12 of a value, need no more than 2^t: the accurate functions cost the
+// backward's first pass 18 instructions an element, where DRAM leaves room for 22.
+template <typename T>
+__device__ __forceinline__ float2 one_plus_exp(float2 z) {
+    if constexpr (sizeof(T) == 2) {
+        return __fadd2_rn(exp2_pair(__fmul2_rn(z, f2_splat(-1.44269504f))), f2_splat(1.f));
+    } else {
+        const float2 c = make_float2(held_to(z.x, 128.f), held_to(z.y, 128.f));
+        const float2 t = __fmul2_rn(c, f2_splat(-1.44269504f));
+        const float2 r = __ffma2_rn(t, f2_splat(0.69314718f), c);
+        return __ffma2_rn(exp2_pair(t), __ffma2_rn(r, f2_splat(-1.f), f2_splat(1.f)), f2_splat(1.f));
+    }
+}
+
 template <typename T, int ACT>
 __device__ __forceinline__ float2 act_pair(float2 z) {
     if constexpr (ACT == RMSNORM_ACT_NONE) {
         return z;
     } else if constexpr (ACT == RMSNORM_ACT_SILU) {
-        const float2 e = exp2_pair(__fmul2_rn(z, f2_splat(-1.44269504f)));
-        return __fmul2_rn(z, rcp_pair(__fadd2_rn(e, f2_splat(1.f))));
+        return __fmul2_rn(z, rcp_pair(one_plus_exp<T>(z)));
     } else {
         float2 phi, bell;
         normal_pair<T>(z, phi, bell);
@@ -204,8 +227,7 @@ template <typename T, int ACT>
 __device__ __forceinline__ float2 slope_pair(float2 z) {
     if constexpr (ACT == RMSNORM_ACT_SILU) {
         // s (1 + z (1 - s)) = s + (z s) (1 - s)
-        const float2 e = exp2_pair(__fmul2_rn(z, f2_splat(-1.44269504f)));
-        const float2 s = rcp_pair(__fadd2_rn(e, f2_splat(1.f)));
+        const float2 s = rcp_pair(one_plus_exp<T>(z));
         const float2 r = __ffma2_rn(s, f2_splat(-1.f), f2_splat(1.f));
         return __fmul2_rn(s, __ffma2_rn(z, r, f2_splat(1.f)));
     } else {

@@ -1,8 +1,8 @@
 """Values of the group norm that random inputs do not reach: the activations over
 their whole range.
 
-Bounds. With weights of zero z is the bias, exactly, so that y = act(b) and, for one
-position and dy = 1, db = act'(b) in fp32."""
+Bounds. F is 2^-24 (an fp32 rounding). With weights of zero z is the bias, exactly,
+so that y = act(b) and, for one position and dy = 1, db = act'(b) in fp32."""
 from __future__ import annotations
 
 import pytest
@@ -16,6 +16,7 @@ pkg = pytest.importorskip("memory_bound_normalization_gb300")
 
 DEV = "cuda:0"
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+F = 2.0 ** -24
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -70,6 +71,30 @@ def exact(z, name):
 
 
 TINY = 2.0 ** -118  # results below may be flushed, or lose bits of a subnormal fp32 factor
+
+
+# fp32: with the exponential and the reciprocal good to 2^-22 of their values (4 F)
+# and some ten roundings of products and sums behind them, 16 F of a value. A slope
+# is a sum of two terms that cancel near its zero: 16 F of either. Silu's takes
+# 1 - s for the other side, in either path: s = 1 / (1 + e^-z) is F (the sum) and 2 F
+# (the reciprocal) of s off, the difference F more, and z s times that is 4 F |z| s.
+# GELU has its polynomial (6 F) and sum of ten steps: 32 F. Its e^(-z^2/2) is a power
+# of a product that is rounded twice, F each, of a constant that is 0.2 F off: the
+# exponent, z^2/2, is 2.2 F of itself off and the power 1.1 z^2 F of itself.
+@pytest.mark.parametrize("C,positions", [(4096, 1), (4097, 2), (512, 30000)], ids=["vectors", "elements", "streamed"])
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_activation_in_32_bits(name, C, positions):
+    z = arguments(C, 80.0 if name == "silu" else 12.5)
+    y, db = value_and_slope(z, F32, name, positions)
+    Z, value, slope, s, o = exact(z, name)
+    k = 16 if name == "silu" else 32 + 1.25 * Z * Z
+    err = (y.double().cpu() - value).abs()
+    bound = k * F * value.abs() + TINY
+    assert (err <= bound).all(), f"value {float((err / bound).max()):.2f} of the bound at {float(Z[(err / bound).argmax()])}"
+    terms = s + (Z * s * o).abs() if name == "silu" else s + (Z * o).abs()
+    err = (db.double().cpu() - slope).abs()
+    bound = k * F * terms + (4 * F * Z.abs() * s if name == "silu" else 0) + TINY
+    assert (err <= bound).all(), f"slope {float((err / bound).max()):.2f} of the bound at {float(Z[(err / bound).argmax()])}"
 
 
 # 16 bits: an approximation is a sixteenth of half an f16 step (2^-16) where f16 has
