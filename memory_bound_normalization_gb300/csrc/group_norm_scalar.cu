@@ -1,14 +1,19 @@
 // Group norm with an activation, channels last, for any channel count and
 // alignment: two kernels and, in the backward, a column sum.
 //   statistics   chunks of a (sample, group) slab: each block takes the mean
-//                of its chunk and then the squares about that mean (a second
-//                read that L1 and L2 serve), so a mean far from zero costs no
-//                digits; chunks are combined by sum n_k m_k and
+//                of its chunk and then the deviations from it and their squares
+//                (a second read that L1 and L2 serve); the deviations' mean puts
+//                right what rounding left out of the first, so a mean far from
+//                zero costs no digits; chunks are combined by the distances of
+//                their means from the first one's and by
 //                sum M2_k + n_k (m_k - mean)^2
 //   apply        y = act(xhat w + b)
 //   backward     per-channel sums of dz and dz xhat over chunks of positions,
 //                then dx = rstd (dz w - A - xhat B); the channel sums of all
 //                chunks add up to db and dw
+// A thread adds in runs of 64, and the runs: a chain of all its values would lose
+// digits where their number is large and they have one sign (12 million values that
+// differ little: the mean was 115 roundings off).
 // The path of shapes that 16-byte vectors do not fit: element by element.
 #include <algorithm>
 
@@ -31,6 +36,22 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) s += scratch[i];
     return s;
+}
+
+// term(i, sums) for i = first, first + step, ... below n: adds to N sums, which are
+// those of runs of kRun terms; `total` is the sum of the runs.
+constexpr int kRun = 64;
+template <int N, typename Term>
+__device__ __forceinline__ void sum_in_runs(float (&total)[N], int64_t first, int64_t n, int step, Term term) {
+#pragma unroll
+    for (float& t : total) t = 0.f;
+    for (int64_t i = first; i < n;) {
+        const int64_t end = min(n, i + static_cast<int64_t>(kRun) * step);
+        float run[N] = {};
+        for (; i < end; i += step) term(i, run);
+#pragma unroll
+        for (int k = 0; k < N; ++k) total[k] += run[k];
+    }
 }
 
 template <typename T>
@@ -63,16 +84,18 @@ __global__ void __launch_bounds__(kThreads) gn_scalar_stats_kernel(const __grid_
     const T* x = static_cast<const T*>(a.x) + (c.b * a.S + c.s0) * a.C + c.g * D;
     const int64_t n = (c.s1 - c.s0) * D;
     wait_for_prerequisite_grid();
-    float s = 0.f;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) s += to_f32(x[i / D * a.C + i % D]);
-    const float mean = n > 0 ? block_sum(s, scratch) / static_cast<float>(n) : 0.f;
-    float m2 = 0.f;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const float d = to_f32(x[i / D * a.C + i % D]) - mean;
-        m2 = fmaf(d, d, m2);
-    }
-    m2 = block_sum(m2, scratch);
-    if (threadIdx.x == 0) parts[blockIdx.x] = make_float2(mean, m2);
+    auto value = [&](int64_t i) { return to_f32(x[i / D * a.C + i % D]); };
+    const float count = fmaxf(static_cast<float>(n), 1.f);
+    float s[1], t[2];
+    sum_in_runs(s, threadIdx.x, n, kThreads, [&](int64_t i, float (&r)[1]) { r[0] += value(i); });
+    const float near = block_sum(s[0], scratch) / count;
+    sum_in_runs(t, threadIdx.x, n, kThreads, [&](int64_t i, float (&r)[2]) {
+        const float d = value(i) - near;
+        r[0] += d;
+        r[1] = fmaf(d, d, r[1]);
+    });
+    const float off = block_sum(t[0], scratch), squares = block_sum(t[1], scratch), shift = off / count;
+    if (threadIdx.x == 0) parts[blockIdx.x] = make_float2(near + shift, fmaxf(fmaf(-off, shift, squares), 0.f));
     allow_dependent_launch();
 }
 
@@ -83,11 +106,12 @@ __global__ void __launch_bounds__(kThreads) gn_scalar_fwd_kernel(const __grid_co
     const int D = a.C / a.G;
     wait_for_prerequisite_grid();  // the statistics are complete
     const float2* mine = parts + (c.b * a.G + c.g) * chunks;
+    const float first = mine[0].x;
     float sum = 0.f;
-    for (int k = 0; k < chunks; ++k)
-        sum = fmaf(mine[k].x, static_cast<float>((a.S * (k + 1) / chunks - a.S * k / chunks) * D), sum);
+    for (int k = 1; k < chunks; ++k)
+        sum = fmaf(mine[k].x - first, static_cast<float>((a.S * (k + 1) / chunks - a.S * k / chunks) * D), sum);
     const float count = static_cast<float>(a.S * D);
-    const float mean = sum / count;
+    const float mean = first + sum / count;
     float m2 = 0.f;
     for (int k = 0; k < chunks; ++k) {
         const float d = mine[k].x - mean;
@@ -140,17 +164,18 @@ __global__ void __launch_bounds__(kThreads) gn_scalar_sums_kernel(const __grid_c
     const int64_t b = row / chunks, k = row % chunks;
     const int64_t s1 = a.S * (k + 1) / chunks;
     wait_for_prerequisite_grid();
-    float p = 0.f, q = 0.f;
+    float t[2] = {};
     if (ch < a.C) {
         const int g = ch / (a.C / a.G);
         const float mean = a.mean[b * a.G + g], rstd = a.rstd[b * a.G + g];
-        for (int64_t s = a.S * k / chunks + ry; s < s1; s += 8) {
+        sum_in_runs(t, a.S * k / chunks + ry, s1, 8, [&](int64_t s, float (&r)[2]) {
             float xhat;
             const float dz = dz_at<T>(a, (b * a.S + s) * a.C + ch, ch, mean, rstd, xhat);
-            p += dz;
-            q = fmaf(dz, xhat, q);
-        }
+            r[0] += dz;
+            r[1] = fmaf(dz, xhat, r[1]);
+        });
     }
+    float p = t[0], q = t[1];
     sp[ry][cx] = p;
     sq[ry][cx] = q;
     __syncthreads();
@@ -175,16 +200,17 @@ __global__ void __launch_bounds__(kThreads) gn_scalar_bwd_kernel(const __grid_co
     const T* x = static_cast<const T*>(a.x);
     T* dx = static_cast<T*>(a.out);
     wait_for_prerequisite_grid();  // the channel sums are complete
-    float p = 0.f, q = 0.f;
-    for (unsigned i = threadIdx.x; i < static_cast<unsigned>(chunks * D); i = next_item(i)) {
-        const int ch = c.g * D + static_cast<int>(i % D);
+    float t[2];
+    sum_in_runs(t, threadIdx.x, static_cast<int64_t>(chunks) * D, kThreads, [&](int64_t i, float (&r)[2]) {
+        const unsigned at = static_cast<unsigned>(i);  // below 2^31
+        const int ch = c.g * D + static_cast<int>(at % D);
         const float w = a.w != nullptr ? weight_at(a.w, ch, a.w_f32, x) : 1.f;
-        const float* r = parts + (c.b * chunks + i / D) * 2 * a.C + ch;
-        p = fmaf(w, r[0], p);
-        q = fmaf(w, r[a.C], q);
-    }
+        const float* row = parts + (c.b * chunks + at / D) * 2 * a.C + ch;
+        r[0] = fmaf(w, row[0], r[0]);
+        r[1] = fmaf(w, row[a.C], r[1]);
+    });
     const float inv = 1.f / static_cast<float>(a.S * D);
-    const float A = block_sum(p, scratch) * inv, Bq = block_sum(q, scratch) * inv;
+    const float A = block_sum(t[0], scratch) * inv, Bq = block_sum(t[1], scratch) * inv;
     const float mean = a.mean[c.b * a.G + c.g], rstd = a.rstd[c.b * a.G + c.g];
     const int64_t base = (c.b * a.S + c.s0) * a.C + c.g * D;
     const int64_t n = (c.s1 - c.s0) * D;

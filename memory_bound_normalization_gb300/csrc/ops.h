@@ -97,8 +97,8 @@ struct PairSum {
     int64_t stride;  // twice the channels of a group norm: past 31 bits from 2^30 on
     int* status;
 };
-// A thread's next item (a row, an element) in a block of 256: unsigned, since it
-// passes 2^31 - 1 behind the last of as many.
+// A thread's next item (a row) in a block of 256: unsigned, since it passes
+// 2^31 - 1 behind the last of as many.
 constexpr int kItemThreads = 256;
 __host__ __device__ inline unsigned next_item(unsigned i) { return i + kItemThreads; }
 cudaError_t pair_sum_launch(const PairSum& a, cudaStream_t s);

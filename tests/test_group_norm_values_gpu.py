@@ -1,5 +1,5 @@
 """Values of the group norm that random inputs do not reach: the activations over
-their whole range.
+their whole range, many positions that differ little.
 
 Bounds. F is 2^-24 (an fp32 rounding). With weights of zero z is the bias, exactly,
 so that y = act(b) and, for one position and dy = 1, db = act'(b) in fp32."""
@@ -114,3 +114,52 @@ def test_activation_in_16_bits(name, dtype, C, positions):
     err = (db.double().cpu() - slope).abs()
     bound = near * terms + TINY
     assert (err <= bound).all(), f"slope {float((err / bound).max()):.2f} of the bound at {float(Z[(err / bound).argmax()])}"
+
+
+# ------------------------------------------------------------- statistics
+# Element by element (3 channels), millions of positions that differ little: the mean
+# is a few roundings off (4 F of it), and what its error leaves in the deviations is
+# rstd times that; their own sums are K F of the mean deviation: n values over 64 blocks
+# of 256 threads, in runs of 64, which are added up, then 13 in a block, 64 over the
+# blocks and a few: K = 149 + n / 16384 / 64.
+@pytest.mark.parametrize("level", [1000.0 / 3, 1.0 / 3])
+@pytest.mark.parametrize("S", [1 << 22, 1000003])
+def test_mean_of_many_positions_element_by_element(S, level):
+    g = torch.Generator().manual_seed(1)
+    x = (level * (1 + 2.0 ** -20 * torch.randn(1, S, 3, generator=g))).to(DEV)
+    y, mean, rstd = pkg.group_norm_forward(x, 1, None, None, 1e-12)
+    X = x.double()
+    m = X.mean()
+    d = X - m
+    var = (d * d).mean()
+    r = (var + 1e-12).rsqrt()
+    K = 149 + X.numel() / 16384 / 64
+    spread = d.abs().mean()
+    e_mean = 4 * F * m.abs() + K * F * spread
+    assert (mean.double() - m).abs() <= e_mean, float((mean.double() - m).abs() / (F * m.abs()))
+    # squares about a mean that is off by e: e^2 more, beside their own roundings
+    e_r = K * F + (e_mean * r) ** 2
+    assert (rstd.double() / r - 1).abs() <= e_r
+    err = (y.double() - d * r).abs()
+    assert (err <= r * e_mean + (e_r + 4 * F) * (d * r).abs()).all(), float((err / (r * e_mean)).max())
+
+
+def test_one_sided_gradients_element_by_element():
+    """Weight gradients over millions of positions whose terms have one sign: sums
+    in runs of 64, some 128 runs a thread, then 8, 64 blocks and the column sum's
+    trees: 256 roundings hold them."""
+    S = 1 << 22
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(1, S, 3, generator=g).abs().to(DEV)
+    dy = (1.0 / 3 + 2.0 ** -22 * torch.randn(1, S, 3, generator=g)).to(DEV)
+    w, b = torch.ones(3, device=DEV), torch.zeros(3, device=DEV)
+    mean, rstd = torch.zeros(1, 1, device=DEV), torch.ones(1, 1, device=DEV)
+    dx, dw, db = pkg.group_norm_backward(x, 1, w, b, dy, mean, rstd)
+    X, D = x.double(), dy.double()
+    for got, terms in ((db, D), (dw, D * X)):
+        want = terms.sum((0, 1))
+        assert ((got.double() - want).abs() <= 256 * F * terms.abs().sum((0, 1))).all(), \
+            float(((got.double() - want).abs() / want / F).max())
+    A, Bq = D.mean(), (D * X).mean()
+    e = 300 * F * (A.abs() + X * Bq.abs()) + 8 * F * (D.abs() + A + X * Bq)
+    assert ((dx.double() - (D - A - X * Bq)).abs() <= e).all()
