@@ -1,7 +1,8 @@
 // Column sums of dw partial rows for two outputs at once (the weight gradients
 // of queries and keys; dw and db of a group norm), in a fixed order: a block of
 // eight warps takes W neighbouring columns, thread t adds rows t, t + 256, ...
-// in ascending order, a butterfly adds a warp's lanes and thread 0 the warps.
+// in ascending order (in runs of 64, and the runs: a chain of a million samples' rows
+// was 645 roundings off), a butterfly adds a warp's lanes and thread 0 the warps.
 // The same bits on every run for given sizes. A few hundred rows of a few
 // hundred columns: the time is the launch and one trip to L2 (some 3 us of 304
 // rows of 128), so every row has a thread of its own where there are no more than
@@ -11,6 +12,8 @@
 
 namespace rmsn {
 namespace {
+
+constexpr unsigned kRun = 64;
 
 template <int W>
 struct Columns;
@@ -51,9 +54,14 @@ __global__ void __launch_bounds__(kItemThreads) pair_sum_kernel(const __grid_con
     if (out == nullptr) return;
     const float* src = a.part[which] + col;
     float s[W] = {};
+    for (unsigned p = threadIdx.x; p < rows;) {
+        const unsigned end = min(rows, p + kRun * kItemThreads);
+        float run[W] = {};
 #pragma unroll 4
-    for (unsigned p = threadIdx.x; p < rows; p = next_item(p))
-        Columns<W>::add(s, *reinterpret_cast<const V*>(src + p * a.stride));
+        for (; p < end; p = next_item(p)) Columns<W>::add(run, *reinterpret_cast<const V*>(src + p * a.stride));
+#pragma unroll
+        for (int i = 0; i < W; ++i) s[i] += run[i];
+    }
 #pragma unroll
     for (int i = 0; i < W; ++i) s[i] = group_allreduce<32>(s[i]);
     if (lane == 0) {

@@ -163,3 +163,19 @@ def test_one_sided_gradients_element_by_element():
     A, Bq = D.mean(), (D * X).mean()
     e = 300 * F * (A.abs() + X * Bq.abs()) + 8 * F * (D.abs() + A + X * Bq)
     assert ((dx.double() - (D - A - X * Bq)).abs() <= e).all()
+
+
+@pytest.mark.parametrize("C", [8, 3], ids=["vectors", "elements"])
+def test_one_sided_gradients_of_many_samples(C):
+    """A partial row a sample, a million of them: 4096 rows a thread of the column
+    sum in runs of 64, 13 in its trees: 256 roundings hold them."""
+    B = 1 << 20
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(B, 1, C, generator=g).abs().to(DEV)
+    dy = (0.4 + 2.0 ** -22 * torch.randn(B, 1, C, generator=g)).to(DEV)
+    w, b = torch.ones(C, device=DEV), torch.zeros(C, device=DEV)
+    mean, rstd = torch.zeros(B, 1, device=DEV), torch.ones(B, 1, device=DEV)
+    _, dw, db = pkg.group_norm_backward(x, 1, w, b, dy, mean, rstd)
+    for got, terms in ((db, dy.double()), (dw, dy.double() * x.double())):
+        want = terms.sum((0, 1))
+        assert ((got.double() - want).abs() <= 256 * F * want).all(), float(((got.double() - want).abs() / want / F).max())
