@@ -17,6 +17,7 @@
 
 #include <array>
 #include <cstdint>
+#include <limits>
 #include <optional>
 #include <string>
 
@@ -257,6 +258,10 @@ PyObject* group_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
         Run run(x, a[6]);
         const at::Tensor y = make(x.sizes(), x.scalar_type(), x);
         const at::Tensor mean = make({g.B, g.G}, at::kFloat, x), rstd = make({g.B, g.G}, at::kFloat, x);
+        if (g.S == 0) {  // means of nothing, which the library leaves unwritten
+            mean.fill_(std::numeric_limits<float>::quiet_NaN());
+            rstd.fill_(std::numeric_limits<float>::quiet_NaN());
+        }
         const size_t need = group_norm_need(g, 0, x.get_device());
         void* ws = run.workspace(need);
         const void *px = x.const_data_ptr(), *pw = data(w), *pb = data(b);

@@ -54,7 +54,8 @@ def _handle(stream):
 def group_norm_forward(x, num_groups: int, weight=None, bias=None, eps: float = 1e-5,
                        activation: str = "none", stream=None):
     """y, mean, rstd of act(group_norm(x) * weight + bias), x [B, ..., C]
-    contiguous with the channels last; mean and rstd fp32 [B, num_groups].
+    contiguous with the channels last; mean and rstd fp32 [B, num_groups] (NaN
+    where there are no positions).
     activation: "none", "silu" or "gelu" (z Phi(z), not a form by tanh). An NCHW tensor in
     channels_last memory format passes as x.permute(0, 2, 3, 1)."""
     return (_bound or _binding()).group_norm_forward(x, num_groups, weight, bias, eps, activation,

@@ -1,5 +1,5 @@
 """Values of the group norm that random inputs do not reach: the activations over
-their whole range, many positions that differ little.
+their whole range, many positions that differ little, none.
 
 Bounds. F is 2^-24 (an fp32 rounding). With weights of zero z is the bias, exactly,
 so that y = act(b) and, for one position and dy = 1, db = act'(b) in fp32."""
@@ -179,3 +179,14 @@ def test_one_sided_gradients_of_many_samples(C):
     for got, terms in ((db, dy.double()), (dw, dy.double() * x.double())):
         want = terms.sum((0, 1))
         assert ((got.double() - want).abs() <= 256 * F * want).all(), float(((got.double() - want).abs() / want / F).max())
+
+
+def test_statistics_of_no_positions():
+    """They are means of nothing: NaN, not what the memory held."""
+    for shape in ((3, 0, 16), (3, 4, 0, 16)):
+        x = torch.empty(shape, device=DEV)
+        junk = torch.full((64, 12), 5.0, device=DEV)
+        del junk
+        y, mean, rstd = pkg.group_norm_forward(x, 4)
+        assert y.shape == x.shape and mean.shape == rstd.shape == (3, 4)
+        assert mean.isnan().all() and rstd.isnan().all()
