@@ -47,17 +47,10 @@ struct Elems {
         T e[E];
         __device__ U() {}
     };
-    // coherent: the output may be the input's buffer
+    // coherent: the output may be the input's buffer (wider words are copied ahead)
     __device__ __forceinline__ static W load(const T* p) {
-        W v;
-        if constexpr (sizeof(W) == 16)
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-        else if constexpr (sizeof(W) == 8)
-            asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-        else
-            v = *reinterpret_cast<const W*>(p);
-        return v;
+        static_assert(sizeof(W) <= 4, "a single element");
+        return *reinterpret_cast<const W*>(p);
     }
     __device__ __forceinline__ static void unpack(const W& w, float2 (&f)[P]) {
         if constexpr (sizeof(W) == 16) {
