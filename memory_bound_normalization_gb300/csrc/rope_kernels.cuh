@@ -20,8 +20,8 @@
 // inf * 0).
 //
 // Angles: one turn is 2^64, so the product of an integer position and the
-// frequency in turns (held to 2^-96) wraps exactly where the circle does, to within
-// 2^-32 turns for any position; an fp32 product at position 2^20 would be off by 0.06 radians.
+// frequency in turns wraps exactly where the circle does, however far the
+// position; an fp32 product at position 2^20 would be off by 0.06 radians.
 #pragma once
 
 #include "common.cuh"
@@ -80,43 +80,27 @@ struct Elems {
     }
 };
 
-// inv_freq / 2 pi in units of 2^-96 turns, without whole turns: the 24-bit mantissa
-// times 2^130/2pi, shifted by the exponent. Off by at most two units for
-// |inv_freq| < 2^25.
-struct Turns {
-    uint64_t hi;  // 2^-64
-    uint32_t lo;
-};
-__device__ __forceinline__ Turns turns_per_position(float f) {
-    using u128 = unsigned __int128;
+// inv_freq / 2 pi in units of 2^-64 turns: the 24-bit mantissa times 2^66/2pi,
+// shifted by the exponent. Off by at most one unit for |inv_freq| < 2^25.
+__device__ __forceinline__ uint64_t turns_per_position(float f) {
     const uint32_t bits = __float_as_uint(f);
     const int e = max(1, static_cast<int>((bits >> 23) & 255));
     const uint32_t m = (bits & 0x7fffffu) | ((bits & 0x7f800000u) ? 0x800000u : 0u);
-    constexpr uint64_t kUpper = 0xA2F9836E4E441529ull, kLower = 0xFC2757D1F534DDC0ull;  // of 2^130/2pi
-    const u128 a = static_cast<u128>(kLower) * m, b = static_cast<u128>(kUpper) * m;
-    const u128 low = a + (b << 64);
-    const uint64_t top = static_cast<uint64_t>(b >> 64) + (low < a ? 1 : 0);
-    const int shift = 184 - e;  // of top:low to the right
-    u128 v;
-    if (shift >= 128) v = top >> min(63, shift - 128);
-    else if (shift > 0) v = (low >> shift) | (static_cast<u128>(top) << (128 - shift));
-    else v = shift > -96 ? low << -shift : 0;
-    if (bits >> 31) v = 0 - v;
-    return {static_cast<uint64_t>(v >> 32), static_cast<uint32_t>(v)};
+    constexpr uint64_t kTwo66OverTwoPi = 0xA2F9836E4E441529ull;
+    const uint64_t lo = kTwo66OverTwoPi * m, hi = __umul64hi(kTwo66OverTwoPi, m);
+    const int shift = 152 - e;  // of hi:lo to the right
+    uint64_t v;
+    if (shift >= 64) v = shift < 128 ? hi >> (shift - 64) : 0;
+    else if (shift > 0) v = (lo >> shift) | (hi << (64 - shift));
+    else v = shift > -64 ? lo << -shift : 0;
+    return (bits >> 31) ? 0ull - v : v;
 }
 
-// cos and sin of pos * turns, with 2^64 turns a circle. The lower bits of the
-// frequency weigh less than 2^-32 turns for a position of 32 bits and are left out
-// there; with them any position's angle is within 2^-32 turns. 16-bit outputs take
-// the fast functions (off by 2^-20, half a step of fp16 is 2^-12).
+// cos and sin of pos * turns, with 2^64 turns a circle. 16-bit outputs take the
+// fast functions (off by 2^-20, half a step of fp16 is 2^-12).
 template <typename T>
-__device__ __forceinline__ float2 cos_sin(int64_t pos, Turns turns) {
-    uint64_t angle = static_cast<uint64_t>(pos) * turns.hi;
-    if (pos != static_cast<int32_t>(pos)) {
-        const uint64_t lo = static_cast<uint64_t>(turns.lo) << 32;
-        angle += __umul64hi(static_cast<uint64_t>(pos), lo) - (pos < 0 ? lo : 0);
-    }
-    const int64_t at = static_cast<int64_t>(angle);
+__device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t turns) {
+    const int64_t at = static_cast<int64_t>(static_cast<uint64_t>(pos) * turns);
     float s, c;
     if constexpr (sizeof(T) == 2) {
         // the top 32 bits of the angle, in radians
@@ -355,7 +339,7 @@ __device__ __forceinline__ void store_info(const RopeArgs& a, TileInfo& info, in
 // A thread's pair: which one, and what turns it. Threads beyond a whole number
 // of tokens' pairs have none.
 struct PairOf {
-    Turns turns;
+    uint64_t turns;
     int pair, token, stride, axis;  // its first token of a tile, and the step
     bool has, turned, bad;
 };

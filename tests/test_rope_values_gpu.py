@@ -1,14 +1,10 @@
 """Values of the rotary calls that random inputs do not reach: infinities and NaN
-in the elements that pass, positions up to the ends of 64 bits."""
+in the elements that pass."""
 from __future__ import annotations
 
-from fractions import Fraction
-
-import numpy as np
 import pytest
 import torch
 
-import image_ref as ref
 import test_rope_gpu as rp
 
 pytestmark = pytest.mark.gpu
@@ -54,41 +50,3 @@ def test_infinities_in_elements_that_pass(where, D, rot, dtype, adjacent, norm):
         t[1, 1, 0, rot + (D - rot) // 2] = nan
         t[1, 7, 1, rot + 1] = inf
     rp.verify(a, dq, dk, adjacent=adjacent)
-
-
-# 80 digits of pi
-PI = Fraction(31415926535897932384626433832795028841971693993751058209749445923078164062862089, 10 ** 79)
-
-
-def exact_angles(positions, freq, axis):
-    """cos and sin of the exact product, reduced in rational arithmetic."""
-    theta = np.empty((positions.shape[1], len(axis)))
-    for p, a in enumerate(axis):
-        turns = Fraction(float(freq[p])) / (2 * PI)
-        for t in range(positions.shape[1]):
-            at = int(positions[a, t]) * turns
-            at -= round(at)
-            theta[t, p] = float(at * 2 * PI)
-    theta = torch.from_numpy(theta).unsqueeze(-2)
-    return torch.cos(theta), torch.sin(theta)
-
-
-@pytest.mark.parametrize("dtype", [F32, F16], ids=["f32", "f16"])
-@pytest.mark.parametrize("D", [64, 100])
-@pytest.mark.parametrize("theta", [10000.0, 0.0001])
-def test_positions_of_64_bits(dtype, D, theta):
-    """The product with an int64 position keeps its digits to the ends of the type."""
-    n, half = 20, D // 2
-    g = torch.Generator().manual_seed(4)
-    a, dq, dk = rp.make((n,), 2, 1, D, (half - 5, 5), dtype, dtype)
-    pos = torch.tensor([0, 1, -1, (1 << 31) - 1, -(1 << 31), (1 << 32) + 1, 1 << 40, -(1 << 40) - 1, (1 << 44) + 3,
-                        (1 << 48) - 1, (1 << 53) + 1, -(1 << 53) - 1, (1 << 58) + 12345, (1 << 60) - 1, (1 << 62) + 1,
-                        -(1 << 62) - 1, (1 << 63) - 1, -(1 << 63), -(1 << 63) + 1, 0x123456789abcdef])
-    a["positions"] = torch.stack([pos, pos[torch.randperm(n, generator=g)]]).to(DEV)
-    a["inv_freq"] = (theta ** (-torch.arange(half, dtype=torch.float64) / half)).float().to(DEV)
-    qo, ko = pkg.qk_rope_forward(**a)
-    gq, gk, gwq, gwk = pkg.qk_rope_backward(**a, dq_out=dq, dk_out=dk)
-    cos, sin = exact_angles(a["positions"].cpu(), a["inv_freq"].cpu(), ref.axis_of_pairs(a["sections"], False))
-    for x, w, y, dy, dx, dw, what in ((a["q"], a["wq"], qo, dq, gq, gwq, "q"), (a["k"], a["wk"], ko, dk, gk, gwk, "k")):
-        ref.check_rope(x, w, cos, sin, D, False, 1e-6, y, what)
-        ref.check_rope_grads(x, w, cos, sin, D, False, 1e-6, dy, dx, dw, what)
