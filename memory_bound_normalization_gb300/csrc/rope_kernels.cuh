@@ -417,24 +417,20 @@ __device__ __forceinline__ void turn(float2 x, float2 y, float2 c, float2 s, flo
     oy = __ffma2_rn(y, c, xs);
 }
 
-// Turns a unit's pairs. `passes` has a bit for each of them that passes; a unit of
-// halves turns or passes as a whole. (Turning all and putting back those that pass
-// costs registers: the backward of 32768 tokens of 40 bf16 heads of 128 takes 158 us
-// so, and 151 this way.)
+// Turns a unit's pairs; in a head that is turned in part (`some`) but those that pass:
+// `passes` has a bit for each of them where pairs are neighbours, and says it of the
+// whole unit of halves.
 template <int E, bool ADJ>
-__device__ __forceinline__ void turn_unit(unsigned passes, float2 (&f)[(E + 1) / 2], float2 (&s)[(E + 1) / 2],
-                                          const float2 (&c)[(E + 1) / 2], const float2 (&n)[(E + 1) / 2]) {
-    if (passes == 0) {
+__device__ __forceinline__ void turn_unit(bool some, unsigned passes, float2 (&f)[(E + 1) / 2],
+                                          float2 (&s)[(E + 1) / 2], const float2 (&c)[(E + 1) / 2],
+                                          const float2 (&n)[(E + 1) / 2]) {
+    auto stays = [&](int e) { return some && (ADJ && E > 1 ? (passes >> e & 1) != 0 : passes != 0); };
 #pragma unroll
-        for (int i = 0; i < (E + 1) / 2; ++i) turn(f[i], s[i], c[i], n[i], f[i], s[i]);
-    } else if constexpr (ADJ && E > 1) {
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            float2 tf, ts;
-            turn(f[i], s[i], c[i], n[i], tf, ts);
-            if (!(passes >> 2 * i & 1)) f[i].x = tf.x, s[i].x = ts.x;
-            if (!(passes >> (2 * i + 1) & 1)) f[i].y = tf.y, s[i].y = ts.y;
-        }
+    for (int i = 0; i < (E + 1) / 2; ++i) {
+        float2 tf, ts;
+        turn(f[i], s[i], c[i], n[i], tf, ts);
+        if (!stays(2 * i)) f[i].x = tf.x, s[i].x = ts.x;
+        if (!stays(2 * i + 1)) f[i].y = tf.y, s[i].y = ts.y;
     }
 }
 
@@ -463,10 +459,20 @@ struct Pieces {
             unit_offsets<E, ADJ>(a, lane + i * lanes, l, h);
             lo[i] = l * static_cast<int>(sizeof(T));
             gap[i] = (h - l) * static_cast<int>(sizeof(T));
-            passes[i] = 0;
+        }
+    }
+    // called once the first copies are under way
+    __device__ __forceinline__ void find_passing(const RopeArgs& a, int lane, int lanes) {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                passes[i] |= pair_at<E, ADJ>(a.units, lane + i * lanes, e) >= a.rot / 2 ? 1u << e : 0u;
+        for (int i = 0; i < NU; ++i) {
+            passes[i] = 0;
+            if constexpr (ADJ && E > 1) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    passes[i] |= pair_at<E, ADJ>(a.units, lane + i * lanes, e) >= a.rot / 2 ? 1u << e : 0u;
+            } else {
+                passes[i] = (lane + i * lanes) * E >= a.rot / 2;
+            }
         }
     }
     __device__ __forceinline__ int hop(int i) const {
@@ -599,6 +605,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
     };
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) fetch(ring_first + i * kRow);
+    at.find_passing(a, lane, lanes);
     fill_angles<T, E, ADJ>(a, pair, tabs, info[0], range.count(0));
     int buf = 0, slot = 0, fill = AHEAD;
 #pragma unroll 1
@@ -664,18 +671,29 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_fwd_kernel(con
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
                 if (LANES == 0 && lane + i * lanes >= a.units) continue;
-                float2 c[P], n[P], yl[P], yh[P];
+                auto put = [&] {
+                    float2 yl[P], yh[P];
+                    join_pairs<E, ADJ>(f[i], s[i], yl, yh);
+                    W* dl = reinterpret_cast<W*>(dst + at.lo[i]);
+                    W* dhi = reinterpret_cast<W*>(dst + at.lo[i] + at.hop(i));
+                    [[maybe_unused]] const RopeTensor& x = a.t[second ? 1 : 0];
+                    if (RMSN_OK(span_in(dl, sizeof(W), x.out, extent_bytes(a, x, x.os, sizeof(T))) &&
+                                    span_in(dhi, sizeof(W), x.out, extent_bytes(a, x, x.os, sizeof(T))),
+                                a.status)) {
+                        *dl = X::pack(yl);
+                        *dhi = X::pack(yh);
+                    }
+                };
+                float2 c[P], n[P];
                 read_table<E, LANES>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
-                turn_unit<E, ADJ>(at.passes[i], f[i], s[i], c, n);
-                join_pairs<E, ADJ>(f[i], s[i], yl, yh);
-                W* dl = reinterpret_cast<W*>(dst + at.lo[i]);
-                W* dhi = reinterpret_cast<W*>(dst + at.lo[i] + at.hop(i));
-                [[maybe_unused]] const RopeTensor& x = a.t[second ? 1 : 0];
-                if (RMSN_OK(span_in(dl, sizeof(W), x.out, extent_bytes(a, x, x.os, sizeof(T))) &&
-                                span_in(dhi, sizeof(W), x.out, extent_bytes(a, x, x.os, sizeof(T))),
-                            a.status)) {
-                    *dl = X::pack(yl);
-                    *dhi = X::pack(yh);
+                // either kind of head down to its stores: with them behind the branch,
+                // arithmetic and stores do not overlap
+                if (a.rot == D) {
+                    turn_unit<E, ADJ>(false, 0, f[i], s[i], c, n);
+                    put();
+                } else {
+                    turn_unit<E, ADJ>(true, at.passes[i], f[i], s[i], c, n);
+                    put();
                 }
             }
         }
@@ -798,6 +816,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     };
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) fetch(ring_first + i * kRow);
+    at.find_passing(a, lane, lanes);
     // fill_weights is complete: this lane's weights, in registers
     float2 wf[NU][P], ws[NU][P];
 #pragma unroll
@@ -848,7 +867,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
                 X::unpack(xh[i], h);
                 split_pairs<E, ADJ>(l, h, f, s);
                 read_table<E, LANES>(tab + cur.t * D, a.units, lane + i * lanes, c, n);
-                turn_unit<E, ADJ>(at.passes[i], gf[i], gs[i], c, n);
+                if constexpr (ADJ && E > 1) {
+                    if (a.rot == D) turn_unit<E, ADJ>(false, 0, gf[i], gs[i], c, n);
+                    else turn_unit<E, ADJ>(true, at.passes[i], gf[i], gs[i], c, n);
+                } else if (at.passes[i] == 0) {
+                    // by lane, unlike the forward: 32768 tokens of 40 bf16 heads of 128
+                    // take 152 us so and 154 by the kind of head
+                    turn_unit<E, ADJ>(false, 0, gf[i], gs[i], c, n);
+                }
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
                     ss = __ffma2_rn(f[e], f[e], __ffma2_rn(s[e], s[e], ss));
