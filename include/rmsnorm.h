@@ -240,9 +240,11 @@ int rmsnorm_bwd_naive(const void *x, const void *w, const void *dy,
  * sections[i] pairs belong to axis i (their sum is rotary_dim / 2): in
  * blocks, axis 0 first, or with `interleaved` dealt in turn to the axes that
  * have pairs left (0, 1, 2, 0, 1, 2, ...). inv_freq[p] is per pair, in the
- * order of the pairs. The angle is the exact product taken modulo one turn,
- * so far positions keep their digits (frequencies below 2^25; an infinite or
- * NaN frequency gives NaN). n is not rounded between the norm and the
+ * order of the pairs. The angle is the product taken modulo one turn, of the
+ * position and the frequency in turns held to 2^-64: off by |position| 2^-63
+ * turns at most, so that positions keep their digits up to some 2^40 (2^-10
+ * turns at 2^53; frequencies below 2^25; an infinite or NaN frequency gives
+ * NaN). n is not rounded between the norm and the
  * rotation: each output is rounded once.
  */
 #define RMSNORM_ROPE_MAX_AXES 4

@@ -20,8 +20,8 @@
 // inf * 0).
 //
 // Angles: one turn is 2^64, so the product of an integer position and the
-// frequency in turns wraps exactly where the circle does, however far the
-// position; an fp32 product at position 2^20 would be off by 0.06 radians.
+// frequency in turns wraps exactly where the circle does, off by what the
+// frequency's last place makes of it, |position| 2^-63 turns; an fp32 product at position 2^20 would be off by 0.06 radians.
 #pragma once
 
 #include "common.cuh"
@@ -80,14 +80,18 @@ struct Elems {
     }
 };
 
-// inv_freq / 2 pi in units of 2^-64 turns: the 24-bit mantissa times 2^66/2pi,
-// shifted by the exponent. Off by at most one unit for |inv_freq| < 2^25.
+// inv_freq / 2 pi in units of 2^-64 turns: the 24-bit mantissa times 2^66/2pi (to 96
+// bits: with 64 a frequency of 10^4 was off by 2^12 units), shifted by the exponent.
+// Off by less than two units for |inv_freq| < 2^25.
 __device__ __forceinline__ uint64_t turns_per_position(float f) {
     const uint32_t bits = __float_as_uint(f);
     const int e = max(1, static_cast<int>((bits >> 23) & 255));
     const uint32_t m = (bits & 0x7fffffu) | ((bits & 0x7f800000u) ? 0x800000u : 0u);
     constexpr uint64_t kTwo66OverTwoPi = 0xA2F9836E4E441529ull;
-    const uint64_t lo = kTwo66OverTwoPi * m, hi = __umul64hi(kTwo66OverTwoPi, m);
+    constexpr uint32_t kNext = 0xFC2757D1u;  // its next 32 bits
+    const uint64_t more = static_cast<uint64_t>(kNext) * m >> 32;
+    const uint64_t lo = kTwo66OverTwoPi * m + more;
+    const uint64_t hi = __umul64hi(kTwo66OverTwoPi, m) + (lo < more ? 1 : 0);
     const int shift = 152 - e;  // of hi:lo to the right
     uint64_t v;
     if (shift >= 64) v = shift < 128 ? hi >> (shift - 64) : 0;
