@@ -140,12 +140,14 @@ __device__ __forceinline__ float2 rcp_pair(float2 v) {
 // 16-bit outputs: the form of Hastings, Approximations for Digital Computers
 // (1955): with y = |z|, t = 1 / (1 + p y),
 //   Phi(-y) = (a1 t + ... + a5 t^5) e^(-y^2/2),
-// p and a1..a5 fitted to the relative error over y up to 13 (least squares,
-// reweighted until the largest errors agree; nine times looser past y = 4.7): off
-// by 1.4e-5 of the value up to y = 4.5, where normal f16 values end (half a step is
-// 2.4e-4), and 1.1e-4 behind (half a bf16 step is 2e-3). (A fit to the absolute
-// error, as that of erf, is steps off in the tail; a term more leaves a third of this
-// and makes a backward 3% slower.)
+// fitted over y up to 13 (least squares, reweighted until the largest errors agree).
+// What is rounded to 16 bits takes p and five terms for the relative error, nine times
+// looser past y = 4.7: off by 1.4e-5 of the value up to y = 4.5, where normal f16
+// values end (half a step is 2.4e-4), and 1.1e-4 behind (half a bf16 step is 2e-3).
+// What is summed (SUMMED) in 32 bits takes p and six terms for the absolute error, as
+// long as the relative one stays below 5e-5: 2e-7 in fp32 arithmetic. (The sums with
+// five terms for the relative error were 1e-5 off; a fit to the absolute error alone,
+// as that of erf, is steps of the output off in the tail.)
 // fp32 outputs: the form of Shepherd and Laframboise, Mathematics of Computation
 // 36 (1981): (1 + 2 x) e^(x^2) erfc(x) is a polynomial in (x - k) / (x + k) to any
 // accuracy; here with y = |z|, half of (1 + sqrt 2 y) e^(y^2/2) erfc(y / sqrt 2) in
@@ -155,7 +157,7 @@ __device__ __forceinline__ float2 rcp_pair(float2 v) {
 // twice, which leaves some z^2 2^-24 of the tail; to put that back, as silu does,
 // makes a backward 12% slower, 166 -> 186 us of 6 samples of 7456 positions of 1024
 // channels, and a form by 1 + erf is off by far more there.)
-template <typename T>
+template <typename T, bool SUMMED>
 __device__ __forceinline__ void normal_pair(float2 z, float2& phi, float2& bell) {
     float2 x = make_float2(fabsf(z.x), fabsf(z.y));
     float2 q;
@@ -176,13 +178,21 @@ __device__ __forceinline__ void normal_pair(float2 z, float2& phi, float2& bell)
         q = __ffma2_rn(q, t, f2_splat(6.370539665e-01f));
         q = __fmul2_rn(__fmul2_rn(q, __fmul2_rn(a, r)), bell);
     } else {
-        const float2 t = rcp_pair(__ffma2_rn(x, f2_splat(0.36571f), f2_splat(1.f)));
+        const float2 t = rcp_pair(__ffma2_rn(x, f2_splat(SUMMED ? 0.29133f : 0.36571f), f2_splat(1.f)));
         // e^(-z^2/2) = 2^(-z^2 log2(e) / 2)
         bell = exp2_pair(__fmul2_rn(__fmul2_rn(z, z), f2_splat(-0.72134752f)));
-        q = __ffma2_rn(t, f2_splat(-9.361262619e-02f), f2_splat(2.265792787e-01f));
-        q = __ffma2_rn(q, t, f2_splat(6.293377280e-02f));
-        q = __ffma2_rn(q, t, f2_splat(1.592284888e-01f));
-        q = __ffma2_rn(q, t, f2_splat(1.448649615e-01f));
+        if constexpr (SUMMED) {
+            q = __ffma2_rn(t, f2_splat(-8.762242645e-02f), f2_splat(2.761290669e-01f));
+            q = __ffma2_rn(q, t, f2_splat(-8.285358548e-02f));
+            q = __ffma2_rn(q, t, f2_splat(1.744683087e-01f));
+            q = __ffma2_rn(q, t, f2_splat(1.025927290e-01f));
+            q = __ffma2_rn(q, t, f2_splat(1.172858700e-01f));
+        } else {
+            q = __ffma2_rn(t, f2_splat(-9.361262619e-02f), f2_splat(2.265792787e-01f));
+            q = __ffma2_rn(q, t, f2_splat(6.293377280e-02f));
+            q = __ffma2_rn(q, t, f2_splat(1.592284888e-01f));
+            q = __ffma2_rn(q, t, f2_splat(1.448649615e-01f));
+        }
         q = __fmul2_rn(__fmul2_rn(q, t), bell);
     }
     phi = make_float2(z.x < 0.f ? q.x : 1.f - q.x, z.y < 0.f ? q.y : 1.f - q.y);
@@ -219,11 +229,11 @@ __device__ __forceinline__ float2 act_pair(float2 z) {
         return __fmul2_rn(z, rcp_pair(one_plus_exp<T>(z)));
     } else {
         float2 phi, bell;
-        normal_pair<T>(z, phi, bell);
+        normal_pair<T, false>(z, phi, bell);
         return __fmul2_rn(z, phi);
     }
 }
-template <typename T, int ACT>
+template <typename T, int ACT, bool SUMMED>
 __device__ __forceinline__ float2 slope_pair(float2 z) {
     if constexpr (ACT == RMSNORM_ACT_SILU) {
         // s (1 + z (1 - s)) = s + (z s) (1 - s)
@@ -232,7 +242,7 @@ __device__ __forceinline__ float2 slope_pair(float2 z) {
         return __fmul2_rn(s, __ffma2_rn(z, r, f2_splat(1.f)));
     } else {
         float2 phi, bell;
-        normal_pair<T>(z, phi, bell);
+        normal_pair<T, SUMMED>(z, phi, bell);
         return __ffma2_rn(__fmul2_rn(z, f2_splat(0.39894228f)), bell, phi);
     }
 }
@@ -299,7 +309,7 @@ struct Columns<T, true, ACT> {
         for (int e = 0; e < PAIRS; ++e) {
             c[e] = __fadd2_rn(c[e], mean[e]);
             if constexpr (ACT != RMSNORM_ACT_NONE)
-                d[e] = __fmul2_rn(d[e], slope_pair<T, ACT>(__ffma2_rn(c[e], k1[e], b[e])));
+                d[e] = __fmul2_rn(d[e], slope_pair<T, ACT, true>(__ffma2_rn(c[e], k1[e], b[e])));
             p[e] = __fadd2_rn(p[e], d[e]);
             q[e] = __ffma2_rn(d[e], c[e], q[e]);
         }
@@ -312,7 +322,7 @@ struct Columns<T, true, ACT> {
 #pragma unroll
         for (int e = 0; e < PAIRS; ++e) {
             if constexpr (ACT != RMSNORM_ACT_NONE)
-                d[e] = __fmul2_rn(d[e], slope_pair<T, ACT>(__ffma2_rn(x[e], k1[e], k2[e])));
+                d[e] = __fmul2_rn(d[e], slope_pair<T, ACT, false>(__ffma2_rn(x[e], k1[e], k2[e])));
             d[e] = __ffma2_rn(d[e], k1[e], __ffma2_rn(x[e], k3[e], k4[e]));
         }
         return Pack<T>::pack2(d);
