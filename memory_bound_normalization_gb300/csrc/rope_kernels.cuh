@@ -12,7 +12,7 @@
 //
 // Everything is bound by DRAM: a row is read once and written once (16384 tokens
 // of 40 bf16 heads of 128 forward, 336 MB, in 56 us: 6.0 TB/s; 32768 backward,
-// 1 GB, in 156 us: 6.5 TB/s; one token of 8 sequences in 3.4 us, the launch and
+// 1 GB, in 152 us: 6.6 TB/s; one token of 8 sequences in 3.4 us, the launch and
 // three trips to memory). A group of `lanes` lanes shares a row and each lane owns whole pairs
 // (both halves), so the rotation needs no exchange between lanes and the row
 // sum is one butterfly. The elements that pass are pairs too, whose values are
