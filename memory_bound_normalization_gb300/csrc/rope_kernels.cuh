@@ -21,7 +21,8 @@
 //
 // Angles: one turn is 2^64, so the product of an integer position and the
 // frequency in turns wraps exactly where the circle does, off by what the
-// frequency's last place makes of it, |position| 2^-63 turns; an fp32 product at position 2^20 would be off by 0.06 radians.
+// frequency's last place makes of it, |position| 2^-63 turns; an fp32 product at
+// position 2^20 would be off by 0.06 radians.
 #pragma once
 
 #include "common.cuh"
