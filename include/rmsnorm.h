@@ -409,6 +409,174 @@ size_t rmsnorm_group_norm_workspace_size(int64_t B, int64_t S, int64_t C,
                                          int device);
 
 /*
+ * Embedding lookup with a scale, and its gradient. Tokens are outer x inner
+ * ids with a stride each (the ids of a batch without its last column are
+ * inner = T - 1, id_stride = {T, 1}); token i = o * inner + j has row i of y
+ * and dy.
+ */
+typedef struct {
+    int64_t outer, inner;  /* tokens: outer * inner <= 2^31-1 */
+    int64_t id_stride[2];  /* elements between ids over (outer, inner) */
+    int64_t num_rows;      /* rows of the table, 1 .. 2^31-1 */
+    int64_t width;         /* elements of a row, 1 .. 2^31-1 */
+    int64_t table_stride;  /* elements between rows of the table, or of its
+                              gradient */
+    int64_t row_stride;    /* elements between rows of y, or of dy */
+    int32_t ids_64;        /* ids are int64 (else int32) */
+    float scale;
+} rmsnorm_embedding_t;
+
+/*
+ * y_i = scale * table[id_i], the product in fp32 and rounded once. A token
+ * whose id lies outside [0, num_rows) gets a row of zeros: a shard of a table
+ * takes ids less its first row, and the shards' results add up. dtype names
+ * the types of y and, as of the norm's weight, of the table: the same, or an
+ * fp32 table with 16-bit rows. One kernel.
+ * No tokens: nothing to do. A NULL pointer, an unknown dtype, a size outside
+ * the ranges above, a negative stride, or a stride of an output below the
+ * width return RMSNORM_ERR_INVALID_ARG; a pointer that is not aligned to its
+ * elements RMSNORM_ERR_MISALIGNED. Rows that 16-byte (8-, 4-byte) pieces fit
+ * are moved by them, others element by element.
+ */
+int rmsnorm_embedding_fwd(const rmsnorm_embedding_t *embedding,
+                          const void *ids, const void *table, void *y,
+                          int dtype, cudaStream_t stream);
+
+/*
+ * The table's gradient: grad_v = scale * sum of dy_i over the tokens with id
+ * v, zero where there are none; tokens whose id is padding_id (negative: none)
+ * or lies outside the table count for nothing. accumulate != 0 adds that to what
+ * grad holds instead (a sum over micro-batches; rows without a token are
+ * neither read nor written). dtype names the types of dy and of grad (as of y
+ * and the table). Tokens are sorted by id, so every row's sum is fp32 in an
+ * order that the sizes alone fix, rounded once: the same bits on every run,
+ * no floating-point atomics. Three launches, or two and three for each nine bits of
+ * num_rows past 131072 tokens. Workspace and errors as the norm's backward
+ * (RMSNORM_ERR_NOMEM), arguments as the forward's.
+ */
+int rmsnorm_embedding_bwd(const rmsnorm_embedding_t *embedding,
+                          const void *ids, const void *dy, void *grad,
+                          int64_t padding_id, int accumulate, int dtype,
+                          cudaStream_t stream);
+
+/*
+ * rmsnorm_embedding_bwd with a caller-provided workspace: device memory of at
+ * least rmsnorm_embedding_bwd_workspace_size bytes, 16-byte aligned, not
+ * shared with another call in flight. A smaller one returns
+ * RMSNORM_ERR_INVALID_ARG, a misaligned one RMSNORM_ERR_MISALIGNED.
+ */
+int rmsnorm_embedding_bwd_ws(const rmsnorm_embedding_t *embedding,
+                             const void *ids, const void *dy, void *grad,
+                             int64_t padding_id, int accumulate, int dtype,
+                             void *workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
+/* Bytes of workspace rmsnorm_embedding_bwd_ws needs; 0 without tokens or if
+   the arguments are invalid. */
+size_t rmsnorm_embedding_bwd_workspace_size(int64_t tokens, int64_t num_rows,
+                                            int64_t width);
+
+/* Experts of an expert sort at most. */
+#define RMSNORM_MAX_EXPERTS 1024
+
+/*
+ * Rows that hold the choices of `tokens` tokens of `choices` experts each,
+ * sorted by expert with every expert's first row a multiple of `align`, however
+ * they fall: the largest multiple of align up to
+ * n + min(num_experts, n) * (align - 1), n = tokens * choices. -1 if that is
+ * past 2^31-1 or the arguments are invalid.
+ */
+int64_t rmsnorm_expert_rows(int64_t tokens, int64_t choices,
+                            int64_t num_experts, int64_t align);
+
+/*
+ * Sorts a router's choices by expert. Reads experts [tokens, choices] (int64
+ * if experts_64, else int32); a choice outside [0, num_experts) is dropped.
+ * Writes
+ *   position [tokens, choices]   the row of each choice, -1 if dropped
+ *   source [rows]                the choice (token * choices + k) of each row,
+ *                                -1 of rows without one
+ *   offsets [num_experts + 1]    each expert's first row, a multiple of align,
+ *                                and behind the last expert's
+ *   counts [num_experts]         choices of each expert
+ * Within an expert, choices keep their order. rows >= rmsnorm_expert_rows(...);
+ * rows behind the last expert have no choice. 1 <= num_experts <=
+ * RMSNORM_MAX_EXPERTS, 1 <= align, tokens * choices <= 2^31-1, else
+ * RMSNORM_ERR_INVALID_ARG. One launch; past 131072 choices three, and a
+ * workspace from the stream-ordered allocator (RMSNORM_ERR_NOMEM).
+ */
+int rmsnorm_expert_sort(const void *experts, int experts_64, int64_t tokens,
+                        int64_t choices, int64_t num_experts, int64_t align,
+                        int64_t rows, int32_t *position, int32_t *source,
+                        int32_t *offsets, int32_t *counts,
+                        cudaStream_t stream);
+
+/* rmsnorm_expert_sort with a caller-provided workspace, on the terms of
+   rmsnorm_embedding_bwd_ws, and its size (0: none needed, or invalid). */
+int rmsnorm_expert_sort_ws(const void *experts, int experts_64,
+                           int64_t tokens, int64_t choices,
+                           int64_t num_experts, int64_t align, int64_t rows,
+                           int32_t *position, int32_t *source,
+                           int32_t *offsets, int32_t *counts, void *workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+size_t rmsnorm_expert_sort_workspace_size(int64_t tokens, int64_t choices,
+                                          int64_t num_experts);
+
+/*
+ * Shapes of the calls between tokens and the rows of their experts. Tensors by
+ * token are [tokens, width], tensors by row [rows, width], strides in elements
+ * between their rows. position and source are an expert sort's; a position
+ * outside [0, rows) counts as dropped. A row is one choice's: no two positions
+ * are alike.
+ */
+typedef struct {
+    int64_t tokens, rows, width;
+    int64_t token_stride;    /* of x, dx, y, dy */
+    int64_t row_stride;      /* of rows, drows read, rows written */
+    int64_t residual_stride; /* combine forward */
+    int64_t drow_stride;     /* of the drows that the combine backward writes */
+    int32_t choices;
+} rmsnorm_experts_t;
+
+/*
+ * Dispatch: rows[position[t, k]] = x[t]; rows without a choice (source < 0) are
+ * zeroed. Its backward: dx[t] = sum over the token's choices of
+ * drows[position[t, k]], in fp32 in the choices' order, rounded once; zero for a
+ * token whose choices are all dropped. dtype names the type of both tensors.
+ * Errors as rmsnorm_embedding_fwd. One kernel each.
+ */
+int rmsnorm_expert_dispatch_fwd(const rmsnorm_experts_t *experts,
+                                const void *x, const int32_t *position,
+                                const int32_t *source, void *rows, int dtype,
+                                cudaStream_t stream);
+int rmsnorm_expert_dispatch_bwd(const rmsnorm_experts_t *experts,
+                                const void *drows, const int32_t *position,
+                                void *dx, int dtype, cudaStream_t stream);
+
+/*
+ * Combine: y[t] = residual[t] + sum over the token's choices of
+ * weights[t, k] * rows[position[t, k]], in fp32 in that order, rounded once.
+ * weights NULL: 1; residual NULL: 0. A dropped choice's weight is not read.
+ * dtype names the type of the tensors and, as of the norm's weight, of
+ * weights [tokens, choices].
+ * Its backward: drows[position[t, k]] = weights[t, k] * dy[t], rows without a
+ * choice zero, and dweights[t, k] = the sum over columns of
+ * dy[t] * rows[position[t, k]] (fp32, 0 if dropped). Without weights, rows and
+ * dweights are not used. The residual's gradient is dy itself. Deterministic.
+ * Errors as rmsnorm_embedding_fwd. One kernel each.
+ */
+int rmsnorm_expert_combine_fwd(const rmsnorm_experts_t *experts,
+                               const void *rows, const int32_t *position,
+                               const void *weights, const void *residual,
+                               void *y, int dtype, cudaStream_t stream);
+int rmsnorm_expert_combine_bwd(const rmsnorm_experts_t *experts,
+                               const void *dy, const void *rows,
+                               const int32_t *position, const int32_t *source,
+                               const void *weights, void *drows,
+                               float *dweights, int dtype,
+                               cudaStream_t stream);
+
+/*
  * Device-side status. Every wait inside the kernels (on a bulk copy landing
  * in shared memory, or on the other blocks of a group norm's slab) is bounded
  * in time; a wait that runs out records

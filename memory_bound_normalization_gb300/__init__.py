@@ -8,9 +8,13 @@ raise ``RMSNormError`` on a non-OK status; ``add_forward`` and
 ``add_backward`` do the same for the residual add, ``qk_rope_forward`` and
 ``qk_rope_backward`` for the QK-norm with rotary positions of several axes,
 ``group_norm_forward`` and ``group_norm_backward`` for group norm with an
-activation on channels-last tensors. ``autograd`` holds differentiable wrappers
-(``rms_norm``, ``fused_add_rms_norm``, ``qk_norm_rope``, ``group_norm`` and the
-modules ``RMSNorm``, ``QKNormRope``, ``GroupNorm``).
+activation on channels-last tensors, ``embedding_forward`` and
+``embedding_backward`` for the embedding lookup with a scale, ``expert_sort``,
+``expert_dispatch_*`` and ``expert_combine_*`` for the rows of a mixture of
+experts. ``autograd`` holds differentiable wrappers (``rms_norm``,
+``fused_add_rms_norm``, ``qk_norm_rope``, ``group_norm``, ``embedding``,
+``expert_dispatch``, ``expert_combine`` and the modules ``RMSNorm``,
+``QKNormRope``, ``GroupNorm``, ``Embedding``).
 """
 from __future__ import annotations
 
@@ -31,6 +35,7 @@ from ._lib import (  # noqa: F401
     F16,
     F16_W_F32,
     F32,
+    MAX_EXPERTS,
     OK,
     PASS_BWD,
     PASS_BWD_RES,
@@ -42,6 +47,8 @@ from ._lib import (  # noqa: F401
     ROPE_MAX_AXES,
     ROPE_MAX_HEAD_DIM,
     VARIANTS,
+    Embedding,
+    Experts,
     Plan,
     RMSNormError,
     Rope,
@@ -57,6 +64,18 @@ from ._lib import (  # noqa: F401
     rmsnorm_bwd_noalloc,
     rmsnorm_bwd_workspace_size,
     rmsnorm_bwd_ws,
+    rmsnorm_embedding_bwd,
+    rmsnorm_embedding_bwd_workspace_size,
+    rmsnorm_embedding_bwd_ws,
+    rmsnorm_embedding_fwd,
+    rmsnorm_expert_combine_bwd,
+    rmsnorm_expert_combine_fwd,
+    rmsnorm_expert_dispatch_bwd,
+    rmsnorm_expert_dispatch_fwd,
+    rmsnorm_expert_rows,
+    rmsnorm_expert_sort,
+    rmsnorm_expert_sort_workspace_size,
+    rmsnorm_expert_sort_ws,
     rmsnorm_fwd,
     rmsnorm_get_last_device_error,
     rmsnorm_group_norm_bwd,
@@ -81,6 +100,16 @@ from .image_ops import (  # noqa: F401
     group_norm_forward,
     qk_rope_backward,
     qk_rope_forward,
+)
+from .token_ops import (  # noqa: F401
+    ExpertRows,
+    embedding_backward,
+    embedding_forward,
+    expert_combine_backward,
+    expert_combine_forward,
+    expert_dispatch_backward,
+    expert_dispatch_forward,
+    expert_sort,
 )
 
 __version__ = "0.2.0"

@@ -53,6 +53,8 @@ ACT_GELU = 2
 ROPE_MAX_AXES = 4
 ROPE_MAX_HEAD_DIM = 256
 
+MAX_EXPERTS = 1024
+
 VARIANTS = {0: "none", 1: "rowgroup", 2: "cta_row", 3: "cluster_row", 4: "scalar",
             5: "two_pass", 6: "ring"}
 
@@ -77,6 +79,18 @@ EXPORTS = (
     "rmsnorm_group_norm_fwd_ws",
     "rmsnorm_group_norm_bwd_ws",
     "rmsnorm_group_norm_workspace_size",
+    "rmsnorm_embedding_fwd",
+    "rmsnorm_embedding_bwd",
+    "rmsnorm_embedding_bwd_ws",
+    "rmsnorm_embedding_bwd_workspace_size",
+    "rmsnorm_expert_rows",
+    "rmsnorm_expert_sort",
+    "rmsnorm_expert_sort_ws",
+    "rmsnorm_expert_sort_workspace_size",
+    "rmsnorm_expert_dispatch_fwd",
+    "rmsnorm_expert_dispatch_bwd",
+    "rmsnorm_expert_combine_fwd",
+    "rmsnorm_expert_combine_bwd",
     "rmsnorm_get_last_device_error",
     "rmsnorm_status_string",
     "rmsnorm_set_wait_limit_ns",
@@ -147,6 +161,38 @@ class Rope(ctypes.Structure):
     ]
 
 
+class Embedding(ctypes.Structure):
+    """rmsnorm_embedding_t: the tokens, sizes and strides of a lookup."""
+
+    _fields_ = [
+        ("outer", ctypes.c_int64),
+        ("inner", ctypes.c_int64),
+        ("id_stride", ctypes.c_int64 * 2),
+        ("num_rows", ctypes.c_int64),
+        ("width", ctypes.c_int64),
+        ("table_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("ids_64", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class Experts(ctypes.Structure):
+    """rmsnorm_experts_t: the shapes of a call between tokens and their experts'
+    rows."""
+
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("width", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64),
+        ("drow_stride", ctypes.c_int64),
+        ("choices", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
 
@@ -203,6 +249,21 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.rmsnorm_group_norm_workspace_size.restype = sz
         lib.rmsnorm_group_norm_fwd.argtypes = [vp] * 6 + [i64] * 4 + [f, i, i, vp]
         lib.rmsnorm_group_norm_bwd.argtypes = [vp] * 9 + [i64] * 4 + [i, i, vp]
+        lib.rmsnorm_embedding_fwd.argtypes = [vp] * 4 + [i, vp]
+        lib.rmsnorm_embedding_bwd.argtypes = [vp] * 4 + [i64, i, i, vp]
+        lib.rmsnorm_embedding_bwd_ws.argtypes = [vp] * 4 + [i64, i, i, vp, sz, vp]
+        lib.rmsnorm_embedding_bwd_workspace_size.argtypes = [i64, i64, i64]
+        lib.rmsnorm_embedding_bwd_workspace_size.restype = sz
+        lib.rmsnorm_expert_rows.argtypes = [i64] * 4
+        lib.rmsnorm_expert_rows.restype = i64
+        lib.rmsnorm_expert_sort.argtypes = [vp, i] + [i64] * 5 + [vp] * 5
+        lib.rmsnorm_expert_sort_ws.argtypes = [vp, i] + [i64] * 5 + [vp] * 5 + [sz, vp]
+        lib.rmsnorm_expert_sort_workspace_size.argtypes = [i64] * 3
+        lib.rmsnorm_expert_sort_workspace_size.restype = sz
+        lib.rmsnorm_expert_dispatch_fwd.argtypes = [vp] * 5 + [i, vp]
+        lib.rmsnorm_expert_dispatch_bwd.argtypes = [vp] * 4 + [i, vp]
+        lib.rmsnorm_expert_combine_fwd.argtypes = [vp] * 6 + [i, vp]
+        lib.rmsnorm_expert_combine_bwd.argtypes = [vp] * 8 + [i, vp]
         lib.rmsnorm_get_last_device_error.argtypes = [vp]
         lib.rmsnorm_status_string.argtypes = [i]
         lib.rmsnorm_status_string.restype = ctypes.c_char_p
@@ -219,7 +280,10 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
                      "rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd", "rmsnorm_group_norm_fwd",
                      "rmsnorm_group_norm_bwd", "rmsnorm_qk_rope_bwd_ws",
                      "rmsnorm_group_norm_fwd_ws", "rmsnorm_group_norm_bwd_ws",
-                     "rmsnorm_get_last_device_error",
+                     "rmsnorm_embedding_fwd", "rmsnorm_embedding_bwd", "rmsnorm_embedding_bwd_ws",
+                     "rmsnorm_expert_sort", "rmsnorm_expert_sort_ws", "rmsnorm_expert_dispatch_fwd",
+                     "rmsnorm_expert_dispatch_bwd", "rmsnorm_expert_combine_fwd",
+                     "rmsnorm_expert_combine_bwd", "rmsnorm_get_last_device_error",
                      "rmsnorm_probe", "rmsnorm_plan"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
@@ -383,6 +447,88 @@ def rmsnorm_group_norm_bwd_ws(x, w, b, dy, mean, rstd, dx, dw, db, B: int, S: in
 def rmsnorm_group_norm_workspace_size(B: int, S: int, C: int, G: int, dtype: int, backward: int,
                                       device: int) -> int:
     return load_library().rmsnorm_group_norm_workspace_size(B, S, C, G, dtype, backward, device)
+
+
+def _struct_ptr(d):
+    return None if d is None else ctypes.addressof(d)
+
+
+def rmsnorm_embedding_fwd(embedding, ids, table, y, dtype: int, stream=None) -> int:
+    """`embedding` is an Embedding or None; tensors it gives strides for may be strided."""
+    return load_library().rmsnorm_embedding_fwd(_struct_ptr(embedding), _strided_ptr(ids),
+                                                _strided_ptr(table), _strided_ptr(y), dtype,
+                                                _stream(stream))
+
+
+def rmsnorm_embedding_bwd(embedding, ids, dy, grad, padding_id: int, accumulate: int, dtype: int,
+                          stream=None) -> int:
+    return load_library().rmsnorm_embedding_bwd(_struct_ptr(embedding), _strided_ptr(ids),
+                                                _strided_ptr(dy), _strided_ptr(grad), padding_id,
+                                                accumulate, dtype, _stream(stream))
+
+
+def rmsnorm_embedding_bwd_ws(embedding, ids, dy, grad, padding_id: int, accumulate: int,
+                             dtype: int, workspace, workspace_bytes: int, stream=None) -> int:
+    return load_library().rmsnorm_embedding_bwd_ws(
+        _struct_ptr(embedding), _strided_ptr(ids), _strided_ptr(dy), _strided_ptr(grad),
+        padding_id, accumulate, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def rmsnorm_embedding_bwd_workspace_size(tokens: int, num_rows: int, width: int) -> int:
+    return load_library().rmsnorm_embedding_bwd_workspace_size(tokens, num_rows, width)
+
+
+def rmsnorm_expert_rows(tokens: int, choices: int, num_experts: int, align: int) -> int:
+    return load_library().rmsnorm_expert_rows(tokens, choices, num_experts, align)
+
+
+def rmsnorm_expert_sort(experts, experts_64: int, tokens: int, choices: int, num_experts: int,
+                        align: int, rows: int, position, source, offsets, counts,
+                        stream=None) -> int:
+    return load_library().rmsnorm_expert_sort(
+        _ptr(experts), experts_64, tokens, choices, num_experts, align, rows, _ptr(position),
+        _ptr(source), _ptr(offsets), _ptr(counts), _stream(stream))
+
+
+def rmsnorm_expert_sort_ws(experts, experts_64: int, tokens: int, choices: int, num_experts: int,
+                           align: int, rows: int, position, source, offsets, counts, workspace,
+                           workspace_bytes: int, stream=None) -> int:
+    return load_library().rmsnorm_expert_sort_ws(
+        _ptr(experts), experts_64, tokens, choices, num_experts, align, rows, _ptr(position),
+        _ptr(source), _ptr(offsets), _ptr(counts), _ptr(workspace), workspace_bytes,
+        _stream(stream))
+
+
+def rmsnorm_expert_sort_workspace_size(tokens: int, choices: int, num_experts: int) -> int:
+    return load_library().rmsnorm_expert_sort_workspace_size(tokens, choices, num_experts)
+
+
+def rmsnorm_expert_dispatch_fwd(experts, x, position, source, rows, dtype: int,
+                                stream=None) -> int:
+    """`experts` is an Experts or None; tensors it gives strides for may be strided."""
+    return load_library().rmsnorm_expert_dispatch_fwd(
+        _struct_ptr(experts), _strided_ptr(x), _ptr(position), _ptr(source), _strided_ptr(rows),
+        dtype, _stream(stream))
+
+
+def rmsnorm_expert_dispatch_bwd(experts, drows, position, dx, dtype: int, stream=None) -> int:
+    return load_library().rmsnorm_expert_dispatch_bwd(
+        _struct_ptr(experts), _strided_ptr(drows), _ptr(position), _strided_ptr(dx), dtype,
+        _stream(stream))
+
+
+def rmsnorm_expert_combine_fwd(experts, rows, position, weights, residual, y, dtype: int,
+                               stream=None) -> int:
+    return load_library().rmsnorm_expert_combine_fwd(
+        _struct_ptr(experts), _strided_ptr(rows), _ptr(position), _ptr(weights),
+        _strided_ptr(residual), _strided_ptr(y), dtype, _stream(stream))
+
+
+def rmsnorm_expert_combine_bwd(experts, dy, rows, position, source, weights, drows, dweights,
+                               dtype: int, stream=None) -> int:
+    return load_library().rmsnorm_expert_combine_bwd(
+        _struct_ptr(experts), _strided_ptr(dy), _strided_ptr(rows), _ptr(position), _ptr(source),
+        _ptr(weights), _strided_ptr(drows), _ptr(dweights), dtype, _stream(stream))
 
 
 def rmsnorm_get_last_device_error(stream=None) -> int:

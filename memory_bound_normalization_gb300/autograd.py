@@ -10,7 +10,9 @@ tensors; rows are the last dimension.
 
 ``group_norm`` / ``GroupNorm`` (channels last, with an activation) and
 ``qk_norm_rope`` / ``QKNormRope`` (QK-norm and rotary positions of several
-axes) do the same over their operators.
+axes) do the same over their operators, and ``embedding`` / ``Embedding``,
+``expert_dispatch`` and ``expert_combine`` over the rows that a language model moves by
+an index.
 
 Backward passes can be captured into CUDA graphs as PyTorch's own can: not while
 an eager graph of the same leaves is alive, whose streams the capture cannot wait
@@ -24,6 +26,7 @@ from torch.autograd.function import once_differentiable
 from . import _lib
 from . import dtype_code
 from . import image_ops
+from . import token_ops
 
 
 def _rows(t: torch.Tensor):
@@ -241,3 +244,116 @@ class QKNormRope(torch.nn.Module):
         return qk_norm_rope(q, k, self.q_weight, None if k is None else self.k_weight, positions,
                             self.inv_freq, self.sections, self.interleaved, self.adjacent,
                             self.eps)
+
+
+def _one_stride(t):
+    """t, or a dense copy where its rows have no one stride (a broadcast gradient)."""
+    if t.numel() and (t.stride(-1) != 1 or t.stride() != _dense_strides(t)):
+        return t.contiguous()
+    return t
+
+
+def _dense_strides(t):
+    """Strides of rows of the stride that t's have, laid out one after another."""
+    step = t.stride(-2) if t.dim() > 1 else 0
+    out = [1]
+    for n in reversed(t.shape[1:-1] if t.dim() > 1 else ()):
+        out.append(step)
+        step *= n
+    if t.dim() > 1:
+        out.append(step)
+    return tuple(reversed(out))
+
+
+class _EmbeddingFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, table, scale, padding_idx, out_dtype):
+        ctx.save_for_backward(ids)
+        ctx.rows, ctx.table_dtype, ctx.style = table.shape[0], table.dtype, (scale, padding_idx)
+        return token_ops.embedding_forward(ids, table, scale, out_dtype)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        (ids,) = ctx.saved_tensors
+        grad = token_ops.embedding_backward(ids, _one_stride(dy), ctx.rows, *ctx.style,
+                                            grad_dtype=ctx.table_dtype)
+        return None, grad, None, None, None
+
+
+def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
+              padding_idx: int | None = None, out_dtype: torch.dtype | None = None):
+    """scale * table[ids], differentiable in table; see token_ops.embedding_forward.
+    The row padding_idx gets no gradient."""
+    return _EmbeddingFn.apply(ids, table, float(scale), padding_idx, out_dtype)
+
+
+class Embedding(torch.nn.Module):
+    """``torch.nn.Embedding``-like table of `num_embeddings` rows, looked up with a
+    scale; `out_dtype` gives 16-bit rows of an fp32 table."""
+
+    def __init__(self, num_embeddings: int, embedding_dim: int, scale: float = 1.0,
+                 padding_idx: int | None = None, device=None,
+                 weight_dtype: torch.dtype = torch.float32, out_dtype: torch.dtype | None = None):
+        super().__init__()
+        self.scale, self.padding_idx, self.out_dtype = scale, padding_idx, out_dtype
+        self.weight = torch.nn.Parameter(torch.empty(num_embeddings, embedding_dim, device=device,
+                                                     dtype=weight_dtype))
+        self.reset_parameters()
+
+    def reset_parameters(self) -> None:
+        torch.nn.init.normal_(self.weight)
+        if self.padding_idx is not None:
+            with torch.no_grad():
+                self.weight[self.padding_idx].zero_()
+
+    def forward(self, ids: torch.Tensor) -> torch.Tensor:
+        return embedding(ids, self.weight, self.scale, self.padding_idx, self.out_dtype)
+
+
+class _ExpertDispatchFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, position, source):
+        ctx.save_for_backward(position)
+        return token_ops.expert_dispatch_forward(x, position, source)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, drows):
+        (position,) = ctx.saved_tensors
+        return token_ops.expert_dispatch_backward(_one_stride(drows), position), None, None
+
+
+class _ExpertCombineFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, weights, residual, position, source):
+        # without weights the backward does not look at the rows
+        ctx.save_for_backward(rows if weights is not None else None, weights, position, source)
+        return token_ops.expert_combine_forward(rows, position, weights, residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        rows, weights, position, source = ctx.saved_tensors
+        dense = _one_stride(dy)
+        if weights is None:
+            drows, dw = token_ops.expert_dispatch_forward(dense, position, source), None
+        else:
+            drows, dw = token_ops.expert_combine_backward(dense, rows, position, source, weights)
+        return drows, dw, dy if ctx.needs_input_grad[2] else None, None, None
+
+
+def expert_dispatch(x: torch.Tensor, plan: token_ops.ExpertRows) -> torch.Tensor:
+    """rows [R, H]: x [..., H] sent to the rows of its experts (plan: expert_sort's),
+    differentiable in x."""
+    return _ExpertDispatchFn.apply(x, plan.position, plan.source)
+
+
+def expert_combine(rows: torch.Tensor, plan: token_ops.ExpertRows,
+                   weights: torch.Tensor | None = None,
+                   residual: torch.Tensor | None = None) -> torch.Tensor:
+    """residual plus each token's weighted sum of its experts' rows, differentiable in
+    rows, weights and residual. The weights' gradient comes back in fp32; autograd
+    casts it to their dtype."""
+    return _ExpertCombineFn.apply(rows, None if weights is None else weights.contiguous(), residual,
+                                  plan.position, plan.source)

@@ -40,13 +40,16 @@ LIB_NAME = "librmsnorm.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 CHECKED_LIB_PATH = os.path.join(CHECKED_BUILD_DIR, LIB_NAME)
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_INPUTS = [BINDING_SOURCE, *(os.path.join(CSRC, f) for f in ("binding_util.h",
+                                                                     "binding_rows.h"))]
 BINDING_PATH = os.path.join(BUILD_DIR, "_binding.so")
 
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "bwd_f32.cu", "bwd_bf16.cu", "bwd_f16.cu",
            "bwd_res_f32.cu", "bwd_res_bf16.cu", "bwd_res_f16.cu", "naive.cu", "probe.cu",
            "noalloc.cu", "rope.cu", "rope_f32.cu", "rope_bf16.cu", "rope_f16.cu",
            "pair_sum.cu", "group_norm.cu",
-           "group_norm_f32.cu", "group_norm_bf16.cu", "group_norm_f16.cu", "group_norm_scalar.cu"]
+           "group_norm_f32.cu", "group_norm_bf16.cu", "group_norm_f16.cu", "group_norm_scalar.cu",
+           "rows_api.cu", "sort.cu", "embedding.cu", "experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -141,7 +144,7 @@ def binding_is_stale() -> bool:
         return True
     t = os.path.getmtime(BINDING_PATH)
     return any(os.path.getmtime(f) > t for f in
-               (BINDING_SOURCE, os.path.join(INCLUDE, "rmsnorm.h"), os.path.abspath(__file__)))
+               (*BINDING_INPUTS, os.path.join(INCLUDE, "rmsnorm.h"), os.path.abspath(__file__)))
 
 
 def _build_binding() -> None:

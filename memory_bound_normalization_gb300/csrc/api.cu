@@ -9,6 +9,7 @@
 #include <mutex>
 #include <utility>
 
+#include "api_util.h"
 #include "kernels.h"
 #include "ops.h"
 
@@ -30,28 +31,10 @@ bool g_dev_ready[kMaxDevices] = {};
 std::atomic<uint64_t> g_wait_limit_ns{kDefaultWaitLimitNs};
 std::atomic<int64_t> g_drop_unit{-1};
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Maps a CUDA result to a status. A failure is also cleared from the
-// runtime's last-error slot, so it does not surface in the caller's next,
-// unrelated CUDA call.
-int cuda_status(cudaError_t e) {
-    if (e == cudaSuccess) return RMSNORM_OK;
-    cudaGetLastError();
-    return RMSNORM_ERR_CUDA;
-}
-
 int shape_status(int64_t M, int64_t N, int dtype) {
     if (M < 0 || N <= 0 || N > INT32_MAX) return RMSNORM_ERR_INVALID_ARG;
     if (!dtype_known(dtype)) return RMSNORM_ERR_INVALID_ARG;
     return RMSNORM_OK;
-}
-
-int current_device(const DeviceInfo** out) {
-    int dev = -1;
-    if (cuda_status(cudaGetDevice(&dev)) != RMSNORM_OK) return RMSNORM_ERR_CUDA;
-    *out = device_info(dev);
-    return *out ? RMSNORM_OK : RMSNORM_ERR_CUDA;
 }
 
 // Backward checks shared by rmsnorm_bwd and rmsnorm_bwd_ws. On success fills
@@ -159,27 +142,6 @@ int bwd_alloc_run(const void* x, const void* w, const void* dy, const float* rst
     if (st == RMSNORM_OK) st = freed;
     return st;
 }
-
-// Workspace of a call: the caller's, or one from the stream-ordered allocator.
-struct Workspace {
-    void* p = nullptr;
-    size_t bytes = 0;
-    bool given = false;
-
-    int take(size_t need, cudaStream_t s) {
-        if (given) {
-            if (need > 0 && (p == nullptr || bytes < need)) return RMSNORM_ERR_INVALID_ARG;
-            return aligned(p, 16) ? RMSNORM_OK : RMSNORM_ERR_MISALIGNED;
-        }
-        if (need == 0) return RMSNORM_OK;
-        return cuda_status(cudaMallocAsync(&p, need, s)) == RMSNORM_OK ? RMSNORM_OK : RMSNORM_ERR_NOMEM;
-    }
-    int give(int status, cudaStream_t s) {
-        if (given || p == nullptr) return status;
-        const int freed = cuda_status(cudaFreeAsync(p, s));
-        return status != RMSNORM_OK ? status : freed;
-    }
-};
 
 // ------------------------------------------------ rotary positions
 // Checks of the descriptor; on success fills everything of `a` that does not

@@ -1,0 +1,128 @@
+// Device helpers of the operators that move rows by an index: pieces of a row
+// (E elements that a thread moves by one access of up to 16 bytes), and items
+// read through strides.
+#pragma once
+
+#include "common.cuh"
+#include "rows.h"
+
+namespace rmsn {
+
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> {
+    using type = uint4;
+};
+template <>
+struct Word<8> {
+    using type = uint2;
+};
+template <>
+struct Word<4> {
+    using type = uint32_t;
+};
+template <>
+struct Word<2> {
+    using type = uint16_t;
+};
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) { return ld_global_16_stream(p); }
+template <typename W>
+__device__ __forceinline__ W ld_stream(const W* p) {
+    return *p;
+}
+
+template <typename T, int E>
+struct Piece {
+    static constexpr int BYTES = E * static_cast<int>(sizeof(T));
+    static constexpr int WORDS = BYTES > 16 ? BYTES / 16 : 1;
+    using W = typename Word<(BYTES > 16 ? 16 : BYTES)>::type;
+    W w[WORDS];
+
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = W{};
+    }
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = ld_stream(reinterpret_cast<const W*>(p) + i);
+    }
+    // in order with this thread's other accesses (what it reads may be written)
+    __device__ __forceinline__ void load_plain(const T* p) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const W*>(p)[i];
+    }
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) reinterpret_cast<W*>(p)[i] = w[i];
+    }
+    __device__ __forceinline__ void unpack(float (&f)[E]) const {
+        T t[E];
+        memcpy(t, w, BYTES);
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] = to_f32(t[i]);
+    }
+    __device__ __forceinline__ void pack(const float (&f)[E]) {
+        if constexpr (sizeof(T) == 2 && E % 2 == 0) {
+            uint32_t u[E / 2];
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) u[i] = Pack<T>::pack2(f[2 * i], f[2 * i + 1]);
+            memcpy(w, u, BYTES);
+        } else if constexpr (sizeof(T) == 2) {
+            T t = Pack<T>::from_float(f[0]);
+            memcpy(w, &t, BYTES);
+        } else {
+            memcpy(w, f, BYTES);
+        }
+    }
+};
+
+// The number at item i.
+__device__ __forceinline__ int64_t id_at(const KeySource& k, unsigned i) {
+    int64_t at;
+    if (k.inner >= k.n) {
+        at = i * k.stride_inner;
+    } else {
+        const unsigned o = i / k.inner;
+        at = o * k.stride_outer + (i - o * k.inner) * k.stride_inner;
+    }
+    return k.ids_64 ? static_cast<const int64_t*>(k.ids)[at] : static_cast<const int32_t*>(k.ids)[at];
+}
+__device__ __forceinline__ uint32_t key_at(const KeySource& k, unsigned i) {
+    const int64_t id = id_at(k, i);
+    return id >= 0 && id < k.limit && id != k.skip ? static_cast<uint32_t>(id) : static_cast<uint32_t>(k.limit);
+}
+
+// Bytes from the first to behind the last of n rows.
+__device__ __forceinline__ int64_t rows_bytes(int64_t n, int64_t stride, int64_t width, int size) {
+    return ((n - 1) * stride + width) * size;
+}
+
+// The group of lanes a thread of a block of THREADS belongs to, over the grid.
+template <int THREADS>
+__device__ __forceinline__ unsigned group_index(int lanes) {
+    return blockIdx.x * (THREADS / lanes) + threadIdx.x / lanes;
+}
+
+// ------------------------------------------------------------ host geometry
+// Groups of lanes (a power of two, up to a warp) that move a row's pieces, U
+// pieces a lane and chunk.
+struct RowShape {
+    int pieces;  // of a row
+    int lanes;   // of a group
+    int chunks;  // of a row
+};
+inline RowShape row_shape(int pieces, int u) {
+    RowShape r{pieces, 1, 1};
+    while (r.lanes < 32 && r.lanes * u < pieces) r.lanes *= 2;
+    r.chunks = static_cast<int>(cdiv(pieces, static_cast<int64_t>(r.lanes) * u));
+    return r;
+}
+// Whether rows of `bytes` pieces can be moved from p.
+inline bool piece_fits(const void* p, int64_t stride, int size, int e) {
+    const int bytes = e * size > 16 ? 16 : e * size;
+    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * size % bytes == 0);
+}
+
+}  // namespace rmsn

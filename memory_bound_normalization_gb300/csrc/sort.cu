@@ -1,0 +1,467 @@
+// Stable sort of small whole numbers (token ids, experts) with the items they
+// came from, by radix passes.
+//
+// A pass: a warp takes 32 neighbouring items a round. Lanes with the same digit
+// find one another (match), the first of them reads and advances the warp's count
+// of that digit in shared memory, and an item's rank in its warp is the count so
+// far and the equal lanes before it. The counts then become sums over the warps
+// before (a digit a thread), over the blocks before, and over the digits before:
+// item i goes to sum + rank. No count depends on which block or warp comes first, so
+// the order is the same on every run.
+//
+// A few thousand to some hundred thousand keys of 4 to 8 bytes: the time is a
+// chain of launches and barriers, not bytes. Up to kClusterItems one cluster of
+// up to eight blocks does every pass in one launch and joins its counts through
+// distributed shared memory. More items take three launches a pass over as many
+// blocks as fill the device (counts, their prefix, placement).
+#include <algorithm>
+#include <mutex>
+
+#include "rows.cuh"
+
+namespace rmsn {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kMaxRounds = 16;
+constexpr int kMaxCluster8 = 8;
+constexpr int64_t kClusterItems = kThreads * kMaxRounds * kMaxCluster8;
+constexpr int kMaxDigitBits = 9;
+constexpr int kMaxExperts = RMSNORM_MAX_EXPERTS;
+
+struct SortArgs {
+    KeySource k;
+    uint32_t* keys[2];
+    int32_t* items[2];
+    uint8_t* present;
+    uint32_t* counts;  // [bins][blocks], then the bins' totals (many blocks)
+    int blocks;
+    int passes, pass, bits, bins;
+    // experts
+    int32_t* position;
+    int32_t* source;
+    int32_t* offsets;
+    int32_t* expert_counts;
+    int experts, rows, align;
+    int* status;
+};
+
+__host__ __device__ inline int bins_stride(int bins) { return (bins + 1) & ~1; }
+inline int sort_smem(int bins, int warps) { return warps * bins_stride(bins) * 2 + 16 + 4 * 4 * (bins + 1); }
+
+struct Smem {
+    uint16_t* cnt;    // [warps][stride]
+    uint32_t* hist;   // [bins]: the block's
+    uint32_t* base;   // [bins]: where the block's items of a digit start
+    uint32_t* start;  // [bins]: where the digit starts
+    uint32_t* total;  // [bins]
+};
+__device__ __forceinline__ Smem smem_of(int bins) {
+    Smem s;
+    const int warps = blockDim.x / 32, stride = bins_stride(bins);
+    s.cnt = reinterpret_cast<uint16_t*>(rmsn_dynamic_smem);
+    s.hist = reinterpret_cast<uint32_t*>(rmsn_dynamic_smem + ((warps * stride * 2 + 15) & ~15));
+    s.base = s.hist + bins + 1;
+    s.start = s.base + bins + 1;
+    s.total = s.start + bins + 1;
+    return s;
+}
+
+// Keys of the warp's items (0xffffffff behind the last).
+template <int R>
+__device__ __forceinline__ void load_keys(const SortArgs& a, int pass, unsigned first, uint32_t (&key)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const unsigned i = first + r * 32 + threadIdx.x % 32;
+        key[r] = 0xffffffffu;
+        if (i < a.k.n) key[r] = pass == 0 ? key_at(a.k, i) : a.keys[(pass - 1) & 1][i];
+    }
+}
+__device__ __forceinline__ uint32_t digit_of(const SortArgs& a, int pass, uint32_t key) {
+    return a.experts > 0 ? key : (key >> (pass * a.bits)) & ((1u << a.bits) - 1);
+}
+
+// Ranks of the warp's items among its items of the same digit, and its counts.
+template <int R>
+__device__ __forceinline__ void rank_keys(const SortArgs& a, int pass, unsigned first, const uint32_t (&key)[R],
+                                          uint16_t* cnt, uint32_t (&rank)[R]) {
+    const unsigned lane = threadIdx.x % 32;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const bool valid = first + r * 32 + lane < a.k.n;
+        const unsigned act = __ballot_sync(0xffffffffu, valid);
+        rank[r] = 0;
+        if (valid) {
+            const uint32_t d = digit_of(a, pass, key[r]);
+            const unsigned peers = __match_any_sync(act, d);
+            const unsigned before = __popc(peers & ((1u << lane) - 1));
+            const unsigned so_far = cnt[d];
+            __syncwarp(act);
+            if (before == 0) cnt[d] = static_cast<uint16_t>(so_far + __popc(peers));
+            rank[r] = so_far + before;
+        }
+        __syncwarp();
+    }
+}
+
+// Sum of the values of the threads before, over the block.
+__device__ __forceinline__ uint32_t scan_before(uint32_t v, uint32_t* sum) {
+    __shared__ uint32_t warp_sum[33];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint32_t s = v;
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += o;
+    }
+    if (lane == 31) warp_sum[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t w = lane < static_cast<int>(blockDim.x) / 32 ? warp_sum[lane] : 0, t = w;
+#pragma unroll
+        for (int off = 1; off < 32; off *= 2) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, t, off);
+            if (lane >= off) t += o;
+        }
+        warp_sum[lane] = t - w;
+        if (lane == 31) warp_sum[32] = t;
+    }
+    __syncthreads();
+    *sum = warp_sum[32];
+    const uint32_t before = warp_sum[warp] + s - v;
+    __syncthreads();
+    return before;
+}
+
+__device__ __forceinline__ uint32_t rounded(uint32_t v, uint32_t align) { return (v + align - 1) / align * align; }
+
+// From the digit's total and the blocks' before (a digit a thread) to where the
+// block's items go; experts: starts and counts, by block 0.
+__device__ __forceinline__ void place_digits(const SortArgs& a, const Smem& s, uint32_t total, uint32_t mine,
+                                             unsigned block) {
+    const int d = threadIdx.x;
+    const int digits = a.experts > 0 ? a.experts : a.bins;
+    uint32_t all;
+    const uint32_t room = a.experts > 0 ? rounded(total, a.align) : total;
+    const uint32_t start = scan_before(d < digits ? room : 0, &all);
+    if (d < digits) {
+        s.base[d] = start + mine;
+        s.start[d] = start;
+        s.total[d] = total;
+        if (a.experts > 0 && block == 0) {
+            if (RMSN_OK(span_in(a.offsets + d, 4, a.offsets, 4ll * (a.experts + 1)), a.status)) a.offsets[d] = start;
+            if (RMSN_OK(span_in(a.expert_counts + d, 4, a.expert_counts, 4ll * a.experts), a.status))
+                a.expert_counts[d] = total;
+        }
+    }
+    if (d == 0) {
+        s.start[digits] = all;
+        if (a.experts > 0) {
+            s.base[digits] = 0;  // the dropped ones go nowhere
+            if (block == 0) a.offsets[digits] = all;
+        }
+    }
+    __syncthreads();
+}
+
+template <int R>
+__device__ __forceinline__ void scatter(const SortArgs& a, int pass, const Smem& s, const uint16_t* cnt, unsigned first,
+                                        const uint32_t (&key)[R], const uint32_t (&rank)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const unsigned i = first + r * 32 + threadIdx.x % 32;
+        if (i >= a.k.n) continue;
+        const uint32_t d = digit_of(a, pass, key[r]);
+        const uint32_t at = s.base[d] + cnt[d] + rank[r];
+        if (a.experts > 0) {
+            const bool dropped = d >= static_cast<uint32_t>(a.experts);
+            if (RMSN_OK(span_in(a.position + i, 4, a.position, 4ll * a.k.n), a.status))
+                a.position[i] = dropped ? -1 : static_cast<int32_t>(at);
+            if (!dropped && RMSN_OK(span_in(a.source + at, 4, a.source, 4ll * a.rows), a.status))
+                a.source[at] = static_cast<int32_t>(i);
+        } else {
+            const int to = pass & 1;
+            const int32_t item = pass == 0 ? static_cast<int32_t>(i) : a.items[to ^ 1][i];
+            if (!RMSN_OK(at < a.k.n, a.status)) continue;
+            a.keys[to][at] = key[r];
+            a.items[to][at] = item;
+            if (pass == 0 && a.present != nullptr && key[r] < a.k.limit) a.present[key[r]] = 1;
+        }
+    }
+}
+
+// Rows without a choice: behind each expert's, and behind the last expert.
+__device__ __forceinline__ void mark_unused(const SortArgs& a, const Smem& s, unsigned block, unsigned blocks) {
+    const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    for (int e = block * warps + threadIdx.x / 32; e < a.experts; e += blocks * warps) {
+        const int64_t to = s.start[e + 1];
+        for (int64_t i = static_cast<int64_t>(s.start[e]) + s.total[e] + lane; i < to; i += 32)
+            if (RMSN_OK(span_in(a.source + i, 4, a.source, 4ll * a.rows), a.status)) a.source[i] = -1;
+    }
+    for (int64_t i = static_cast<int64_t>(s.start[a.experts]) + block * blockDim.x + threadIdx.x; i < a.rows;
+         i += static_cast<int64_t>(blocks) * blockDim.x)
+        a.source[i] = -1;
+}
+
+__device__ __forceinline__ void clear_present(const SortArgs& a, unsigned block, unsigned blocks) {
+    if (a.present == nullptr) return;
+    // limit bytes from a 16-byte boundary, room up to the next one
+    uint4* p = reinterpret_cast<uint4*>(a.present);
+    for (int64_t i = static_cast<int64_t>(block) * blockDim.x + threadIdx.x; i < (a.k.limit + 15) / 16;
+         i += static_cast<int64_t>(blocks) * blockDim.x)
+        p[i] = make_uint4(0, 0, 0, 0);
+}
+
+// Clears the counts of the warps in use; their number.
+template <int R>
+__device__ __forceinline__ int clear_counts(const SortArgs& a, const Smem& s, unsigned block_first) {
+    const unsigned left = block_first < a.k.n ? a.k.n - block_first : 0;
+    const int warps = static_cast<int>(min((left + 32 * R - 1) / (32 * R), blockDim.x / 32));
+    uint32_t* z = reinterpret_cast<uint32_t*>(s.cnt);
+    for (int i = threadIdx.x; i < warps * bins_stride(a.bins) / 2; i += blockDim.x) z[i] = 0;
+    return warps;
+}
+// Counts of the warps become sums over the warps before; the block's counts.
+__device__ __forceinline__ void sum_warps(const SortArgs& a, const Smem& s, int warps) {
+    const int stride = bins_stride(a.bins);
+    for (int d = threadIdx.x; d < a.bins; d += blockDim.x) {
+        uint32_t sum = 0;
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) {
+            const uint32_t c = s.cnt[w * stride + d];
+            s.cnt[w * stride + d] = static_cast<uint16_t>(sum);
+            sum += c;
+        }
+        s.hist[d] = sum;
+    }
+}
+
+// Every pass, by one cluster.
+template <int R>
+__global__ void __launch_bounds__(kThreads) sort_cluster_kernel(const __grid_constant__ SortArgs a) {
+    const Smem s = smem_of(a.bins);
+    const unsigned rank = cluster_rank(), blocks = cluster_size();
+    const unsigned block_first = rank * blockDim.x * R, warp = threadIdx.x / 32;
+    const unsigned first = block_first + warp * 32 * R;
+    uint16_t* cnt = s.cnt + warp * bins_stride(a.bins);
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
+    clear_present(a, rank, blocks);
+    for (int pass = 0; pass < a.passes; ++pass) {
+        uint32_t key[R], place[R];
+        load_keys<R>(a, pass, first, key);
+        const int warps = clear_counts<R>(a, s, block_first);
+        __syncthreads();
+        rank_keys<R>(a, pass, first, key, cnt, place);
+        __syncthreads();
+        sum_warps(a, s, warps);
+        uint32_t total = 0, mine = 0;
+        if (blocks > 1) {
+            cluster_sync_all();
+            if (threadIdx.x < a.bins) {
+                for (unsigned b = 0; b < blocks; ++b) {
+                    uint32_t v;
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                                 : "=r"(v)
+                                 : "r"(cluster_map(s.hist + threadIdx.x, b))
+                                 : "memory");
+                    total += v;
+                    if (b < rank) mine += v;
+                }
+            }
+        } else {
+            __syncthreads();
+            if (threadIdx.x < a.bins) total = s.hist[threadIdx.x];
+        }
+        place_digits(a, s, total, mine, rank);
+        scatter<R>(a, pass, s, cnt, first, key, place);
+        if (a.experts > 0) mark_unused(a, s, rank, blocks);
+        // every block has read the others' counts, and the next pass reads what they placed
+        if (blocks > 1) cluster_sync_all();
+        else __syncthreads();
+    }
+}
+
+// One pass over many blocks: the counts of each block's digits, ...
+template <int R>
+__global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_constant__ SortArgs a) {
+    uint32_t* hist = reinterpret_cast<uint32_t*>(rmsn_dynamic_smem);
+    for (int d = threadIdx.x; d < a.bins; d += blockDim.x) hist[d] = 0;
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
+    if (a.pass == 0) clear_present(a, blockIdx.x, gridDim.x);
+    uint32_t key[R];
+    const unsigned first = blockIdx.x * (kThreads * R) + threadIdx.x / 32 * 32 * R;
+    load_keys<R>(a, a.pass, first, key);
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (first + r * 32 + threadIdx.x % 32 < a.k.n) atomicAdd(hist + digit_of(a, a.pass, key[r]), 1u);
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.bins; d += blockDim.x)
+        a.counts[static_cast<int64_t>(d) * a.blocks + blockIdx.x] = hist[d];
+}
+// ... a digit's counts become sums over the blocks before, ...
+__global__ void __launch_bounds__(256) sort_prefix_kernel(const __grid_constant__ SortArgs a) {
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
+    uint32_t* c = a.counts + static_cast<int64_t>(blockIdx.x) * a.blocks;
+    uint32_t sum = 0;
+    for (int b0 = 0; b0 < a.blocks; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        const uint32_t v = b < a.blocks ? c[b] : 0;
+        uint32_t all;
+        const uint32_t before = scan_before(v, &all);
+        if (b < a.blocks) c[b] = sum + before;
+        sum += all;
+    }
+    if (threadIdx.x == 0) a.counts[static_cast<int64_t>(a.bins) * a.blocks + blockIdx.x] = sum;
+}
+// ... and the items go to their places.
+template <int R>
+__global__ void __launch_bounds__(kThreads) sort_place_kernel(const __grid_constant__ SortArgs a) {
+    const Smem s = smem_of(a.bins);
+    const unsigned block_first = blockIdx.x * (kThreads * R), warp = threadIdx.x / 32;
+    const unsigned first = block_first + warp * 32 * R;
+    uint16_t* cnt = s.cnt + warp * bins_stride(a.bins);
+    const int warps = clear_counts<R>(a, s, block_first);
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
+    uint32_t key[R], place[R];
+    load_keys<R>(a, a.pass, first, key);
+    uint32_t total = 0, mine = 0;
+    if (threadIdx.x < a.bins) {
+        mine = a.counts[static_cast<int64_t>(threadIdx.x) * a.blocks + blockIdx.x];
+        total = a.counts[static_cast<int64_t>(a.bins) * a.blocks + threadIdx.x];
+    }
+    __syncthreads();
+    rank_keys<R>(a, a.pass, first, key, cnt, place);
+    __syncthreads();
+    sum_warps(a, s, warps);
+    place_digits(a, s, total, mine, blockIdx.x);
+    scatter<R>(a, a.pass, s, cnt, first, key, place);
+    if (a.experts > 0) mark_unused(a, s, blockIdx.x, gridDim.x);
+}
+
+int bits_of(int64_t limit) {
+    int b = 1;
+    while ((limit >> b) != 0) ++b;
+    return b;
+}
+
+// Blocks of a pass over many blocks, kThreads * rounds items each.
+int many_rounds(int64_t n) {
+    int r = 1;
+    while (r < kMaxRounds && cdiv(n, static_cast<int64_t>(kThreads) * r) > 152) r *= 2;
+    return r;
+}
+
+using SortFn = void (*)(const SortArgs);
+template <int R>
+SortFn kernel_of(int which) {
+    if (which == 0) return sort_cluster_kernel<R>;
+    return which == 1 ? SortFn(sort_count_kernel<R>) : SortFn(sort_place_kernel<R>);
+}
+SortFn kernel_for(int which, int rounds) {
+    switch (rounds) {
+        case 1: return kernel_of<1>(which);
+        case 2: return kernel_of<2>(which);
+        case 4: return kernel_of<4>(which);
+        case 8: return kernel_of<8>(which);
+        default: return kernel_of<16>(which);
+    }
+}
+
+// Lets a kernel have the shared memory of the most bins, once a device.
+cudaError_t allow_smem(const DeviceInfo& dev, SortFn fn) {
+    static std::mutex mu;
+    static struct {
+        int device;
+        SortFn fn;
+    } done[1024];
+    static int n = 0;
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < n; ++i)
+        if (done[i].device == dev.device && done[i].fn == fn) return cudaSuccess;
+    const cudaError_t err =
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sort_smem(kMaxExperts + 1, kThreads / 32));
+    if (err == cudaSuccess && n < 1024) done[n++] = {dev.device, fn};
+    return err;
+}
+
+cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
+    const int64_t n = a.k.n;
+    if (n <= kClusterItems) {
+        // one block while its items are few; then eight, a power of two of rounds
+        int blocks = n <= 4 * kThreads ? 1 : kMaxCluster8, rounds = 1;
+        while (static_cast<int64_t>(blocks) * kThreads * rounds < n) rounds *= 2;
+        // no more threads than items or digits need
+        const int digits = a.experts > 0 ? a.experts : a.bins;
+        const int need = std::max<int>(static_cast<int>(std::min<int64_t>(cdiv(n, rounds), kThreads)), digits);
+        const int threads = blocks > 1 ? kThreads : std::min(kThreads, std::max(128, round_up(need, 32)));
+        const SortFn fn = kernel_for(0, rounds);
+        const cudaError_t err = allow_smem(dev, fn);
+        if (err != cudaSuccess) return err;
+        return launch_pdl(fn, blocks, threads, sort_smem(a.bins, threads / 32), blocks, s, a);
+    }
+    const int rounds = many_rounds(n);
+    a.blocks = static_cast<int>(cdiv(n, static_cast<int64_t>(kThreads) * rounds));
+    for (a.pass = 0; a.pass < a.passes; ++a.pass) {
+        cudaError_t err = launch_pdl(kernel_for(1, rounds), a.blocks, kThreads, a.bins * 4, 1, s, a);
+        if (err != cudaSuccess) return err;
+        err = launch_pdl(sort_prefix_kernel, a.bins, 256, 0, 1, s, a);
+        if (err != cudaSuccess) return err;
+        const SortFn fn = kernel_for(2, rounds);
+        err = allow_smem(dev, fn);
+        if (err != cudaSuccess) return err;
+        err = launch_pdl(fn, a.blocks, kThreads, sort_smem(a.bins, kThreads / 32), 1, s, a);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+int sort_passes(int64_t limit) { return static_cast<int>(cdiv(bits_of(limit), kMaxDigitBits)); }
+int sort_max_bins(int64_t limit) { return 1 << cdiv(bits_of(limit), sort_passes(limit)); }
+
+int64_t sort_counts_words(int64_t n, int bins) {
+    if (n <= kClusterItems) return 0;
+    return static_cast<int64_t>(bins) * (cdiv(n, static_cast<int64_t>(kThreads) * many_rounds(n)) + 1);
+}
+
+cudaError_t sort_launch(const DeviceInfo& dev, const KeySource& k, const SortBuffers& b, cudaStream_t s) {
+    SortArgs a{};
+    a.k = k;
+    for (int i = 0; i < 2; ++i) {
+        a.keys[i] = b.keys[i];
+        a.items[i] = b.items[i];
+    }
+    a.present = b.present;
+    a.counts = b.counts;
+    a.passes = sort_passes(k.limit);
+    a.bits = static_cast<int>(cdiv(bits_of(k.limit), a.passes));
+    a.bins = 1 << a.bits;
+    a.status = b.status;
+    return run(dev, a, s);
+}
+
+cudaError_t expert_sort_launch(const DeviceInfo& dev, const ExpertSortArgs& e, cudaStream_t s) {
+    SortArgs a{};
+    a.k = e.k;
+    a.counts = e.block_counts;
+    a.passes = 1;
+    a.experts = static_cast<int>(e.k.limit);
+    a.bins = a.experts + 1;
+    a.position = e.position;
+    a.source = e.source;
+    a.offsets = e.offsets;
+    a.expert_counts = e.counts;
+    a.rows = e.rows;
+    a.align = e.align;
+    a.status = e.status;
+    return run(dev, a, s);
+}
+
+}  // namespace rmsn

@@ -20,10 +20,15 @@ import os
 from . import _lib
 from . import build as _build
 
-# the entry points binding.cpp calls, in the order of its table
+# the entry points binding.cpp calls, in the order of its tables
 _ENTRIES = ("rmsnorm_group_norm_fwd_ws", "rmsnorm_group_norm_bwd_ws",
             "rmsnorm_group_norm_workspace_size", "rmsnorm_qk_rope_fwd", "rmsnorm_qk_rope_bwd_ws",
-            "rmsnorm_qk_rope_bwd_workspace_size")
+            "rmsnorm_qk_rope_bwd_workspace_size",
+            "rmsnorm_embedding_fwd", "rmsnorm_embedding_bwd_ws",
+            "rmsnorm_embedding_bwd_workspace_size", "rmsnorm_expert_rows",
+            "rmsnorm_expert_sort_ws", "rmsnorm_expert_sort_workspace_size",
+            "rmsnorm_expert_dispatch_fwd", "rmsnorm_expert_dispatch_bwd",
+            "rmsnorm_expert_combine_fwd", "rmsnorm_expert_combine_bwd")
 _bound = None
 
 
