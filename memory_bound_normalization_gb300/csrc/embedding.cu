@@ -7,13 +7,15 @@
 // Backward: row v of the gradient is scale * the sum of dy_i over the tokens with
 // id v, in fp32 and in an order that the sizes alone fix. The tokens are sorted
 // by id (sort.cu); the sorted list is cut in segments of a few tokens. A group of
-// lanes adds up its columns of a segment: runs of one id that lie inside are
-// written to their row at once, a run that crosses a border leaves its share in the
-// workspace, and embedding_join_kernel adds the shares of such a run in the
-// segments' order. So a token that fills half of the batch is as much work for each
-// group as any other, and nothing depends on which block is first. Rows without
-// a token are zeroed by blocks of their own, which the sort's marks guide.
-// Bytes: dy once, the whole gradient once.
+// lanes adds up its columns of a segment, a block those of neighbouring segments. Runs
+// of one id that lie in a segment are written to their row at once; a run over
+// several is joined, in the segments' order, through shared memory, and one over
+// several blocks through shares in the workspace, which embedding_join_kernel adds
+// in the blocks' order. So a token that fills half of the batch is as much work for
+// each group as any other, and nothing depends on which block is first.
+// Bytes: dy once, the whole gradient once. Most of them are the rows without a token,
+// which blocks of their own zero beside all three launches: the last rows beside
+// the sort, whether they have a token or not, the others by the sort's marks.
 #include <algorithm>
 
 #include "rows.cuh"
@@ -22,9 +24,9 @@ namespace rmsn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFwdPieces = 4;  // of a lane
 constexpr int kRun = 8;        // rows of dy in flight a lane
-constexpr int kZeroBytes = 16384;
+constexpr int kZeroBytes = 16384;  // of a warp
+constexpr int kMaxSpan = 2048;     // sorted tokens of a block
 
 struct FwdKernelArgs {
     KeySource k;
@@ -36,8 +38,12 @@ struct FwdKernelArgs {
     int* status;
 };
 
+// Pieces of a lane: small ones need more of them in flight.
+__host__ __device__ constexpr int fwd_pieces(int e) { return e >= 4 ? 4 : 8; }
+
 template <typename TT, typename TA, int E>
 __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_constant__ FwdKernelArgs a) {
+    constexpr int kFwdPieces = fwd_pieces(E);
     const unsigned lane = threadIdx.x & (a.shape.lanes - 1);
     const unsigned group = group_index<kThreads>(a.shape.lanes);
     wait_for_prerequisite_grid();
@@ -76,195 +82,299 @@ __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_co
 struct BwdKernelArgs {
     const uint32_t* keys;   // sorted
     const int32_t* items;
-    const uint8_t* present;  // null: rows without a token stay
+    const uint8_t* present;
     const void* dy;
     void* grad;
-    float* partial;  // [segments][2][width]: of the run that comes in, of the one that goes out
+    float* partial;  // [spans][2][width]: of the run that comes in, of the one that goes out
     int64_t dy_stride, grad_stride;
     int64_t rows;  // of the table
-    int64_t zero_units;
     uint32_t n, limit;
-    RowShape shape;  // lanes of a group, one piece each
+    RowShape shape;
+    unsigned spans;       // of the sorted tokens: a block's share
     unsigned sum_blocks;  // blocks that add; the others zero rows
-    int segment;
-    unsigned segments;
-    int zero_rows, zero_pieces, zero_slices;  // of a warp's share
+    int segment;          // tokens of a group
+    int span;             // tokens of a block
+    int64_t zero_from, zero_to;  // rows that this launch zeroes where they have no token
+    int zero_rows, zero_slices;  // rows of a warp's share, shares of a row
     int accumulate;
     float scale;
     int* status;
 };
 
-// Row v's columns: scale * sum, on top of what is there with accumulate.
-template <typename TG, int E>
-__device__ __forceinline__ void put_row(const BwdKernelArgs& a, uint32_t v, int piece, const float (&sum)[E]) {
-    TG* to = static_cast<TG*>(a.grad) + v * a.grad_stride + static_cast<int64_t>(piece) * E;
-    if (!RMSN_OK(span_in(to, E * sizeof(TG), a.grad,
-                         rows_bytes(a.rows, a.grad_stride, static_cast<int64_t>(a.shape.pieces) * E, sizeof(TG))),
-                 a.status))
-        return;
-    Piece<TG, E> out;
-    float f[E];
-    if (a.accumulate) {
-        out.load_plain(to);
-        out.unpack(f);
+template <int E, int U>
+struct Columns {
+    float v[U][E];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = fmaf(a.scale, sum[e], f[e]);
-    } else {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = a.scale * sum[e];
+            for (int e = 0; e < E; ++e) v[u][e] = 0.f;
     }
-    out.pack(f);
-    out.store(to);
+    __device__ __forceinline__ void add(const Columns& o) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[u][e] += o.v[u][e];
+    }
+};
+
+// Row v's columns: scale * sum, on top of what is there with accumulate.
+template <typename TG, int E, int U>
+__device__ __forceinline__ void put_row(const BwdKernelArgs& a, uint32_t v, int piece, const Columns<E, U>& sum) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int p = piece + u * a.shape.lanes;
+        if (p >= a.shape.pieces) continue;
+        TG* to = static_cast<TG*>(a.grad) + v * a.grad_stride + static_cast<int64_t>(p) * E;
+        if (!RMSN_OK(span_in(to, E * sizeof(TG), a.grad,
+                             rows_bytes(a.rows, a.grad_stride, static_cast<int64_t>(a.shape.pieces) * E, sizeof(TG))),
+                     a.status))
+            continue;
+        Piece<TG, E> out;
+        float f[E];
+        if (a.accumulate) {
+            out.load_plain(to);
+            out.unpack(f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = fmaf(a.scale, sum.v[u][e], f[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = a.scale * sum.v[u][e];
+        }
+        out.pack(f);
+        out.store(to);
+    }
 }
 
 template <int E>
-__device__ __forceinline__ float* partial_at(const BwdKernelArgs& a, unsigned segment, int slot, int piece) {
-    return a.partial + (static_cast<int64_t>(segment) * 2 + slot) * a.shape.pieces * E + static_cast<int64_t>(piece) * E;
+__device__ __forceinline__ float* partial_at(const BwdKernelArgs& a, unsigned span, int slot, int piece) {
+    return a.partial + (static_cast<int64_t>(span) * 2 + slot) * a.shape.pieces * E + static_cast<int64_t>(piece) * E;
+}
+template <int E, int U>
+__device__ __forceinline__ void put_partial(const BwdKernelArgs& a, unsigned span, int slot, int piece,
+                                            const Columns<E, U>& sum) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int p = piece + u * a.shape.lanes;
+        if (p >= a.shape.pieces) continue;
+        float* to = partial_at<E>(a, span, slot, p);
+        if (!RMSN_OK(span_in(to, E * 4, a.partial, static_cast<int64_t>(a.spans) * 8 * a.shape.pieces * E), a.status))
+            continue;
+        Piece<float, E> out;
+        out.pack(sum.v[u]);
+        out.store(to);
+    }
 }
 
-template <typename TA, typename TG, int E>
-__device__ __forceinline__ void add_segment(const BwdKernelArgs& a, unsigned segment, int piece) {
-    const uint32_t first = segment * static_cast<uint32_t>(a.segment);
-    const uint32_t end = min(first + a.segment, a.n);
-    uint32_t run = a.keys[first];
-    // the run that this segment starts with began before
-    bool came_in = first > 0 && a.keys[first - 1] == run;
-    const uint32_t behind = end < a.n ? a.keys[end] : 0xffffffffu;
-    float sum[E] = {};
-    auto flush = [&](bool goes_on) {
-        if (run >= a.limit) return;
-        if (!came_in && !goes_on) {
-            put_row<TG, E>(a, run, piece, sum);
-            return;
-        }
-        float* to = partial_at<E>(a, segment, came_in ? 0 : 1, piece);
-        if (!RMSN_OK(span_in(to, E * 4, a.partial, static_cast<int64_t>(a.segments) * 8 * a.shape.pieces * E), a.status))
-            return;
-        Piece<float, E> out;
-        out.pack(sum);
-        out.store(to);
+// What a group's tokens leave for the block to join.
+constexpr int kHead = 1;     // the sum of a run that began before them
+constexpr int kTail = 2;     // the sum of a run that goes on behind them
+constexpr int kThrough = 4;  // both: one run fills them (its sum is the head)
+
+template <typename TA, typename TG, int E, int U>
+__device__ __forceinline__ void add_tokens(const BwdKernelArgs& a, unsigned span, int slice) {
+    __shared__ float held[2][U * E][kThreads];  // heads and tails, a column a thread
+    __shared__ unsigned char state[kThreads];
+    uint32_t* const key = reinterpret_cast<uint32_t*>(rmsn_dynamic_smem);  // [span + 2]: the token before, ours, the next
+    int32_t* const item = reinterpret_cast<int32_t*>(key + a.span + 2);
+    const int lanes = a.shape.lanes, group = threadIdx.x / lanes, groups = kThreads / lanes;
+    const int piece = slice * lanes * U + (threadIdx.x & (lanes - 1));
+    const uint32_t first = span * static_cast<uint32_t>(a.span);
+    const int count = static_cast<int>(min(static_cast<uint32_t>(a.span), a.n - first));
+    const uint32_t none = 0xffffffffu;
+    for (int i = threadIdx.x; i < count + 2; i += kThreads) {
+        const int64_t at = static_cast<int64_t>(first) + i - 1;
+        key[i] = at >= 0 && at < a.n ? a.keys[at] : none;
+        if (i < count) item[i] = a.items[first + i];
+    }
+    __syncthreads();
+    const int from = group * a.segment, to = min(from + a.segment, count);
+    Columns<E, U> sum;
+    sum.clear();
+    int left = 0;
+    auto hold = [&](int slot) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e) held[slot][u * E + e][threadIdx.x] = sum.v[u][e];
     };
-    const TA* dy = static_cast<const TA*>(a.dy) + static_cast<int64_t>(piece) * E;
-    for (uint32_t i = first; i < end; i += kRun) {
-        uint32_t key[kRun];
-        Piece<TA, E> in[kRun];
+    auto held_by = [&](int slot, int g) {
+        Columns<E, U> c;
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) {
-            key[j] = a.limit;
-            in[j].zero();
-            if (i + j < end) {
-                key[j] = a.keys[i + j];
-                if (key[j] < a.limit) in[j].load(dy + a.items[i + j] * a.dy_stride);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e) c.v[u][e] = held[slot][u * E + e][threadIdx.x + (g - group) * lanes];
+        return c;
+    };
+    if (from < to) {
+        uint32_t run = key[from + 1];
+        bool came_in = key[from] == run;
+        const TA* dy = static_cast<const TA*>(a.dy);
+        for (int i = from; i < to; i += kRun) {
+            Piece<TA, E> in[kRun][U];
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) {
+                const bool live = i + j < to && key[i + j + 1] < a.limit;
+                const TA* row = dy + (live ? item[i + j] : 0) * a.dy_stride;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int p = piece + u * lanes;
+                    in[j][u].zero();
+                    if (live && p < a.shape.pieces) in[j][u].load(row + static_cast<int64_t>(p) * E);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) {
+                if (i + j >= to) break;
+                const uint32_t k = key[i + j + 1];
+                if (k != run) {
+                    if (came_in) {
+                        hold(0);
+                        left |= kHead;
+                    } else if (run < a.limit) {
+                        put_row<TG, E, U>(a, run, piece, sum);
+                    }
+                    run = k;
+                    came_in = false;
+                    sum.clear();
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[E];
+                    in[j][u].unpack(f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sum.v[u][e] += f[e];
+                }
             }
         }
-#pragma unroll
-        for (int j = 0; j < kRun; ++j) {
-            if (i + j >= end) break;
-            if (key[j] != run) {
-                flush(false);
-                run = key[j];
-                came_in = false;
-#pragma unroll
-                for (int e = 0; e < E; ++e) sum[e] = 0.f;
-            }
-            float f[E];
-            in[j].unpack(f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) sum[e] += f[e];
+        const bool goes_on = key[to + 1] == run;
+        if (came_in) {
+            hold(0);
+            left |= goes_on ? kHead | kThrough : kHead;
+        } else if (goes_on) {
+            hold(1);
+            left |= kTail;
+        } else if (run < a.limit) {
+            put_row<TG, E, U>(a, run, piece, sum);
         }
     }
-    flush(behind == run);
+    if ((threadIdx.x & (lanes - 1)) == 0) state[group] = static_cast<unsigned char>(left);
+    __syncthreads();
+    // A run over several groups is joined, in order, by the group where it begins, and
+    // the one that came into the block by the first group.
+    auto join = [&](int slot, bool came_in, bool goes_on) {
+        const uint32_t run = key[slot == 0 ? from + 1 : to];
+        if (run >= a.limit) return;
+        Columns<E, U> all = held_by(slot, group);
+        for (int g = group + 1; goes_on && g < groups; ++g) {
+            if (!(state[g] & kHead)) break;  // behind the last token
+            all.add(held_by(0, g));
+            goes_on = (state[g] & kThrough) != 0;
+        }
+        if (came_in) put_partial<E, U>(a, span, 0, piece, all);
+        else if (goes_on) put_partial<E, U>(a, span, 1, piece, all);
+        else put_row<TG, E, U>(a, run, piece, all);
+    };
+    if (group == 0 && (left & kHead)) join(0, true, (left & kThrough) != 0);
+    if (left & kTail) join(1, false, true);
 }
 
-// Zeroes rows without a token: a warp takes a few rows' columns.
-template <typename TG, int E>
-__device__ __forceinline__ void zero_unit(const BwdKernelArgs& a, int64_t unit) {
+// Zeroes rows without a token: a warp takes a few rows, or a part of a long one.
+template <typename TG>
+__device__ __forceinline__ void zero_unit(const BwdKernelArgs& a, int64_t width, int64_t unit) {
     const int lane = threadIdx.x % 32;
     const int64_t part = unit / a.zero_slices;
     const int slice = static_cast<int>(unit - part * a.zero_slices);
-    const int64_t row0 = part * a.zero_rows;
-    const int rows = static_cast<int>(min(static_cast<int64_t>(a.zero_rows), a.rows - row0));
-    const bool absent = lane < rows && a.present[row0 + lane] == 0;
-    unsigned todo = __ballot_sync(0xffffffffu, absent);
-    const int from = slice * a.zero_pieces, to = min(from + a.zero_pieces, a.shape.pieces);
-    Piece<TG, E> z;
-    z.zero();
+    const int64_t row0 = a.zero_from + part * a.zero_rows;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(a.zero_rows), a.zero_to - row0));
+    unsigned todo = __ballot_sync(0xffffffffu, lane < rows && a.present[row0 + lane] == 0);
+    const int64_t row_bytes = width * static_cast<int>(sizeof(TG));
+    const int64_t from = static_cast<int64_t>(slice) * kZeroBytes;
     while (todo) {
         const int r = __ffs(todo) - 1;
         todo &= todo - 1;
-        TG* row = static_cast<TG*>(a.grad) + (row0 + r) * a.grad_stride;
-        for (int p = from + lane; p < to; p += 32)
-            if (RMSN_OK(span_in(row + static_cast<int64_t>(p) * E, E * sizeof(TG), a.grad,
-                                rows_bytes(a.rows, a.grad_stride, static_cast<int64_t>(a.shape.pieces) * E, sizeof(TG))),
-                        a.status))
-                z.store(row + static_cast<int64_t>(p) * E);
+        char* row = reinterpret_cast<char*>(static_cast<TG*>(a.grad) + (row0 + r) * a.grad_stride);
+        zero_span(row + from, min(static_cast<int64_t>(kZeroBytes), row_bytes - from), lane, 32, a.grad,
+                  rows_bytes(a.rows, a.grad_stride, width, sizeof(TG)), a.status);
     }
 }
+template <typename TG, int E>
+__device__ __forceinline__ void zero_share(const BwdKernelArgs& a) {
+    const int64_t unit = static_cast<int64_t>(blockIdx.x - a.sum_blocks) * (kThreads / 32) + threadIdx.x / 32;
+    if (unit < ceil_div(a.zero_to - a.zero_from, a.zero_rows) * a.zero_slices)
+        zero_unit<TG>(a, static_cast<int64_t>(a.shape.pieces) * E, unit);
+}
 
-template <typename TA, typename TG, int E>
+template <typename TA, typename TG, int E, int U>
 __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_constant__ BwdKernelArgs a) {
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    if (blockIdx.x < a.sum_blocks) {
-        const unsigned group = group_index<kThreads>(a.shape.lanes);
-        const unsigned segment = group / a.shape.chunks;
-        const int piece = (group - segment * a.shape.chunks) * a.shape.lanes + (threadIdx.x & (a.shape.lanes - 1));
-        if (segment < a.segments && piece < a.shape.pieces) add_segment<TA, TG, E>(a, segment, piece);
-    } else {
-        const int64_t unit =
-            static_cast<int64_t>(blockIdx.x - a.sum_blocks) * (kThreads / 32) + threadIdx.x / 32;
-        if (unit < a.zero_units) zero_unit<TG, E>(a, unit);
+    if (blockIdx.x >= a.sum_blocks) {
+        zero_share<TG, E>(a);
+        return;
     }
+    const unsigned span = blockIdx.x / a.shape.chunks;
+    add_tokens<TA, TG, E, U>(a, span, static_cast<int>(blockIdx.x - span * a.shape.chunks));
 }
 
-// Runs that cross segments: the group of the segment where one begins adds the
-// shares in order, in runs of 64.
-template <typename TG, int E>
+// Runs that cross blocks: the group that takes the span where one begins adds the
+// spans' shares in order, eight and eight.
+template <typename TG, int E, int U>
 __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ BwdKernelArgs a) {
     wait_for_prerequisite_grid();
     allow_dependent_launch();
+    if (blockIdx.x >= a.sum_blocks) {
+        zero_share<TG, E>(a);
+        return;
+    }
+    constexpr int kAhead = 8;
     const unsigned group = group_index<kThreads>(a.shape.lanes);
-    const unsigned segment = group / a.shape.chunks;
-    const int piece = (group - segment * a.shape.chunks) * a.shape.lanes + (threadIdx.x & (a.shape.lanes - 1));
-    if (segment >= a.segments || piece >= a.shape.pieces) return;
-    const uint32_t first = segment * static_cast<uint32_t>(a.segment);
-    const uint32_t end = min(first + a.segment, a.n);
-    if (end >= a.n) return;
-    const uint32_t run = a.keys[end - 1];
-    if (run >= a.limit || a.keys[end] != run) return;
-    if (first > 0 && a.keys[first] == run && a.keys[first - 1] == run) return;  // began before
-    // the last segment with a share: the last one that starts with this id
-    uint32_t last = segment + 1;
-    for (uint32_t other = a.segments; other - last > 1;) {
-        const uint32_t mid = last + (other - last) / 2;
-        if (a.keys[mid * static_cast<uint32_t>(a.segment)] == run) last = mid;
-        else other = mid;
-    }
-    float sum[E];
-    Piece<float, E> in;
-    in.load_plain(partial_at<E>(a, segment, 1, piece));
-    in.unpack(sum);
-    for (uint32_t s = segment + 1; s <= last;) {
-        const uint32_t stop = min(last + 1, s + 64);
-        float part[E] = {};
-#pragma unroll 8
-        for (; s < stop; ++s) {
-            float f[E];
-            in.load_plain(partial_at<E>(a, s, 0, piece));
-            in.unpack(f);
+    const unsigned span = group / a.shape.chunks;
+    const int piece = (group - span * a.shape.chunks) * (a.shape.lanes * U) + (threadIdx.x & (a.shape.lanes - 1));
+    if (span + 1 >= a.spans) return;
+    const uint32_t first = span * static_cast<uint32_t>(a.span), next = first + a.span;
+    const uint32_t run = a.keys[next - 1], behind = a.keys[next], begin = a.keys[first],
+                   before = first > 0 ? a.keys[first - 1] : 0xffffffffu;
+    if (run >= a.limit || behind != run || (begin == run && before == run)) return;  // ends here, or began before
+    Columns<E, U> sum;
+    auto load = [&](Columns<E, U>& c, unsigned s, int slot, bool live) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) part[e] += f[e];
+        for (int u = 0; u < U; ++u) {
+            const int p = piece + u * a.shape.lanes;
+            Piece<float, E> in;
+            in.zero();
+            if (live && p < a.shape.pieces) in.load_plain(partial_at<E>(a, s, slot, p));
+            in.unpack(c.v[u]);
         }
+    };
+    load(sum, span, 1, true);
+    bool on = true;
+    for (unsigned s = span + 1; on && s < a.spans; s += kAhead) {
+        // a span has a share where it starts with this id; what others hold is not used
+        bool live[kAhead];
+        Columns<E, U> in[kAhead], eight;
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum[e] += part[e];
+        for (int j = 0; j < kAhead; ++j) {
+            const bool there = s + j < a.spans;
+            load(in[j], s + j, 0, there);
+            live[j] = there && a.keys[(s + j) * static_cast<uint32_t>(a.span)] == run;
+        }
+        eight.clear();
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (live[j]) eight.add(in[j]);
+            on = live[j];
+        }
+        sum.add(eight);
     }
-    put_row<TG, E>(a, run, piece, sum);
+    put_row<TG, E, U>(a, run, piece, sum);
 }
 
-// Widest piece (elements) of rows of `width` of two types.
+// Widest piece (elements) of rows of `width` of two types: 16 bytes of the wider one,
+// so that a group's accesses are dense in both.
 int piece_of(const void* p, int64_t ps, int size_p, const void* q, int64_t qs, int size_q, int width) {
     for (int e : {8, 4, 2}) {
-        if (e * (size_p < size_q ? size_p : size_q) > 16 || width % e) continue;
+        if (e * std::max(size_p, size_q) > 16 || width % e) continue;
         if (piece_fits(p, ps, size_p, e) && piece_fits(q, qs, size_q, e)) return e;
     }
     return 1;
@@ -273,7 +383,7 @@ int piece_of(const void* p, int64_t ps, int size_p, const void* q, int64_t qs, i
 template <typename TT, typename TA>
 cudaError_t fwd_typed(int e, const FwdKernelArgs& a, int64_t blocks, cudaStream_t s) {
     auto go = [&](auto fn) { return launch_pdl(fn, static_cast<int>(blocks), kThreads, 0, 1, s, a); };
-    if constexpr (sizeof(TA) == 2) {
+    if constexpr (sizeof(TT) == 2) {
         if (e == 8) return go(embedding_fwd_kernel<TT, TA, 8>);
     }
     if (e == 4) return go(embedding_fwd_kernel<TT, TA, 4>);
@@ -281,31 +391,59 @@ cudaError_t fwd_typed(int e, const FwdKernelArgs& a, int64_t blocks, cudaStream_
     return go(embedding_fwd_kernel<TT, TA, 1>);
 }
 
-template <typename TA, typename TG, int E>
-cudaError_t bwd_launches(const BwdKernelArgs& a, int64_t sum_blocks, int64_t zero_blocks, cudaStream_t s) {
-    cudaError_t err = launch_pdl(embedding_sum_kernel<TA, TG, E>, static_cast<int>(sum_blocks + zero_blocks), kThreads,
-                                 0, 1, s, a);
-    if (err != cudaSuccess || a.segments < 2) return err;
-    return launch_pdl(embedding_join_kernel<TG, E>, static_cast<int>(sum_blocks), kThreads, 0, 1, s, a);
-}
-template <typename TA, typename TG>
-cudaError_t bwd_typed(int e, const BwdKernelArgs& a, int64_t sum_blocks, int64_t zero_blocks, cudaStream_t s) {
-    if constexpr (sizeof(TA) == 2) {
-        if (e == 8) return bwd_launches<TA, TG, 8>(a, sum_blocks, zero_blocks, s);
-    }
-    if (e == 4) return bwd_launches<TA, TG, 4>(a, sum_blocks, zero_blocks, s);
-    if (e == 2) return bwd_launches<TA, TG, 2>(a, sum_blocks, zero_blocks, s);
-    return bwd_launches<TA, TG, 1>(a, sum_blocks, zero_blocks, s);
+// Rows that each of the three launches zeroes: the last ones beside the sort, the
+// first ones beside the join, the others beside the sums.
+struct ZeroShares {
+    int64_t sort, join;
+};
+constexpr int64_t kZeroBesideSort = 48 << 20, kZeroBesideJoin = 16 << 20;  // bytes
+
+int64_t zero_blocks(const BwdKernelArgs& a) {
+    return cdiv(cdiv(a.zero_to - a.zero_from, a.zero_rows) * a.zero_slices, kThreads / 32);
 }
 
-// Tokens of a segment: as many as 32, but groups enough for every SM to have
-// some 32 warps.
+template <typename TA, typename TG, int E>
+cudaError_t bwd_launches(BwdKernelArgs a, int64_t width, const ZeroShares& z, cudaStream_t s) {
+    constexpr int U = E >= 4 ? 1 : 4 / E;
+    a.shape = row_shape(static_cast<int>(width / E), U);
+    a.segment = std::min(a.segment, kMaxSpan * a.shape.lanes / kThreads);
+    a.span = a.segment * (kThreads / a.shape.lanes);
+    a.spans = static_cast<unsigned>(cdiv(a.n, a.span));
+    a.sum_blocks = a.spans * a.shape.chunks;
+    const bool join = a.spans > 1;
+    if (!a.accumulate) {
+        a.zero_from = join ? z.join : 0;
+        a.zero_to = a.rows - z.sort;
+    }
+    cudaError_t err = launch_pdl(embedding_sum_kernel<TA, TG, E, U>, static_cast<int>(a.sum_blocks + zero_blocks(a)),
+                                 kThreads, (a.span * 2 + 2) * 4, 1, s, a);
+    if (err != cudaSuccess || !join) return err;
+    a.zero_to = a.zero_from;
+    a.zero_from = 0;
+    a.sum_blocks = static_cast<unsigned>(cdiv(static_cast<int64_t>(a.spans) * a.shape.chunks * a.shape.lanes, kThreads));
+    return launch_pdl(embedding_join_kernel<TG, E, U>, static_cast<int>(a.sum_blocks + zero_blocks(a)), kThreads, 0, 1,
+                      s, a);
+}
+template <typename TA, typename TG>
+cudaError_t bwd_typed(int e, const BwdKernelArgs& a, int64_t width, const ZeroShares& z, cudaStream_t s) {
+    if constexpr (sizeof(TG) == 2) {
+        if (e == 8) return bwd_launches<TA, TG, 8>(a, width, z, s);
+    }
+    if (e == 4) return bwd_launches<TA, TG, 4>(a, width, z, s);
+    if (e == 2) return bwd_launches<TA, TG, 2>(a, width, z, s);
+    return bwd_launches<TA, TG, 1>(a, width, z, s);
+}
+
+// Tokens of a group: as many as 32, but groups enough for every SM to have
+// some 32 warps. A block's: kMaxSpan at most.
 constexpr int kMaxSegment = 32, kMinSegment = 8;
 int segment_of(int64_t n, int64_t width) {
     int seg = kMaxSegment;
     while (seg > kMinSegment && cdiv(n, seg) * cdiv(width, 256) < 152 * 32) seg /= 2;
     return seg;
 }
+// A block takes at least kMinSegment tokens a warp.
+int64_t most_spans(int64_t n) { return cdiv(n, kMinSegment * (kThreads / 32)); }
 
 struct BwdLayout {
     size_t keys[2], items[2], present, counts, partial, bytes;
@@ -320,13 +458,13 @@ struct BwdLayout {
         for (int i = 0; i < 2; ++i) items[i] = take(n * 4);
         present = take(rows);
         counts = take(sort_counts_words(n, sort_max_bins(rows)) * 4);
-        partial = take(static_cast<size_t>(cdiv(n, segment_of(n, width))) * 2 * width * 4);
+        partial = take(static_cast<size_t>(most_spans(n)) * 2 * width * 4);
         bytes = at;
     }
 };
 
 int64_t fwd_blocks(const EmbeddingArgs& a, int e, RowShape* shape) {
-    *shape = row_shape(a.width / e, kFwdPieces);
+    *shape = row_shape(a.width / e, fwd_pieces(e));
     return cdiv(static_cast<int64_t>(a.k.n) * shape->chunks * shape->lanes, kThreads);
 }
 
@@ -334,7 +472,7 @@ int64_t fwd_blocks(const EmbeddingArgs& a, int e, RowShape* shape) {
 
 bool embedding_fits(int64_t n, int64_t width) {
     // element by element, which takes the most groups; they are counted in 32 bits
-    return n * cdiv(width, 32 * kFwdPieces) <= kMaxGrid && cdiv(n, kMinSegment) * cdiv(width, 32) <= kMaxGrid;
+    return n * cdiv(width, 32 * fwd_pieces(1)) <= kMaxGrid && most_spans(n) * cdiv(width, 128) <= kMaxGrid / 2;
 }
 
 cudaError_t embedding_fwd_launch(const DeviceInfo&, int dtype, const EmbeddingArgs& in, cudaStream_t s) {
@@ -370,6 +508,17 @@ cudaError_t embedding_bwd_launch(const DeviceInfo& dev, int dtype, const Embeddi
     b.present = accumulate ? nullptr : ws + l.present;
     b.counts = reinterpret_cast<uint32_t*>(ws + l.counts);
     b.status = in.status;
+    const int64_t row_bytes = static_cast<int64_t>(in.width) * sg, stride_bytes = in.dst_stride * sg;
+    ZeroShares z{};
+    if (!accumulate) {
+        if (sort_takes_zero_job(n)) {
+            z.sort = std::min(in.rows, cdiv(kZeroBesideSort, row_bytes));
+            char* at = static_cast<char*>(in.dst) + (in.rows - z.sort) * stride_bytes;
+            b.zero = stride_bytes == row_bytes ? ZeroJob{at, z.sort * row_bytes, 0, 1}
+                                               : ZeroJob{at, row_bytes, stride_bytes, z.sort};
+        }
+        z.join = std::min(in.rows - z.sort, kZeroBesideJoin / row_bytes);
+    }
     const cudaError_t err = sort_launch(dev, in.k, b, s);
     if (err != cudaSuccess) return err;
     const int result = sort_result(sort_passes(in.k.limit));
@@ -385,32 +534,19 @@ cudaError_t embedding_bwd_launch(const DeviceInfo& dev, int dtype, const Embeddi
     a.rows = in.rows;
     a.n = in.k.n;
     a.limit = static_cast<uint32_t>(in.k.limit);
-    a.shape = row_shape(in.width / e, 1);
     a.segment = segment_of(n, in.width);
-    a.segments = static_cast<unsigned>(cdiv(n, a.segment));
     a.accumulate = accumulate;
     a.scale = in.scale;
     a.status = in.status;
-    const int64_t sum_blocks =
-        cdiv(static_cast<int64_t>(a.segments) * a.shape.chunks * a.shape.lanes, kThreads);
-    a.sum_blocks = static_cast<unsigned>(sum_blocks);
-    int64_t zero_blocks = 0;
-    if (!accumulate) {
-        // some 16 KB a warp: a few rows, or a part of a long one
-        const int64_t row_bytes = static_cast<int64_t>(in.width) * sg;
-        a.zero_rows = static_cast<int>(row_bytes >= kZeroBytes ? 1 : std::min<int64_t>(32, kZeroBytes / row_bytes));
-        a.zero_pieces = a.zero_rows > 1 ? a.shape.pieces : kZeroBytes / (e * sg);
-        a.zero_slices = static_cast<int>(cdiv(a.shape.pieces, a.zero_pieces));
-        a.zero_units = cdiv(in.rows, a.zero_rows) * a.zero_slices;
-        zero_blocks = cdiv(a.zero_units, kThreads / 32);
-    }
-    if (sum_blocks + zero_blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
+    // some 16 KB a warp: a few rows, or a part of a long one
+    a.zero_rows = static_cast<int>(row_bytes >= kZeroBytes ? 1 : std::min<int64_t>(32, kZeroBytes / row_bytes));
+    a.zero_slices = static_cast<int>(cdiv(row_bytes, kZeroBytes));
     switch (dtype) {
-        case RMSNORM_F32: return bwd_typed<float, float>(e, a, sum_blocks, zero_blocks, s);
-        case RMSNORM_BF16: return bwd_typed<__nv_bfloat16, __nv_bfloat16>(e, a, sum_blocks, zero_blocks, s);
-        case RMSNORM_F16: return bwd_typed<__half, __half>(e, a, sum_blocks, zero_blocks, s);
-        case RMSNORM_BF16_W_F32: return bwd_typed<__nv_bfloat16, float>(e, a, sum_blocks, zero_blocks, s);
-        default: return bwd_typed<__half, float>(e, a, sum_blocks, zero_blocks, s);
+        case RMSNORM_F32: return bwd_typed<float, float>(e, a, in.width, z, s);
+        case RMSNORM_BF16: return bwd_typed<__nv_bfloat16, __nv_bfloat16>(e, a, in.width, z, s);
+        case RMSNORM_F16: return bwd_typed<__half, __half>(e, a, in.width, z, s);
+        case RMSNORM_BF16_W_F32: return bwd_typed<__nv_bfloat16, float>(e, a, in.width, z, s);
+        default: return bwd_typed<__half, float>(e, a, in.width, z, s);
     }
 }
 

@@ -10,8 +10,8 @@
 // One to three operations a byte: bytes bound all three. The positions are
 // what a row's loads wait for, so a thread has the pieces of several choices in
 // flight. Sums are fp32 in the choices' order; a result is rounded once.
-// Rows of the sorted order without a choice are zeroed by blocks behind the
-// others, by `source`.
+// Rows of the sorted order without a choice are zeroed by the first blocks, by
+// `source` (by the last ones they were the tail of the call).
 #include <algorithm>
 
 #include "rows.cuh"
@@ -20,53 +20,48 @@ namespace rmsn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kScatterPieces = 4;  // of a lane
-constexpr int kGatherPieces = 2;
+// Pieces of a lane: small ones need more of them in flight.
+__host__ __device__ constexpr int scatter_pieces(int e) { return e >= 4 ? 4 : 8; }
+__host__ __device__ constexpr int gather_pieces(int e) { return e >= 4 ? 2 : 8 / e; }
+__host__ __device__ constexpr int bwd_pieces(int e) { return e >= 4 ? 2 : 4; }
 constexpr int kChoices = 4;     // in flight
-constexpr int kBwdPieces = 2;
 constexpr int kBwdChoices = 8;  // dots a thread holds
-constexpr int kZeroRows = 32;   // of a warp
+constexpr int kZeroRows = 64;   // of a block
 
 struct KernelArgs {
     ExpertArgs x;
     RowShape shape;
-    unsigned token_blocks;  // the others zero rows without a choice
+    unsigned zero_blocks;  // the first ones, which zero rows without a choice
     int team;               // threads of a token (gather_bwd)
 };
 
-// Rows without a choice, 32 a warp.
-template <typename T, int E>
-__device__ __forceinline__ void zero_rows(const KernelArgs& a) {
+// Rows without a choice, of kZeroRows: the whole block zeroes one after another.
+__device__ __forceinline__ void zero_rows(const KernelArgs& a, int size) {
     const ExpertArgs& x = a.x;
     const int lane = threadIdx.x % 32;
-    const int64_t row0 =
-        (static_cast<int64_t>(blockIdx.x - a.token_blocks) * (kThreads / 32) + threadIdx.x / 32) * kZeroRows;
-    const int64_t row = row0 + lane;
-    unsigned todo = __ballot_sync(0xffffffffu, row < x.rows && x.source[row] < 0);
-    Piece<T, E> z;
-    z.zero();
-    while (todo) {
-        const int r = __ffs(todo) - 1;
-        todo &= todo - 1;
-        T* to = static_cast<T*>(x.out) + (row0 + r) * x.out_stride;
-        for (int p = lane; p < a.shape.pieces; p += 32)
-            if (RMSN_OK(span_in(to + static_cast<int64_t>(p) * E, E * sizeof(T), x.out,
-                                rows_bytes(x.rows, x.out_stride, x.width, sizeof(T))),
-                        x.status))
-                z.store(to + static_cast<int64_t>(p) * E);
+    for (int half = 0; half < kZeroRows; half += 32) {
+        const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kZeroRows + half;
+        unsigned todo = __ballot_sync(0xffffffffu, row0 + lane < x.rows && x.source[row0 + lane] < 0);
+        while (todo) {
+            const int r = __ffs(todo) - 1;
+            todo &= todo - 1;
+            zero_span(static_cast<char*>(x.out) + (row0 + r) * x.out_stride * size, static_cast<int64_t>(x.width) * size,
+                      threadIdx.x, kThreads, x.out, rows_bytes(x.rows, x.out_stride, x.width, size), x.status);
+        }
     }
 }
 
 template <typename T, int E>
 __global__ void __launch_bounds__(kThreads) expert_scatter_kernel(const __grid_constant__ KernelArgs a) {
+    constexpr int kScatterPieces = scatter_pieces(E);
     const ExpertArgs& x = a.x;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    if (blockIdx.x >= a.token_blocks) {
-        zero_rows<T, E>(a);
+    if (blockIdx.x < a.zero_blocks) {
+        zero_rows(a, sizeof(T));
         return;
     }
-    const unsigned group = group_index<kThreads>(a.shape.lanes);
+    const unsigned group = group_index<kThreads>(a.shape.lanes, a.zero_blocks);
     const unsigned token = group / a.shape.chunks;
     if (token >= x.tokens) return;
     const int first =
@@ -98,10 +93,11 @@ __global__ void __launch_bounds__(kThreads) expert_scatter_kernel(const __grid_c
 
 template <typename T, typename TW, int E>
 __global__ void __launch_bounds__(kThreads) expert_gather_kernel(const __grid_constant__ KernelArgs a) {
+    constexpr int kGatherPieces = gather_pieces(E);
     const ExpertArgs& x = a.x;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    const unsigned group = group_index<kThreads>(a.shape.lanes);
+    const unsigned group = group_index<kThreads>(a.shape.lanes, a.zero_blocks);
     const unsigned token = group / a.shape.chunks;
     if (token >= x.tokens) return;
     const int first =
@@ -164,16 +160,17 @@ __global__ void __launch_bounds__(kThreads) expert_gather_kernel(const __grid_co
 // A team of threads (a power of two, 4 to 256) takes a token and all its columns.
 template <typename T, typename TW, int E>
 __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __grid_constant__ KernelArgs a) {
+    constexpr int kBwdPieces = bwd_pieces(E);
     __shared__ float part[kThreads / 32][kBwdChoices];
     const ExpertArgs& x = a.x;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    if (blockIdx.x >= a.token_blocks) {
-        zero_rows<T, E>(a);
+    if (blockIdx.x < a.zero_blocks) {
+        zero_rows(a, sizeof(T));
         return;
     }
     const int team = a.team, lane = threadIdx.x & (team - 1);
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * (kThreads / team) + threadIdx.x / team;
+    const int64_t token = static_cast<int64_t>(blockIdx.x - a.zero_blocks) * (kThreads / team) + threadIdx.x / team;
     const bool live = token < x.tokens;  // the others keep the barriers company
     const T* dy = static_cast<const T*>(x.x) + token * x.x_stride;
     const int32_t* pos = x.position + token * x.choices;
@@ -270,7 +267,7 @@ int piece_of(const ExpertArgs& a, int dtype) {
     return 1;
 }
 
-int64_t zero_blocks(const ExpertArgs& a) { return cdiv(a.rows, kZeroRows * (kThreads / 32)); }
+unsigned zero_blocks(const ExpertArgs& a) { return static_cast<unsigned>(cdiv(a.rows, kZeroRows)); }
 
 // fn(E) for the piece's width
 template <typename T, typename F>
@@ -297,15 +294,15 @@ cudaError_t with_types(int dtype, F fn) {
 }  // namespace
 
 bool experts_fit(const ExpertArgs& a) {
-    return a.tokens * cdiv(a.width, 32 * kGatherPieces) <= kMaxGrid;  // groups, element by element
+    return a.tokens * cdiv(a.width, 32 * gather_pieces(1)) <= kMaxGrid;  // groups, element by element
 }
 
 cudaError_t expert_scatter_launch(const DeviceInfo&, int dtype, const ExpertArgs& in, cudaStream_t s) {
     KernelArgs a{in, {}, 0, 0};
     const int e = piece_of(in, dtype);
-    a.shape = row_shape(in.width / e, kScatterPieces);
-    a.token_blocks = static_cast<unsigned>(cdiv(in.tokens * a.shape.chunks * a.shape.lanes, kThreads));
-    const int grid = static_cast<int>(a.token_blocks + zero_blocks(in));
+    a.shape = row_shape(in.width / e, scatter_pieces(e));
+    a.zero_blocks = zero_blocks(in);
+    const int grid = static_cast<int>(a.zero_blocks + cdiv(in.tokens * a.shape.chunks * a.shape.lanes, kThreads));
     auto go = [&](auto t) {
         using T = decltype(t);
         return with_piece<T>(e, [&](auto n) {
@@ -319,7 +316,7 @@ cudaError_t expert_scatter_launch(const DeviceInfo&, int dtype, const ExpertArgs
 cudaError_t expert_gather_launch(const DeviceInfo&, int dtype, const ExpertArgs& in, cudaStream_t s) {
     KernelArgs a{in, {}, 0, 0};
     const int e = piece_of(in, dtype);
-    a.shape = row_shape(in.width / e, kGatherPieces);
+    a.shape = row_shape(in.width / e, gather_pieces(e));
     const int grid = static_cast<int>(cdiv(in.tokens * a.shape.chunks * a.shape.lanes, kThreads));
     return with_types(dtype, [&](auto t, auto w) {
         using T = decltype(t);
@@ -332,11 +329,11 @@ cudaError_t expert_gather_launch(const DeviceInfo&, int dtype, const ExpertArgs&
 cudaError_t expert_gather_bwd_launch(const DeviceInfo&, int dtype, const ExpertArgs& in, cudaStream_t s) {
     KernelArgs a{in, {}, 0, 0};
     const int e = piece_of(in, dtype);
-    a.shape = row_shape(in.width / e, kBwdPieces);
+    a.shape = row_shape(in.width / e, bwd_pieces(e));
     a.team = 4;
-    while (a.team < kThreads && a.team * kBwdPieces < a.shape.pieces) a.team *= 2;
-    a.token_blocks = static_cast<unsigned>(cdiv(in.tokens, kThreads / a.team));
-    const int grid = static_cast<int>(a.token_blocks + zero_blocks(in));
+    while (a.team < kThreads && a.team * bwd_pieces(e) < a.shape.pieces) a.team *= 2;
+    a.zero_blocks = zero_blocks(in);
+    const int grid = static_cast<int>(a.zero_blocks + cdiv(in.tokens, kThreads / a.team));
     return with_types(dtype, [&](auto t, auto w) {
         using T = decltype(t);
         return with_piece<T>(e, [&](auto n) {

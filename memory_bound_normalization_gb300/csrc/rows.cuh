@@ -8,6 +8,8 @@
 
 namespace rmsn {
 
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 template <int BYTES>
 struct Word;
 template <>
@@ -99,10 +101,24 @@ __device__ __forceinline__ int64_t rows_bytes(int64_t n, int64_t stride, int64_t
     return ((n - 1) * stride + width) * size;
 }
 
-// The group of lanes a thread of a block of THREADS belongs to, over the grid.
+// Zeroes `bytes` bytes from p (aligned to 2) by `threads` threads: 16 bytes a store
+// between the first and the last boundary.
+__device__ __forceinline__ void zero_span(char* p, int64_t bytes, int thread, int threads, const void* base,
+                                          int64_t extent, int* status) {
+    if (!RMSN_OK(span_in(p, bytes, base, extent), status)) return;
+    const int64_t head = min(static_cast<int64_t>(-reinterpret_cast<uintptr_t>(p) & 15), bytes);
+    const int64_t words = (bytes - head) / 16, tail = head + words * 16;
+    for (int64_t i = 2 * thread; i < head; i += 2 * threads) *reinterpret_cast<uint16_t*>(p + i) = 0;
+    for (int64_t i = thread; i < words; i += threads)
+        *reinterpret_cast<uint4*>(p + head + i * 16) = make_uint4(0, 0, 0, 0);
+    for (int64_t i = tail + 2 * thread; i < bytes; i += 2 * threads) *reinterpret_cast<uint16_t*>(p + i) = 0;
+}
+
+// The group of lanes a thread of a block of THREADS belongs to, counted over the grid
+// from its first_block on.
 template <int THREADS>
-__device__ __forceinline__ unsigned group_index(int lanes) {
-    return blockIdx.x * (THREADS / lanes) + threadIdx.x / lanes;
+__device__ __forceinline__ unsigned group_index(int lanes, unsigned first_block = 0) {
+    return (blockIdx.x - first_block) * (THREADS / lanes) + threadIdx.x / lanes;
 }
 
 // ------------------------------------------------------------ host geometry

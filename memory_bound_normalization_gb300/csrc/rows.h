@@ -22,6 +22,12 @@ struct KeySource {
     int ids_64;
 };
 
+// Rows to be zeroed, of any alignment: `rows` rows of `bytes`, `stride` apart.
+struct ZeroJob {
+    char* at;
+    int64_t bytes, stride, rows;
+};
+
 // Stable order of the keys by radix passes: sorted keys and the items they
 // came from. `present`, unless null: limit bytes, 1 where the key occurs.
 struct SortBuffers {
@@ -29,8 +35,11 @@ struct SortBuffers {
     int32_t* items[2];
     uint8_t* present;
     uint32_t* counts;  // sort_counts_words(n, bins) words, null if that is 0
+    ZeroJob zero;      // done on the SMs that a sort by one cluster leaves idle
     int* status;
 };
+// Whether a sort of n keys is one launch, which takes a zero job along.
+bool sort_takes_zero_job(int64_t n);
 int sort_passes(int64_t limit);
 // Words of counts for n items: 0 where one cluster of blocks takes them all.
 int64_t sort_counts_words(int64_t n, int bins);

@@ -24,8 +24,8 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMaxRounds = 16;
-constexpr int kMaxCluster8 = 8;
-constexpr int64_t kClusterItems = kThreads * kMaxRounds * kMaxCluster8;
+constexpr int kCluster = 8;
+constexpr int64_t kClusterItems = kThreads * kMaxRounds * kCluster;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxExperts = RMSNORM_MAX_EXPERTS;
 
@@ -43,6 +43,7 @@ struct SortArgs {
     int32_t* offsets;
     int32_t* expert_counts;
     int experts, rows, align;
+    ZeroJob zero;
     int* status;
 };
 
@@ -221,18 +222,31 @@ __device__ __forceinline__ int clear_counts(const SortArgs& a, const Smem& s, un
     for (int i = threadIdx.x; i < warps * bins_stride(a.bins) / 2; i += blockDim.x) z[i] = 0;
     return warps;
 }
-// Counts of the warps become sums over the warps before; the block's counts.
+// Counts of the warps become sums over the warps before; the block's counts. The
+// counts are read together: one trip to shared memory instead of one a warp.
 __device__ __forceinline__ void sum_warps(const SortArgs& a, const Smem& s, int warps) {
     const int stride = bins_stride(a.bins);
     for (int d = threadIdx.x; d < a.bins; d += blockDim.x) {
-        uint32_t sum = 0;
-#pragma unroll 8
-        for (int w = 0; w < warps; ++w) {
-            const uint32_t c = s.cnt[w * stride + d];
-            s.cnt[w * stride + d] = static_cast<uint16_t>(sum);
-            sum += c;
+        uint32_t c[kThreads / 32], sum = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) c[w] = w < warps ? s.cnt[w * stride + d] : 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warps) s.cnt[w * stride + d] = static_cast<uint16_t>(sum);
+            sum += c[w];
         }
         s.hist[d] = sum;
+    }
+}
+
+// Rows that are zeroed beside the sort, by block `block` of `blocks`.
+constexpr int64_t kZeroUnit = 32768;  // bytes
+__device__ __forceinline__ void zero_beside(const SortArgs& a, unsigned block, unsigned blocks) {
+    const int64_t slices = ceil_div(a.zero.bytes, kZeroUnit);
+    for (int64_t unit = block; unit < slices * a.zero.rows; unit += blocks) {
+        const int64_t row = unit / slices, from = (unit - row * slices) * kZeroUnit;
+        zero_span(a.zero.at + row * a.zero.stride + from, min(kZeroUnit, a.zero.bytes - from), threadIdx.x, blockDim.x,
+                  a.zero.at, (a.zero.rows - 1) * a.zero.stride + a.zero.bytes, a.status);
     }
 }
 
@@ -246,6 +260,10 @@ __global__ void __launch_bounds__(kThreads) sort_cluster_kernel(const __grid_con
     uint16_t* cnt = s.cnt + warp * bins_stride(a.bins);
     wait_for_prerequisite_grid();
     allow_dependent_launch();
+    if (blockIdx.x >= blocks) {  // not of the first cluster
+        zero_beside(a, blockIdx.x - blocks, gridDim.x - blocks);
+        return;
+    }
     clear_present(a, rank, blocks);
     for (int pass = 0; pass < a.passes; ++pass) {
         uint32_t key[R], place[R];
@@ -259,14 +277,16 @@ __global__ void __launch_bounds__(kThreads) sort_cluster_kernel(const __grid_con
         if (blocks > 1) {
             cluster_sync_all();
             if (threadIdx.x < a.bins) {
-                for (unsigned b = 0; b < blocks; ++b) {
-                    uint32_t v;
+                uint32_t v[kCluster];  // one trip for all
+#pragma unroll
+                for (int b = 0; b < kCluster; ++b)
                     asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                                 : "=r"(v)
-                                 : "r"(cluster_map(s.hist + threadIdx.x, b))
-                                 : "memory");
-                    total += v;
-                    if (b < rank) mine += v;
+                                 : "=r"(v[b])
+                                 : "r"(cluster_map(s.hist + threadIdx.x, b)));
+#pragma unroll
+                for (int b = 0; b < kCluster; ++b) {
+                    total += v[b];
+                    if (b < static_cast<int>(rank)) mine += v[b];
                 }
             }
         } else {
@@ -394,7 +414,7 @@ cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
     const int64_t n = a.k.n;
     if (n <= kClusterItems) {
         // one block while its items are few; then eight, a power of two of rounds
-        int blocks = n <= 4 * kThreads ? 1 : kMaxCluster8, rounds = 1;
+        int blocks = n <= 4 * kThreads ? 1 : kCluster, rounds = 1;
         while (static_cast<int64_t>(blocks) * kThreads * rounds < n) rounds *= 2;
         // no more threads than items or digits need
         const int digits = a.experts > 0 ? a.experts : a.bins;
@@ -403,7 +423,12 @@ cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
         const SortFn fn = kernel_for(0, rounds);
         const cudaError_t err = allow_smem(dev, fn);
         if (err != cudaSuccess) return err;
-        return launch_pdl(fn, blocks, threads, sort_smem(a.bins, threads / 32), blocks, s, a);
+        // blocks that zero rows: whole clusters, up to the SMs left
+        const int64_t units = a.zero.rows * cdiv(a.zero.bytes, kZeroUnit);
+        const int64_t idle =
+            std::min<int64_t>(cdiv(units, 2), (dev.sm_count - blocks) * (kThreads / threads)) / blocks * blocks;
+        const int zero = units > 0 ? static_cast<int>(std::max<int64_t>(idle, blocks)) : 0;
+        return launch_pdl(fn, blocks + zero, threads, sort_smem(a.bins, threads / 32), blocks, s, a);
     }
     const int rounds = many_rounds(n);
     a.blocks = static_cast<int>(cdiv(n, static_cast<int64_t>(kThreads) * rounds));
@@ -431,6 +456,8 @@ int64_t sort_counts_words(int64_t n, int bins) {
     return static_cast<int64_t>(bins) * (cdiv(n, static_cast<int64_t>(kThreads) * many_rounds(n)) + 1);
 }
 
+bool sort_takes_zero_job(int64_t n) { return n <= kClusterItems; }
+
 cudaError_t sort_launch(const DeviceInfo& dev, const KeySource& k, const SortBuffers& b, cudaStream_t s) {
     SortArgs a{};
     a.k = k;
@@ -439,6 +466,7 @@ cudaError_t sort_launch(const DeviceInfo& dev, const KeySource& k, const SortBuf
         a.items[i] = b.items[i];
     }
     a.present = b.present;
+    a.zero = b.zero;
     a.counts = b.counts;
     a.passes = sort_passes(k.limit);
     a.bits = static_cast<int>(cdiv(bits_of(k.limit), a.passes));
