@@ -174,7 +174,7 @@ constexpr int kThrough = 4;  // both: one run fills them (its sum is the head)
 template <typename TA, typename TG, int E, int U>
 __device__ __forceinline__ void add_tokens(const BwdKernelArgs& a, unsigned span, int slice) {
     __shared__ float held[2][U * E][kThreads];  // heads and tails, a column a thread
-    __shared__ unsigned char state[kThreads];
+    __shared__ bool state[kThreads];  // a group's: the scan's second part
     uint32_t* const key = reinterpret_cast<uint32_t*>(rmsn_dynamic_smem);  // [span + 2]: the token before, ours, the next
     int32_t* const item = reinterpret_cast<int32_t*>(key + a.span + 2);
     const int lanes = a.shape.lanes, group = threadIdx.x / lanes, groups = kThreads / lanes;
@@ -182,21 +182,34 @@ __device__ __forceinline__ void add_tokens(const BwdKernelArgs& a, unsigned span
     const uint32_t first = span * static_cast<uint32_t>(a.span);
     const int count = static_cast<int>(min(static_cast<uint32_t>(a.span), a.n - first));
     const uint32_t none = 0xffffffffu;
-    for (int i = threadIdx.x; i < count + 2; i += kThreads) {
-        const int64_t at = static_cast<int64_t>(first) + i - 1;
-        key[i] = at >= 0 && at < a.n ? a.keys[at] : none;
-        if (i < count) item[i] = a.items[first + i];
+    constexpr int kAhead = 4;  // of a thread's tokens, read together
+    for (int i0 = threadIdx.x; i0 < count + 2; i0 += kAhead * kThreads) {
+        uint32_t k[kAhead];
+        int32_t t[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kThreads;
+            const int64_t at = static_cast<int64_t>(first) + i - 1;
+            k[j] = i < count + 2 && at >= 0 && at < a.n ? a.keys[at] : none;
+            t[j] = i < count ? a.items[first + i] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kThreads;
+            if (i < count + 2) key[i] = k[j];
+            if (i < count) item[i] = t[j];
+        }
     }
     __syncthreads();
     const int from = group * a.segment, to = min(from + a.segment, count);
     Columns<E, U> sum;
     sum.clear();
     int left = 0;
-    auto hold = [&](int slot) {
+    auto put = [&](int slot, const Columns<E, U>& c) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < E; ++e) held[slot][u * E + e][threadIdx.x] = sum.v[u][e];
+            for (int e = 0; e < E; ++e) held[slot][u * E + e][threadIdx.x] = c.v[u][e];
     };
     auto held_by = [&](int slot, int g) {
         Columns<E, U> c;
@@ -229,7 +242,7 @@ __device__ __forceinline__ void add_tokens(const BwdKernelArgs& a, unsigned span
                 const uint32_t k = key[i + j + 1];
                 if (k != run) {
                     if (came_in) {
-                        hold(0);
+                        put(0, sum);
                         left |= kHead;
                     } else if (run < a.limit) {
                         put_row<TG, E, U>(a, run, piece, sum);
@@ -249,34 +262,57 @@ __device__ __forceinline__ void add_tokens(const BwdKernelArgs& a, unsigned span
         }
         const bool goes_on = key[to + 1] == run;
         if (came_in) {
-            hold(0);
+            put(0, sum);
             left |= goes_on ? kHead | kThrough : kHead;
         } else if (goes_on) {
-            hold(1);
+            put(1, sum);
             left |= kTail;
         } else if (run < a.limit) {
             put_row<TG, E, U>(a, run, piece, sum);
         }
     }
-    if ((threadIdx.x & (lanes - 1)) == 0) state[group] = static_cast<unsigned char>(left);
-    __syncthreads();
-    // A run over several groups is joined, in order, by the group where it begins, and
-    // the one that came into the block by the first group.
-    auto join = [&](int slot, bool came_in, bool goes_on) {
-        const uint32_t run = key[slot == 0 ? from + 1 : to];
-        if (run >= a.limit) return;
-        Columns<E, U> all = held_by(slot, group);
-        for (int g = group + 1; goes_on && g < groups; ++g) {
-            if (!(state[g] & kHead)) break;  // behind the last token
-            all.add(held_by(0, g));
-            goes_on = (state[g] & kThrough) != 0;
+    // A run over several groups belongs to the group where it begins (the one that came
+    // into the block, to the first), which needs the heads of the groups behind as far
+    // as the run goes: a scan from behind, sum and "goes on to the block's end".
+    Columns<E, U> heads;  // from this group on
+    bool on;
+    {
+        const int member = threadIdx.x & (lanes - 1);
+        heads.clear();
+        if (left & kHead) heads = held_by(0, group);
+        on = (left & kThrough) != 0;
+        if (member == 0) state[group] = on;
+        if (__syncthreads_or(on)) {
+            for (int d = 1; d < groups; d *= 2) {
+                const bool more = on && group + d < groups;
+                Columns<E, U> next;
+                bool next_on = on;
+                if (more) {
+                    next = held_by(0, group + d);
+                    next_on = state[group + d] != 0;
+                }
+                __syncthreads();
+                if (more) {
+                    heads.add(next);
+                    on = next_on;
+                    put(0, heads);
+                    if (member == 0) state[group] = on;
+                }
+                __syncthreads();
+            }
         }
-        if (came_in) put_partial<E, U>(a, span, 0, piece, all);
-        else if (goes_on) put_partial<E, U>(a, span, 1, piece, all);
-        else put_row<TG, E, U>(a, run, piece, all);
-    };
-    if (group == 0 && (left & kHead)) join(0, true, (left & kThrough) != 0);
-    if (left & kTail) join(1, false, true);
+    }
+    if (group == 0 && (left & kHead) && key[1] < a.limit) put_partial<E, U>(a, span, 0, piece, heads);
+    if ((left & kTail) && key[to] < a.limit) {
+        Columns<E, U> all = held_by(1, group);
+        bool goes_on = true;
+        if (group + 1 < groups) {
+            all.add(held_by(0, group + 1));
+            goes_on = state[group + 1] != 0;
+        }
+        if (goes_on) put_partial<E, U>(a, span, 1, piece, all);
+        else put_row<TG, E, U>(a, key[to], piece, all);
+    }
 }
 
 // Zeroes rows without a token: a warp takes a few rows, or a part of a long one.
@@ -306,7 +342,7 @@ __device__ __forceinline__ void zero_share(const BwdKernelArgs& a) {
 }
 
 template <typename TA, typename TG, int E, int U>
-__global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_constant__ BwdKernelArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) embedding_sum_kernel(const __grid_constant__ BwdKernelArgs a) {
     wait_for_prerequisite_grid();
     allow_dependent_launch();
     if (blockIdx.x >= a.sum_blocks) {
@@ -343,7 +379,7 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
             const int p = piece + u * a.shape.lanes;
             Piece<float, E> in;
             in.zero();
-            if (live && p < a.shape.pieces) in.load_plain(partial_at<E>(a, s, slot, p));
+            if (live && p < a.shape.pieces) in.load_now(partial_at<E>(a, s, slot, p));
             in.unpack(c.v[u]);
         }
     };
@@ -354,15 +390,18 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
         bool live[kAhead];
         Columns<E, U> in[kAhead], eight;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const bool there = s + j < a.spans;
-            load(in[j], s + j, 0, there);
-            live[j] = there && a.keys[(s + j) * static_cast<uint32_t>(a.span)] == run;
-        }
+        for (int j = 0; j < kAhead; ++j)
+            live[j] = s + j < a.spans && a.keys[(s + j) * static_cast<uint32_t>(a.span)] == run;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) load(in[j], s + j, 0, s + j < a.spans);
         eight.clear();
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            if (live[j]) eight.add(in[j]);
+            // selected, not branched on: the loads stay together
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e) eight.v[u][e] += live[j] ? in[j].v[u][e] : 0.f;
             on = live[j];
         }
         sum.add(eight);
@@ -404,7 +443,7 @@ int64_t zero_blocks(const BwdKernelArgs& a) {
 
 template <typename TA, typename TG, int E>
 cudaError_t bwd_launches(BwdKernelArgs a, int64_t width, const ZeroShares& z, cudaStream_t s) {
-    constexpr int U = E >= 4 ? 1 : 4 / E;
+    constexpr int U = E >= 4 ? 1 : 2;
     a.shape = row_shape(static_cast<int>(width / E), U);
     a.segment = std::min(a.segment, kMaxSpan * a.shape.lanes / kThreads);
     a.span = a.segment * (kThreads / a.shape.lanes);
@@ -435,11 +474,11 @@ cudaError_t bwd_typed(int e, const BwdKernelArgs& a, int64_t width, const ZeroSh
 }
 
 // Tokens of a group: as many as 32, but groups enough for every SM to have
-// some 32 warps. A block's: kMaxSpan at most.
+// some 16 warps. A block's: kMaxSpan at most.
 constexpr int kMaxSegment = 32, kMinSegment = 8;
 int segment_of(int64_t n, int64_t width) {
     int seg = kMaxSegment;
-    while (seg > kMinSegment && cdiv(n, seg) * cdiv(width, 256) < 152 * 32) seg /= 2;
+    while (seg > kMinSegment && cdiv(n, seg) * cdiv(width, 256) < 152 * 16) seg /= 2;
     return seg;
 }
 // A block takes at least kMinSegment tokens a warp.

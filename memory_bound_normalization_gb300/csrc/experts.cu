@@ -13,7 +13,9 @@
 // Rows of the sorted order without a choice are zeroed by the first blocks, by
 // `source` (by the last ones they were the tail of the call).
 #include <algorithm>
+#include <mutex>
 
+#include "own_copy.cuh"
 #include "rows.cuh"
 
 namespace rmsn {
@@ -21,11 +23,11 @@ namespace {
 
 constexpr int kThreads = 256;
 // Pieces of a lane: small ones need more of them in flight.
-__host__ __device__ constexpr int scatter_pieces(int e) { return e >= 4 ? 4 : 8; }
-__host__ __device__ constexpr int gather_pieces(int e) { return e >= 4 ? 2 : 8 / e; }
-__host__ __device__ constexpr int bwd_pieces(int e) { return e >= 4 ? 2 : 4; }
+__host__ __device__ constexpr int scatter_pieces(int bytes) { return bytes == 16 ? 4 : 8; }
+__host__ __device__ constexpr int gather_pieces(int bytes) { return bytes == 16 ? 2 : bytes == 8 ? 4 : 8; }
+// by the choices taken together: 128 bytes in flight
+__host__ __device__ constexpr int bwd_pieces(int bytes, int kc) { return 8 / kc * (bytes >= 8 ? 16 / bytes : 4); }
 constexpr int kChoices = 4;     // in flight
-constexpr int kBwdChoices = 8;  // dots a thread holds
 constexpr int kZeroRows = 64;   // of a block
 
 struct KernelArgs {
@@ -33,6 +35,11 @@ struct KernelArgs {
     RowShape shape;
     unsigned zero_blocks;  // the first ones, which zero rows without a choice
     int team;               // threads of a token (gather_bwd)
+    // ring: the first blocks' tokens are every main_blocks-th of main_tokens, the
+    // others' `tail` each of the rest
+    unsigned main_blocks;
+    int64_t main_tokens;
+    int tail;
 };
 
 // Rows without a choice, of kZeroRows: the whole block zeroes one after another.
@@ -53,7 +60,7 @@ __device__ __forceinline__ void zero_rows(const KernelArgs& a, int size) {
 
 template <typename T, int E>
 __global__ void __launch_bounds__(kThreads) expert_scatter_kernel(const __grid_constant__ KernelArgs a) {
-    constexpr int kScatterPieces = scatter_pieces(E);
+    constexpr int kScatterPieces = scatter_pieces(E * sizeof(T));
     const ExpertArgs& x = a.x;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
@@ -93,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) expert_scatter_kernel(const __grid_c
 
 template <typename T, typename TW, int E>
 __global__ void __launch_bounds__(kThreads) expert_gather_kernel(const __grid_constant__ KernelArgs a) {
-    constexpr int kGatherPieces = gather_pieces(E);
+    constexpr int kGatherPieces = gather_pieces(E * sizeof(T));
     const ExpertArgs& x = a.x;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
@@ -157,11 +164,11 @@ __global__ void __launch_bounds__(kThreads) expert_gather_kernel(const __grid_co
     }
 }
 
-// A team of threads (a power of two, 4 to 256) takes a token and all its columns.
-template <typename T, typename TW, int E>
+// A team of threads (a power of two, 4 to 256) takes a token and all its columns, KC
+// choices at a time: a thread has U pieces of each in flight.
+template <typename T, typename TW, int E, int U, int KC>
 __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __grid_constant__ KernelArgs a) {
-    constexpr int kBwdPieces = bwd_pieces(E);
-    __shared__ float part[kThreads / 32][kBwdChoices];
+    __shared__ float part[kThreads / 32][KC];
     const ExpertArgs& x = a.x;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
@@ -175,75 +182,73 @@ __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __gri
     const T* dy = static_cast<const T*>(x.x) + token * x.x_stride;
     const int32_t* pos = x.position + token * x.choices;
     const TW* wgt = static_cast<const TW*>(x.weights) + token * x.choices;
-    for (int k0 = 0; k0 < x.choices; k0 += kBwdChoices) {
-        float dot[kBwdChoices] = {};
-        const int here = live ? min(kBwdChoices, x.choices - k0) : 0;
-        for (int c = lane; c < (live ? a.shape.pieces : 0); c += team * kBwdPieces) {
-            Piece<T, E> g[kBwdPieces];
+    for (int k0 = 0; k0 < x.choices; k0 += KC) {
+        const int here = live ? min(KC, x.choices - k0) : 0;
+        int32_t row[KC];
+        float w[KC], dot[KC];
 #pragma unroll
-            for (int u = 0; u < kBwdPieces; ++u) {
+        for (int k = 0; k < KC; ++k) {
+            row[k] = k < here ? pos[k0 + k] : -1;
+            w[k] = k < here ? to_f32(wgt[k0 + k]) : 0.f;
+            if (static_cast<uint32_t>(row[k]) >= static_cast<uint32_t>(x.rows)) row[k] = -1;
+            dot[k] = 0.f;
+        }
+        for (int c = lane; c < (live ? a.shape.pieces : 0); c += team * U) {
+            Piece<T, E> g[U], v[KC][U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
                 const int p = c + u * team;
                 g[u].zero();
                 if (p < a.shape.pieces) g[u].load(dy + static_cast<int64_t>(p) * E);
             }
 #pragma unroll
-            for (int k1 = 0; k1 < kBwdChoices; k1 += kChoices) {
-                Piece<T, E> v[kChoices][kBwdPieces];
-                int32_t row[kChoices];
-                if (k1 >= here) break;
+            for (int k = 0; k < KC; ++k) {
+                const T* src = static_cast<const T*>(x.in) + row[k] * x.in_stride;
 #pragma unroll
-                for (int k = 0; k < kChoices; ++k) {
-                    row[k] = k1 + k < here ? pos[k0 + k1 + k] : -1;
-                    if (static_cast<uint32_t>(row[k]) >= static_cast<uint32_t>(x.rows)) row[k] = -1;
-                    const T* src = static_cast<const T*>(x.in) + row[k] * x.in_stride;
-#pragma unroll
-                    for (int u = 0; u < kBwdPieces; ++u) {
-                        const int p = c + u * team;
-                        v[k][u].zero();
-                        if (row[k] >= 0 && p < a.shape.pieces) v[k][u].load(src + static_cast<int64_t>(p) * E);
-                    }
+                for (int u = 0; u < U; ++u) {
+                    const int p = c + u * team;
+                    v[k][u].zero();
+                    if (row[k] >= 0 && p < a.shape.pieces) v[k][u].load(src + static_cast<int64_t>(p) * E);
                 }
+            }
 #pragma unroll
-                for (int k = 0; k < kChoices; ++k) {
+            for (int u = 0; u < U; ++u) {
+                const int p = c + u * team;
+                float h[E];
+                g[u].unpack(h);
+#pragma unroll
+                for (int k = 0; k < KC; ++k) {
                     if (row[k] < 0) continue;
-                    const float w = to_f32(wgt[k0 + k1 + k]);
-                    T* to = static_cast<T*>(x.out) + row[k] * x.out_stride;
+                    T* to = static_cast<T*>(x.out) + row[k] * x.out_stride + static_cast<int64_t>(p) * E;
+                    float f[E];
+                    v[k][u].unpack(f);
 #pragma unroll
-                    for (int u = 0; u < kBwdPieces; ++u) {
-                        const int p = c + u * team;
-                        float f[E], h[E];
-                        v[k][u].unpack(f);
-                        g[u].unpack(h);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            dot[k1 + k] = fmaf(f[e], h[e], dot[k1 + k]);
-                            f[e] = w * h[e];
-                        }
-                        Piece<T, E> out;
-                        out.pack(f);
-                        if (p < a.shape.pieces &&
-                            RMSN_OK(span_in(to + static_cast<int64_t>(p) * E, E * sizeof(T), x.out,
-                                            rows_bytes(x.rows, x.out_stride, x.width, sizeof(T))),
-                                    x.status))
-                            out.store(to + static_cast<int64_t>(p) * E);
+                    for (int e = 0; e < E; ++e) {
+                        dot[k] = fmaf(f[e], h[e], dot[k]);
+                        f[e] = w[k] * h[e];
                     }
+                    Piece<T, E> out;
+                    out.pack(f);
+                    if (p < a.shape.pieces &&
+                        RMSN_OK(span_in(to, E * sizeof(T), x.out, rows_bytes(x.rows, x.out_stride, x.width, sizeof(T))),
+                                x.status))
+                        out.store(to);
                 }
             }
         }
 #pragma unroll
-        for (int k = 0; k < kBwdChoices; ++k)
+        for (int k = 0; k < KC; ++k)
             for (int off = min(team, 32) / 2; off >= 1; off /= 2) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], off);
         float* to = x.dweights + token * x.choices + k0;
         if (team <= 32) {
 #pragma unroll
-            for (int k = 0; k < kBwdChoices; ++k)
-                if (lane == 0 && k < here &&
-                    RMSN_OK(span_in(to + k, 4, x.dweights, 4 * x.tokens * x.choices), x.status))
+            for (int k = 0; k < KC; ++k)
+                if (lane == 0 && k < here && RMSN_OK(span_in(to + k, 4, x.dweights, 4 * x.tokens * x.choices), x.status))
                     to[k] = dot[k];
         } else {
             if (threadIdx.x % 32 == 0) {
 #pragma unroll
-                for (int k = 0; k < kBwdChoices; ++k) part[threadIdx.x / 32][k] = dot[k];
+                for (int k = 0; k < KC; ++k) part[threadIdx.x / 32][k] = dot[k];
             }
             __syncthreads();
             if (lane < here && RMSN_OK(span_in(to + lane, 4, x.dweights, 4 * x.tokens * x.choices), x.status)) {
@@ -254,6 +259,207 @@ __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __gri
             __syncthreads();
         }
     }
+}
+
+// ---------------------------------------------------------------- by a ring
+// The same for rows of 16-byte pieces: persistent blocks, a token at a time, a piece of
+// each choice's row a thread. The pieces are copied into the thread's own slots of
+// shared memory, D - 1 steps (a step: a token's KC choices of a block's columns) ahead,
+// so no thread waits for another's copies. With loads into registers (the kernel above)
+// 16384 tokens of 8 rows of 2048 bf16 took 221 us: too few bytes on the way.
+template <int KC>
+struct Ring {
+    static constexpr int kDepth = KC == 8 ? 3 : KC == 4 ? 5 : 8;
+    static constexpr int kSlots = KC + 1;  // of a step: the choices, then dy
+    static constexpr int kThreadBytes = kDepth * kSlots * 16;
+};
+
+// Sums over a warp of KC values each lane has; lane l returns that of value
+// l / (32 / KC).
+template <int KC>
+__device__ __forceinline__ float sum_of_lanes(float (&v)[KC]) {
+    const unsigned lane = threadIdx.x % 32;
+#pragma unroll
+    for (int n = KC / 2, off = 16; n >= 1; n /= 2, off /= 2) {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float give = upper ? v[k] : v[k + n], keep = upper ? v[k + n] : v[k];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+    }
+    float s = v[0];
+#pragma unroll
+    for (int off = 16 / KC; off >= 1; off /= 2) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return s;
+}
+
+template <typename T, typename TW, int KC>
+__global__ void __launch_bounds__(kThreads) expert_ring_bwd_kernel(const __grid_constant__ KernelArgs a) {
+    using R = Ring<KC>;
+    constexpr int D = R::kDepth, E = Pack<T>::VEC;
+    __shared__ float part[2][kThreads / 32][KC];
+    const ExpertArgs& x = a.x;
+    const int team = blockDim.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = team / 32;
+    const uint32_t slots = smem_u32(rmsn_dynamic_smem) + threadIdx.x * 16;  // [D][slots][team]
+    const int groups = (x.choices + KC - 1) / KC, chunks = (a.shape.pieces + team - 1) / team;
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
+
+    // Step n of the block. A warp's lanes keep the rows (and weights) of kBatch steps at a
+    // time, lane l those of choice l % KC in step l / KC, read two batches (one) ahead: a
+    // step's own would be waited for, which was 1.8 us a step.
+    constexpr int kBatch = 32 / KC;
+    static_assert(D - 1 <= kBatch, "a step's copies are issued from this batch or the next");
+    struct Step {
+        int64_t token;
+        int group, chunk;
+    };
+    const int per_token = groups * chunks;
+    const bool main = blockIdx.x < a.main_blocks;
+    const int64_t token0 = main ? blockIdx.x : a.main_tokens + static_cast<int64_t>(blockIdx.x - a.main_blocks) * a.tail,
+                  stride = main ? a.main_blocks : 1,
+                  end = main ? a.main_tokens : min(token0 + a.tail, x.tokens);
+    auto step_at = [&](unsigned n) {
+        const unsigned t = n / per_token, left = n - t * per_token, g = left / chunks;
+        return Step{token0 + t * stride, static_cast<int>(g), static_cast<int>(left - g * chunks)};
+    };
+    auto next = [&](Step& s) {
+        if (++s.chunk < chunks) return;
+        s.chunk = 0;
+        if (++s.group < groups) return;
+        s.group = 0;
+        s.token += stride;
+    };
+    auto choice_at = [&](unsigned batch) {  // of this lane; -1: none
+        const Step s = step_at(batch * kBatch + lane / KC);
+        const int k = s.group * KC + lane % KC;
+        return s.token < end && k < x.choices ? s.token * x.choices + k : -1;
+    };
+    auto rows_of = [&](unsigned batch) {
+        const int64_t c = choice_at(batch);
+        int32_t row = -1;
+        if (c >= 0) row = x.position[c];
+        return row;
+    };
+    auto weights_of = [&](unsigned batch) {
+        const int64_t c = choice_at(batch);
+        TW w{};
+        if (c >= 0) w = static_cast<const TW*>(x.weights)[c];
+        return w;
+    };
+    auto valid = [&](int32_t row) { return static_cast<uint32_t>(row) < static_cast<uint32_t>(x.rows); };
+    auto slot = [&](int at, int k) { return slots + (at * R::kSlots + k) * team * 16; };
+
+    int32_t rows0 = rows_of(0), rows1 = rows_of(1), rows2 = -1;  // of this batch and the next ones
+    TW weights0 = weights_of(0), weights1{};
+    auto issue = [&](const Step& s, int in_batch, int at) {
+        const int p = s.chunk * team + threadIdx.x;
+        const bool live = s.token < end && p < a.shape.pieces;
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+            const int32_t r = __shfl_sync(0xffffffffu, in_batch < kBatch ? rows0 : rows1, in_batch % kBatch * KC + k);
+            if (live && valid(r))
+                copy_own(slot(at, k), static_cast<const T*>(x.in) + r * x.in_stride + static_cast<int64_t>(p) * E,
+                         x.status);
+        }
+        if (live)
+            copy_own(slot(at, KC), static_cast<const T*>(x.x) + s.token * x.x_stride + static_cast<int64_t>(p) * E,
+                     x.status);
+        copies_commit();
+    };
+
+    Step here{token0, 0, 0}, copied = here;  // the step that is computed; the next one to be copied
+#pragma unroll
+    for (int j = 0; j < D - 1; ++j) {
+        issue(copied, j, j);
+        next(copied);
+    }
+
+    // Meanwhile the rows without a choice: a warp looks at 32, the team zeroes what
+    // all of its warps found. Neighbouring runs of 32 are different blocks'.
+    if (main) {
+        __shared__ unsigned found[kThreads / 32];
+        for (int64_t run0 = 0; (run0 * a.main_blocks + blockIdx.x) * 32 < x.rows; run0 += warps) {
+            const int64_t row = ((run0 + warp) * a.main_blocks + blockIdx.x) * 32 + lane;
+            const unsigned none = __ballot_sync(0xffffffffu, row < x.rows && x.source[row] < 0);
+            if (lane == 0) found[warp] = none;
+            __syncthreads();
+            for (int w = 0; w < warps; ++w) {
+                const int64_t row0 = ((run0 + w) * a.main_blocks + blockIdx.x) * 32;
+                for (unsigned todo = found[w]; todo; todo &= todo - 1)
+                    zero_span(reinterpret_cast<char*>(static_cast<T*>(x.out) + (row0 + __ffs(todo) - 1) * x.out_stride),
+                              static_cast<int64_t>(x.width) * sizeof(T), threadIdx.x, team, x.out,
+                              rows_bytes(x.rows, x.out_stride, x.width, sizeof(T)), x.status);
+            }
+            __syncthreads();
+        }
+    }
+
+    float dot[KC] = {};
+    int at = 0, parity = 0, in_batch = 0;
+    unsigned batch = 0;
+    while (here.token < end) {
+        if (in_batch == 0) {
+            rows2 = rows_of(batch + 2);
+            weights1 = weights_of(batch + 1);
+        }
+        issue(copied, in_batch + D - 1, at == 0 ? D - 1 : at - 1);
+        next(copied);
+        copies_wait<D - 1>();
+        const int p = here.chunk * team + threadIdx.x;
+        const bool live = p < a.shape.pieces;
+        const float weight = to_f32(weights0);
+        Piece<T, E> g;
+        float h[E];
+        g.w[0] = ld_slot(slot(at, KC));
+        g.unpack(h);
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+            const int32_t r = __shfl_sync(0xffffffffu, rows0, in_batch * KC + k);
+            const float w = __shfl_sync(0xffffffffu, weight, in_batch * KC + k);
+            if (!valid(r) || !live) continue;
+            Piece<T, E> v;
+            float f[E];
+            v.w[0] = ld_slot(slot(at, k));
+            v.unpack(f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                dot[k] = fmaf(f[e], h[e], dot[k]);
+                f[e] = w * h[e];
+            }
+            v.pack(f);
+            T* to = static_cast<T*>(x.out) + r * x.out_stride + static_cast<int64_t>(p) * E;
+            if (RMSN_OK(span_in(to, 16, x.out, rows_bytes(x.rows, x.out_stride, x.width, sizeof(T))), x.status))
+                v.store(to);
+        }
+        if (here.chunk + 1 == chunks) {  // the columns are done: the team's sums
+            const float s = sum_of_lanes<KC>(dot);
+            if (lane % (32 / KC) == 0) part[parity][warp][lane / (32 / KC)] = s;
+            __syncthreads();
+            const int k = here.group * KC + threadIdx.x;
+            float* to = x.dweights + here.token * x.choices + k;
+            if (threadIdx.x < KC && k < x.choices &&
+                RMSN_OK(span_in(to, 4, x.dweights, 4 * x.tokens * x.choices), x.status)) {
+                float all = 0.f;
+                for (int w = 0; w < warps; ++w) all += part[parity][w][threadIdx.x];
+                *to = all;
+            }
+            parity ^= 1;  // written again behind the next barrier but one
+#pragma unroll
+            for (int i = 0; i < KC; ++i) dot[i] = 0.f;
+        }
+        next(here);
+        at = at + 1 == D ? 0 : at + 1;
+        if (++in_batch == kBatch) {
+            in_batch = 0;
+            ++batch;
+            rows0 = rows1;
+            rows1 = rows2;
+            weights0 = weights1;
+        }
+    }
+    copies_wait<0>();
 }
 
 int piece_of(const ExpertArgs& a, int dtype) {
@@ -291,16 +497,54 @@ cudaError_t with_types(int dtype, F fn) {
     }
 }
 
+// Lets a kernel have a ring's shared memory, once a device.
+cudaError_t allow_smem(const DeviceInfo& dev, const void* fn, int bytes) {
+    static std::mutex mu;
+    static struct {
+        int device;
+        const void* fn;
+    } done[1024];
+    static int n = 0;
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < n; ++i)
+        if (done[i].device == dev.device && done[i].fn == fn) return cudaSuccess;
+    const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess && n < 1024) done[n++] = {dev.device, fn};
+    return err;
+}
+
+template <typename T, typename TW, int KC>
+cudaError_t ring_launch(const DeviceInfo& dev, const KernelArgs& in, cudaStream_t s) {
+    const int pieces = in.shape.pieces, team = pieces <= 32 ? 32 : pieces <= 64 ? 64 : pieces <= 128 ? 128 : kThreads;
+    constexpr int kBytes = Ring<KC>::kThreadBytes;
+    const auto fn = expert_ring_bwd_kernel<T, TW, KC>;
+    const cudaError_t err = allow_smem(dev, reinterpret_cast<const void*>(fn), kBytes * kThreads);
+    if (err != cudaSuccess) return err;
+    // Blocks of 256 threads two an SM, smaller ones as many more. SMs get up to 15% more
+    // or less of the memory's rate than the mean: the blocks that fit at once share
+    // 12/16 of the tokens out evenly, and the rest goes in small blocks to SMs as they
+    // come free (16384 tokens of 8 rows of 2048 bf16: 205 us with all shared out evenly,
+    // 178 so). Few tokens go in small blocks altogether (777 of 4 rows of 2880 fp32: 23
+    // us shared out, 17 so); the first blocks then only zero rows.
+    const int64_t resident = static_cast<int64_t>(dev.sm_count) * 2 * (kThreads / team);
+    KernelArgs a = in;
+    a.main_tokens = in.x.tokens >= 16 * resident ? in.x.tokens / 16 * 12 : 0;
+    a.tail = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16 / KC, in.x.tokens / resident)));
+    a.main_blocks = static_cast<unsigned>(std::min(std::max<int64_t>(a.main_tokens, cdiv(in.x.rows, 32)), resident));
+    const int grid = static_cast<int>(a.main_blocks + cdiv(in.x.tokens - a.main_tokens, a.tail));
+    return launch_pdl(fn, grid, team, kBytes * team, 1, s, a);
+}
+
 }  // namespace
 
 bool experts_fit(const ExpertArgs& a) {
-    return a.tokens * cdiv(a.width, 32 * gather_pieces(1)) <= kMaxGrid;  // groups, element by element
+    return a.tokens * cdiv(a.width, 32 * gather_pieces(2)) <= kMaxGrid;  // groups, element by element
 }
 
 cudaError_t expert_scatter_launch(const DeviceInfo&, int dtype, const ExpertArgs& in, cudaStream_t s) {
     KernelArgs a{in, {}, 0, 0};
     const int e = piece_of(in, dtype);
-    a.shape = row_shape(in.width / e, scatter_pieces(e));
+    a.shape = row_shape(in.width / e, scatter_pieces(e * dtype_size(dtype)));
     a.zero_blocks = zero_blocks(in);
     const int grid = static_cast<int>(a.zero_blocks + cdiv(in.tokens * a.shape.chunks * a.shape.lanes, kThreads));
     auto go = [&](auto t) {
@@ -316,7 +560,7 @@ cudaError_t expert_scatter_launch(const DeviceInfo&, int dtype, const ExpertArgs
 cudaError_t expert_gather_launch(const DeviceInfo&, int dtype, const ExpertArgs& in, cudaStream_t s) {
     KernelArgs a{in, {}, 0, 0};
     const int e = piece_of(in, dtype);
-    a.shape = row_shape(in.width / e, gather_pieces(e));
+    a.shape = row_shape(in.width / e, gather_pieces(e * dtype_size(dtype)));
     const int grid = static_cast<int>(cdiv(in.tokens * a.shape.chunks * a.shape.lanes, kThreads));
     return with_types(dtype, [&](auto t, auto w) {
         using T = decltype(t);
@@ -326,18 +570,34 @@ cudaError_t expert_gather_launch(const DeviceInfo&, int dtype, const ExpertArgs&
     });
 }
 
-cudaError_t expert_gather_bwd_launch(const DeviceInfo&, int dtype, const ExpertArgs& in, cudaStream_t s) {
+cudaError_t expert_gather_bwd_launch(const DeviceInfo& dev, int dtype, const ExpertArgs& in, cudaStream_t s) {
     KernelArgs a{in, {}, 0, 0};
     const int e = piece_of(in, dtype);
-    a.shape = row_shape(in.width / e, bwd_pieces(e));
-    a.team = 4;
-    while (a.team < kThreads && a.team * bwd_pieces(e) < a.shape.pieces) a.team *= 2;
+    a.shape.pieces = in.width / e;
+    if (e * dtype_size(dtype) == 16 && a.shape.pieces > 16) {
+        return with_types(dtype, [&](auto t, auto w) {
+            auto go = [&](auto kc) { return ring_launch<decltype(t), decltype(w), decltype(kc)::value>(dev, a, s); };
+            if (in.choices <= 2) return go(std::integral_constant<int, 2>());
+            if (in.choices <= 4) return go(std::integral_constant<int, 4>());
+            return go(std::integral_constant<int, 8>());
+        });
+    }
     a.zero_blocks = zero_blocks(in);
-    const int grid = static_cast<int>(a.zero_blocks + cdiv(in.tokens, kThreads / a.team));
     return with_types(dtype, [&](auto t, auto w) {
         using T = decltype(t);
         return with_piece<T>(e, [&](auto n) {
-            return launch_pdl(expert_gather_bwd_kernel<T, decltype(w), decltype(n)::value>, grid, kThreads, 0, 1, s, a);
+            constexpr int E = decltype(n)::value;
+            auto go = [&](auto kc) {
+                constexpr int KC = decltype(kc)::value, U = bwd_pieces(E * sizeof(T), KC);
+                a.shape = row_shape(in.width / E, U);
+                a.team = 4;
+                while (a.team < kThreads && a.team * U < a.shape.pieces) a.team *= 2;
+                const int grid = static_cast<int>(a.zero_blocks + cdiv(in.tokens, kThreads / a.team));
+                return launch_pdl(expert_gather_bwd_kernel<T, decltype(w), E, U, KC>, grid, kThreads, 0, 1, s, a);
+            };
+            if (in.choices <= 2) return go(std::integral_constant<int, 2>());
+            if (in.choices <= 4) return go(std::integral_constant<int, 4>());
+            return go(std::integral_constant<int, 8>());
         });
     });
 }

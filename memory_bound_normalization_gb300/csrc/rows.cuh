@@ -55,6 +55,20 @@ struct Piece {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const W*>(p)[i];
     }
+    // issued here, whatever becomes of it
+    __device__ __forceinline__ void load_now(const T* p) {
+        if constexpr (BYTES >= 16) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                W& o = w[i];
+                asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                             : "l"(reinterpret_cast<const W*>(p) + i));
+            }
+        } else {
+            load_plain(p);
+        }
+    }
     __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) reinterpret_cast<W*>(p)[i] = w[i];
