@@ -450,8 +450,8 @@ int rmsnorm_embedding_fwd(const rmsnorm_embedding_t *embedding,
  * neither read nor written). dtype names the types of dy and of grad (as of y
  * and the table). Tokens are sorted by id, so every row's sum is fp32 in an
  * order that the sizes alone fix, rounded once: the same bits on every run,
- * no floating-point atomics. Three launches, or two and three for each nine bits of
- * num_rows past 131072 tokens. Workspace and errors as the norm's backward
+ * no floating-point atomics. Three launches; two, and two for each nine bits of
+ * num_rows, past 16384 tokens. Workspace and errors as the norm's backward
  * (RMSNORM_ERR_NOMEM), arguments as the forward's.
  */
 int rmsnorm_embedding_bwd(const rmsnorm_embedding_t *embedding,
@@ -502,7 +502,7 @@ int64_t rmsnorm_expert_rows(int64_t tokens, int64_t choices,
  * Within an expert, choices keep their order. rows >= rmsnorm_expert_rows(...);
  * rows behind the last expert have no choice. 1 <= num_experts <=
  * RMSNORM_MAX_EXPERTS, 1 <= align, tokens * choices <= 2^31-1, else
- * RMSNORM_ERR_INVALID_ARG. One launch; past 131072 choices three, and a
+ * RMSNORM_ERR_INVALID_ARG. One launch; past 16384 choices two, and a
  * workspace from the stream-ordered allocator (RMSNORM_ERR_NOMEM).
  */
 int rmsnorm_expert_sort(const void *experts, int experts_64, int64_t tokens,

@@ -189,8 +189,20 @@ PyObject* expert_sort(PyObject*, PyObject* const* a, Py_ssize_t) {
                    std::to_string(align) + ": 1 to " + std::to_string(RMSNORM_MAX_EXPERTS) +
                    " experts, an alignment of 1 or more, rows up to 2^31-1");
         Run run(experts, a[3]);
-        const at::Tensor position = make(experts.sizes(), at::kInt, experts), source = make({R}, at::kInt, experts),
-                         offsets = make({E + 1}, at::kInt, experts), counts = make({E}, at::kInt, experts);
+        // one allocation for the four: each cost as much as a fourth of the kernel
+        auto room = [](int64_t n) { return (n + 3) / 4 * 4; };
+        const at::Tensor all = make({room(T * K) + room(R) + room(E + 1) + E}, at::kInt, experts);
+        int64_t used = 0;
+        auto part = [&](at::IntArrayRef sizes, int64_t n) {
+            at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                                    all.dtype());
+            t.unsafeGetTensorImpl()->set_storage_offset(used);
+            t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+            used += room(n);
+            return t;
+        };
+        const at::Tensor position = part(experts.sizes(), T * K), source = part({R}, R), offsets = part({E + 1}, E + 1),
+                         counts = part({E}, E);
         const size_t need = g_rows.expert_sort_need(T, K, E);
         void* ws = run.workspace(need);
         const void* pe = experts.const_data_ptr();

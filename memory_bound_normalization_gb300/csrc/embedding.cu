@@ -326,6 +326,16 @@ __device__ __forceinline__ void zero_unit(const BwdKernelArgs& a, int64_t width,
     unsigned todo = __ballot_sync(0xffffffffu, lane < rows && a.present[row0 + lane] == 0);
     const int64_t row_bytes = width * static_cast<int>(sizeof(TG));
     const int64_t from = static_cast<int64_t>(slice) * kZeroBytes;
+    if (row_bytes <= 256 && row_bytes % 16 == 0 && a.grad_stride == width &&
+        reinterpret_cast<uintptr_t>(a.grad) % 16 == 0) {  // short rows by their words, not one after another
+        const int words = static_cast<int>(row_bytes) / 16;
+        char* to = reinterpret_cast<char*>(static_cast<TG*>(a.grad) + row0 * width);
+        for (int i = lane; i < rows * words; i += 32)
+            if (todo >> (i / words) & 1 &&
+                RMSN_OK(span_in(to + i * 16, 16, a.grad, rows_bytes(a.rows, width, width, sizeof(TG))), a.status))
+                *reinterpret_cast<uint4*>(to + i * 16) = make_uint4(0, 0, 0, 0);
+        return;
+    }
     while (todo) {
         const int r = __ffs(todo) - 1;
         todo &= todo - 1;
@@ -556,7 +566,7 @@ cudaError_t embedding_bwd_launch(const DeviceInfo& dev, int dtype, const Embeddi
             b.zero = stride_bytes == row_bytes ? ZeroJob{at, z.sort * row_bytes, 0, 1}
                                                : ZeroJob{at, row_bytes, stride_bytes, z.sort};
         }
-        z.join = std::min(in.rows - z.sort, kZeroBesideJoin / row_bytes);
+        z.join = std::min((in.rows - z.sort) / 4, kZeroBesideJoin / row_bytes);
     }
     const cudaError_t err = sort_launch(dev, in.k, b, s);
     if (err != cudaSuccess) return err;

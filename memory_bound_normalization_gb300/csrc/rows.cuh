@@ -74,10 +74,21 @@ struct Piece {
         for (int i = 0; i < WORDS; ++i) reinterpret_cast<W*>(p)[i] = w[i];
     }
     __device__ __forceinline__ void unpack(float (&f)[E]) const {
-        T t[E];
-        memcpy(t, w, BYTES);
+        if constexpr (sizeof(T) == 2 && E % 2 == 0) {
+            uint32_t u[E / 2];
+            memcpy(u, w, BYTES);
 #pragma unroll
-        for (int i = 0; i < E; ++i) f[i] = to_f32(t[i]);
+            for (int i = 0; i < E / 2; ++i) {
+                const float2 v = Pack<T>::word_to_f2(u[i]);
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            }
+        } else {
+            T t[E];
+            memcpy(t, w, BYTES);
+#pragma unroll
+            for (int i = 0; i < E; ++i) f[i] = to_f32(t[i]);
+        }
     }
     __device__ __forceinline__ void pack(const float (&f)[E]) {
         if constexpr (sizeof(T) == 2 && E % 2 == 0) {

@@ -12,8 +12,8 @@
 // A few thousand to some hundred thousand keys of 4 to 8 bytes: the time is a
 // chain of launches and barriers, not bytes. Up to kClusterItems one cluster of
 // up to eight blocks does every pass in one launch and joins its counts through
-// distributed shared memory. More items take three launches a pass over as many
-// blocks as fill the device (counts, their prefix, placement).
+// distributed shared memory. More items take two launches a pass over up to 152
+// blocks (counts, placement).
 #include <algorithm>
 #include <mutex>
 
@@ -23,11 +23,11 @@ namespace rmsn {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kMaxRounds = 16;
 constexpr int kCluster = 8;
 // One cluster's scattered stores are slow: 1.3 us for every 8192 items. 16384 items take
-// it 6.6 us, 32768 9.0; 131073 take many blocks 7.1 us in three launches.
+// it 6.6 us, 32768 9.0; 131073 take many blocks 7.
 constexpr int64_t kClusterItems = 2 * kThreads * kCluster;
+constexpr int kManyBlocks = 152;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxExperts = RMSNORM_MAX_EXPERTS;
 
@@ -36,8 +36,10 @@ struct SortArgs {
     uint32_t* keys[2];
     int32_t* items[2];
     uint8_t* present;
-    uint32_t* counts;  // [bins][blocks], then the bins' totals (many blocks)
-    int blocks;
+    // many blocks, in clusters of kCluster: [blocks][bins] counts of the cluster's blocks
+    // before, then [clusters][bins] counts of the clusters
+    uint32_t* counts;
+    int blocks, tiles;  // kThreads * R items a tile
     int passes, pass, bits, bins;
     // experts
     int32_t* position;
@@ -50,7 +52,7 @@ struct SortArgs {
 };
 
 __host__ __device__ inline int bins_stride(int bins) { return (bins + 1) & ~1; }
-inline int sort_smem(int bins, int warps) { return warps * bins_stride(bins) * 2 + 16 + 4 * 4 * (bins + 1); }
+inline int sort_smem(int bins, int warps) { return warps * bins_stride(bins) * 2 + 16 + 5 * 4 * (bins + 1); }
 
 struct Smem {
     uint16_t* cnt;    // [warps][stride]
@@ -58,6 +60,7 @@ struct Smem {
     uint32_t* base;   // [bins]: where the block's items of a digit start
     uint32_t* start;  // [bins]: where the digit starts
     uint32_t* total;  // [bins]
+    uint32_t* seen;   // [bins]: the key of the block's first item of a digit
 };
 __device__ __forceinline__ Smem smem_of(int bins) {
     Smem s;
@@ -67,6 +70,7 @@ __device__ __forceinline__ Smem smem_of(int bins) {
     s.base = s.hist + bins + 1;
     s.start = s.base + bins + 1;
     s.total = s.start + bins + 1;
+    s.seen = s.total + bins + 1;
     return s;
 }
 
@@ -196,8 +200,27 @@ __device__ __forceinline__ void scatter(const SortArgs& a, int pass, const Smem&
             if (!RMSN_OK(at < a.k.n, a.status)) continue;
             a.keys[to][at] = key[r];
             a.items[to][at] = item;
-            if (pass == 0 && a.present != nullptr && key[r] < a.k.limit) a.present[key[r]] = 1;
         }
+    }
+}
+
+// Marks the keys of a tile. A frequent one is marked by its digit's first item alone: a
+// store from every warp to the same few bytes took longer than the rest of the pass.
+template <int R>
+__device__ __forceinline__ void mark_present(const SortArgs& a, const Smem& s, const uint16_t* cnt, unsigned first,
+                                             const uint32_t (&key)[R], const uint32_t (&rank)[R]) {
+    bool is_first[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint32_t d = digit_of(a, 0, key[r]);
+        is_first[r] = first + r * 32 + threadIdx.x % 32 < a.k.n && cnt[d] + rank[r] == 0;
+        if (is_first[r]) s.seen[d] = key[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const bool live = first + r * 32 + threadIdx.x % 32 < a.k.n && key[r] < a.k.limit;
+        if (live && (is_first[r] || s.seen[digit_of(a, 0, key[r])] != key[r])) a.present[key[r]] = 1;
     }
 }
 
@@ -309,6 +332,7 @@ __global__ void __launch_bounds__(kThreads) sort_cluster_kernel(const __grid_con
         place_digits(a, s, total, mine, rank);
         scatter<R>(a, pass, s, cnt, first, key, place);
         if (a.experts > 0) mark_unused(a, s, rank, blocks);
+        else if (pass == 0 && a.present != nullptr) mark_present<R>(a, s, cnt, first, key, place);
         // every block has read the others' counts, and the next pass reads what they placed
         if (blocks > 1) cluster_sync_all();
         else __syncthreads();
@@ -323,56 +347,74 @@ __global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_const
     wait_for_prerequisite_grid();
     allow_dependent_launch();
     if (a.pass == 0) clear_present(a, blockIdx.x, gridDim.x);
-    uint32_t key[R];
-    const unsigned first = blockIdx.x * (kThreads * R) + threadIdx.x / 32 * 32 * R;
-    load_keys<R>(a, a.pass, first, key);
     __syncthreads();
+    for (int tile = 0; tile < a.tiles; ++tile) {
+        uint32_t key[R];
+        const unsigned first = (blockIdx.x * a.tiles + tile) * (kThreads * R) + threadIdx.x / 32 * 32 * R;
+        load_keys<R>(a, a.pass, first, key);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (first + r * 32 + threadIdx.x % 32 < a.k.n) atomicAdd(hist + digit_of(a, a.pass, key[r]), 1u);
-    __syncthreads();
-    for (int d = threadIdx.x; d < a.bins; d += blockDim.x)
-        a.counts[static_cast<int64_t>(d) * a.blocks + blockIdx.x] = hist[d];
-}
-// ... a digit's counts become sums over the blocks before, ...
-__global__ void __launch_bounds__(256) sort_prefix_kernel(const __grid_constant__ SortArgs a) {
-    wait_for_prerequisite_grid();
-    allow_dependent_launch();
-    uint32_t* c = a.counts + static_cast<int64_t>(blockIdx.x) * a.blocks;
-    uint32_t sum = 0;
-    for (int b0 = 0; b0 < a.blocks; b0 += blockDim.x) {
-        const int b = b0 + threadIdx.x;
-        const uint32_t v = b < a.blocks ? c[b] : 0;
-        uint32_t all;
-        const uint32_t before = scan_before(v, &all);
-        if (b < a.blocks) c[b] = sum + before;
-        sum += all;
+        for (int r = 0; r < R; ++r)
+            if (first + r * 32 + threadIdx.x % 32 < a.k.n) atomicAdd(hist + digit_of(a, a.pass, key[r]), 1u);
     }
-    if (threadIdx.x == 0) a.counts[static_cast<int64_t>(a.bins) * a.blocks + blockIdx.x] = sum;
+    // a cluster adds its blocks' counts up, so that the next kernel reads an eighth of them
+    cluster_sync_all();
+    const int rank = static_cast<int>(cluster_rank());
+    for (int d = threadIdx.x; d < a.bins; d += blockDim.x) {
+        uint32_t v[kCluster], total = 0, before = 0;
+#pragma unroll
+        for (int b = 0; b < kCluster; ++b)
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v[b]) : "r"(cluster_map(hist + d, b)));
+#pragma unroll
+        for (int b = 0; b < kCluster; ++b) {
+            total += v[b];
+            if (b < rank) before += v[b];
+        }
+        a.counts[static_cast<int64_t>(blockIdx.x) * a.bins + d] = before;
+        if (rank == 0) a.counts[static_cast<int64_t>(a.blocks + blockIdx.x / kCluster) * a.bins + d] = total;
+    }
+    cluster_sync_all();  // the others have read this block's
 }
 // ... and the items go to their places.
 template <int R>
 __global__ void __launch_bounds__(kThreads) sort_place_kernel(const __grid_constant__ SortArgs a) {
     const Smem s = smem_of(a.bins);
-    const unsigned block_first = blockIdx.x * (kThreads * R), warp = threadIdx.x / 32;
-    const unsigned first = block_first + warp * 32 * R;
+    const unsigned warp = threadIdx.x / 32;
     uint16_t* cnt = s.cnt + warp * bins_stride(a.bins);
-    const int warps = clear_counts<R>(a, s, block_first);
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    uint32_t key[R], place[R];
-    load_keys<R>(a, a.pass, first, key);
+    uint32_t key[R];
+    load_keys<R>(a, a.pass, blockIdx.x * a.tiles * (kThreads * R) + warp * 32 * R, key);  // on their way meanwhile
     uint32_t total = 0, mine = 0;
     if (threadIdx.x < a.bins) {
-        mine = a.counts[static_cast<int64_t>(threadIdx.x) * a.blocks + blockIdx.x];
-        total = a.counts[static_cast<int64_t>(a.bins) * a.blocks + threadIdx.x];
+        const uint32_t* clusters = a.counts + static_cast<int64_t>(a.blocks) * a.bins + threadIdx.x;
+        const int count = a.blocks / kCluster, own = blockIdx.x / kCluster;
+        mine = a.counts[static_cast<int64_t>(blockIdx.x) * a.bins + threadIdx.x];
+        uint32_t c[kManyBlocks / kCluster];
+#pragma unroll
+        for (int b = 0; b < kManyBlocks / kCluster; ++b) c[b] = b < count ? clusters[b * a.bins] : 0;
+#pragma unroll
+        for (int b = 0; b < kManyBlocks / kCluster; ++b) {
+            total += c[b];
+            if (b < own) mine += c[b];
+        }
     }
-    __syncthreads();
-    rank_keys<R>(a, a.pass, first, key, cnt, place);
-    __syncthreads();
-    sum_warps(a, s, warps);
     place_digits(a, s, total, mine, blockIdx.x);
-    scatter<R>(a, a.pass, s, cnt, first, key, place);
+    for (int tile = 0; tile < a.tiles; ++tile) {
+        const unsigned block_first = (blockIdx.x * a.tiles + tile) * (kThreads * R), first = block_first + warp * 32 * R;
+        uint32_t place[R];
+        if (tile > 0) load_keys<R>(a, a.pass, first, key);
+        const int warps = clear_counts<R>(a, s, block_first);
+        __syncthreads();
+        rank_keys<R>(a, a.pass, first, key, cnt, place);
+        __syncthreads();
+        sum_warps(a, s, warps);
+        __syncthreads();
+        scatter<R>(a, a.pass, s, cnt, first, key, place);
+        if (a.pass == 0 && a.present != nullptr) mark_present<R>(a, s, cnt, first, key, place);
+        if (tile + 1 == a.tiles) break;
+        __syncthreads();  // the next tile's items start behind these
+        for (int d = threadIdx.x; d < a.bins; d += blockDim.x) s.base[d] += s.hist[d];
+    }
     if (a.experts > 0) mark_unused(a, s, blockIdx.x, gridDim.x);
 }
 
@@ -382,29 +424,20 @@ int bits_of(int64_t limit) {
     return b;
 }
 
-// Blocks of a pass over many blocks, kThreads * rounds items each.
-int many_rounds(int64_t n) {
-    int r = 1;
-    while (r < kMaxRounds && cdiv(n, static_cast<int64_t>(kThreads) * r) > 152) r *= 2;
-    return r;
-}
+// A pass over many blocks, whole clusters of them: a tile (kThreads items, twice as many
+// past kManyBlocks of them) each, or as many as keep them at kManyBlocks. A block's
+// scattered stores drain at some two cycles each, so more SMs come before fuller ones.
+struct Many {
+    int rounds, tiles, blocks;
+    explicit Many(int64_t n) {
+        rounds = n <= kThreads * kManyBlocks ? 1 : 2;
+        const int64_t tile = kThreads * rounds;
+        tiles = static_cast<int>(cdiv(n, tile * kManyBlocks));
+        blocks = static_cast<int>(cdiv(cdiv(n, tile * tiles), kCluster)) * kCluster;
+    }
+};
 
 using SortFn = void (*)(const SortArgs);
-template <int R>
-SortFn kernel_of(int which) {
-    if (which == 0) return sort_cluster_kernel<R>;
-    return which == 1 ? SortFn(sort_count_kernel<R>) : SortFn(sort_place_kernel<R>);
-}
-SortFn kernel_for(int which, int rounds) {
-    switch (rounds) {
-        case 1: return kernel_of<1>(which);
-        case 2: return kernel_of<2>(which);
-        case 4: return kernel_of<4>(which);
-        case 8: return kernel_of<8>(which);
-        default: return kernel_of<16>(which);
-    }
-}
-
 // Lets a kernel have the shared memory of the most bins, once a device.
 cudaError_t allow_smem(const DeviceInfo& dev, SortFn fn) {
     static std::mutex mu;
@@ -426,15 +459,14 @@ cudaError_t allow_smem(const DeviceInfo& dev, SortFn fn) {
 cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
     const int64_t n = a.k.n;
     if (n <= kClusterItems) {
-        // one block while its items and the rows it marks are few; then eight, a power of
-        // two of rounds
-        int blocks = n <= kThreads && a.rows <= 4 * kThreads ? 1 : kCluster, rounds = 1;
-        while (static_cast<int64_t>(blocks) * kThreads * rounds < n) rounds *= 2;
+        // one block while its items and the rows it marks are few; then eight
+        const int blocks = n <= kThreads && a.rows <= 4 * kThreads ? 1 : kCluster;
+        const int rounds = n <= blocks * kThreads ? 1 : 2;
         // no more threads than items or digits need
         const int digits = a.experts > 0 ? a.experts : a.bins;
         const int need = std::max<int>(static_cast<int>(std::min<int64_t>(cdiv(n, rounds), kThreads)), digits);
         const int threads = blocks > 1 ? kThreads : std::min(kThreads, std::max(128, round_up(need, 32)));
-        const SortFn fn = kernel_for(0, rounds);
+        const SortFn fn = rounds == 1 ? sort_cluster_kernel<1> : SortFn(sort_cluster_kernel<2>);
         const cudaError_t err = allow_smem(dev, fn);
         if (err != cudaSuccess) return err;
         // blocks that zero rows: whole clusters, up to the SMs left
@@ -444,17 +476,17 @@ cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
         const int zero = units > 0 ? static_cast<int>(std::max<int64_t>(idle, blocks)) : 0;
         return launch_pdl(fn, blocks + zero, threads, sort_smem(a.bins, threads / 32), blocks, s, a);
     }
-    const int rounds = many_rounds(n);
-    a.blocks = static_cast<int>(cdiv(n, static_cast<int64_t>(kThreads) * rounds));
+    const Many m(n);
+    a.blocks = m.blocks;
+    a.tiles = m.tiles;
     for (a.pass = 0; a.pass < a.passes; ++a.pass) {
-        cudaError_t err = launch_pdl(kernel_for(1, rounds), a.blocks, kThreads, a.bins * 4, 1, s, a);
+        cudaError_t err = launch_pdl(m.rounds == 1 ? sort_count_kernel<1> : SortFn(sort_count_kernel<2>), m.blocks, kThreads,
+                                     a.bins * 4, kCluster, s, a);
         if (err != cudaSuccess) return err;
-        err = launch_pdl(sort_prefix_kernel, a.bins, 256, 0, 1, s, a);
-        if (err != cudaSuccess) return err;
-        const SortFn fn = kernel_for(2, rounds);
+        const SortFn fn = m.rounds == 1 ? sort_place_kernel<1> : SortFn(sort_place_kernel<2>);
         err = allow_smem(dev, fn);
         if (err != cudaSuccess) return err;
-        err = launch_pdl(fn, a.blocks, kThreads, sort_smem(a.bins, kThreads / 32), 1, s, a);
+        err = launch_pdl(fn, m.blocks, kThreads, sort_smem(a.bins, kThreads / 32), 1, s, a);
         if (err != cudaSuccess) return err;
     }
     return cudaSuccess;
@@ -467,7 +499,7 @@ int sort_max_bins(int64_t limit) { return 1 << cdiv(bits_of(limit), sort_passes(
 
 int64_t sort_counts_words(int64_t n, int bins) {
     if (n <= kClusterItems) return 0;
-    return static_cast<int64_t>(bins) * (cdiv(n, static_cast<int64_t>(kThreads) * many_rounds(n)) + 1);
+    return static_cast<int64_t>(bins) * (Many(n).blocks + Many(n).blocks / kCluster);
 }
 
 bool sort_takes_zero_job(int64_t n) { return n <= kClusterItems; }

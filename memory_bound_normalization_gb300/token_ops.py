@@ -49,9 +49,9 @@ def expert_sort(experts, num_experts: int, align: int = 1, stream=None) -> Exper
     """The choices experts [..., K] (int32 or int64; outside [0, num_experts): dropped)
     sorted by expert, in their order within an expert, every expert's first row a
     multiple of `align`. The rows number R = rmsnorm_expert_rows(...), however the
-    choices fall."""
-    return ExpertRows(*(image_ops._bound or _binding()).expert_sort(experts, num_experts, align,
-                                                                   _handle(stream)))
+    choices fall. The four tensors share one allocation."""
+    return ExpertRows._make((image_ops._bound or _binding()).expert_sort(experts, num_experts, align,
+                                                                        _handle(stream)))
 
 
 def expert_dispatch_forward(x, position, source, stream=None):
