@@ -80,8 +80,7 @@ __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_co
 }
 
 struct BwdKernelArgs {
-    const uint32_t* keys;   // sorted
-    const int32_t* items;
+    const KeyItem* pairs;  // sorted
     const uint8_t* present;
     const void* dy;
     void* grad;
@@ -184,20 +183,19 @@ __device__ __forceinline__ void add_tokens(const BwdKernelArgs& a, unsigned span
     const uint32_t none = 0xffffffffu;
     constexpr int kAhead = 4;  // of a thread's tokens, read together
     for (int i0 = threadIdx.x; i0 < count + 2; i0 += kAhead * kThreads) {
-        uint32_t k[kAhead];
-        int32_t t[kAhead];
+        uint2 pair[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int i = i0 + j * kThreads;
             const int64_t at = static_cast<int64_t>(first) + i - 1;
-            k[j] = i < count + 2 && at >= 0 && at < a.n ? a.keys[at] : none;
-            t[j] = i < count ? a.items[first + i] : 0;
+            pair[j] = make_uint2(none, 0);
+            if (i < count + 2 && at >= 0 && at < a.n) pair[j] = *reinterpret_cast<const uint2*>(a.pairs + at);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int i = i0 + j * kThreads;
-            if (i < count + 2) key[i] = k[j];
-            if (i < count) item[i] = t[j];
+            if (i < count + 2) key[i] = pair[j].x;
+            if (i > 0 && i <= count) item[i - 1] = static_cast<int32_t>(pair[j].y);
         }
     }
     __syncthreads();
@@ -319,7 +317,7 @@ __device__ __forceinline__ void add_tokens(const BwdKernelArgs& a, unsigned span
 template <typename TG>
 __device__ __forceinline__ void zero_unit(const BwdKernelArgs& a, int64_t width, int64_t unit) {
     const int lane = threadIdx.x % 32;
-    const int64_t part = unit / a.zero_slices;
+    const int64_t part = a.zero_slices == 1 ? unit : unit / a.zero_slices;
     const int slice = static_cast<int>(unit - part * a.zero_slices);
     const int64_t row0 = a.zero_from + part * a.zero_rows;
     const int rows = static_cast<int>(min(static_cast<int64_t>(a.zero_rows), a.zero_to - row0));
@@ -379,9 +377,17 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
     const int piece = (group - span * a.shape.chunks) * (a.shape.lanes * U) + (threadIdx.x & (a.shape.lanes - 1));
     if (span + 1 >= a.spans) return;
     const uint32_t first = span * static_cast<uint32_t>(a.span), next = first + a.span;
-    const uint32_t run = a.keys[next - 1], behind = a.keys[next], begin = a.keys[first],
-                   before = first > 0 ? a.keys[first - 1] : 0xffffffffu;
-    if (run >= a.limit || behind != run || (begin == run && before == run)) return;  // ends here, or began before
+    // the first ids of the next spans, read before those of the last ones are looked at
+    uint32_t begins[kAhead];
+    auto read_begins = [&](unsigned s) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            begins[j] = s + j < a.spans ? a.pairs[(s + j) * static_cast<uint32_t>(a.span)].key : 0xffffffffu;
+    };
+    const uint32_t run = a.pairs[next - 1].key, begin = a.pairs[first].key,
+                   before = first > 0 ? a.pairs[first - 1].key : 0xffffffffu;
+    read_begins(span + 1);
+    if (run >= a.limit || begins[0] != run || (begin == run && before == run)) return;  // ends here, or began before
     Columns<E, U> sum;
     auto load = [&](Columns<E, U>& c, unsigned s, int slot, bool live) {
 #pragma unroll
@@ -394,16 +400,15 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
         }
     };
     load(sum, span, 1, true);
-    bool on = true;
-    for (unsigned s = span + 1; on && s < a.spans; s += kAhead) {
+    for (unsigned s = span + 1;; s += kAhead) {
         // a span has a share where it starts with this id; what others hold is not used
         bool live[kAhead];
         Columns<E, U> in[kAhead], eight;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            live[j] = s + j < a.spans && a.keys[(s + j) * static_cast<uint32_t>(a.span)] == run;
+        for (int j = 0; j < kAhead; ++j) live[j] = begins[j] == run;
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) load(in[j], s + j, 0, s + j < a.spans);
+        read_begins(s + kAhead);
         eight.clear();
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -412,9 +417,9 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int e = 0; e < E; ++e) eight.v[u][e] += live[j] ? in[j].v[u][e] : 0.f;
-            on = live[j];
         }
         sum.add(eight);
+        if (!live[kAhead - 1]) break;
     }
     put_row<TG, E, U>(a, run, piece, sum);
 }
@@ -495,7 +500,7 @@ int segment_of(int64_t n, int64_t width) {
 int64_t most_spans(int64_t n) { return cdiv(n, kMinSegment * (kThreads / 32)); }
 
 struct BwdLayout {
-    size_t keys[2], items[2], present, counts, partial, bytes;
+    size_t pairs[2], present, counts, partial, bytes;
     BwdLayout(int64_t n, int64_t rows, int64_t width) {
         size_t at = 0;
         auto take = [&](size_t b) {
@@ -503,8 +508,7 @@ struct BwdLayout {
             at += (b + 255) / 256 * 256;
             return here;
         };
-        for (int i = 0; i < 2; ++i) keys[i] = take(n * 4);
-        for (int i = 0; i < 2; ++i) items[i] = take(n * 4);
+        for (int i = 0; i < 2; ++i) pairs[i] = take(n * sizeof(KeyItem));
         present = take(rows);
         counts = take(sort_counts_words(n, sort_max_bins(rows)) * 4);
         partial = take(static_cast<size_t>(most_spans(n)) * 2 * width * 4);
@@ -550,30 +554,24 @@ cudaError_t embedding_bwd_launch(const DeviceInfo& dev, int dtype, const Embeddi
     const BwdLayout l(n, in.rows, in.width);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     SortBuffers b{};
-    for (int i = 0; i < 2; ++i) {
-        b.keys[i] = reinterpret_cast<uint32_t*>(ws + l.keys[i]);
-        b.items[i] = reinterpret_cast<int32_t*>(ws + l.items[i]);
-    }
-    b.present = accumulate ? nullptr : ws + l.present;
+    for (int i = 0; i < 2; ++i) b.pairs[i] = reinterpret_cast<KeyItem*>(ws + l.pairs[i]);
     b.counts = reinterpret_cast<uint32_t*>(ws + l.counts);
     b.status = in.status;
     const int64_t row_bytes = static_cast<int64_t>(in.width) * sg, stride_bytes = in.dst_stride * sg;
     ZeroShares z{};
     if (!accumulate) {
-        if (sort_takes_zero_job(n)) {
-            z.sort = std::min(in.rows, cdiv(kZeroBesideSort, row_bytes));
-            char* at = static_cast<char*>(in.dst) + (in.rows - z.sort) * stride_bytes;
-            b.zero = stride_bytes == row_bytes ? ZeroJob{at, z.sort * row_bytes, 0, 1}
-                                               : ZeroJob{at, row_bytes, stride_bytes, z.sort};
-        }
+        z.sort = std::min(in.rows, cdiv(kZeroBesideSort, row_bytes));
+        char* at = static_cast<char*>(in.dst) + (in.rows - z.sort) * stride_bytes;
+        b.zero = stride_bytes == row_bytes ? ZeroJob{at, z.sort * row_bytes, 0, 1}
+                                           : ZeroJob{at, row_bytes, stride_bytes, z.sort};
+        if (z.sort < in.rows) b.present = ws + l.present;
         z.join = std::min((in.rows - z.sort) / 4, kZeroBesideJoin / row_bytes);
     }
     const cudaError_t err = sort_launch(dev, in.k, b, s);
     if (err != cudaSuccess) return err;
     const int result = sort_result(sort_passes(in.k.limit));
     BwdKernelArgs a{};
-    a.keys = b.keys[result];
-    a.items = b.items[result];
+    a.pairs = b.pairs[result];
     a.present = b.present;
     a.dy = in.src;
     a.grad = in.dst;

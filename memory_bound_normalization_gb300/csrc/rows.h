@@ -28,18 +28,19 @@ struct ZeroJob {
     int64_t bytes, stride, rows;
 };
 
-// Stable order of the keys by radix passes: sorted keys and the items they
-// came from. `present`, unless null: limit bytes, 1 where the key occurs.
+// Stable order of the keys by radix passes: pairs of a key and the item it came
+// from. `present`, unless null: limit bytes, 1 where the key occurs.
+struct KeyItem {
+    uint32_t key;
+    int32_t item;
+};
 struct SortBuffers {
-    uint32_t* keys[2];
-    int32_t* items[2];
+    KeyItem* pairs[2];
     uint8_t* present;
     uint32_t* counts;  // sort_counts_words(n, bins) words, null if that is 0
-    ZeroJob zero;      // done on the SMs that a sort by one cluster leaves idle
+    ZeroJob zero;      // done beside the first launch, on the SMs it leaves idle
     int* status;
 };
-// Whether a sort of n keys is one launch, which takes a zero job along.
-bool sort_takes_zero_job(int64_t n);
 int sort_passes(int64_t limit);
 // Words of counts for n items: 0 where one cluster of blocks takes them all.
 int64_t sort_counts_words(int64_t n, int bins);

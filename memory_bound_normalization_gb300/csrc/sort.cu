@@ -33,8 +33,7 @@ constexpr int kMaxExperts = RMSNORM_MAX_EXPERTS;
 
 struct SortArgs {
     KeySource k;
-    uint32_t* keys[2];
-    int32_t* items[2];
+    KeyItem* pairs[2];
     uint8_t* present;
     // many blocks, in clusters of kCluster: [blocks][bins] counts of the cluster's blocks
     // before, then [clusters][bins] counts of the clusters
@@ -81,7 +80,7 @@ __device__ __forceinline__ void load_keys(const SortArgs& a, int pass, unsigned 
     for (int r = 0; r < R; ++r) {
         const unsigned i = first + r * 32 + threadIdx.x % 32;
         key[r] = 0xffffffffu;
-        if (i < a.k.n) key[r] = pass == 0 ? key_at(a.k, i) : a.keys[(pass - 1) & 1][i];
+        if (i < a.k.n) key[r] = pass == 0 ? key_at(a.k, i) : a.pairs[(pass - 1) & 1][i].key;
     }
 }
 __device__ __forceinline__ uint32_t digit_of(const SortArgs& a, int pass, uint32_t key) {
@@ -196,10 +195,9 @@ __device__ __forceinline__ void scatter(const SortArgs& a, int pass, const Smem&
                 a.source[at] = static_cast<int32_t>(i);
         } else {
             const int to = pass & 1;
-            const int32_t item = pass == 0 ? static_cast<int32_t>(i) : a.items[to ^ 1][i];
-            if (!RMSN_OK(at < a.k.n, a.status)) continue;
-            a.keys[to][at] = key[r];
-            a.items[to][at] = item;
+            const uint32_t item = pass == 0 ? i : static_cast<uint32_t>(a.pairs[to ^ 1][i].item);
+            // one store of 8 bytes: scattered ones cost by their number
+            if (RMSN_OK(at < a.k.n, a.status)) *reinterpret_cast<uint2*>(a.pairs[to] + at) = make_uint2(key[r], item);
         }
     }
 }
@@ -276,13 +274,18 @@ __device__ __forceinline__ void sum_warps(const SortArgs& a, const Smem& s, int 
 }
 
 // Rows that are zeroed beside the sort, by block `block` of `blocks`.
-constexpr int64_t kZeroUnit = 32768;  // bytes
+constexpr int64_t kZeroUnit = 65536;  // bytes
 __device__ __forceinline__ void zero_beside(const SortArgs& a, unsigned block, unsigned blocks) {
-    const int64_t slices = ceil_div(a.zero.bytes, kZeroUnit);
-    for (int64_t unit = block; unit < slices * a.zero.rows; unit += blocks) {
-        const int64_t row = unit / slices, from = (unit - row * slices) * kZeroUnit;
-        zero_span(a.zero.at + row * a.zero.stride + from, min(kZeroUnit, a.zero.bytes - from), threadIdx.x, blockDim.x,
-                  a.zero.at, (a.zero.rows - 1) * a.zero.stride + a.zero.bytes, a.status);
+    const ZeroJob& z = a.zero;
+    const int64_t slices = ceil_div(z.bytes, kZeroUnit), extent = (z.rows - 1) * z.stride + z.bytes;
+    auto slice = [&](char* row, int64_t from) {
+        zero_span(row + from, min(kZeroUnit, z.bytes - from), threadIdx.x, blockDim.x, z.at, extent, a.status);
+    };
+    if (z.rows == 1) {
+        for (int64_t i = block; i < slices; i += blocks) slice(z.at, i * kZeroUnit);
+    } else {
+        for (int64_t r = block; r < z.rows; r += blocks)
+            for (int64_t i = 0; i < slices; ++i) slice(z.at + r * z.stride, i * kZeroUnit);
     }
 }
 
@@ -346,7 +349,11 @@ __global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_const
     for (int d = threadIdx.x; d < a.bins; d += blockDim.x) hist[d] = 0;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    if (a.pass == 0) clear_present(a, blockIdx.x, gridDim.x);
+    if (blockIdx.x >= a.blocks) {  // whole clusters
+        zero_beside(a, blockIdx.x - a.blocks, gridDim.x - a.blocks);
+        return;
+    }
+    if (a.pass == 0) clear_present(a, blockIdx.x, a.blocks);
     __syncthreads();
     for (int tile = 0; tile < a.tiles; ++tile) {
         uint32_t key[R];
@@ -456,6 +463,15 @@ cudaError_t allow_smem(const DeviceInfo& dev, SortFn fn) {
     return err;
 }
 
+// Blocks that zero rows beside `blocks` that sort: whole clusters, up to the SMs left,
+// or to as many as sort.
+int zero_blocks(const DeviceInfo& dev, const ZeroJob& z, int blocks, int threads, int cluster) {
+    const int64_t units = z.rows == 1 ? cdiv(z.bytes, kZeroUnit) : z.rows;
+    if (z.bytes == 0 || units == 0) return 0;
+    const int64_t room = std::max(dev.sm_count - blocks, dev.sm_count / 2) * (kThreads / threads);
+    return static_cast<int>(std::max<int64_t>(std::min(units, room) / cluster, 1) * cluster);
+}
+
 cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
     const int64_t n = a.k.n;
     if (n <= kClusterItems) {
@@ -469,19 +485,16 @@ cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
         const SortFn fn = rounds == 1 ? sort_cluster_kernel<1> : SortFn(sort_cluster_kernel<2>);
         const cudaError_t err = allow_smem(dev, fn);
         if (err != cudaSuccess) return err;
-        // blocks that zero rows: whole clusters, up to the SMs left
-        const int64_t units = a.zero.rows * cdiv(a.zero.bytes, kZeroUnit);
-        const int64_t idle =
-            std::min<int64_t>(cdiv(units, 2), (dev.sm_count - blocks) * (kThreads / threads)) / blocks * blocks;
-        const int zero = units > 0 ? static_cast<int>(std::max<int64_t>(idle, blocks)) : 0;
+        const int zero = zero_blocks(dev, a.zero, blocks, threads, blocks);
         return launch_pdl(fn, blocks + zero, threads, sort_smem(a.bins, threads / 32), blocks, s, a);
     }
     const Many m(n);
     a.blocks = m.blocks;
     a.tiles = m.tiles;
     for (a.pass = 0; a.pass < a.passes; ++a.pass) {
-        cudaError_t err = launch_pdl(m.rounds == 1 ? sort_count_kernel<1> : SortFn(sort_count_kernel<2>), m.blocks, kThreads,
-                                     a.bins * 4, kCluster, s, a);
+        const int zero = a.pass == 0 ? zero_blocks(dev, a.zero, m.blocks, kThreads, kCluster) : 0;
+        cudaError_t err = launch_pdl(m.rounds == 1 ? sort_count_kernel<1> : SortFn(sort_count_kernel<2>),
+                                     m.blocks + zero, kThreads, a.bins * 4, kCluster, s, a);
         if (err != cudaSuccess) return err;
         const SortFn fn = m.rounds == 1 ? sort_place_kernel<1> : SortFn(sort_place_kernel<2>);
         err = allow_smem(dev, fn);
@@ -502,15 +515,10 @@ int64_t sort_counts_words(int64_t n, int bins) {
     return static_cast<int64_t>(bins) * (Many(n).blocks + Many(n).blocks / kCluster);
 }
 
-bool sort_takes_zero_job(int64_t n) { return n <= kClusterItems; }
-
 cudaError_t sort_launch(const DeviceInfo& dev, const KeySource& k, const SortBuffers& b, cudaStream_t s) {
     SortArgs a{};
     a.k = k;
-    for (int i = 0; i < 2; ++i) {
-        a.keys[i] = b.keys[i];
-        a.items[i] = b.items[i];
-    }
+    for (int i = 0; i < 2; ++i) a.pairs[i] = b.pairs[i];
     a.present = b.present;
     a.zero = b.zero;
     a.counts = b.counts;
