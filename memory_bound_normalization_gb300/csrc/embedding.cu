@@ -38,12 +38,11 @@ struct FwdKernelArgs {
     int* status;
 };
 
-// Pieces of a lane: small ones need more of them in flight.
-__host__ __device__ constexpr int fwd_pieces(int e) { return e >= 4 ? 4 : 8; }
+constexpr int kFwdPieces = 4;  // of a lane
+
 
 template <typename TT, typename TA, int E>
 __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_constant__ FwdKernelArgs a) {
-    constexpr int kFwdPieces = fwd_pieces(E);
     const unsigned lane = threadIdx.x & (a.shape.lanes - 1);
     const unsigned group = group_index<kThreads>(a.shape.lanes);
     wait_for_prerequisite_grid();
@@ -450,7 +449,8 @@ cudaError_t fwd_typed(int e, const FwdKernelArgs& a, int64_t blocks, cudaStream_
 struct ZeroShares {
     int64_t sort, join;
 };
-constexpr int64_t kZeroBesideSort = 48 << 20, kZeroBesideJoin = 16 << 20;  // bytes
+// bytes: beside a sort by one cluster, beside each launch of another, beside the join
+constexpr int64_t kZeroBesideSort = 48 << 20, kZeroBesidePass = 24 << 20, kZeroBesideJoin = 16 << 20;
 
 int64_t zero_blocks(const BwdKernelArgs& a) {
     return cdiv(cdiv(a.zero_to - a.zero_from, a.zero_rows) * a.zero_slices, kThreads / 32);
@@ -517,7 +517,7 @@ struct BwdLayout {
 };
 
 int64_t fwd_blocks(const EmbeddingArgs& a, int e, RowShape* shape) {
-    *shape = row_shape(a.width / e, fwd_pieces(e));
+    *shape = row_shape(a.width / e, kFwdPieces);
     return cdiv(static_cast<int64_t>(a.k.n) * shape->chunks * shape->lanes, kThreads);
 }
 
@@ -525,7 +525,7 @@ int64_t fwd_blocks(const EmbeddingArgs& a, int e, RowShape* shape) {
 
 bool embedding_fits(int64_t n, int64_t width) {
     // element by element, which takes the most groups; they are counted in 32 bits
-    return n * cdiv(width, 32 * fwd_pieces(1)) <= kMaxGrid && most_spans(n) * cdiv(width, 128) <= kMaxGrid / 2;
+    return n * cdiv(width, 32 * kFwdPieces) <= kMaxGrid && most_spans(n) * cdiv(width, 128) <= kMaxGrid / 2;
 }
 
 cudaError_t embedding_fwd_launch(const DeviceInfo&, int dtype, const EmbeddingArgs& in, cudaStream_t s) {
@@ -560,7 +560,8 @@ cudaError_t embedding_bwd_launch(const DeviceInfo& dev, int dtype, const Embeddi
     const int64_t row_bytes = static_cast<int64_t>(in.width) * sg, stride_bytes = in.dst_stride * sg;
     ZeroShares z{};
     if (!accumulate) {
-        z.sort = std::min(in.rows, cdiv(kZeroBesideSort, row_bytes));
+        const int launches = sort_launches(n, in.k.limit);
+        z.sort = std::min(in.rows, cdiv(launches > 1 ? launches * kZeroBesidePass : kZeroBesideSort, row_bytes));
         char* at = static_cast<char*>(in.dst) + (in.rows - z.sort) * stride_bytes;
         b.zero = stride_bytes == row_bytes ? ZeroJob{at, z.sort * row_bytes, 0, 1}
                                            : ZeroJob{at, row_bytes, stride_bytes, z.sort};

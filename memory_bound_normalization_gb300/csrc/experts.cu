@@ -28,12 +28,12 @@ __host__ __device__ constexpr int gather_pieces(int bytes) { return bytes == 16 
 // by the choices taken together: 128 bytes in flight
 __host__ __device__ constexpr int bwd_pieces(int bytes, int kc) { return 8 / kc * (bytes >= 8 ? 16 / bytes : 4); }
 constexpr int kChoices = 4;     // in flight
-constexpr int kZeroRows = 64;   // of a block
 
 struct KernelArgs {
     ExpertArgs x;
     RowShape shape;
-    unsigned zero_blocks;  // the first ones, which zero rows without a choice
+    unsigned zero_blocks;  // the first ones, which zero rows without a choice,
+    int zero_runs;         // so many times 32 of them a block
     int team;               // threads of a token (gather_bwd)
     // ring: the first blocks' tokens are every main_blocks-th of main_tokens, the
     // others' `tail` each of the rest
@@ -42,19 +42,23 @@ struct KernelArgs {
     int tail;
 };
 
-// Rows without a choice, of kZeroRows: the whole block zeroes one after another.
+// Zeroes those of 32 rows from row0 on that are in `todo`: a warp of several each.
+__device__ __forceinline__ void zero_found(const ExpertArgs& x, int64_t row0, unsigned todo, int warp, int warps, int size) {
+    const int64_t bytes = static_cast<int64_t>(x.width) * size;
+    for (int i = 0; todo; todo &= todo - 1, ++i) {
+        if (i % warps != warp) continue;
+        zero_span(static_cast<char*>(x.out) + (row0 + __ffs(todo) - 1) * x.out_stride * size, bytes, threadIdx.x % 32, 32,
+                  x.out, rows_bytes(x.rows, x.out_stride, x.width, size), x.status);
+    }
+}
+
+// Rows without a choice, of a block's share: all its warps look at the same 32.
 __device__ __forceinline__ void zero_rows(const KernelArgs& a, int size) {
     const ExpertArgs& x = a.x;
-    const int lane = threadIdx.x % 32;
-    for (int half = 0; half < kZeroRows; half += 32) {
-        const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kZeroRows + half;
-        unsigned todo = __ballot_sync(0xffffffffu, row0 + lane < x.rows && x.source[row0 + lane] < 0);
-        while (todo) {
-            const int r = __ffs(todo) - 1;
-            todo &= todo - 1;
-            zero_span(static_cast<char*>(x.out) + (row0 + r) * x.out_stride * size, static_cast<int64_t>(x.width) * size,
-                      threadIdx.x, kThreads, x.out, rows_bytes(x.rows, x.out_stride, x.width, size), x.status);
-        }
+    for (int i = 0; i < a.zero_runs; ++i) {
+        const int64_t row0 = (static_cast<int64_t>(i) * a.zero_blocks + blockIdx.x) * 32, row = row0 + threadIdx.x % 32;
+        const unsigned todo = __ballot_sync(0xffffffffu, row < x.rows && x.source[row] < 0);
+        zero_found(x, row0, todo, threadIdx.x / 32, kThreads / 32, size);
     }
 }
 
@@ -262,17 +266,21 @@ __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __gri
 }
 
 // ---------------------------------------------------------------- by a ring
-// The same for rows of 16-byte pieces: persistent blocks, a token at a time, a piece of
-// each choice's row a thread. The pieces are copied into the thread's own slots of
+// The same for rows that asynchronous copies can move (pieces of 16, 8 or 4 bytes): a
+// token at a time, 16 bytes of each choice's row a thread. The pieces are copied into the thread's own slots of
 // shared memory, D - 1 steps (a step: a token's KC choices of a block's columns) ahead,
-// so no thread waits for another's copies. With loads into registers (the kernel above)
-// 16384 tokens of 8 rows of 2048 bf16 took 221 us: too few bytes on the way.
-template <int KC>
+// so no thread waits for another's copies. For more than four choices of some bytes:
+// 16384 tokens of 8 rows of 2048 bf16 take 178 us, 221 with loads into registers (the
+// kernel above), which of 4 rows take 102 as well, of 2 rows 58 instead of 67, and of
+// 1000 tokens of 8 rows of 256 7 instead of 10.
 struct Ring {
-    static constexpr int kDepth = KC == 8 ? 3 : KC == 4 ? 5 : 8;
-    static constexpr int kSlots = KC + 1;  // of a step: the choices, then dy
+    static constexpr int kChoices = 8;
+    static constexpr int kDepth = 3;
+    static constexpr int kSlots = kChoices + 1;  // of a step: the choices, then dy
     static constexpr int kThreadBytes = kDepth * kSlots * 16;
 };
+
+constexpr int64_t kRingBytes = 8 << 20;  // of rows, from which on
 
 // Sums over a warp of KC values each lane has; lane l returns that of value
 // l / (32 / KC).
@@ -294,15 +302,15 @@ __device__ __forceinline__ float sum_of_lanes(float (&v)[KC]) {
     return s;
 }
 
-template <typename T, typename TW, int KC>
+template <typename T, typename TW, int E>
 __global__ void __launch_bounds__(kThreads) expert_ring_bwd_kernel(const __grid_constant__ KernelArgs a) {
-    using R = Ring<KC>;
-    constexpr int D = R::kDepth, E = Pack<T>::VEC;
+    using R = Ring;
+    constexpr int KC = R::kChoices, D = R::kDepth, kPiece = E * static_cast<int>(sizeof(T)), U = 16 / kPiece;  // a slot holds U pieces
     __shared__ float part[2][kThreads / 32][KC];
     const ExpertArgs& x = a.x;
     const int team = blockDim.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = team / 32;
     const uint32_t slots = smem_u32(rmsn_dynamic_smem) + threadIdx.x * 16;  // [D][slots][team]
-    const int groups = (x.choices + KC - 1) / KC, chunks = (a.shape.pieces + team - 1) / team;
+    const int groups = (x.choices + KC - 1) / KC, chunks = (a.shape.pieces + team * U - 1) / (team * U);
     wait_for_prerequisite_grid();
     allow_dependent_launch();
 
@@ -354,18 +362,20 @@ __global__ void __launch_bounds__(kThreads) expert_ring_bwd_kernel(const __grid_
     int32_t rows0 = rows_of(0), rows1 = rows_of(1), rows2 = -1;  // of this batch and the next ones
     TW weights0 = weights_of(0), weights1{};
     auto issue = [&](const Step& s, int in_batch, int at) {
-        const int p = s.chunk * team + threadIdx.x;
-        const bool live = s.token < end && p < a.shape.pieces;
+        const int p0 = s.chunk * team * U + threadIdx.x;
+        auto copy = [&](int k, const T* row) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (p0 + u * team < a.shape.pieces)
+                    copy_own<kPiece>(slot(at, k) + u * kPiece, row + static_cast<int64_t>(p0 + u * team) * E, x.status);
+        };
+        const bool live = s.token < end;
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
             const int32_t r = __shfl_sync(0xffffffffu, in_batch < kBatch ? rows0 : rows1, in_batch % kBatch * KC + k);
-            if (live && valid(r))
-                copy_own(slot(at, k), static_cast<const T*>(x.in) + r * x.in_stride + static_cast<int64_t>(p) * E,
-                         x.status);
+            if (live && valid(r)) copy(k, static_cast<const T*>(x.in) + r * x.in_stride);
         }
-        if (live)
-            copy_own(slot(at, KC), static_cast<const T*>(x.x) + s.token * x.x_stride + static_cast<int64_t>(p) * E,
-                     x.status);
+        if (live) copy(KC, static_cast<const T*>(x.x) + s.token * x.x_stride);
         copies_commit();
     };
 
@@ -385,13 +395,8 @@ __global__ void __launch_bounds__(kThreads) expert_ring_bwd_kernel(const __grid_
             const unsigned none = __ballot_sync(0xffffffffu, row < x.rows && x.source[row] < 0);
             if (lane == 0) found[warp] = none;
             __syncthreads();
-            for (int w = 0; w < warps; ++w) {
-                const int64_t row0 = ((run0 + w) * a.main_blocks + blockIdx.x) * 32;
-                for (unsigned todo = found[w]; todo; todo &= todo - 1)
-                    zero_span(reinterpret_cast<char*>(static_cast<T*>(x.out) + (row0 + __ffs(todo) - 1) * x.out_stride),
-                              static_cast<int64_t>(x.width) * sizeof(T), threadIdx.x, team, x.out,
-                              rows_bytes(x.rows, x.out_stride, x.width, sizeof(T)), x.status);
-            }
+            for (int w = 0; w < warps; ++w)
+                zero_found(x, ((run0 + w) * a.main_blocks + blockIdx.x) * 32, found[w], warp, warps, sizeof(T));
             __syncthreads();
         }
     }
@@ -407,31 +412,48 @@ __global__ void __launch_bounds__(kThreads) expert_ring_bwd_kernel(const __grid_
         issue(copied, in_batch + D - 1, at == 0 ? D - 1 : at - 1);
         next(copied);
         copies_wait<D - 1>();
-        const int p = here.chunk * team + threadIdx.x;
-        const bool live = p < a.shape.pieces;
+        const int p0 = here.chunk * team * U + threadIdx.x;
         const float weight = to_f32(weights0);
-        Piece<T, E> g;
-        float h[E];
+        // the U pieces of a slot together, as one of 16 bytes
+        Piece<T, U * E> g;
+        float h[U * E];
         g.w[0] = ld_slot(slot(at, KC));
         g.unpack(h);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (U > 1 && p0 + u * team >= a.shape.pieces) h[u * E + e] = 0.f;
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
             const int32_t r = __shfl_sync(0xffffffffu, rows0, in_batch * KC + k);
             const float w = __shfl_sync(0xffffffffu, weight, in_batch * KC + k);
-            if (!valid(r) || !live) continue;
-            Piece<T, E> v;
-            float f[E];
+            if (!valid(r) || p0 >= a.shape.pieces) continue;
+            Piece<T, U * E> v;
+            float f[U * E];
             v.w[0] = ld_slot(slot(at, k));
             v.unpack(f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                dot[k] = fmaf(f[e], h[e], dot[k]);
-                f[e] = w * h[e];
+            for (int u = 0; u < U; ++u) {
+                const bool live = U == 1 || p0 + u * team < a.shape.pieces;
+#pragma unroll
+                for (int e = u * E; e < (u + 1) * E; ++e) {
+                    if (live) dot[k] = fmaf(f[e], h[e], dot[k]);  // what no copy wrote may be anything
+                    f[e] = w * h[e];
+                }
             }
             v.pack(f);
-            T* to = static_cast<T*>(x.out) + r * x.out_stride + static_cast<int64_t>(p) * E;
-            if (RMSN_OK(span_in(to, 16, x.out, rows_bytes(x.rows, x.out_stride, x.width, sizeof(T))), x.status))
-                v.store(to);
+            T* row = static_cast<T*>(x.out) + r * x.out_stride;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                T* to = row + static_cast<int64_t>(p0 + u * team) * E;
+                if (p0 + u * team < a.shape.pieces &&
+                    RMSN_OK(span_in(to, kPiece, x.out, rows_bytes(x.rows, x.out_stride, x.width, sizeof(T))), x.status)) {
+                    Piece<T, E> part;
+                    memcpy(part.w, reinterpret_cast<const char*>(v.w) + u * kPiece, kPiece);
+                    part.store(to);
+                }
+            }
         }
         if (here.chunk + 1 == chunks) {  // the columns are done: the team's sums
             const float s = sum_of_lanes<KC>(dot);
@@ -473,7 +495,12 @@ int piece_of(const ExpertArgs& a, int dtype) {
     return 1;
 }
 
-unsigned zero_blocks(const ExpertArgs& a) { return static_cast<unsigned>(cdiv(a.rows, kZeroRows)); }
+// Blocks that zero rows: 32 rows each, or as many as keep them at one wave.
+void zero_shape(const DeviceInfo& dev, KernelArgs* a) {
+    const int64_t runs = cdiv(a->x.rows, 32), most = dev.sm_count * 4;
+    a->zero_runs = static_cast<int>(cdiv(runs, most));
+    a->zero_blocks = static_cast<unsigned>(a->zero_runs ? cdiv(runs, a->zero_runs) : 0);
+}
 
 // fn(E) for the piece's width
 template <typename T, typename F>
@@ -513,23 +540,24 @@ cudaError_t allow_smem(const DeviceInfo& dev, const void* fn, int bytes) {
     return err;
 }
 
-template <typename T, typename TW, int KC>
+template <typename T, typename TW, int E>
 cudaError_t ring_launch(const DeviceInfo& dev, const KernelArgs& in, cudaStream_t s) {
-    const int pieces = in.shape.pieces, team = pieces <= 32 ? 32 : pieces <= 64 ? 64 : pieces <= 128 ? 128 : kThreads;
-    constexpr int kBytes = Ring<KC>::kThreadBytes;
-    const auto fn = expert_ring_bwd_kernel<T, TW, KC>;
+    constexpr int U = 16 / (E * static_cast<int>(sizeof(T)));
+    const int pieces = static_cast<int>(cdiv(in.shape.pieces, U)), team = pieces <= 32 ? 32 : pieces <= 64 ? 64 : pieces <= 128 ? 128 : kThreads;
+    constexpr int kBytes = Ring::kThreadBytes;
+    const auto fn = expert_ring_bwd_kernel<T, TW, E>;
     const cudaError_t err = allow_smem(dev, reinterpret_cast<const void*>(fn), kBytes * kThreads);
     if (err != cudaSuccess) return err;
     // Blocks of 256 threads two an SM, smaller ones as many more. SMs get up to 15% more
     // or less of the memory's rate than the mean: the blocks that fit at once share
     // 12/16 of the tokens out evenly, and the rest goes in small blocks to SMs as they
     // come free (16384 tokens of 8 rows of 2048 bf16: 205 us with all shared out evenly,
-    // 178 so). Few tokens go in small blocks altogether (777 of 4 rows of 2880 fp32: 23
-    // us shared out, 17 so); the first blocks then only zero rows.
+    // 178 so). Few tokens go in small blocks altogether (2048 of 8 rows: 39 us
+    // shared out, 34 so); the first blocks then only zero rows.
     const int64_t resident = static_cast<int64_t>(dev.sm_count) * 2 * (kThreads / team);
     KernelArgs a = in;
     a.main_tokens = in.x.tokens >= 16 * resident ? in.x.tokens / 16 * 12 : 0;
-    a.tail = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16 / KC, in.x.tokens / resident)));
+    a.tail = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(2, in.x.tokens / resident)));
     a.main_blocks = static_cast<unsigned>(std::min(std::max<int64_t>(a.main_tokens, cdiv(in.x.rows, 32)), resident));
     const int grid = static_cast<int>(a.main_blocks + cdiv(in.x.tokens - a.main_tokens, a.tail));
     return launch_pdl(fn, grid, team, kBytes * team, 1, s, a);
@@ -541,11 +569,11 @@ bool experts_fit(const ExpertArgs& a) {
     return a.tokens * cdiv(a.width, 32 * gather_pieces(2)) <= kMaxGrid;  // groups, element by element
 }
 
-cudaError_t expert_scatter_launch(const DeviceInfo&, int dtype, const ExpertArgs& in, cudaStream_t s) {
-    KernelArgs a{in, {}, 0, 0};
+cudaError_t expert_scatter_launch(const DeviceInfo& dev, int dtype, const ExpertArgs& in, cudaStream_t s) {
+    KernelArgs a{in};
     const int e = piece_of(in, dtype);
     a.shape = row_shape(in.width / e, scatter_pieces(e * dtype_size(dtype)));
-    a.zero_blocks = zero_blocks(in);
+    zero_shape(dev, &a);
     const int grid = static_cast<int>(a.zero_blocks + cdiv(in.tokens * a.shape.chunks * a.shape.lanes, kThreads));
     auto go = [&](auto t) {
         using T = decltype(t);
@@ -558,7 +586,7 @@ cudaError_t expert_scatter_launch(const DeviceInfo&, int dtype, const ExpertArgs
 }
 
 cudaError_t expert_gather_launch(const DeviceInfo&, int dtype, const ExpertArgs& in, cudaStream_t s) {
-    KernelArgs a{in, {}, 0, 0};
+    KernelArgs a{in};
     const int e = piece_of(in, dtype);
     a.shape = row_shape(in.width / e, gather_pieces(e * dtype_size(dtype)));
     const int grid = static_cast<int>(cdiv(in.tokens * a.shape.chunks * a.shape.lanes, kThreads));
@@ -571,18 +599,21 @@ cudaError_t expert_gather_launch(const DeviceInfo&, int dtype, const ExpertArgs&
 }
 
 cudaError_t expert_gather_bwd_launch(const DeviceInfo& dev, int dtype, const ExpertArgs& in, cudaStream_t s) {
-    KernelArgs a{in, {}, 0, 0};
+    KernelArgs a{in};
     const int e = piece_of(in, dtype);
     a.shape.pieces = in.width / e;
-    if (e * dtype_size(dtype) == 16 && a.shape.pieces > 16) {
+    if (in.choices > 4 && e * dtype_size(dtype) >= 4 &&
+        static_cast<int64_t>(in.rows) * in.width * dtype_size(dtype) >= kRingBytes) {
         return with_types(dtype, [&](auto t, auto w) {
-            auto go = [&](auto kc) { return ring_launch<decltype(t), decltype(w), decltype(kc)::value>(dev, a, s); };
-            if (in.choices <= 2) return go(std::integral_constant<int, 2>());
-            if (in.choices <= 4) return go(std::integral_constant<int, 4>());
-            return go(std::integral_constant<int, 8>());
+            using T = decltype(t);
+            return with_piece<T>(e, [&](auto n) {
+                constexpr int E = decltype(n)::value;
+                if constexpr (E * sizeof(T) >= 4) return ring_launch<T, decltype(w), E>(dev, a, s);
+                else return cudaErrorInvalidValue;
+            });
         });
     }
-    a.zero_blocks = zero_blocks(in);
+    zero_shape(dev, &a);
     return with_types(dtype, [&](auto t, auto w) {
         using T = decltype(t);
         return with_piece<T>(e, [&](auto n) {
@@ -596,8 +627,7 @@ cudaError_t expert_gather_bwd_launch(const DeviceInfo& dev, int dtype, const Exp
                 return launch_pdl(expert_gather_bwd_kernel<T, decltype(w), E, U, KC>, grid, kThreads, 0, 1, s, a);
             };
             if (in.choices <= 2) return go(std::integral_constant<int, 2>());
-            if (in.choices <= 4) return go(std::integral_constant<int, 4>());
-            return go(std::integral_constant<int, 8>());
+            return go(std::integral_constant<int, 4>());
         });
     });
 }

