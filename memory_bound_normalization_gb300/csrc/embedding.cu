@@ -17,6 +17,7 @@
 // which blocks of their own zero beside all three launches: the last rows beside
 // the sort, whether they have a token or not, the others by the sort's marks.
 #include <algorithm>
+#include <type_traits>
 
 #include "rows.cuh"
 
@@ -38,44 +39,53 @@ struct FwdKernelArgs {
     int* status;
 };
 
-constexpr int kFwdPieces = 4;  // of a lane
+// Pieces of a lane: small ones need more of them in flight.
+__host__ __device__ constexpr int fwd_pieces(int e) { return e >= 4 ? 4 : 8; }
 
 
-template <typename TT, typename TA, int E>
+template <typename TT, typename TA, int E, int LANES>
 __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_constant__ FwdKernelArgs a) {
-    const unsigned lane = threadIdx.x & (a.shape.lanes - 1);
-    const unsigned group = group_index<kThreads>(a.shape.lanes);
+    constexpr int U = fwd_pieces(E);
+    const int lanes = LANES > 0 ? LANES : a.shape.lanes;
+    const unsigned group = group_index<kThreads>(lanes);
     wait_for_prerequisite_grid();
     allow_dependent_launch();
     const unsigned item = group / a.shape.chunks;
     if (item >= a.k.n) return;
-    const int first = (group - item * a.shape.chunks) * (a.shape.lanes * kFwdPieces) + lane;
+    const int first = (group - item * a.shape.chunks) * (lanes * U) + (threadIdx.x & (lanes - 1));
     const uint32_t row = key_at(a.k, item);
-    const TT* src = static_cast<const TT*>(a.table) + row * a.table_stride;
-    TA* dst = static_cast<TA*>(a.y) + item * a.y_stride;
-    Piece<TT, E> in[kFwdPieces];
+    const bool there = row < a.k.limit;
+    const TT* src = static_cast<const TT*>(a.table) + row * a.table_stride + static_cast<int64_t>(first) * E;
+    TA* dst = static_cast<TA*>(a.y) + item * a.y_stride + static_cast<int64_t>(first) * E;
+    // whole: every piece of the lane is there, so that none has to be asked for
+    auto look_up = [&](auto whole) {
+        auto live = [&](int u) { return decltype(whole)::value || first + u * lanes < a.shape.pieces; };
+        Piece<TT, E> in[U];
 #pragma unroll
-    for (int u = 0; u < kFwdPieces; ++u) {
-        const int p = first + u * a.shape.lanes;
-        in[u].zero();
-        if (p < a.shape.pieces && row < a.k.limit) in[u].load(src + static_cast<int64_t>(p) * E);
-    }
+        for (int u = 0; u < U; ++u) {
+            in[u].zero();
+            if (there && live(u)) in[u].load(src + u * lanes * E);
+        }
 #pragma unroll
-    for (int u = 0; u < kFwdPieces; ++u) {
-        const int p = first + u * a.shape.lanes;
-        float f[E];
-        in[u].unpack(f);
+        for (int u = 0; u < U; ++u) {
+            float f[E];
+            in[u].unpack(f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] *= a.scale;
-        Piece<TA, E> out;
-        out.pack(f);
-        TA* to = dst + static_cast<int64_t>(p) * E;
-        if (p < a.shape.pieces &&
-            RMSN_OK(span_in(to, E * sizeof(TA), a.y,
-                            rows_bytes(a.k.n, a.y_stride, static_cast<int64_t>(a.shape.pieces) * E, sizeof(TA))),
-                    a.status))
-            out.store(to);
-    }
+            for (int e = 0; e < E; ++e) f[e] *= a.scale;
+            Piece<TA, E> out;
+            out.pack(f);
+            TA* to = dst + u * lanes * E;
+            if (live(u) && RMSN_OK(span_in(to, E * sizeof(TA), a.y,
+                                           rows_bytes(a.k.n, a.y_stride, static_cast<int64_t>(a.shape.pieces) * E,
+                                                      sizeof(TA))),
+                                   a.status))
+                out.store(to);
+        }
+    };
+    if (E < 4 && LANES > 0 && first - static_cast<int>(threadIdx.x & 31) + 32 * U <= a.shape.pieces)
+        look_up(std::true_type());
+    else
+        look_up(std::false_type());
 }
 
 struct BwdKernelArgs {
@@ -435,13 +445,18 @@ int piece_of(const void* p, int64_t ps, int size_p, const void* q, int64_t qs, i
 
 template <typename TT, typename TA>
 cudaError_t fwd_typed(int e, const FwdKernelArgs& a, int64_t blocks, cudaStream_t s) {
-    auto go = [&](auto fn) { return launch_pdl(fn, static_cast<int>(blocks), kThreads, 0, 1, s, a); };
+    auto go = [&](auto n) {
+        return with_lanes(a.shape.lanes, [&](auto lanes) {
+            return launch_pdl(embedding_fwd_kernel<TT, TA, decltype(n)::value, decltype(lanes)::value>,
+                              static_cast<int>(blocks), kThreads, 0, 1, s, a);
+        });
+    };
     if constexpr (sizeof(TT) == 2) {
-        if (e == 8) return go(embedding_fwd_kernel<TT, TA, 8>);
+        if (e == 8) return go(std::integral_constant<int, 8>());
     }
-    if (e == 4) return go(embedding_fwd_kernel<TT, TA, 4>);
-    if (e == 2) return go(embedding_fwd_kernel<TT, TA, 2>);
-    return go(embedding_fwd_kernel<TT, TA, 1>);
+    if (e == 4) return go(std::integral_constant<int, 4>());
+    if (e == 2) return go(std::integral_constant<int, 2>());
+    return go(std::integral_constant<int, 1>());
 }
 
 // Rows that each of the three launches zeroes: the last ones beside the sort, the
@@ -517,7 +532,7 @@ struct BwdLayout {
 };
 
 int64_t fwd_blocks(const EmbeddingArgs& a, int e, RowShape* shape) {
-    *shape = row_shape(a.width / e, kFwdPieces);
+    *shape = row_shape(a.width / e, fwd_pieces(e));
     return cdiv(static_cast<int64_t>(a.k.n) * shape->chunks * shape->lanes, kThreads);
 }
 
@@ -525,7 +540,7 @@ int64_t fwd_blocks(const EmbeddingArgs& a, int e, RowShape* shape) {
 
 bool embedding_fits(int64_t n, int64_t width) {
     // element by element, which takes the most groups; they are counted in 32 bits
-    return n * cdiv(width, 32 * kFwdPieces) <= kMaxGrid && most_spans(n) * cdiv(width, 128) <= kMaxGrid / 2;
+    return n * cdiv(width, 32 * fwd_pieces(1)) <= kMaxGrid && most_spans(n) * cdiv(width, 128) <= kMaxGrid / 2;
 }
 
 cudaError_t embedding_fwd_launch(const DeviceInfo&, int dtype, const EmbeddingArgs& in, cudaStream_t s) {

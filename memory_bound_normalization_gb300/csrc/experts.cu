@@ -14,6 +14,7 @@
 // `source` (by the last ones they were the tail of the call).
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "own_copy.cuh"
 #include "rows.cuh"
@@ -62,110 +63,114 @@ __device__ __forceinline__ void zero_rows(const KernelArgs& a, int size) {
     }
 }
 
-template <typename T, int E>
+template <typename T, int E, int LANES>
 __global__ void __launch_bounds__(kThreads) expert_scatter_kernel(const __grid_constant__ KernelArgs a) {
     constexpr int kScatterPieces = scatter_pieces(E * sizeof(T));
     const ExpertArgs& x = a.x;
+    const int lanes = LANES > 0 ? LANES : a.shape.lanes;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
     if (blockIdx.x < a.zero_blocks) {
         zero_rows(a, sizeof(T));
         return;
     }
-    const unsigned group = group_index<kThreads>(a.shape.lanes, a.zero_blocks);
+    const unsigned group = group_index<kThreads>(lanes, a.zero_blocks);
     const unsigned token = group / a.shape.chunks;
     if (token >= x.tokens) return;
-    const int first =
-        (group - token * a.shape.chunks) * (a.shape.lanes * kScatterPieces) + (threadIdx.x & (a.shape.lanes - 1));
-    const T* src = static_cast<const T*>(x.x) + token * x.x_stride;
+    const int first = (group - token * a.shape.chunks) * (lanes * kScatterPieces) + (threadIdx.x & (lanes - 1));
+    const T* src = static_cast<const T*>(x.x) + token * x.x_stride + static_cast<int64_t>(first) * E;
     Piece<T, E> v[kScatterPieces];
 #pragma unroll
     for (int u = 0; u < kScatterPieces; ++u) {
-        const int p = first + u * a.shape.lanes;
         v[u].zero();
-        if (p < a.shape.pieces) v[u].load(src + static_cast<int64_t>(p) * E);
+        if (first + u * lanes < a.shape.pieces) v[u].load(src + u * lanes * E);
     }
     const int32_t* pos = x.position + static_cast<int64_t>(token) * x.choices;
     for (int k = 0; k < x.choices; ++k) {
         const int32_t row = pos[k];
         if (static_cast<uint32_t>(row) >= static_cast<uint32_t>(x.rows)) continue;
-        T* to = static_cast<T*>(x.out) + row * x.out_stride;
+        T* to = static_cast<T*>(x.out) + row * x.out_stride + static_cast<int64_t>(first) * E;
 #pragma unroll
         for (int u = 0; u < kScatterPieces; ++u) {
-            const int p = first + u * a.shape.lanes;
-            if (p < a.shape.pieces &&
-                RMSN_OK(span_in(to + static_cast<int64_t>(p) * E, E * sizeof(T), x.out,
+            if (first + u * lanes < a.shape.pieces &&
+                RMSN_OK(span_in(to + u * lanes * E, E * sizeof(T), x.out,
                                 rows_bytes(x.rows, x.out_stride, x.width, sizeof(T))),
                         x.status))
-                v[u].store(to + static_cast<int64_t>(p) * E);
+                v[u].store(to + u * lanes * E);
         }
     }
 }
 
-template <typename T, typename TW, int E>
-__global__ void __launch_bounds__(kThreads) expert_gather_kernel(const __grid_constant__ KernelArgs a) {
+template <typename T, typename TW, int E, int LANES>
+__global__ void __launch_bounds__(kThreads, E >= 4 ? 4 : 3) expert_gather_kernel(const __grid_constant__ KernelArgs a) {
     constexpr int kGatherPieces = gather_pieces(E * sizeof(T));
     const ExpertArgs& x = a.x;
+    const int lanes = LANES > 0 ? LANES : a.shape.lanes;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    const unsigned group = group_index<kThreads>(a.shape.lanes, a.zero_blocks);
+    const unsigned group = group_index<kThreads>(lanes);
     const unsigned token = group / a.shape.chunks;
     if (token >= x.tokens) return;
-    const int first =
-        (group - token * a.shape.chunks) * (a.shape.lanes * kGatherPieces) + (threadIdx.x & (a.shape.lanes - 1));
+    const int first = (group - token * a.shape.chunks) * (lanes * kGatherPieces) + (threadIdx.x & (lanes - 1));
+    const int64_t column = static_cast<int64_t>(first) * E;
     float sum[kGatherPieces][E];
+    // whole: every piece of the lane is there, so that none has to be asked for
+    auto gather = [&](auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
+        auto live = [&](int u) { return kWhole || first + u * lanes < a.shape.pieces; };
+        const T* res = static_cast<const T*>(x.x) + token * x.x_stride + column;
 #pragma unroll
-    for (int u = 0; u < kGatherPieces; ++u) {
-        const int p = first + u * a.shape.lanes;
-        Piece<T, E> v;
-        v.zero();
-        if (x.x != nullptr && p < a.shape.pieces)
-            v.load(static_cast<const T*>(x.x) + token * x.x_stride + static_cast<int64_t>(p) * E);
-        v.unpack(sum[u]);
-    }
-    const int32_t* pos = x.position + static_cast<int64_t>(token) * x.choices;
-    const TW* wgt = static_cast<const TW*>(x.weights) + static_cast<int64_t>(token) * x.choices;
-    for (int k0 = 0; k0 < x.choices; k0 += kChoices) {
-        Piece<T, E> v[kChoices][kGatherPieces];
-        float w[kChoices];
-        bool there[kChoices];
+        for (int u = 0; u < kGatherPieces; ++u) {
+            Piece<T, E> v;
+            v.zero();
+            if (x.x != nullptr && live(u)) v.load(res + u * lanes * E);
+            v.unpack(sum[u]);
+        }
+        const int32_t* pos = x.position + static_cast<int64_t>(token) * x.choices;
+        const TW* wgt = static_cast<const TW*>(x.weights) + static_cast<int64_t>(token) * x.choices;
+        for (int k0 = 0; k0 < x.choices; k0 += kChoices) {
+            Piece<T, E> v[kChoices][kGatherPieces];
+            float w[kChoices];
+            bool there[kChoices];
 #pragma unroll
-        for (int k = 0; k < kChoices; ++k) {
-            const int32_t row = k0 + k < x.choices ? pos[k0 + k] : -1;
-            there[k] = static_cast<uint32_t>(row) < static_cast<uint32_t>(x.rows);
-            w[k] = there[k] && x.weights != nullptr ? to_f32(wgt[k0 + k]) : 1.f;
-            const T* src = static_cast<const T*>(x.in) + row * x.in_stride;
+            for (int k = 0; k < kChoices; ++k) {
+                const int32_t row = k0 + k < x.choices ? pos[k0 + k] : -1;
+                there[k] = static_cast<uint32_t>(row) < static_cast<uint32_t>(x.rows);
+                w[k] = there[k] && x.weights != nullptr ? to_f32(wgt[k0 + k]) : 1.f;
+                const T* src = static_cast<const T*>(x.in) + row * x.in_stride + column;
 #pragma unroll
-            for (int u = 0; u < kGatherPieces; ++u) {
-                const int p = first + u * a.shape.lanes;
-                v[k][u].zero();
-                if (there[k] && p < a.shape.pieces) v[k][u].load(src + static_cast<int64_t>(p) * E);
+                for (int u = 0; u < kGatherPieces; ++u) {
+                    v[k][u].zero();
+                    if (there[k] && live(u)) v[k][u].load(src + u * lanes * E);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kChoices; ++k) {
+                if (!there[k]) continue;  // also where its weight is infinite or NaN
+#pragma unroll
+                for (int u = 0; u < kGatherPieces; ++u) {
+                    float f[E];
+                    v[k][u].unpack(f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sum[u][e] = fmaf(w[k], f[e], sum[u][e]);
+                }
             }
         }
+        T* to = static_cast<T*>(x.out) + token * x.out_stride + column;
 #pragma unroll
-        for (int k = 0; k < kChoices; ++k) {
-            if (!there[k]) continue;  // also where its weight is infinite or NaN
-#pragma unroll
-            for (int u = 0; u < kGatherPieces; ++u) {
-                float f[E];
-                v[k][u].unpack(f);
-#pragma unroll
-                for (int e = 0; e < E; ++e) sum[u][e] = fmaf(w[k], f[e], sum[u][e]);
-            }
+        for (int u = 0; u < kGatherPieces; ++u) {
+            Piece<T, E> out;
+            out.pack(sum[u]);
+            if (live(u) && RMSN_OK(span_in(to + u * lanes * E, E * sizeof(T), x.out,
+                                           rows_bytes(x.tokens, x.out_stride, x.width, sizeof(T))),
+                                   x.status))
+                out.store(to + u * lanes * E);
         }
-    }
-    T* to = static_cast<T*>(x.out) + token * x.out_stride;
-#pragma unroll
-    for (int u = 0; u < kGatherPieces; ++u) {
-        const int p = first + u * a.shape.lanes;
-        Piece<T, E> out;
-        out.pack(sum[u]);
-        if (p < a.shape.pieces &&
-            RMSN_OK(span_in(to + static_cast<int64_t>(p) * E, E * sizeof(T), x.out,
-                            rows_bytes(x.tokens, x.out_stride, x.width, sizeof(T))),
-                    x.status))
-            out.store(to + static_cast<int64_t>(p) * E);
-    }
+    };
+    if (E * sizeof(T) < 8 && LANES > 0 && first - static_cast<int>(threadIdx.x & 31) + 32 * kGatherPieces <= a.shape.pieces)
+        gather(std::true_type());
+    else
+        gather(std::false_type());
 }
 
 // A team of threads (a power of two, 4 to 256) takes a token and all its columns, KC
@@ -197,34 +202,34 @@ __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __gri
             if (static_cast<uint32_t>(row[k]) >= static_cast<uint32_t>(x.rows)) row[k] = -1;
             dot[k] = 0.f;
         }
+        const int step = team * E;
         for (int c = lane; c < (live ? a.shape.pieces : 0); c += team * U) {
+            const int64_t column = static_cast<int64_t>(c) * E;
+            const int count = (a.shape.pieces - c + team - 1) / team;  // of this thread's pieces
             Piece<T, E> g[U], v[KC][U];
+            const T* src = dy + column;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int p = c + u * team;
+            for (int u = 0; u < U; ++u, src += step) {
                 g[u].zero();
-                if (p < a.shape.pieces) g[u].load(dy + static_cast<int64_t>(p) * E);
+                if (u < count) g[u].load(src);
             }
 #pragma unroll
             for (int k = 0; k < KC; ++k) {
-                const T* src = static_cast<const T*>(x.in) + row[k] * x.in_stride;
+                src = static_cast<const T*>(x.in) + row[k] * x.in_stride + column;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int p = c + u * team;
+                for (int u = 0; u < U; ++u, src += step) {
                     v[k][u].zero();
-                    if (row[k] >= 0 && p < a.shape.pieces) v[k][u].load(src + static_cast<int64_t>(p) * E);
+                    if (row[k] >= 0 && u < count) v[k][u].load(src);
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int p = c + u * team;
-                float h[E];
-                g[u].unpack(h);
+            for (int k = 0; k < KC; ++k) {
+                if (row[k] < 0) continue;
+                T* to = static_cast<T*>(x.out) + row[k] * x.out_stride + column;
 #pragma unroll
-                for (int k = 0; k < KC; ++k) {
-                    if (row[k] < 0) continue;
-                    T* to = static_cast<T*>(x.out) + row[k] * x.out_stride + static_cast<int64_t>(p) * E;
-                    float f[E];
+                for (int u = 0; u < U; ++u, to += step) {
+                    float f[E], h[E];
+                    g[u].unpack(h);
                     v[k][u].unpack(f);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __gri
                     }
                     Piece<T, E> out;
                     out.pack(f);
-                    if (p < a.shape.pieces &&
+                    if (u < count &&
                         RMSN_OK(span_in(to, E * sizeof(T), x.out, rows_bytes(x.rows, x.out_stride, x.width, sizeof(T))),
                                 x.status))
                         out.store(to);
@@ -578,7 +583,10 @@ cudaError_t expert_scatter_launch(const DeviceInfo& dev, int dtype, const Expert
     auto go = [&](auto t) {
         using T = decltype(t);
         return with_piece<T>(e, [&](auto n) {
-            return launch_pdl(expert_scatter_kernel<T, decltype(n)::value>, grid, kThreads, 0, 1, s, a);
+            return with_lanes(a.shape.lanes, [&](auto l) {
+                return launch_pdl(expert_scatter_kernel<T, decltype(n)::value, decltype(l)::value>, grid, kThreads, 0, 1,
+                                  s, a);
+            });
         });
     };
     // a copy: the type's size alone counts
@@ -593,7 +601,10 @@ cudaError_t expert_gather_launch(const DeviceInfo&, int dtype, const ExpertArgs&
     return with_types(dtype, [&](auto t, auto w) {
         using T = decltype(t);
         return with_piece<T>(e, [&](auto n) {
-            return launch_pdl(expert_gather_kernel<T, decltype(w), decltype(n)::value>, grid, kThreads, 0, 1, s, a);
+            return with_lanes(a.shape.lanes, [&](auto l) {
+                return launch_pdl(expert_gather_kernel<T, decltype(w), decltype(n)::value, decltype(l)::value>, grid,
+                                  kThreads, 0, 1, s, a);
+            });
         });
     });
 }

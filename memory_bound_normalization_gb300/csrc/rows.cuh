@@ -161,6 +161,12 @@ inline RowShape row_shape(int pieces, int u) {
     r.chunks = static_cast<int>(cdiv(pieces, static_cast<int64_t>(r.lanes) * u));
     return r;
 }
+// Calls fn with the group's lanes: a constant where they are a whole warp, whose
+// pieces then lie at constant offsets.
+template <typename F>
+cudaError_t with_lanes(int lanes, F fn) {
+    return lanes == 32 ? fn(std::integral_constant<int, 32>()) : fn(std::integral_constant<int, 0>());
+}
 // Whether rows of `bytes` pieces can be moved from p.
 inline bool piece_fits(const void* p, int64_t stride, int size, int e) {
     const int bytes = e * size > 16 ? 16 : e * size;
