@@ -248,21 +248,15 @@ class QKNormRope(torch.nn.Module):
 
 def _one_stride(t):
     """t, or a dense copy where its rows have no one stride (a broadcast gradient)."""
-    if t.numel() and (t.stride(-1) != 1 or t.stride() != _dense_strides(t)):
-        return t.contiguous()
-    return t
-
-
-def _dense_strides(t):
-    """Strides of rows of the stride that t's have, laid out one after another."""
-    step = t.stride(-2) if t.dim() > 1 else 0
-    out = [1]
-    for n in reversed(t.shape[1:-1] if t.dim() > 1 else ()):
-        out.append(step)
-        step *= n
-    if t.dim() > 1:
-        out.append(step)
-    return tuple(reversed(out))
+    if t.numel() == 0:
+        return t
+    rows, step, fits = 1, None, t.shape[-1] == 1 or t.stride(-1) == 1
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size != 1:
+            step = stride if step is None else step
+            fits = fits and stride == rows * step
+            rows *= size
+    return t if fits else t.contiguous()
 
 
 class _EmbeddingFn(torch.autograd.Function):

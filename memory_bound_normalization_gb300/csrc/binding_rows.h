@@ -180,14 +180,14 @@ PyObject* expert_sort(PyObject*, PyObject* const* a, Py_ssize_t) {
         const int64_t E = integer(a[1]), align = integer(a[2]);
         if (!is_index(experts) || experts.dim() < 1 || experts.size(-1) < 1)
             refuse("experts " + text(experts) + ": expected int32 or int64 [..., choices]");
-        on_gpu(experts);
-        dense(experts);
         const int64_t K = experts.size(-1), T = experts.numel() / K;
         const int64_t R = g_rows.expert_rows(T, K, E, align);
         if (R < 0)
             refuse("experts " + text(experts) + " of " + std::to_string(E) + " experts aligned to " +
                    std::to_string(align) + ": 1 to " + std::to_string(RMSNORM_MAX_EXPERTS) +
                    " experts, an alignment of 1 or more, rows up to 2^31-1");
+        on_gpu(experts);
+        dense(experts);
         Run run(experts, a[3]);
         // one allocation for the four: each cost as much as a fourth of the kernel
         auto room = [](int64_t n) { return (n + 3) / 4 * 4; };
@@ -306,7 +306,6 @@ PyObject* expert_combine_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
         Experts e(rows, position);
         check_weights(w, position, rows);
         const int code = dtype_code(rows, w);
-        on_gpu(rows);
         const Rows r(rows, "rows");
         e.d.rows = r.n;
         e.d.width = e.d.token_stride = r.width;
@@ -319,6 +318,7 @@ PyObject* expert_combine_forward(PyObject*, PyObject* const* a, Py_ssize_t) {
             same_device(rows, residual);
             e.d.residual_stride = Rows(*residual, "residual").stride;
         }
+        on_gpu(rows);
         Run run(rows, a[4]);
         const at::Tensor y = by_token(position, r.width, rows);
         const void *pr = rows.const_data_ptr(), *pw = data(w), *ph = data(residual);

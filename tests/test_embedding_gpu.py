@@ -198,3 +198,11 @@ def test_offsets_past_32_bits():
     assert torch.equal(grad[V - 2], dy[2]) and torch.equal(grad[0], dy[1])
     ref.close(grad[V - 1], dy[0].double() + dy[3].double())
     assert not grad[1:V - 2].any()
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _status():
+    """No kernel of this module recorded a failure (of the checked build, a store
+    outside its tensor)."""
+    yield
+    assert pkg.rmsnorm_get_last_device_error() == pkg.OK

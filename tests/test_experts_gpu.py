@@ -225,3 +225,11 @@ def test_offsets_past_32_bits():
     dots = (x[-1].double() ** 2).sum()
     ref.close(dw[-1], dots.expand(2), H, dots)
     assert not dw[:-1].any()
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _status():
+    """No kernel of this module recorded a failure (of the checked build, a store
+    outside its tensor)."""
+    yield
+    assert pkg.rmsnorm_get_last_device_error() == pkg.OK

@@ -1,6 +1,7 @@
 """64-bit references of the operators that move rows by an index, and how far
-a result may be off: half a step of its type for the one rounding, and
-terms * 2^-24 of the sum of magnitudes for fp32 sums in any order."""
+a result may be off: half a step of its type for the one rounding, 2^-24 of it for
+the scale's product in fp32, and terms * 2^-24 of the sum of magnitudes for fp32
+sums in any order."""
 from __future__ import annotations
 
 import torch
@@ -21,7 +22,7 @@ def bound(ref, dtype, terms=0, magnitude=0.0):
     sum (tensors or numbers)."""
     sums = (terms + 2) * 2.0 ** -24 * magnitude
     half = torch.finfo(dtype).eps / 2
-    return sums + half * (ref.abs() + sums) + 2.0 ** -23 * ref.abs() + TINY[dtype]
+    return sums + half * (ref.abs() + sums) + 2.0 ** -24 * ref.abs() + TINY[dtype]
 
 
 def close(got, ref, terms=0, magnitude=0.0):
