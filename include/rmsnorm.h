@@ -450,8 +450,8 @@ int rmsnorm_embedding_fwd(const rmsnorm_embedding_t *embedding,
  * neither read nor written). dtype names the types of dy and of grad (as of y
  * and the table). Tokens are sorted by id, so every row's sum is fp32 in an
  * order that the sizes alone fix, rounded once: the same bits on every run,
- * no floating-point atomics. Three launches; two, and two for each nine bits of
- * num_rows, past 16384 tokens. Workspace and errors as the norm's backward
+ * no floating-point atomics. One launch of up to 256 tokens, three, and past 16384
+ * tokens two and two for each nine bits of num_rows. Workspace and errors as the norm's backward
  * (RMSNORM_ERR_NOMEM), arguments as the forward's.
  */
 int rmsnorm_embedding_bwd(const rmsnorm_embedding_t *embedding,
@@ -471,8 +471,8 @@ int rmsnorm_embedding_bwd_ws(const rmsnorm_embedding_t *embedding,
                              void *workspace, size_t workspace_bytes,
                              cudaStream_t stream);
 
-/* Bytes of workspace rmsnorm_embedding_bwd_ws needs; 0 without tokens or if
-   the arguments are invalid. */
+/* Bytes of workspace rmsnorm_embedding_bwd_ws needs; 0 for up to 256 tokens or
+   if the arguments are invalid. */
 size_t rmsnorm_embedding_bwd_workspace_size(int64_t tokens, int64_t num_rows,
                                             int64_t width);
 

@@ -73,6 +73,11 @@ struct Piece {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) reinterpret_cast<W*>(p)[i] = w[i];
     }
+    // not to be kept in L2
+    __device__ __forceinline__ void store_streamed(T* p) const {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) __stcs(reinterpret_cast<W*>(p) + i, w[i]);
+    }
     __device__ __forceinline__ void unpack(float (&f)[E]) const {
         if constexpr (sizeof(T) == 2 && E % 2 == 0) {
             uint32_t u[E / 2];

@@ -13,7 +13,8 @@ pkg = pytest.importorskip("memory_bound_normalization_gb300")
 DEV = "cuda"
 # tokens, rows of the table, width: one of each; less and more than a warp; widths of
 # 16-, 8-, 4- and 2-byte pieces; more tokens than one cluster sorts (131072)
-SHAPES = [(1, 1, 1), (1, 7, 4096), (3, 5, 8), (33, 10, 40), (257, 1000, 1412), (1021, 50, 129),
+SHAPES = [(1, 1, 1), (1, 7, 4096), (3, 5, 8), (33, 10, 40), (256, 70000, 24), (200, 3, 4104),
+          (255, 40, 77), (257, 1000, 1412), (1021, 50, 129),
           (4097, 3, 64), (5000, 70000, 24), (31, 300, 20000), (131072, 511, 16), (131073, 512, 6),
           (140001, 5, 3), (300000, 400000, 2)]
 
@@ -62,7 +63,7 @@ def test_backward(shape, pair):
 
 
 @pytest.mark.parametrize("which", ["same", "two", "none", "each", "outside"])
-@pytest.mark.parametrize("n", [1, 31, 32, 33, 64, 2048, 9000, 131073])
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 64, 255, 256, 257, 2048, 9000, 131073])
 def test_runs(which, n):
     """One id for all, two in turn, none, an id for each: runs over many segments
     and none."""
@@ -76,9 +77,10 @@ def test_runs(which, n):
     ref.close(grad, want, terms, magnitude)
 
 
+@pytest.mark.parametrize("n", [100, 700])
 @pytest.mark.parametrize("pair", ref.PAIRS, ids=ref.pair_id)
-def test_accumulate(pair):
-    n, V, H = 700, 90, 72
+def test_accumulate(pair, n):
+    V, H = 90, 72
     ids, dy = tokens(n, V // 2), normal(n, H, dtype=pair[0])
     grad = normal(V, H, dtype=pair[1], seed=5)
     before = grad.clone()

@@ -99,7 +99,8 @@ def test_model_with_gradients():
     wloss.backward()
     logits, want = logits.detach().double(), want.detach()
     assert float((logits - want).abs().max()) <= 2.0 ** -12 * float(want.abs().max())
-    assert abs(float(loss) - float(wloss)) <= 2.0 ** -12 * abs(float(wloss))
+    loss, wloss = float(loss.detach()), float(wloss.detach())
+    assert abs(loss - wloss) <= 2.0 ** -12 * abs(wloss)
     for n in p:
         a, b = p[n].grad.double(), q[n].grad
         assert float((a - b).abs().max()) <= 2.0 ** -12 * float(b.abs().max()), n

@@ -40,7 +40,7 @@ def expert_descriptor(T, K, R, H, stride=None):
 
 
 # ------------------------------------------------------------- workspaces
-@pytest.mark.parametrize("shape", [(40, 90, 64), (5000, 7001, 40), (20000, 300, 33), (17000, 100000, 8)],
+@pytest.mark.parametrize("shape", [(257, 90, 64), (5000, 7001, 40), (20000, 300, 33), (17000, 100000, 8)],
                          ids=emb.shape_id)
 def test_embedding_workspace(shape):
     n, V, H = shape

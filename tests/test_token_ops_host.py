@@ -114,7 +114,8 @@ def test_workspace_sizes():
     size = pkg.rmsnorm_embedding_bwd_workspace_size
     assert size(0, 10, 8) == 0 and size(-1, 10, 8) == 0 and size(5, 0, 8) == 0 and size(5, 10, 0) == 0
     assert size(1 << 31, 10, 8) == 0 and size(BIG, 10, BIG) == 0
-    assert 0 < size(1, 1, 1) <= size(1000, 10, 8) <= size(100000, 10, 8) <= size(100000, 1 << 20, 8)
+    assert size(256, 1 << 20, 4096) == 0  # sorted on chip
+    assert 0 < size(257, 1, 1) <= size(1000, 10, 8) <= size(100000, 10, 8) <= size(100000, 1 << 20, 8)
     assert pkg.rmsnorm_expert_sort_workspace_size(16, 8, 128) == 0
     assert pkg.rmsnorm_expert_sort_workspace_size(1 << 20, 8, 128) > 0
     assert pkg.rmsnorm_expert_sort_workspace_size(1 << 20, 8, 2000) == 0
