@@ -40,13 +40,17 @@ struct FwdKernelArgs {
     int* status;
 };
 
-// Pieces of a lane: small ones need more of them in flight.
-__host__ __device__ constexpr int fwd_pieces(int e) { return e >= 4 ? 4 : 8; }
+// Pieces of a lane: 8 where they are small or rows are many and end early in a second
+// chunk of 4, else 4.
+constexpr int kFwdPieces = 8;
+bool fwd_by_four(int e, int pieces, int64_t rows) {
+    const int64_t by4 = cdiv(pieces, 32 * 4), by8 = cdiv(pieces, 32 * 8);
+    return e >= 4 && (2 * by8 > by4 || rows * by4 < kFullWarps);
+}
 
 
-template <typename TT, typename TA, int E, int LANES>
+template <typename TT, typename TA, int E, int U, int LANES>
 __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_constant__ FwdKernelArgs a) {
-    constexpr int U = fwd_pieces(E);
     const int lanes = LANES > 0 ? LANES : a.shape.lanes;
     const unsigned group = group_index<kThreads>(lanes);
     wait_for_prerequisite_grid();
@@ -65,8 +69,11 @@ __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_co
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             in[u].zero();
-            if (there && live(u)) in[u].load(src + u * lanes * E);
+            // a frequent token's row is in many warps' hands: from L2 alone, 22400 tokens of 22
+            // rows of 520 fp32 waited for the few lines that hold them (14.8 us)
+            if (there && live(u)) in[u].load_shared_row(src + u * lanes * E);
         }
+        asm volatile("" ::: "memory");  // every load before the first store
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float f[E];
@@ -107,7 +114,7 @@ struct BwdKernelArgs {
     int segment;          // tokens of a group
     int span;             // tokens of a block
     int64_t zero_to;  // rows before it are zeroed beside the sums where they have no token
-    int zero_rows, zero_slices;  // rows of a warp's share, shares of a row
+    int zero_rows, zero_slices;  // rows of a warp's share (whole 32s, if more), shares of a row
     int accumulate;
     float scale;
     int* status;
@@ -342,43 +349,38 @@ __device__ __forceinline__ void add_tokens(const BwdKernelArgs& a, const Staged&
     }
 }
 
-// Zeroes rows without a token: a warp takes a few rows, or a part of a long one.
-// absent(row0, rows): those of the rows from row0 on that have none, a bit each.
-template <typename TG, typename Absent>
-__device__ __forceinline__ void zero_unit(const BwdKernelArgs& a, int64_t width, int64_t unit, Absent absent) {
-    const int lane = threadIdx.x % 32;
-    const int64_t part = a.zero_slices == 1 ? unit : unit / a.zero_slices;
-    const int slice = static_cast<int>(unit - part * a.zero_slices);
-    const int64_t row0 = part * a.zero_rows;
-    const int rows = static_cast<int>(min(static_cast<int64_t>(a.zero_rows), a.zero_to - row0));
-    unsigned todo = absent(row0, rows);
-    const int64_t row_bytes = width * static_cast<int>(sizeof(TG));
-    const int64_t from = static_cast<int64_t>(slice) * kZeroBytes;
-    if (row_bytes <= 256 && row_bytes % 16 == 0 && a.grad_stride == width &&
-        reinterpret_cast<uintptr_t>(a.grad) % 16 == 0) {  // short rows by their words, not one after another
-        const int words = static_cast<int>(row_bytes) / 16;
-        char* to = reinterpret_cast<char*>(static_cast<TG*>(a.grad) + row0 * width);
-        for (int i = lane; i < rows * words; i += 32)
-            if (todo >> (i / words) & 1 &&
-                RMSN_OK(span_in(to + i * 16, 16, a.grad, rows_bytes(a.rows, width, width, sizeof(TG))), a.status))
-                *reinterpret_cast<uint4*>(to + i * 16) = make_uint4(0, 0, 0, 0);
-        return;
-    }
-    while (todo) {
-        const int r = __ffs(todo) - 1;
-        todo &= todo - 1;
-        char* row = reinterpret_cast<char*>(static_cast<TG*>(a.grad) + (row0 + r) * a.grad_stride);
-        zero_span(row + from, min(static_cast<int64_t>(kZeroBytes), row_bytes - from), lane, 32, a.grad,
-                  rows_bytes(a.rows, a.grad_stride, width, sizeof(TG)), a.status);
-    }
-}
+// Zeroes rows without a token: a warp takes some 16 KB, rows or a part of a long one.
+// absent(row0, rows): those of up to 32 rows from row0 on that have none, a bit each.
 template <typename TG, int E, typename Absent>
 __device__ __forceinline__ void zero_share(const BwdKernelArgs& a, Absent absent) {
     const int64_t unit = static_cast<int64_t>(blockIdx.x - a.sum_blocks) * (kThreads / 32) + threadIdx.x / 32;
-    if (unit < ceil_div(a.zero_to, a.zero_rows) * a.zero_slices)
-        zero_unit<TG>(a, static_cast<int64_t>(a.shape.pieces) * E, unit, absent);
+    if (unit >= ceil_div(a.zero_to, a.zero_rows) * a.zero_slices) return;
+    const int lane = threadIdx.x % 32;
+    const int64_t part = a.zero_slices == 1 ? unit : unit / a.zero_slices;
+    const int slice = static_cast<int>(unit - part * a.zero_slices);
+    const int64_t width = static_cast<int64_t>(a.shape.pieces) * E, row_bytes = width * static_cast<int>(sizeof(TG)),
+                  stride_bytes = a.grad_stride * static_cast<int>(sizeof(TG)),
+                  extent = rows_bytes(a.rows, a.grad_stride, width, sizeof(TG));
+    const bool dense = a.grad_stride == width && a.zero_slices == 1;  // neighbouring rows are one piece of memory
+    const int64_t end = min((part + 1) * a.zero_rows, a.zero_to);
+    for (int64_t row0 = part * a.zero_rows; row0 < end; row0 += 32) {
+        unsigned todo = absent(row0, static_cast<int>(min(end - row0, static_cast<int64_t>(32))));
+        char* rows = static_cast<char*>(a.grad) + row0 * stride_bytes;
+        while (todo) {
+            if (dense) {
+                int length;
+                const int from = take_run(todo, &length);
+                zero_span(rows + from * row_bytes, length * row_bytes, lane, 32, a.grad, extent, a.status);
+            } else {
+                const int r = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const int64_t from = static_cast<int64_t>(slice) * kZeroBytes;
+                zero_span(rows + r * stride_bytes + from, min(static_cast<int64_t>(kZeroBytes), row_bytes - from), lane, 32,
+                          a.grad, extent, a.status);
+            }
+        }
+    }
 }
-
 __device__ __forceinline__ auto by_marks(const BwdKernelArgs& a) {
     return [&a](int64_t row0, int rows) {
         const int lane = threadIdx.x % 32;
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 3) embedding_few_kernel(const __grid
                 const int64_t r = static_cast<int64_t>(raw[j]) - row0;
                 if (r >= 0 && r < rows) there |= 1u << r;
             }
-            return ~__reduce_or_sync(0xffffffffu, there) & (rows == 32 ? 0xffffffffu : (1u << rows) - 1);
+            return ~__reduce_or_sync(0xffffffffu, there) & (rows >= 32 ? 0xffffffffu : (1u << rows) - 1);
         });
         return;
     }
@@ -504,12 +506,22 @@ int piece_of(const void* p, int64_t ps, int size_p, const void* q, int64_t qs, i
 }
 
 template <typename TT, typename TA>
-cudaError_t fwd_typed(int e, const FwdKernelArgs& a, int64_t blocks, cudaStream_t s) {
+cudaError_t fwd_typed(int e, int width, FwdKernelArgs a, cudaStream_t s) {
     auto go = [&](auto n) {
-        return with_lanes(a.shape.lanes, [&](auto lanes) {
-            return launch_pdl(embedding_fwd_kernel<TT, TA, decltype(n)::value, decltype(lanes)::value>,
-                              static_cast<int>(blocks), kThreads, 0, 1, s, a);
-        });
+        constexpr int E = decltype(n)::value;
+        auto with_pieces = [&](auto u) {
+            constexpr int U = decltype(u)::value;
+            a.shape = row_shape(width / E, U, a.k.n);
+            const int64_t blocks = cdiv(static_cast<int64_t>(a.k.n) * a.shape.chunks * a.shape.lanes, kThreads);
+            return with_lanes(a.shape.lanes, [&](auto lanes) {
+                return launch_pdl(embedding_fwd_kernel<TT, TA, E, U, decltype(lanes)::value>, static_cast<int>(blocks),
+                                  kThreads, 0, 1, s, a);
+            });
+        };
+        if constexpr (E >= 4) {
+            if (fwd_by_four(E, width / E, a.k.n)) return with_pieces(std::integral_constant<int, 4>());
+        }
+        return with_pieces(std::integral_constant<int, kFwdPieces>());
     };
     if constexpr (sizeof(TT) == 2) {
         if (e == 8) return go(std::integral_constant<int, 8>());
@@ -531,7 +543,7 @@ int64_t zero_blocks(const BwdKernelArgs& a) {
 template <typename TA, typename TG, int E>
 cudaError_t bwd_launches(BwdKernelArgs a, int64_t width, int64_t zeroed, cudaStream_t s) {
     constexpr int U = E >= 4 ? 1 : 2;
-    a.shape = row_shape(static_cast<int>(width / E), U);
+    a.shape = row_shape(static_cast<int>(width / E), U, 0);
     if (a.n <= kThreads) {
         // narrower groups while that shortens a group's tokens to what it has in flight
         while (a.shape.lanes > 8 && cdiv(a.n, kThreads / a.shape.lanes) > kRun) a.shape.lanes /= 2;
@@ -593,16 +605,11 @@ struct BwdLayout {
     }
 };
 
-int64_t fwd_blocks(const EmbeddingArgs& a, int e, RowShape* shape) {
-    *shape = row_shape(a.width / e, fwd_pieces(e));
-    return cdiv(static_cast<int64_t>(a.k.n) * shape->chunks * shape->lanes, kThreads);
-}
-
 }  // namespace
 
 bool embedding_fits(int64_t n, int64_t width) {
     // element by element, which takes the most groups; they are counted in 32 bits
-    return n * cdiv(width, 32 * fwd_pieces(1)) <= kMaxGrid && most_spans(n) * cdiv(width, 128) <= kMaxGrid / 2;
+    return n * cdiv(width, 32 * kFwdPieces) <= kMaxGrid && most_spans(n) * cdiv(width, 128) <= kMaxGrid / 2;
 }
 
 cudaError_t embedding_fwd_launch(const DeviceInfo& dev, int dtype, const EmbeddingArgs& in, cudaStream_t s) {
@@ -611,13 +618,12 @@ cudaError_t embedding_fwd_launch(const DeviceInfo& dev, int dtype, const Embeddi
     FwdKernelArgs a{in.k, in.src, in.dst, in.src_stride, in.dst_stride, {}, in.scale, 0, in.status};
     // streamed: 134 MB of rows in 31 us, 35 otherwise; 33 MB in 7.8, 7.5 otherwise
     a.streamed = static_cast<int64_t>(in.k.n) * in.width * sa > dev.l2_bytes / 2;
-    const int64_t blocks = fwd_blocks(in, e, &a.shape);
     switch (dtype) {
-        case RMSNORM_F32: return fwd_typed<float, float>(e, a, blocks, s);
-        case RMSNORM_BF16: return fwd_typed<__nv_bfloat16, __nv_bfloat16>(e, a, blocks, s);
-        case RMSNORM_F16: return fwd_typed<__half, __half>(e, a, blocks, s);
-        case RMSNORM_BF16_W_F32: return fwd_typed<float, __nv_bfloat16>(e, a, blocks, s);
-        default: return fwd_typed<float, __half>(e, a, blocks, s);
+        case RMSNORM_F32: return fwd_typed<float, float>(e, in.width, a, s);
+        case RMSNORM_BF16: return fwd_typed<__nv_bfloat16, __nv_bfloat16>(e, in.width, a, s);
+        case RMSNORM_F16: return fwd_typed<__half, __half>(e, in.width, a, s);
+        case RMSNORM_BF16_W_F32: return fwd_typed<float, __nv_bfloat16>(e, in.width, a, s);
+        default: return fwd_typed<float, __half>(e, in.width, a, s);
     }
 }
 
@@ -667,7 +673,8 @@ cudaError_t embedding_bwd_launch(const DeviceInfo& dev, int dtype, const Embeddi
     a.scale = in.scale;
     a.status = in.status;
     // some 16 KB a warp: a few rows, or a part of a long one
-    a.zero_rows = static_cast<int>(row_bytes >= kZeroBytes ? 1 : std::min<int64_t>(32, kZeroBytes / row_bytes));
+    a.zero_rows = static_cast<int>(std::max<int64_t>(1, kZeroBytes / row_bytes));
+    if (a.zero_rows > 32) a.zero_rows = a.zero_rows / 32 * 32;
     a.zero_slices = static_cast<int>(cdiv(row_bytes, kZeroBytes));
     switch (dtype) {
         case RMSNORM_F32: return bwd_typed<float, float>(e, a, in.width, zeroed, s);

@@ -26,7 +26,7 @@ constexpr int kThreads = 256;
 // Pieces of a lane: small ones need more of them in flight.
 __host__ __device__ constexpr int scatter_pieces(int bytes) { return bytes == 16 ? 4 : 8; }
 __host__ __device__ constexpr int gather_pieces(int bytes) { return bytes == 16 ? 2 : bytes == 8 ? 4 : 8; }
-// by the choices taken together: 128 bytes in flight
+// by the choices taken together: 128 bytes of rows in flight
 __host__ __device__ constexpr int bwd_pieces(int bytes, int kc) { return 8 / kc * (bytes >= 8 ? 16 / bytes : 4); }
 constexpr int kChoices = 4;     // in flight
 
@@ -35,6 +35,7 @@ struct KernelArgs {
     RowShape shape;
     unsigned zero_blocks;  // the first ones, which zero rows without a choice,
     int zero_runs;         // so many times 32 of them a block
+    int zero_slices;       // blocks that share the same rows' bytes
     int team;               // threads of a token (gather_bwd)
     // ring: the first blocks' tokens are every main_blocks-th of main_tokens, the
     // others' `tail` each of the rest
@@ -43,23 +44,43 @@ struct KernelArgs {
     int tail;
 };
 
-// Zeroes those of 32 rows from row0 on that are in `todo`: a warp of several each.
-__device__ __forceinline__ void zero_found(const ExpertArgs& x, int64_t row0, unsigned todo, int warp, int warps, int size) {
-    const int64_t bytes = static_cast<int64_t>(x.width) * size;
-    for (int i = 0; todo; todo &= todo - 1, ++i) {
-        if (i % warps != warp) continue;
-        zero_span(static_cast<char*>(x.out) + (row0 + __ffs(todo) - 1) * x.out_stride * size, bytes, threadIdx.x % 32, 32,
-                  x.out, rows_bytes(x.rows, x.out_stride, x.width, size), x.status);
+// Zeroes those of 32 rows from row0 on that are in `todo`, by `threads` threads: where
+// rows follow one another a run of them as one piece of memory (part `slice` of
+// `slices`), else a warp each.
+__device__ __forceinline__ void zero_found(const ExpertArgs& x, int64_t row0, unsigned todo, int size, int threads, int slice,
+                                           int slices) {
+    const int64_t bytes = static_cast<int64_t>(x.width) * size, stride = x.out_stride * size,
+                  extent = rows_bytes(x.rows, x.out_stride, x.width, size);
+    char* rows = static_cast<char*>(x.out) + row0 * stride;
+    if (bytes == stride) {
+        while (todo) {
+            int length;
+            const int from = take_run(todo, &length);
+            const int64_t all = length * bytes, part = slices == 1 ? all : ceil_div(all, slices * 16) * 16,
+                          at = min(part * slice, all);
+            zero_span(rows + from * bytes + at, min(part, all - at), threadIdx.x, threads, x.out, extent, x.status);
+        }
+    } else if (slice == 0) {
+        for (int i = 0; todo; todo &= todo - 1, ++i)
+            if (i % (threads / 32) == static_cast<int>(threadIdx.x / 32))
+                zero_span(rows + (__ffs(todo) - 1) * stride, bytes, threadIdx.x % 32, 32, x.out, extent, x.status);
     }
 }
 
 // Rows without a choice, of a block's share: all its warps look at the same 32.
 __device__ __forceinline__ void zero_rows(const KernelArgs& a, int size) {
     const ExpertArgs& x = a.x;
+    const int slice = blockIdx.x % a.zero_slices, block = blockIdx.x / a.zero_slices,
+              blocks = a.zero_blocks / a.zero_slices;
+    auto source_of = [&](int i) {  // of this lane in the block's i-th 32
+        const int64_t row = (static_cast<int64_t>(i) * blocks + block) * 32 + threadIdx.x % 32;
+        return i < a.zero_runs && row < x.rows ? x.source[row] : 0;
+    };
+    int32_t next = source_of(0);
     for (int i = 0; i < a.zero_runs; ++i) {
-        const int64_t row0 = (static_cast<int64_t>(i) * a.zero_blocks + blockIdx.x) * 32, row = row0 + threadIdx.x % 32;
-        const unsigned todo = __ballot_sync(0xffffffffu, row < x.rows && x.source[row] < 0);
-        zero_found(x, row0, todo, threadIdx.x / 32, kThreads / 32, size);
+        const unsigned todo = __ballot_sync(0xffffffffu, next < 0);
+        next = source_of(i + 1);
+        if (todo) zero_found(x, (static_cast<int64_t>(i) * blocks + block) * 32, todo, size, kThreads, slice, a.zero_slices);
     }
 }
 
@@ -401,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) expert_ring_bwd_kernel(const __grid_
             if (lane == 0) found[warp] = none;
             __syncthreads();
             for (int w = 0; w < warps; ++w)
-                zero_found(x, ((run0 + w) * a.main_blocks + blockIdx.x) * 32, found[w], warp, warps, sizeof(T));
+                zero_found(x, ((run0 + w) * a.main_blocks + blockIdx.x) * 32, found[w], sizeof(T), team, 0, 1);
             __syncthreads();
         }
     }
@@ -500,11 +521,15 @@ int piece_of(const ExpertArgs& a, int dtype) {
     return 1;
 }
 
-// Blocks that zero rows: 32 rows each, or as many as keep them at one wave.
-void zero_shape(const DeviceInfo& dev, KernelArgs* a) {
+// Blocks that zero rows: 32 rows each, or as many as keep them at one wave; where rows
+// are few and long, several for the same ones (some 64 KB each).
+void zero_shape(const DeviceInfo& dev, int dtype, KernelArgs* a) {
     const int64_t runs = cdiv(a->x.rows, 32), most = dev.sm_count * 4;
     a->zero_runs = static_cast<int>(cdiv(runs, most));
-    a->zero_blocks = static_cast<unsigned>(a->zero_runs ? cdiv(runs, a->zero_runs) : 0);
+    const int64_t blocks = a->zero_runs ? cdiv(runs, a->zero_runs) : 0,
+                  slices = cdiv(static_cast<int64_t>(a->x.width) * dtype_size(dtype) * 32, 65536);
+    a->zero_slices = static_cast<int>(std::max<int64_t>(1, std::min(slices, blocks ? most / blocks : 1)));
+    a->zero_blocks = static_cast<unsigned>(blocks * a->zero_slices);
 }
 
 // fn(E) for the piece's width
@@ -577,8 +602,8 @@ bool experts_fit(const ExpertArgs& a) {
 cudaError_t expert_scatter_launch(const DeviceInfo& dev, int dtype, const ExpertArgs& in, cudaStream_t s) {
     KernelArgs a{in};
     const int e = piece_of(in, dtype);
-    a.shape = row_shape(in.width / e, scatter_pieces(e * dtype_size(dtype)));
-    zero_shape(dev, &a);
+    a.shape = row_shape(in.width / e, scatter_pieces(e * dtype_size(dtype)), in.tokens);
+    zero_shape(dev, dtype, &a);
     const int grid = static_cast<int>(a.zero_blocks + cdiv(in.tokens * a.shape.chunks * a.shape.lanes, kThreads));
     auto go = [&](auto t) {
         using T = decltype(t);
@@ -596,7 +621,7 @@ cudaError_t expert_scatter_launch(const DeviceInfo& dev, int dtype, const Expert
 cudaError_t expert_gather_launch(const DeviceInfo&, int dtype, const ExpertArgs& in, cudaStream_t s) {
     KernelArgs a{in};
     const int e = piece_of(in, dtype);
-    a.shape = row_shape(in.width / e, gather_pieces(e * dtype_size(dtype)));
+    a.shape = row_shape(in.width / e, gather_pieces(e * dtype_size(dtype)), in.tokens);
     const int grid = static_cast<int>(cdiv(in.tokens * a.shape.chunks * a.shape.lanes, kThreads));
     return with_types(dtype, [&](auto t, auto w) {
         using T = decltype(t);
@@ -613,7 +638,7 @@ cudaError_t expert_gather_bwd_launch(const DeviceInfo& dev, int dtype, const Exp
     KernelArgs a{in};
     const int e = piece_of(in, dtype);
     a.shape.pieces = in.width / e;
-    if (in.choices > 4 && e * dtype_size(dtype) >= 4 &&
+    if (in.choices > 4 && e * dtype_size(dtype) >= 4 && in.width * dtype_size(dtype) >= 512 &&
         static_cast<int64_t>(in.rows) * in.width * dtype_size(dtype) >= kRingBytes) {
         return with_types(dtype, [&](auto t, auto w) {
             using T = decltype(t);
@@ -624,20 +649,21 @@ cudaError_t expert_gather_bwd_launch(const DeviceInfo& dev, int dtype, const Exp
             });
         });
     }
-    zero_shape(dev, &a);
+    zero_shape(dev, dtype, &a);
     return with_types(dtype, [&](auto t, auto w) {
         using T = decltype(t);
         return with_piece<T>(e, [&](auto n) {
             constexpr int E = decltype(n)::value;
             auto go = [&](auto kc) {
                 constexpr int KC = decltype(kc)::value, U = bwd_pieces(E * sizeof(T), KC);
-                a.shape = row_shape(in.width / E, U);
+                a.shape = row_shape(in.width / E, U, 0);
                 a.team = 4;
                 while (a.team < kThreads && a.team * U < a.shape.pieces) a.team *= 2;
                 const int grid = static_cast<int>(a.zero_blocks + cdiv(in.tokens, kThreads / a.team));
                 return launch_pdl(expert_gather_bwd_kernel<T, decltype(w), E, U, KC>, grid, kThreads, 0, 1, s, a);
             };
-            if (in.choices <= 2) return go(std::integral_constant<int, 2>());
+            if (in.choices == 1) return go(std::integral_constant<int, 1>());
+            if (in.choices == 2) return go(std::integral_constant<int, 2>());
             return go(std::integral_constant<int, 4>());
         });
     });

@@ -55,6 +55,20 @@ struct Piece {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const W*>(p)[i];
     }
+    // through L1: others of the SM read the same
+    __device__ __forceinline__ void load_shared_row(const T* p) {
+        if constexpr (BYTES >= 16) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                W& o = w[i];
+                asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                             : "l"(reinterpret_cast<const W*>(p) + i));
+            }
+        } else {
+            load(p);
+        }
+    }
     // issued here, whatever becomes of it
     __device__ __forceinline__ void load_now(const T* p) {
         if constexpr (BYTES >= 16) {
@@ -144,6 +158,16 @@ __device__ __forceinline__ void zero_span(char* p, int64_t bytes, int thread, in
     for (int64_t i = tail + 2 * thread; i < bytes; i += 2 * threads) *reinterpret_cast<uint16_t*>(p + i) = 0;
 }
 
+// The first run of neighbouring bits that are set: where it starts, and how long;
+// cleared in `bits`.
+__device__ __forceinline__ int take_run(unsigned& bits, int* length) {
+    const int from = __ffs(bits) - 1;
+    const unsigned rest = bits >> from;
+    *length = rest == 0xffffffffu ? 32 : __ffs(~rest) - 1;
+    bits &= *length == 32 ? 0u : ~(((1u << *length) - 1) << from);
+    return from;
+}
+
 // The group of lanes a thread of a block of THREADS belongs to, counted over the grid
 // from its first_block on.
 template <int THREADS>
@@ -153,16 +177,19 @@ __device__ __forceinline__ unsigned group_index(int lanes, unsigned first_block 
 
 // ------------------------------------------------------------ host geometry
 // Groups of lanes (a power of two, up to a warp) that move a row's pieces, up to U
-// pieces a lane and chunk: more groups before more pieces each (5835 rows of 51 pieces by
-// 32 lanes 6.6 us, by 8 lanes of 8 pieces 10.0).
+// pieces a lane and chunk.
 struct RowShape {
     int pieces;  // of a row
     int lanes;   // of a group
     int chunks;  // of a row
 };
-inline RowShape row_shape(int pieces, int u) {
+// Few lanes with many pieces each move more at a time, but only once there are warps
+// enough to fill the device: 5835 rows of 51 pieces take 6.6 us by 32 lanes and 10.0 by
+// 8, 33660 rows of 32 pieces 6.8 and 5.7.
+constexpr int64_t kFullWarps = 152 * 48;
+inline RowShape row_shape(int pieces, int u, int64_t rows) {
     RowShape r{pieces, 1, 1};
-    while (r.lanes < 32 && r.lanes < pieces) r.lanes *= 2;
+    while (r.lanes < 32 && r.lanes < pieces && (r.lanes * u < pieces || rows * r.lanes / 32 < kFullWarps)) r.lanes *= 2;
     r.chunks = static_cast<int>(cdiv(pieces, static_cast<int64_t>(r.lanes) * u));
     return r;
 }

@@ -490,9 +490,10 @@ cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
         // one block while its items and the rows it marks are few; then eight
         const int blocks = n <= kThreads && a.rows <= 4 * kThreads ? 1 : kCluster;
         const int rounds = n <= blocks * kThreads ? 1 : 2;
-        // no more threads than items or digits need
+        // no more threads than items, digits or rows to mark need
         const int digits = a.experts > 0 ? a.experts : a.bins;
-        const int need = std::max<int>(static_cast<int>(std::min<int64_t>(cdiv(n, rounds), kThreads)), digits);
+        const int need = static_cast<int>(
+            std::max<int64_t>(digits, std::min<int64_t>(std::max<int64_t>(cdiv(n, rounds), a.rows / 4), kThreads)));
         const int threads = blocks > 1 ? kThreads : std::min(kThreads, std::max(128, round_up(need, 32)));
         const SortFn fn = rounds == 1 ? sort_cluster_kernel<1> : SortFn(sort_cluster_kernel<2>);
         const cudaError_t err = allow_smem(dev, fn);
