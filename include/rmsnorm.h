@@ -449,10 +449,11 @@ int rmsnorm_embedding_fwd(const rmsnorm_embedding_t *embedding,
  * grad holds instead (a sum over micro-batches; rows without a token are
  * neither read nor written). dtype names the types of dy and of grad (as of y
  * and the table). Tokens are sorted by id, so every row's sum is fp32 in an
- * order that the sizes alone fix, rounded once: the same bits on every run,
- * no floating-point atomics. One launch of up to 256 tokens, three, and past 16384
- * tokens two and two for each nine bits of num_rows. Workspace and errors as the norm's backward
- * (RMSNORM_ERR_NOMEM), arguments as the forward's.
+ * order that the sizes and the alignment alone fix, rounded once: the same bits
+ * on every run, no floating-point atomics. One launch for up to 256 tokens,
+ * three for more, and past 16384 two and two for each nine bits of num_rows.
+ * Workspace and errors as the norm's backward (RMSNORM_ERR_NOMEM), arguments
+ * as the forward's.
  */
 int rmsnorm_embedding_bwd(const rmsnorm_embedding_t *embedding,
                           const void *ids, const void *dy, void *grad,

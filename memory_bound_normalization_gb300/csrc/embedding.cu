@@ -5,7 +5,7 @@
 // in; every token's, out).
 //
 // Backward: row v of the gradient is scale * the sum of dy_i over the tokens with
-// id v, in fp32 and in an order that the sizes alone fix. The tokens are sorted
+// id v, in fp32 and in an order that the sizes and the alignment alone fix. The tokens are sorted
 // by id (sort.cu); the sorted list is cut in segments of a few tokens. A group of
 // lanes adds up its columns of a segment, a block those of neighbouring segments. Runs
 // of one id that lie in a segment are written to their row at once; a run over
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_co
             else out.store(to);
         }
     };
-    if (E < 4 && LANES > 0 && first - static_cast<int>(threadIdx.x & 31) + 32 * U <= a.shape.pieces)
+    if (E < 4 && LANES > 0 && first - static_cast<int>(threadIdx.x & 31) <= a.shape.pieces - 32 * U)
         look_up(std::true_type());
     else
         look_up(std::false_type());

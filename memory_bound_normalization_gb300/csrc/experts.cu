@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, E >= 4 ? 4 : 3) expert_gather_kernel
                 out.store(to + u * lanes * E);
         }
     };
-    if (E * sizeof(T) < 8 && LANES > 0 && first - static_cast<int>(threadIdx.x & 31) + 32 * kGatherPieces <= a.shape.pieces)
+    if (E * sizeof(T) < 8 && LANES > 0 && first - static_cast<int>(threadIdx.x & 31) <= a.shape.pieces - 32 * kGatherPieces)
         gather(std::true_type());
     else
         gather(std::false_type());
@@ -224,9 +224,11 @@ __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __gri
             dot[k] = 0.f;
         }
         const int step = team * E;
-        for (int c = lane; c < (live ? a.shape.pieces : 0); c += team * U) {
+        // unsigned: behind the last of 2^31 - 1 pieces
+        const unsigned pieces = live ? a.shape.pieces : 0;
+        for (unsigned c = lane; c < pieces; c += team * U) {
             const int64_t column = static_cast<int64_t>(c) * E;
-            const int count = (a.shape.pieces - c + team - 1) / team;  // of this thread's pieces
+            const unsigned count = (pieces - c + team - 1) / team;  // of this thread's pieces
             Piece<T, E> g[U], v[KC][U];
             const T* src = dy + column;
 #pragma unroll
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) expert_ring_bwd_kernel(const __grid_
     const ExpertArgs& x = a.x;
     const int team = blockDim.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = team / 32;
     const uint32_t slots = smem_u32(rmsn_dynamic_smem) + threadIdx.x * 16;  // [D][slots][team]
-    const int groups = (x.choices + KC - 1) / KC, chunks = (a.shape.pieces + team * U - 1) / (team * U);
+    const int groups = (x.choices + KC - 1) / KC, chunks = static_cast<int>((static_cast<unsigned>(a.shape.pieces) + team * U - 1) / (team * U));
     wait_for_prerequisite_grid();
     allow_dependent_launch();
 

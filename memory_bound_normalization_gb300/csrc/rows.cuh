@@ -61,7 +61,7 @@ struct Piece {
 #pragma unroll
             for (int i = 0; i < WORDS; ++i) {
                 W& o = w[i];
-                asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                asm volatile("ld.global.ca.v4.u32 {%0,%1,%2,%3}, [%4];"
                              : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
                              : "l"(reinterpret_cast<const W*>(p) + i));
             }

@@ -6,8 +6,8 @@ outputs from PyTorch, ``RMSNormError`` on a non-OK status, the tensors' own
 device, its current stream or ``stream`` as if that were the current one.
 ``autograd`` holds the differentiable forms.
 
-Sums are fp32 in an order that the sizes alone fix, without floating-point
-atomics: the same bits on every run, gradients included.
+Sums are fp32 in an order that the sizes and the alignment alone fix, without
+floating-point atomics: the same bits on every run, gradients included.
 """
 from __future__ import annotations
 

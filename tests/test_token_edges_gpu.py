@@ -202,6 +202,41 @@ def test_ring_of_many_choices(dtype, H, K, T):
     ref.close(dw, dots, H, magnitude)
 
 
+def test_rows_of_the_largest_width():
+    """Rows of 2^31 - 1 elements, one by one (no piece of 4 bytes fits): where a thread's
+    next element passes 31 bits. Ones and powers of two, whose sums fp32 holds."""
+    H = (1 << 31) - 1
+    x = torch.ones(1, H, dtype=BF16, device=DEV)
+    x[0, -1] = 4
+    zero = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    rows = pkg.expert_dispatch_forward(x, zero, zero[0])
+    assert torch.equal(rows, x)
+    w = torch.full((1, 1), 0.5, device=DEV)
+    y = pkg.expert_combine_forward(rows, zero, w, x)
+    assert float(y[0, -1]) == 6 and float(y[0, -2]) == 1.5 and float(y.amin()) == 1.5
+    del y
+    drows, dw = pkg.expert_combine_backward(x, rows, zero, zero[0], w)
+    assert float(drows[0, -1]) == 2 and float(drows[0, -2]) == 0.5 and float(drows.amin()) == 0.5
+    # a thread's 2^23 ones are exact, as are sums of powers of two; the 4^2 is below a step
+    assert abs(float(dw) - 2.0 ** 31) <= 2.0 ** 8
+    del drows, rows
+    ids = torch.zeros(1, dtype=torch.int64, device=DEV)
+    assert torch.equal(pkg.embedding_forward(ids, x), x)
+    assert torch.equal(pkg.embedding_backward(ids, x, 1), x)
+
+
+def test_result_larger_than_the_cache():
+    """Stored without being kept: more than half of L2."""
+    ids, table = emb.tokens(20001, 900), emb.normal(900, 2056, dtype=BF16)
+    y = pkg.embedding_forward(ids, table)
+    assert y.numel() * 2 > torch.cuda.get_device_properties(0).L2_cache_size // 2
+    there = (ids >= 0) & (ids < 900)
+    assert torch.equal(y, torch.where(there[:, None], table[ids.clamp(0, 899)], 0))
+    odd = emb.normal(900, 2055, dtype=F16)
+    y = pkg.embedding_forward(ids, odd)
+    assert torch.equal(y, torch.where(there[:, None], odd[ids.clamp(0, 899)], 0))
+
+
 # ------------------------------------------------------------- streams and graphs
 def calls():
     """Every operator on inputs of its own: name -> (call(stream), what it gave first)."""
