@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_co
     const bool there = row < a.k.limit;
     const TT* src = static_cast<const TT*>(a.table) + row * a.table_stride + static_cast<int64_t>(first) * E;
     TA* dst = static_cast<TA*>(a.y) + item * a.y_stride + static_cast<int64_t>(first) * E;
+    const float scale = there ? a.scale : 0.f;  // a row of zeros, also where the scale is infinite or NaN
     // whole: every piece of the lane is there, so that none has to be asked for
     auto look_up = [&](auto whole) {
         auto live = [&](int u) { return decltype(whole)::value || first + u * lanes < a.shape.pieces; };
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_co
             float f[E];
             in[u].unpack(f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) f[e] *= a.scale;
+            for (int e = 0; e < E; ++e) f[e] *= scale;
             Piece<TA, E> out;
             out.pack(f);
             TA* to = dst + u * lanes * E;
