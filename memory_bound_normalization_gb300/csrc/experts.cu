@@ -149,13 +149,13 @@ __global__ void __launch_bounds__(kThreads, E >= 4 ? 4 : 3) expert_gather_kernel
         }
         const int32_t* pos = x.position + static_cast<int64_t>(token) * x.choices;
         const TW* wgt = static_cast<const TW*>(x.weights) + static_cast<int64_t>(token) * x.choices;
-        for (int k0 = 0; k0 < x.choices; k0 += kChoices) {
+        for (unsigned k0 = 0; more_choices(k0, x.choices); k0 += kChoices) {
             Piece<T, E> v[kChoices][kGatherPieces];
             float w[kChoices];
             bool there[kChoices];
 #pragma unroll
             for (int k = 0; k < kChoices; ++k) {
-                const int32_t row = k0 + k < x.choices ? pos[k0 + k] : -1;
+                const int32_t row = more_choices(k0 + k, x.choices) ? pos[k0 + k] : -1;
                 there[k] = static_cast<uint32_t>(row) < static_cast<uint32_t>(x.rows);
                 w[k] = there[k] && x.weights != nullptr ? to_f32(wgt[k0 + k]) : 1.f;
                 const T* src = static_cast<const T*>(x.in) + row * x.in_stride + column;
@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __gri
     const T* dy = static_cast<const T*>(x.x) + token * x.x_stride;
     const int32_t* pos = x.position + token * x.choices;
     const TW* wgt = static_cast<const TW*>(x.weights) + token * x.choices;
-    for (int k0 = 0; k0 < x.choices; k0 += KC) {
-        const int here = live ? min(KC, x.choices - k0) : 0;
+    for (unsigned k0 = 0; more_choices(k0, x.choices); k0 += KC) {
+        const int here = live ? min(KC, x.choices - static_cast<int>(k0)) : 0;
         int32_t row[KC];
         float w[KC], dot[KC];
 #pragma unroll
@@ -309,6 +309,7 @@ struct Ring {
 };
 
 constexpr int64_t kRingBytes = 8 << 20;  // of rows, from which on
+constexpr int kRingMostChoices = RMSNORM_MAX_EXPERTS;
 
 // Sums over a warp of KC values each lane has; lane l returns that of value
 // l / (32 / KC).
@@ -640,7 +641,8 @@ cudaError_t expert_gather_bwd_launch(const DeviceInfo& dev, int dtype, const Exp
     KernelArgs a{in};
     const int e = piece_of(in, dtype);
     a.shape.pieces = in.width / e;
-    if (in.choices > 4 && e * dtype_size(dtype) >= 4 && in.width * dtype_size(dtype) >= 512 &&
+    // a block's steps (groups of choices times chunks of columns times tokens) are counted in 32 bits
+    if (in.choices > 4 && in.choices <= kRingMostChoices && e * dtype_size(dtype) >= 4 && in.width * dtype_size(dtype) >= 512 &&
         static_cast<int64_t>(in.rows) * in.width * dtype_size(dtype) >= kRingBytes) {
         return with_types(dtype, [&](auto t, auto w) {
             using T = decltype(t);

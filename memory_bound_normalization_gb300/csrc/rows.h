@@ -99,6 +99,9 @@ struct ExpertArgs {
     int* status;
 };
 bool experts_fit(const ExpertArgs& a);
+// Whether choice k is one of a token's. Unsigned: a few behind the last of 2^31 - 1 pass
+// 31 bits.
+__host__ __device__ constexpr bool more_choices(unsigned k, int choices) { return k < static_cast<unsigned>(choices); }
 // rows[position[t, k]] = x[t] (times nothing), rows without a choice zero
 cudaError_t expert_scatter_launch(const DeviceInfo& dev, int dtype, const ExpertArgs& a, cudaStream_t s);
 // y[t] = x[t] + sum_k w[t, k] in[position[t, k]]

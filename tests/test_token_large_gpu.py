@@ -192,6 +192,22 @@ def test_ring_shared_out(T, K, H, dtype):
     assert not drows[plan.source < 0].any()
 
 
+@pytest.mark.parametrize("K", [1024, 1025, 1500])
+def test_choices_up_to_the_rings_most_and_past_it(K):
+    T, E, H = 5, 1024, 1024
+    e = torch.randint(-1, E, (T, K), generator=torch.Generator().manual_seed(K)).to(DEV)
+    plan = pkg.expert_sort(e, E)
+    R = plan.source.numel()
+    dy, rows = normal(T, H, dtype=BF16), normal(R, H, dtype=BF16, seed=2)
+    w = torch.softmax(normal(T, K, dtype=F32, seed=3), -1)
+    drows, dw = pkg.expert_combine_backward(dy, rows, plan.position, plan.source, w)
+    want, dots, magnitude = ref.combine_grads(dy, rows, plan.position, w)
+    ref.close(drows, want)
+    ref.close(dw, dots, H, magnitude)
+    y, magnitude = ref.combine(rows, plan.position, w)
+    ref.close(pkg.expert_combine_forward(rows, plan.position, w), y, K, magnitude)
+
+
 # ------------------------------------------------------------- checked build
 def test_large_calls_under_checks():
     """These tests in the checked build; a failed check is recorded on the device."""

@@ -1,0 +1,66 @@
+"""The host side of the rows by index, and what its kernels count by, at the ends of
+their ranges: over a CUDA runtime that launches nothing, or compiled for the host."""
+from __future__ import annotations
+
+import os
+import subprocess
+
+import pytest
+
+from memory_bound_normalization_gb300 import build as libbuild
+from test_image_launches_host import run  # noqa: F401  (a fixture)
+
+BIG = (1 << 31) - 1
+
+STEPS_PROGRAM = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "rows.h"
+int main(int, char** v) {
+    const int choices = atoi(v[1]), step = atoi(v[2]);
+    // the loop of a kernel from its last few steps on
+    long long taken = 0, steps = 0;
+    for (unsigned k0 = static_cast<unsigned>((choices > 1000 ? choices - 1000 : 0) / step) * step;
+         rmsn::more_choices(k0, choices); k0 += step) {
+        if (++steps > 2000) break;
+        for (int k = 0; k < step; ++k) taken += rmsn::more_choices(k0 + k, choices);
+    }
+    std::printf("%lld\n", taken);
+    return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def steps(tmp_path_factory):
+    d = tmp_path_factory.mktemp("steps")
+    (d / "steps.cpp").write_text(STEPS_PROGRAM)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(libbuild._nvcc())), "include")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-I", cuda, "-I", libbuild.CSRC, "-I", libbuild.INCLUDE,
+                    str(d / "steps.cpp"), "-o", str(d / "steps")], check=True)
+
+    def call(*a):
+        return int(subprocess.run([str(d / "steps"), *map(str, a)], capture_output=True, text=True, check=True).stdout)
+
+    return call
+
+
+@pytest.mark.parametrize("step", [1, 2, 4])
+@pytest.mark.parametrize("choices", [1, 3, 4, 5, 999, 1000, BIG - 4, BIG - 3, BIG - 2, BIG - 1, BIG])
+def test_choices_end(steps, choices, step):
+    """Steps of several choices end behind the last one, also of 2^31 - 1 (a signed count
+    went on from -2^31, before the token's positions)."""
+    first = max(0, choices - 1000) // step * step
+    assert steps(choices, step) == choices - first
+
+
+def test_ring_of_choices(run):  # noqa: F811
+    """The combine backward's ring (the one launch with shared memory) takes 5 to 1024
+    choices: its blocks count their steps in 32 bits."""
+    run(f"""
+    for choices, ring in ((4, False), (5, True), (1024, True), (1025, False), (1 << 28, False), ({BIG}, False)):
+        d = _lib.Experts(tokens=1, rows=4096, width=4096, token_stride=4096, row_stride=4096, residual_stride=4096,
+                         drow_stride=4096, choices=choices)
+        assert lib.rmsnorm_expert_combine_bwd(ctypes.byref(d), A, A, A, A, A, A, A, _lib.BF16, None) == _lib.OK
+        assert (launches()[-1]["smem"] > 0) == ring, (choices, launches()[-1])
+    """)
