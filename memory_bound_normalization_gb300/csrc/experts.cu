@@ -641,9 +641,10 @@ cudaError_t expert_gather_bwd_launch(const DeviceInfo& dev, int dtype, const Exp
     KernelArgs a{in};
     const int e = piece_of(in, dtype);
     a.shape.pieces = in.width / e;
+    const int64_t row_bytes = static_cast<int64_t>(in.width) * dtype_size(dtype);
     // a block's steps (groups of choices times chunks of columns times tokens) are counted in 32 bits
-    if (in.choices > 4 && in.choices <= kRingMostChoices && e * dtype_size(dtype) >= 4 && in.width * dtype_size(dtype) >= 512 &&
-        static_cast<int64_t>(in.rows) * in.width * dtype_size(dtype) >= kRingBytes) {
+    if (in.choices > 4 && in.choices <= kRingMostChoices && e * dtype_size(dtype) >= 4 && row_bytes >= 512 &&
+        in.rows * row_bytes >= kRingBytes) {
         return with_types(dtype, [&](auto t, auto w) {
             using T = decltype(t);
             return with_piece<T>(e, [&](auto n) {

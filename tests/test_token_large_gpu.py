@@ -208,6 +208,28 @@ def test_choices_up_to_the_rings_most_and_past_it(K):
     ref.close(pkg.expert_combine_forward(rows, plan.position, w), y, K, magnitude)
 
 
+@pytest.mark.parametrize("H", [(1 << 29) + 4, (1 << 29) + 1])
+def test_ring_of_rows_past_31_bits_of_bytes(H):
+    """One token of five choices, by pieces of 16 and of 4 bytes. Ones and powers of two,
+    whose sums fp32 holds."""
+    K = 5
+    plan = pkg.expert_sort(torch.tensor([[3, 0, -1, 1, 2]], device=DEV), 4)
+    dy = torch.ones(1, H, device=DEV)
+    dy[0, -1] = 4
+    rows = torch.ones(K, H, device=DEV)
+    rows[2, -1] = 2
+    w = torch.tensor([[0.5, 1.0, NAN, 2.0, 4.0]], device=DEV)
+    drows, dw = pkg.expert_combine_backward(dy, rows, plan.position, plan.source, w)
+    # rows in the experts' order: choices 1, 3, 4 and 0, then none
+    for row, weight in enumerate((1.0, 2.0, 4.0, 0.5, 0.0)):
+        assert float(drows[row, -1]) == 4 * weight
+        assert bool((drows[row, :-1] == weight).all())
+    base = float(1 << 29) + (H - (1 << 29) - 1)
+    want = [base + 4, base + 4, 0.0, base + 4, base + 8]
+    # a thread's sums are exact; joined, half steps of sums of 2^25 to 2^30: 1 + 2 + ... + 32
+    assert all(abs(a - b) <= 2.0 ** 6 for a, b in zip(dw[0].tolist(), want))
+
+
 # ------------------------------------------------------------- checked build
 def test_large_calls_under_checks():
     """These tests in the checked build; a failed check is recorded on the device."""

@@ -64,3 +64,17 @@ def test_ring_of_choices(run):  # noqa: F811
         assert lib.rmsnorm_expert_combine_bwd(ctypes.byref(d), A, A, A, A, A, A, A, _lib.BF16, None) == _lib.OK
         assert (launches()[-1]["smem"] > 0) == ring, (choices, launches()[-1])
     """)
+
+
+@pytest.mark.parametrize("dtype,size", [("F32", 4), ("BF16", 2), ("F16_W_F32", 2)])
+def test_ring_of_the_widest_rows(run, dtype, size):  # noqa: F811
+    """Rows of 2^31 bytes and more go by the ring as shorter ones do."""
+    run(f"""
+    for width in (512 // {size} - 4, 512 // {size}, 1 << 28, (1 << 31) // {size} - 4, (1 << 31) // {size},
+                  (1 << 31) // {size} + 4, (1 << 31) - 4):
+        d = _lib.Experts(tokens=1, rows=1 << 17, width=width, token_stride=width, row_stride=width,
+                         residual_stride=width, drow_stride=width, choices=6)
+        assert lib.rmsnorm_expert_combine_bwd(ctypes.byref(d), A, A, A, A, A, A, A, _lib.{dtype}, None) == _lib.OK
+        ring = launches()[-1]["smem"] > 0
+        assert ring == (width * {size} >= 512), width
+    """)
