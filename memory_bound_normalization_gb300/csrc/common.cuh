@@ -439,7 +439,8 @@ __device__ __forceinline__ void report_status(int* status, int code) {
 // global access of the kernels against the extent of the tensor it belongs
 // to (M*N elements for the activations, N for w and dw, M for rstd, the
 // partial rows for the workspace) and every ring access against the block's
-// dynamic shared memory, before it happens. A failed check records
+// dynamic shared memory, before it happens; where rows are moved by an index
+// every store, every copy and every load through an index. A failed check records
 // kStatusOutOfBounds on the device status word and skips the access: it
 // never traps. In the normal build RMSN_OK(...) is the constant true and the
 // checks are not compiled at all, so the kernels are unchanged.

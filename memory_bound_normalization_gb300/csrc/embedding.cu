@@ -72,7 +72,12 @@ __global__ void __launch_bounds__(kThreads) embedding_fwd_kernel(const __grid_co
             in[u].zero();
             // a frequent token's row is in many warps' hands: from L2 alone, 22400 tokens of 22
             // rows of 520 fp32 waited for the few lines that hold them (14.8 us)
-            if (there && live(u)) in[u].load_shared_row(src + u * lanes * E);
+            if (there && live(u) &&
+                RMSN_OK(span_in(src + u * lanes * E, E * sizeof(TT), a.table,
+                                rows_bytes(a.k.limit, a.table_stride, static_cast<int64_t>(a.shape.pieces) * E,
+                                           sizeof(TT))),
+                        a.status))
+                in[u].load_shared_row(src + u * lanes * E);
         }
         asm volatile("" ::: "memory");  // every load before the first store
 #pragma unroll
@@ -268,7 +273,12 @@ __device__ __forceinline__ void add_tokens(const BwdKernelArgs& a, const Staged&
                 for (int u = 0; u < U; ++u) {
                     const int p = piece + u * lanes;
                     in[j][u].zero();
-                    if (live && p < a.shape.pieces) in[j][u].load(row + static_cast<int64_t>(p) * E);
+                    if (live && p < a.shape.pieces &&
+                        RMSN_OK(span_in(row + static_cast<int64_t>(p) * E, E * sizeof(TA), a.dy,
+                                        rows_bytes(a.n, a.dy_stride, static_cast<int64_t>(a.shape.pieces) * E,
+                                                   sizeof(TA))),
+                                a.status))
+                        in[j][u].load(row + static_cast<int64_t>(p) * E);
                 }
             }
 #pragma unroll
@@ -467,7 +477,11 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_c
             const int p = piece + u * a.shape.lanes;
             Piece<float, E> in;
             in.zero();
-            if (live && p < a.shape.pieces) in.load_now(partial_at<E>(a, s, slot, p));
+            if (live && p < a.shape.pieces &&
+                RMSN_OK(span_in(partial_at<E>(a, s, slot, p), E * 4, a.partial,
+                                static_cast<int64_t>(a.spans) * 8 * a.shape.pieces * E),
+                        a.status))
+                in.load_now(partial_at<E>(a, s, slot, p));
             in.unpack(c.v[u]);
         }
     };
@@ -652,8 +666,9 @@ cudaError_t embedding_bwd_launch(const DeviceInfo& dev, int dtype, const Embeddi
             const int launches = sort_launches(n, in.k.limit);
             zeroed = std::min(in.rows, cdiv(launches > 1 ? launches * kZeroBesidePass : kZeroBesideSort, row_bytes));
             char* at = static_cast<char*>(in.dst) + (in.rows - zeroed) * stride_bytes;
-            b.zero = stride_bytes == row_bytes ? ZeroJob{at, zeroed * row_bytes, 0, 1}
-                                               : ZeroJob{at, row_bytes, stride_bytes, zeroed};
+            const int64_t extent = (in.rows - 1) * stride_bytes + row_bytes;
+            b.zero = stride_bytes == row_bytes ? ZeroJob{at, zeroed * row_bytes, 0, 1, in.dst, extent}
+                                               : ZeroJob{at, row_bytes, stride_bytes, zeroed, in.dst, extent};
             if (zeroed < in.rows) b.present = ws + l.present;
         }
         const cudaError_t err = sort_launch(dev, in.k, b, s);

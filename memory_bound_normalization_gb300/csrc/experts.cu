@@ -162,7 +162,11 @@ __global__ void __launch_bounds__(kThreads, E >= 4 ? 4 : 3) expert_gather_kernel
 #pragma unroll
                 for (int u = 0; u < kGatherPieces; ++u) {
                     v[k][u].zero();
-                    if (there[k] && live(u)) v[k][u].load(src + u * lanes * E);
+                    if (there[k] && live(u) &&
+                        RMSN_OK(span_in(src + u * lanes * E, E * sizeof(T), x.in,
+                                        rows_bytes(x.rows, x.in_stride, x.width, sizeof(T))),
+                                x.status))
+                        v[k][u].load(src + u * lanes * E);
                 }
             }
 #pragma unroll
@@ -242,7 +246,10 @@ __global__ void __launch_bounds__(kThreads) expert_gather_bwd_kernel(const __gri
 #pragma unroll
                 for (int u = 0; u < U; ++u, src += step) {
                     v[k][u].zero();
-                    if (row[k] >= 0 && u < count) v[k][u].load(src);
+                    if (row[k] >= 0 && u < count &&
+                        RMSN_OK(span_in(src, E * sizeof(T), x.in, rows_bytes(x.rows, x.in_stride, x.width, sizeof(T))),
+                                x.status))
+                        v[k][u].load(src);
                 }
             }
 #pragma unroll
@@ -392,19 +399,22 @@ __global__ void __launch_bounds__(kThreads) expert_ring_bwd_kernel(const __grid_
     TW weights0 = weights_of(0), weights1{};
     auto issue = [&](const Step& s, int in_batch, int at) {
         const int p0 = s.chunk * team * U + threadIdx.x;
-        auto copy = [&](int k, const T* row) {
+        auto copy = [&](int k, const T* row, const void* base, int64_t rows, int64_t row_stride) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (p0 + u * team < a.shape.pieces)
+                if (p0 + u * team < a.shape.pieces &&
+                    RMSN_OK(span_in(row + static_cast<int64_t>(p0 + u * team) * E, kPiece, base,
+                                    rows_bytes(rows, row_stride, x.width, sizeof(T))),
+                            x.status))
                     copy_own<kPiece>(slot(at, k) + u * kPiece, row + static_cast<int64_t>(p0 + u * team) * E, x.status);
         };
         const bool live = s.token < end;
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
             const int32_t r = __shfl_sync(0xffffffffu, in_batch < kBatch ? rows0 : rows1, in_batch % kBatch * KC + k);
-            if (live && valid(r)) copy(k, static_cast<const T*>(x.in) + r * x.in_stride);
+            if (live && valid(r)) copy(k, static_cast<const T*>(x.in) + r * x.in_stride, x.in, x.rows, x.in_stride);
         }
-        if (live) copy(KC, static_cast<const T*>(x.x) + s.token * x.x_stride);
+        if (live) copy(KC, static_cast<const T*>(x.x) + s.token * x.x_stride, x.x, x.tokens, x.x_stride);
         copies_commit();
     };
 

@@ -22,10 +22,13 @@ struct KeySource {
     int ids_64;
 };
 
-// Rows to be zeroed, of any alignment: `rows` rows of `bytes`, `stride` apart.
+// Rows to be zeroed, of any alignment: `rows` rows of `bytes`, `stride` apart, inside the
+// `extent` bytes from `base` on.
 struct ZeroJob {
     char* at;
     int64_t bytes, stride, rows;
+    const void* base;
+    int64_t extent;
 };
 
 // Stable order of the keys by radix passes: pairs of a key and the item it came

@@ -38,6 +38,7 @@ struct SortArgs {
     // many blocks, in clusters of kCluster: [blocks][bins] counts of the cluster's blocks
     // before, then [clusters][bins] counts of the clusters
     uint32_t* counts;
+    int64_t counts_bytes;
     int blocks, tiles;  // kThreads * R items a tile
     int passes, pass, bits, bins;
     // experts
@@ -172,7 +173,8 @@ __device__ __forceinline__ void place_digits(const SortArgs& a, const Smem& s, u
         s.start[digits] = all;
         if (a.experts > 0) {
             s.base[digits] = 0;  // the dropped ones go nowhere
-            if (block == 0) a.offsets[digits] = all;
+            if (block == 0 && RMSN_OK(span_in(a.offsets + digits, 4, a.offsets, 4ll * (a.experts + 1)), a.status))
+                a.offsets[digits] = all;
         }
     }
     __syncthreads();
@@ -218,7 +220,9 @@ __device__ __forceinline__ void mark_present(const SortArgs& a, const Smem& s, c
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const bool live = first + r * 32 + threadIdx.x % 32 < a.k.n && key[r] < a.k.limit;
-        if (live && (is_first[r] || s.seen[digit_of(a, 0, key[r])] != key[r])) a.present[key[r]] = 1;
+        if (live && (is_first[r] || s.seen[digit_of(a, 0, key[r])] != key[r]) &&
+            RMSN_OK(span_in(a.present + key[r], 1, a.present, a.k.limit), a.status))
+            a.present[key[r]] = 1;
     }
 }
 
@@ -240,7 +244,7 @@ __device__ __forceinline__ void mark_unused(const SortArgs& a, const Smem& s, un
     }
     for (int64_t i = static_cast<int64_t>(s.start[a.experts]) + block * blockDim.x + threadIdx.x; i < a.rows;
          i += static_cast<int64_t>(blocks) * blockDim.x)
-        a.source[i] = -1;
+        if (RMSN_OK(span_in(a.source + i, 4, a.source, 4ll * a.rows), a.status)) a.source[i] = -1;
 }
 
 __device__ __forceinline__ void clear_present(const SortArgs& a, unsigned block, unsigned blocks) {
@@ -249,7 +253,7 @@ __device__ __forceinline__ void clear_present(const SortArgs& a, unsigned block,
     uint4* p = reinterpret_cast<uint4*>(a.present);
     for (int64_t i = static_cast<int64_t>(block) * blockDim.x + threadIdx.x; i < (a.k.limit + 15) / 16;
          i += static_cast<int64_t>(blocks) * blockDim.x)
-        p[i] = make_uint4(0, 0, 0, 0);
+        if (RMSN_OK(span_in(p + i, 16, p, (a.k.limit + 15) / 16 * 16), a.status)) p[i] = make_uint4(0, 0, 0, 0);
 }
 
 // Clears the counts of the warps in use; their number.
@@ -285,9 +289,9 @@ __device__ __forceinline__ void sum_warps(const SortArgs& a, const Smem& s, int 
 constexpr int64_t kZeroUnit = 65536;  // bytes
 __device__ __forceinline__ void zero_beside(const SortArgs& a, unsigned block, unsigned blocks) {
     const ZeroJob& z = a.zero;
-    const int64_t slices = ceil_div(z.bytes, kZeroUnit), extent = (z.rows - 1) * z.stride + z.bytes;
+    const int64_t slices = ceil_div(z.bytes, kZeroUnit);
     auto slice = [&](char* row, int64_t from) {
-        zero_span(row + from, min(kZeroUnit, z.bytes - from), threadIdx.x, blockDim.x, z.at, extent, a.status);
+        zero_span(row + from, min(kZeroUnit, z.bytes - from), threadIdx.x, blockDim.x, z.base, z.extent, a.status);
     };
     if (z.rows == 1) {
         for (int64_t i = block; i < slices; i += blocks) slice(z.at, i * kZeroUnit);
@@ -384,8 +388,10 @@ __global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_const
             total += v[b];
             if (b < rank) before += v[b];
         }
-        a.counts[static_cast<int64_t>(blockIdx.x) * a.bins + d] = before;
-        if (rank == 0) a.counts[static_cast<int64_t>(a.blocks + blockIdx.x / kCluster) * a.bins + d] = total;
+        uint32_t* own = a.counts + static_cast<int64_t>(blockIdx.x) * a.bins + d;
+        uint32_t* all = a.counts + static_cast<int64_t>(a.blocks + blockIdx.x / kCluster) * a.bins + d;
+        if (RMSN_OK(span_in(own, 4, a.counts, a.counts_bytes), a.status)) *own = before;
+        if (rank == 0 && RMSN_OK(span_in(all, 4, a.counts, a.counts_bytes), a.status)) *all = total;
     }
     cluster_sync_all();  // the others have read this block's
 }
@@ -502,6 +508,7 @@ cudaError_t run(const DeviceInfo& dev, SortArgs a, cudaStream_t s) {
         return launch_pdl(fn, blocks + zero, threads, sort_smem(a.bins, threads / 32), blocks, s, a);
     }
     const Many m(n);
+    a.counts_bytes = sort_counts_words(n, a.bins) * 4;
     a.blocks = m.blocks;
     a.tiles = m.tiles;
     // each launch zeroes its part of the rows

@@ -3,6 +3,7 @@ their ranges: over a CUDA runtime that launches nothing, or compiled for the hos
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 
 import pytest
@@ -78,3 +79,25 @@ def test_ring_of_the_widest_rows(run, dtype, size):  # noqa: F811
         ring = launches()[-1]["smem"] > 0
         assert ring == (width * {size} >= 512), width
     """)
+
+
+# ------------------------------------------------------------- the checked build's checks
+def unchecked(name, access):
+    """Lines with such an access that no check of the checked build stands before."""
+    with open(os.path.join(libbuild.CSRC, name)) as fh:
+        lines = fh.read().split("\n")
+    found = [i for i, line in enumerate(lines) if re.search(access, line)]
+    assert found, f"no {access} in {name}"
+    return [lines[i].strip() for i in found if not any("RMSN_OK" in near for near in lines[max(0, i - 5):i + 1])]
+
+
+@pytest.mark.parametrize("access", [r"\ba\.(?!pairs)\w+\[[^=]*\] = (?!b\.)", r"\*(own|all) = ", r"\bp\[i\] = ", r"\*reinterpret_cast<uint2"])
+def test_stores_of_sorts_are_checked(access):
+    assert unchecked("sort.cu", access) == []
+
+
+@pytest.mark.parametrize("name,access", [("embedding.cu", r"load_shared_row\("), ("embedding.cu", r"in\[j\]\[u\]\.load\("),
+                                         ("embedding.cu", r"load_now\("), ("experts.cu", r"v\[k\]\[u\]\.load\("),
+                                         ("experts.cu", r"copy_own<kPiece>\(")])
+def test_loads_through_an_index_are_checked(name, access):
+    assert unchecked(name, access) == []
