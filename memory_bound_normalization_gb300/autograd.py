@@ -248,7 +248,7 @@ class QKNormRope(torch.nn.Module):
 
 def _one_stride(t):
     """t, or a dense copy where its rows have no one stride (a broadcast gradient)."""
-    if t.numel() == 0:
+    if t.numel() == 0 or t.dim() == 0:
         return t
     rows, step, fits = 1, None, t.shape[-1] == 1 or t.stride(-1) == 1
     for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
@@ -257,6 +257,19 @@ def _one_stride(t):
             fits = fits and stride == rows * step
             rows *= size
     return t if fits else t.contiguous()
+
+
+def _two_strides(ids):
+    """ids, or a dense copy where they have more strides than a lookup takes."""
+    if ids.numel() == 0:
+        return ids
+    runs = []  # [size, stride], the innermost first
+    for size, stride in zip(reversed(ids.shape), reversed(ids.stride())):
+        if runs and stride == runs[-1][0] * runs[-1][1]:
+            runs[-1][0] *= size
+        elif size != 1:
+            runs.append([size, stride])
+    return ids if len(runs) <= 2 else ids.contiguous()
 
 
 class _EmbeddingFn(torch.autograd.Function):
@@ -278,8 +291,8 @@ class _EmbeddingFn(torch.autograd.Function):
 def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
               padding_idx: int | None = None, out_dtype: torch.dtype | None = None):
     """scale * table[ids], differentiable in table; see token_ops.embedding_forward.
-    The row padding_idx gets no gradient."""
-    return _EmbeddingFn.apply(ids, table, float(scale), padding_idx, out_dtype)
+    The row padding_idx gets no gradient. What has more strides than the call takes is copied."""
+    return _EmbeddingFn.apply(_two_strides(ids), _one_stride(table), float(scale), padding_idx, out_dtype)
 
 
 class Embedding(torch.nn.Module):
@@ -339,15 +352,16 @@ class _ExpertCombineFn(torch.autograd.Function):
 
 def expert_dispatch(x: torch.Tensor, plan: token_ops.ExpertRows) -> torch.Tensor:
     """rows [R, H]: x [..., H] sent to the rows of its experts (plan: expert_sort's),
-    differentiable in x."""
-    return _ExpertDispatchFn.apply(x, plan.position, plan.source)
+    differentiable in x, which is copied where its rows have no one stride."""
+    return _ExpertDispatchFn.apply(_one_stride(x), plan.position, plan.source)
 
 
 def expert_combine(rows: torch.Tensor, plan: token_ops.ExpertRows,
                    weights: torch.Tensor | None = None,
                    residual: torch.Tensor | None = None) -> torch.Tensor:
     """residual plus each token's weighted sum of its experts' rows, differentiable in
-    rows, weights and residual. The weights' gradient comes back in fp32; autograd
-    casts it to their dtype."""
-    return _ExpertCombineFn.apply(rows, None if weights is None else weights.contiguous(), residual,
+    rows, weights and residual, which are copied where their rows have no one stride. The
+    weights' gradient comes back in fp32; autograd casts it to their dtype."""
+    return _ExpertCombineFn.apply(_one_stride(rows), None if weights is None else weights.contiguous(),
+                                  None if residual is None else _one_stride(residual),
                                   plan.position, plan.source)
