@@ -292,6 +292,9 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
               padding_idx: int | None = None, out_dtype: torch.dtype | None = None):
     """scale * table[ids], differentiable in table; see token_ops.embedding_forward.
     The row padding_idx gets no gradient. What has more strides than the call takes is copied."""
+    V = table.shape[0] if table.dim() == 2 else 0
+    if padding_idx is not None and V and not -V <= padding_idx < V:
+        raise _lib.RMSNormError(_lib.ERR_INVALID_ARG, f"padding_idx {padding_idx} of {V} embeddings")
     return _EmbeddingFn.apply(_two_strides(ids), _one_stride(table), float(scale), padding_idx, out_dtype)
 
 

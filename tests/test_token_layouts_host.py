@@ -98,3 +98,20 @@ def test_forms_copy_what_the_calls_refuse(monkeypatch):
     with pytest.raises(Taken):
         autograd.expert_combine(torch.zeros(12, 16)[:, :8], plan, None, wide)
     assert seen[1][0].stride() == (16, 1) and seen[1][3].data_ptr() == wide.data_ptr()
+
+
+def test_padding_outside_the_table_is_refused_by_the_forward(monkeypatch):
+    """Before anything is looked up, as the gradient would refuse it."""
+    seen = taken(monkeypatch, "embedding_forward")
+    ids, table = torch.zeros(3, dtype=torch.int64), torch.zeros(6, 9)
+    for padding in (6, -7, 1 << 40):
+        with pytest.raises(pkg.RMSNormError, match="padding_idx .*INVALID_ARG") as e:
+            autograd.embedding(ids, table, padding_idx=padding)
+        assert e.value.status == pkg.ERR_INVALID_ARG
+    assert not seen
+    for padding in (5, 0, -1, -6, None):
+        with pytest.raises(Taken):
+            autograd.embedding(ids, table, padding_idx=padding)
+    # the module finds it when it is made
+    with pytest.raises(IndexError):
+        autograd.Embedding(6, 9, padding_idx=6)
