@@ -337,20 +337,24 @@ class _ExpertDispatchFn(torch.autograd.Function):
 class _ExpertCombineFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, weights, residual, position, source):
-        # without weights the backward does not look at the rows
-        ctx.save_for_backward(rows if weights is not None else None, weights, position, source)
+        # without weights, or for the residual's gradient alone, the backward does not look at the rows
+        seen = weights is not None and any(ctx.needs_input_grad[:2])
+        ctx.save_for_backward(rows if seen else None, weights, position, source)
         return token_ops.expert_combine_forward(rows, position, weights, residual)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         rows, weights, position, source = ctx.saved_tensors
+        dres = dy if ctx.needs_input_grad[2] else None
+        if not any(ctx.needs_input_grad[:2]):
+            return None, None, dres, None, None
         dense = _one_stride(dy)
         if weights is None:
             drows, dw = token_ops.expert_dispatch_forward(dense, position, source), None
         else:
             drows, dw = token_ops.expert_combine_backward(dense, rows, position, source, weights)
-        return drows, dw, dy if ctx.needs_input_grad[2] else None, None, None
+        return drows, dw, dres, None, None
 
 
 def expert_dispatch(x: torch.Tensor, plan: token_ops.ExpertRows) -> torch.Tensor:

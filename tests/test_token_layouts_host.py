@@ -115,3 +115,33 @@ def test_padding_outside_the_table_is_refused_by_the_forward(monkeypatch):
     # the module finds it when it is made
     with pytest.raises(IndexError):
         autograd.Embedding(6, 9, padding_idx=6)
+
+
+@pytest.mark.parametrize("weighted", [True, False])
+@pytest.mark.parametrize("asked", ["rows", "weights", "residual", "rows and residual"])
+def test_combine_gradients_that_nobody_asks_for(monkeypatch, asked, weighted):
+    """The residual's gradient is the result's own: nothing is computed for it, and the
+    rows are not kept."""
+    if asked == "weights" and not weighted:
+        pytest.skip("no weights")
+    called = []
+    monkeypatch.setattr(token_ops, "expert_combine_forward", lambda rows, position, w, residual: residual.clone())
+    monkeypatch.setattr(token_ops, "expert_combine_backward",
+                        lambda dy, rows, position, source, w: called.append("combine") or (rows * 0 + 1, w * 0 + 1))
+    monkeypatch.setattr(token_ops, "expert_dispatch_forward",
+                        lambda dy, position, source: called.append("dispatch") or torch.ones(8, 16))
+    plan = token_ops.ExpertRows(torch.zeros(4, 2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), None, None)
+    t = {"rows": torch.zeros(8, 16), "weights": torch.zeros(4, 2) if weighted else None, "residual": torch.zeros(4, 16)}
+    for name, value in t.items():
+        if value is not None:
+            value.requires_grad_(name in asked)
+    y = autograd.expert_combine(t["rows"], plan, t["weights"], t["residual"])
+    kept = [s for s in y.grad_fn.saved_tensors if s is not None and s.shape == (8, 16)]
+    needed = asked != "residual"
+    assert bool(kept) == (needed and weighted)
+    dy = torch.randn(4, 16, generator=torch.Generator().manual_seed(1))
+    y.backward(dy)
+    assert called == ([] if not needed else ["combine" if weighted else "dispatch"])
+    assert (t["rows"].grad is not None) == ("rows" in asked)
+    if "residual" in asked:
+        assert torch.equal(t["residual"].grad, dy)
