@@ -473,7 +473,8 @@ int rmsnorm_embedding_bwd_ws(const rmsnorm_embedding_t *embedding,
                              cudaStream_t stream);
 
 /* Bytes of workspace rmsnorm_embedding_bwd_ws needs; 0 for up to 256 tokens or
-   if the arguments are invalid. */
+   if the arguments are invalid. It does not shrink with more tokens: one for
+   the largest batch serves the smaller ones. */
 size_t rmsnorm_embedding_bwd_workspace_size(int64_t tokens, int64_t num_rows,
                                             int64_t width);
 
@@ -513,7 +514,8 @@ int rmsnorm_expert_sort(const void *experts, int experts_64, int64_t tokens,
                         cudaStream_t stream);
 
 /* rmsnorm_expert_sort with a caller-provided workspace, on the terms of
-   rmsnorm_embedding_bwd_ws, and its size (0: none needed, or invalid). */
+   rmsnorm_embedding_bwd_ws, and its size (0: none needed, or invalid), which
+   does not shrink with more tokens either. */
 int rmsnorm_expert_sort_ws(const void *experts, int experts_64,
                            int64_t tokens, int64_t choices,
                            int64_t num_experts, int64_t align, int64_t rows,

@@ -595,13 +595,20 @@ cudaError_t bwd_typed(int e, const BwdKernelArgs& a, int64_t width, int64_t zero
 // Tokens of a group: as many as 32, but groups enough for every SM to have
 // some 16 warps. A block's: kMaxSpan at most.
 constexpr int kMaxSegment = 32, kMinSegment = 8;
+constexpr int64_t kFullGroups = 152 * 16;
 int segment_of(int64_t n, int64_t width) {
     int seg = kMaxSegment;
-    while (seg > kMinSegment && cdiv(n, seg) * cdiv(width, 256) < 152 * 16) seg /= 2;
+    while (seg > kMinSegment && cdiv(n, seg) * cdiv(width, 256) < kFullGroups) seg /= 2;
     return seg;
 }
-// A block takes at least kMinSegment tokens a warp.
-int64_t most_spans(int64_t n) { return cdiv(n, kMinSegment * (kThreads / 32)); }
+// Spans of up to n tokens: a block takes a segment a warp at least. Shorter segments than
+// the longest are taken while those twice as long are too few to fill the device, so that
+// no fewer tokens than n have more spans than n is given room for.
+int64_t most_spans(int64_t n, int64_t width) {
+    constexpr int kGroups = kThreads / 32;
+    const int64_t of_short = kFullGroups / cdiv(width, 256) * 2 / kGroups + 1;
+    return std::min(cdiv(n, kMinSegment * kGroups), std::max(cdiv(n, kMaxSegment * kGroups), of_short));
+}
 
 struct BwdLayout {
     size_t pairs[2], present, counts, partial, bytes;
@@ -615,7 +622,7 @@ struct BwdLayout {
         for (int i = 0; i < 2; ++i) pairs[i] = take(n * sizeof(KeyItem));
         present = take(rows);
         counts = take(sort_counts_words(n, sort_max_bins(rows)) * 4);
-        partial = take(static_cast<size_t>(most_spans(n)) * 2 * width * 4);
+        partial = take(static_cast<size_t>(most_spans(n, width)) * 2 * width * 4);
         bytes = at;
     }
 };
@@ -624,7 +631,7 @@ struct BwdLayout {
 
 bool embedding_fits(int64_t n, int64_t width) {
     // element by element, which takes the most groups; they are counted in 32 bits
-    return n * cdiv(width, 32 * kFwdPieces) <= kMaxGrid && most_spans(n) * cdiv(width, 128) <= kMaxGrid / 2;
+    return n * cdiv(width, 32 * kFwdPieces) <= kMaxGrid && most_spans(n, width) * cdiv(width, 128) <= kMaxGrid / 2;
 }
 
 cudaError_t embedding_fwd_launch(const DeviceInfo& dev, int dtype, const EmbeddingArgs& in, cudaStream_t s) {

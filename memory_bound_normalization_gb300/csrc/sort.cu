@@ -552,7 +552,9 @@ int sort_max_bins(int64_t limit) { return 1 << cdiv(bits_of(limit), sort_passes(
 
 int64_t sort_counts_words(int64_t n, int bins) {
     if (n <= kClusterItems) return 0;
-    return static_cast<int64_t>(bins) * (Many(n).blocks + Many(n).blocks / kCluster);
+    // past a tile for each of the most blocks their number falls and grows again; the room does not
+    const int64_t blocks = n > kThreads * kManyBlocks ? kManyBlocks : Many(n).blocks;
+    return bins * (blocks + blocks / kCluster);
 }
 
 cudaError_t sort_launch(const DeviceInfo& dev, const KeySource& k, const SortBuffers& b, cudaStream_t s) {

@@ -141,6 +141,22 @@ def test_sorted_gradients_past_32_bits(n):
     assert not any(bool(part.isnan().any()) for part in grad.split(8192))
 
 
+@pytest.mark.parametrize("shape", [(4863, 300, 4096), (9727, 70001, 2048), (2432, 600, 8200), (131_072, 511, 1032),
+                                   (311_297, 70001, 66), (40_000, 9, 4096)], ids=emb.shape_id)
+def test_a_workspace_is_not_left(shape):
+    """A workspace of the bytes that are asked for, and of what a larger batch asks for."""
+    n, V, H = shape
+    ids, dy = ids_of("text", n, V), normal(n, H, dtype=BF16)
+    want = pkg.embedding_backward(ids, dy, V)
+    for size in (pkg.rmsnorm_embedding_bwd_workspace_size(n, V, H),
+                 pkg.rmsnorm_embedding_bwd_workspace_size(n + n // 3, V, H)):
+        room = torch.full((size + 4096,), 255, dtype=torch.uint8, device=DEV)
+        grad = torch.full_like(want, NAN)
+        assert pkg.rmsnorm_embedding_bwd_ws(edges.descriptor(n, V, H), ids, dy, grad, -1, 0, _lib.BF16,
+                                            room.data_ptr(), size) == _lib.OK
+        assert bool((room[size:] == 255).all()) and torch.equal(grad, want)
+
+
 # ------------------------------------------------------------- sorts of several tiles
 # one cluster takes up to 16384 items, a block one tile of 1024 up to 155648, of 2048 up to
 # 311296, then two and more

@@ -8,6 +8,7 @@ import subprocess
 
 import pytest
 
+import memory_bound_normalization_gb300 as pkg
 from memory_bound_normalization_gb300 import build as libbuild
 from test_image_launches_host import run  # noqa: F401  (a fixture)
 
@@ -78,6 +79,50 @@ def test_ring_of_the_widest_rows(run, dtype, size):  # noqa: F811
         assert lib.rmsnorm_expert_combine_bwd(ctypes.byref(d), A, A, A, A, A, A, A, _lib.{dtype}, None) == _lib.OK
         ring = launches()[-1]["smem"] > 0
         assert ring == (width * {size} >= 512), width
+    """)
+
+
+# ------------------------------------------------------------- workspaces
+# around every limit: one launch, one cluster, tiles, segments of 8, 16 and 32 tokens
+TOKENS = sorted({257, 300, 1000, 2432, 4863, 4864, 4865, 9727, 9728, 16383, 16384, 16385, 20000, 38911, 38912, 77823, 77824,
+                 77825, 100_000, 131_072, 155_647, 155_648, 155_649, 200_000, 311_295, 311_296, 311_297, 400_000, 700_000,
+                 1 << 20, 1 << 24})
+
+
+@pytest.mark.parametrize("width", [1, 8, 129, 256, 1000, 4096, 8192, 100_000])
+@pytest.mark.parametrize("rows", [1, 511, 512, 131072])
+def test_workspaces_do_not_shrink(rows, width):
+    """One for the largest batch serves smaller ones."""
+    size = [pkg.rmsnorm_embedding_bwd_workspace_size(n, rows, width) for n in TOKENS if n * width <= 1 << 38]
+    assert size == sorted(size), [(n, a, b) for n, a, b in zip(TOKENS, size, size[1:]) if b < a]
+    size = [pkg.rmsnorm_expert_sort_workspace_size(n, 1, min(rows, 1024)) for n in TOKENS]
+    assert size == sorted(size)
+
+
+def test_workspaces_hold_what_is_launched(run):  # noqa: F811
+    """Room for the spans that the launches have (a block's tokens by its shared memory),
+    and no more than a few times that for large calls."""
+    run(f"""
+    for width in (1, 2, 8, 64, 129, 256, 1000, 4096, 8192, 100000):
+        for n in {TOKENS}:
+            if n * width > 1 << 38:
+                continue
+            for rows in (1, 511, 131072):
+                e = _lib.Embedding(outer=1, inner=n, num_rows=rows, width=width, table_stride=width, row_stride=width,
+                                   ids_64=1, scale=1.0)
+                e.id_stride[1] = 1
+                need = lib.rmsnorm_embedding_bwd_workspace_size(n, rows, width)
+                for at in (A, A + 2):  # by pieces of 16 bytes, element by element
+                    before = len(launches())
+                    st = lib.rmsnorm_embedding_bwd_ws(ctypes.byref(e), A, at, A, -1, 1, _lib.BF16, A, need, None)
+                    assert st == _lib.OK, (n, rows, width)
+                    sums = [l for l in launches()[before:] if l["threads"] == 256][0]
+                    span = (sums["smem"] // 4 - 2) // 2
+                    spans = -(-n // span)
+                    used = 16 * n + 8 * spans * width
+                    assert used <= need, (n, rows, width, span)
+                    if n >= 131072 and at == A:
+                        assert need <= 1.5 * used + rows + (1 << 20), (n, rows, width, need, used)
     """)
 
 
