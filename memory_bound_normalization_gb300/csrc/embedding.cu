@@ -595,7 +595,7 @@ cudaError_t bwd_typed(int e, const BwdKernelArgs& a, int64_t width, int64_t zero
 // Tokens of a group: as many as 32, but groups enough for every SM to have
 // some 16 warps. A block's: kMaxSpan at most.
 constexpr int kMaxSegment = 32, kMinSegment = 8;
-constexpr int64_t kFullGroups = 152 * 16;
+constexpr int64_t kFullGroups = kSms * 16;
 int segment_of(int64_t n, int64_t width) {
     int seg = kMaxSegment;
     while (seg > kMinSegment && cdiv(n, seg) * cdiv(width, 256) < kFullGroups) seg /= 2;

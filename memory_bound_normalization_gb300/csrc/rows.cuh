@@ -186,7 +186,7 @@ struct RowShape {
 // Few lanes with many pieces each move more at a time, but only once there are warps
 // enough to fill the device: 5835 rows of 51 pieces take 6.6 us by 32 lanes and 10.0 by
 // 8, 33660 rows of 32 pieces 6.8 and 5.7.
-constexpr int64_t kFullWarps = 152 * 48;
+constexpr int64_t kFullWarps = kSms * 48;
 inline RowShape row_shape(int pieces, int u, int64_t rows) {
     RowShape r{pieces, 1, 1};
     while (r.lanes < 32 && r.lanes < pieces && (r.lanes * u < pieces || rows * r.lanes / 32 < kFullWarps)) r.lanes *= 2;

@@ -9,6 +9,10 @@
 
 namespace rmsn {
 
+// The SMs that shapes and workspaces are made for, a GB300's: constant, as a workspace's
+// size is asked without a device. On another number the work is shared less evenly.
+constexpr int kSms = 152;
+
 // ------------------------------------------------------------- sorting keys
 // n small whole numbers, read where they lie: `outer` runs of `inner` with a
 // stride each. A key is the number itself where it lies in [0, limit) and is

@@ -27,7 +27,7 @@ constexpr int kCluster = 8;
 // One cluster's scattered stores are slow: 1.3 us for every 8192 items. 16384 items take
 // it 6.6 us, 32768 9.0; 131073 take many blocks 7.
 constexpr int64_t kClusterItems = 2 * kThreads * kCluster;
-constexpr int kManyBlocks = 152;
+constexpr int kManyBlocks = kSms;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxExperts = RMSNORM_MAX_EXPERTS;
 
@@ -89,8 +89,9 @@ __device__ __forceinline__ uint32_t digit_of(const SortArgs& a, int pass, uint32
 }
 
 // Ranks of the warp's items among its items of the same digit, and its counts. Lanes
-// of one digit find one another by a vote a bit: nine votes for every round, where
-// a match instruction on 32 mostly different digits took 1.7 us a round of 32 warps.
+// of one digit find one another by a vote a bit of the digit (up to nine in a radix pass,
+// eleven for 1024 experts), where a match instruction on 32 mostly different digits took
+// 1.7 us a round of 32 warps.
 template <int R>
 __device__ __forceinline__ void rank_keys(const SortArgs& a, int pass, unsigned first, const uint32_t (&key)[R],
                                           uint16_t* cnt, uint32_t (&rank)[R]) {
