@@ -551,12 +551,18 @@ cudaError_t fwd_typed(int e, int width, FwdKernelArgs a, cudaStream_t s) {
 // than they saved (32001 rows of 1000 fp32: 38 us, 34 without).
 constexpr int64_t kZeroBesideSort = 48 << 20, kZeroBesidePass = 12 << 20;
 
+// Four times the warps that fit at once. With shares of 16 KB however short the rows, 253
+// tokens' gradient of 5288 rows of 2 f16 was two warps' work (107 us, 6 so), that of 10^6
+// rows of 1 bf16 took 120 (9 so); by as many warps as fit at once 3000017 rows of 9 fp32
+// take 60 us, by four times as many 36.
+constexpr int64_t kZeroWarps = kSms * 96;
+
 int64_t zero_blocks(const BwdKernelArgs& a) {
     return cdiv(cdiv(a.zero_to, a.zero_rows) * a.zero_slices, kThreads / 32);
 }
 
 template <typename TA, typename TG, int E>
-cudaError_t bwd_launches(BwdKernelArgs a, int64_t width, int64_t zeroed, cudaStream_t s) {
+cudaError_t bwd_launches(BwdKernelArgs a, int64_t width, cudaStream_t s) {
     constexpr int U = E >= 4 ? 1 : 2;
     a.shape = row_shape(static_cast<int>(width / E), U, 0);
     if (a.n <= kThreads) {
@@ -566,7 +572,6 @@ cudaError_t bwd_launches(BwdKernelArgs a, int64_t width, int64_t zeroed, cudaStr
         a.segment = static_cast<int>(cdiv(a.n, kThreads / a.shape.lanes));
         a.spans = 1;
         a.sum_blocks = static_cast<unsigned>(a.shape.chunks);
-        a.zero_to = a.accumulate ? 0 : a.rows;
         return launch_pdl(embedding_few_kernel<TA, TG, E, U>, static_cast<int>(a.sum_blocks + zero_blocks(a)), kThreads, 0,
                           1, s, a);
     }
@@ -574,7 +579,6 @@ cudaError_t bwd_launches(BwdKernelArgs a, int64_t width, int64_t zeroed, cudaStr
     a.span = a.segment * (kThreads / a.shape.lanes);
     a.spans = static_cast<unsigned>(cdiv(a.n, a.span));
     a.sum_blocks = a.spans * a.shape.chunks;
-    if (!a.accumulate) a.zero_to = a.rows - zeroed;
     cudaError_t err = launch_pdl(embedding_sum_kernel<TA, TG, E, U>, static_cast<int>(a.sum_blocks + zero_blocks(a)),
                                  kThreads, (a.span * 2 + 2) * 4, 1, s, a);
     if (err != cudaSuccess || a.spans == 1) return err;
@@ -583,13 +587,13 @@ cudaError_t bwd_launches(BwdKernelArgs a, int64_t width, int64_t zeroed, cudaStr
                       0, 1, s, a);
 }
 template <typename TA, typename TG>
-cudaError_t bwd_typed(int e, const BwdKernelArgs& a, int64_t width, int64_t zeroed, cudaStream_t s) {
+cudaError_t bwd_typed(int e, const BwdKernelArgs& a, int64_t width, cudaStream_t s) {
     if constexpr (sizeof(TG) == 2) {
-        if (e == 8) return bwd_launches<TA, TG, 8>(a, width, zeroed, s);
+        if (e == 8) return bwd_launches<TA, TG, 8>(a, width, s);
     }
-    if (e == 4) return bwd_launches<TA, TG, 4>(a, width, zeroed, s);
-    if (e == 2) return bwd_launches<TA, TG, 2>(a, width, zeroed, s);
-    return bwd_launches<TA, TG, 1>(a, width, zeroed, s);
+    if (e == 4) return bwd_launches<TA, TG, 4>(a, width, s);
+    if (e == 2) return bwd_launches<TA, TG, 2>(a, width, s);
+    return bwd_launches<TA, TG, 1>(a, width, s);
 }
 
 // Tokens of a group: as many as 32, but groups enough for every SM to have
@@ -695,16 +699,19 @@ cudaError_t embedding_bwd_launch(const DeviceInfo& dev, int dtype, const Embeddi
     a.accumulate = accumulate;
     a.scale = in.scale;
     a.status = in.status;
-    // some 16 KB a warp: a few rows, or a part of a long one
-    a.zero_rows = static_cast<int>(std::max<int64_t>(1, kZeroBytes / row_bytes));
-    if (a.zero_rows > 32) a.zero_rows = a.zero_rows / 32 * 32;
+    a.zero_to = accumulate ? 0 : in.rows - zeroed;
+    // some 16 KB a warp: a few rows, or a part of a long one; of short rows at most an even
+    // share of kZeroWarps, in whole 32s (a warp looks at 32 after 32)
+    const int64_t of_bytes = kZeroBytes / row_bytes, of_warps = cdiv(cdiv(a.zero_to, kZeroWarps), 32) * 32;
+    a.zero_rows = static_cast<int>(of_bytes <= 32 ? std::max<int64_t>(1, of_bytes)
+                                                  : std::max<int64_t>(32, std::min(of_bytes / 32 * 32, of_warps)));
     a.zero_slices = static_cast<int>(cdiv(row_bytes, kZeroBytes));
     switch (dtype) {
-        case RMSNORM_F32: return bwd_typed<float, float>(e, a, in.width, zeroed, s);
-        case RMSNORM_BF16: return bwd_typed<__nv_bfloat16, __nv_bfloat16>(e, a, in.width, zeroed, s);
-        case RMSNORM_F16: return bwd_typed<__half, __half>(e, a, in.width, zeroed, s);
-        case RMSNORM_BF16_W_F32: return bwd_typed<__nv_bfloat16, float>(e, a, in.width, zeroed, s);
-        default: return bwd_typed<__half, float>(e, a, in.width, zeroed, s);
+        case RMSNORM_F32: return bwd_typed<float, float>(e, a, in.width, s);
+        case RMSNORM_BF16: return bwd_typed<__nv_bfloat16, __nv_bfloat16>(e, a, in.width, s);
+        case RMSNORM_F16: return bwd_typed<__half, __half>(e, a, in.width, s);
+        case RMSNORM_BF16_W_F32: return bwd_typed<__nv_bfloat16, float>(e, a, in.width, s);
+        default: return bwd_typed<__half, float>(e, a, in.width, s);
     }
 }
 

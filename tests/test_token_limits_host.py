@@ -126,6 +126,34 @@ def test_workspaces_hold_what_is_launched(run):  # noqa: F811
     """)
 
 
+@pytest.mark.parametrize("n", [1, 200, 3000, 20000])
+def test_short_rows_are_shared_out(run, n):  # noqa: F811
+    """Rows without a token: a warp looks at 32 after 32, so a share of short ones is
+    bounded by their number, not by their bytes alone."""
+    run(f"""
+    for rows, width, wide in ((5288, 2, 0), (1000000, 1, 0), (40000, 8, 0), (200984, 10, 1), (40000000, 3, 1)):
+        e = _lib.Embedding(outer=1, inner={n}, num_rows=rows, width=width, table_stride=width, row_stride=width,
+                           ids_64=1, scale=1.0)
+        e.id_stride[1] = 1
+        dtype = _lib.BF16_W_F32 if wide else _lib.BF16
+        def blocks(accumulate):
+            before = len(launches())
+            assert lib.rmsnorm_embedding_bwd_ws(ctypes.byref(e), A, A, A, -1, accumulate, dtype, A, 1 << 40,
+                                                None) == _lib.OK
+            return [l for l in launches()[before:] if l["threads"] == 256][0]["grid"]
+        size = (4 if wide else 2) * width
+        if {n} <= 256:
+            left = rows
+        else:  # what is zeroed beside the sort
+            passes = -(-rows.bit_length() // 9)
+            left = rows - min(rows, -(-(48 << 20 if {n} <= 16384 else passes * 24 << 20) // size))
+        zero = blocks(0) - blocks(1)  # with nothing to zero there are the sums' blocks alone
+        # an even share of 96 warps an SM, in whole 32s; no share is larger than 16 KB
+        share = max(32, min(16384 // size // 32 * 32, -(-left // (152 * 96 * 32)) * 32))
+        assert zero == -(-(-(-left // share)) // 8), (rows, width, zero, share)
+    """)
+
+
 # ------------------------------------------------------------- the checked build's checks
 def unchecked(name, access):
     """Lines with such an access that no check of the checked build stands before."""
